@@ -1,0 +1,401 @@
+// Global gradient norm over a list of tensors, and clipping by it:
+//   norm = sqrt(sum over all elements g^2),  dst = min(1, max_norm / norm) src.
+//
+// The list's device table holds chunks: runs of at most GC_CHUNK_BYTES of one
+// tensor, so that tensors of any size give the warps equal shares and a warp
+// finds its work with one 32-byte load.
+//
+//   gc_norm   one warp per chunk; each block leaves its sum of squares (fp64).
+//   gc_stats  adds the blocks' sums (the norm alone).
+//   gc_clip   every block adds the same sums in the same order, so all take
+//             the same coefficient, and scales its chunks.
+//
+// Squares: a lane's batch of values (32 fp32 or 64 bf16) is squared and summed
+// in fp32 while its largest magnitude lies in [2^-56, 2^60]: no sum of squares
+// overflows, and a square that fp32 holds as a subnormal is off by at most
+// 2^-150, 2^-38 of the largest square.  Other batches are squared in fp64
+// (exact); batches of zeros add nothing.  Batches are added in fp64.
+#include <math.h>
+#include <stdlib.h>
+
+#include "lrm_internal.cuh"
+#include "vec.cuh"
+
+struct lrm_grad_list {
+  int device;
+  long long chunks;
+  int in_place, has_dst;  // every dst is its src; every non-empty tensor has a dst
+  int grid_norm, grid_clip;
+  void* table;
+};
+
+namespace lrm {
+namespace {
+
+constexpr int GC_THREADS = 256;
+constexpr int GC_WARPS = GC_THREADS / 32;
+constexpr int GC_CHUNK_BYTES = 16384;
+constexpr int GC_MAX_GRID = 152 * 8 * 2;  // upper bound of the norm kernel's grid, sizes the partial sums
+
+enum : int32_t { GC_F32_VEC = 0, GC_BF16_VEC = 1, GC_F32_ANY = 2, GC_BF16_ANY = 3 };
+
+struct __align__(32) Chunk {
+  const void* src;
+  void* dst;
+  int32_t n;     // elements
+  int32_t kind;  // *_VEC: src and dst 16-byte aligned, n a multiple of 16 bytes
+  int64_t pad;
+};
+
+constexpr size_t GC_SCRATCH_BYTES = GC_MAX_GRID * sizeof(double);
+
+// The chunks of a list, in order: sink(chunk) for each.  Tensors whose src
+// starts off a 16-byte boundary get a short first chunk up to it.
+template <typename Sink>
+void for_chunks(const lrm_tensor* tensors, int32_t count, Sink sink) {
+  for (int32_t i = 0; i < count; ++i) {
+    const lrm_tensor& t = tensors[i];
+    const int64_t es = t.dtype == LRM_F32 ? 4 : 2, per = 16 / es;
+    const char* src = static_cast<const char*>(t.src);
+    char* dst = static_cast<char*>(t.dst);
+    int64_t at = 0;
+    while (at < t.n) {
+      const char* s = src + at * es;
+      char* d = dst == nullptr ? nullptr : dst + at * es;
+      const int64_t left = t.n - at, off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(s) % 16) / es;
+      int64_t n;
+      bool vec = false;
+      if (off != 0) {
+        n = per - off < left ? per - off : left;
+      } else if (left < per) {
+        n = left;
+      } else {
+        const int64_t whole = left / per * per, most = GC_CHUNK_BYTES / es;
+        n = whole < most ? whole : most;
+        vec = d == nullptr || aligned(d, 16);
+      }
+      Chunk c;
+      c.src = s;
+      c.dst = d;
+      c.n = static_cast<int32_t>(n);
+      c.kind = t.dtype == LRM_F32 ? (vec ? GC_F32_VEC : GC_F32_ANY) : (vec ? GC_BF16_VEC : GC_BF16_ANY);
+      c.pad = 0;
+      sink(c);
+      at += n;
+    }
+  }
+}
+
+// Number of chunks of for_chunks without walking them.
+int64_t count_chunks(const lrm_tensor* tensors, int32_t count) {
+  int64_t total = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const lrm_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    const int64_t es = t.dtype == LRM_F32 ? 4 : 2, per = 16 / es, most = GC_CHUNK_BYTES / es;
+    const int64_t off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(t.src) % 16) / es;
+    int64_t left = t.n;
+    if (off != 0) {
+      ++total;
+      left -= per - off < left ? per - off : left;
+    }
+    const int64_t whole = left / per * per;
+    total += (whole + most - 1) / most + (left > whole ? 1 : 0);
+  }
+  return total;
+}
+
+lrm_status check_tensors(const lrm_tensor* tensors, int32_t count) {
+  if (count < 0 || (count > 0 && tensors == nullptr)) return LRM_ERR_INVALID_ARG;
+  int64_t elements = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const lrm_tensor& t = tensors[i];
+    if (t.n < 0 || (t.dtype != LRM_F32 && t.dtype != LRM_BF16)) return LRM_ERR_INVALID_ARG;
+    if (t.n > (static_cast<int64_t>(1) << 42)) return LRM_ERR_SHAPE;
+    elements += t.n;
+    if (elements > (static_cast<int64_t>(1) << 43)) return LRM_ERR_SHAPE;
+    if (t.n > 0 && t.src == nullptr) return LRM_ERR_INVALID_ARG;
+    const size_t es = t.dtype == LRM_F32 ? 4 : 2;
+    if (!aligned(t.src, es) || !aligned(t.dst, es)) return LRM_ERR_ALIGN;
+  }
+  return LRM_OK;
+}
+
+__device__ __forceinline__ bool in_fp32_range(float mx) { return mx >= 0x1p-56f && mx <= 0x1p60f; }
+
+// Adds the squares of a batch of n values to sum.
+template <int N>
+__device__ __forceinline__ void add_squares(const float (&v)[N], double& sum) {
+  float mx = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    mx = fmaxf(mx, fabsf(v[i]));
+    a[i % 4] = fmaf(v[i], v[i], a[i % 4]);
+  }
+  const float s = (a[0] + a[1]) + (a[2] + a[3]);
+  if (in_fp32_range(mx)) {
+    sum += s;  // a NaN among the values is in s
+  } else if (mx != 0.f || s != 0.f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += static_cast<double>(v[i]) * v[i];
+  }
+}
+
+__device__ __forceinline__ void unpack(const uint4& x, float* v) {
+  v[0] = bf16_lo(x.x);
+  v[1] = bf16_hi(x.x);
+  v[2] = bf16_lo(x.y);
+  v[3] = bf16_hi(x.y);
+  v[4] = bf16_lo(x.z);
+  v[5] = bf16_hi(x.z);
+  v[6] = bf16_lo(x.w);
+  v[7] = bf16_hi(x.w);
+}
+
+constexpr int GC_BATCH = 8;  // 16-byte loads a lane has in flight
+
+__device__ double chunk_squares(const Chunk& c, int lane) {
+  double sum = 0.0;
+  if (c.kind == GC_F32_VEC || c.kind == GC_BF16_VEC) {
+    const uint4* p = static_cast<const uint4*>(c.src);
+    const int nv = c.n / (c.kind == GC_F32_VEC ? 4 : 8);
+    for (int v0 = 0; v0 < nv; v0 += 32 * GC_BATCH) {
+      uint4 x[GC_BATCH];
+#pragma unroll
+      for (int j = 0; j < GC_BATCH; ++j) {
+        const int v = v0 + lane + 32 * j;
+        x[j] = v < nv ? ld_stream(p + v) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (c.kind == GC_F32_VEC) {
+        float v[4 * GC_BATCH];
+#pragma unroll
+        for (int j = 0; j < GC_BATCH; ++j) {
+          v[4 * j] = __uint_as_float(x[j].x);
+          v[4 * j + 1] = __uint_as_float(x[j].y);
+          v[4 * j + 2] = __uint_as_float(x[j].z);
+          v[4 * j + 3] = __uint_as_float(x[j].w);
+        }
+        add_squares(v, sum);
+      } else {
+        float v[8 * GC_BATCH];
+#pragma unroll
+        for (int j = 0; j < GC_BATCH; ++j) unpack(x[j], v + 8 * j);
+        add_squares(v, sum);
+      }
+    }
+  } else {
+    for (int i = lane; i < c.n; i += 32) {
+      const float v = c.kind == GC_F32_ANY ? static_cast<const float*>(c.src)[i]
+                                           : __bfloat162float(static_cast<const __nv_bfloat16*>(c.src)[i]);
+      sum += static_cast<double>(v) * v;
+    }
+  }
+  return sum;
+}
+
+__global__ void __launch_bounds__(GC_THREADS) gc_norm(const Chunk* __restrict__ chunks, long long count,
+                                                      double* __restrict__ partial) {
+  __shared__ double s_sum[GC_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long step = static_cast<long long>(gridDim.x) * GC_WARPS;
+  double sum = 0.0;
+  for (long long i = static_cast<long long>(blockIdx.x) * GC_WARPS + warp; i < count; i += step)
+    sum += chunk_squares(chunks[i], lane);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double a = 0.0;
+    for (int w = 0; w < GC_WARPS; ++w) a += s_sum[w];
+    partial[blockIdx.x] = a;
+  }
+}
+
+// The blocks' sums added in a fixed order; every thread gets the total.
+__device__ double total_squares(const double* __restrict__ partial, int nblk) {
+  __shared__ double s_part[GC_WARPS];
+  double a = 0.0;
+  for (int i = threadIdx.x; i < nblk; i += GC_THREADS) a += partial[i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = a;
+  __syncthreads();
+  a = 0.0;
+  for (int w = 0; w < GC_WARPS; ++w) a += s_part[w];
+  return a;
+}
+
+__device__ lrm_grad_stats make_stats(double squares, float max_norm) {
+  const double norm = sqrt(squares);
+  lrm_grad_stats r;
+  r.norm = static_cast<float>(norm);
+  r.nonfinite = isfinite(norm) ? 0 : 1;
+  r.coef = !r.nonfinite && norm > max_norm ? static_cast<float>(max_norm / norm) : 1.f;
+  return r;
+}
+
+__global__ void __launch_bounds__(GC_THREADS) gc_stats(const double* __restrict__ partial, int nblk,
+                                                       lrm_grad_stats* __restrict__ stats) {
+  const double sq = total_squares(partial, nblk);
+  if (threadIdx.x == 0) *stats = make_stats(sq, INFINITY);
+}
+
+__device__ __forceinline__ uint4 scale_f32x4(const uint4& x, float c) {
+  return make_uint4(__float_as_uint(__uint_as_float(x.x) * c), __float_as_uint(__uint_as_float(x.y) * c),
+                    __float_as_uint(__uint_as_float(x.z) * c), __float_as_uint(__uint_as_float(x.w) * c));
+}
+
+__device__ void scale_chunk(const Chunk& c, float coef, int lane) {
+  if (c.kind == GC_F32_VEC || c.kind == GC_BF16_VEC) {
+    const uint4* p = static_cast<const uint4*>(c.src);
+    uint4* q = static_cast<uint4*>(c.dst);
+    const int nv = c.n / (c.kind == GC_F32_VEC ? 4 : 8);
+    for (int v0 = 0; v0 < nv; v0 += 32 * GC_BATCH) {
+      uint4 x[GC_BATCH];
+#pragma unroll
+      for (int j = 0; j < GC_BATCH; ++j) {
+        const int v = v0 + lane + 32 * j;
+        if (v < nv) x[j] = p[v];
+      }
+#pragma unroll
+      for (int j = 0; j < GC_BATCH; ++j) {
+        const int v = v0 + lane + 32 * j;
+        if (v < nv) st_v4(q + v, c.kind == GC_F32_VEC ? scale_f32x4(x[j], coef) : scale_bf16x8(x[j], coef));
+      }
+    }
+  } else {
+    for (int i = lane; i < c.n; i += 32) {
+      if (c.kind == GC_F32_ANY)
+        static_cast<float*>(c.dst)[i] = static_cast<const float*>(c.src)[i] * coef;
+      else
+        static_cast<__nv_bfloat16*>(c.dst)[i] =
+            __float2bfloat16_rn(__bfloat162float(static_cast<const __nv_bfloat16*>(c.src)[i]) * coef);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(GC_THREADS) gc_clip(const Chunk* __restrict__ chunks, long long count,
+                                                      const double* __restrict__ partial, int nblk, float max_norm,
+                                                      int in_place, lrm_grad_stats* __restrict__ stats) {
+  const lrm_grad_stats r = make_stats(total_squares(partial, nblk), max_norm);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *stats = r;
+  if (in_place && r.coef == 1.f) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long step = static_cast<long long>(gridDim.x) * GC_WARPS;
+  for (long long i = static_cast<long long>(blockIdx.x) * GC_WARPS + warp; i < count; i += step)
+    scale_chunk(chunks[i], r.coef, lane);
+}
+
+lrm_status launch_norm(const lrm_grad_list* list, cudaStream_t s) {
+  if (list->chunks == 0) return LRM_OK;
+  gc_norm<<<list->grid_norm, GC_THREADS, 0, s>>>(
+      reinterpret_cast<const Chunk*>(static_cast<char*>(list->table) + GC_SCRATCH_BYTES), list->chunks,
+      static_cast<double*>(list->table));
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace lrm
+
+using namespace lrm;
+
+extern "C" lrm_status lrm_grad_table_size(const lrm_tensor* tensors, int32_t count, size_t* bytes) {
+  if (bytes == nullptr) return LRM_ERR_INVALID_ARG;
+  const lrm_status st = check_tensors(tensors, count);
+  if (st != LRM_OK) return st;
+  *bytes = GC_SCRATCH_BYTES + static_cast<size_t>(count_chunks(tensors, count)) * sizeof(Chunk);
+  return LRM_OK;
+}
+
+extern "C" lrm_status lrm_grad_list_create(lrm_ctx* ctx, const lrm_tensor* tensors, int32_t count, void* table,
+                                           size_t table_bytes, void* stream, lrm_grad_list** out) {
+  if (out == nullptr) return LRM_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (ctx == nullptr) return LRM_ERR_INVALID_ARG;
+  size_t need = 0;
+  lrm_status st = lrm_grad_table_size(tensors, count, &need);
+  if (st != LRM_OK) return st;
+  if (table == nullptr || table_bytes < need) return LRM_ERR_WORKSPACE;
+  if (!aligned(table, 256)) return LRM_ERR_ALIGN;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return LRM_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) {
+    cudaGetLastError();
+    return LRM_ERR_CUDA;
+  }
+  if (cap != cudaStreamCaptureStatusNone) return LRM_ERR_INVALID_ARG;
+  lrm_grad_list* list = static_cast<lrm_grad_list*>(calloc(1, sizeof(lrm_grad_list)));
+  if (list == nullptr) return LRM_ERR_CUDA;
+  list->device = ctx->device;
+  list->table = table;
+  list->in_place = 1;
+  list->has_dst = 1;
+  for (int32_t i = 0; i < count; ++i) {
+    if (tensors[i].n == 0) continue;
+    if (tensors[i].dst == nullptr) list->has_dst = 0;
+    if (tensors[i].dst != tensors[i].src) list->in_place = 0;
+  }
+  list->chunks = count_chunks(tensors, count);
+  if (list->chunks > 0) {
+    Chunk* host = static_cast<Chunk*>(malloc(static_cast<size_t>(list->chunks) * sizeof(Chunk)));
+    if (host == nullptr) {
+      free(list);
+      return LRM_ERR_CUDA;
+    }
+    int64_t at = 0;
+    for_chunks(tensors, count, [&](const Chunk& c) { host[at++] = c; });
+    // a copy from pageable memory has read `host` when it returns
+    const cudaError_t e = cudaMemcpyAsync(static_cast<char*>(table) + GC_SCRATCH_BYTES, host,
+                                          static_cast<size_t>(list->chunks) * sizeof(Chunk), cudaMemcpyHostToDevice, s);
+    free(host);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      free(list);
+      return LRM_ERR_CUDA;
+    }
+    const long long blocks = (list->chunks + GC_WARPS - 1) / GC_WARPS;
+    const int gn = resident_grid(ctx, gc_norm, GC_THREADS, 0), gc = resident_grid(ctx, gc_clip, GC_THREADS, 0);
+    const int cap_n = gn < GC_MAX_GRID ? gn : GC_MAX_GRID;
+    list->grid_norm = static_cast<int>(blocks < cap_n ? blocks : cap_n);
+    list->grid_clip = static_cast<int>(blocks < gc ? blocks : gc);
+  }
+  *out = list;
+  return LRM_OK;
+}
+
+extern "C" lrm_status lrm_grad_list_destroy(lrm_grad_list* list) {
+  free(list);
+  return LRM_OK;
+}
+
+extern "C" lrm_status lrm_grad_norm(lrm_ctx* ctx, const lrm_grad_list* list, lrm_grad_stats* stats, void* stream) {
+  if (ctx == nullptr || list == nullptr || stats == nullptr || list->device != ctx->device) return LRM_ERR_INVALID_ARG;
+  if (!aligned(stats, 4)) return LRM_ERR_ALIGN;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return LRM_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const lrm_status st = launch_norm(list, s);
+  if (st != LRM_OK) return st;
+  gc_stats<<<1, GC_THREADS, 0, s>>>(static_cast<const double*>(list->table), list->grid_norm, stats);
+  return launch_status();
+}
+
+extern "C" lrm_status lrm_grad_clip(lrm_ctx* ctx, const lrm_grad_list* list, float max_norm, lrm_grad_stats* stats,
+                                    void* stream) {
+  if (ctx == nullptr || list == nullptr || stats == nullptr || list->device != ctx->device || !list->has_dst ||
+      !(max_norm >= 0.f))
+    return LRM_ERR_INVALID_ARG;
+  if (!aligned(stats, 4)) return LRM_ERR_ALIGN;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return LRM_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const lrm_status st = launch_norm(list, s);
+  if (st != LRM_OK) return st;
+  gc_clip<<<list->grid_clip > 0 ? list->grid_clip : 1, GC_THREADS, 0, s>>>(
+      reinterpret_cast<const Chunk*>(static_cast<char*>(list->table) + GC_SCRATCH_BYTES), list->chunks,
+      static_cast<const double*>(list->table), list->grid_norm, max_norm, list->in_place, stats);
+  return launch_status();
+}

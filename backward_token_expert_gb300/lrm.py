@@ -35,6 +35,8 @@ LRM_OP_ROUTE_STATS = 0
 LRM_OP_SELECT = 1
 LRM_OP_ZERO_DROPPED = 2
 LRM_OP_COMBINE = 3
+LRM_OP_ROUTER = 4
+DTYPE_F32, DTYPE_BF16 = 0, 1
 
 # every entry point declared in include/lrm.h
 EXPORTED = (
@@ -63,6 +65,14 @@ EXPORTED = (
     "lrm_combine_rows",
     "lrm_capacity",
     "lrm_max_rows",
+    "lrm_router_forward",
+    "lrm_router_backward",
+    "lrm_gate_grad",
+    "lrm_grad_table_size",
+    "lrm_grad_list_create",
+    "lrm_grad_list_destroy",
+    "lrm_grad_norm",
+    "lrm_grad_clip",
 )
 
 # selection metrics of lrm_score_metric (the ablation of LRMoE sec. 4.7, Table 2)
@@ -101,6 +111,18 @@ class RouteSummary(ctypes.Structure):
         ("max_over_mean", ctypes.c_float),
         ("sum_P", ctypes.c_float),
     ]
+
+
+class RouterLosses(ctypes.Structure):
+    _fields_ = [("loss", ctypes.c_float), ("aux", ctypes.c_float), ("z", ctypes.c_float), ("tokens", ctypes.c_int32)]
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class GradStats(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_float), ("coef", ctypes.c_float), ("nonfinite", ctypes.c_int32)]
 
 
 SUMMARY_BYTES = ctypes.sizeof(RouteSummary)
@@ -146,6 +168,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lrm_capacity": ([Dims, i32, i32, ctypes.POINTER(i32)], st),
         "lrm_max_rows": ([Dims, i32, i32, i32, i32, ctypes.POINTER(i32)], st),
     }
+    f32 = ctypes.c_float
+    size = ctypes.c_size_t
+    sig.update({
+        "lrm_router_forward": ([P, P, i32, P, Dims, i32, f32, f32, P, P, P, P, P, P, P, P, size, P], st),
+        "lrm_router_backward": ([P, P, i32, P, P, P, P, P, P, Dims, i32, f32, f32, P, i32, P], st),
+        "lrm_gate_grad": ([P, P, P, P, P, Dims, i32, P, P], st),
+        "lrm_grad_table_size": ([ctypes.POINTER(Tensor), i32, ctypes.POINTER(size)], st),
+        "lrm_grad_list_create": ([P, ctypes.POINTER(Tensor), i32, P, size, P, ctypes.POINTER(P)], st),
+        "lrm_grad_list_destroy": ([P], st),
+        "lrm_grad_norm": ([P, P, P, P], st),
+        "lrm_grad_clip": ([P, P, f32, P, P], st),
+    })
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -332,6 +366,59 @@ def lrm_compact_padded(ctx, delta_c, phi_c, sel_offsets, dims: Dims, C: int, del
     _check(load_library().lrm_compact_padded(ctx, _ptr(delta_c), _ptr(phi_c), _ptr(sel_offsets), dims, int(C),
                                              _ptr(delta_pad), _ptr(phi_pad), _ptr(pad_offsets), _stream(stream)),
            "lrm_compact_padded")
+
+
+def lrm_router_forward(ctx, logits, logits_dtype: int, valid, dims: Dims, renorm: bool, aux_coef: float,
+                       z_coef: float, expert_idx, alpha, row_stats, counts, f, P, losses, ws, ws_bytes: int,
+                       stream=None) -> None:
+    _check(load_library().lrm_router_forward(ctx, _ptr(logits), logits_dtype, _ptr(valid), dims, renorm, aux_coef,
+                                             z_coef, _ptr(expert_idx), _ptr(alpha), _ptr(row_stats), _ptr(counts),
+                                             _ptr(f), _ptr(P), _ptr(losses), _ptr(ws), ws_bytes, _stream(stream)),
+           "lrm_router_forward")
+
+
+def lrm_router_backward(ctx, logits, logits_dtype: int, expert_idx, alpha, row_stats, dgate, f, losses, dims: Dims,
+                        renorm: bool, aux_coef: float, z_coef: float, dlogits, dlogits_dtype: int,
+                        stream=None) -> None:
+    _check(load_library().lrm_router_backward(ctx, _ptr(logits), logits_dtype, _ptr(expert_idx), _ptr(alpha),
+                                              _ptr(row_stats), _ptr(dgate), _ptr(f), _ptr(losses), dims, renorm,
+                                              aux_coef, z_coef, _ptr(dlogits), dlogits_dtype, _stream(stream)),
+           "lrm_router_backward")
+
+
+def lrm_gate_grad(ctx, dphi_c, phi_c, sel_offsets, sel_ids, dims: Dims, max_rows: int, dgate, stream=None) -> None:
+    _check(load_library().lrm_gate_grad(ctx, _ptr(dphi_c), _ptr(phi_c), _ptr(sel_offsets), _ptr(sel_ids), dims,
+                                        max_rows, _ptr(dgate), _stream(stream)), "lrm_gate_grad")
+
+
+def tensor_array(entries):
+    """A C array of lrm_tensor from (src, dst, n, dtype) entries."""
+    return (Tensor * max(1, len(entries)))(*[Tensor(_ptr(s), _ptr(d), int(n), int(dt)) for s, d, n, dt in entries])
+
+
+def lrm_grad_table_size(tensors, count: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load_library().lrm_grad_table_size(tensors, int(count), ctypes.byref(out)), "lrm_grad_table_size")
+    return out.value
+
+
+def lrm_grad_list_create(ctx, tensors, count: int, table, table_bytes: int, stream=None) -> int:
+    out = ctypes.c_void_p()
+    _check(load_library().lrm_grad_list_create(ctx, tensors, int(count), _ptr(table), int(table_bytes),
+                                               _stream(stream), ctypes.byref(out)), "lrm_grad_list_create")
+    return out.value
+
+
+def lrm_grad_list_destroy(grad_list: int) -> None:
+    _check(load_library().lrm_grad_list_destroy(grad_list), "lrm_grad_list_destroy")
+
+
+def lrm_grad_norm(ctx, grad_list: int, stats, stream=None) -> None:
+    _check(load_library().lrm_grad_norm(ctx, grad_list, _ptr(stats), _stream(stream)), "lrm_grad_norm")
+
+
+def lrm_grad_clip(ctx, grad_list: int, max_norm: float, stats, stream=None) -> None:
+    _check(load_library().lrm_grad_clip(ctx, grad_list, max_norm, _ptr(stats), _stream(stream)), "lrm_grad_clip")
 
 
 def lrm_get_device_status(ctx, stream=None) -> int:

@@ -200,6 +200,17 @@ class Recalibration:
                 ws=torch.empty(max(ws, 4), dtype=torch.uint8, device=dev))
         return self.fc1
 
+    def gate_grad(self, stream=None):
+        """alpha_u dL/dalpha_u of every pair in ``self.dgate`` ([N] fp32, 0 for
+        pairs that were not retained), after dgrad and compact: what
+        ``Router.backward`` takes."""
+        b = self.buf
+        if getattr(self, "dgate", None) is None:
+            self.dgate = torch.empty(max(1, self.N), dtype=torch.float32, device=b.dW.device)[: self.N]
+        L.lrm_gate_grad(self.ctx, b.dphi_c, b.phi_c, b.sel_offsets, b.sel_ids, self.dims, self.max_rows, self.dgate,
+                        stream)
+        return self.dgate
+
     def wgrad(self, stream=None, accumulate=0):
         b = self.buf
         L.lrm_grouped_wgrad(self.ctx, b.delta_c, b.phi_c, b.sel_offsets, self.dims, self.max_rows, accumulate,
@@ -293,6 +304,166 @@ class StepGraph:
     def replay(self) -> None:
         """Enqueue one step on the current stream."""
         self.graph.replay()
+
+
+_DTYPES = {torch.float32: L.DTYPE_F32, torch.bfloat16: L.DTYPE_BF16}
+
+
+def _require(t, name, dtype, shape, device):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+class Router:
+    """The router of one layer shape through the C ABI: gates and balance loss
+    of a batch of logits (lrm_router_forward) and the logits' gradient
+    (lrm_router_backward).  The outputs of ``forward`` are the buffers
+    ``expert_idx`` [T, k], ``alpha`` [T*k], ``row_stats`` [T, 2], ``counts``,
+    ``f``, ``P`` [E], ``losses`` (fp32 [3]: loss, aux, z) and ``tokens`` (int32
+    [1]); ``backward`` reads them and writes ``dlogits`` [T, E]."""
+
+    def __init__(self, T, E, k, renorm: bool = True, aux_coef: float = 0.0, z_coef: float = 0.0,
+                 dtype=torch.float32, dlogits_dtype=None, device=0, ctx=None):
+        self.T, self.E, self.k = int(T), int(E), int(k)
+        self.renorm, self.aux_coef, self.z_coef = bool(renorm), float(aux_coef), float(z_coef)
+        self.dtype = dtype
+        self.dlogits_dtype = dtype if dlogits_dtype is None else dlogits_dtype
+        if dtype not in _DTYPES or self.dlogits_dtype not in _DTYPES:
+            raise ValueError("router logits and their gradient are float32 or bfloat16")
+        self.device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+        self.dims = L.dims_of(T, E, k, 8, 8)
+        self._own_ctx = ctx is None
+        self.ctx = L.lrm_create(self.device.index or 0) if ctx is None else ctx
+        i32 = dict(dtype=torch.int32, device=self.device)
+        f32 = dict(dtype=torch.float32, device=self.device)
+        self.expert_idx = torch.empty(self.T, self.k, **i32)
+        self.alpha = torch.empty(self.T * self.k, **f32)
+        self.row_stats = torch.empty(self.T, 2, **f32)
+        self.counts = torch.empty(self.E, **i32)
+        self.f = torch.empty(self.E, **f32)
+        self.P = torch.empty(self.E, **f32)
+        self._losses = torch.zeros(4, **f32)  # lrm_router_losses
+        self.losses = self._losses[:3]
+        self.tokens = self._losses.view(torch.int32)[3:]
+        self.dlogits = torch.empty(self.T, self.E, dtype=self.dlogits_dtype, device=self.device)
+        need = L.lrm_workspace_size(self.ctx, L.LRM_OP_ROUTER, self.dims)
+        self.ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+
+    def close(self):
+        if self._own_ctx and getattr(self, "ctx", None):
+            L.lrm_destroy(self.ctx)
+        self.ctx = None
+
+    def __del__(self):  # pragma: no cover - best effort
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def forward(self, logits, valid=None, stream=None):
+        """Gates, counts and losses of a batch; `valid` [T] uint8 leaves the
+        tokens whose entry is 0 out of the counts and losses, with gate 0."""
+        _require(logits, "logits", self.dtype, (self.T, self.E), self.device)
+        if valid is not None:
+            _require(valid, "valid", torch.uint8, (self.T,), self.device)
+        L.lrm_router_forward(self.ctx, logits, _DTYPES[self.dtype], valid, self.dims, self.renorm, self.aux_coef,
+                             self.z_coef, self.expert_idx, self.alpha, self.row_stats, self.counts, self.f, self.P,
+                             self._losses, self.ws, self.ws.numel(), stream)
+
+    def backward(self, logits, dgate=None, f=None, stream=None):
+        """The gradient of the loss (with its coefficients) and, given `dgate`
+        [T*k] (alpha dL/dalpha of every pair, from ``Recalibration.gate_grad``),
+        of the gates, with respect to the logits of the last ``forward``.  `f`
+        [E] replaces the batch's own load fractions."""
+        _require(logits, "logits", self.dtype, (self.T, self.E), self.device)
+        if dgate is not None and (dgate.dtype != torch.float32 or dgate.numel() != self.T * self.k
+                                  or dgate.device != self.device or not dgate.is_contiguous()):
+            raise ValueError(f"dgate must hold {self.T * self.k} contiguous float32 values on {self.device}")
+        if f is not None:
+            _require(f, "f", torch.float32, (self.E,), self.device)
+        L.lrm_router_backward(self.ctx, logits, _DTYPES[self.dtype], self.expert_idx, self.alpha, self.row_stats,
+                              dgate, self.f if f is None else f, self._losses, self.dims, self.renorm, self.aux_coef,
+                              self.z_coef, self.dlogits, _DTYPES[self.dlogits_dtype], stream)
+        return self.dlogits
+
+
+def _dense(t) -> bool:
+    """Whether the tensor's elements fill its memory range, in any dimension order."""
+    run = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != run:
+            return False
+        run *= size
+    return True
+
+
+class GradClip:
+    """Global gradient norm and clipping over a fixed list of tensors
+    (lrm_grad_norm, lrm_grad_clip).  `outs` receive the clipped values (the
+    gradients themselves where it is None).  The tensors are fp32 or bf16, of
+    any shape and dimension order, but dense: their elements fill their memory
+    range; an output has its gradient's type, shape and strides.  The result's
+    ``norm``, ``coef`` (fp32 [1]) and ``nonfinite`` (int32 [1]) stay on the
+    device."""
+
+    def __init__(self, grads, outs=None, ctx=None, stream=None):
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        if len(outs) != len(grads):
+            raise ValueError("as many outputs as gradients are wanted")
+        if not grads:
+            raise ValueError("no gradients")
+        self.device = grads[0].device
+        spans = []
+        for g, o in zip(grads, outs):
+            if g.dtype not in _DTYPES or g.device.type != "cuda":
+                raise ValueError("gradients are float32 or bfloat16 CUDA tensors")
+            if g.device != self.device or o.device != self.device:
+                raise ValueError("all tensors must be on one device")
+            if o.dtype != g.dtype or o.shape != g.shape or (g.numel() and o.stride() != g.stride()):
+                raise ValueError("an output needs its gradient's type, shape and strides")
+            if g.numel() and not _dense(g):
+                raise ValueError("gradients and outputs must be dense in memory")
+            size = g.numel() * g.element_size()
+            if size:
+                spans.append((g.data_ptr(), size))
+                if o.data_ptr() != g.data_ptr():
+                    spans.append((o.data_ptr(), size))
+        spans.sort()
+        if any(a + n > b for (a, n), (b, _) in zip(spans, spans[1:])):
+            raise ValueError("gradients and outputs must not overlap")
+        self.grads, self.outs = grads, outs  # kept alive: the list holds their addresses
+        self._own_ctx = ctx is None
+        self.ctx = L.lrm_create(self.device.index or 0) if ctx is None else ctx
+        tensors = L.tensor_array([(g, o, g.numel(), _DTYPES[g.dtype]) for g, o in zip(grads, outs)])
+        need = L.lrm_grad_table_size(tensors, len(grads))
+        self.table = torch.empty(need, dtype=torch.uint8, device=self.device)
+        self.list = L.lrm_grad_list_create(self.ctx, tensors, len(grads), self.table, need, stream)
+        self._stats = torch.zeros(3, dtype=torch.float32, device=self.device)  # lrm_grad_stats
+        self.norm, self.coef = self._stats[0:1], self._stats[1:2]
+        self.nonfinite = self._stats.view(torch.int32)[2:3]
+
+    def close(self):
+        if getattr(self, "list", None):
+            L.lrm_grad_list_destroy(self.list)
+            self.list = None
+        if getattr(self, "_own_ctx", False) and getattr(self, "ctx", None):
+            L.lrm_destroy(self.ctx)
+        self.ctx = None
+
+    def __del__(self):  # pragma: no cover - best effort
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def measure(self, stream=None) -> None:
+        """norm of all gradients, nothing clipped."""
+        L.lrm_grad_norm(self.ctx, self.list, self._stats, stream)
+
+    def clip(self, max_norm: float, stream=None) -> None:
+        """norm, and every gradient times min(1, max_norm / norm) into its output."""
+        L.lrm_grad_clip(self.ctx, self.list, max_norm, self._stats, stream)
 
 
 def to_device_inputs(inp, device="cuda"):

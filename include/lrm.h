@@ -81,8 +81,12 @@ typedef enum lrm_op {
   LRM_OP_ROUTE_STATS = 0,
   LRM_OP_SELECT = 1,
   LRM_OP_ZERO_DROPPED = 2,
-  LRM_OP_COMBINE = 3
+  LRM_OP_COMBINE = 3,
+  LRM_OP_ROUTER = 4
 } lrm_op;
+
+/* Element types of the calls that take more than one. */
+typedef enum lrm_dtype { LRM_F32 = 0, LRM_BF16 = 1 } lrm_dtype;
 
 /* Layer sizes.  Limits: 1 <= E <= 1024, 1 <= k <= 32, k <= E, N = T*k < 2^31,
  * h and I multiples of 8 in [8, 65536]. */
@@ -380,6 +384,125 @@ LRM_API lrm_status lrm_route_stats_noalloc(lrm_ctx* ctx, const float* logits, co
                                            int32_t rho_den, int32_t* counts, int32_t* offsets, int32_t* bucket,
                                            float* P, float* f, int32_t* quota, lrm_route_summary* summary,
                                            void* stream);
+
+/*
+ * The router around the experts' backward: the gates and the balance loss of
+ * a batch, the gate gradient of the retained pairs, and the gradient of the
+ * logits ("Expert Parallel Math Deep": routing as an expectation over a batch
+ * and the load-balancing auxiliary loss).  Only T, E and k of dims are used,
+ * except by lrm_gate_grad.
+ *
+ * lrm_router_forward, per token t with logits l (m = max l, s = sum exp(l - m)):
+ *   expert_idx[t] = the k largest logits in descending order; equal logits
+ *                   (-0 equals +0) go to the lower expert, NaN ranks below -inf
+ *   alpha[t,j]    = exp(l_j) / sum over the k slots (renorm = 1), or
+ *                   exp(l_j - m) / s (renorm = 0)
+ *   row_stats[t]  = (m, s)
+ * and over the counted tokens (Tc of them), with p = exp(l - m) / s:
+ *   n_e = their pairs routed to e, f_e = n_e / (Tc k), P_e = sum p_te / Tc,
+ *   aux = E sum f_e P_e, z = sum (m + ln s)^2 / Tc,
+ *   loss = aux_coef aux + z_coef z.
+ * A token is counted unless valid[t] is 0 or all its logits are -inf.  Every
+ * token gets k distinct experts; one that is not counted gets alpha = 0 and
+ * row_stats = (0, 0), and no value of its logits reaches any other output.
+ * Without a counted token f, P and the losses are 0.  +inf and NaN logits of
+ * a counted token give NaN in its gates and in the sums, as the formulas do.
+ * The same inputs give the same bits.
+ *   logits     [T, E] fp32 or bf16 (logits_dtype, an lrm_dtype)
+ *   valid      [T]    uint8, or NULL: every token is valid
+ *   expert_idx [T, k] int32 out, alpha [T*k] fp32 out, row_stats [T, 2] fp32 out
+ *   counts     [E]    int32 out, f, P [E] fp32 out, losses [1] device struct out
+ *   ws                workspace of lrm_workspace_size(LRM_OP_ROUTER), 256-byte aligned
+ * expert_idx, alpha and logits (fp32) are what lrm_route_stats and lrm_score take.
+ */
+typedef struct lrm_router_losses {
+  float loss, aux, z;
+  int32_t tokens; /* Tc */
+} lrm_router_losses;
+LRM_API lrm_status lrm_router_forward(lrm_ctx* ctx, const void* logits, int32_t logits_dtype, const uint8_t* valid,
+                                      lrm_dims dims, int32_t renorm, float aux_coef, float z_coef,
+                                      int32_t* expert_idx, float* alpha, float* row_stats, int32_t* counts, float* f,
+                                      float* P, lrm_router_losses* losses, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * lrm_gate_grad: the gate weights' gradient on the retained pairs, in the form
+ * the softmax's backward takes it: dgate[u] = alpha_u dL/dalpha_u.  With
+ * y_t = sum_u alpha_u W_e phi_u and dphi_c[r] = (alpha_u g_t) W_e (the rows of
+ * lrm_grouped_dgrad) that is the product <dphi_c[r], phi_c[r]>, summed in fp32
+ * for row r of pair u = sel_ids[r]; pairs that were not retained get 0.
+ *   dphi_c, phi_c [max_rows, I] bf16; dgate [N] fp32 out
+ * Rows at or beyond sel_offsets[E] (clamped to max_rows) are not read.  A
+ * sel_ids entry outside [0, N) sets LRM_ERR_INDEX and is skipped.
+ */
+LRM_API lrm_status lrm_gate_grad(lrm_ctx* ctx, const uint16_t* dphi_c, const uint16_t* phi_c,
+                                 const int32_t* sel_offsets, const int32_t* sel_ids, lrm_dims dims, int32_t max_rows,
+                                 float* dgate, void* stream);
+
+/*
+ * lrm_router_backward: the logits' gradient.  With S = sum_j dgate[t,j] and
+ * lse = m + ln s, a counted token gets
+ *   dlogits[t,e] = aux_coef E / Tc p_e (f_e - sum_i f_i p_i) + 2 z_coef / Tc lse p_e
+ *                  + dgate[t,j] - alpha[t,j] S where e is slot j's expert (renorm = 1), or
+ *                  + dgate[t,j] there and - p_e S everywhere (renorm = 0),
+ * and a token that is not counted gets zeros.  f is a constant of the gradient
+ * (a count has none); it may be the caller's own, for example of a larger batch.
+ *   logits as given to the forward; expert_idx, alpha, row_stats, f and losses
+ *   (only its token count is read) as the forward wrote them
+ *   dgate   [N] fp32 alpha_u dL/dalpha_u, or NULL: no gradient through the gates
+ *   dlogits [T, E] out, fp32 or bf16 (dlogits_dtype), not overlapping an input
+ * An expert id outside [0, E) or repeated within a token sets LRM_ERR_INDEX;
+ * the first slot of a repeated id counts, the others are skipped.
+ */
+LRM_API lrm_status lrm_router_backward(lrm_ctx* ctx, const void* logits, int32_t logits_dtype,
+                                       const int32_t* expert_idx, const float* alpha, const float* row_stats,
+                                       const float* dgate, const float* f, const lrm_router_losses* losses,
+                                       lrm_dims dims, int32_t renorm, float aux_coef, float z_coef, void* dlogits,
+                                       int32_t dlogits_dtype, void* stream);
+
+/*
+ * Global gradient norm and clipping over a list of tensors.
+ *
+ * lrm_grad_list_create writes the list's device table (device memory of
+ * lrm_grad_table_size bytes, 256-byte aligned, owned by the caller and used by
+ * the list alone until lrm_grad_list_destroy) on `stream` and returns a host
+ * handle.  The tensors' addresses are kept, their values are not: a list is
+ * made once for gradients that stay where they are.  It cannot be created
+ * while `stream` is capturing; the calls on it can be captured.
+ *   lrm_tensor: n >= 0 elements of `dtype` at src, aligned to their size; the
+ *   clipped values go to dst (src itself, or memory that overlaps no tensor of
+ *   the list).  A list that is only normed may have dst = NULL.
+ *
+ * lrm_grad_norm: stats->norm = sqrt(sum of the squares of every element of
+ * every tensor), coef = 1.
+ * lrm_grad_clip: coef = max_norm / norm if norm is finite and above max_norm,
+ * else 1, and dst = coef * src in fp32, rounded once to the tensor's type.
+ * In place with coef = 1 nothing is written.  If an element is infinite or NaN,
+ * nonfinite is 1, coef is 1 and norm is that infinity or NaN: the caller skips
+ * its step.  max_norm >= 0; infinity never clips.
+ *
+ * Squares are summed so that neither large nor small values are lost (fp64
+ * where a square would leave fp32's range, and across batches of elements);
+ * the order is fixed, so the same inputs give the same bits.  Calls on one
+ * list share its table: serialise them.
+ */
+typedef struct lrm_tensor {
+  const void* src;
+  void* dst;
+  int64_t n;
+  int32_t dtype; /* lrm_dtype */
+} lrm_tensor;
+typedef struct lrm_grad_stats {
+  float norm, coef;
+  int32_t nonfinite;
+} lrm_grad_stats;
+typedef struct lrm_grad_list lrm_grad_list;
+LRM_API lrm_status lrm_grad_table_size(const lrm_tensor* tensors, int32_t count, size_t* bytes);
+LRM_API lrm_status lrm_grad_list_create(lrm_ctx* ctx, const lrm_tensor* tensors, int32_t count, void* table,
+                                        size_t table_bytes, void* stream, lrm_grad_list** out);
+LRM_API lrm_status lrm_grad_list_destroy(lrm_grad_list* list);
+LRM_API lrm_status lrm_grad_norm(lrm_ctx* ctx, const lrm_grad_list* list, lrm_grad_stats* stats, void* stream);
+LRM_API lrm_status lrm_grad_clip(lrm_ctx* ctx, const lrm_grad_list* list, float max_norm, lrm_grad_stats* stats,
+                                 void* stream);
 
 /* Synchronise `stream`, return the device status word in *flags (bit
  * (1u << code) for every lrm_status code raised on the device since the last

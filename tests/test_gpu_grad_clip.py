@@ -1,0 +1,259 @@
+"""Gradient norm and clipping against the fp64 oracle.
+
+A batch of at most 64 squares is summed in fp32 in four chains: at most 19
+roundings of 2^-24 on the squares, half of that on the norm, and the norm's own
+rounding: 1e-6 relative.  The clipped values are exactly the fp32 product of
+the value and the reported coefficient, rounded once to the type."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from gpu_common import built_library, need_gpu
+
+pytestmark = pytest.mark.gpu
+
+REL = 1e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup():
+    need_gpu()
+    built_library()
+
+
+def _ref(grads, max_norm):
+    """The oracle's values for the limit the call takes (fp32), the norm in the
+    type it is reported in (fp32: its subnormals are coarse)."""
+    norm, coef, out = O.clip([g.double().cpu().numpy() for g in grads], float(np.float32(max_norm)))
+    with np.errstate(over="ignore"):  # a norm above fp32's largest is reported as infinity
+        return float(np.float32(norm)), coef, out
+
+
+def _expect(g, coef):
+    return (g.float() * coef).to(g.dtype)
+
+
+def check(grads, max_norm, in_place=False, outs=None):
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    norm, coef, _ = _ref(grads, max_norm)
+    before = [g.clone() for g in grads]
+    if not in_place and outs is None:
+        outs = [torch.full_like(g, 7.0) for g in grads]
+    c = GradClip(grads, None if in_place else outs)
+    c.clip(max_norm)
+    torch.cuda.synchronize()
+    got = float(c.norm.item())
+    assert got == norm or abs(got - norm) <= REL * norm, (got, norm)
+    assert abs(float(c.coef.item()) - coef) <= 1.2 * REL * coef
+    assert int(c.nonfinite.item()) == 0
+    for b, o, g in zip(before, grads if in_place else outs, grads):
+        assert torch.equal(o, _expect(b, c.coef))
+        if not in_place:
+            assert torch.equal(g, b)
+    if not in_place:
+        c.measure()
+        assert float(c.norm.item()) == got and float(c.coef.item()) == 1.0
+    return c
+
+
+def _tensors(sizes, dtype, seed, scale=0.01):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return [(torch.randn(n, generator=g, device="cuda") * scale).to(dtype) for n in sizes]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sizes", [[1], [2, 3], [7, 8, 9, 1, 16, 17], [31, 4095, 4096, 4097], [8191, 8192, 8193, 1],
+                                   [100003], [1 << 20, 5, 300001], [1] * 1500, list(range(1, 400))])
+def test_sizes(sizes, dtype):
+    grads = _tensors(sizes, dtype, len(sizes))
+    full = math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+    check(grads, 0.5 * full)
+    check(grads, 2.0 * full)
+
+
+def test_mixed_types_in_place():
+    grads = _tensors([1000, 33], torch.float32, 1) + _tensors([70001, 3], torch.bfloat16, 2)
+    check(grads, 0.1, in_place=True)
+    kept = [g.clone() for g in grads]
+    check(grads, 1e9, in_place=True)
+    assert all(torch.equal(a, b) for a, b in zip(kept, grads))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("so,do", [(1, 1), (3, 0), (0, 5), (7, 2), (2, 10)])
+def test_offsets_inside_buffers(dtype, so, do):
+    src = _tensors([20000], dtype, 3)[0]
+    dst = torch.zeros(20000, dtype=dtype, device="cuda")
+    grads = [src[so:so + 9001], src[10000 + so:10000 + so + 5]]
+    outs = [dst[do:do + 9001], dst[10000 + do:10000 + do + 5]]
+    check(grads, 0.05, outs=outs)
+    written = torch.zeros(20000, dtype=torch.bool, device="cuda")
+    written[do:do + 9001] = True
+    written[10000 + do:10000 + do + 5] = True
+    assert not dst[~written].any()
+
+
+def test_empty_and_zero_gradients():
+    c = check(_tensors([0, 5, 0], torch.float32, 4), 0.001)
+    assert c.outs[0].numel() == 0
+    z = [torch.zeros(3000, device="cuda"), torch.zeros(10, dtype=torch.bfloat16, device="cuda")]
+    c = check(z, 0.0)
+    assert float(c.norm.item()) == 0.0 and float(c.coef.item()) == 1.0
+    check(_tensors([0], torch.float32, 5), 1.0)
+    check(_tensors([100], torch.float32, 5), 0.0)  # everything to zero
+
+
+def test_dimension_orders():
+    g = torch.Generator(device="cuda").manual_seed(6)
+    a = torch.randn(6, 5, 7, generator=g, device="cuda")
+    check([a.permute(2, 0, 1), torch.randn(8, 3, generator=g, device="cuda").t()], 0.7,
+          outs=[torch.empty_like(a).permute(2, 0, 1), torch.empty(8, 3, device="cuda").t()])
+
+
+@pytest.mark.parametrize("scale", [1e-44, 1e-38, 1e-30, 1e-20, 1e-15, 1e15, 1e19, 1e30, 3e37])
+def test_magnitudes_whose_squares_leave_fp32(scale):
+    x = torch.linspace(-1, 1, 30001, device="cuda") * scale
+    full = float(_ref([x], 1.0)[0])
+    check([x], 0.25 * full if full * 0.25 > 1e-45 else 1.0)
+    y = (torch.linspace(-1, 1, 3001, device="cuda") * scale).to(torch.bfloat16)
+    check([y, torch.ones(5, device="cuda") * scale], 1.0)
+
+
+def test_mixed_magnitudes():
+    x = torch.full((10000,), 1e-25, device="cuda")
+    x[::97] = 1e22
+    x[5] = 1.0
+    check([x, torch.full((4000,), 1e-3, device="cuda")], 1.0)
+
+
+def test_norm_beyond_fp32_still_scales():
+    # every value is finite and the norm is above fp32's largest: reported as infinity, clipped all the same
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    x = torch.full((1 << 16,), 3e38, device="cuda")
+    out = torch.empty_like(x)
+    c = GradClip([x], [out])
+    c.clip(1.0)
+    assert math.isinf(float(c.norm.item())) and int(c.nonfinite.item()) == 0
+    # the coefficient is a subnormal of fp32: rounded to a multiple of 2^-149
+    coef = 1.0 / (3e38 * 256)
+    assert abs(float(c.coef.item()) - coef) <= 2.0 ** -149
+    assert torch.equal(out, x * c.coef)
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_nonfinite_gradients_are_reported_and_left_alone(value, dtype):
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    for n, at in ((1, 0), (37, 36), (50000, 31234)):
+        grads = _tensors([200, n], dtype, 7)
+        grads[1][at] = value
+        before = [g.clone() for g in grads]
+        outs = [torch.zeros_like(g) for g in grads]
+        c = GradClip(grads, outs)
+        c.clip(0.001)
+        assert int(c.nonfinite.item()) == 1 and float(c.coef.item()) == 1.0
+        assert not math.isfinite(float(c.norm.item())) and math.isnan(float(c.norm.item())) == math.isnan(value)
+        c.measure()
+        assert int(c.nonfinite.item()) == 1
+        d = GradClip(grads)
+        d.clip(0.001)
+        for a, b, o in zip(before, grads, outs):
+            assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
+            assert torch.equal(a.isnan(), o.isnan()) and torch.equal(a.nan_to_num(), o.nan_to_num())
+
+
+def test_infinite_limit_copies():
+    check(_tensors([5000, 3], torch.bfloat16, 8), float("inf"))
+
+
+def test_same_bits_graph_and_streams():
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    grads = _tensors([300000, 77, 1 << 18], torch.float32, 9)
+    outs = [torch.empty_like(g) for g in grads]
+    c = GradClip(grads, outs)
+    c.clip(0.3)
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs] + [c._stats.clone()]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    [o.zero_() for o in outs]
+    torch.cuda.synchronize()
+    c.clip(0.3, stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, outs + [c._stats]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        c.clip(0.3)
+    [g.mul_(2.0) for g in grads]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert abs(float(c.norm.item()) - 2.0 * float(want[-1][0])) <= 4e-7 * float(c.norm.item())
+    for g, o in zip(grads, outs):
+        assert torch.equal(o, g * c.coef)
+
+
+def test_refusals():
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    a, b = _tensors([64, 64], torch.float32, 10)
+    for grads, outs in [([], None), ([a.half()], None), ([a.cpu()], None), ([a], [b, a]), ([a], [b.bfloat16()]),
+                        ([a], [b[:32]]), ([a[::2]], None), ([a.view(8, 8)], [b.view(8, 8).t()]), ([a, a], None),
+                        ([a[:40], a[32:]], None), ([a, b], [b, a]), ([a], [torch.empty(65, device="cuda")[1:][:64].cpu()]),
+                        ([a.expand(3, 64)], None)]:
+        with pytest.raises(ValueError):
+            GradClip(grads, outs)
+    c = GradClip([a], [b])
+    stats = torch.zeros(3, device="cuda")
+    inv = L.LRM_ERR_INVALID_ARG
+    for call, code in [(lambda: L.lrm_grad_clip(c.ctx, c.list, -1.0, stats), inv),
+                       (lambda: L.lrm_grad_clip(c.ctx, c.list, float("nan"), stats), inv),
+                       (lambda: L.lrm_grad_clip(c.ctx, c.list, 1.0, None), inv),
+                       (lambda: L.lrm_grad_clip(c.ctx, None, 1.0, stats), inv),
+                       (lambda: L.lrm_grad_norm(c.ctx, c.list, None), inv),
+                       (lambda: L.lrm_grad_norm(c.ctx, c.list, stats.data_ptr() + 1), L.LRM_ERR_ALIGN)]:
+        with pytest.raises(L.LrmError) as ei:
+            call()
+        assert ei.value.code == code
+    arr = L.tensor_array([(a, None, 64, L.DTYPE_F32)])
+    need = L.lrm_grad_table_size(arr, 1)
+    table = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for t, n, code in [(None, need, L.LRM_ERR_WORKSPACE), (table, need - 1, L.LRM_ERR_WORKSPACE),
+                       (table.data_ptr() + 16, need, L.LRM_ERR_ALIGN)]:
+        with pytest.raises(L.LrmError) as ei:
+            L.lrm_grad_list_create(c.ctx, arr, 1, t, n)
+        assert ei.value.code == code
+    only_norm = L.lrm_grad_list_create(c.ctx, arr, 1, table, need)
+    L.lrm_grad_norm(c.ctx, only_norm, stats)
+    assert abs(float(stats[0]) - float(a.double().norm())) <= REL * float(stats[0])
+    with pytest.raises(L.LrmError) as ei:
+        L.lrm_grad_clip(c.ctx, only_norm, 1.0, stats)
+    assert ei.value.code == inv
+    L.lrm_grad_list_destroy(only_norm)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        with pytest.raises(L.LrmError) as ei:  # a list is made before capturing
+            L.lrm_grad_list_create(c.ctx, arr, 1, table, need, s)
+        a.add_(0.0)
+    assert ei.value.code == inv
+
+
+def test_large_tensor():
+    n = (1 << 27) + 12345
+    x = torch.full((n,), 0.5, device="cuda")
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    c = GradClip([x])
+    c.clip(1.0)
+    assert abs(float(c.norm.item()) - 0.5 * math.sqrt(n)) <= REL * 0.5 * math.sqrt(n)
+    assert torch.all(x == 0.5 * c.coef)
