@@ -69,6 +69,36 @@ inline int resident_grid(const lrm_ctx* ctx, Kern kern, int threads, size_t dyn_
   return per_sm * ctx->sm_count;
 }
 
+// Launches `kern` so that it may start while the kernel before it on the
+// stream still runs (programmatic dependent launch); it must call
+// grid_dependency_wait() before it touches that kernel's results.
+template <typename... Params, typename... Args>
+inline lrm_status launch_dependent(void (*kern)(Params...), int grid, int block, size_t smem, int cluster,
+                                   cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  if (cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return LRM_ERR_CUDA;
+  }
+  return LRM_OK;
+}
+
 inline lrm_status launch_status() {
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? LRM_OK : LRM_ERR_CUDA;
@@ -97,6 +127,12 @@ __device__ __forceinline__ void raise_flag(unsigned int* status, lrm_status code
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
+
+// Waits until the kernels before this one on the stream have completed and
+// their writes are visible (launch_dependent).
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets a kernel launched with launch_dependent after this one start.
+__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;

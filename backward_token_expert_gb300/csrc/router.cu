@@ -3,18 +3,29 @@
 // and the auxiliary loss E sum f_e P_e; the z loss is the mean squared
 // log-partition).
 //
-//   rf_rows    one warp per token.  The k largest logits are taken in k
-//              rounds of a warp-wide maximum over order-preserving integer
-//              keys (ties to the lower expert); the softmax of the same
-//              registers is summed per lane for P, so the logits are read
-//              once.  Every block leaves its sums of p, its counts, its sum
-//              of lse^2 and its number of counted tokens in the workspace.
-//   rf_sums    adds the blocks' sums in a fixed order and writes counts, f, P
-//              and the losses.
-//   rb_rows    one warp per token: p again from the saved (max, sum), the
-//              balance term needs sum_e f_e p_e over the row, and the gates'
-//              part touches k experts, which are placed through a row of
-//              shared memory.
+//   rf_rows    G lanes per token, VPL consecutive logits a lane, so a warp
+//              holds 32 / G tokens (E = 128: a warp a token; E = 8: eight).
+//              The logits are read once, a token ahead.  From the same
+//              registers come the maximum, the softmax (summed per lane for
+//              P) and the k largest.  Every block leaves its sums of p, its
+//              counts, its sum of lse^2 and its counted tokens in the
+//              workspace.
+//   rf_sums    one cluster adds the blocks' sums in a fixed order and writes
+//              counts, f, P and the losses; launched dependently, so that
+//              only its work and not its launch follows rf_rows.  A batch of
+//              one block is finished inside rf_rows.
+//   rb_rows    the same lanes: p again from the saved (max, sum), the balance
+//              term needs sum_e f_e p_e over the row, and the gates' part
+//              touches k experts, which are placed through shared memory.
+//
+// The k largest: a lane sorts its logits as 32-bit keys whose top bits order
+// like the value and whose low log2(G VPL) bits hold the expert, inverted, so
+// that keys are unique and equal values go to the lower expert.  A round is
+// one warp-wide integer maximum; the lane that owns it moves up its list.  For
+// bf16 logits the cut-off bits are zero and the order is exact.  For fp32, two
+// neighbours in the result (or the last one and the next) that agree in all
+// the bits kept send the warp to an exact selection on full keys, as do NaN
+// and rows of -inf.
 #include <math.h>
 
 #include "lrm_internal.cuh"
@@ -23,9 +34,28 @@
 namespace lrm {
 namespace {
 
-constexpr int RT_THREADS = 256;
-constexpr int RT_WARPS = RT_THREADS / 32;
-constexpr int RT_MAX_BLOCKS_PER_SM = 2;  // the grid of rf_rows, and so the workspace
+constexpr int RF_MAX_THREADS = 1024;  // one block an SM: few sums for rf_sums to add
+constexpr int RF_ONE_BLOCK_PASSES = 2;  // batches of up to this many passes of one block use one block
+constexpr int RS_SUM_THREADS = 1024;
+constexpr int RB_THREADS = 256;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+// Lanes per token and logits per lane of a layer: at least four logits a
+// lane (one 16-byte load of fp32), a lane for each of the k slots.
+struct Split {
+  int G, VPL;
+};
+Split split_of(int E, int k) {
+  if (E <= 16 && k <= 4) return {4, 4};
+  if (E <= 32 && k <= 8) return {8, 4};
+  if (E <= 64 && k <= 16) return {16, 4};
+  if (E <= 128) return {32, 4};
+  if (E <= 256) return {32, 8};
+  if (E <= 512) return {32, 16};
+  return {32, 32};
+}
+__host__ __device__ constexpr int rf_threads(int vpl) { return vpl <= 8 ? RF_MAX_THREADS : RF_MAX_THREADS / 4; }
 
 struct RouterLayout {
   int nblk;  // blocks of rf_rows
@@ -34,304 +64,482 @@ struct RouterLayout {
 
 RouterLayout router_layout(const lrm_ctx* ctx, const lrm_dims& d) {
   RouterLayout L;
-  const long long need = (static_cast<long long>(d.T) + RT_WARPS - 1) / RT_WARPS;
-  const long long cap = static_cast<long long>(ctx->sm_count) * RT_MAX_BLOCKS_PER_SM;
+  const Split sp = split_of(d.E, d.k);
+  const long long pass = rf_threads(sp.VPL) / sp.G;  // tokens of a block in flight
+  long long need = (static_cast<long long>(d.T) + pass - 1) / pass;
+  if (need <= RF_ONE_BLOCK_PASSES) need = need > 0 ? 1 : 0;
+  const long long cap = ctx->sm_count;
   L.nblk = static_cast<int>(need < cap ? need : cap);
   const size_t cells = static_cast<size_t>(L.nblk) * d.E;
   L.p_off = 0;
   L.cnt_off = L.p_off + cells * sizeof(float);
   L.z_off = (L.cnt_off + cells * sizeof(int32_t) + 15) / 16 * 16;
-  L.tok_off = L.z_off + L.nblk * sizeof(double);
+  L.tok_off = L.z_off + L.nblk * sizeof(float);
   L.bytes = L.tok_off + L.nblk * sizeof(int32_t);
   return L;
 }
+
+// ---------------------------------------------------------------------------
+// elements
+
+template <typename T>
+constexpr bool is_bf16 = sizeof(T) == 2;
 
 __device__ __forceinline__ float load_elem(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
 __device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// A key that orders like the value: NaN is 1, -inf the next, -0 like +0.  0 is
-// left for places that hold no logit.
+// VPL consecutive logits of a lane as they lie in memory; places beyond the
+// row hold -inf.  vec: rows start at a multiple of four elements' bytes.
+template <typename TL, int VPL>
+struct Raw {
+  uint32_t w[VPL * sizeof(TL) / 4];
+
+  __device__ __forceinline__ void load(const TL* __restrict__ row, int e0, int E, bool vec) {
+    if (vec) {
+#pragma unroll
+      for (int c = 0; c < VPL / 4; ++c) {
+        const bool in = e0 + 4 * c < E;
+        if constexpr (is_bf16<TL>) {
+          const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(row + e0) + c) : make_uint2(0xFF80FF80u, 0xFF80FF80u);
+          w[2 * c] = x.x;
+          w[2 * c + 1] = x.y;
+        } else {
+          const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(row + e0) + c)
+                             : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+          w[4 * c] = x.x;
+          w[4 * c + 1] = x.y;
+          w[4 * c + 2] = x.z;
+          w[4 * c + 3] = x.w;
+        }
+      }
+    } else if constexpr (is_bf16<TL>) {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+      for (int i = 0; i < VPL / 2; ++i) {
+        const uint32_t lo = e0 + 2 * i < E ? __ldg(p + e0 + 2 * i) : 0xFF80u;
+        const uint32_t hi = e0 + 2 * i + 1 < E ? __ldg(p + e0 + 2 * i + 1) : 0xFF80u;
+        w[i] = lo | hi << 16;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        w[i] = e0 + i < E ? __float_as_uint(__ldg(reinterpret_cast<const float*>(row) + e0 + i)) : 0xFF800000u;
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (is_bf16<TL>)
+      return (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    else
+      return __uint_as_float(w[i]);
+  }
+};
+
+template <typename TO, int VPL>
+__device__ __forceinline__ void store_row(TO* __restrict__ row, int e0, int E, bool vec, const float (&v)[VPL]) {
+  if (vec) {
+#pragma unroll
+    for (int c = 0; c < VPL / 4; ++c) {
+      if (e0 + 4 * c >= E) continue;
+      if constexpr (is_bf16<TO>) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[4 * c], v[4 * c + 1]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[4 * c + 2], v[4 * c + 3]);
+        reinterpret_cast<uint2*>(row + e0)[c] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      } else {
+        reinterpret_cast<float4*>(row + e0)[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (e0 + i < E) store_elem(row + e0 + i, v[i]);
+  }
+}
+
+// e^x for x <= 0 as 2^(x log2 e): the product's rounding is 2^-24 |x| log2 e in
+// the exponent, so the relative error is about 6e-8 |x| + 2 ulp, largest where
+// the term itself is smallest; results below 2^-126 are 0.
+__device__ __forceinline__ float exp_neg(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * LOG2E));
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// keys and group reductions
+
+// A key that orders like the value (-0 like +0; NaN has no place).
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
-  const uint32_t key = b ^ ((b & 0x80000000u) ? 0xFFFFFFFFu : 0x80000000u);
-  return v != v ? 1u : key;
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The group's largest value, NaN left out unless there is nothing else.
+template <int G>
+__device__ __forceinline__ float group_fmax(float v) {
+  if constexpr (G == 32) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (G == 32) {
+    return __reduce_max_sync(0xffffffffu, v);
+  } else {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+
+// The sum over a group whose lanes from k on hold 0, valid in the lanes below k.
+template <int G>
+__device__ __forceinline__ float slot_sum(float v, int k) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = 1; o < G; o <<= 1)
+    if (o < k) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-template <typename TL, int VPL>
-__global__ void __launch_bounds__(RT_THREADS) rf_rows(const TL* __restrict__ logits,
-                                                      const uint8_t* __restrict__ valid, int T, int E, int k,
-                                                      int renorm, int32_t* __restrict__ expert_idx,
-                                                      float* __restrict__ alpha, float2* __restrict__ row_stats,
-                                                      float* __restrict__ ws_p, int32_t* __restrict__ ws_cnt,
-                                                      double* __restrict__ ws_z, int32_t* __restrict__ ws_tok) {
-  extern __shared__ float rt_smem[];
-  float* sp = rt_smem;                                        // [RT_WARPS][E]
-  int* hist = reinterpret_cast<int*>(rt_smem + RT_WARPS * E);  // [E]
-  __shared__ double s_z[RT_WARPS];
-  __shared__ int s_tok[RT_WARPS];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < E; i += RT_THREADS) hist[i] = 0;
-  __syncthreads();
-
-  float acc[VPL];
+// Descending sort of a lane's keys: Batcher's odd-even merge sort.
+template <int N>
+__device__ __forceinline__ void sort_desc(uint32_t (&a)[N]) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
-  double z = 0.0;
-  int tokens = 0;
-  const long long step = static_cast<long long>(gridDim.x) * RT_WARPS;
-  for (long long t = static_cast<long long>(blockIdx.x) * RT_WARPS + warp; t < T; t += step) {
-    const TL* row = logits + static_cast<size_t>(t) * E;
-    float v[VPL];
-    uint32_t key[VPL];
+  for (int p = 1; p < N; p *= 2) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      v[i] = e < E ? load_elem(row + e) : -INFINITY;
-      key[i] = e < E ? order_key(v[i]) : 0u;
-    }
-    float m = v[0];
+    for (int k = p; k >= 1; k /= 2) {
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) m = fmaxf(m, v[i]);
-    m = warp_max(m);
-    const float base = m == -INFINITY ? 0.f : m;
-    float p[VPL], s = 0.f;
+      for (int j = k % p; j + k < N; j += 2 * k) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      p[i] = expf(v[i] - base);
-      s += p[i];
-    }
-    s = warp_sum(s);
-    const bool counted = s != 0.f && (valid == nullptr || valid[t] != 0);
-
-    // slot j's expert and exponential go to lane j
-    int my_e = 0;
-    float my_p = 0.f;
-    for (int j = 0; j < k; ++j) {
-      uint32_t best = key[0];
-      int e = lane;
-      float pe = p[0];
-#pragma unroll
-      for (int i = 1; i < VPL; ++i)
-        if (key[i] > best) best = key[i], e = lane + 32 * i, pe = p[i];
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      const int win = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(e) : ~0u));
-      const float wp = __shfl_sync(0xffffffffu, pe, win & 31);
-      if (lane == j) my_e = win, my_p = wp;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (win == lane + 32 * i) key[i] = 0u;
-    }
-    const float sel = warp_sum(my_p);  // lanes beyond k hold 0
-    if (lane < k) {
-      const size_t u = static_cast<size_t>(t) * k + lane;
-      expert_idx[u] = my_e;
-      alpha[u] = counted ? my_p / (renorm ? sel : s) : 0.f;
-      if (counted) atomicAdd(&hist[my_e], 1);
-    }
-    if (lane == 0) row_stats[t] = counted ? make_float2(base, s) : make_float2(0.f, 0.f);
-    if (counted) {
-      const float inv = 1.f / s;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[i] += p[i] * inv;
-      const float lse = base + logf(s);
-      z += static_cast<double>(lse) * lse;
-      ++tokens;
+        for (int i = 0; i < k; ++i) {
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t hi = max(a[i + j], a[i + j + k]), lo = min(a[i + j], a[i + j + k]);
+            a[i + j] = hi;
+            a[i + j + k] = lo;
+          }
+        }
+      }
     }
   }
+}
+
+// The exact selection: k rounds over full keys, NaN below -inf, equal keys to
+// the lower expert (the lower lane, then the lower place).  Returns slot q's
+// expert.
+template <typename TL, int G, int VPL>
+__device__ __noinline__ int select_exact(Raw<TL, VPL> raw, int E, int k) {
+  const int lane = threadIdx.x & 31, q = lane % G;
+  const unsigned group = (G == 32 ? 0xffffffffu : ((1u << G) - 1u)) << (lane - q);
+  uint32_t key[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 32 * i;
-    if (e < E) sp[warp * E + e] = acc[i];
+    const float v = raw.get(i);
+    key[i] = q * VPL + i >= E ? 0u : v != v ? 1u : order_key(v);
   }
-  if (lane == 0) s_z[warp] = z, s_tok[warp] = tokens;
-  __syncthreads();
-  for (int e = tid; e < E; e += RT_THREADS) {
-    float a = 0.f;
+  int mine = 0;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = key[0];
+    int at = 0;
 #pragma unroll
-    for (int w = 0; w < RT_WARPS; ++w) a += sp[w * E + e];
-    ws_p[static_cast<size_t>(blockIdx.x) * E + e] = a;
-    ws_cnt[static_cast<size_t>(blockIdx.x) * E + e] = hist[e];
-  }
-  if (tid == 0) {
-    double a = 0.0;
-    int n = 0;
-    for (int w = 0; w < RT_WARPS; ++w) a += s_z[w], n += s_tok[w];
-    ws_z[blockIdx.x] = a;
-    ws_tok[blockIdx.x] = n;
-  }
-}
-
-// One block of 1024 threads: thread e owns expert e.
-__global__ void __launch_bounds__(1024) rf_sums(const float* __restrict__ ws_p, const int32_t* __restrict__ ws_cnt,
-                                                const double* __restrict__ ws_z, const int32_t* __restrict__ ws_tok,
-                                                int nblk, int E, int k, float aux_coef, float z_coef,
-                                                int32_t* __restrict__ counts, float* __restrict__ f,
-                                                float* __restrict__ P, lrm_router_losses* __restrict__ losses) {
-  __shared__ double s_red[32];
-  __shared__ double s_z;
-  __shared__ int s_tok;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (warp == 0) {
-    double z = 0.0;
-    int n = 0;
-    for (int b = lane; b < nblk; b += 32) z += ws_z[b], n += ws_tok[b];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      z += __shfl_xor_sync(0xffffffffu, z, o);
-      n += __shfl_xor_sync(0xffffffffu, n, o);
-    }
-    if (lane == 0) s_z = z, s_tok = n;
-  }
-  __syncthreads();
-  const int tokens = s_tok;
-  double fp = 0.0;
-  for (int e = tid; e < E; e += 1024) {
-    double a = 0.0;
-    int n = 0;
-    for (int b = 0; b < nblk; ++b) {
-      a += ws_p[static_cast<size_t>(b) * E + e];
-      n += ws_cnt[static_cast<size_t>(b) * E + e];
-    }
-    const float Pe = tokens > 0 ? static_cast<float>(a / tokens) : 0.f;
-    const float fe = tokens > 0 ? static_cast<float>(static_cast<double>(n) / (static_cast<double>(tokens) * k)) : 0.f;
-    counts[e] = n;
-    P[e] = Pe;
-    f[e] = fe;
-    fp += static_cast<double>(fe) * Pe;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) fp += __shfl_xor_sync(0xffffffffu, fp, o);
-  if (lane == 0) s_red[warp] = fp;
-  __syncthreads();
-  if (tid == 0) {
-    double a = 0.0;
-    for (int w = 0; w < 32; ++w) a += s_red[w];
-    const double aux = a * E, zl = tokens > 0 ? s_z / tokens : 0.0;
-    lrm_router_losses r;
-    r.aux = static_cast<float>(aux);
-    r.z = static_cast<float>(zl);
-    r.loss = static_cast<float>(aux_coef * aux + z_coef * zl);
-    r.tokens = tokens;
-    *losses = r;
-  }
-}
-
-template <typename TL, typename TO, int VPL>
-__global__ void __launch_bounds__(RT_THREADS) rb_rows(const TL* __restrict__ logits,
-                                                      const int32_t* __restrict__ expert_idx,
-                                                      const float* __restrict__ alpha,
-                                                      const float2* __restrict__ row_stats,
-                                                      const float* __restrict__ dgate, const float* __restrict__ f,
-                                                      const lrm_router_losses* __restrict__ losses, int T, int E,
-                                                      int k, int renorm, float aux_coef, float z_coef,
-                                                      TO* __restrict__ dlogits, unsigned int* status) {
-  extern __shared__ float rt_smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* add = rt_smem + warp * E;  // the gates' part of this warp's row
-  for (int e = lane; e < E; e += 32) add[e] = 0.f;
-  float fe[VPL];
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) fe[i] = lane + 32 * i < E ? f[lane + 32 * i] : 0.f;
-  const float tokens = static_cast<float>(max(1, losses->tokens));
-  const float ca = aux_coef * static_cast<float>(E) / tokens, cz = 2.f * z_coef / tokens;
-  __syncwarp();
-  const long long step = static_cast<long long>(gridDim.x) * RT_WARPS;
-  for (long long t = static_cast<long long>(blockIdx.x) * RT_WARPS + warp; t < T; t += step) {
-    TO* out = dlogits + static_cast<size_t>(t) * E;
-    const float2 ms = row_stats[t];
-    if (ms.y == 0.f) {  // not counted
+    for (int i = 1; i < VPL; ++i)
+      if (key[i] > best) best = key[i], at = i;
+    const uint32_t top = group_max<G>(best);
+    const int win = __ffs(__ballot_sync(0xffffffffu, best == top) & group) - 1;
+    const int e = __shfl_sync(0xffffffffu, q * VPL + at, win);
+    if (q == j) mine = e;
+    if (lane == win) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < E) store_elem(out + lane + 32 * i, 0.f);
-      continue;
+        if (i == at) key[i] = 0u;
     }
-    const TL* row = logits + static_cast<size_t>(t) * E;
-    const float inv = 1.f / ms.y;
-    float p[VPL], fp = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      p[i] = lane + 32 * i < E ? expf(load_elem(row + lane + 32 * i) - ms.x) * inv : 0.f;
-      fp = fmaf(fe[i], p[i], fp);
-    }
-    fp = warp_sum(fp);
-    float S = 0.f;
-    int my_e = -1;
-    if (dgate != nullptr) {
-      const size_t u = static_cast<size_t>(t) * k + lane;
-      float dg = 0.f;
-      int e = -1 - lane;  // distinct among the lanes
-      if (lane < k) {
-        const int id = expert_idx[u];
-        if (id >= 0 && id < E) e = id, dg = dgate[u];
-      }
-      const unsigned peers = __match_any_sync(0xffffffffu, e);
-      const bool first = (peers & ((1u << lane) - 1u)) == 0;
-      if (lane < k && (e < 0 || !first)) raise_flag(status, LRM_ERR_INDEX);
-      if (!first) dg = 0.f;
-      S = warp_sum(dg);
-      if (e >= 0 && first) {
-        my_e = e;
-        add[e] = renorm ? dg - alpha[u] * S : dg;
-      }
-      __syncwarp();
-    }
-    const float zt = cz * (ms.x + logf(ms.y)) - (renorm ? 0.f : S);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E) store_elem(out + e, fmaf(p[i], fmaf(ca, fe[i] - fp, zt), add[e]));
-    }
-    __syncwarp();
-    if (my_e >= 0) add[my_e] = 0.f;
-    __syncwarp();
   }
+  return mine;
 }
+
+// ---------------------------------------------------------------------------
+// forward
 
 struct ForwardArgs {
   const uint8_t* valid;
-  lrm_dims d;
-  int renorm;
+  int T, E, k, renorm;
+  float aux_coef, z_coef;
   int32_t* expert_idx;
   float* alpha;
   float2* row_stats;
   float* ws_p;
   int32_t* ws_cnt;
-  double* ws_z;
+  float* ws_z;
   int32_t* ws_tok;
+  int32_t* counts;
+  float *f, *P;
+  lrm_router_losses* losses;
 };
 
-template <typename TL, int VPL>
-lrm_status launch_rf(const TL* logits, const ForwardArgs& a, int nblk, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(RT_WARPS + 1) * a.d.E * sizeof(float);
-  rf_rows<TL, VPL><<<nblk, RT_THREADS, smem, s>>>(logits, a.valid, a.d.T, a.d.E, a.d.k, a.renorm, a.expert_idx,
-                                                  a.alpha, a.row_stats, a.ws_p, a.ws_cnt, a.ws_z, a.ws_tok);
-  return launch_status();
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
 }
 
-template <typename TL>
-lrm_status dispatch_rf(const void* logits, const ForwardArgs& a, int nblk, cudaStream_t s) {
-  const TL* l = static_cast<const TL*>(logits);
-  const int vpl = (a.d.E + 31) / 32;
-  if (vpl <= 1) return launch_rf<TL, 1>(l, a, nblk, s);
-  if (vpl <= 2) return launch_rf<TL, 2>(l, a, nblk, s);
-  if (vpl <= 4) return launch_rf<TL, 4>(l, a, nblk, s);
-  if (vpl <= 8) return launch_rf<TL, 8>(l, a, nblk, s);
-  if (vpl <= 16) return launch_rf<TL, 16>(l, a, nblk, s);
-  return launch_rf<TL, 32>(l, a, nblk, s);
+__device__ __forceinline__ float ld_cluster_f32(const float* p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(p, rank)) : "memory");
+  return v;
 }
+
+__device__ __forceinline__ float warp_sum(float v) { return group_sum<32>(v); }
+
+// counts, P and f of expert e from its sums; returns f P.
+__device__ __forceinline__ float write_expert(const ForwardArgs& a, int e, float p, int c, int tokens) {
+  const float Pe = tokens > 0 ? __fdiv_rn(p, static_cast<float>(tokens)) : 0.f;
+  const long long pairs = static_cast<long long>(tokens) * a.k;
+  float fe = 0.f;
+  if (tokens > 0)  // correctly rounded: fp32 holds integers up to 2^24
+    fe = pairs <= (1 << 24) ? __fdiv_rn(static_cast<float>(c), static_cast<float>(pairs))
+                            : static_cast<float>(static_cast<double>(c) / static_cast<double>(pairs));
+  a.counts[e] = c;
+  a.P[e] = Pe;
+  a.f[e] = fe;
+  return fe * Pe;
+}
+
+__device__ __forceinline__ void write_losses(const ForwardArgs& a, float fp, float z, int tokens) {
+  lrm_router_losses r;
+  r.aux = static_cast<float>(a.E) * fp;
+  r.z = tokens > 0 ? __fdiv_rn(z, static_cast<float>(tokens)) : 0.f;
+  r.loss = fmaf(a.aux_coef, r.aux, a.z_coef * r.z);
+  r.tokens = tokens;
+  *a.losses = r;
+}
+
+// Adds nblk blocks' sums.  The cluster's CTAs share the experts; a warp adds
+// every 32nd row of 32 experts, then warp w the warps' sums of the w-th expert.
+__global__ void __launch_bounds__(RS_SUM_THREADS) rf_sums(ForwardArgs a, int nblk) {
+  constexpr int NW = RS_SUM_THREADS / 32;
+  __shared__ float s_p[NW][33];
+  __shared__ int s_c[NW][33];
+  __shared__ float s_fp[NW];
+  __shared__ float s_total;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank()), ranks = static_cast<int>(cluster_nctarank());
+  const int per = (a.E + ranks - 1) / ranks;
+  const int e0 = min(a.E, rank * per), e1 = min(a.E, e0 + per);
+  grid_dependency_wait();
+  float z = 0.f, fp = 0.f;
+  int tokens = 0;
+  for (int b = lane; b < nblk; b += 32) z += a.ws_z[b], tokens += a.ws_tok[b];
+  z = warp_sum(z);
+  tokens = __reduce_add_sync(0xffffffffu, tokens);
+  for (int c0 = e0; c0 < e1; c0 += 32) {
+    const int e = c0 + lane;
+    float p = 0.f;
+    int c = 0;
+    if (e < e1) {
+#pragma unroll 8
+      for (int b = warp; b < nblk; b += NW) {
+        p += a.ws_p[static_cast<size_t>(b) * a.E + e];
+        c += a.ws_cnt[static_cast<size_t>(b) * a.E + e];
+      }
+    }
+    s_p[warp][lane] = p;
+    s_c[warp][lane] = c;
+    __syncthreads();
+    p = warp_sum(s_p[lane][warp]);
+    c = __reduce_add_sync(0xffffffffu, s_c[lane][warp]);
+    if (c0 + warp < e1 && lane == 0) fp += write_expert(a, c0 + warp, p, c, tokens);
+    __syncthreads();
+  }
+  if (lane == 0) s_fp[warp] = fp;
+  __syncthreads();
+  if (warp == 0) {
+    fp = warp_sum(s_fp[lane]);
+    if (lane == 0) s_total = fp;
+  }
+  if (ranks > 1) cluster_sync_all();
+  if (rank == 0 && warp == 0) {
+    if (ranks > 1) fp = warp_sum(lane < ranks ? ld_cluster_f32(&s_total, lane) : 0.f);
+    if (lane == 0) write_losses(a, fp, z, tokens);
+  }
+  if (ranks > 1) cluster_sync_all();  // s_total stays until rank 0 has read it
+}
+
+template <typename TL, int G, int VPL>
+__global__ void __launch_bounds__(rf_threads(VPL), 1) rf_rows(const TL* __restrict__ logits, ForwardArgs a, bool vec) {
+  constexpr int NT = rf_threads(VPL), NW = NT / 32, PER_WARP = 32 / G;
+  constexpr uint32_t LOW = G * VPL - 1;  // the key's bits that hold the expert
+  extern __shared__ float rt_smem[];
+  float* sp = rt_smem;                                     // [NW][E]
+  int* hist = reinterpret_cast<int*>(rt_smem + NW * a.E);  // [E]
+  __shared__ uint32_t s_sel[NW][32];                       // the slots' keys
+  __shared__ float s_z[NW];
+  __shared__ int s_tok[NW];
+  __shared__ float s_fp[NW];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = lane % G, e0 = q * VPL;
+  const int T = a.T, E = a.E, k = a.k;
+  uint32_t* sel = s_sel[warp] + (lane - q);
+  grid_dependency_launch();
+  for (int i = tid; i < E; i += NT) hist[i] = 0;
+  __syncthreads();
+
+  float acc[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+  // (m, s) of the group's counted tokens are kept a lane each until G are there
+  float z = 0.f, km = 0.f, ks = 1.f;
+  int held = 0, tokens = 0;
+  // tokens lie 32-bit (T < 2^31); the first token of the warp, its groups' tokens follow
+  const long long step = static_cast<long long>(gridDim.x) * NW * PER_WARP;
+  long long t = (static_cast<long long>(blockIdx.x) * NW + warp) * PER_WARP + lane / G;
+  const TL* row = logits + static_cast<size_t>(t) * E;
+  const size_t row_step = static_cast<size_t>(step) * E;
+  Raw<TL, VPL> next;
+  next.load(row, e0, t < T ? E : 0, vec);
+  for (; t - lane / G < T; t += step, row += row_step) {
+    const bool here = G == 32 || t < T;
+    const Raw<TL, VPL> raw = next;
+    next.load(row + row_step, e0, t + step < T ? E : 0, vec);
+    bool ok = here;
+    if (a.valid != nullptr && here) ok = a.valid[t] != 0;
+
+    float m = raw.get(0);
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, raw.get(i));
+    m = group_fmax<G>(m);
+    const float base = m == -INFINITY ? 0.f : m;
+    uint32_t key[VPL];
+    float p[VPL], s = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const float d = raw.get(i) - base;  // <= 0: the larger its bits, the smaller it is
+      const uint32_t order = is_bf16<TL> ? order_key(raw.get(i)) : ~__float_as_uint(d);
+      key[i] = (order & ~LOW) | (LOW - (e0 + i));
+      p[i] = exp_neg(d);
+      s += p[i];
+    }
+    s = group_sum<G>(s);
+    const bool counted = ok && s != 0.f;
+
+    sort_desc(key);
+#pragma unroll 4
+    for (int j = 0; j < k; ++j) {
+      const uint32_t top = group_max<G>(key[0]);
+      if (key[0] == top) {
+        sel[j] = top;
+#pragma unroll
+        for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
+        key[VPL - 1] = 0u;
+      }
+    }
+    uint32_t after = 0;  // the largest key left out
+    if constexpr (!is_bf16<TL>) after = group_max<G>(key[0]);
+    __syncwarp();
+    const bool slot = q < k && here;
+    const uint32_t mine = sel[q];
+    int e = static_cast<int>(LOW - (mine & LOW));
+    float v = slot ? load_elem(row + e) : 0.f;
+    bool unclear = here && !(s > 0.f);
+    if constexpr (!is_bf16<TL>) {
+      const float vn = __shfl_down_sync(0xffffffffu, v, 1, G);
+      unclear = unclear || (slot && (q == k - 1 ? (mine ^ after) <= LOW : v < vn));
+    }
+    if (__any_sync(0xffffffffu, unclear)) {
+      e = select_exact<TL, G, VPL>(raw, E, k);
+      if (slot) v = load_elem(row + e);
+    }
+    __syncwarp();  // sel is read before the next token writes it
+
+    const float pj = slot ? exp_neg(v - base) : 0.f;
+    const float den = a.renorm ? slot_sum<G>(pj, k) : s;
+    if (slot) {
+      const size_t u = static_cast<size_t>(t) * k + q;
+      a.expert_idx[u] = e;
+      a.alpha[u] = counted ? pj * rcp(den) : 0.f;
+      if (counted) atomicAdd(&hist[e], 1);
+    }
+    if (q == 0 && here) a.row_stats[t] = counted ? make_float2(base, s) : make_float2(0.f, 0.f);
+    if (counted) {
+      const float inv = rcp(s);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
+      if (q == held) km = base, ks = s;
+      ++tokens;
+      if (++held == G) {
+        const float lse = km + logf(ks);
+        z = fmaf(lse, lse, z);
+        held = 0;
+      }
+    }
+  }
+  if (q < held) {
+    const float lse = km + logf(ks);
+    z = fmaf(lse, lse, z);
+  }
+
+  // the block's sums, in a fixed order
+  z = warp_sum(z);
+  tokens = __reduce_add_sync(0xffffffffu, q == 0 ? tokens : 0);
+  if (lane == 0) s_z[warp] = z, s_tok[warp] = tokens;
+#pragma unroll
+  for (int o = G; o < 32; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+  }
+  if (lane < G) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (e0 + i < E) sp[warp * E + e0 + i] = acc[i];
+  }
+  __syncthreads();
+  const bool alone = gridDim.x == 1;
+  z = warp_sum(lane < NW ? s_z[lane] : 0.f);
+  tokens = __reduce_add_sync(0xffffffffu, lane < NW ? s_tok[lane] : 0);
+  float fp = 0.f;
+  for (int e = tid; e < E; e += NT) {
+    float own = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) own += sp[w * E + e];
+    if (alone) {
+      fp += write_expert(a, e, own, hist[e], tokens);
+    } else {
+      a.ws_p[static_cast<size_t>(blockIdx.x) * E + e] = own;
+      a.ws_cnt[static_cast<size_t>(blockIdx.x) * E + e] = hist[e];
+    }
+  }
+  if (!alone) {
+    if (tid == 0) a.ws_z[blockIdx.x] = z, a.ws_tok[blockIdx.x] = tokens;
+    return;
+  }
+  fp = warp_sum(fp);
+  if (lane == 0) s_fp[warp] = fp;
+  __syncthreads();
+  if (warp == 0) {
+    fp = warp_sum(lane < NW ? s_fp[lane] : 0.f);
+    if (lane == 0) write_losses(a, fp, z, tokens);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// backward
 
 struct BackwardArgs {
   const int32_t* expert_idx;
@@ -340,32 +548,179 @@ struct BackwardArgs {
   const float* dgate;
   const float* f;
   const lrm_router_losses* losses;
-  lrm_dims d;
-  int renorm;
+  int T, E, k, renorm;
   float aux_coef, z_coef;
   unsigned int* status;
 };
 
-template <typename TL, typename TO, int VPL>
-lrm_status launch_rb(const TL* logits, TO* dlogits, const BackwardArgs& a, int grid, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(RT_WARPS) * a.d.E * sizeof(float);
-  rb_rows<TL, TO, VPL><<<grid, RT_THREADS, smem, s>>>(logits, a.expert_idx, a.alpha, a.row_stats, a.dgate, a.f,
-                                                      a.losses, a.d.T, a.d.E, a.d.k, a.renorm, a.aux_coef, a.z_coef,
-                                                      dlogits, a.status);
+// What a lane reads of one token.
+template <typename TL, int VPL>
+struct TokenIn {
+  Raw<TL, VPL> raw;
+  float2 ms;  // (max, sum); sum 0: not counted
+  int id;
+  float dg, al;
+};
+
+template <typename TL, typename TO, int G, int VPL>
+__global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ logits, TO* __restrict__ dlogits,
+                                                      BackwardArgs a, bool vec_in, bool vec_out) {
+  constexpr int NW = RB_THREADS / 32, PER_WARP = 32 / G;
+  __shared__ float4 s_add[NW][32 * VPL / 4];  // the gates' part of the warp's tokens
+  __shared__ uint8_t s_slot[NW][32 * VPL];    // the slot that named an expert last
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane % G, e0 = q * VPL;
+  const int T = a.T, E = a.E, k = a.k;
+  float* add = reinterpret_cast<float*>(s_add[warp]) + (lane - q) * VPL;  // the group's rows
+  uint8_t* slot_of = s_slot[warp] + (lane - q) * VPL;
+  float4* own = s_add[warp] + lane * (VPL / 4);
+#pragma unroll
+  for (int c = 0; c < VPL / 4; ++c) own[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float tc = static_cast<float>(max(1, a.losses->tokens));
+  const float ca = a.aux_coef * static_cast<float>(E) / tc, cz = 2.f * a.z_coef / tc;
+  float cf[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) cf[i] = e0 + i < E ? ca * a.f[e0 + i] : 0.f;
+  __syncwarp();
+
+  const bool gates = a.dgate != nullptr;
+  const long long step = static_cast<long long>(gridDim.x) * NW * PER_WARP;
+  long long t = (static_cast<long long>(blockIdx.x) * NW + warp) * PER_WARP + lane / G;
+  const auto load = [&](long long at) {
+    TokenIn<TL, VPL> x;
+    const bool in = at < T;
+    x.raw.load(logits + static_cast<size_t>(at) * E, e0, in ? E : 0, vec_in);
+    x.ms = in ? __ldg(a.row_stats + at) : make_float2(0.f, 0.f);
+    x.id = 0;
+    x.dg = x.al = 0.f;
+    if (gates && in && q < k) {
+      const size_t u = static_cast<size_t>(at) * k + q;
+      x.id = __ldg(a.expert_idx + u);
+      x.dg = __ldg(a.dgate + u);
+      x.al = __ldg(a.alpha + u);
+    }
+    return x;
+  };
+  TokenIn<TL, VPL> next = load(t);
+  for (; t - lane / G < T; t += step) {
+    const bool here = G == 32 || t < T;
+    const TokenIn<TL, VPL> x = next;
+    next = load(t + step);
+    const bool counted = x.ms.y != 0.f;
+    const float inv = rcp(x.ms.y);
+    float p[VPL], fp = 0.f, dg = x.dg;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) p[i] = exp_neg(x.raw.get(i) - x.ms.x) * inv;
+    int e = gates && counted && q < k ? x.id : -1;
+    if (!counted) {
+      dg = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) p[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) fp = fmaf(cf[i], p[i], fp);
+    float w = 0.f;
+    if (gates) {
+      bool bad = static_cast<unsigned>(e) >= static_cast<unsigned>(E);
+      if (!bad) slot_of[e] = static_cast<uint8_t>(q);
+      __syncwarp();
+      const bool lost = !bad && slot_of[e] != q;
+      bad = bad && counted && q < k;
+      if (__any_sync(0xffffffffu, bad || lost)) {  // an id out of range, or one named by several slots
+        const bool in = !bad && e >= 0;
+        const unsigned peers = __match_any_sync(0xffffffffu, in ? ((lane - q) << 16) | e : -1 - lane);
+        if (bad || (in && (peers & ((1u << lane) - 1u)) != 0)) {
+          raise_flag(a.status, LRM_ERR_INDEX);
+          e = -1;
+          dg = 0.f;
+        }
+      }
+      if (a.renorm) {
+        const float S = slot_sum<G>(dg, k);
+        if (e >= 0) add[e] = fmaf(-x.al, S, dg);
+      } else {
+        fp += dg;  // p_e takes off S = sum dg like the balance term's sum
+        if (e >= 0) add[e] = dg;
+      }
+      __syncwarp();
+    }
+    w -= group_sum<G>(fp);
+    if (cz != 0.f && counted) w = fmaf(cz, x.ms.x + __log2f(x.ms.y) * LN2, w);
+    float out[VPL];
+#pragma unroll
+    for (int c = 0; c < VPL / 4; ++c) {
+      const float4 g = own[c];
+      out[4 * c] = fmaf(p[4 * c], cf[4 * c] + w, g.x);
+      out[4 * c + 1] = fmaf(p[4 * c + 1], cf[4 * c + 1] + w, g.y);
+      out[4 * c + 2] = fmaf(p[4 * c + 2], cf[4 * c + 2] + w, g.z);
+      out[4 * c + 3] = fmaf(p[4 * c + 3], cf[4 * c + 3] + w, g.w);
+    }
+    if (!counted) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) out[i] = 0.f;
+    }
+    if (here) store_row<TO, VPL>(dlogits + static_cast<size_t>(t) * E, e0, E, vec_out, out);
+    __syncwarp();
+    if (e >= 0) add[e] = 0.f;
+    __syncwarp();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+
+template <typename TL, int G, int VPL>
+lrm_status launch_rf(const TL* logits, const ForwardArgs& a, int nblk, bool vec, cudaStream_t s) {
+  constexpr int NT = rf_threads(VPL);
+  const size_t smem = static_cast<size_t>(NT / 32 + 1) * a.E * sizeof(float);
+  rf_rows<TL, G, VPL><<<nblk, NT, smem, s>>>(logits, a, vec);
+  return launch_status();
+}
+
+// rows of four-element groups that start on the group's bytes
+template <typename T>
+bool rows_vec(const T* p, int E) {
+  return E % 4 == 0 && aligned(p, 4 * sizeof(T));
+}
+
+template <typename TL>
+lrm_status dispatch_rf(const void* logits, const ForwardArgs& a, int nblk, cudaStream_t s) {
+  const TL* l = static_cast<const TL*>(logits);
+  const bool vec = rows_vec(l, a.E);
+  const Split sp = split_of(a.E, a.k);
+  if (sp.G == 4) return launch_rf<TL, 4, 4>(l, a, nblk, vec, s);
+  if (sp.G == 8) return launch_rf<TL, 8, 4>(l, a, nblk, vec, s);
+  if (sp.G == 16) return launch_rf<TL, 16, 4>(l, a, nblk, vec, s);
+  if (sp.VPL == 4) return launch_rf<TL, 32, 4>(l, a, nblk, vec, s);
+  if (sp.VPL == 8) return launch_rf<TL, 32, 8>(l, a, nblk, vec, s);
+  if (sp.VPL == 16) return launch_rf<TL, 32, 16>(l, a, nblk, vec, s);
+  return launch_rf<TL, 32, 32>(l, a, nblk, vec, s);
+}
+
+template <typename TL, typename TO, int G, int VPL>
+lrm_status launch_rb(lrm_ctx* ctx, const TL* logits, TO* dlogits, const BackwardArgs& a, cudaStream_t s) {
+  static thread_local int dev = -1, grid = 0;
+  if (dev != ctx->device) {
+    grid = resident_grid(ctx, rb_rows<TL, TO, G, VPL>, RB_THREADS, 0);
+    dev = ctx->device;
+  }
+  const long long pass = RB_THREADS / G, need = (a.T + pass - 1) / pass;
+  rb_rows<TL, TO, G, VPL><<<static_cast<int>(need < grid ? need : grid), RB_THREADS, 0, s>>>(
+      logits, dlogits, a, rows_vec(logits, a.E), rows_vec(dlogits, a.E));
   return launch_status();
 }
 
 template <typename TL, typename TO>
-lrm_status dispatch_rb(const void* logits, void* dlogits, const BackwardArgs& a, int grid, cudaStream_t s) {
+lrm_status dispatch_rb(lrm_ctx* ctx, const void* logits, void* dlogits, const BackwardArgs& a, cudaStream_t s) {
   const TL* l = static_cast<const TL*>(logits);
   TO* o = static_cast<TO*>(dlogits);
-  const int vpl = (a.d.E + 31) / 32;
-  if (vpl <= 1) return launch_rb<TL, TO, 1>(l, o, a, grid, s);
-  if (vpl <= 2) return launch_rb<TL, TO, 2>(l, o, a, grid, s);
-  if (vpl <= 4) return launch_rb<TL, TO, 4>(l, o, a, grid, s);
-  if (vpl <= 8) return launch_rb<TL, TO, 8>(l, o, a, grid, s);
-  if (vpl <= 16) return launch_rb<TL, TO, 16>(l, o, a, grid, s);
-  return launch_rb<TL, TO, 32>(l, o, a, grid, s);
+  const Split sp = split_of(a.E, a.k);
+  if (sp.G == 4) return launch_rb<TL, TO, 4, 4>(ctx, l, o, a, s);
+  if (sp.G == 8) return launch_rb<TL, TO, 8, 4>(ctx, l, o, a, s);
+  if (sp.G == 16) return launch_rb<TL, TO, 16, 4>(ctx, l, o, a, s);
+  if (sp.VPL == 4) return launch_rb<TL, TO, 32, 4>(ctx, l, o, a, s);
+  if (sp.VPL == 8) return launch_rb<TL, TO, 32, 8>(ctx, l, o, a, s);
+  if (sp.VPL == 16) return launch_rb<TL, TO, 32, 16>(ctx, l, o, a, s);
+  return launch_rb<TL, TO, 32, 32>(ctx, l, o, a, s);
 }
 
 bool dtype_ok(int32_t t) { return t == LRM_F32 || t == LRM_BF16; }
@@ -403,17 +758,17 @@ extern "C" lrm_status lrm_router_forward(lrm_ctx* ctx, const void* logits, int32
   if (!guard.ok) return LRM_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* w = static_cast<char*>(ws);
-  ForwardArgs a{valid, dims, renorm, expert_idx, alpha, reinterpret_cast<float2*>(row_stats),
-                reinterpret_cast<float*>(w + L.p_off), reinterpret_cast<int32_t*>(w + L.cnt_off),
-                reinterpret_cast<double*>(w + L.z_off), reinterpret_cast<int32_t*>(w + L.tok_off)};
+  ForwardArgs a{valid, dims.T, dims.E, dims.k, renorm, aux_coef, z_coef, expert_idx, alpha,
+                reinterpret_cast<float2*>(row_stats), reinterpret_cast<float*>(w + L.p_off),
+                reinterpret_cast<int32_t*>(w + L.cnt_off), reinterpret_cast<float*>(w + L.z_off),
+                reinterpret_cast<int32_t*>(w + L.tok_off), counts, f, P, losses};
   if (L.nblk > 0) {
     st = logits_dtype == LRM_F32 ? dispatch_rf<float>(logits, a, L.nblk, s)
                                  : dispatch_rf<__nv_bfloat16>(logits, a, L.nblk, s);
-    if (st != LRM_OK) return st;
+    if (st != LRM_OK || L.nblk == 1) return st;
   }
-  rf_sums<<<1, 1024, 0, s>>>(a.ws_p, a.ws_cnt, a.ws_z, a.ws_tok, L.nblk, dims.E, dims.k, aux_coef, z_coef, counts, f,
-                             P, losses);
-  return launch_status();
+  const int cluster = dims.E >= 256 ? 8 : dims.E > 64 ? 4 : dims.E > 32 ? 2 : 1;
+  return launch_dependent(rf_sums, cluster, RS_SUM_THREADS, 0, cluster, s, a, L.nblk);
 }
 
 extern "C" lrm_status lrm_router_backward(lrm_ctx* ctx, const void* logits, int32_t logits_dtype,
@@ -437,15 +792,12 @@ extern "C" lrm_status lrm_router_backward(lrm_ctx* ctx, const void* logits, int3
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return LRM_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  BackwardArgs a{expert_idx, alpha, reinterpret_cast<const float2*>(row_stats), dgate, f, losses, dims, renorm,
-                 aux_coef, z_coef, ctx->d_status};
-  const long long need = (static_cast<long long>(dims.T) + RT_WARPS - 1) / RT_WARPS;
-  const int cap = ctx->sm_count * 4;
-  const int grid = static_cast<int>(need < cap ? need : cap);
+  const BackwardArgs a{expert_idx, alpha, reinterpret_cast<const float2*>(row_stats), dgate, f, losses, dims.T,
+                       dims.E, dims.k, renorm, aux_coef, z_coef, ctx->d_status};
   using bf = __nv_bfloat16;
   if (logits_dtype == LRM_F32)
-    return dlogits_dtype == LRM_F32 ? dispatch_rb<float, float>(logits, dlogits, a, grid, s)
-                                    : dispatch_rb<float, bf>(logits, dlogits, a, grid, s);
-  return dlogits_dtype == LRM_F32 ? dispatch_rb<bf, float>(logits, dlogits, a, grid, s)
-                                  : dispatch_rb<bf, bf>(logits, dlogits, a, grid, s);
+    return dlogits_dtype == LRM_F32 ? dispatch_rb<float, float>(ctx, logits, dlogits, a, s)
+                                    : dispatch_rb<float, bf>(ctx, logits, dlogits, a, s);
+  return dlogits_dtype == LRM_F32 ? dispatch_rb<bf, float>(ctx, logits, dlogits, a, s)
+                                  : dispatch_rb<bf, bf>(ctx, logits, dlogits, a, s);
 }
