@@ -1,17 +1,21 @@
 // Global gradient norm over a list of tensors, and clipping by it:
 //   norm = sqrt(sum over all elements g^2),  dst = min(1, max_norm / norm) src.
 //
-// The list's device table holds chunks: runs of at most GC_CHUNK_BYTES of one
-// tensor, so that tensors of any size give the warps equal shares and a warp
-// finds its work with one 32-byte load.
+// The list's device table holds chunks: runs of one tensor, so that tensors of
+// any size give the warps equal shares and a warp finds its work with one
+// 32-byte load.
 //
-//   gc_norm   one warp per chunk; each block leaves its sum of squares (fp64).
-//   gc_stats  adds the blocks' sums (the norm alone).
-//   gc_clip   every block adds the same sums in the same order, so all take
-//             the same coefficient, and scales its chunks.
+//   gc_small   lists of up to 256 chunks: one cluster, a chunk a warp, held in
+//              registers between the norm and the scaling, so it is read once
+//              and there is one launch.
+//   gc_norm    one warp per chunk; each block leaves its sum of squares (fp64).
+//   gc_stats   adds the blocks' sums (the norm alone).
+//   gc_clip    launched dependently; every block adds the same sums in the
+//              same order, so all take the same coefficient, and scales its
+//              chunks, last ones first: those are still in L2.
 //
 // Squares: a lane's batch of values (32 fp32 or 64 bf16) is squared and summed
-// in fp32 while its largest magnitude lies in [2^-56, 2^60]: no sum of squares
+// in fp32 while its largest magnitude lies in [2^-56, 2^55]: no sum of squares
 // overflows, and a square that fp32 holds as a subnormal is off by at most
 // 2^-150, 2^-38 of the largest square.  Other batches are squared in fp64
 // (exact); batches of zeros add nothing.  Batches are added in fp64.
@@ -23,6 +27,7 @@
 
 struct lrm_grad_list {
   int device;
+  int small;  // ranks of gc_small's cluster, 0: gc_norm and gc_clip
   long long chunks;
   int in_place, has_dst;  // every dst is its src; every non-empty tensor has a dst
   int grid_norm, grid_clip;
@@ -32,10 +37,16 @@ struct lrm_grad_list {
 namespace lrm {
 namespace {
 
-constexpr int GC_THREADS = 256;
+constexpr int GC_THREADS = 512;
 constexpr int GC_WARPS = GC_THREADS / 32;
-constexpr int GC_CHUNK_BYTES = 16384;
-constexpr int GC_MAX_GRID = 152 * 8 * 2;  // upper bound of the norm kernel's grid, sizes the partial sums
+constexpr int GC_BATCH = 8;                                    // 16-byte loads a lane has in flight
+constexpr int GC_BATCH_BYTES = 32 * 16 * GC_BATCH;             // a warp's batch
+constexpr int GC_MAX_GRID = 152 * 4;                           // of gc_norm: sizes the partial sums
+constexpr int64_t GC_ONE_BATCH_BYTES = int64_t{128} << 20;     // lists up to this size have chunks of one batch
+constexpr int GC_SMALL_THREADS = 1024;
+constexpr int GC_SMALL_WARPS = GC_SMALL_THREADS / 32;
+constexpr int GC_SMALL_CLUSTER = 8;
+constexpr int GC_SMALL_CHUNKS = GC_SMALL_WARPS * GC_SMALL_CLUSTER;
 
 enum : int32_t { GC_F32_VEC = 0, GC_BF16_VEC = 1, GC_F32_ANY = 2, GC_BF16_ANY = 3 };
 
@@ -52,7 +63,7 @@ constexpr size_t GC_SCRATCH_BYTES = GC_MAX_GRID * sizeof(double);
 // The chunks of a list, in order: sink(chunk) for each.  Tensors whose src
 // starts off a 16-byte boundary get a short first chunk up to it.
 template <typename Sink>
-void for_chunks(const lrm_tensor* tensors, int32_t count, Sink sink) {
+void for_chunks(const lrm_tensor* tensors, int32_t count, int64_t chunk_bytes, Sink sink) {
   for (int32_t i = 0; i < count; ++i) {
     const lrm_tensor& t = tensors[i];
     const int64_t es = t.dtype == LRM_F32 ? 4 : 2, per = 16 / es;
@@ -70,7 +81,7 @@ void for_chunks(const lrm_tensor* tensors, int32_t count, Sink sink) {
       } else if (left < per) {
         n = left;
       } else {
-        const int64_t whole = left / per * per, most = GC_CHUNK_BYTES / es;
+        const int64_t whole = left / per * per, most = chunk_bytes / es;
         n = whole < most ? whole : most;
         vec = d == nullptr || aligned(d, 16);
       }
@@ -87,12 +98,12 @@ void for_chunks(const lrm_tensor* tensors, int32_t count, Sink sink) {
 }
 
 // Number of chunks of for_chunks without walking them.
-int64_t count_chunks(const lrm_tensor* tensors, int32_t count) {
+int64_t count_chunks(const lrm_tensor* tensors, int32_t count, int64_t chunk_bytes) {
   int64_t total = 0;
   for (int32_t i = 0; i < count; ++i) {
     const lrm_tensor& t = tensors[i];
     if (t.n == 0) continue;
-    const int64_t es = t.dtype == LRM_F32 ? 4 : 2, per = 16 / es, most = GC_CHUNK_BYTES / es;
+    const int64_t es = t.dtype == LRM_F32 ? 4 : 2, per = 16 / es, most = chunk_bytes / es;
     const int64_t off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(t.src) % 16) / es;
     int64_t left = t.n;
     if (off != 0) {
@@ -103,6 +114,15 @@ int64_t count_chunks(const lrm_tensor* tensors, int32_t count) {
     total += (whole + most - 1) / most + (left > whole ? 1 : 0);
   }
   return total;
+}
+
+// Bytes of a chunk: one batch of a warp while that makes no more than a few
+// chunks a warp of the GPU, then up to four batches (a descriptor then costs
+// 0.2 % of the bytes it stands for).
+int64_t chunk_bytes_of(const lrm_tensor* tensors, int32_t count) {
+  int64_t bytes = 0;
+  for (int32_t i = 0; i < count; ++i) bytes += tensors[i].n * (tensors[i].dtype == LRM_F32 ? 4 : 2);
+  return bytes <= GC_ONE_BATCH_BYTES ? GC_BATCH_BYTES : 4 * GC_BATCH_BYTES;
 }
 
 lrm_status check_tensors(const lrm_tensor* tensors, int32_t count) {
@@ -121,7 +141,7 @@ lrm_status check_tensors(const lrm_tensor* tensors, int32_t count) {
   return LRM_OK;
 }
 
-__device__ __forceinline__ bool in_fp32_range(float mx) { return mx >= 0x1p-56f && mx <= 0x1p60f; }
+__device__ __forceinline__ bool in_fp32_range(float mx) { return mx >= 0x1p-56f && mx <= 0x1p55f; }
 
 // Adds the squares of a batch of n values to sum.
 template <int N>
@@ -152,93 +172,47 @@ __device__ __forceinline__ void unpack(const uint4& x, float* v) {
   v[7] = bf16_hi(x.w);
 }
 
-constexpr int GC_BATCH = 8;  // 16-byte loads a lane has in flight
-
-__device__ double chunk_squares(const Chunk& c, int lane) {
-  double sum = 0.0;
-  if (c.kind == GC_F32_VEC || c.kind == GC_BF16_VEC) {
-    const uint4* p = static_cast<const uint4*>(c.src);
-    const int nv = c.n / (c.kind == GC_F32_VEC ? 4 : 8);
-    for (int v0 = 0; v0 < nv; v0 += 32 * GC_BATCH) {
-      uint4 x[GC_BATCH];
+// A lane's batch of squares.  Its words are NaN-free of padding: places beyond
+// the chunk hold 0.
+__device__ __forceinline__ void batch_squares(const uint4 (&x)[GC_BATCH], bool f32, double& sum) {
+  if (f32) {
+    float v[4 * GC_BATCH];
 #pragma unroll
-      for (int j = 0; j < GC_BATCH; ++j) {
-        const int v = v0 + lane + 32 * j;
-        x[j] = v < nv ? ld_stream(p + v) : make_uint4(0u, 0u, 0u, 0u);
-      }
-      if (c.kind == GC_F32_VEC) {
-        float v[4 * GC_BATCH];
-#pragma unroll
-        for (int j = 0; j < GC_BATCH; ++j) {
-          v[4 * j] = __uint_as_float(x[j].x);
-          v[4 * j + 1] = __uint_as_float(x[j].y);
-          v[4 * j + 2] = __uint_as_float(x[j].z);
-          v[4 * j + 3] = __uint_as_float(x[j].w);
-        }
-        add_squares(v, sum);
-      } else {
-        float v[8 * GC_BATCH];
-#pragma unroll
-        for (int j = 0; j < GC_BATCH; ++j) unpack(x[j], v + 8 * j);
-        add_squares(v, sum);
-      }
+    for (int j = 0; j < GC_BATCH; ++j) {
+      v[4 * j] = __uint_as_float(x[j].x);
+      v[4 * j + 1] = __uint_as_float(x[j].y);
+      v[4 * j + 2] = __uint_as_float(x[j].z);
+      v[4 * j + 3] = __uint_as_float(x[j].w);
     }
+    add_squares(v, sum);
   } else {
-    for (int i = lane; i < c.n; i += 32) {
-      const float v = c.kind == GC_F32_ANY ? static_cast<const float*>(c.src)[i]
-                                           : __bfloat162float(static_cast<const __nv_bfloat16*>(c.src)[i]);
-      sum += static_cast<double>(v) * v;
-    }
-  }
-  return sum;
-}
-
-__global__ void __launch_bounds__(GC_THREADS) gc_norm(const Chunk* __restrict__ chunks, long long count,
-                                                      double* __restrict__ partial) {
-  __shared__ double s_sum[GC_WARPS];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long step = static_cast<long long>(gridDim.x) * GC_WARPS;
-  double sum = 0.0;
-  for (long long i = static_cast<long long>(blockIdx.x) * GC_WARPS + warp; i < count; i += step)
-    sum += chunk_squares(chunks[i], lane);
+    float v[8 * GC_BATCH];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double a = 0.0;
-    for (int w = 0; w < GC_WARPS; ++w) a += s_sum[w];
-    partial[blockIdx.x] = a;
+    for (int j = 0; j < GC_BATCH; ++j) unpack(x[j], v + 8 * j);
+    add_squares(v, sum);
   }
 }
 
-// The blocks' sums added in a fixed order; every thread gets the total.
-__device__ double total_squares(const double* __restrict__ partial, int nblk) {
-  __shared__ double s_part[GC_WARPS];
-  double a = 0.0;
-  for (int i = threadIdx.x; i < nblk; i += GC_THREADS) a += partial[i];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = a;
-  __syncthreads();
-  a = 0.0;
-  for (int w = 0; w < GC_WARPS; ++w) a += s_part[w];
-  return a;
-}
-
-__device__ lrm_grad_stats make_stats(double squares, float max_norm) {
-  const double norm = sqrt(squares);
-  lrm_grad_stats r;
-  r.norm = static_cast<float>(norm);
-  r.nonfinite = isfinite(norm) ? 0 : 1;
-  r.coef = !r.nonfinite && norm > max_norm ? static_cast<float>(max_norm / norm) : 1.f;
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
   return r;
 }
 
-__global__ void __launch_bounds__(GC_THREADS) gc_stats(const double* __restrict__ partial, int nblk,
-                                                       lrm_grad_stats* __restrict__ stats) {
-  const double sq = total_squares(partial, nblk);
-  if (threadIdx.x == 0) *stats = make_stats(sq, INFINITY);
+__device__ __forceinline__ void load_batch(const uint4* p, int v0, int nv, int lane, uint4 (&x)[GC_BATCH]) {
+  if (v0 + 32 * GC_BATCH <= nv) {
+#pragma unroll
+    for (int j = 0; j < GC_BATCH; ++j) x[j] = ld_once(p + v0 + lane + 32 * j);
+  } else {
+#pragma unroll
+    for (int j = 0; j < GC_BATCH; ++j) {
+      const int v = v0 + lane + 32 * j;
+      x[j] = v < nv ? ld_once(p + v) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
 }
 
 __device__ __forceinline__ uint4 scale_f32x4(const uint4& x, float c) {
@@ -246,52 +220,233 @@ __device__ __forceinline__ uint4 scale_f32x4(const uint4& x, float c) {
                     __float_as_uint(__uint_as_float(x.z) * c), __float_as_uint(__uint_as_float(x.w) * c));
 }
 
-__device__ void scale_chunk(const Chunk& c, float coef, int lane) {
-  if (c.kind == GC_F32_VEC || c.kind == GC_BF16_VEC) {
-    const uint4* p = static_cast<const uint4*>(c.src);
-    uint4* q = static_cast<uint4*>(c.dst);
-    const int nv = c.n / (c.kind == GC_F32_VEC ? 4 : 8);
-    for (int v0 = 0; v0 < nv; v0 += 32 * GC_BATCH) {
-      uint4 x[GC_BATCH];
+__device__ __forceinline__ void store_batch(uint4* q, int v0, int nv, int lane, const uint4 (&x)[GC_BATCH], bool f32,
+                                            float coef) {
 #pragma unroll
-      for (int j = 0; j < GC_BATCH; ++j) {
-        const int v = v0 + lane + 32 * j;
-        if (v < nv) x[j] = p[v];
-      }
+  for (int j = 0; j < GC_BATCH; ++j) {
+    const int v = v0 + lane + 32 * j;
+    if (v < nv) __stcs(q + v, f32 ? scale_f32x4(x[j], coef) : scale_bf16x8(x[j], coef));
+  }
+}
+
+__device__ __forceinline__ bool is_vec(const Chunk& c) { return c.kind == GC_F32_VEC || c.kind == GC_BF16_VEC; }
+__device__ __forceinline__ int vectors(const Chunk& c) { return c.n / (c.kind == GC_F32_VEC ? 4 : 8); }
+
+// Chunks off the 16-byte grid, element by element.
+__device__ __noinline__ double any_squares(const Chunk& c, int lane) {
+  double sum = 0.0;
+  for (int i = lane; i < c.n; i += 32) {
+    const float v = c.kind == GC_F32_ANY ? static_cast<const float*>(c.src)[i]
+                                         : __bfloat162float(static_cast<const __nv_bfloat16*>(c.src)[i]);
+    sum += static_cast<double>(v) * v;
+  }
+  return sum;
+}
+__device__ __noinline__ void any_scale(const Chunk& c, float coef, int lane) {
+  for (int i = lane; i < c.n; i += 32) {
+    if (c.kind == GC_F32_ANY)
+      static_cast<float*>(c.dst)[i] = static_cast<const float*>(c.src)[i] * coef;
+    else
+      static_cast<__nv_bfloat16*>(c.dst)[i] =
+          __float2bfloat16_rn(__bfloat162float(static_cast<const __nv_bfloat16*>(c.src)[i]) * coef);
+  }
+}
+
+// Sums of squares (v >= 0, infinite or NaN) over a warp, for every lane.  The
+// SM's fp64 unit takes a warp's addition in 16 clocks, so sums that fp32 holds
+// with room to spare are added in fp32 (six roundings more).
+__device__ __forceinline__ bool fits_f32(double v) {
+  const int ex = __double2hiint(v) >> 20;  // biased exponent; negative values do not occur
+  return v == 0.0 || (ex >= 1023 - 112 && ex <= 1023 + 121);
+}
+__device__ __forceinline__ double warp_sum(double v) {
+  if (__all_sync(0xffffffffu, fits_f32(v))) {
+    float f = static_cast<float>(v);
 #pragma unroll
-      for (int j = 0; j < GC_BATCH; ++j) {
-        const int v = v0 + lane + 32 * j;
-        if (v < nv) st_v4(q + v, c.kind == GC_F32_VEC ? scale_f32x4(x[j], coef) : scale_bf16x8(x[j], coef));
+    for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+    return f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ lrm_grad_stats make_stats(double squares, float max_norm) {
+  lrm_grad_stats r;
+  if (fits_f32(squares)) {
+    r.norm = sqrtf(static_cast<float>(squares));
+    r.nonfinite = 0;
+    r.coef = r.norm > max_norm ? max_norm / r.norm : 1.f;
+    return r;
+  }
+  const double norm = sqrt(squares);
+  r.norm = static_cast<float>(norm);
+  r.nonfinite = isfinite(norm) ? 0 : 1;
+  r.coef = !r.nonfinite && norm > max_norm ? static_cast<float>(max_norm / norm) : 1.f;
+  return r;
+}
+
+__global__ void __launch_bounds__(GC_THREADS) gc_norm(const Chunk* __restrict__ chunks, long long count,
+                                                      double* __restrict__ partial) {
+  __shared__ double s_sum[GC_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_launch();
+  const long long step = static_cast<long long>(gridDim.x) * GC_WARPS;
+  long long i = static_cast<long long>(blockIdx.x) * GC_WARPS + warp;
+  double sum = 0.0;
+  Chunk next = {};
+  if (i < count) next = chunks[i];
+  for (; i < count; i += step) {
+    const Chunk c = next;
+    if (i + step < count) next = chunks[i + step];
+    if (is_vec(c)) {
+      const int nv = vectors(c);
+      for (int v0 = 0; v0 < nv; v0 += 32 * GC_BATCH) {
+        uint4 x[GC_BATCH];
+        load_batch(static_cast<const uint4*>(c.src), v0, nv, lane, x);
+        batch_squares(x, c.kind == GC_F32_VEC, sum);
       }
-    }
-  } else {
-    for (int i = lane; i < c.n; i += 32) {
-      if (c.kind == GC_F32_ANY)
-        static_cast<float*>(c.dst)[i] = static_cast<const float*>(c.src)[i] * coef;
-      else
-        static_cast<__nv_bfloat16*>(c.dst)[i] =
-            __float2bfloat16_rn(__bfloat162float(static_cast<const __nv_bfloat16*>(c.src)[i]) * coef);
+    } else {
+      sum += any_squares(c, lane);
     }
   }
+  sum = warp_sum(sum);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    sum = warp_sum(lane < GC_WARPS ? s_sum[lane] : 0.0);
+    if (lane == 0) partial[blockIdx.x] = sum;
+  }
+}
+
+// The blocks' sums added in a fixed order; the whole block gets the result.
+// One thread takes the root and the quotient: the SM's fp64 unit finishes two
+// lanes a clock, and every warp doing so cost 7 us.
+__device__ lrm_grad_stats block_stats(const double* __restrict__ partial, int nblk, float max_norm) {
+  __shared__ double s_part[GC_WARPS];
+  __shared__ lrm_grad_stats s_stats;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  double a = 0.0;
+  for (int i = threadIdx.x; i < nblk; i += GC_THREADS) a += partial[i];
+  if (warp * 32 < nblk) a = warp_sum(a);
+  if (lane == 0) s_part[warp] = a;
+  __syncthreads();
+  if (warp == 0) {
+    a = warp_sum(lane < GC_WARPS ? s_part[lane] : 0.0);
+    if (lane == 0) s_stats = make_stats(a, max_norm);
+  }
+  __syncthreads();
+  return s_stats;
+}
+
+__global__ void __launch_bounds__(GC_THREADS) gc_stats(const double* __restrict__ partial, int nblk,
+                                                       lrm_grad_stats* __restrict__ stats) {
+  grid_dependency_wait();
+  const lrm_grad_stats r = block_stats(partial, nblk, INFINITY);
+  if (threadIdx.x == 0) *stats = r;
 }
 
 __global__ void __launch_bounds__(GC_THREADS) gc_clip(const Chunk* __restrict__ chunks, long long count,
                                                       const double* __restrict__ partial, int nblk, float max_norm,
                                                       int in_place, lrm_grad_stats* __restrict__ stats) {
-  const lrm_grad_stats r = make_stats(total_squares(partial, nblk), max_norm);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *stats = r;
-  if (in_place && r.coef == 1.f) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long step = static_cast<long long>(gridDim.x) * GC_WARPS;
-  for (long long i = static_cast<long long>(blockIdx.x) * GC_WARPS + warp; i < count; i += step)
-    scale_chunk(chunks[i], r.coef, lane);
+  long long i = count - 1 - (static_cast<long long>(blockIdx.x) * GC_WARPS + warp);
+  Chunk next = {};
+  if (i >= 0) next = chunks[i];  // the table was there before gc_norm began
+  grid_dependency_wait();
+  const lrm_grad_stats r = block_stats(partial, nblk, max_norm);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *stats = r;
+  if (in_place && r.coef == 1.f) return;
+  for (; i >= 0; i -= step) {
+    const Chunk c = next;
+    if (i >= step) next = chunks[i - step];
+    if (is_vec(c)) {
+      const int nv = vectors(c);
+      for (int v0 = 0; v0 < nv; v0 += 32 * GC_BATCH) {
+        uint4 x[GC_BATCH];
+        load_batch(static_cast<const uint4*>(c.src), v0, nv, lane, x);
+        store_batch(static_cast<uint4*>(c.dst), v0, nv, lane, x, c.kind == GC_F32_VEC, r.coef);
+      }
+    } else {
+      any_scale(c, r.coef, lane);
+    }
+  }
+}
+
+// scale = 0: the norm alone.
+__global__ void __launch_bounds__(GC_SMALL_THREADS) gc_small(const Chunk* __restrict__ chunks, int count, int scale,
+                                                             float max_norm, int in_place,
+                                                             lrm_grad_stats* __restrict__ stats) {
+  __shared__ double s_sum[GC_SMALL_WARPS];
+  __shared__ double s_rank[GC_SMALL_CLUSTER];
+  __shared__ lrm_grad_stats s_stats;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank(), ranks = gridDim.x;  // one cluster
+  const int i = static_cast<int>(rank) * GC_SMALL_WARPS + warp;
+  Chunk c = {};
+  if (i < count) c = chunks[i];
+  const bool vec = i < count && is_vec(c);
+  uint4 x[GC_BATCH];
+  double sum = 0.0;
+  if (vec) {
+    load_batch(static_cast<const uint4*>(c.src), 0, vectors(c), lane, x);
+    batch_squares(x, c.kind == GC_F32_VEC, sum);
+  } else if (i < count) {
+    sum = any_squares(c, lane);
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) s_sum[warp] = sum;
+  if (ranks > 1) cluster_sync_all();  // every CTA has started
+  else __syncthreads();
+  if (warp == 0) {
+    sum = warp_sum(s_sum[lane]);
+    if (lane < static_cast<int>(ranks))
+      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa_shared(&s_rank[rank], lane)), "d"(sum) : "memory");
+  }
+  if (ranks > 1) cluster_sync_all();
+  else __syncthreads();
+  if (threadIdx.x == 0) {
+    sum = 0.0;
+    for (uint32_t r = 0; r < ranks; ++r) sum += s_rank[r];
+    s_stats = make_stats(sum, scale ? max_norm : INFINITY);
+    if (rank == 0) *stats = s_stats;
+  }
+  __syncthreads();
+  const lrm_grad_stats r = s_stats;
+  if (!scale || (in_place && r.coef == 1.f)) return;
+  if (vec)
+    store_batch(static_cast<uint4*>(c.dst), 0, vectors(c), lane, x, c.kind == GC_F32_VEC, r.coef);
+  else if (i < count)
+    any_scale(c, r.coef, lane);
+}
+
+const Chunk* chunks_of(const lrm_grad_list* list) {
+  return reinterpret_cast<const Chunk*>(static_cast<char*>(list->table) + GC_SCRATCH_BYTES);
+}
+
+lrm_status launch_small(const lrm_grad_list* list, int scale, float max_norm, lrm_grad_stats* stats, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(list->small);
+  cfg.blockDim = dim3(GC_SMALL_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = list->small;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, gc_small, chunks_of(list), static_cast<int>(list->chunks), scale, max_norm,
+                         list->in_place, stats) != cudaSuccess) {
+    cudaGetLastError();
+    return LRM_ERR_CUDA;
+  }
+  return LRM_OK;
 }
 
 lrm_status launch_norm(const lrm_grad_list* list, cudaStream_t s) {
   if (list->chunks == 0) return LRM_OK;
-  gc_norm<<<list->grid_norm, GC_THREADS, 0, s>>>(
-      reinterpret_cast<const Chunk*>(static_cast<char*>(list->table) + GC_SCRATCH_BYTES), list->chunks,
-      static_cast<double*>(list->table));
+  gc_norm<<<list->grid_norm, GC_THREADS, 0, s>>>(chunks_of(list), list->chunks, static_cast<double*>(list->table));
   return launch_status();
 }
 
@@ -304,7 +459,8 @@ extern "C" lrm_status lrm_grad_table_size(const lrm_tensor* tensors, int32_t cou
   if (bytes == nullptr) return LRM_ERR_INVALID_ARG;
   const lrm_status st = check_tensors(tensors, count);
   if (st != LRM_OK) return st;
-  *bytes = GC_SCRATCH_BYTES + static_cast<size_t>(count_chunks(tensors, count)) * sizeof(Chunk);
+  *bytes = GC_SCRATCH_BYTES +
+           static_cast<size_t>(count_chunks(tensors, count, chunk_bytes_of(tensors, count))) * sizeof(Chunk);
   return LRM_OK;
 }
 
@@ -338,7 +494,10 @@ extern "C" lrm_status lrm_grad_list_create(lrm_ctx* ctx, const lrm_tensor* tenso
     if (tensors[i].dst == nullptr) list->has_dst = 0;
     if (tensors[i].dst != tensors[i].src) list->in_place = 0;
   }
-  list->chunks = count_chunks(tensors, count);
+  const int64_t chunk_bytes = chunk_bytes_of(tensors, count);
+  list->chunks = count_chunks(tensors, count, chunk_bytes);
+  if (list->chunks <= GC_SMALL_CHUNKS)
+    list->small = list->chunks > 0 ? static_cast<int>((list->chunks + GC_SMALL_WARPS - 1) / GC_SMALL_WARPS) : 1;
   if (list->chunks > 0) {
     Chunk* host = static_cast<Chunk*>(malloc(static_cast<size_t>(list->chunks) * sizeof(Chunk)));
     if (host == nullptr) {
@@ -346,7 +505,7 @@ extern "C" lrm_status lrm_grad_list_create(lrm_ctx* ctx, const lrm_tensor* tenso
       return LRM_ERR_CUDA;
     }
     int64_t at = 0;
-    for_chunks(tensors, count, [&](const Chunk& c) { host[at++] = c; });
+    for_chunks(tensors, count, chunk_bytes, [&](const Chunk& c) { host[at++] = c; });
     // a copy from pageable memory has read `host` when it returns
     const cudaError_t e = cudaMemcpyAsync(static_cast<char*>(table) + GC_SCRATCH_BYTES, host,
                                           static_cast<size_t>(list->chunks) * sizeof(Chunk), cudaMemcpyHostToDevice, s);
@@ -377,10 +536,11 @@ extern "C" lrm_status lrm_grad_norm(lrm_ctx* ctx, const lrm_grad_list* list, lrm
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return LRM_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (list->small) return launch_small(list, 0, 0.f, stats, s);
   const lrm_status st = launch_norm(list, s);
   if (st != LRM_OK) return st;
-  gc_stats<<<1, GC_THREADS, 0, s>>>(static_cast<const double*>(list->table), list->grid_norm, stats);
-  return launch_status();
+  return launch_dependent(gc_stats, 1, GC_THREADS, 0, 1, s, static_cast<const double*>(list->table), list->grid_norm,
+                          stats);
 }
 
 extern "C" lrm_status lrm_grad_clip(lrm_ctx* ctx, const lrm_grad_list* list, float max_norm, lrm_grad_stats* stats,
@@ -392,10 +552,9 @@ extern "C" lrm_status lrm_grad_clip(lrm_ctx* ctx, const lrm_grad_list* list, flo
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return LRM_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (list->small) return launch_small(list, 1, max_norm, stats, s);
   const lrm_status st = launch_norm(list, s);
   if (st != LRM_OK) return st;
-  gc_clip<<<list->grid_clip > 0 ? list->grid_clip : 1, GC_THREADS, 0, s>>>(
-      reinterpret_cast<const Chunk*>(static_cast<char*>(list->table) + GC_SCRATCH_BYTES), list->chunks,
-      static_cast<const double*>(list->table), list->grid_norm, max_norm, list->in_place, stats);
-  return launch_status();
+  return launch_dependent(gc_clip, list->grid_clip, GC_THREADS, 0, 1, s, chunks_of(list), list->chunks,
+                          static_cast<const double*>(list->table), list->grid_norm, max_norm, list->in_place, stats);
 }

@@ -301,11 +301,11 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
   return r;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(const float* p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(p, rank)) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32(const float* p, uint32_t rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(p, rank)), "f"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float warp_sum(float v) { return group_sum<32>(v); }
 
@@ -333,33 +333,43 @@ __device__ __forceinline__ void write_losses(const ForwardArgs& a, float fp, flo
 }
 
 // Adds nblk blocks' sums.  The cluster's CTAs share the experts; a warp adds
-// every 32nd row of 32 experts, then warp w the warps' sums of the w-th expert.
+// every 32nd row of 32 experts, then warp w the warps' sums of the w-th
+// expert.  The CTAs push their sums of f P to CTA 0.
 __global__ void __launch_bounds__(RS_SUM_THREADS) rf_sums(ForwardArgs a, int nblk) {
-  constexpr int NW = RS_SUM_THREADS / 32;
+  constexpr int NW = RS_SUM_THREADS / 32, BATCH = 5;  // rows a warp has in flight: all of 152 blocks
   __shared__ float s_p[NW][33];
   __shared__ int s_c[NW][33];
   __shared__ float s_fp[NW];
-  __shared__ float s_total;
+  __shared__ float s_total[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank()), ranks = static_cast<int>(cluster_nctarank());
   const int per = (a.E + ranks - 1) / ranks;
   const int e0 = min(a.E, rank * per), e1 = min(a.E, e0 + per);
+  if (ranks > 1) cluster_arrive();  // waited for before the push: CTA 0 has started by then
   grid_dependency_wait();
   float z = 0.f, fp = 0.f;
   int tokens = 0;
   for (int b = lane; b < nblk; b += 32) z += a.ws_z[b], tokens += a.ws_tok[b];
-  z = warp_sum(z);
-  tokens = __reduce_add_sync(0xffffffffu, tokens);
   for (int c0 = e0; c0 < e1; c0 += 32) {
     const int e = c0 + lane;
     float p = 0.f;
     int c = 0;
-    if (e < e1) {
-#pragma unroll 8
-      for (int b = warp; b < nblk; b += NW) {
-        p += a.ws_p[static_cast<size_t>(b) * a.E + e];
-        c += a.ws_cnt[static_cast<size_t>(b) * a.E + e];
+    for (int b0 = warp; b0 < nblk; b0 += BATCH * NW) {
+      float pv[BATCH];
+      int cv[BATCH];
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        const int b = b0 + j * NW;
+        const bool in = b < nblk && e < e1;
+        pv[j] = in ? a.ws_p[static_cast<size_t>(b) * a.E + e] : 0.f;
+        cv[j] = in ? a.ws_cnt[static_cast<size_t>(b) * a.E + e] : 0;
       }
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) p += pv[j], c += cv[j];
+    }
+    if (c0 == e0) {
+      z = warp_sum(z);
+      tokens = __reduce_add_sync(0xffffffffu, tokens);
     }
     s_p[warp][lane] = p;
     s_c[warp][lane] = c;
@@ -371,16 +381,16 @@ __global__ void __launch_bounds__(RS_SUM_THREADS) rf_sums(ForwardArgs a, int nbl
   }
   if (lane == 0) s_fp[warp] = fp;
   __syncthreads();
-  if (warp == 0) {
-    fp = warp_sum(s_fp[lane]);
-    if (lane == 0) s_total = fp;
+  if (warp == 0) fp = warp_sum(s_fp[lane]);
+  if (ranks > 1) {
+    cluster_wait();
+    if (rank != 0 && threadIdx.x == 0) st_cluster_f32(&s_total[rank], 0, fp);
+    cluster_arrive();
+    if (rank != 0) return;
+    cluster_wait();
+    if (warp == 0) fp = warp_sum(lane == 0 ? fp : lane < ranks ? s_total[lane] : 0.f);
   }
-  if (ranks > 1) cluster_sync_all();
-  if (rank == 0 && warp == 0) {
-    if (ranks > 1) fp = warp_sum(lane < ranks ? ld_cluster_f32(&s_total, lane) : 0.f);
-    if (lane == 0) write_losses(a, fp, z, tokens);
-  }
-  if (ranks > 1) cluster_sync_all();  // s_total stays until rank 0 has read it
+  if (threadIdx.x == 0) write_losses(a, fp, z, tokens);
 }
 
 template <typename TL, int G, int VPL>
@@ -443,12 +453,11 @@ __global__ void __launch_bounds__(rf_threads(VPL), 1) rf_rows(const TL* __restri
 #pragma unroll 4
     for (int j = 0; j < k; ++j) {
       const uint32_t top = group_max<G>(key[0]);
-      if (key[0] == top) {
-        sel[j] = top;
+      const bool hit = key[0] == top;
+      if (hit) sel[j] = top;
 #pragma unroll
-        for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
-        key[VPL - 1] = 0u;
-      }
+      for (int i = 0; i + 1 < VPL; ++i) key[i] = hit ? key[i + 1] : key[i];
+      key[VPL - 1] = hit ? 0u : key[VPL - 1];
     }
     uint32_t after = 0;  // the largest key left out
     if constexpr (!is_bf16<TL>) after = group_max<G>(key[0]);
@@ -611,11 +620,9 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
 #pragma unroll
     for (int i = 0; i < VPL; ++i) p[i] = exp_neg(x.raw.get(i) - x.ms.x) * inv;
     int e = gates && counted && q < k ? x.id : -1;
-    if (!counted) {
-      dg = 0.f;
+    dg = counted ? dg : 0.f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) p[i] = 0.f;
-    }
+    for (int i = 0; i < VPL; ++i) p[i] = counted ? p[i] : 0.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) fp = fmaf(cf[i], p[i], fp);
     float w = 0.f;
@@ -654,10 +661,8 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
       out[4 * c + 2] = fmaf(p[4 * c + 2], cf[4 * c + 2] + w, g.z);
       out[4 * c + 3] = fmaf(p[4 * c + 3], cf[4 * c + 3] + w, g.w);
     }
-    if (!counted) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) out[i] = 0.f;
-    }
+    for (int i = 0; i < VPL; ++i) out[i] = counted ? out[i] : 0.f;
     if (here) store_row<TO, VPL>(dlogits + static_cast<size_t>(t) * E, e0, E, vec_out, out);
     __syncwarp();
     if (e >= 0) add[e] = 0.f;

@@ -200,6 +200,9 @@ def _stream(stream) -> int | None:
     if stream is None:
         import torch
 
+        # the raw handle: making a torch stream object costs about 3 us a call, a third of a small call's host time
+        if torch.cuda.is_initialized():
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
