@@ -42,7 +42,7 @@ constexpr int GC_WARPS = GC_THREADS / 32;
 constexpr int GC_BATCH = 8;                                    // 16-byte loads a lane has in flight
 constexpr int GC_BATCH_BYTES = 32 * 16 * GC_BATCH;             // a warp's batch
 constexpr int GC_MAX_GRID = 152 * 4;                           // of gc_norm: sizes the partial sums
-constexpr int64_t GC_ONE_BATCH_BYTES = int64_t{128} << 20;     // lists up to this size have chunks of one batch
+constexpr int64_t GC_LARGE_BYTES = int64_t{128} << 20;         // about the L2's size
 constexpr int GC_SMALL_THREADS = 1024;
 constexpr int GC_SMALL_WARPS = GC_SMALL_THREADS / 32;
 constexpr int GC_SMALL_CLUSTER = 8;
@@ -116,13 +116,20 @@ int64_t count_chunks(const lrm_tensor* tensors, int32_t count, int64_t chunk_byt
   return total;
 }
 
-// Bytes of a chunk: one batch of a warp while that makes no more than a few
-// chunks a warp of the GPU, then up to four batches (a descriptor then costs
-// 0.2 % of the bytes it stands for).
+// Bytes of a chunk.  Small lists: the smallest that gives gc_small's warps no
+// more than one each.  Others: up to a batch of a warp, cut so that the warps
+// of two blocks an SM get equal numbers; above GC_LARGE_BYTES four batches (a
+// descriptor then costs 0.2 % of the bytes it stands for).
 int64_t chunk_bytes_of(const lrm_tensor* tensors, int32_t count) {
   int64_t bytes = 0;
   for (int32_t i = 0; i < count; ++i) bytes += tensors[i].n * (tensors[i].dtype == LRM_F32 ? 4 : 2);
-  return bytes <= GC_ONE_BATCH_BYTES ? GC_BATCH_BYTES : 4 * GC_BATCH_BYTES;
+  if (bytes > GC_LARGE_BYTES) return 4 * GC_BATCH_BYTES;
+  if (bytes <= static_cast<int64_t>(GC_SMALL_CHUNKS) * GC_BATCH_BYTES)
+    for (int64_t b = 512; b <= GC_BATCH_BYTES; b *= 2)
+      if (count_chunks(tensors, count, b) <= GC_SMALL_CHUNKS) return b;
+  const int64_t warps = 152 * 2 * GC_WARPS, rounds = (bytes + warps * GC_BATCH_BYTES - 1) / (warps * GC_BATCH_BYTES);
+  const int64_t even = (bytes + warps * rounds - 1) / (warps * rounds);
+  return even > 512 ? (even + 127) / 128 * 128 : 512;
 }
 
 lrm_status check_tensors(const lrm_tensor* tensors, int32_t count) {
@@ -143,53 +150,61 @@ lrm_status check_tensors(const lrm_tensor* tensors, int32_t count) {
 
 __device__ __forceinline__ bool in_fp32_range(float mx) { return mx >= 0x1p-56f && mx <= 0x1p55f; }
 
-// Adds the squares of a batch of n values to sum.
-template <int N>
-__device__ __forceinline__ void add_squares(const float (&v)[N], double& sum) {
+template <bool F32>
+__device__ __forceinline__ void unpack(const uint4& x, float (&v)[8]) {
+  if constexpr (F32) {
+    v[0] = __uint_as_float(x.x);
+    v[1] = __uint_as_float(x.y);
+    v[2] = __uint_as_float(x.z);
+    v[3] = __uint_as_float(x.w);
+  } else {
+    v[0] = bf16_lo(x.x);
+    v[1] = bf16_hi(x.x);
+    v[2] = bf16_lo(x.y);
+    v[3] = bf16_hi(x.y);
+    v[4] = bf16_lo(x.z);
+    v[5] = bf16_hi(x.z);
+    v[6] = bf16_lo(x.w);
+    v[7] = bf16_hi(x.w);
+  }
+}
+
+template <bool F32>
+__device__ __noinline__ double exact_squares(uint4 x) {
+  float v[8];
+  unpack<F32>(x, v);
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < (F32 ? 4 : 8); ++i) sum += static_cast<double>(v[i]) * v[i];
+  return sum;
+}
+
+// Adds the squares of a lane's batch to sum; places beyond the chunk hold 0.
+template <bool F32>
+__device__ __forceinline__ void batch_squares(const uint4 (&x)[GC_BATCH], double& sum) {
   float mx = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    mx = fmaxf(mx, fabsf(v[i]));
-    a[i % 4] = fmaf(v[i], v[i], a[i % 4]);
+  for (int j = 0; j < GC_BATCH; ++j) {
+    float v[8];
+    unpack<F32>(x[j], v);
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 8); ++i) {
+      mx = fmaxf(mx, fabsf(v[i]));
+      a[i % 4] = fmaf(v[i], v[i], a[i % 4]);
+    }
   }
   const float s = (a[0] + a[1]) + (a[2] + a[3]);
   if (in_fp32_range(mx)) {
     sum += s;  // a NaN among the values is in s
   } else if (mx != 0.f || s != 0.f) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) sum += static_cast<double>(v[i]) * v[i];
-  }
-}
-
-__device__ __forceinline__ void unpack(const uint4& x, float* v) {
-  v[0] = bf16_lo(x.x);
-  v[1] = bf16_hi(x.x);
-  v[2] = bf16_lo(x.y);
-  v[3] = bf16_hi(x.y);
-  v[4] = bf16_lo(x.z);
-  v[5] = bf16_hi(x.z);
-  v[6] = bf16_lo(x.w);
-  v[7] = bf16_hi(x.w);
-}
-
-// A lane's batch of squares.  Its words are NaN-free of padding: places beyond
-// the chunk hold 0.
-__device__ __forceinline__ void batch_squares(const uint4 (&x)[GC_BATCH], bool f32, double& sum) {
-  if (f32) {
-    float v[4 * GC_BATCH];
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < GC_BATCH; ++j) {
-      v[4 * j] = __uint_as_float(x[j].x);
-      v[4 * j + 1] = __uint_as_float(x[j].y);
-      v[4 * j + 2] = __uint_as_float(x[j].z);
-      v[4 * j + 3] = __uint_as_float(x[j].w);
-    }
-    add_squares(v, sum);
-  } else {
-    float v[8 * GC_BATCH];
+      uint4 y = x[0];
 #pragma unroll
-    for (int j = 0; j < GC_BATCH; ++j) unpack(x[j], v + 8 * j);
-    add_squares(v, sum);
+      for (int i = 1; i < GC_BATCH; ++i)
+        if (i == j) y = x[i];
+      sum += exact_squares<F32>(y);
+    }
   }
 }
 
@@ -286,7 +301,7 @@ __device__ __forceinline__ lrm_grad_stats make_stats(double squares, float max_n
   return r;
 }
 
-__global__ void __launch_bounds__(GC_THREADS) gc_norm(const Chunk* __restrict__ chunks, long long count,
+__global__ void __launch_bounds__(GC_THREADS, 2) gc_norm(const Chunk* __restrict__ chunks, long long count,
                                                       double* __restrict__ partial) {
   __shared__ double s_sum[GC_WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -304,7 +319,10 @@ __global__ void __launch_bounds__(GC_THREADS) gc_norm(const Chunk* __restrict__ 
       for (int v0 = 0; v0 < nv; v0 += 32 * GC_BATCH) {
         uint4 x[GC_BATCH];
         load_batch(static_cast<const uint4*>(c.src), v0, nv, lane, x);
-        batch_squares(x, c.kind == GC_F32_VEC, sum);
+        if (c.kind == GC_F32_VEC)
+          batch_squares<true>(x, sum);
+        else
+          batch_squares<false>(x, sum);
       }
     } else {
       sum += any_squares(c, lane);
@@ -391,7 +409,10 @@ __global__ void __launch_bounds__(GC_SMALL_THREADS) gc_small(const Chunk* __rest
   double sum = 0.0;
   if (vec) {
     load_batch(static_cast<const uint4*>(c.src), 0, vectors(c), lane, x);
-    batch_squares(x, c.kind == GC_F32_VEC, sum);
+    if (c.kind == GC_F32_VEC)
+      batch_squares<true>(x, sum);
+    else
+      batch_squares<false>(x, sum);
   } else if (i < count) {
     sum = any_squares(c, lane);
   }
@@ -516,9 +537,9 @@ extern "C" lrm_status lrm_grad_list_create(lrm_ctx* ctx, const lrm_tensor* tenso
       return LRM_ERR_CUDA;
     }
     const long long blocks = (list->chunks + GC_WARPS - 1) / GC_WARPS;
-    const int gn = resident_grid(ctx, gc_norm, GC_THREADS, 0), gc = resident_grid(ctx, gc_clip, GC_THREADS, 0);
-    const int cap_n = gn < GC_MAX_GRID ? gn : GC_MAX_GRID;
-    list->grid_norm = static_cast<int>(blocks < cap_n ? blocks : cap_n);
+    int gn = resident_grid(ctx, gc_norm, GC_THREADS, 0), gc = resident_grid(ctx, gc_clip, GC_THREADS, 0);
+    if (gn > GC_MAX_GRID) gn = GC_MAX_GRID;
+    list->grid_norm = static_cast<int>(blocks < gn ? blocks : gn);
     list->grid_clip = static_cast<int>(blocks < gc ? blocks : gc);
   }
   *out = list;

@@ -562,42 +562,70 @@ struct BackwardArgs {
   unsigned int* status;
 };
 
+// A lane's logits in the backward: C groups of four, G groups apart, so that
+// the lanes of a token read consecutive 16-byte pieces.
+template <typename TL, int G, int C>
+struct Pieces {
+  uint32_t w[C * sizeof(TL)];
+
+  __device__ __forceinline__ void load(const TL* __restrict__ row, int q, int E, bool vec) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      Raw<TL, 4> r;
+      r.load(row, 4 * (q + G * c), E, vec);
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(TL)); ++i) w[c * sizeof(TL) + i] = r.w[i];
+    }
+  }
+  __device__ __forceinline__ float get(int c, int i) const {
+    if constexpr (is_bf16<TL>)
+      return (i & 1) ? bf16_hi(w[2 * c + i / 2]) : bf16_lo(w[2 * c + i / 2]);
+    else
+      return __uint_as_float(w[4 * c + i]);
+  }
+};
+
 // What a lane reads of one token.
-template <typename TL, int VPL>
+template <typename TL, int G, int C>
 struct TokenIn {
-  Raw<TL, VPL> raw;
+  Pieces<TL, G, C> raw;
   float2 ms;  // (max, sum); sum 0: not counted
   int id;
   float dg, al;
 };
 
-template <typename TL, typename TO, int G, int VPL>
+template <typename TL, typename TO, int G, int C>
 __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ logits, TO* __restrict__ dlogits,
                                                       BackwardArgs a, bool vec_in, bool vec_out) {
   constexpr int NW = RB_THREADS / 32, PER_WARP = 32 / G;
-  __shared__ float4 s_add[NW][32 * VPL / 4];  // the gates' part of the warp's tokens
-  __shared__ uint8_t s_slot[NW][32 * VPL];    // the slot that named an expert last
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane % G, e0 = q * VPL;
+  __shared__ float4 s_add[NW][32 * C];         // the gates' part of the warp's tokens
+  __shared__ uint8_t s_slot[NW][32 * 4 * C];   // the slot that named an expert last
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane % G;
   const int T = a.T, E = a.E, k = a.k;
-  float* add = reinterpret_cast<float*>(s_add[warp]) + (lane - q) * VPL;  // the group's rows
-  uint8_t* slot_of = s_slot[warp] + (lane - q) * VPL;
-  float4* own = s_add[warp] + lane * (VPL / 4);
+  float4* own = s_add[warp] + (lane - q) * C + q;  // the group's row, at the lane's first piece
+  float* add = reinterpret_cast<float*>(s_add[warp] + (lane - q) * C);
+  uint8_t* slot_of = s_slot[warp] + (lane - q) * C * 4;
 #pragma unroll
-  for (int c = 0; c < VPL / 4; ++c) own[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < C; ++c) own[c * G] = make_float4(0.f, 0.f, 0.f, 0.f);
   const float tc = static_cast<float>(max(1, a.losses->tokens));
   const float ca = a.aux_coef * static_cast<float>(E) / tc, cz = 2.f * a.z_coef / tc;
-  float cf[VPL];
+  float cf[C][4];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) cf[i] = e0 + i < E ? ca * a.f[e0 + i] : 0.f;
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * (q + G * c) + i;
+      cf[c][i] = e < E ? ca * a.f[e] : 0.f;
+    }
   __syncwarp();
 
   const bool gates = a.dgate != nullptr;
   const long long step = static_cast<long long>(gridDim.x) * NW * PER_WARP;
   long long t = (static_cast<long long>(blockIdx.x) * NW + warp) * PER_WARP + lane / G;
   const auto load = [&](long long at) {
-    TokenIn<TL, VPL> x;
+    TokenIn<TL, G, C> x;
     const bool in = at < T;
-    x.raw.load(logits + static_cast<size_t>(at) * E, e0, in ? E : 0, vec_in);
+    x.raw.load(logits + static_cast<size_t>(at) * E, q, in ? E : 0, vec_in);
     x.ms = in ? __ldg(a.row_stats + at) : make_float2(0.f, 0.f);
     x.id = 0;
     x.dg = x.al = 0.f;
@@ -609,31 +637,38 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
     }
     return x;
   };
-  TokenIn<TL, VPL> next = load(t);
+  TokenIn<TL, G, C> next = load(t);
   for (; t - lane / G < T; t += step) {
-    const bool here = G == 32 || t < T;
-    const TokenIn<TL, VPL> x = next;
+    const TokenIn<TL, G, C> x = next;
     next = load(t + step);
     const bool counted = x.ms.y != 0.f;
+    const bool rare = __any_sync(0xffffffffu, !counted);  // a token of the warp that gets zeros, or none
     const float inv = rcp(x.ms.y);
-    float p[VPL], fp = 0.f, dg = x.dg;
+    float p[C][4], dg = x.dg;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) p[i] = exp_neg(x.raw.get(i) - x.ms.x) * inv;
-    int e = gates && counted && q < k ? x.id : -1;
-    dg = counted ? dg : 0.f;
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) p[i] = counted ? p[i] : 0.f;
+      for (int i = 0; i < 4; ++i) p[c][i] = exp_neg(x.raw.get(c, i) - x.ms.x) * inv;
+    int e = gates && q < k ? x.id : -1;
+    if (rare && !counted) {
+      e = -1;
+      dg = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) fp = fmaf(cf[i], p[i], fp);
-    float w = 0.f;
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[c][i] = 0.f;
+    }
+    float fp = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fp = fmaf(cf[c][i], p[c][i], fp);
     if (gates) {
-      bool bad = static_cast<unsigned>(e) >= static_cast<unsigned>(E);
-      if (!bad) slot_of[e] = static_cast<uint8_t>(q);
+      const bool in = static_cast<unsigned>(e) < static_cast<unsigned>(E);
+      if (in) slot_of[e] = static_cast<uint8_t>(q);
       __syncwarp();
-      const bool lost = !bad && slot_of[e] != q;
-      bad = bad && counted && q < k;
+      const bool lost = in && slot_of[e] != q, bad = !in && q < k && counted;
       if (__any_sync(0xffffffffu, bad || lost)) {  // an id out of range, or one named by several slots
-        const bool in = !bad && e >= 0;
         const unsigned peers = __match_any_sync(0xffffffffu, in ? ((lane - q) << 16) | e : -1 - lane);
         if (bad || (in && (peers & ((1u << lane) - 1u)) != 0)) {
           raise_flag(a.status, LRM_ERR_INDEX);
@@ -650,20 +685,20 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
       }
       __syncwarp();
     }
-    w -= group_sum<G>(fp);
-    if (cz != 0.f && counted) w = fmaf(cz, x.ms.x + __log2f(x.ms.y) * LN2, w);
-    float out[VPL];
+    float w = -group_sum<G>(fp);
+    if (cz != 0.f) w = counted ? fmaf(cz, x.ms.x + __log2f(x.ms.y) * LN2, w) : 0.f;
+    TO* row = dlogits + static_cast<size_t>(t) * E;
 #pragma unroll
-    for (int c = 0; c < VPL / 4; ++c) {
-      const float4 g = own[c];
-      out[4 * c] = fmaf(p[4 * c], cf[4 * c] + w, g.x);
-      out[4 * c + 1] = fmaf(p[4 * c + 1], cf[4 * c + 1] + w, g.y);
-      out[4 * c + 2] = fmaf(p[4 * c + 2], cf[4 * c + 2] + w, g.z);
-      out[4 * c + 3] = fmaf(p[4 * c + 3], cf[4 * c + 3] + w, g.w);
+    for (int c = 0; c < C; ++c) {
+      const float4 g = own[c * G];
+      float out[4];
+      out[0] = fmaf(p[c][0], cf[c][0] + w, g.x);
+      out[1] = fmaf(p[c][1], cf[c][1] + w, g.y);
+      out[2] = fmaf(p[c][2], cf[c][2] + w, g.z);
+      out[3] = fmaf(p[c][3], cf[c][3] + w, g.w);
+      if (rare && !counted) out[0] = out[1] = out[2] = out[3] = 0.f;
+      if (t < T) store_row<TO, 4>(row, 4 * (q + G * c), E, vec_out, out);
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) out[i] = counted ? out[i] : 0.f;
-    if (here) store_row<TO, VPL>(dlogits + static_cast<size_t>(t) * E, e0, E, vec_out, out);
     __syncwarp();
     if (e >= 0) add[e] = 0.f;
     __syncwarp();
@@ -701,31 +736,39 @@ lrm_status dispatch_rf(const void* logits, const ForwardArgs& a, int nblk, cudaS
   return launch_rf<TL, 32, 32>(l, a, nblk, vec, s);
 }
 
-template <typename TL, typename TO, int G, int VPL>
+template <typename TL, typename TO, int G, int C>
 lrm_status launch_rb(lrm_ctx* ctx, const TL* logits, TO* dlogits, const BackwardArgs& a, cudaStream_t s) {
   static thread_local int dev = -1, grid = 0;
   if (dev != ctx->device) {
-    grid = resident_grid(ctx, rb_rows<TL, TO, G, VPL>, RB_THREADS, 0);
+    grid = resident_grid(ctx, rb_rows<TL, TO, G, C>, RB_THREADS, 0);
     dev = ctx->device;
   }
   const long long pass = RB_THREADS / G, need = (a.T + pass - 1) / pass;
-  rb_rows<TL, TO, G, VPL><<<static_cast<int>(need < grid ? need : grid), RB_THREADS, 0, s>>>(
+  rb_rows<TL, TO, G, C><<<static_cast<int>(need < grid ? need : grid), RB_THREADS, 0, s>>>(
       logits, dlogits, a, rows_vec(logits, a.E), rows_vec(dlogits, a.E));
   return launch_status();
 }
 
+// Lanes a token and groups of four a lane: the fewest lanes that have a slot
+// each and no more than 16 logits, so that what a token costs once (its
+// reductions, its slots, its addresses) is shared by the tokens of a warp.
 template <typename TL, typename TO>
 lrm_status dispatch_rb(lrm_ctx* ctx, const void* logits, void* dlogits, const BackwardArgs& a, cudaStream_t s) {
   const TL* l = static_cast<const TL*>(logits);
   TO* o = static_cast<TO*>(dlogits);
-  const Split sp = split_of(a.E, a.k);
-  if (sp.G == 4) return launch_rb<TL, TO, 4, 4>(ctx, l, o, a, s);
-  if (sp.G == 8) return launch_rb<TL, TO, 8, 4>(ctx, l, o, a, s);
-  if (sp.G == 16) return launch_rb<TL, TO, 16, 4>(ctx, l, o, a, s);
-  if (sp.VPL == 4) return launch_rb<TL, TO, 32, 4>(ctx, l, o, a, s);
-  if (sp.VPL == 8) return launch_rb<TL, TO, 32, 8>(ctx, l, o, a, s);
-  if (sp.VPL == 16) return launch_rb<TL, TO, 32, 16>(ctx, l, o, a, s);
-  return launch_rb<TL, TO, 32, 32>(ctx, l, o, a, s);
+  const int E = a.E, k = a.k;
+  if (E <= 16 && k <= 4) return launch_rb<TL, TO, 4, 1>(ctx, l, o, a, s);
+  if (E <= 32 && k <= 8) return launch_rb<TL, TO, 8, 1>(ctx, l, o, a, s);
+  if (E <= 64 && k <= 8) return launch_rb<TL, TO, 8, 2>(ctx, l, o, a, s);
+  if (E <= 128 && k <= 8) return launch_rb<TL, TO, 8, 4>(ctx, l, o, a, s);
+  if (E <= 64 && k <= 16) return launch_rb<TL, TO, 16, 1>(ctx, l, o, a, s);
+  if (E <= 128 && k <= 16) return launch_rb<TL, TO, 16, 2>(ctx, l, o, a, s);
+  if (E <= 192 && k <= 16) return launch_rb<TL, TO, 16, 3>(ctx, l, o, a, s);
+  if (E <= 256 && k <= 16) return launch_rb<TL, TO, 16, 4>(ctx, l, o, a, s);
+  if (E <= 128) return launch_rb<TL, TO, 32, 1>(ctx, l, o, a, s);
+  if (E <= 256) return launch_rb<TL, TO, 32, 2>(ctx, l, o, a, s);
+  if (E <= 512) return launch_rb<TL, TO, 32, 4>(ctx, l, o, a, s);
+  return launch_rb<TL, TO, 32, 8>(ctx, l, o, a, s);
 }
 
 bool dtype_ok(int32_t t) { return t == LRM_F32 || t == LRM_BF16; }
