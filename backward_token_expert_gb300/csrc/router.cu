@@ -28,34 +28,61 @@
 // and rows of -inf.
 #include <math.h>
 
+#include <type_traits>
+
 #include "lrm_internal.cuh"
 #include "vec.cuh"
 
 namespace lrm {
 namespace {
 
-constexpr int RF_MAX_THREADS = 1024;  // one block an SM: few sums for rf_sums to add
 constexpr int RF_ONE_BLOCK_PASSES = 2;  // batches of up to this many passes of one block use one block
 constexpr int RS_SUM_THREADS = 1024;
 constexpr int RB_THREADS = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
-// Lanes per token and logits per lane of a layer: at least four logits a
-// lane (one 16-byte load of fp32), a lane for each of the k slots.
+// Lanes per token (G) and groups of four logits per lane (C): the fewest lanes
+// that have a slot each and at most 16 logits (32 for the widest layers), so
+// that what a token costs once (reductions, slots, addresses) is shared by the
+// tokens of a warp.  A warp a token took 346 instructions at E = 128 (46 us for
+// 131072 tokens), four tokens a warp take RF_MEASURED.
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 struct Split {
-  int G, VPL;
+  int G, C;
 };
+constexpr Split kSplits[] = {{4, 1}, {8, 1}, {8, 2}, {8, 4}, {16, 1}, {16, 2}, {16, 3}, {16, 4}, {32, 1}, {32, 2}, {32, 4}, {32, 8}};
 Split split_of(int E, int k) {
-  if (E <= 16 && k <= 4) return {4, 4};
-  if (E <= 32 && k <= 8) return {8, 4};
-  if (E <= 64 && k <= 16) return {16, 4};
-  if (E <= 128) return {32, 4};
-  if (E <= 256) return {32, 8};
-  if (E <= 512) return {32, 16};
-  return {32, 32};
+  for (const Split& s : kSplits)
+    if (E <= 4 * s.G * s.C && k <= s.G) return s;
+  return {32, 8};
 }
-__host__ __device__ constexpr int rf_threads(int vpl) { return vpl <= 8 ? RF_MAX_THREADS : RF_MAX_THREADS / 4; }
+
+// Calls run(std::integral_constant...) with the layer's G and C.
+template <typename Run>
+lrm_status with_split(int E, int k, Run run) {
+  const Split s = split_of(E, k);
+  const auto pick = [&](auto g, auto c) { return run(g, c); };
+  switch (s.G * 16 + s.C) {
+    case 4 * 16 + 1: return pick(Int<4>{}, Int<1>{});
+    case 8 * 16 + 1: return pick(Int<8>{}, Int<1>{});
+    case 8 * 16 + 2: return pick(Int<8>{}, Int<2>{});
+    case 8 * 16 + 4: return pick(Int<8>{}, Int<4>{});
+    case 16 * 16 + 1: return pick(Int<16>{}, Int<1>{});
+    case 16 * 16 + 2: return pick(Int<16>{}, Int<2>{});
+    case 16 * 16 + 3: return pick(Int<16>{}, Int<3>{});
+    case 16 * 16 + 4: return pick(Int<16>{}, Int<4>{});
+    case 32 * 16 + 1: return pick(Int<32>{}, Int<1>{});
+    case 32 * 16 + 2: return pick(Int<32>{}, Int<2>{});
+    case 32 * 16 + 4: return pick(Int<32>{}, Int<4>{});
+  }
+  return pick(Int<32>{}, Int<8>{});
+}
+
+// Threads of a block of rf_rows: as many as the registers of C groups allow.
+__host__ __device__ constexpr int rf_threads(int C) { return C == 1 ? 1024 : C <= 4 ? 512 : 256; }
 
 struct RouterLayout {
   int nblk;  // blocks of rf_rows
@@ -65,7 +92,7 @@ struct RouterLayout {
 RouterLayout router_layout(const lrm_ctx* ctx, const lrm_dims& d) {
   RouterLayout L;
   const Split sp = split_of(d.E, d.k);
-  const long long pass = rf_threads(sp.VPL) / sp.G;  // tokens of a block in flight
+  const long long pass = rf_threads(sp.C) / sp.G;  // tokens of a block in flight
   long long need = (static_cast<long long>(d.T) + pass - 1) / pass;
   if (need <= RF_ONE_BLOCK_PASSES) need = need > 0 ? 1 : 0;
   const long long cap = ctx->sm_count;
@@ -90,70 +117,81 @@ __device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bf
 __device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// VPL consecutive logits of a lane as they lie in memory; places beyond the
-// row hold -inf.  vec: rows start at a multiple of four elements' bytes.
-template <typename TL, int VPL>
-struct Raw {
-  uint32_t w[VPL * sizeof(TL) / 4];
+// Four consecutive logits as they lie in memory; places beyond the row hold
+// -inf.  vec: rows start at a multiple of four elements' bytes.
+template <typename TL>
+struct Four {
+  uint32_t w[sizeof(TL)];
 
   __device__ __forceinline__ void load(const TL* __restrict__ row, int e0, int E, bool vec) {
+    constexpr uint32_t none = is_bf16<TL> ? 0xFF80FF80u : 0xFF800000u;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(TL)); ++i) w[i] = none;
     if (vec) {
-#pragma unroll
-      for (int c = 0; c < VPL / 4; ++c) {
-        const bool in = e0 + 4 * c < E;
-        if constexpr (is_bf16<TL>) {
-          const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(row + e0) + c) : make_uint2(0xFF80FF80u, 0xFF80FF80u);
-          w[2 * c] = x.x;
-          w[2 * c + 1] = x.y;
-        } else {
-          const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(row + e0) + c)
-                             : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
-          w[4 * c] = x.x;
-          w[4 * c + 1] = x.y;
-          w[4 * c + 2] = x.z;
-          w[4 * c + 3] = x.w;
-        }
-      }
-    } else if constexpr (is_bf16<TL>) {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
-#pragma unroll
-      for (int i = 0; i < VPL / 2; ++i) {
-        const uint32_t lo = e0 + 2 * i < E ? __ldg(p + e0 + 2 * i) : 0xFF80u;
-        const uint32_t hi = e0 + 2 * i + 1 < E ? __ldg(p + e0 + 2 * i + 1) : 0xFF80u;
-        w[i] = lo | hi << 16;
+      if (e0 >= E) return;
+      if constexpr (is_bf16<TL>) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(row + e0));
+        w[0] = x.x;
+        w[1] = x.y;
+      } else {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + e0));
+        w[0] = x.x;
+        w[1] = x.y;
+        w[2] = x.z;
+        w[3] = x.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        w[i] = e0 + i < E ? __float_as_uint(__ldg(reinterpret_cast<const float*>(row) + e0 + i)) : 0xFF800000u;
+      for (int i = 0; i < 4; ++i) {
+        if (e0 + i >= E) continue;
+        if constexpr (is_bf16<TL>) {
+          const uint32_t x = __ldg(reinterpret_cast<const uint16_t*>(row) + e0 + i);
+          w[i / 2] = (i & 1) ? (w[i / 2] & 0xFFFFu) | x << 16 : (w[i / 2] & 0xFFFF0000u) | x;
+        } else {
+          w[i] = __float_as_uint(__ldg(reinterpret_cast<const float*>(row) + e0 + i));
+        }
+      }
     }
-  }
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (is_bf16<TL>)
-      return (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
-    else
-      return __uint_as_float(w[i]);
   }
 };
 
-template <typename TO, int VPL>
-__device__ __forceinline__ void store_row(TO* __restrict__ row, int e0, int E, bool vec, const float (&v)[VPL]) {
-  if (vec) {
+// A lane's logits: C groups of four, G groups apart, so that
+// the lanes of a token read consecutive 16-byte pieces.
+template <typename TL, int G, int C>
+struct Pieces {
+  uint32_t w[C * sizeof(TL)];
+
+  __device__ __forceinline__ void load(const TL* __restrict__ row, int q, int E, bool vec) {
 #pragma unroll
-    for (int c = 0; c < VPL / 4; ++c) {
-      if (e0 + 4 * c >= E) continue;
-      if constexpr (is_bf16<TO>) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v[4 * c], v[4 * c + 1]);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[4 * c + 2], v[4 * c + 3]);
-        reinterpret_cast<uint2*>(row + e0)[c] =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-      } else {
-        reinterpret_cast<float4*>(row + e0)[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-      }
+    for (int c = 0; c < C; ++c) {
+      Four<TL> r;
+      r.load(row, 4 * (q + G * c), E, vec);
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(TL)); ++i) w[c * sizeof(TL) + i] = r.w[i];
+    }
+  }
+  __device__ __forceinline__ float get(int c, int i) const {
+    if constexpr (is_bf16<TL>)
+      return (i & 1) ? bf16_hi(w[2 * c + i / 2]) : bf16_lo(w[2 * c + i / 2]);
+    else
+      return __uint_as_float(w[4 * c + i]);
+  }
+};
+
+template <typename TO>
+__device__ __forceinline__ void store_four(TO* __restrict__ row, int e0, int E, bool vec, const float (&v)[4]) {
+  if (vec) {
+    if (e0 >= E) return;
+    if constexpr (is_bf16<TO>) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+      *reinterpret_cast<uint2*>(row + e0) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+      *reinterpret_cast<float4*>(row + e0) = make_float4(v[0], v[1], v[2], v[3]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
+    for (int i = 0; i < 4; ++i)
       if (e0 + i < E) store_elem(row + e0 + i, v[i]);
   }
 }
@@ -243,35 +281,76 @@ __device__ __forceinline__ void sort_desc(uint32_t (&a)[N]) {
   }
 }
 
-// The exact selection: k rounds over full keys, NaN below -inf, equal keys to
-// the lower expert (the lower lane, then the lower place).  Returns slot q's
-// expert.
-template <typename TL, int G, int VPL>
-__device__ __noinline__ int select_exact(Raw<TL, VPL> raw, int E, int k) {
-  const int lane = threadIdx.x & 31, q = lane % G;
-  const unsigned group = (G == 32 ? 0xffffffffu : ((1u << G) - 1u)) << (lane - q);
-  uint32_t key[VPL];
+// a: the eight largest of two descending lists of eight, descending.  The
+// larger of a[i] and b[7 - i] are those eight, as a bitonic list.
+__device__ __forceinline__ void merge_top8(uint32_t* a, const uint32_t* b) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const float v = raw.get(i);
-    key[i] = q * VPL + i >= E ? 0u : v != v ? 1u : order_key(v);
+  for (int i = 0; i < 8; ++i) a[i] = max(a[i], b[7 - i]);
+#pragma unroll
+  for (int d = 4; d >= 1; d /= 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((i & d) == 0) {
+        const uint32_t hi = max(a[i], a[i + d]), lo = min(a[i], a[i + d]);
+        a[i] = hi;
+        a[i + d] = lo;
+      }
+    }
   }
+}
+
+// The keys' LIST largest in front, descending.
+template <int N, int LIST>
+__device__ __forceinline__ void sort_top(uint32_t (&a)[N]) {
+  if constexpr (LIST >= N) {
+    sort_desc(a);
+  } else {
+    static_assert(LIST == 8 && N % 8 == 0, "lists of eight");
+#pragma unroll
+    for (int b = 0; b < N / 8; ++b) {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = a[8 * b + i];
+      sort_desc(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[8 * b + i] = v[i];
+      if (b > 0) merge_top8(a, a + 8 * b);
+    }
+  }
+}
+
+// The exact selection: k rounds over full keys, NaN below -inf, equal keys to
+// the lower expert.  Returns slot q's expert.
+template <typename TL, int G, int C>
+__device__ __noinline__ int select_exact(const TL* row, int E, int k, bool vec) {
+  const int lane = threadIdx.x & 31, q = lane % G;
+  Pieces<TL, G, C> raw;
+  raw.load(row, q, E, vec);
+  uint32_t key[C][4];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = raw.get(c, i);
+      key[c][i] = 4 * (q + G * c) + i >= E ? 0u : v != v ? 1u : order_key(v);
+    }
   int mine = 0;
   for (int j = 0; j < k; ++j) {
-    uint32_t best = key[0];
+    uint32_t best = 0;
     int at = 0;
 #pragma unroll
-    for (int i = 1; i < VPL; ++i)
-      if (key[i] > best) best = key[i], at = i;
-    const uint32_t top = group_max<G>(best);
-    const int win = __ffs(__ballot_sync(0xffffffffu, best == top) & group) - 1;
-    const int e = __shfl_sync(0xffffffffu, q * VPL + at, win);
-    if (q == j) mine = e;
-    if (lane == win) {
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i == at) key[i] = 0u;
-    }
+      for (int i = 0; i < 4; ++i)
+        if (key[c][i] > best) best = key[c][i], at = 4 * (q + G * c) + i;
+    const uint32_t top = group_max<G>(best);
+    const int e = static_cast<int>(~group_max<G>(best == top ? ~static_cast<uint32_t>(at) : 0u));
+    if (q == j) mine = e;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * (q + G * c) + i == e) key[c][i] = 0u;
   }
   return mine;
 }
@@ -393,10 +472,11 @@ __global__ void __launch_bounds__(RS_SUM_THREADS) rf_sums(ForwardArgs a, int nbl
   if (threadIdx.x == 0) write_losses(a, fp, z, tokens);
 }
 
-template <typename TL, int G, int VPL>
-__global__ void __launch_bounds__(rf_threads(VPL), 1) rf_rows(const TL* __restrict__ logits, ForwardArgs a, bool vec) {
-  constexpr int NT = rf_threads(VPL), NW = NT / 32, PER_WARP = 32 / G;
-  constexpr uint32_t LOW = G * VPL - 1;  // the key's bits that hold the expert
+template <typename TL, int G, int C, int LIST>
+__global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict__ logits, ForwardArgs a, bool vec) {
+  constexpr int NT = rf_threads(C), NW = NT / 32, PER_WARP = 32 / G, N = 4 * C;
+  constexpr int NK = C == 3 ? 16 : N;    // keys of a lane, a power of two
+  constexpr uint32_t LOW = G * NK - 1;  // the key's bits that hold the expert
   extern __shared__ float rt_smem[];
   float* sp = rt_smem;                                     // [NW][E]
   int* hist = reinterpret_cast<int*>(rt_smem + NW * a.E);  // [E]
@@ -404,60 +484,60 @@ __global__ void __launch_bounds__(rf_threads(VPL), 1) rf_rows(const TL* __restri
   __shared__ float s_z[NW];
   __shared__ int s_tok[NW];
   __shared__ float s_fp[NW];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = lane % G, e0 = q * VPL;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = lane % G;
   const int T = a.T, E = a.E, k = a.k;
   uint32_t* sel = s_sel[warp] + (lane - q);
   grid_dependency_launch();
   for (int i = tid; i < E; i += NT) hist[i] = 0;
   __syncthreads();
 
-  float acc[VPL];
+  float acc[N];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
   // (m, s) of the group's counted tokens are kept a lane each until G are there
   float z = 0.f, km = 0.f, ks = 1.f;
   int held = 0, tokens = 0;
-  // tokens lie 32-bit (T < 2^31); the first token of the warp, its groups' tokens follow
   const long long step = static_cast<long long>(gridDim.x) * NW * PER_WARP;
   long long t = (static_cast<long long>(blockIdx.x) * NW + warp) * PER_WARP + lane / G;
   const TL* row = logits + static_cast<size_t>(t) * E;
   const size_t row_step = static_cast<size_t>(step) * E;
-  Raw<TL, VPL> next;
-  next.load(row, e0, t < T ? E : 0, vec);
+  Pieces<TL, G, C> next;
+  next.load(row, q, t < T ? E : 0, vec);
   for (; t - lane / G < T; t += step, row += row_step) {
     const bool here = G == 32 || t < T;
-    const Raw<TL, VPL> raw = next;
-    next.load(row + row_step, e0, t + step < T ? E : 0, vec);
+    const Pieces<TL, G, C> raw = next;
+    next.load(row + row_step, q, t + step < T ? E : 0, vec);
     bool ok = here;
     if (a.valid != nullptr && here) ok = a.valid[t] != 0;
 
-    float m = raw.get(0);
+    float m = raw.get(0, 0);
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) m = fmaxf(m, raw.get(i));
+    for (int i = 1; i < N; ++i) m = fmaxf(m, raw.get(i / 4, i % 4));
     m = group_fmax<G>(m);
     const float base = m == -INFINITY ? 0.f : m;
-    uint32_t key[VPL];
-    float p[VPL], s = 0.f;
+    uint32_t key[NK] = {};
+    float p[N], s = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const float d = raw.get(i) - base;  // <= 0: the larger its bits, the smaller it is
-      const uint32_t order = is_bf16<TL> ? order_key(raw.get(i)) : ~__float_as_uint(d);
-      key[i] = (order & ~LOW) | (LOW - (e0 + i));
+    for (int i = 0; i < N; ++i) {
+      const float v = raw.get(i / 4, i % 4), d = v - base;  // <= 0: the larger its bits, the smaller it is
+      const uint32_t order = is_bf16<TL> ? order_key(v) : ~__float_as_uint(d);
+      key[i] = (order & ~LOW) | (LOW - static_cast<uint32_t>(4 * (q + G * (i / 4)) + i % 4));
       p[i] = exp_neg(d);
       s += p[i];
     }
     s = group_sum<G>(s);
     const bool counted = ok && s != 0.f;
 
-    sort_desc(key);
+    sort_top<NK, LIST>(key);
+    constexpr int L = LIST;
 #pragma unroll 4
     for (int j = 0; j < k; ++j) {
       const uint32_t top = group_max<G>(key[0]);
       const bool hit = key[0] == top;
       if (hit) sel[j] = top;
 #pragma unroll
-      for (int i = 0; i + 1 < VPL; ++i) key[i] = hit ? key[i + 1] : key[i];
-      key[VPL - 1] = hit ? 0u : key[VPL - 1];
+      for (int i = 0; i + 1 < L; ++i) key[i] = hit ? key[i + 1] : key[i];
+      key[L - 1] = hit ? 0u : key[L - 1];
     }
     uint32_t after = 0;  // the largest key left out
     if constexpr (!is_bf16<TL>) after = group_max<G>(key[0]);
@@ -472,7 +552,7 @@ __global__ void __launch_bounds__(rf_threads(VPL), 1) rf_rows(const TL* __restri
       unclear = unclear || (slot && (q == k - 1 ? (mine ^ after) <= LOW : v < vn));
     }
     if (__any_sync(0xffffffffu, unclear)) {
-      e = select_exact<TL, G, VPL>(raw, E, k);
+      e = select_exact<TL, G, C>(row, here ? E : 0, k, vec);
       if (slot) v = load_elem(row + e);
     }
     __syncwarp();  // sel is read before the next token writes it
@@ -489,7 +569,7 @@ __global__ void __launch_bounds__(rf_threads(VPL), 1) rf_rows(const TL* __restri
     if (counted) {
       const float inv = rcp(s);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
+      for (int i = 0; i < N; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
       if (q == held) km = base, ks = s;
       ++tokens;
       if (++held == G) {
@@ -511,12 +591,14 @@ __global__ void __launch_bounds__(rf_threads(VPL), 1) rf_rows(const TL* __restri
 #pragma unroll
   for (int o = G; o < 32; o <<= 1) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    for (int i = 0; i < N; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
   }
   if (lane < G) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (e0 + i < E) sp[warp * E + e0 + i] = acc[i];
+    for (int i = 0; i < N; ++i) {
+      const int e = 4 * (q + G * (i / 4)) + i % 4;
+      if (e < E) sp[warp * E + e] = acc[i];
+    }
   }
   __syncthreads();
   const bool alone = gridDim.x == 1;
@@ -560,29 +642,6 @@ struct BackwardArgs {
   int T, E, k, renorm;
   float aux_coef, z_coef;
   unsigned int* status;
-};
-
-// A lane's logits in the backward: C groups of four, G groups apart, so that
-// the lanes of a token read consecutive 16-byte pieces.
-template <typename TL, int G, int C>
-struct Pieces {
-  uint32_t w[C * sizeof(TL)];
-
-  __device__ __forceinline__ void load(const TL* __restrict__ row, int q, int E, bool vec) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      Raw<TL, 4> r;
-      r.load(row, 4 * (q + G * c), E, vec);
-#pragma unroll
-      for (int i = 0; i < static_cast<int>(sizeof(TL)); ++i) w[c * sizeof(TL) + i] = r.w[i];
-    }
-  }
-  __device__ __forceinline__ float get(int c, int i) const {
-    if constexpr (is_bf16<TL>)
-      return (i & 1) ? bf16_hi(w[2 * c + i / 2]) : bf16_lo(w[2 * c + i / 2]);
-    else
-      return __uint_as_float(w[4 * c + i]);
-  }
 };
 
 // What a lane reads of one token.
@@ -697,7 +756,7 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
       out[2] = fmaf(p[c][2], cf[c][2] + w, g.z);
       out[3] = fmaf(p[c][3], cf[c][3] + w, g.w);
       if (rare && !counted) out[0] = out[1] = out[2] = out[3] = 0.f;
-      if (t < T) store_row<TO, 4>(row, 4 * (q + G * c), E, vec_out, out);
+      if (t < T) store_four<TO>(row, 4 * (q + G * c), E, vec_out, out);
     }
     __syncwarp();
     if (e >= 0) add[e] = 0.f;
@@ -708,11 +767,11 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
 // ---------------------------------------------------------------------------
 // launches
 
-template <typename TL, int G, int VPL>
+template <typename TL, int G, int C, int LIST>
 lrm_status launch_rf(const TL* logits, const ForwardArgs& a, int nblk, bool vec, cudaStream_t s) {
-  constexpr int NT = rf_threads(VPL);
+  constexpr int NT = rf_threads(C);
   const size_t smem = static_cast<size_t>(NT / 32 + 1) * a.E * sizeof(float);
-  rf_rows<TL, G, VPL><<<nblk, NT, smem, s>>>(logits, a, vec);
+  rf_rows<TL, G, C, LIST><<<nblk, NT, smem, s>>>(logits, a, vec);
   return launch_status();
 }
 
@@ -722,18 +781,18 @@ bool rows_vec(const T* p, int E) {
   return E % 4 == 0 && aligned(p, 4 * sizeof(T));
 }
 
+// A lane's list holds as many keys as slots can come from it: 8 where k <= 8.
 template <typename TL>
 lrm_status dispatch_rf(const void* logits, const ForwardArgs& a, int nblk, cudaStream_t s) {
   const TL* l = static_cast<const TL*>(logits);
   const bool vec = rows_vec(l, a.E);
-  const Split sp = split_of(a.E, a.k);
-  if (sp.G == 4) return launch_rf<TL, 4, 4>(l, a, nblk, vec, s);
-  if (sp.G == 8) return launch_rf<TL, 8, 4>(l, a, nblk, vec, s);
-  if (sp.G == 16) return launch_rf<TL, 16, 4>(l, a, nblk, vec, s);
-  if (sp.VPL == 4) return launch_rf<TL, 32, 4>(l, a, nblk, vec, s);
-  if (sp.VPL == 8) return launch_rf<TL, 32, 8>(l, a, nblk, vec, s);
-  if (sp.VPL == 16) return launch_rf<TL, 32, 16>(l, a, nblk, vec, s);
-  return launch_rf<TL, 32, 32>(l, a, nblk, vec, s);
+  return with_split(a.E, a.k, [&](auto g, auto c) {
+    constexpr int G = decltype(g)::value, C = decltype(c)::value;
+    if constexpr (C > 2 && G > 8) {
+      if (a.k > 8) return launch_rf<TL, G, C, C == 3 ? 16 : 4 * C>(l, a, nblk, vec, s);
+    }
+    return launch_rf<TL, G, C, (C > 2 ? 8 : 4 * C)>(l, a, nblk, vec, s);
+  });
 }
 
 template <typename TL, typename TO, int G, int C>
@@ -749,26 +808,12 @@ lrm_status launch_rb(lrm_ctx* ctx, const TL* logits, TO* dlogits, const Backward
   return launch_status();
 }
 
-// Lanes a token and groups of four a lane: the fewest lanes that have a slot
-// each and no more than 16 logits, so that what a token costs once (its
-// reductions, its slots, its addresses) is shared by the tokens of a warp.
 template <typename TL, typename TO>
 lrm_status dispatch_rb(lrm_ctx* ctx, const void* logits, void* dlogits, const BackwardArgs& a, cudaStream_t s) {
-  const TL* l = static_cast<const TL*>(logits);
-  TO* o = static_cast<TO*>(dlogits);
-  const int E = a.E, k = a.k;
-  if (E <= 16 && k <= 4) return launch_rb<TL, TO, 4, 1>(ctx, l, o, a, s);
-  if (E <= 32 && k <= 8) return launch_rb<TL, TO, 8, 1>(ctx, l, o, a, s);
-  if (E <= 64 && k <= 8) return launch_rb<TL, TO, 8, 2>(ctx, l, o, a, s);
-  if (E <= 128 && k <= 8) return launch_rb<TL, TO, 8, 4>(ctx, l, o, a, s);
-  if (E <= 64 && k <= 16) return launch_rb<TL, TO, 16, 1>(ctx, l, o, a, s);
-  if (E <= 128 && k <= 16) return launch_rb<TL, TO, 16, 2>(ctx, l, o, a, s);
-  if (E <= 192 && k <= 16) return launch_rb<TL, TO, 16, 3>(ctx, l, o, a, s);
-  if (E <= 256 && k <= 16) return launch_rb<TL, TO, 16, 4>(ctx, l, o, a, s);
-  if (E <= 128) return launch_rb<TL, TO, 32, 1>(ctx, l, o, a, s);
-  if (E <= 256) return launch_rb<TL, TO, 32, 2>(ctx, l, o, a, s);
-  if (E <= 512) return launch_rb<TL, TO, 32, 4>(ctx, l, o, a, s);
-  return launch_rb<TL, TO, 32, 8>(ctx, l, o, a, s);
+  return with_split(a.E, a.k, [&](auto g, auto c) {
+    return launch_rb<TL, TO, decltype(g)::value, decltype(c)::value>(ctx, static_cast<const TL*>(logits),
+                                                                      static_cast<TO*>(dlogits), a, s);
+  });
 }
 
 bool dtype_ok(int32_t t) { return t == LRM_F32 || t == LRM_BF16; }
