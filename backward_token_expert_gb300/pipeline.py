@@ -466,6 +466,68 @@ class GradClip:
         L.lrm_grad_clip(self.ctx, self.list, max_norm, self._stats, stream)
 
 
+class TrainingStep:
+    """One MoE layer's share of a training step: the router's forward, the
+    recalibrated backward of the experts, the router's backward and the clipping
+    of the layer's weight gradients, enqueued on one stream with no host
+    synchronisation in between.
+
+        route      logits -> ids, gates, balance and z losses (``router``)
+        backward   route stats .. wgrad (``rec``), gate gradients, the FC1 side,
+                   dlogits, the router's weight and input gradients (one
+                   "expert" of E rows through the grouped GEMMs), clipping
+
+    Results: ``rec.buf.dW`` [E, h, I], ``rec.fc1.dW1`` [E, 2I, h] and ``dWr`` [E, h]
+    fp32, clipped in place to the norm `max_norm` over all three; ``rec.fc1.dx``
+    and ``dxr`` [T, h] bf16, the token gradients through the experts and through
+    the router; ``clip.norm``, ``clip.coef``, ``clip.nonfinite``.  E is a multiple
+    of 8 (the grouped GEMMs' row width for the router's weight [E, h])."""
+
+    def __init__(self, T, E, k, h, I, cf=Fraction(5, 4), rho=Fraction(3, 4), aux_coef: float = 0.01,
+                 z_coef: float = 0.001, max_norm: float = 1.0, device=0):
+        if int(E) % 8 != 0:
+            raise ValueError("the router's weight gradient needs a multiple of 8 experts")
+        if not max_norm >= 0:
+            raise ValueError("max_norm must be at least 0")
+        self.rec = Recalibration(T, E, k, h, I, cf, rho, device=device)
+        dev = self.rec.device
+        self.max_norm = float(max_norm)
+        self.router = Router(T, E, k, True, aux_coef, z_coef, dtype=torch.float32, dlogits_dtype=torch.bfloat16,
+                             device=dev, ctx=self.rec.ctx)
+        self.dWr = torch.zeros(E, h, dtype=torch.float32, device=dev)
+        self.dxr = torch.zeros(T, h, dtype=torch.bfloat16, device=dev)
+        self._dims_r = L.dims_of(T, 1, 1, E, h)  # the router as one expert: rows of width E, weight [E, h]
+        self._segment = torch.tensor([0, T], dtype=torch.int32, device=dev)
+        self.clip = GradClip([self.rec.buf.dW, self.rec._fc1_buffers().dW1, self.dWr], ctx=self.rec.ctx)
+
+    def route(self, logits, valid=None, stream=None):
+        """Ids and gates of the batch (``router.expert_idx``, ``router.alpha``) and its losses."""
+        self.router.forward(logits, valid, stream)
+
+    def backward(self, logits, g, phi, W, x, ab, W1, Wr, stream=None):
+        """The backward of the batch that ``route`` saw last.  g [T, h] the layer
+        output's gradient, phi [N, I] and ab [N, 2I] the saved FC2 input and FC1
+        output of every pair, x [T, h] the layer's input (bf16); W [E, h, I],
+        W1 [E, 2I, h], Wr [E, h] the weights (bf16)."""
+        rec, r = self.rec, self.router
+        rec.run(logits, r.expert_idx, g, phi, r.alpha, W, stream)
+        rec.gate_grad(stream)
+        rec.fc1_backward(x, ab, W1, stream)
+        r.backward(logits, rec.dgate, stream=stream)
+        T = rec.T
+        L.lrm_grouped_wgrad(rec.ctx, r.dlogits, x, self._segment, self._dims_r, T, 0, self.dWr, stream)
+        L.lrm_grouped_dgrad(rec.ctx, r.dlogits, Wr, self._segment, self._dims_r, T, self.dxr, stream)
+        self.clip.clip(self.max_norm, stream)
+
+    def device_status(self, stream=None) -> int:
+        return self.rec.device_status(stream)
+
+    def close(self):
+        self.clip.close()
+        self.router.close()
+        self.rec.close()
+
+
 def to_device_inputs(inp, device="cuda"):
     """Copy a workloads.Inputs record to device tensors (bf16 bits viewed as bf16)."""
     import numpy as np
