@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
     __syncwarp();
     const bool slot = q < k && here;
     const uint32_t mine = sel[q];
-    int e = static_cast<int>(LOW - (mine & LOW));
+    int e = min(static_cast<int>(LOW - (mine & LOW)), E - 1);
     float v = slot ? load_elem(row + e) : 0.f;
     bool unclear = here && !(s > 0.f);
     if constexpr (!is_bf16<TL>) {
@@ -860,7 +860,7 @@ extern "C" lrm_status lrm_router_forward(lrm_ctx* ctx, const void* logits, int32
                                  : dispatch_rf<__nv_bfloat16>(logits, a, L.nblk, s);
     if (st != LRM_OK || L.nblk == 1) return st;
   }
-  const int cluster = dims.E >= 256 ? 8 : dims.E > 64 ? 4 : dims.E > 32 ? 2 : 1;
+  const int cluster = dims.E > 128 ? 8 : dims.E > 64 ? 4 : dims.E > 32 ? 2 : 1;
   return launch_dependent(rf_sums, cluster, RS_SUM_THREADS, 0, cluster, s, a, L.nblk);
 }
 

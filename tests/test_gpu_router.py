@@ -60,8 +60,10 @@ def check_forward(r, ref, z_scale):
     loss, aux, z = r.losses.cpu().numpy().astype(np.float64)
     assert abs(aux - ref["aux"]) <= REL * ref["aux"] + TINY
     z_tol = 2 * REL * (1.0 + z_scale) * (z_scale + REL)
-    assert abs(z - ref["z"]) <= z_tol
-    assert abs(loss - ref["loss"]) <= AUX * REL * ref["aux"] + Z * z_tol + 2.0 ** -23 * abs(ref["loss"])
+    with np.errstate(over="ignore"):  # the oracle's values in the type they are reported in
+        z_ref, loss_ref = float(np.float32(ref["z"])), float(np.float32(ref["loss"]))
+    assert z == z_ref or abs(z - z_ref) <= z_tol
+    assert loss == loss_ref or abs(loss - ref["loss"]) <= AUX * REL * ref["aux"] + Z * z_tol + 2.0 ** -23 * abs(ref["loss"])
 
 
 def backward_tol(l, ref, f, dgate, renorm, bf16_out, want):
@@ -144,6 +146,68 @@ def test_no_token_counts():
 
 def test_large_batch_uses_every_block():
     run(40000, 16, 2, seed=7)
+
+
+# batches above the size from which a token is a lane's work; E off every grid of 4, 8 and 32
+@pytest.mark.parametrize("T,E,k,dtype,masked", [
+    (16384, 8, 2, "f32", False), (16385, 5, 5, "f32", True), (16400, 20, 8, "bf16", False), (16999, 33, 3, "f32", False),
+    (20011, 160, 6, "bf16", True), (16384, 64, 8, "f32", True), (17000, 128, 8, "f32", False),
+    (16390, 255, 7, "f32", False), (16384, 256, 8, "bf16", False), (16384, 256, 1, "f32", False), (16500, 1, 1, "f32", False)])
+def test_large_batches(T, E, k, dtype, masked):
+    valid = np.random.default_rng(T).random(T) < 0.7 if masked else None
+    run(T, E, k, dtype, renorm=bool(E % 2), valid=valid, seed=T)
+
+
+@pytest.mark.parametrize("E,k", [(16, 3), (100, 8), (128, 8)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_batches_with_ties_and_dead_rows(E, k, dtype):
+    rng = np.random.default_rng(E)
+    x = np.round(rng.standard_normal((16500, E)) * 4) / 4
+    x[rng.random(x.shape) < 0.1] = -np.inf
+    x[rng.random(x.shape) < 0.1] = -0.0
+    x[::50] = -np.inf
+    x[7::90, 1:] = float(np.finfo(np.float32).min)
+    run(16500, E, k, dtype, logits=torch.from_numpy(x.astype(np.float32)).to(DT[dtype]), seed=E)
+
+
+def test_logits_that_differ_below_the_keys_resolution():
+    # neighbours in fp32: the last bits decide the order
+    rng = np.random.default_rng(30)
+    for T, E, k in [(700, 128, 8), (16400, 128, 8), (16400, 40, 5), (200, 512, 20)]:
+        base = np.float32(1.5) * np.ones((T, E), np.float32)
+        x = np.nextafter(base, np.float32(2), dtype=np.float32)
+        step = rng.integers(0, 40, (T, E)).astype(np.int32)
+        x = (base.view(np.int32) + step).view(np.float32)
+        run(T, E, k, logits=torch.from_numpy(x), with_gates=False, seed=T)
+
+
+def test_garbage_and_nan_in_large_batches():
+    from backward_token_expert_gb300.pipeline import Router
+
+    T, E, k = 16400, 36, 4
+    x = _logits(T, E, "f32", 31)
+    valid = torch.ones(T, dtype=torch.uint8)
+    valid[::9] = 0
+    outs = []
+    for fill in (0.0, float("nan"), -float("nan"), float("inf")):
+        y = x.clone()
+        y[valid == 0] = fill
+        r = Router(T, E, k, False, AUX, Z)
+        r.forward(y.cuda(), valid.cuda())
+        ids = r.expert_idx.cpu()
+        assert torch.all(ids.sort(1).values.diff(dim=1) > 0) and int(ids.min()) >= 0 and int(ids.max()) < E
+        outs.append([t.clone() for t in (r.alpha, r.row_stats, r.counts, r.f, r.P, r._losses.view(torch.int32))])
+    for o in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(outs[0], o))
+    y = x.clone()
+    y[100, 3], y[16399, 35], y[16398] = float("nan"), float("inf"), -float("nan")
+    r = Router(T, E, k, True, AUX, Z)
+    r.forward(y.cuda())
+    ids, alpha = r.expert_idx.cpu(), r.alpha.view(T, k).cpu()
+    assert 3 not in ids[100].tolist() and ids[16399, 0] == 35 and ids[16398].tolist() == [0, 1, 2, 3]
+    assert torch.isnan(r.losses[0]) and torch.isnan(alpha[16399]).any()
+    good = [t for t in range(T) if t not in (100, 16398, 16399)]
+    assert torch.isfinite(alpha[good]).all()
 
 
 @pytest.mark.parametrize("E,k", [(8, 4), (100, 10), (128, 8)])
