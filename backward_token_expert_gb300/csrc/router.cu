@@ -3,8 +3,8 @@
 // and the auxiliary loss E sum f_e P_e; the z loss is the mean squared
 // log-partition).
 //
-//   rf_rows    G lanes per token, VPL consecutive logits a lane, so a warp
-//              holds 32 / G tokens (E = 128: a warp a token; E = 8: eight).
+//   rf_rows    G lanes per token, 4 C logits a lane, so a warp holds 32 / G
+//              tokens (E = 128: four; E = 8: eight).
 //              The logits are read once, a token ahead.  From the same
 //              registers come the maximum, the softmax (summed per lane for
 //              P) and the k largest.  Every block leaves its sums of p, its
@@ -19,7 +19,7 @@
 //              touches k experts, which are placed through shared memory.
 //
 // The k largest: a lane sorts its logits as 32-bit keys whose top bits order
-// like the value and whose low log2(G VPL) bits hold the expert, inverted, so
+// like the value and whose low bits hold the expert, inverted, so
 // that keys are unique and equal values go to the lower expert.  A round is
 // one warp-wide integer maximum; the lane that owns it moves up its list.  For
 // bf16 logits the cut-off bits are zero and the order is exact.  For fp32, two
@@ -45,8 +45,9 @@ constexpr float LN2 = 0.6931471805599453f;
 // Lanes per token (G) and groups of four logits per lane (C): the fewest lanes
 // that have a slot each and at most 16 logits (32 for the widest layers), so
 // that what a token costs once (reductions, slots, addresses) is shared by the
-// tokens of a warp.  A warp a token took 346 instructions at E = 128 (46 us for
-// 131072 tokens), four tokens a warp take RF_MEASURED.
+// tokens of a warp.  At E = 128 a warp a token took 346 instructions a token in
+// the forward (45 us for 131072 tokens) and 31.3 us in the backward; four tokens a
+// warp take 175, 37 us and 27 us.
 template <int N>
 using Int = std::integral_constant<int, N>;
 
@@ -117,16 +118,18 @@ __device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bf
 __device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Four consecutive logits as they lie in memory; places beyond the row hold
-// -inf.  vec: rows start at a multiple of four elements' bytes.
+// Four consecutive logits as they lie in memory.  load() leaves the places
+// beyond the row as they are: -inf, from clear().  vec: rows start at a multiple
+// of four elements' bytes.
 template <typename TL>
 struct Four {
   uint32_t w[sizeof(TL)];
 
-  __device__ __forceinline__ void load(const TL* __restrict__ row, int e0, int E, bool vec) {
-    constexpr uint32_t none = is_bf16<TL> ? 0xFF80FF80u : 0xFF800000u;
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(TL)); ++i) w[i] = none;
+    for (int i = 0; i < static_cast<int>(sizeof(TL)); ++i) w[i] = is_bf16<TL> ? 0xFF80FF80u : 0xFF800000u;
+  }
+  __device__ __forceinline__ void load(const TL* __restrict__ row, int e0, int E, bool vec) {
     if (vec) {
       if (e0 >= E) return;
       if constexpr (is_bf16<TL>) {
@@ -159,22 +162,21 @@ struct Four {
 // the lanes of a token read consecutive 16-byte pieces.
 template <typename TL, int G, int C>
 struct Pieces {
-  uint32_t w[C * sizeof(TL)];
+  Four<TL> f[C];
 
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int c = 0; c < C; ++c) f[c].clear();
+  }
   __device__ __forceinline__ void load(const TL* __restrict__ row, int q, int E, bool vec) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      Four<TL> r;
-      r.load(row, 4 * (q + G * c), E, vec);
-#pragma unroll
-      for (int i = 0; i < static_cast<int>(sizeof(TL)); ++i) w[c * sizeof(TL) + i] = r.w[i];
-    }
+    for (int c = 0; c < C; ++c) f[c].load(row, 4 * (q + G * c), E, vec);
   }
   __device__ __forceinline__ float get(int c, int i) const {
     if constexpr (is_bf16<TL>)
-      return (i & 1) ? bf16_hi(w[2 * c + i / 2]) : bf16_lo(w[2 * c + i / 2]);
+      return (i & 1) ? bf16_hi(f[c].w[i / 2]) : bf16_lo(f[c].w[i / 2]);
     else
-      return __uint_as_float(w[4 * c + i]);
+      return __uint_as_float(f[c].w[i]);
   }
 };
 
@@ -325,6 +327,7 @@ template <typename TL, int G, int C>
 __device__ __noinline__ int select_exact(const TL* row, int E, int k, bool vec) {
   const int lane = threadIdx.x & 31, q = lane % G;
   Pieces<TL, G, C> raw;
+  raw.clear();
   raw.load(row, q, E, vec);
   uint32_t key[C][4];
 #pragma unroll
@@ -499,14 +502,18 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
   int held = 0, tokens = 0;
   const long long step = static_cast<long long>(gridDim.x) * NW * PER_WARP;
   long long t = (static_cast<long long>(blockIdx.x) * NW + warp) * PER_WARP + lane / G;
-  const TL* row = logits + static_cast<size_t>(t) * E;
+  // a group without a token of its own (here false) reads a row that another has
+  const TL* next_row = logits + static_cast<size_t>(t < T ? t : 0) * E;
   const size_t row_step = static_cast<size_t>(step) * E;
   Pieces<TL, G, C> next;
-  next.load(row, q, t < T ? E : 0, vec);
-  for (; t - lane / G < T; t += step, row += row_step) {
+  next.clear();
+  if (T > 0) next.load(next_row, q, E, vec);
+  for (; t - lane / G < T; t += step) {
     const bool here = G == 32 || t < T;
+    const TL* row = next_row;
     const Pieces<TL, G, C> raw = next;
-    next.load(row + row_step, q, t + step < T ? E : 0, vec);
+    if (t + step < T) next_row += row_step;
+    next.load(next_row, q, E, vec);
     bool ok = here;
     if (a.valid != nullptr && here) ok = a.valid[t] != 0;
 
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
       unclear = unclear || (slot && (q == k - 1 ? (mine ^ after) <= LOW : v < vn));
     }
     if (__any_sync(0xffffffffu, unclear)) {
-      e = select_exact<TL, G, C>(row, here ? E : 0, k, vec);
+      e = select_exact<TL, G, C>(row, E, k, vec);
       if (slot) v = load_elem(row + e);
     }
     __syncwarp();  // sel is read before the next token writes it
@@ -681,25 +688,29 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
   const bool gates = a.dgate != nullptr;
   const long long step = static_cast<long long>(gridDim.x) * NW * PER_WARP;
   long long t = (static_cast<long long>(blockIdx.x) * NW + warp) * PER_WARP + lane / G;
-  const auto load = [&](long long at) {
-    TokenIn<TL, G, C> x;
+  const bool slot = gates && q < k;
+  // a group without a token of its own reads the first one's and stores nothing
+  const auto load = [&](TokenIn<TL, G, C>& x, long long at) {
     const bool in = at < T;
-    x.raw.load(logits + static_cast<size_t>(at) * E, q, in ? E : 0, vec_in);
-    x.ms = in ? __ldg(a.row_stats + at) : make_float2(0.f, 0.f);
-    x.id = 0;
-    x.dg = x.al = 0.f;
-    if (gates && in && q < k) {
-      const size_t u = static_cast<size_t>(at) * k + q;
+    const long long from = in ? at : 0;
+    x.raw.load(logits + static_cast<size_t>(from) * E, q, E, vec_in);
+    x.ms = __ldg(a.row_stats + from);
+    if (slot) {
+      const size_t u = static_cast<size_t>(from) * k + q;
       x.id = __ldg(a.expert_idx + u);
       x.dg = __ldg(a.dgate + u);
       x.al = __ldg(a.alpha + u);
     }
-    return x;
   };
-  TokenIn<TL, G, C> next = load(t);
+  TokenIn<TL, G, C> next;
+  next.raw.clear();
+  next.ms = make_float2(0.f, 0.f);
+  next.id = -1;
+  next.dg = next.al = 0.f;
+  load(next, t);
   for (; t - lane / G < T; t += step) {
     const TokenIn<TL, G, C> x = next;
-    next = load(t + step);
+    load(next, t + step);
     const bool counted = x.ms.y != 0.f;
     const bool rare = __any_sync(0xffffffffu, !counted);  // a token of the warp that gets zeros, or none
     const float inv = rcp(x.ms.y);
@@ -708,7 +719,7 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[c][i] = exp_neg(x.raw.get(c, i) - x.ms.x) * inv;
-    int e = gates && q < k ? x.id : -1;
+    int e = x.id;  // -1 in lanes without a slot
     if (rare && !counted) {
       e = -1;
       dg = 0.f;
@@ -726,7 +737,7 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
       const bool in = static_cast<unsigned>(e) < static_cast<unsigned>(E);
       if (in) slot_of[e] = static_cast<uint8_t>(q);
       __syncwarp();
-      const bool lost = in && slot_of[e] != q, bad = !in && q < k && counted;
+      const bool lost = in && slot_of[e] != q, bad = !in && slot && counted;
       if (__any_sync(0xffffffffu, bad || lost)) {  // an id out of range, or one named by several slots
         const unsigned peers = __match_any_sync(0xffffffffu, in ? ((lane - q) << 16) | e : -1 - lane);
         if (bad || (in && (peers & ((1u << lane) - 1u)) != 0)) {

@@ -70,6 +70,22 @@ def test_rows(ctx, N, E, I, rows, spare):
     _check(out, x, y, host_ids, N, I)
 
 
+def test_offsets_beyond_32_bits(ctx):
+    from backward_token_expert_gb300 import lrm as L
+
+    I = 2048
+    rows = (1 << 31) // I + 777
+    x = torch.zeros(rows, I, dtype=torch.bfloat16, device="cuda")
+    y = torch.ones(rows, I, dtype=torch.bfloat16, device="cuda")
+    x[-3:, 5] = torch.tensor([1.0, 2.0, 3.0], dtype=torch.bfloat16, device="cuda")
+    ids = torch.arange(rows, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    out = torch.empty(rows, device="cuda")
+    L.lrm_gate_grad(ctx, x, y, off, ids, L.dims_of(rows, 1, 1, 8, I), rows, out)
+    torch.cuda.synchronize()
+    assert out[-3:].tolist() == [1.0, 2.0, 3.0] and not out[:-3].any()
+
+
 def test_total_beyond_max_rows_and_bad_ids(ctx):
     from backward_token_expert_gb300 import lrm as L
 

@@ -248,6 +248,20 @@ def test_refusals():
     assert ei.value.code == inv
 
 
+def test_more_elements_than_32_bits():
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    n = (1 << 31) + 4099
+    x = torch.full((n,), 0.25, dtype=torch.bfloat16, device="cuda")
+    x[-1] = 64.0
+    c = GradClip([x])
+    norm = math.sqrt((n - 1) * 0.0625 + 4096.0)
+    c.clip(norm / 2)
+    assert abs(float(c.norm.item()) - norm) <= REL * norm
+    assert x[0] == 0.125 and x[-2] == 0.125 and x[-1] == 32.0
+    assert int((x == 0.125).sum()) == n - 1
+
+
 def test_large_tensor():
     n = (1 << 27) + 12345
     x = torch.full((n,), 0.5, device="cuda")

@@ -460,6 +460,34 @@ def test_refusals():
         Router(4, 4, 2, dtype=torch.float16)
 
 
+def test_offsets_beyond_32_bits():
+    # 2^31 + logits: the last tokens equal those of a batch that holds nothing else
+    from backward_token_expert_gb300.pipeline import Router
+
+    E, k = 256, 4
+    T = (1 << 31) // E + 20003
+    x = torch.randint(0, 1 << 16, (1 << 20,), dtype=torch.int32, device="cuda").to(torch.float32).sub_(32768.0)
+    x = (x / 8192.0).to(torch.bfloat16)
+    big = torch.empty(T, E, dtype=torch.bfloat16, device="cuda")
+    big.view(-1)[: T * E // x.numel() * x.numel()].view(-1, x.numel()).copy_(x)
+    big.view(-1)[T * E // x.numel() * x.numel():].copy_(x[: T * E % x.numel()])
+    n = 5000
+    tail = torch.randn(n, E, device="cuda").to(torch.bfloat16)
+    big[-n:] = tail
+    r, s = Router(T, E, k, True, 0.0, 0.0, dtype=torch.bfloat16), Router(n, E, k, True, 0.0, 0.0, dtype=torch.bfloat16)
+    r.forward(big)
+    s.forward(tail)
+    dg = torch.zeros(T * k, device="cuda")
+    dg[-n * k:] = torch.randn(n * k, device="cuda")
+    r.backward(big, dg)
+    s.backward(tail, dg[-n * k:].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(r.expert_idx[-n:], s.expert_idx) and torch.equal(r.alpha[-n * k:], s.alpha)
+    assert torch.equal(r.row_stats[-n:], s.row_stats) and torch.equal(r.dlogits[-n:], s.dlogits)
+    assert int(r.counts.sum()) == T * k and int(r.tokens) == T
+    assert not r.dlogits[: T - n].any()
+
+
 def test_no_tokens():
     from backward_token_expert_gb300.pipeline import Router
 
