@@ -20,12 +20,16 @@
 //
 // The k largest: a lane sorts its logits as 32-bit keys whose top bits order
 // like the value and whose low bits hold the expert, inverted, so
-// that keys are unique and equal values go to the lower expert.  A round is
-// one warp-wide integer maximum; the lane that owns it moves up its list.  For
-// bf16 logits the cut-off bits are zero and the order is exact.  For fp32, two
-// neighbours in the result (or the last one and the next) that agree in all
-// the bits kept send the warp to an exact selection on full keys, as do NaN
-// and rows of -inf.
+// that keys are unique and equal values go to the lower expert.  Few slots are
+// found by rounds of a group-wide maximum, the lane that owns it moving up its
+// list; more by merging the lanes' lists of eight pairwise.  For bf16 logits the
+// cut-off bits are zero and the order is exact.  For fp32 the keys are made of
+// l - m, and the order is checked against the logits: slots out of order, a
+// logit left out whose key agrees with the last slot's in all the bits kept, NaN
+// and rows of -inf send the warp to an exact selection on full keys.
+//
+// Bound by instruction issue: 131072 x 128 fp32 logits take 34 us of which
+// the 77 MB to move need 11.
 #include <math.h>
 
 #include <type_traits>
@@ -37,6 +41,10 @@ namespace lrm {
 namespace {
 
 constexpr int RF_ONE_BLOCK_PASSES = 2;  // batches of up to this many passes of one block use one block
+// Up to this k the slots are found by rounds of a maximum, above it by merging
+// the lanes' lists (131072 x 128, rounds against merges: k = 2 28.7 / 32.5 us,
+// k = 4 31.2 / 33.2, k = 8 37.4 / 34.3).
+constexpr int RF_ROUNDS = 4;
 constexpr int RS_SUM_THREADS = 1024;
 constexpr int RB_THREADS = 256;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -47,7 +55,7 @@ constexpr float LN2 = 0.6931471805599453f;
 // that what a token costs once (reductions, slots, addresses) is shared by the
 // tokens of a warp.  At E = 128 a warp a token took 346 instructions a token in
 // the forward (45 us for 131072 tokens) and 31.3 us in the backward; four tokens a
-// warp take 175, 37 us and 27 us.
+// warp take 175 (37 us; 34 with merged lists) and 27 us.
 template <int N>
 using Int = std::integral_constant<int, N>;
 
@@ -82,8 +90,12 @@ lrm_status with_split(int E, int k, Run run) {
   return pick(Int<32>{}, Int<8>{});
 }
 
-// Threads of a block of rf_rows: as many as the registers of C groups allow.
-__host__ __device__ constexpr int rf_threads(int C) { return C == 1 ? 1024 : C <= 4 ? 512 : 256; }
+// Threads of a block of rf_rows, one block an SM: as many as the registers of C
+// groups allow without spilling (640 threads of 96 registers at C = 4 gain 1 %
+// at 131072 x 128 and lose 10 % at 16384 x 128; blocks sized to the batch, so
+// that a small one has a warp on every SM, lose 4 % at 8192 x 128: rf_sums then
+// adds more rows).
+__host__ __device__ constexpr int rf_threads(int C) { return C == 1 ? 768 : C <= 4 ? 512 : 256; }
 
 struct RouterLayout {
   int nblk;  // blocks of rf_rows
@@ -483,7 +495,7 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
   extern __shared__ float rt_smem[];
   float* sp = rt_smem;                                     // [NW][E]
   int* hist = reinterpret_cast<int*>(rt_smem + NW * a.E);  // [E]
-  __shared__ uint32_t s_sel[NW][32];                       // the slots' keys
+  __shared__ __align__(16) uint32_t s_sel[NW][32];                     // the slots' keys
   __shared__ float s_z[NW];
   __shared__ int s_tok[NW];
   __shared__ float s_fp[NW];
@@ -536,19 +548,49 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
     const bool counted = ok && s != 0.f;
 
     sort_top<NK, LIST>(key);
-    constexpr int L = LIST;
-#pragma unroll 4
-    for (int j = 0; j < k; ++j) {
-      const uint32_t top = group_max<G>(key[0]);
-      const bool hit = key[0] == top;
-      if (hit) sel[j] = top;
+    bool crowded = false;  // fp32: a key left out may stand for a larger logit than the last one kept
+    if (LIST == 8 && G <= 16 && k > RF_ROUNDS) {
+      // the lanes' lists merged pairwise: every lane ends with the token's eight largest
+      uint32_t own[LIST];
 #pragma unroll
-      for (int i = 0; i + 1 < L; ++i) key[i] = hit ? key[i + 1] : key[i];
-      key[L - 1] = hit ? 0u : key[L - 1];
+      for (int i = 0; i < LIST; ++i) own[i] = key[i];
+      if constexpr (LIST == 8 && G <= 16) {  // (the condition above, for the compiler)
+#pragma unroll
+        for (int o = 1; o < G; o <<= 1) {
+          uint32_t other[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(0xffffffffu, key[i], o);
+          merge_top8(key, other);
+        }
+        if (q == 0) {
+          *reinterpret_cast<uint4*>(sel) = make_uint4(key[0], key[1], key[2], key[3]);
+          *reinterpret_cast<uint4*>(sel + 4) = make_uint4(key[4], key[5], key[6], key[7]);
+        }
+      }
+      __syncwarp();
+      if constexpr (!is_bf16<TL>) {
+        const uint32_t last = sel[k - 1] & ~LOW;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < LIST; ++i) n += own[i] >= last;
+        crowded = NK > LIST && n == LIST;
+#pragma unroll
+        for (int o = 1; o < G; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        crowded = crowded || n != k;
+      }
+    } else {
+#pragma unroll 4
+      for (int j = 0; j < k; ++j) {
+        const uint32_t top = group_max<G>(key[0]);
+        const bool hit = key[0] == top;
+        if (hit) sel[j] = top;
+#pragma unroll
+        for (int i = 0; i + 1 < LIST; ++i) key[i] = hit ? key[i + 1] : key[i];
+        key[LIST - 1] = hit ? 0u : key[LIST - 1];
+      }
+      __syncwarp();
+      if constexpr (!is_bf16<TL>) crowded = (sel[k - 1] ^ group_max<G>(key[0])) <= LOW;
     }
-    uint32_t after = 0;  // the largest key left out
-    if constexpr (!is_bf16<TL>) after = group_max<G>(key[0]);
-    __syncwarp();
     const bool slot = q < k && here;
     const uint32_t mine = sel[q];
     int e = min(static_cast<int>(LOW - (mine & LOW)), E - 1);
@@ -556,7 +598,7 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
     bool unclear = here && !(s > 0.f);
     if constexpr (!is_bf16<TL>) {
       const float vn = __shfl_down_sync(0xffffffffu, v, 1, G);
-      unclear = unclear || (slot && (q == k - 1 ? (mine ^ after) <= LOW : v < vn));
+      unclear = unclear || (here && crowded) || (q < k - 1 && here && v < vn);
     }
     if (__any_sync(0xffffffffu, unclear)) {
       e = select_exact<TL, G, C>(row, E, k, vec);

@@ -396,7 +396,10 @@ def lrm_gate_grad(ctx, dphi_c, phi_c, sel_offsets, sel_ids, dims: Dims, max_rows
 
 def tensor_array(entries):
     """A C array of lrm_tensor from (src, dst, n, dtype) entries."""
-    return (Tensor * max(1, len(entries)))(*[Tensor(_ptr(s), _ptr(d), int(n), int(dt)) for s, d, n, dt in entries])
+    array = (Tensor * max(1, len(entries)))()
+    for t, (src, dst, n, dtype) in zip(array, entries):
+        t.src, t.dst, t.n, t.dtype = _ptr(src), _ptr(dst), n, dtype
+    return array
 
 
 def lrm_grad_table_size(tensors, count: int) -> int:

@@ -397,6 +397,17 @@ def _dense(t) -> bool:
     return True
 
 
+_clip_contexts: dict[int, int] = {}
+
+
+def _clip_context(device: int) -> int:
+    """The context of a device's clips that were given none (they raise no
+    device status, so they can share one)."""
+    if device not in _clip_contexts:
+        _clip_contexts[device] = L.lrm_create(device)
+    return _clip_contexts[device]
+
+
 class GradClip:
     """Global gradient norm and clipping over a fixed list of tensors
     (lrm_grad_norm, lrm_grad_clip).  `outs` receive the clipped values (the
@@ -414,28 +425,35 @@ class GradClip:
         if not grads:
             raise ValueError("no gradients")
         self.device = grads[0].device
-        spans = []
+        if self.device.type != "cuda":
+            raise ValueError("gradients are float32 or bfloat16 CUDA tensors")
+        spans, entries = [], []
         for g, o in zip(grads, outs):
-            if g.dtype not in _DTYPES or g.device.type != "cuda":
+            dtype = _DTYPES.get(g.dtype)
+            if dtype is None:
                 raise ValueError("gradients are float32 or bfloat16 CUDA tensors")
-            if g.device != self.device or o.device != self.device:
+            if g.device != self.device or (o is not g and o.device != self.device):
                 raise ValueError("all tensors must be on one device")
-            if o.dtype != g.dtype or o.shape != g.shape or (g.numel() and o.stride() != g.stride()):
-                raise ValueError("an output needs its gradient's type, shape and strides")
-            if g.numel() and not _dense(g):
-                raise ValueError("gradients and outputs must be dense in memory")
-            size = g.numel() * g.element_size()
-            if size:
-                spans.append((g.data_ptr(), size))
-                if o.data_ptr() != g.data_ptr():
-                    spans.append((o.data_ptr(), size))
+            n, src = g.numel(), g.data_ptr()
+            dst = src
+            if o is not g:
+                if o.dtype != g.dtype or o.shape != g.shape or (n and o.stride() != g.stride()):
+                    raise ValueError("an output needs its gradient's type, shape and strides")
+                dst = o.data_ptr()
+            if n:
+                if not g.is_contiguous() and not _dense(g):
+                    raise ValueError("gradients and outputs must be dense in memory")
+                size = n * g.element_size()
+                spans.append((src, size))
+                if dst != src:
+                    spans.append((dst, size))
+            entries.append((src, dst, n, dtype))
         spans.sort()
         if any(a + n > b for (a, n), (b, _) in zip(spans, spans[1:])):
             raise ValueError("gradients and outputs must not overlap")
         self.grads, self.outs = grads, outs  # kept alive: the list holds their addresses
-        self._own_ctx = ctx is None
-        self.ctx = L.lrm_create(self.device.index or 0) if ctx is None else ctx
-        tensors = L.tensor_array([(g, o, g.numel(), _DTYPES[g.dtype]) for g, o in zip(grads, outs)])
+        self.ctx = _clip_context(self.device.index or 0) if ctx is None else ctx
+        tensors = L.tensor_array(entries)
         need = L.lrm_grad_table_size(tensors, len(grads))
         self.table = torch.empty(need, dtype=torch.uint8, device=self.device)
         self.list = L.lrm_grad_list_create(self.ctx, tensors, len(grads), self.table, need, stream)
@@ -447,8 +465,6 @@ class GradClip:
         if getattr(self, "list", None):
             L.lrm_grad_list_destroy(self.list)
             self.list = None
-        if getattr(self, "_own_ctx", False) and getattr(self, "ctx", None):
-            L.lrm_destroy(self.ctx)
         self.ctx = None
 
     def __del__(self):  # pragma: no cover - best effort
