@@ -464,8 +464,8 @@ LRM_API lrm_status lrm_router_backward(lrm_ctx* ctx, const void* logits, int32_t
  *
  * lrm_grad_list_create writes the list's device table (device memory of
  * lrm_grad_table_size bytes, 256-byte aligned, owned by the caller and used by
- * the list alone until lrm_grad_list_destroy) on `stream` and returns a host
- * handle.  The tensors' addresses are kept, their values are not: a list is
+ * the list alone until lrm_grad_list_destroy) on `stream`, waits for it, and
+ * returns a host handle.  The tensors' addresses are kept, their values are not: a list is
  * made once for gradients that stay where they are.  It cannot be created
  * while `stream` is capturing; the calls on it can be captured.
  *   lrm_tensor: n >= 0 elements of `dtype` at src, aligned to their size; the

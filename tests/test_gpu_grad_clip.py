@@ -248,6 +248,43 @@ def test_refusals():
     assert ei.value.code == inv
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_lists_beyond_the_l2(dtype):
+    # above 128 MB: whole runs, short ones, tensors off the 16-byte grid (src, dst, both), single elements
+    n = 40_000_000 if dtype == torch.float32 else 80_000_000
+    g = torch.Generator(device="cuda").manual_seed(20)
+    src = (torch.randn(n, generator=g, device="cuda") * 0.01).to(dtype)
+    dst = torch.full_like(src, 3.0)
+    cuts = [(0, 1), (8, 8191), (8208, 8192), (16400 + 3, 50001), (70000, 7), (70016, 4096 * 5 + 1), (100003, 12_000_000),
+            (12_200_000, n - 12_200_000 - 5)]
+    grads = [src[a:a + m] for a, m in cuts]
+    outs = [dst[a + (1 if i == 2 else 0):a + (1 if i == 2 else 0) + m] for i, (a, m) in enumerate(cuts)]
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    norm = math.sqrt(sum(float(t.double().square().sum()) for t in grads))
+    kept = src.clone()
+    for limit in (0.3 * norm, 2.0 * norm):
+        c = GradClip(grads, outs)
+        c.clip(limit)
+        assert abs(float(c.norm) - norm) <= REL * norm
+        assert abs(float(c.coef) - min(1.0, limit / norm)) <= 1.2 * REL
+        for a, b in zip(grads, outs):
+            assert torch.equal(b, _expect(a, c.coef))
+    assert torch.equal(src, kept)
+    written = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for i, (a, m) in enumerate(cuts):
+        written[a + (1 if i == 2 else 0):a + (1 if i == 2 else 0) + m] = True
+    assert bool((dst[~written] == 3.0).all())
+    c = GradClip(grads)
+    c.clip(2.0 * norm)  # in place, nothing to do
+    assert torch.equal(src, kept)
+    c.clip(0.3 * norm)
+    inside = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for a, m in cuts:
+        inside[a:a + m] = True
+    assert torch.equal(src, torch.where(inside, _expect(kept, c.coef), kept))
+
+
 def test_more_elements_than_32_bits():
     from backward_token_expert_gb300.pipeline import GradClip
 
