@@ -356,7 +356,7 @@ __device__ lrm_grad_stats block_stats(const double* __restrict__ partial, int nb
   __shared__ lrm_grad_stats s_stats;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   double a = 0.0;
-  for (int i = threadIdx.x; i < nblk; i += blockDim.x) a += partial[i];
+  for (int i = threadIdx.x; i < nblk; i += blockDim.x) a += __ldcg(partial + i);  // written by the kernel before: not through L1
   if (warp * 32 < nblk) a = warp_sum(a);
   if (lane == 0) s_part[warp] = a;
   __syncthreads();

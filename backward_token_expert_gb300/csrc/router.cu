@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(RS_SUM_THREADS) rf_sums(ForwardArgs a, int nbl
   grid_dependency_wait();
   float z = 0.f, fp = 0.f;
   int tokens = 0;
-  for (int b = lane; b < nblk; b += 32) z += a.ws_z[b], tokens += a.ws_tok[b];
+  for (int b = lane; b < nblk; b += 32) z += __ldcg(a.ws_z + b), tokens += __ldcg(a.ws_tok + b);
   for (int c0 = e0; c0 < e1; c0 += 32) {
     const int e = c0 + lane;
     float p = 0.f;
@@ -455,8 +455,8 @@ __global__ void __launch_bounds__(RS_SUM_THREADS) rf_sums(ForwardArgs a, int nbl
       for (int j = 0; j < BATCH; ++j) {
         const int b = b0 + j * NW;
         const bool in = b < nblk && e < e1;
-        pv[j] = in ? a.ws_p[static_cast<size_t>(b) * a.E + e] : 0.f;
-        cv[j] = in ? a.ws_cnt[static_cast<size_t>(b) * a.E + e] : 0;
+        pv[j] = in ? __ldcg(a.ws_p + static_cast<size_t>(b) * a.E + e) : 0.f;
+        cv[j] = in ? __ldcg(a.ws_cnt + static_cast<size_t>(b) * a.E + e) : 0;
       }
 #pragma unroll
       for (int j = 0; j < BATCH; ++j) p += pv[j], c += cv[j];
@@ -533,7 +533,8 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
 #pragma unroll
     for (int i = 1; i < N; ++i) m = fmaxf(m, raw.get(i / 4, i % 4));
     m = group_fmax<G>(m);
-    const float base = m == -INFINITY ? 0.f : m;
+    // -0 takes both zeros to d = +0, so that they tie
+    const float base = m == -INFINITY ? 0.f : m == 0.f ? -0.f : m;
     uint32_t key[NK] = {};
     float p[N], s = 0.f;
 #pragma unroll
@@ -589,7 +590,9 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
         key[LIST - 1] = hit ? 0u : key[LIST - 1];
       }
       __syncwarp();
-      if constexpr (!is_bf16<TL>) crowded = (sel[k - 1] ^ group_max<G>(key[0])) <= LOW;
+      // a lane whose list ran out may hold more
+      if constexpr (!is_bf16<TL>)
+        crowded = (sel[k - 1] ^ group_max<G>(key[0])) <= LOW || (NK > LIST && key[0] == 0u);
     }
     const bool slot = q < k && here;
     const uint32_t mine = sel[q];
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
       a.alpha[u] = counted ? pj * rcp(den) : 0.f;
       if (counted) atomicAdd(&hist[e], 1);
     }
-    if (q == 0 && here) a.row_stats[t] = counted ? make_float2(base, s) : make_float2(0.f, 0.f);
+    if (q == 0 && here) a.row_stats[t] = counted ? make_float2(base + 0.f, s) : make_float2(0.f, 0.f);
     if (counted) {
       const float inv = rcp(s);
 #pragma unroll

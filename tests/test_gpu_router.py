@@ -181,6 +181,52 @@ def test_logits_that_differ_below_the_keys_resolution():
         run(T, E, k, logits=torch.from_numpy(x), with_gates=False, seed=T)
 
 
+@pytest.mark.parametrize("E", [20, 64, 128, 160, 256, 512, 1000])
+@pytest.mark.parametrize("stride", [4, 8, 16, 32])
+def test_close_logits_side_by_side(E, stride):
+    # more logits than slots within a few units in the last place, in experts that lie `stride` groups of four apart
+    rng = np.random.default_rng(E + stride)
+    T, k = 64, 8
+    near = np.flatnonzero((np.arange(E) // 4) % stride == 0)
+    x = (rng.standard_normal((T, E)) - 6.0).astype(np.float32)
+    close = (np.float32(1.5).view(np.int32) + rng.integers(0, 30, (T, near.size))).astype(np.int32).view(np.float32)
+    x[:, near] = close
+    run(T, E, k, logits=torch.from_numpy(x), seed=E)
+    # a far larger logit beside them: their differences to it round together
+    y = x.copy()
+    y[:, near[-1]] = 40.0
+    run(T, E, k, logits=torch.from_numpy(y), seed=E)
+    z = x.copy()
+    z[:, int(np.setdiff1d(np.arange(E), near)[0]) if near.size < E else 0] = 40.0
+    run(T, E, k, logits=torch.from_numpy(z), seed=E)
+    run(T, E, k + 1 if E < 300 else 9, logits=torch.from_numpy(z), seed=E)
+
+
+@pytest.mark.parametrize("E,stride", [(128, 8), (256, 16), (512, 32), (1000, 32)])
+@pytest.mark.parametrize("k", [2, 4, 5, 8])
+def test_last_slot_against_its_neighbour(E, stride, k):
+    # k + 1 candidates `stride` groups of four apart; the largest that stays out of k and the last that
+    # comes in differ by one unit in the last place, the larger one in the higher expert
+    near = np.flatnonzero((np.arange(E) // 4) % stride == 0)
+    assert near.size >= k + 1
+    x = np.full((40, E), -90.0, np.float32)
+    x[:, near[:k - 1]] = 40.0 - np.arange(k - 1, dtype=np.float32)
+    x[:, near[k - 1]] = 1.5
+    x[:, near[k]] = np.nextafter(np.float32(1.5), np.float32(2))
+    r, _, _ = run(40, E, k, logits=torch.from_numpy(x), seed=k)
+    assert int(r.expert_idx[0, -1]) == near[k]
+
+
+@pytest.mark.parametrize("E,k", [(3, 2), (16, 4), (64, 8), (128, 3), (128, 8), (300, 8), (512, 20)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_both_zeros_as_the_largest_logits(E, k, dtype):
+    rng = np.random.default_rng(E)
+    x = rng.choice([0.0, -0.0, -1.0, -1e-30, -np.inf], size=(200, E))
+    x[:, rng.integers(0, E)] = -0.0
+    x[::3][x[::3] == 0] = -0.0
+    run(200, E, k, dtype, logits=torch.from_numpy(x.astype(np.float32)).to(DT[dtype]), seed=E)
+
+
 def test_garbage_and_nan_in_large_batches():
     from backward_token_expert_gb300.pipeline import Router
 
