@@ -28,8 +28,10 @@
 // logit left out whose key agrees with the last slot's in all the bits kept, NaN
 // and rows of -inf send the warp to an exact selection on full keys.
 //
-// Bound by instruction issue: 131072 x 128 fp32 logits take 34 us of which
-// the 77 MB to move need 11.
+// The forward is bound by instruction issue: 131072 x 128 fp32 logits take 34 us,
+// of which the 77 MB to move need 11; 32768 x 128 take 16 us, half of it launch,
+// first load and rf_sums.  The backward is bound by memory: 131072 x 128 fp32 in
+// 27 us, 5.5 TB/s.
 #include <math.h>
 
 #include <type_traits>
