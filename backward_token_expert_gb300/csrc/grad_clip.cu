@@ -5,9 +5,11 @@
 // any size give the warps equal shares and a warp finds its work with one
 // 32-byte load.
 //
-//   gc_small   lists of up to 256 chunks: one cluster, a chunk a warp, held in
-//              registers between the norm and the scaling, so it is read once
-//              and there is one launch.
+//   gc_small   up to 64 KB: one block, a chunk a warp, held in registers between
+//              the norm and the scaling (60 KB 5.7 us against 6.1 by gc_hold, 2 KB
+//              4.0 against 5.5; 120 KB 7.0 against 6.3).
+//   gc_hold    up to 24 MB: one launch, the chunks held in shared memory over a
+//              barrier of the grid.
 //   gc_norm    one warp per chunk; each block leaves its sum of squares (fp64).
 //   gc_stats   adds the blocks' sums (the norm alone).
 //   gc_clip    launched dependently; every block adds the same sums in the
@@ -16,10 +18,10 @@
 //   gc_ring    the same for lists beyond the L2, through shared memory.
 //
 // Bound by memory: the norm has to be known before the first value is scaled, so
-// what the L2 does not hold is read twice.  2.4 GB of fp32: 1038 us, the norm at
-// 6.8 TB/s and the scaling at 7.0 (4.8 GB moved, some of it from L2); 59 MB of
-// bf16 in 400 tensors 31 us; 160 KB in six tensors 5.7 us, most of it launch and
-// latency.
+// what neither the SMs nor the L2 hold is read twice.  2.4 GB of fp32: 1040 us,
+// the norm at 6.8 TB/s and the scaling at 7.0 (4.8 GB moved, some of it from L2);
+// 59 MB of bf16 in 400 tensors 31 us; 160 KB in six tensors 5.7 us, most of it
+// launch and latency.
 //
 // Squares: a lane's batch of values (32 fp32 or 64 bf16) is squared and summed
 // in fp32 while its largest magnitude lies in [2^-56, 2^55]: no sum of squares
@@ -28,17 +30,17 @@
 // (exact); batches of zeros add nothing.  Batches are added in fp64.
 #include <math.h>
 #include <stdlib.h>
+#include <string.h>
 
 #include "lrm_internal.cuh"
 #include "vec.cuh"
 
 struct lrm_grad_list {
   int device;
-  int small;  // ranks of gc_small's cluster, 0: gc_norm and a scaling kernel
-  int ring;   // that kernel is gc_ring, else gc_clip
+  int by;  // which kernels (Plan)
   long long chunks;
   int in_place, has_dst;  // every dst is its src; every non-empty tensor has a dst
-  int grid_norm, grid_clip;
+  int grid_norm, grid_clip;  // of gc_norm; of gc_hold, gc_clip or gc_ring
   void* table;
 };
 
@@ -54,10 +56,13 @@ constexpr int64_t GC_LARGE_BYTES = int64_t{128} << 20;         // about the L2's
 constexpr int GC_RING_WARPS = 4, GC_RING_THREADS = 32 * GC_RING_WARPS, GC_STAGES = 3;
 constexpr int GC_RING_BYTES = 4 * GC_BATCH_BYTES;               // a stage, and the chunks of such lists
 constexpr int GC_RING_SMEM = GC_RING_WARPS * GC_STAGES * GC_RING_BYTES;
+constexpr int GC_HELD = 3;                                     // chunks a warp of gc_hold keeps in shared memory
+constexpr int GC_HOLD_SMEM = GC_WARPS * GC_HELD * GC_BATCH_BYTES;
+constexpr int GC_SMS = 152;                                    // the shares of the warps are cut for this many SMs
+constexpr int64_t GC_HOLD_BYTES = int64_t{24} << 20;           // of 29 MB that GC_SMS blocks hold: chunks are not all full
 constexpr int GC_SMALL_THREADS = 1024;
-constexpr int GC_SMALL_WARPS = GC_SMALL_THREADS / 32;
-constexpr int GC_SMALL_CLUSTER = 8;
-constexpr int GC_SMALL_CHUNKS = GC_SMALL_WARPS * GC_SMALL_CLUSTER;
+constexpr int GC_SMALL_CHUNKS = GC_SMALL_THREADS / 32;
+constexpr int64_t GC_SMALL_BYTES = 64 << 10;                   // a block's latency against a grid's launch and barrier
 
 enum : int32_t { GC_F32_VEC = 0, GC_BF16_VEC = 1, GC_F32_ANY = 2, GC_BF16_ANY = 3 };
 
@@ -69,7 +74,9 @@ struct __align__(32) Chunk {
   int64_t pad;
 };
 
-constexpr size_t GC_SCRATCH_BYTES = GC_MAX_GRID * sizeof(double);
+// The table's head: the blocks' sums, then the arrivals at gc_hold's barrier (zero when the list is made).
+constexpr size_t GC_ARRIVALS_OFF = GC_MAX_GRID * sizeof(double);
+constexpr size_t GC_SCRATCH_BYTES = GC_ARRIVALS_OFF + 256;
 
 // The chunks of a list, in order: sink(chunk) for each.  Tensors whose src
 // starts off a 16-byte boundary get a short first chunk up to it.
@@ -127,20 +134,35 @@ int64_t count_chunks(const lrm_tensor* tensors, int32_t count, int64_t chunk_byt
   return total;
 }
 
-// Bytes of a chunk.  Small lists: the smallest that gives gc_small's warps no
-// more than one each.  Others: up to a batch of a warp, cut so that the warps
-// of two blocks an SM get equal numbers; above GC_LARGE_BYTES four batches (a
-// descriptor then costs 0.2 % of the bytes it stands for).
-int64_t chunk_bytes_of(const lrm_tensor* tensors, int32_t count) {
+// How a list is worked on, and how it is cut.
+enum : int { GC_BY_SMALL, GC_BY_HOLD, GC_BY_CLIP, GC_BY_RING };
+struct Plan {
+  int by;
+  int64_t chunk_bytes, chunks;
+};
+
+Plan plan_of(const lrm_tensor* tensors, int32_t count) {
   int64_t bytes = 0;
   for (int32_t i = 0; i < count; ++i) bytes += tensors[i].n * (tensors[i].dtype == LRM_F32 ? 4 : 2);
-  if (bytes > GC_LARGE_BYTES) return GC_RING_BYTES;
-  if (bytes <= static_cast<int64_t>(GC_SMALL_CHUNKS) * GC_BATCH_BYTES)
-    for (int64_t b = 512; b <= GC_BATCH_BYTES; b *= 2)
-      if (count_chunks(tensors, count, b) <= GC_SMALL_CHUNKS) return b;
-  const int64_t warps = 152 * 2 * GC_WARPS, rounds = (bytes + warps * GC_BATCH_BYTES - 1) / (warps * GC_BATCH_BYTES);
-  const int64_t even = (bytes + warps * rounds - 1) / (warps * rounds);
-  return even > 512 ? (even + 127) / 128 * 128 : 512;
+  const auto plan = [&](int by, int64_t b) { return Plan{by, b, count_chunks(tensors, count, b)}; };
+  if (bytes > GC_LARGE_BYTES) return plan(GC_BY_RING, GC_RING_BYTES);
+  // the smallest chunks that give gc_small's warps no more than one each
+  if (bytes <= GC_SMALL_BYTES)
+    for (int64_t b = 512; b <= GC_BATCH_BYTES; b *= 2) {
+      const Plan p = plan(GC_BY_SMALL, b);
+      if (p.chunks <= GC_SMALL_CHUNKS) return p;
+    }
+  // up to a batch of a warp, cut so that the warps get equal numbers: of one block an SM, or of two
+  const auto even = [&](int64_t warps) {
+    const int64_t rounds = (bytes + warps * GC_BATCH_BYTES - 1) / (warps * GC_BATCH_BYTES);
+    const int64_t b = (bytes + warps * rounds - 1) / (warps * rounds);
+    return b > 512 ? (b + 127) / 128 * 128 : int64_t{512};
+  };
+  if (bytes <= GC_HOLD_BYTES) {
+    const Plan p = plan(GC_BY_HOLD, even(GC_SMS * GC_WARPS));
+    if (p.chunks <= static_cast<int64_t>(GC_HELD) * GC_SMS * GC_WARPS) return p;
+  }
+  return plan(GC_BY_CLIP, even(2 * GC_SMS * GC_WARPS));
 }
 
 lrm_status check_tensors(const lrm_tensor* tensors, int32_t count) {
@@ -375,6 +397,138 @@ __global__ void __launch_bounds__(GC_THREADS) gc_stats(const double* __restrict_
   if (threadIdx.x == 0) *stats = r;
 }
 
+// Every block of the launch arrives once and waits for the others (all are
+// resident: the launch is cooperative).  The arrivals are never reset, so that a
+// call needs nothing cleared before it: they are a multiple of the grid between
+// calls.  False when the wait ran out.
+__device__ bool grid_barrier(unsigned long long* arrivals, unsigned long long wait_ns) {
+  __shared__ int s_ok;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const unsigned long long mine = atomicAdd(arrivals, 1ull), want = (mine / gridDim.x + 1) * gridDim.x;
+    const uint64_t t0 = globaltimer_ns();
+    int ok = 1;
+    for (uint32_t it = 1;; ++it) {
+      unsigned long long now;
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(now) : "l"(arrivals) : "memory");
+      if (now >= want) break;
+      if ((it & 15u) == 0 && globaltimer_ns() - t0 > wait_ns) {
+        ok = 0;
+        break;
+      }
+    }
+    s_ok = ok;
+  }
+  __syncthreads();
+  return s_ok != 0;
+}
+
+// Norm and scaling in one launch, for lists of up to GC_HELD chunks a warp: they
+// come to shared memory by bulk copies and stay there over the grid's barrier, so
+// that they are read once (4 MB of fp32 6.8 us against 8.8 with two launches, 8 MB
+// 7.3 against 9.3, 16 MB 10.2 against 11.9; holding part of a longer list and
+// reading the rest twice gains nothing: 60 MB 33.6 us against 32.0).
+__global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict__ chunks, long long count,
+                                                        double* __restrict__ partial, unsigned long long* arrivals,
+                                                        int scale, float max_norm, int in_place,
+                                                        lrm_grad_stats* __restrict__ stats,
+                                                        unsigned long long wait_ns, unsigned int* status) {
+  extern __shared__ __align__(128) unsigned char gc_smem[];
+  __shared__ uint64_t s_full[GC_WARPS][GC_HELD];
+  __shared__ double s_sum[GC_WARPS];
+  __shared__ int s_late;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint4* held = reinterpret_cast<uint4*>(gc_smem + warp * (GC_HELD * GC_BATCH_BYTES));
+  constexpr int HELD_VECS = GC_BATCH_BYTES / 16;
+  uint64_t* full = s_full[warp];
+  const long long step = static_cast<long long>(gridDim.x) * GC_WARPS;
+  const long long first = static_cast<long long>(blockIdx.x) * GC_WARPS + warp;
+  if (threadIdx.x == 0) s_late = 0;
+  if (lane == 0) {
+#pragma unroll
+    for (int j = 0; j < GC_HELD; ++j) mbar_init(&full[j], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  Chunk kept[GC_HELD];
+#pragma unroll
+  for (int j = 0; j < GC_HELD; ++j) {
+    kept[j].n = 0;
+    if (first + j * step < count) kept[j] = chunks[first + j * step];
+  }
+#pragma unroll
+  for (int j = 0; j < GC_HELD; ++j) {
+    if (kept[j].n > 0 && is_vec(kept[j]) && lane == 0) {
+      const uint32_t bytes = static_cast<uint32_t>(vectors(kept[j])) * 16u;
+      mbar_arrive_expect_tx(&full[j], bytes);
+      bulk_load(held + j * HELD_VECS, kept[j].src, bytes, &full[j]);
+    }
+  }
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < GC_HELD; ++j) {
+    const Chunk& c = kept[j];
+    if (c.n == 0) continue;
+    if (is_vec(c)) {
+      if (!mbar_wait(&full[j], 0, wait_ns, nullptr)) s_late = 1;
+      const int nv = vectors(c);
+      uint4 x[GC_BATCH];
+#pragma unroll
+      for (int b = 0; b < GC_BATCH; ++b) {
+        const int v = lane + 32 * b;
+        x[b] = v < nv ? held[j * HELD_VECS + v] : make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (c.kind == GC_F32_VEC)
+        batch_squares<true>(x, sum);
+      else
+        batch_squares<false>(x, sum);
+    } else {
+      sum += any_squares(c, lane);
+    }
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    sum = warp_sum(lane < GC_WARPS ? s_sum[lane] : 0.0);
+    // a copy that did not come makes the norm NaN, so that no block scales by it
+    if (lane == 0) partial[blockIdx.x] = s_late ? __longlong_as_double(0x7ff8000000000000ll) : sum;
+  }
+  const bool met = grid_barrier(arrivals, wait_ns);
+  if ((s_late || !met) && threadIdx.x == 0) raise_flag(status, LRM_ERR_TIMEOUT);
+  if (s_late) {  // a late copy gets a last chance to land before the block ends
+#pragma unroll
+    for (int j = 0; j < GC_HELD; ++j)
+      if (kept[j].n > 0 && is_vec(kept[j])) mbar_wait(&full[j], 0, wait_ns, nullptr);
+    return;
+  }
+  if (!met || (!scale && blockIdx.x != 0)) return;
+  const lrm_grad_stats r = block_stats(partial, gridDim.x, scale ? max_norm : INFINITY);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *stats = r;
+  if (!scale || (in_place && r.coef == 1.f)) return;
+#pragma unroll
+  for (int j = 0; j < GC_HELD; ++j) {
+    const Chunk& c = kept[j];
+    if (c.n == 0) continue;
+    if (is_vec(c)) {
+      const int nv = vectors(c);
+      uint4* q = static_cast<uint4*>(c.dst);
+      const bool f32 = c.kind == GC_F32_VEC;
+#pragma unroll
+      for (int b = 0; b < GC_BATCH; ++b) {
+        const int v = lane + 32 * b;
+        if (v < nv) {
+          const uint4 x = held[j * HELD_VECS + v];
+          __stcs(q + v, f32 ? scale_f32x4(x, r.coef) : scale_bf16x8(x, r.coef));
+        }
+      }
+    } else {
+      any_scale(c, r.coef, lane);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(GC_THREADS) gc_clip(const Chunk* __restrict__ chunks, long long count,
                                                       const double* __restrict__ partial, int nblk, float max_norm,
                                                       int in_place, lrm_grad_stats* __restrict__ stats) {
@@ -491,19 +645,17 @@ __global__ void __launch_bounds__(GC_RING_THREADS, 1) gc_ring(const Chunk* __res
   if (lane == 0) bulk_wait<0>();
 }
 
-// scale = 0: the norm alone.
+// One block, a chunk a warp, the values in registers between the norm and the
+// scaling.  scale = 0: the norm alone.
 __global__ void __launch_bounds__(GC_SMALL_THREADS) gc_small(const Chunk* __restrict__ chunks, int count, int scale,
                                                              float max_norm, int in_place,
                                                              lrm_grad_stats* __restrict__ stats) {
-  __shared__ double s_sum[GC_SMALL_WARPS];
-  __shared__ double s_rank[GC_SMALL_CLUSTER];
+  __shared__ double s_sum[GC_SMALL_CHUNKS];
   __shared__ lrm_grad_stats s_stats;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank(), ranks = gridDim.x;  // one cluster
-  const int i = static_cast<int>(rank) * GC_SMALL_WARPS + warp;
   Chunk c = {};
-  if (i < count) c = chunks[i];
-  const bool vec = i < count && is_vec(c);
+  if (warp < count) c = chunks[warp];
+  const bool vec = warp < count && is_vec(c);
   uint4 x[GC_BATCH];
   double sum = 0.0;
   if (vec) {
@@ -512,32 +664,25 @@ __global__ void __launch_bounds__(GC_SMALL_THREADS) gc_small(const Chunk* __rest
       batch_squares<true>(x, sum);
     else
       batch_squares<false>(x, sum);
-  } else if (i < count) {
+  } else if (warp < count) {
     sum = any_squares(c, lane);
   }
   sum = warp_sum(sum);
   if (lane == 0) s_sum[warp] = sum;
-  if (ranks > 1) cluster_sync_all();  // every CTA has started
-  else __syncthreads();
+  __syncthreads();
   if (warp == 0) {
-    sum = warp_sum(s_sum[lane]);
-    if (lane < static_cast<int>(ranks))
-      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa_shared(&s_rank[rank], lane)), "d"(sum) : "memory");
-  }
-  if (ranks > 1) cluster_sync_all();
-  else __syncthreads();
-  if (threadIdx.x == 0) {
-    sum = 0.0;
-    for (uint32_t r = 0; r < ranks; ++r) sum += s_rank[r];
-    s_stats = make_stats(sum, scale ? max_norm : INFINITY);
-    if (rank == 0) *stats = s_stats;
+    sum = warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? s_sum[lane] : 0.0);
+    if (lane == 0) {
+      s_stats = make_stats(sum, scale ? max_norm : INFINITY);
+      *stats = s_stats;
+    }
   }
   __syncthreads();
   const lrm_grad_stats r = s_stats;
   if (!scale || (in_place && r.coef == 1.f)) return;
   if (vec)
     store_batch(static_cast<uint4*>(c.dst), 0, vectors(c), lane, x, c.kind == GC_F32_VEC, r.coef);
-  else if (i < count)
+  else if (warp < count)
     any_scale(c, r.coef, lane);
 }
 
@@ -546,18 +691,29 @@ const Chunk* chunks_of(const lrm_grad_list* list) {
 }
 
 lrm_status launch_small(const lrm_grad_list* list, int scale, float max_norm, lrm_grad_stats* stats, cudaStream_t s) {
+  const int warps = list->chunks > 0 ? static_cast<int>(list->chunks) : 1;
+  gc_small<<<1, 32 * warps, 0, s>>>(chunks_of(list), static_cast<int>(list->chunks), scale, max_norm, list->in_place,
+                                    stats);
+  return launch_status();
+}
+
+// scale = 0: the norm alone.
+lrm_status launch_hold(lrm_ctx* ctx, const lrm_grad_list* list, int scale, float max_norm, lrm_grad_stats* stats,
+                       cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(list->small);
-  cfg.blockDim = dim3(GC_SMALL_THREADS);
+  cfg.gridDim = dim3(list->grid_clip);
+  cfg.blockDim = dim3(GC_THREADS);
+  cfg.dynamicSmemBytes = GC_HOLD_SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = list->small;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, gc_small, chunks_of(list), static_cast<int>(list->chunks), scale, max_norm,
-                         list->in_place, stats) != cudaSuccess) {
+  unsigned long long* arrivals =
+      reinterpret_cast<unsigned long long*>(static_cast<char*>(list->table) + GC_ARRIVALS_OFF);
+  if (cudaLaunchKernelEx(&cfg, gc_hold, chunks_of(list), list->chunks, static_cast<double*>(list->table), arrivals,
+                         scale, max_norm, list->in_place, stats, ctx->wait_budget_ns, ctx->d_status) != cudaSuccess) {
     cudaGetLastError();
     return LRM_ERR_CUDA;
   }
@@ -579,8 +735,7 @@ extern "C" lrm_status lrm_grad_table_size(const lrm_tensor* tensors, int32_t cou
   if (bytes == nullptr) return LRM_ERR_INVALID_ARG;
   const lrm_status st = check_tensors(tensors, count);
   if (st != LRM_OK) return st;
-  *bytes = GC_SCRATCH_BYTES +
-           static_cast<size_t>(count_chunks(tensors, count, chunk_bytes_of(tensors, count))) * sizeof(Chunk);
+  *bytes = GC_SCRATCH_BYTES + static_cast<size_t>(plan_of(tensors, count).chunks) * sizeof(Chunk);
   return LRM_OK;
 }
 
@@ -614,20 +769,23 @@ extern "C" lrm_status lrm_grad_list_create(lrm_ctx* ctx, const lrm_tensor* tenso
     if (tensors[i].dst == nullptr) list->has_dst = 0;
     if (tensors[i].dst != tensors[i].src) list->in_place = 0;
   }
-  const int64_t chunk_bytes = chunk_bytes_of(tensors, count);
-  list->chunks = count_chunks(tensors, count, chunk_bytes);
-  if (list->chunks <= GC_SMALL_CHUNKS)
-    list->small = list->chunks > 0 ? static_cast<int>((list->chunks + GC_SMALL_WARPS - 1) / GC_SMALL_WARPS) : 1;
+  const Plan plan = plan_of(tensors, count);
+  list->by = plan.by;
+  list->chunks = plan.chunks;
+  list->grid_clip = 1;
   if (list->chunks > 0) {
-    Chunk* host = static_cast<Chunk*>(malloc(static_cast<size_t>(list->chunks) * sizeof(Chunk)));
+    // the arrivals (zero) and, after them, the chunks
+    constexpr size_t head = GC_SCRATCH_BYTES - GC_ARRIVALS_OFF;
+    const size_t size = head + static_cast<size_t>(list->chunks) * sizeof(Chunk);
+    char* host = static_cast<char*>(aligned_alloc(256, (size + 255) / 256 * 256));
     if (host == nullptr) {
       free(list);
       return LRM_ERR_CUDA;
     }
-    int64_t at = 0;
-    for_chunks(tensors, count, chunk_bytes, [&](const Chunk& c) { host[at++] = c; });
-    cudaError_t e = cudaMemcpyAsync(static_cast<char*>(table) + GC_SCRATCH_BYTES, host,
-                                    static_cast<size_t>(list->chunks) * sizeof(Chunk), cudaMemcpyHostToDevice, s);
+    memset(host, 0, head);
+    Chunk* at = reinterpret_cast<Chunk*>(host + head);
+    for_chunks(tensors, count, plan.chunk_bytes, [&](const Chunk& c) { *at++ = c; });
+    cudaError_t e = cudaMemcpyAsync(static_cast<char*>(table) + GC_ARRIVALS_OFF, host, size, cudaMemcpyHostToDevice, s);
     // where the GPU reads pageable memory itself the copy may still be reading `host` when the call returns
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     free(host);
@@ -637,17 +795,23 @@ extern "C" lrm_status lrm_grad_list_create(lrm_ctx* ctx, const lrm_tensor* tenso
       return LRM_ERR_CUDA;
     }
     const long long blocks = (list->chunks + GC_WARPS - 1) / GC_WARPS;
-    int gn = resident_grid(ctx, gc_norm, GC_THREADS, 0), gc = resident_grid(ctx, gc_clip, GC_THREADS, 0);
-    if (gn > GC_MAX_GRID) gn = GC_MAX_GRID;
-    if (chunk_bytes == GC_RING_BYTES) {
-      if (cudaFuncSetAttribute(gc_ring, cudaFuncAttributeMaxDynamicSharedMemorySize, GC_RING_SMEM) != cudaSuccess) {
+    static thread_local int dev = -1, resident_norm = 0, resident_clip = 0;
+    if (dev != ctx->device) {
+      if (cudaFuncSetAttribute(gc_hold, cudaFuncAttributeMaxDynamicSharedMemorySize, GC_HOLD_SMEM) != cudaSuccess ||
+          cudaFuncSetAttribute(gc_ring, cudaFuncAttributeMaxDynamicSharedMemorySize, GC_RING_SMEM) != cudaSuccess) {
         cudaGetLastError();
         free(list);
         return LRM_ERR_CUDA;
       }
-      list->ring = 1;
-      gc = ctx->sm_count;
+      resident_norm = resident_grid(ctx, gc_norm, GC_THREADS, 0);
+      resident_clip = resident_grid(ctx, gc_clip, GC_THREADS, 0);
+      dev = ctx->device;
     }
+    const int gn = resident_norm < GC_MAX_GRID ? resident_norm : GC_MAX_GRID;
+    // a part with fewer SMs than the plan counts on
+    if (plan.by == GC_BY_HOLD && plan.chunks > static_cast<int64_t>(GC_HELD) * ctx->sm_count * GC_WARPS)
+      list->by = GC_BY_CLIP;
+    const int gc = list->by == GC_BY_CLIP ? resident_clip : ctx->sm_count;
     list->grid_norm = static_cast<int>(blocks < gn ? blocks : gn);
     list->grid_clip = static_cast<int>(blocks < gc ? blocks : gc);
   }
@@ -666,7 +830,8 @@ extern "C" lrm_status lrm_grad_norm(lrm_ctx* ctx, const lrm_grad_list* list, lrm
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return LRM_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (list->small) return launch_small(list, 0, 0.f, stats, s);
+  if (list->by == GC_BY_SMALL) return launch_small(list, 0, 0.f, stats, s);
+  if (list->by == GC_BY_HOLD) return launch_hold(ctx, list, 0, 0.f, stats, s);
   const lrm_status st = launch_norm(list, s);
   if (st != LRM_OK) return st;
   return launch_dependent(gc_stats, 1, GC_THREADS, 0, 1, s, static_cast<const double*>(list->table), list->grid_norm,
@@ -682,12 +847,13 @@ extern "C" lrm_status lrm_grad_clip(lrm_ctx* ctx, const lrm_grad_list* list, flo
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return LRM_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (list->small) return launch_small(list, 1, max_norm, stats, s);
+  if (list->by == GC_BY_SMALL) return launch_small(list, 1, max_norm, stats, s);
+  if (list->by == GC_BY_HOLD) return launch_hold(ctx, list, 1, max_norm, stats, s);
   const lrm_status st = launch_norm(list, s);
   if (st != LRM_OK) return st;
   const Chunk* chunks = chunks_of(list);
   const double* partial = static_cast<const double*>(list->table);
-  if (list->ring)
+  if (list->by == GC_BY_RING)
     return launch_dependent(gc_ring, list->grid_clip, GC_RING_THREADS, GC_RING_SMEM, 1, s, chunks, list->chunks, partial,
                             list->grid_norm, max_norm, list->in_place, stats, ctx->wait_budget_ns, ctx->d_status);
   return launch_dependent(gc_clip, list->grid_clip, GC_THREADS, 0, 1, s, chunks, list->chunks, partial,
