@@ -60,6 +60,7 @@ constexpr int GC_HELD = 3;                                     // chunks a warp 
 constexpr int GC_HOLD_SMEM = GC_WARPS * GC_HELD * GC_BATCH_BYTES;
 constexpr int GC_SMS = 152;                                    // the shares of the warps are cut for this many SMs
 constexpr int64_t GC_HOLD_BYTES = int64_t{24} << 20;           // of 29 MB that GC_SMS blocks hold: chunks are not all full
+constexpr unsigned long long GC_DRAIN_NS = 1000000000ull;      // for copies under way after a wait ran out
 constexpr int GC_SMALL_THREADS = 1024;
 constexpr int GC_SMALL_CHUNKS = GC_SMALL_THREADS / 32;
 constexpr int64_t GC_SMALL_BYTES = 64 << 10;                   // a block's latency against a grid's launch and barrier
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
   if (s_late) {  // a late copy gets a last chance to land before the block ends
 #pragma unroll
     for (int j = 0; j < GC_HELD; ++j)
-      if (kept[j].n > 0 && is_vec(kept[j])) mbar_wait(&full[j], 0, wait_ns, nullptr);
+      if (kept[j].n > 0 && is_vec(kept[j])) mbar_wait(&full[j], 0, GC_DRAIN_NS, nullptr);
     return;
   }
   if (!met || (!scale && blockIdx.x != 0)) return;
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(GC_RING_THREADS, 1) gc_ring(const Chunk* __res
   // copies still under way (after a wait that ran out) get a last chance to land
 #pragma unroll
   for (int j = 0; j < GC_STAGES; ++j)
-    if (held[j].n > 0 && is_vec(held[j])) mbar_wait(&full[j], (phases >> j) & 1u, wait_ns, nullptr);
+    if (held[j].n > 0 && is_vec(held[j])) mbar_wait(&full[j], (phases >> j) & 1u, GC_DRAIN_NS, nullptr);
   if (lane == 0) bulk_wait<0>();
 }
 

@@ -483,7 +483,10 @@ LRM_API lrm_status lrm_router_backward(lrm_ctx* ctx, const void* logits, int32_t
  * Squares are summed so that neither large nor small values are lost (fp64
  * where a square would leave fp32's range, and across batches of elements);
  * the order is fixed, so the same inputs give the same bits.  Calls on one
- * list share its table: serialise them.
+ * list share its table: serialise them.  Lists up to 24 MB run as one cooperative
+ * launch, whose blocks wait for one another; that wait and those on copies are
+ * bounded (lrm_set_wait_budget): one that runs out sets LRM_ERR_TIMEOUT, the
+ * outputs are then incomplete, and the list stays usable.
  */
 typedef struct lrm_tensor {
   const void* src;
@@ -510,7 +513,7 @@ LRM_API lrm_status lrm_grad_clip(lrm_ctx* ctx, const lrm_grad_list* list, float 
 LRM_API lrm_status lrm_get_device_status(lrm_ctx* ctx, void* stream, uint32_t* flags);
 
 /* Time limit, in nanoseconds, of every device-side wait of the grouped GEMM
- * kernels (default 2e9).  A wait that runs out sets LRM_ERR_TIMEOUT and the
+ * and the clipping kernels (default 2e9).  A wait that runs out sets LRM_ERR_TIMEOUT and the
  * kernel winds down and returns. */
 LRM_API lrm_status lrm_set_wait_budget(lrm_ctx* ctx, uint64_t ns);
 

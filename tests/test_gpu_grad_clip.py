@@ -299,6 +299,33 @@ def test_more_elements_than_32_bits():
     assert int((x == 0.125).sum()) == n - 1
 
 
+@pytest.mark.parametrize("n", [1 << 20, 50_000_000])
+def test_a_wait_that_runs_out_is_reported_and_the_list_stays_usable(n):
+    # no time at all for the waits on copies and on the other blocks
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    ctx = L.lrm_create(0)
+    try:
+        x = torch.full((n,), 0.5, device="cuda")
+        out = torch.zeros_like(x)
+        c = GradClip([x], [out], ctx=ctx)
+        L.lrm_set_wait_budget(ctx, 0)
+        for _ in range(3):
+            c.clip(1.0)
+        assert L.lrm_get_device_status(ctx) in (0, 1 << L.LRM_ERR_TIMEOUT)
+        L.lrm_set_wait_budget(ctx, 2_000_000_000)
+        for _ in range(3):
+            out.zero_()
+            c.clip(1.0)
+            assert L.lrm_get_device_status(ctx) == 0
+            assert abs(float(c.norm.item()) - 0.5 * math.sqrt(n)) <= REL * 0.5 * math.sqrt(n)
+            assert torch.equal(out, x * c.coef)
+        c.close()
+    finally:
+        L.lrm_destroy(ctx)
+
+
 def test_large_tensor():
     n = (1 << 27) + 12345
     x = torch.full((n,), 0.5, device="cuda")
