@@ -31,7 +31,7 @@
 // The forward is bound by instruction issue: 131072 x 128 fp32 logits take 34 us,
 // of which the 77 MB to move need 11; 32768 x 128 take 16 us, half of it launch,
 // first load and rf_sums.  The backward is bound by memory: 131072 x 128 fp32 in
-// 27 us, 5.5 TB/s.
+// 25 us, 5.8 TB/s.
 #include <math.h>
 
 #include <type_traits>
@@ -48,7 +48,7 @@ constexpr int RF_ONE_BLOCK_PASSES = 2;  // batches of up to this many passes of 
 // k = 4 31.2 / 33.2, k = 8 37.4 / 34.3).
 constexpr int RF_ROUNDS = 4;
 constexpr int RS_SUM_THREADS = 1024;
-constexpr int RB_THREADS = 256;
+constexpr int RB_THREADS = 128;  // 131072 x 128 fp32: 25.3 us, blocks of 256 26.5, of 512 27.2
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -57,7 +57,7 @@ constexpr float LN2 = 0.6931471805599453f;
 // that what a token costs once (reductions, slots, addresses) is shared by the
 // tokens of a warp.  At E = 128 a warp a token took 346 instructions a token in
 // the forward (45 us for 131072 tokens) and 31.3 us in the backward; four tokens a
-// warp take 175 (37 us; 34 with merged lists) and 27 us.
+// warp take 175 (37 us; 34 with merged lists) and 25 us.
 template <int N>
 using Int = std::integral_constant<int, N>;
 
