@@ -43,8 +43,8 @@ namespace lrm {
 namespace {
 
 constexpr int RF_ONE_BLOCK_PASSES = 2;  // batches of up to this many passes of one block use one block
-// Up to this k the slots are found by rounds of a maximum, above it by merging
-// the lanes' lists (131072 x 128, rounds against merges: k = 2 28.7 / 32.5 us,
+// Up to this k, and above 8, the slots are found by rounds of a maximum, between
+// them by merging the lanes' lists of eight (131072 x 128, rounds against merges: k = 2 28.7 / 32.5 us,
 // k = 4 31.2 / 33.2, k = 8 37.4 / 34.3).
 constexpr int RF_ROUNDS = 4;
 constexpr int RS_SUM_THREADS = 1024;
@@ -133,8 +133,9 @@ __device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // Four consecutive logits as they lie in memory.  load() leaves the places
-// beyond the row as they are: -inf, from clear().  vec: rows start at a multiple
-// of four elements' bytes.
+// beyond the row as they are: -inf, from clear().  V: the elements that rows
+// start at a multiple of, 4, 2 or 1 (bf16 backward of 80000 x 210: 22.7 us in
+// pairs, 38.9 one by one).
 template <typename TL>
 struct Four {
   uint32_t w[sizeof(TL)];
@@ -143,30 +144,33 @@ struct Four {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(TL)); ++i) w[i] = is_bf16<TL> ? 0xFF80FF80u : 0xFF800000u;
   }
-  __device__ __forceinline__ void load(const TL* __restrict__ row, int e0, int E, bool vec) {
-    if (vec) {
-      if (e0 >= E) return;
-      if constexpr (is_bf16<TL>) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(row + e0));
+  template <int V>
+  __device__ __forceinline__ void load(const TL* __restrict__ row, int e0, int E) {
+#pragma unroll
+    for (int i = 0; i < 4; i += V) {
+      if (e0 + i >= E) continue;
+      const TL* p = row + e0 + i;
+      if constexpr (V == 4 && is_bf16<TL>) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
         w[0] = x.x;
         w[1] = x.y;
-      } else {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + e0));
+      } else if constexpr (V == 4) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
         w[0] = x.x;
         w[1] = x.y;
         w[2] = x.z;
         w[3] = x.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (e0 + i >= E) continue;
-        if constexpr (is_bf16<TL>) {
-          const uint32_t x = __ldg(reinterpret_cast<const uint16_t*>(row) + e0 + i);
-          w[i / 2] = (i & 1) ? (w[i / 2] & 0xFFFFu) | x << 16 : (w[i / 2] & 0xFFFF0000u) | x;
-        } else {
-          w[i] = __float_as_uint(__ldg(reinterpret_cast<const float*>(row) + e0 + i));
-        }
+      } else if constexpr (V == 2 && is_bf16<TL>) {
+        w[i / 2] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      } else if constexpr (V == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+        w[i] = x.x;
+        w[i + 1] = x.y;
+      } else if constexpr (is_bf16<TL>) {
+        const uint32_t x = __ldg(reinterpret_cast<const uint16_t*>(p));
+        w[i / 2] = (i & 1) ? (w[i / 2] & 0xFFFFu) | x << 16 : (w[i / 2] & 0xFFFF0000u) | x;
+      } else {
+        w[i] = __float_as_uint(__ldg(reinterpret_cast<const float*>(p)));
       }
     }
   }
@@ -182,9 +186,18 @@ struct Pieces {
 #pragma unroll
     for (int c = 0; c < C; ++c) f[c].clear();
   }
-  __device__ __forceinline__ void load(const TL* __restrict__ row, int q, int E, bool vec) {
+  template <int V>
+  __device__ __forceinline__ void load_by(const TL* __restrict__ row, int q, int E) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) f[c].load(row, 4 * (q + G * c), E, vec);
+    for (int c = 0; c < C; ++c) f[c].template load<V>(row, 4 * (q + G * c), E);
+  }
+  __device__ __forceinline__ void load(const TL* __restrict__ row, int q, int E, int vec) {
+    if (vec == 4)
+      load_by<4>(row, q, E);
+    else if (vec == 2)
+      load_by<2>(row, q, E);
+    else
+      load_by<1>(row, q, E);
   }
   __device__ __forceinline__ float get(int c, int i) const {
     if constexpr (is_bf16<TL>)
@@ -195,8 +208,8 @@ struct Pieces {
 };
 
 template <typename TO>
-__device__ __forceinline__ void store_four(TO* __restrict__ row, int e0, int E, bool vec, const float (&v)[4]) {
-  if (vec) {
+__device__ __forceinline__ void store_four(TO* __restrict__ row, int e0, int E, int vec, const float (&v)[4]) {
+  if (vec == 4) {
     if (e0 >= E) return;
     if constexpr (is_bf16<TO>) {
       const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
@@ -204,6 +217,15 @@ __device__ __forceinline__ void store_four(TO* __restrict__ row, int e0, int E, 
           make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     } else {
       *reinterpret_cast<float4*>(row + e0) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  } else if (vec == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      if (e0 + i >= E) continue;
+      if constexpr (is_bf16<TO>)
+        *reinterpret_cast<__nv_bfloat162*>(row + e0 + i) = __floats2bfloat162_rn(v[i], v[i + 1]);
+      else
+        *reinterpret_cast<float2*>(row + e0 + i) = make_float2(v[i], v[i + 1]);
     }
   } else {
 #pragma unroll
@@ -338,7 +360,7 @@ __device__ __forceinline__ void sort_top(uint32_t (&a)[N]) {
 // The exact selection: k rounds over full keys, NaN below -inf, equal keys to
 // the lower expert.  Returns slot q's expert.
 template <typename TL, int G, int C>
-__device__ __noinline__ int select_exact(const TL* row, int E, int k, bool vec) {
+__device__ __noinline__ int select_exact(const TL* row, int E, int k, int vec) {
   const int lane = threadIdx.x & 31, q = lane % G;
   Pieces<TL, G, C> raw;
   raw.clear();
@@ -489,10 +511,12 @@ __global__ void __launch_bounds__(RS_SUM_THREADS) rf_sums(ForwardArgs a, int nbl
   if (threadIdx.x == 0) write_losses(a, fp, z, tokens);
 }
 
-template <typename TL, int G, int C, int LIST>
-__global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict__ logits, ForwardArgs a, bool vec) {
+template <typename TL, int G, int C>
+__global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict__ logits, ForwardArgs a, int vec) {
   constexpr int NT = rf_threads(C), NW = NT / 32, PER_WARP = 32 / G, N = 4 * C;
   constexpr int NK = C == 3 ? 16 : N;    // keys of a lane, a power of two
+  // those it keeps for the selection, more slots than that included (80000 x 208, k = 12: 55 us, 80 with lists of 16)
+  constexpr int LIST = NK < 8 ? NK : 8;
   constexpr uint32_t LOW = G * NK - 1;  // the key's bits that hold the expert
   extern __shared__ float rt_smem[];
   float* sp = rt_smem;                                     // [NW][E]
@@ -551,8 +575,8 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
     const bool counted = ok && s != 0.f;
 
     sort_top<NK, LIST>(key);
-    bool crowded = false;  // fp32: a key left out may stand for a larger logit than the last one kept
-    if (LIST == 8 && G <= 16 && k > RF_ROUNDS) {
+    bool crowded = false;  // a logit left out may be larger than the last one kept
+    if (LIST == 8 && G <= 16 && k > RF_ROUNDS && (G <= LIST || k <= LIST)) {
       // the lanes' lists merged pairwise: every lane ends with the token's eight largest
       uint32_t own[LIST];
 #pragma unroll
@@ -592,18 +616,20 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
         key[LIST - 1] = hit ? 0u : key[LIST - 1];
       }
       __syncwarp();
-      // a lane whose list ran out may hold more
+      // a lane whose list ran out may hold more (with 16 lanes and 16 random slots one token in 30000)
       if constexpr (!is_bf16<TL>)
         crowded = (sel[k - 1] ^ group_max<G>(key[0])) <= LOW || (NK > LIST && key[0] == 0u);
+      else
+        crowded = NK > LIST && k > LIST && key[0] == 0u;
     }
     const bool slot = q < k && here;
     const uint32_t mine = sel[q];
     int e = min(static_cast<int>(LOW - (mine & LOW)), E - 1);
     float v = slot ? load_elem(row + e) : 0.f;
-    bool unclear = here && !(s > 0.f);
+    bool unclear = here && (crowded || !(s > 0.f));
     if constexpr (!is_bf16<TL>) {
       const float vn = __shfl_down_sync(0xffffffffu, v, 1, G);
-      unclear = unclear || (here && crowded) || (q < k - 1 && here && v < vn);
+      unclear = unclear || (q < k - 1 && here && v < vn);
     }
     if (__any_sync(0xffffffffu, unclear)) {
       e = select_exact<TL, G, C>(row, E, k, vec);
@@ -709,7 +735,7 @@ struct TokenIn {
 
 template <typename TL, typename TO, int G, int C>
 __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ logits, TO* __restrict__ dlogits,
-                                                      BackwardArgs a, bool vec_in, bool vec_out) {
+                                                      BackwardArgs a, int vec_in, int vec_out) {
   constexpr int NW = RB_THREADS / 32, PER_WARP = 32 / G;
   __shared__ float4 s_add[NW][32 * C];         // the gates' part of the warp's tokens
   __shared__ uint8_t s_slot[NW][32 * 4 * C];   // the slot that named an expert last
@@ -825,31 +851,26 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
 // ---------------------------------------------------------------------------
 // launches
 
-template <typename TL, int G, int C, int LIST>
-lrm_status launch_rf(const TL* logits, const ForwardArgs& a, int nblk, bool vec, cudaStream_t s) {
+template <typename TL, int G, int C>
+lrm_status launch_rf(const TL* logits, const ForwardArgs& a, int nblk, int vec, cudaStream_t s) {
   constexpr int NT = rf_threads(C);
   const size_t smem = static_cast<size_t>(NT / 32 + 1) * a.E * sizeof(float);
-  rf_rows<TL, G, C, LIST><<<nblk, NT, smem, s>>>(logits, a, vec);
+  rf_rows<TL, G, C><<<nblk, NT, smem, s>>>(logits, a, vec);
   return launch_status();
 }
 
-// rows of four-element groups that start on the group's bytes
+// The elements of a group that every row starts on the bytes of.
 template <typename T>
-bool rows_vec(const T* p, int E) {
-  return E % 4 == 0 && aligned(p, 4 * sizeof(T));
+int rows_vec(const T* p, int E) {
+  return E % 4 == 0 && aligned(p, 4 * sizeof(T)) ? 4 : E % 2 == 0 && aligned(p, 2 * sizeof(T)) ? 2 : 1;
 }
 
-// A lane's list holds as many keys as slots can come from it: 8 where k <= 8.
 template <typename TL>
 lrm_status dispatch_rf(const void* logits, const ForwardArgs& a, int nblk, cudaStream_t s) {
   const TL* l = static_cast<const TL*>(logits);
-  const bool vec = rows_vec(l, a.E);
+  const int vec = rows_vec(l, a.E);
   return with_split(a.E, a.k, [&](auto g, auto c) {
-    constexpr int G = decltype(g)::value, C = decltype(c)::value;
-    if constexpr (C > 2 && G > 8) {
-      if (a.k > 8) return launch_rf<TL, G, C, C == 3 ? 16 : 4 * C>(l, a, nblk, vec, s);
-    }
-    return launch_rf<TL, G, C, (C > 2 ? 8 : 4 * C)>(l, a, nblk, vec, s);
+    return launch_rf<TL, decltype(g)::value, decltype(c)::value>(l, a, nblk, vec, s);
   });
 }
 

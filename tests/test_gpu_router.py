@@ -202,6 +202,27 @@ def test_close_logits_side_by_side(E, stride):
     run(T, E, k + 1 if E < 300 else 9, logits=torch.from_numpy(z), seed=E)
 
 
+@pytest.mark.parametrize("E,stride,k", [(160, 16, 9), (256, 16, 9), (256, 16, 12), (256, 16, 16), (128, 8, 12), (512, 32, 12),
+                                        (1000, 32, 16), (1024, 32, 32)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_slots_than_a_list_from_one_lane(E, stride, k, dtype):
+    # the largest logits all in experts `stride` groups of four apart
+    near = np.flatnonzero((np.arange(E) // 4) % stride == 0)
+    rng = np.random.default_rng(E + k)
+    x = np.full((50, E), -30.0, np.float32)
+    for t in range(50):
+        x[t, near] = rng.permutation(near.size) * 0.25 + 1.0
+    x[25:, near[: near.size // 2]] -= 40.0
+    run(50, E, k, dtype, logits=torch.from_numpy(x).to(DT[dtype]), seed=k)
+
+
+# rows that start on two elements' bytes, or on one's
+@pytest.mark.parametrize("T,E,k", [(300, 34, 3), (301, 66, 9), (97, 210, 12), (64, 258, 8), (50, 514, 20), (111, 35, 10), (90, 213, 16)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_row_starts(T, E, k, dtype):
+    run(T, E, k, dtype, renorm=bool(T % 2), out="f32" if T % 3 else "bf16", seed=T)
+
+
 @pytest.mark.parametrize("E,stride", [(128, 8), (256, 16), (512, 32), (1000, 32)])
 @pytest.mark.parametrize("k", [2, 4, 5, 8])
 def test_last_slot_against_its_neighbour(E, stride, k):
