@@ -65,13 +65,14 @@ constexpr int GC_SMALL_THREADS = 1024;
 constexpr int GC_SMALL_CHUNKS = GC_SMALL_THREADS / 32;
 constexpr int64_t GC_SMALL_BYTES = 64 << 10;                   // a block's latency against a grid's launch and barrier
 
-enum : int32_t { GC_F32_VEC = 0, GC_BF16_VEC = 1, GC_F32_ANY = 2, GC_BF16_ANY = 3 };
+// A chunk's kind: its type and what of it lies on 16-byte boundaries.
+enum : int32_t { GC_BF16 = 1, GC_DST_ANY = 2, GC_SRC_ANY = 4 };
 
 struct __align__(32) Chunk {
   const void* src;
   void* dst;
   int32_t n;     // elements
-  int32_t kind;  // *_VEC: src and dst 16-byte aligned, n a multiple of 16 bytes
+  int32_t kind;  // without GC_SRC_ANY: src 16-byte aligned, n a multiple of 16 bytes; without GC_DST_ANY: dst too
   int64_t pad;
 };
 
@@ -94,7 +95,7 @@ void for_chunks(const lrm_tensor* tensors, int32_t count, int64_t chunk_bytes, S
       char* d = dst == nullptr ? nullptr : dst + at * es;
       const int64_t left = t.n - at, off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(s) % 16) / es;
       int64_t n;
-      bool vec = false;
+      int32_t any = GC_SRC_ANY | GC_DST_ANY;
       if (off != 0) {
         n = per - off < left ? per - off : left;
       } else if (left < per) {
@@ -102,13 +103,13 @@ void for_chunks(const lrm_tensor* tensors, int32_t count, int64_t chunk_bytes, S
       } else {
         const int64_t whole = left / per * per, most = chunk_bytes / es;
         n = whole < most ? whole : most;
-        vec = d == nullptr || aligned(d, 16);
+        any = d == nullptr || aligned(d, 16) ? 0 : GC_DST_ANY;
       }
       Chunk c;
       c.src = s;
       c.dst = d;
       c.n = static_cast<int32_t>(n);
-      c.kind = t.dtype == LRM_F32 ? (vec ? GC_F32_VEC : GC_F32_ANY) : (vec ? GC_BF16_VEC : GC_BF16_ANY);
+      c.kind = (t.dtype == LRM_F32 ? 0 : GC_BF16) | any;
       c.pad = 0;
       sink(c);
       at += n;
@@ -143,10 +144,17 @@ struct Plan {
 };
 
 Plan plan_of(const lrm_tensor* tensors, int32_t count) {
-  int64_t bytes = 0;
-  for (int32_t i = 0; i < count; ++i) bytes += tensors[i].n * (tensors[i].dtype == LRM_F32 ? 4 : 2);
+  int64_t bytes = 0, skew = 0;  // skew: of tensors whose dst lies on another place of the 16-byte grid than src
+  for (int32_t i = 0; i < count; ++i) {
+    const int64_t b = tensors[i].n * (tensors[i].dtype == LRM_F32 ? 4 : 2);
+    const uintptr_t src = reinterpret_cast<uintptr_t>(tensors[i].src), dst = reinterpret_cast<uintptr_t>(tensors[i].dst);
+    bytes += b;
+    if (dst != 0 && (src ^ dst) % 16 != 0) skew += b;
+  }
   const auto plan = [&](int by, int64_t b) { return Plan{by, b, count_chunks(tensors, count, b)}; };
-  if (bytes > GC_LARGE_BYTES) return plan(GC_BY_RING, GC_RING_BYTES);
+  // bulk copies need both ends on the grid; what is not wants the warps of gc_clip (200 MB off it: 1460 us by
+  // gc_ring's four warps an SM)
+  if (bytes > GC_LARGE_BYTES && skew <= bytes / 16) return plan(GC_BY_RING, GC_RING_BYTES);
   // the smallest chunks that give gc_small's warps no more than one each
   if (bytes <= GC_SMALL_BYTES)
     for (int64_t b = 512; b <= GC_BATCH_BYTES; b *= 2) {
@@ -278,26 +286,40 @@ __device__ __forceinline__ void store_batch(uint4* q, int v0, int nv, int lane, 
   }
 }
 
-__device__ __forceinline__ bool is_vec(const Chunk& c) { return c.kind == GC_F32_VEC || c.kind == GC_BF16_VEC; }
-__device__ __forceinline__ int vectors(const Chunk& c) { return c.n / (c.kind == GC_F32_VEC ? 4 : 8); }
+__device__ __forceinline__ bool is_f32(const Chunk& c) { return (c.kind & GC_BF16) == 0; }
+__device__ __forceinline__ bool src_vec(const Chunk& c) { return (c.kind & GC_SRC_ANY) == 0; }
+__device__ __forceinline__ bool both_vec(const Chunk& c) { return (c.kind & (GC_SRC_ANY | GC_DST_ANY)) == 0; }
+__device__ __forceinline__ int vectors(const Chunk& c) { return c.n / (is_f32(c) ? 4 : 8); }
 
-// Chunks off the 16-byte grid, element by element.
+// Chunks off the 16-byte grid, element by element, GC_BATCH of them a lane at a
+// time.
+__device__ __forceinline__ float any_load(const Chunk& c, int i) {
+  return is_f32(c) ? static_cast<const float*>(c.src)[i]
+                   : __bfloat162float(static_cast<const __nv_bfloat16*>(c.src)[i]);
+}
 __device__ __noinline__ double any_squares(const Chunk& c, int lane) {
   double sum = 0.0;
   for (int i = lane; i < c.n; i += 32) {
-    const float v = c.kind == GC_F32_ANY ? static_cast<const float*>(c.src)[i]
-                                         : __bfloat162float(static_cast<const __nv_bfloat16*>(c.src)[i]);
+    const float v = any_load(c, i);
     sum += static_cast<double>(v) * v;
   }
   return sum;
 }
 __device__ __noinline__ void any_scale(const Chunk& c, float coef, int lane) {
-  for (int i = lane; i < c.n; i += 32) {
-    if (c.kind == GC_F32_ANY)
-      static_cast<float*>(c.dst)[i] = static_cast<const float*>(c.src)[i] * coef;
-    else
-      static_cast<__nv_bfloat16*>(c.dst)[i] =
-          __float2bfloat16_rn(__bfloat162float(static_cast<const __nv_bfloat16*>(c.src)[i]) * coef);
+  for (int i0 = lane; i0 < c.n; i0 += 32 * GC_BATCH) {
+    float v[GC_BATCH];
+#pragma unroll
+    for (int j = 0; j < GC_BATCH; ++j)
+      if (i0 + 32 * j < c.n) v[j] = any_load(c, i0 + 32 * j);
+#pragma unroll
+    for (int j = 0; j < GC_BATCH; ++j) {
+      const int i = i0 + 32 * j;
+      if (i >= c.n) continue;
+      if (is_f32(c))
+        static_cast<float*>(c.dst)[i] = v[j] * coef;
+      else
+        static_cast<__nv_bfloat16*>(c.dst)[i] = __float2bfloat16_rn(v[j] * coef);
+    }
   }
 }
 
@@ -348,12 +370,12 @@ __global__ void __launch_bounds__(GC_THREADS, 2) gc_norm(const Chunk* __restrict
   for (; i < count; i += step) {
     const Chunk c = next;
     if (i + step < count) next = chunks[i + step];
-    if (is_vec(c)) {
+    if (src_vec(c)) {
       const int nv = vectors(c);
       for (int v0 = 0; v0 < nv; v0 += 32 * GC_BATCH) {
         uint4 x[GC_BATCH];
         load_batch(static_cast<const uint4*>(c.src), v0, nv, lane, x);
-        if (c.kind == GC_F32_VEC)
+        if (is_f32(c))
           batch_squares<true>(x, sum);
         else
           batch_squares<false>(x, sum);
@@ -460,7 +482,7 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
   }
 #pragma unroll
   for (int j = 0; j < GC_HELD; ++j) {
-    if (kept[j].n > 0 && is_vec(kept[j]) && lane == 0) {
+    if (kept[j].n > 0 && src_vec(kept[j]) && lane == 0) {
       const uint32_t bytes = static_cast<uint32_t>(vectors(kept[j])) * 16u;
       mbar_arrive_expect_tx(&full[j], bytes);
       bulk_load(held + j * HELD_VECS, kept[j].src, bytes, &full[j]);
@@ -471,7 +493,7 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
   for (int j = 0; j < GC_HELD; ++j) {
     const Chunk& c = kept[j];
     if (c.n == 0) continue;
-    if (is_vec(c)) {
+    if (src_vec(c)) {
       if (!mbar_wait(&full[j], 0, wait_ns, nullptr)) s_late = 1;
       const int nv = vectors(c);
       uint4 x[GC_BATCH];
@@ -480,7 +502,7 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
         const int v = lane + 32 * b;
         x[b] = v < nv ? held[j * HELD_VECS + v] : make_uint4(0u, 0u, 0u, 0u);
       }
-      if (c.kind == GC_F32_VEC)
+      if (is_f32(c))
         batch_squares<true>(x, sum);
       else
         batch_squares<false>(x, sum);
@@ -501,7 +523,7 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
   if (s_late) {  // a late copy gets a last chance to land before the block ends
 #pragma unroll
     for (int j = 0; j < GC_HELD; ++j)
-      if (kept[j].n > 0 && is_vec(kept[j])) mbar_wait(&full[j], 0, GC_DRAIN_NS, nullptr);
+      if (kept[j].n > 0 && src_vec(kept[j])) mbar_wait(&full[j], 0, GC_DRAIN_NS, nullptr);
     return;
   }
   if (!met || (!scale && blockIdx.x != 0)) return;
@@ -512,10 +534,10 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
   for (int j = 0; j < GC_HELD; ++j) {
     const Chunk& c = kept[j];
     if (c.n == 0) continue;
-    if (is_vec(c)) {
+    if (both_vec(c)) {
       const int nv = vectors(c);
       uint4* q = static_cast<uint4*>(c.dst);
-      const bool f32 = c.kind == GC_F32_VEC;
+      const bool f32 = is_f32(c);
 #pragma unroll
       for (int b = 0; b < GC_BATCH; ++b) {
         const int v = lane + 32 * b;
@@ -545,12 +567,12 @@ __global__ void __launch_bounds__(GC_THREADS) gc_clip(const Chunk* __restrict__ 
   for (; i >= 0; i -= step) {
     const Chunk c = next;
     if (i >= step) next = chunks[i - step];
-    if (is_vec(c)) {
+    if (both_vec(c)) {
       const int nv = vectors(c);
       for (int v0 = 0; v0 < nv; v0 += 32 * GC_BATCH) {
         uint4 x[GC_BATCH];
         load_batch(static_cast<const uint4*>(c.src), v0, nv, lane, x);
-        store_batch(static_cast<uint4*>(c.dst), v0, nv, lane, x, c.kind == GC_F32_VEC, r.coef);
+        store_batch(static_cast<uint4*>(c.dst), v0, nv, lane, x, is_f32(c), r.coef);
       }
     } else {
       any_scale(c, r.coef, lane);
@@ -587,7 +609,7 @@ __global__ void __launch_bounds__(GC_RING_THREADS, 1) gc_ring(const Chunk* __res
     held[j].n = 0;
     if (i < 0) return;
     held[j] = chunks[i];
-    if (is_vec(held[j]) && lane == 0) {
+    if (both_vec(held[j]) && lane == 0) {
       const uint32_t bytes = static_cast<uint32_t>(vectors(held[j])) * 16u;
       mbar_arrive_expect_tx(&full[j], bytes);
       bulk_load(ring + j * GC_RING_BYTES, held[j].src, bytes, &full[j]);
@@ -608,14 +630,14 @@ __global__ void __launch_bounds__(GC_RING_THREADS, 1) gc_ring(const Chunk* __res
       const long long at = i - j * step;
       uint4* buf = reinterpret_cast<uint4*>(ring + j * GC_RING_BYTES);
       if (ok && c.n > 0) {
-        if (is_vec(c)) {
+        if (both_vec(c)) {
           ok = __all_sync(0xffffffffu, mbar_wait(&full[j], (phases >> j) & 1u, wait_ns, nullptr));
           if (ok) {
             phases ^= 1u << j;
             held[j].n = 0;  // nothing under way in this stage
             if (scale) {
               const int nv = vectors(c);
-              const bool f32 = c.kind == GC_F32_VEC;
+              const bool f32 = is_f32(c);
 #pragma unroll 4
               for (int v = lane; v < nv; v += 32) buf[v] = f32 ? scale_f32x4(buf[v], r.coef) : scale_bf16x8(buf[v], r.coef);
               fence_proxy_async_smem();
@@ -642,7 +664,7 @@ __global__ void __launch_bounds__(GC_RING_THREADS, 1) gc_ring(const Chunk* __res
   // copies still under way (after a wait that ran out) get a last chance to land
 #pragma unroll
   for (int j = 0; j < GC_STAGES; ++j)
-    if (held[j].n > 0 && is_vec(held[j])) mbar_wait(&full[j], (phases >> j) & 1u, GC_DRAIN_NS, nullptr);
+    if (held[j].n > 0 && both_vec(held[j])) mbar_wait(&full[j], (phases >> j) & 1u, GC_DRAIN_NS, nullptr);
   if (lane == 0) bulk_wait<0>();
 }
 
@@ -656,12 +678,12 @@ __global__ void __launch_bounds__(GC_SMALL_THREADS) gc_small(const Chunk* __rest
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Chunk c = {};
   if (warp < count) c = chunks[warp];
-  const bool vec = warp < count && is_vec(c);
+  const bool vec = warp < count && src_vec(c);
   uint4 x[GC_BATCH];
   double sum = 0.0;
   if (vec) {
     load_batch(static_cast<const uint4*>(c.src), 0, vectors(c), lane, x);
-    if (c.kind == GC_F32_VEC)
+    if (is_f32(c))
       batch_squares<true>(x, sum);
     else
       batch_squares<false>(x, sum);
@@ -681,8 +703,8 @@ __global__ void __launch_bounds__(GC_SMALL_THREADS) gc_small(const Chunk* __rest
   __syncthreads();
   const lrm_grad_stats r = s_stats;
   if (!scale || (in_place && r.coef == 1.f)) return;
-  if (vec)
-    store_batch(static_cast<uint4*>(c.dst), 0, vectors(c), lane, x, c.kind == GC_F32_VEC, r.coef);
+  if (vec && both_vec(c))
+    store_batch(static_cast<uint4*>(c.dst), 0, vectors(c), lane, x, is_f32(c), r.coef);
   else if (warp < count)
     any_scale(c, r.coef, lane);
 }
