@@ -19,16 +19,19 @@
 //              touches k experts, which are placed through shared memory.
 //
 // The k largest: a lane sorts its logits as 32-bit keys whose top bits order
-// like the value and whose low bits hold the expert, inverted, so
-// that keys are unique and equal values go to the lower expert.  Few slots are
+// like the value and whose low bits hold the expert, inverted, so that
+// keys are unique and equal values go to the lower expert.  Few slots are
 // found by rounds of a group-wide maximum, the lane that owns it moving up its
 // list; more by merging the lanes' lists of eight pairwise.  For bf16 logits the
 // cut-off bits are zero and the order is exact.  For fp32 the keys are made of
-// l - m, and the order is checked against the logits: slots out of order, a
-// logit left out whose key agrees with the last slot's in all the bits kept, NaN
-// and rows of -inf send the warp to an exact selection on full keys.
+// l - m, and the order is checked against the logits: where a logit left out has a
+// key that agrees with the last slot's in all the bits kept, the logits up to the
+// last slot are counted; more than k of them, slots out of order, NaN and rows of
+// -inf send the warp to an exact selection on full keys (131072 x 128, k = 8:
+// random logits 35 us, logits of bf16 precision, where ties abound, 38 us, all
+// logits equal 44 us; 53 and 82 without the count).
 //
-// The forward is bound by instruction issue: 131072 x 128 fp32 logits take 34 us,
+// The forward is bound by instruction issue: 131072 x 128 fp32 logits take 35 us,
 // of which the 77 MB to move need 11; 32768 x 128 take 16 us, half of it launch,
 // first load and rf_sums.  The backward is bound by memory: 131072 x 128 fp32 in
 // 25 us, 5.8 TB/s.
@@ -57,7 +60,7 @@ constexpr float LN2 = 0.6931471805599453f;
 // that what a token costs once (reductions, slots, addresses) is shared by the
 // tokens of a warp.  At E = 128 a warp a token took 346 instructions a token in
 // the forward (45 us for 131072 tokens) and 31.3 us in the backward; four tokens a
-// warp take 175 (37 us; 34 with merged lists) and 25 us.
+// warp take 175 (37 us; 35 with merged lists) and 25 us.
 template <int N>
 using Int = std::integral_constant<int, N>;
 
@@ -357,6 +360,28 @@ __device__ __forceinline__ void sort_top(uint32_t (&a)[N]) {
   }
 }
 
+// Whether no more than k of the token's logits come before or at the last slot's
+// (v, e): larger, or equal in an expert up to e.  Slots in order are then the k
+// largest.
+template <typename TL, int G, int C>
+__device__ __noinline__ bool is_last(const TL* row, int E, int k, int vec, float v, int e) {
+  const int q = threadIdx.x % G;
+  Pieces<TL, G, C> raw;
+  raw.clear();
+  raw.load(row, q, E, vec);
+  int n = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = raw.get(c, i);
+      n += x > v || (x == v && 4 * (q + G * c) + i <= e);
+    }
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n == k;
+}
+
 // The exact selection: k rounds over full keys, NaN below -inf, equal keys to
 // the lower expert.  Returns slot q's expert.
 template <typename TL, int G, int C>
@@ -626,6 +651,12 @@ __global__ void __launch_bounds__(rf_threads(C), 1) rf_rows(const TL* __restrict
     const uint32_t mine = sel[q];
     int e = min(static_cast<int>(LOW - (mine & LOW)), E - 1);
     float v = slot ? load_elem(row + e) : 0.f;
+    if constexpr (!is_bf16<TL>) {
+      if (__any_sync(0xffffffffu, crowded && here)) {
+        const int at = lane - q + k - 1;
+        crowded = !is_last<TL, G, C>(row, E, k, vec, __shfl_sync(0xffffffffu, v, at), __shfl_sync(0xffffffffu, e, at));
+      }
+    }
     bool unclear = here && (crowded || !(s > 0.f));
     if constexpr (!is_bf16<TL>) {
       const float vn = __shfl_down_sync(0xffffffffu, v, 1, G);
