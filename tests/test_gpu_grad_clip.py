@@ -299,6 +299,37 @@ def test_more_elements_than_32_bits():
     assert int((x == 0.125).sum()) == n - 1
 
 
+def test_two_lists_at_once():
+    # lists that each fill the GPU, clipped on two streams at the same time, beside other work on a third
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    ctx = L.lrm_create(0)
+    try:
+        grads = [_tensors([3_000_000 + 7 * i, 77], torch.float32, 30 + i) for i in range(2)]
+        outs = [[torch.empty_like(t) for t in g] for g in grads]
+        clips = [GradClip(g, o, ctx=ctx) for g, o in zip(grads, outs)]
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        work = torch.randn(2048, 2048, device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(60):
+            for c, s in zip(clips, streams):
+                c.clip(0.5, stream=s)
+            with torch.cuda.stream(streams[2]):
+                work = torch.tanh(work @ work)
+        torch.cuda.synchronize()
+        assert L.lrm_get_device_status(ctx) == 0
+        for g, o, c in zip(grads, outs, clips):
+            norm = math.sqrt(sum(float(t.double().square().sum()) for t in g))
+            assert abs(float(c.norm) - norm) <= REL * norm
+            for a, b in zip(g, o):
+                assert torch.equal(b, _expect(a, c.coef))
+        for c in clips:
+            c.close()
+    finally:
+        L.lrm_destroy(ctx)
+
+
 @pytest.mark.parametrize("n", [1 << 20, 50_000_000])
 def test_a_wait_that_runs_out_is_reported_and_the_list_stays_usable(n):
     # no time at all for the waits on copies and on the other blocks
