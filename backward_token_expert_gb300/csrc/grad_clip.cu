@@ -24,10 +24,12 @@
 // launch and latency.
 //
 // Squares: a lane's batch of values (32 fp32 or 64 bf16) is squared and summed
-// in fp32 while its largest magnitude lies in [2^-56, 2^55]: no sum of squares
+// in fp32 while its largest magnitude lies in [2^-56, 2^52]: no sum of squares
 // overflows, and a square that fp32 holds as a subnormal is off by at most
 // 2^-150, 2^-38 of the largest square.  Other batches are squared in fp64
-// (exact); batches of zeros add nothing.  Batches are added in fp64.
+// (exact); batches of zeros add nothing.  A lane's few batches in gc_small and
+// gc_hold and the sums of a block are added in fp32 too, the many batches of
+// gc_norm and the blocks' sums in fp64.
 #include <math.h>
 #include <stdlib.h>
 #include <string.h>
@@ -190,7 +192,7 @@ lrm_status check_tensors(const lrm_tensor* tensors, int32_t count) {
   return LRM_OK;
 }
 
-__device__ __forceinline__ bool in_fp32_range(float mx) { return mx >= 0x1p-56f && mx <= 0x1p55f; }
+__device__ __forceinline__ bool in_fp32_range(float mx) { return mx >= 0x1p-56f && mx <= 0x1p52f; }
 
 template <bool F32>
 __device__ __forceinline__ void unpack(const uint4& x, float (&v)[8]) {
@@ -221,9 +223,21 @@ __device__ __noinline__ double exact_squares(uint4 x) {
   return sum;
 }
 
-// Adds the squares of a lane's batch to sum; places beyond the chunk hold 0.
+// A lane's sum of squares: of batches that fp32 holds, and of the others.
+struct Squares {
+  float f;
+  double d;
+};
+
+__device__ __forceinline__ bool is_wide(const Squares& q) { return (__double2hiint(q.d) | __double2loint(q.d)) != 0; }
+__device__ __forceinline__ void add_to(double& sum, const Squares& q) {
+  sum += q.f;
+  if (is_wide(q)) sum += q.d;
+}
+
+// Adds the squares of a lane's batch; places beyond the chunk hold 0.
 template <bool F32>
-__device__ __forceinline__ void batch_squares(const uint4 (&x)[GC_BATCH], double& sum) {
+__device__ __forceinline__ void batch_squares(const uint4 (&x)[GC_BATCH], Squares& sum) {
   float mx = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < GC_BATCH; ++j) {
@@ -237,7 +251,7 @@ __device__ __forceinline__ void batch_squares(const uint4 (&x)[GC_BATCH], double
   }
   const float s = (a[0] + a[1]) + (a[2] + a[3]);
   if (in_fp32_range(mx)) {
-    sum += s;  // a NaN among the values is in s
+    sum.f += s;  // a NaN among the values is in s
   } else if (mx != 0.f || s != 0.f) {
 #pragma unroll 1
     for (int j = 0; j < GC_BATCH; ++j) {
@@ -245,9 +259,16 @@ __device__ __forceinline__ void batch_squares(const uint4 (&x)[GC_BATCH], double
 #pragma unroll
       for (int i = 1; i < GC_BATCH; ++i)
         if (i == j) y = x[i];
-      sum += exact_squares<F32>(y);
+      sum.d += exact_squares<F32>(y);
     }
   }
+}
+
+__device__ __forceinline__ void batch_squares(const uint4 (&x)[GC_BATCH], bool f32, Squares& sum) {
+  if (f32)
+    batch_squares<true>(x, sum);
+  else
+    batch_squares<false>(x, sum);
 }
 
 __device__ __forceinline__ uint4 ld_once(const uint4* p) {
@@ -297,13 +318,14 @@ __device__ __forceinline__ float any_load(const Chunk& c, int i) {
   return is_f32(c) ? static_cast<const float*>(c.src)[i]
                    : __bfloat162float(static_cast<const __nv_bfloat16*>(c.src)[i]);
 }
-__device__ __noinline__ double any_squares(const Chunk& c, int lane) {
-  double sum = 0.0;
-  for (int i = lane; i < c.n; i += 32) {
-    const float v = any_load(c, i);
-    sum += static_cast<double>(v) * v;
-  }
-  return sum;
+// (a chunk whose src is off the grid is shorter than a vector: a lane an element)
+__device__ __forceinline__ void any_squares(const Chunk& c, int lane, Squares& sum) {
+  const float v = lane < c.n ? any_load(c, lane) : 0.f;
+  if (v == 0.f) return;
+  if (in_fp32_range(fabsf(v)))
+    sum.f = fmaf(v, v, sum.f);
+  else
+    sum.d += static_cast<double>(v) * v;
 }
 __device__ __noinline__ void any_scale(const Chunk& c, float coef, int lane) {
   for (int i0 = lane; i0 < c.n; i0 += 32 * GC_BATCH) {
@@ -342,6 +364,31 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
+// A block's sum, for warp 0.  The common case leaves the fp64 unit alone.
+__device__ __forceinline__ double block_squares(const Squares& mine) {
+  __shared__ float s_f[32];
+  __shared__ double s_d[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float f = mine.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+  if (lane == 0) s_f[warp] = f;
+  const int any_wide = __syncthreads_or(is_wide(mine));
+  if (warp == 0) {
+    f = lane < static_cast<int>(blockDim.x >> 5) ? s_f[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+  }
+  double sum = f;
+  if (any_wide) {
+    const double d = warp_sum(mine.d);
+    if (lane == 0) s_d[warp] = d;
+    __syncthreads();
+    if (warp == 0) sum += warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? s_d[lane] : 0.0);
+  }
+  return sum;
+}
+
 __device__ __forceinline__ lrm_grad_stats make_stats(double squares, float max_norm) {
   lrm_grad_stats r;
   if (fits_f32(squares)) {
@@ -375,13 +422,14 @@ __global__ void __launch_bounds__(GC_THREADS, 2) gc_norm(const Chunk* __restrict
       for (int v0 = 0; v0 < nv; v0 += 32 * GC_BATCH) {
         uint4 x[GC_BATCH];
         load_batch(static_cast<const uint4*>(c.src), v0, nv, lane, x);
-        if (is_f32(c))
-          batch_squares<true>(x, sum);
-        else
-          batch_squares<false>(x, sum);
+        Squares q{0.f, 0.0};
+        batch_squares(x, is_f32(c), q);
+        add_to(sum, q);
       }
     } else {
-      sum += any_squares(c, lane);
+      Squares q{0.f, 0.0};
+      any_squares(c, lane, q);
+      add_to(sum, q);
     }
   }
   sum = warp_sum(sum);
@@ -459,7 +507,6 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
                                                         unsigned long long wait_ns, unsigned int* status) {
   extern __shared__ __align__(128) unsigned char gc_smem[];
   __shared__ uint64_t s_full[GC_WARPS][GC_HELD];
-  __shared__ double s_sum[GC_WARPS];
   __shared__ int s_late;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint4* held = reinterpret_cast<uint4*>(gc_smem + warp * (GC_HELD * GC_BATCH_BYTES));
@@ -488,7 +535,7 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
       bulk_load(held + j * HELD_VECS, kept[j].src, bytes, &full[j]);
     }
   }
-  double sum = 0.0;
+  Squares sum{0.f, 0.0};
 #pragma unroll
   for (int j = 0; j < GC_HELD; ++j) {
     const Chunk& c = kept[j];
@@ -502,22 +549,14 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
         const int v = lane + 32 * b;
         x[b] = v < nv ? held[j * HELD_VECS + v] : make_uint4(0u, 0u, 0u, 0u);
       }
-      if (is_f32(c))
-        batch_squares<true>(x, sum);
-      else
-        batch_squares<false>(x, sum);
+      batch_squares(x, is_f32(c), sum);
     } else {
-      sum += any_squares(c, lane);
+      any_squares(c, lane, sum);
     }
   }
-  sum = warp_sum(sum);
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  if (warp == 0) {
-    sum = warp_sum(lane < GC_WARPS ? s_sum[lane] : 0.0);
-    // a copy that did not come makes the norm NaN, so that no block scales by it
-    if (lane == 0) partial[blockIdx.x] = s_late ? __longlong_as_double(0x7ff8000000000000ll) : sum;
-  }
+  const double total = block_squares(sum);
+  // a copy that did not come makes the norm NaN, so that no block scales by it
+  if (threadIdx.x == 0) partial[blockIdx.x] = s_late ? __longlong_as_double(0x7ff8000000000000ll) : total;
   const bool met = grid_barrier(arrivals, wait_ns);
   if ((s_late || !met) && threadIdx.x == 0) raise_flag(status, LRM_ERR_TIMEOUT);
   if (s_late) {  // a late copy gets a last chance to land before the block ends
@@ -673,32 +712,23 @@ __global__ void __launch_bounds__(GC_RING_THREADS, 1) gc_ring(const Chunk* __res
 __global__ void __launch_bounds__(GC_SMALL_THREADS) gc_small(const Chunk* __restrict__ chunks, int count, int scale,
                                                              float max_norm, int in_place,
                                                              lrm_grad_stats* __restrict__ stats) {
-  __shared__ double s_sum[GC_SMALL_CHUNKS];
   __shared__ lrm_grad_stats s_stats;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Chunk c = {};
   if (warp < count) c = chunks[warp];
   const bool vec = warp < count && src_vec(c);
   uint4 x[GC_BATCH];
-  double sum = 0.0;
+  Squares sum{0.f, 0.0};
   if (vec) {
     load_batch(static_cast<const uint4*>(c.src), 0, vectors(c), lane, x);
-    if (is_f32(c))
-      batch_squares<true>(x, sum);
-    else
-      batch_squares<false>(x, sum);
+    batch_squares(x, is_f32(c), sum);
   } else if (warp < count) {
-    sum = any_squares(c, lane);
+    any_squares(c, lane, sum);
   }
-  sum = warp_sum(sum);
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  if (warp == 0) {
-    sum = warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? s_sum[lane] : 0.0);
-    if (lane == 0) {
-      s_stats = make_stats(sum, scale ? max_norm : INFINITY);
-      *stats = s_stats;
-    }
+  const double total = block_squares(sum);
+  if (threadIdx.x == 0) {
+    s_stats = make_stats(total, scale ? max_norm : INFINITY);
+    *stats = s_stats;
   }
   __syncthreads();
   const lrm_grad_stats r = s_stats;
