@@ -5,9 +5,9 @@
 // any size give the warps equal shares and a warp finds its work with one
 // 32-byte load.
 //
-//   gc_small   up to 64 KB: one block, a chunk a warp, held in registers between
-//              the norm and the scaling (60 KB 5.7 us against 6.1 by gc_hold, 2 KB
-//              4.0 against 5.5; 120 KB 7.0 against 6.3).
+//   gc_small   up to 512 KB: one cluster, a chunk a warp, held in registers
+//              between the norm and the scaling (2 KB 2.4 us, 160 KB 3.8 against
+//              5.6 by gc_hold, 500 KB 4.9 against 5.6).
 //   gc_hold    up to 24 MB: one launch, the chunks held in shared memory over a
 //              barrier of the grid.
 //   gc_norm    one warp per chunk; each block leaves its sum of squares (fp64).
@@ -20,8 +20,8 @@
 // Bound by memory: the norm has to be known before the first value is scaled, so
 // what neither the SMs nor the L2 hold is read twice.  2.4 GB of fp32: 1040 us,
 // the norm at 6.8 TB/s and the scaling at 7.0 (4.8 GB moved, some of it from L2);
-// 59 MB of bf16 in 400 tensors 31 us; 160 KB in six tensors 5.7 us, most of it
-// launch and latency.
+// 59 MB of bf16 in 400 tensors 31 us; 160 KB in six tensors 4 us, most of it launch
+// and latency.
 //
 // Squares: a lane's batch of values (32 fp32 or 64 bf16) is squared and summed
 // in fp32 while its largest magnitude lies in [2^-56, 2^52]: no sum of squares
@@ -63,9 +63,11 @@ constexpr int GC_HOLD_SMEM = GC_WARPS * GC_HELD * GC_BATCH_BYTES;
 constexpr int GC_SMS = 152;                                    // the shares of the warps are cut for this many SMs
 constexpr int64_t GC_HOLD_BYTES = int64_t{24} << 20;           // of 29 MB that GC_SMS blocks hold: chunks are not all full
 constexpr unsigned long long GC_DRAIN_NS = 1000000000ull;      // for copies under way after a wait ran out
-constexpr int GC_SMALL_THREADS = 1024;
-constexpr int GC_SMALL_CHUNKS = GC_SMALL_THREADS / 32;
-constexpr int64_t GC_SMALL_BYTES = 64 << 10;                   // a block's latency against a grid's launch and barrier
+constexpr int GC_SMALL_THREADS = 512;
+constexpr int GC_SMALL_WARPS = GC_SMALL_THREADS / 32;
+constexpr int GC_SMALL_CLUSTER = 8;
+constexpr int GC_SMALL_CHUNKS = GC_SMALL_WARPS * GC_SMALL_CLUSTER;
+constexpr int64_t GC_SMALL_BYTES = 512 << 10;                  // a cluster's latency against a grid's launch and barrier
 
 // A chunk's kind: its type and what of it lies on 16-byte boundaries.
 enum : int32_t { GC_BF16 = 1, GC_DST_ANY = 2, GC_SRC_ANY = 4 };
@@ -157,11 +159,11 @@ Plan plan_of(const lrm_tensor* tensors, int32_t count) {
   // bulk copies need both ends on the grid; what is not wants the warps of gc_clip (200 MB off it: 1460 us by
   // gc_ring's four warps an SM)
   if (bytes > GC_LARGE_BYTES && skew <= bytes / 16) return plan(GC_BY_RING, GC_RING_BYTES);
-  // the smallest chunks that give gc_small's warps no more than one each
+  // chunks for up to 32 warps of gc_small, or as many as it has
   if (bytes <= GC_SMALL_BYTES)
     for (int64_t b = 512; b <= GC_BATCH_BYTES; b *= 2) {
       const Plan p = plan(GC_BY_SMALL, b);
-      if (p.chunks <= GC_SMALL_CHUNKS) return p;
+      if (p.chunks <= (b < GC_BATCH_BYTES ? 32 : GC_SMALL_CHUNKS)) return p;
     }
   // up to a batch of a warp, cut so that the warps get equal numbers: of one block an SM, or of two
   const auto even = [&](int64_t warps) {
@@ -707,35 +709,49 @@ __global__ void __launch_bounds__(GC_RING_THREADS, 1) gc_ring(const Chunk* __res
   if (lane == 0) bulk_wait<0>();
 }
 
-// One block, a chunk a warp, the values in registers between the norm and the
-// scaling.  scale = 0: the norm alone.
+// One cluster, a chunk a warp, the values in registers between the norm and the
+// scaling; every block gets the other blocks' sums.  scale = 0: the norm alone.
 __global__ void __launch_bounds__(GC_SMALL_THREADS) gc_small(const Chunk* __restrict__ chunks, int count, int scale,
                                                              float max_norm, int in_place,
                                                              lrm_grad_stats* __restrict__ stats) {
+  __shared__ double s_rank[GC_SMALL_CLUSTER];
   __shared__ lrm_grad_stats s_stats;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank()), ranks = static_cast<int>(gridDim.x);
+  const int i = rank * static_cast<int>(blockDim.x >> 5) + warp;
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this block has started
   Chunk c = {};
-  if (warp < count) c = chunks[warp];
-  const bool vec = warp < count && src_vec(c);
+  if (i < count) c = chunks[i];
+  const bool vec = i < count && src_vec(c);
   uint4 x[GC_BATCH];
   Squares sum{0.f, 0.0};
   if (vec) {
     load_batch(static_cast<const uint4*>(c.src), 0, vectors(c), lane, x);
     batch_squares(x, is_f32(c), sum);
-  } else if (warp < count) {
+  } else if (i < count) {
     any_squares(c, lane, sum);
   }
-  const double total = block_squares(sum);
+  double total = block_squares(sum);
+  if (ranks > 1) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (warp == 0 && lane < ranks)
+      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa_shared(&s_rank[rank], lane)), "d"(total) : "memory");
+    cluster_sync_all();
+  }
   if (threadIdx.x == 0) {
+    if (ranks > 1) {
+      total = 0.0;
+      for (int r = 0; r < ranks; ++r) total += s_rank[r];
+    }
     s_stats = make_stats(total, scale ? max_norm : INFINITY);
-    *stats = s_stats;
+    if (rank == 0) *stats = s_stats;
   }
   __syncthreads();
   const lrm_grad_stats r = s_stats;
   if (!scale || (in_place && r.coef == 1.f)) return;
   if (vec && both_vec(c))
     store_batch(static_cast<uint4*>(c.dst), 0, vectors(c), lane, x, is_f32(c), r.coef);
-  else if (warp < count)
+  else if (i < count)
     any_scale(c, r.coef, lane);
 }
 
@@ -744,10 +760,26 @@ const Chunk* chunks_of(const lrm_grad_list* list) {
 }
 
 lrm_status launch_small(const lrm_grad_list* list, int scale, float max_norm, lrm_grad_stats* stats, cudaStream_t s) {
-  const int warps = list->chunks > 0 ? static_cast<int>(list->chunks) : 1;
-  gc_small<<<1, 32 * warps, 0, s>>>(chunks_of(list), static_cast<int>(list->chunks), scale, max_norm, list->in_place,
-                                    stats);
-  return launch_status();
+  const int count = static_cast<int>(list->chunks);
+  int ranks = (count + 7) / 8;  // eight warps a block, more once there are eight blocks
+  ranks = ranks < 1 ? 1 : ranks < GC_SMALL_CLUSTER ? ranks : GC_SMALL_CLUSTER;
+  const int warps = count > 0 ? (count + ranks - 1) / ranks : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ranks);
+  cfg.blockDim = dim3(32 * warps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ranks;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = ranks > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, gc_small, chunks_of(list), count, scale, max_norm, list->in_place, stats) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return LRM_ERR_CUDA;
+  }
+  return LRM_OK;
 }
 
 // scale = 0: the norm alone.
