@@ -51,7 +51,7 @@ constexpr int RF_ONE_BLOCK_PASSES = 2;  // batches of up to this many passes of 
 // k = 4 31.2 / 33.2, k = 8 37.4 / 34.3).
 constexpr int RF_ROUNDS = 4;
 constexpr int RS_SUM_THREADS = 1024;
-constexpr int RB_THREADS = 128;  // 131072 x 128 fp32: 25.3 us, blocks of 256 26.5, of 512 27.2
+constexpr int RB_THREADS = 128;  // 131072 x 128 fp32: 24.8 us; measured when it was 25.3: blocks of 256 26.5, of 512 27.2
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -775,20 +775,6 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
   float4* own = s_add[warp] + (lane - q) * C + q;  // the group's row, at the lane's first piece
   float* add = reinterpret_cast<float*>(s_add[warp] + (lane - q) * C);
   uint8_t* slot_of = s_slot[warp] + (lane - q) * C * 4;
-#pragma unroll
-  for (int c = 0; c < C; ++c) own[c * G] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float tc = static_cast<float>(max(1, a.losses->tokens));
-  const float ca = a.aux_coef * static_cast<float>(E) / tc, cz = 2.f * a.z_coef / tc;
-  float cf[C][4];
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = 4 * (q + G * c) + i;
-      cf[c][i] = e < E ? ca * a.f[e] : 0.f;
-    }
-  __syncwarp();
-
   const bool gates = a.dgate != nullptr;
   const long long step = static_cast<long long>(gridDim.x) * NW * PER_WARP;
   long long t = (static_cast<long long>(blockIdx.x) * NW + warp) * PER_WARP + lane / G;
@@ -811,7 +797,21 @@ __global__ void __launch_bounds__(RB_THREADS) rb_rows(const TL* __restrict__ log
   next.ms = make_float2(0.f, 0.f);
   next.id = -1;
   next.dg = next.al = 0.f;
-  load(next, t);
+  load(next, t);  // before the rest of the set-up, which it hides: 32768 x 128 fp32 8.7 -> 8.2 us
+#pragma unroll
+  for (int c = 0; c < C; ++c) own[c * G] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float tc = static_cast<float>(max(1, a.losses->tokens));
+  const float ca = a.aux_coef * static_cast<float>(E) / tc, cz = 2.f * a.z_coef / tc;
+  float cf[C][4];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * (q + G * c) + i;
+      cf[c][i] = e < E ? ca * a.f[e] : 0.f;
+    }
+  __syncwarp();
+
   for (; t - lane / G < T; t += step) {
     const TokenIn<TL, G, C> x = next;
     load(next, t + step);
