@@ -76,6 +76,25 @@ def test_sizes(sizes, dtype):
     check(grads, 2.0 * full)
 
 
+# one cluster takes up to 128 chunks: blocks that fill unevenly, the last chunk short, and one chunk more
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("count", [8, 9, 15, 17, 32, 33, 57, 63, 65, 121, 127, 128, 129])
+@pytest.mark.parametrize("each", [1, 37, 128])
+def test_chunks_of_a_cluster(count, each, dtype):
+    grads = _tensors([each] * (count - 1) + [1], dtype, count)
+    full = math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+    check(grads, 0.5 * full)
+    check(grads, 0.5 * full, in_place=True)
+
+
+@pytest.mark.parametrize("words", [32 * 1024 - 4, 32 * 1024, 32 * 1024 + 4, 128 * 1024 - 1, 128 * 1024, 128 * 1024 + 1])
+def test_sizes_around_a_cluster(words):
+    grads = _tensors([words], torch.float32, words)
+    full = math.sqrt(float(grads[0].double().square().sum()))
+    check(grads, 0.5 * full)
+    check(grads, 2.0 * full)
+
+
 def test_mixed_types_in_place():
     grads = _tensors([1000, 33], torch.float32, 1) + _tensors([70001, 3], torch.bfloat16, 2)
     check(grads, 0.1, in_place=True)
