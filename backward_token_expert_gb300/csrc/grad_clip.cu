@@ -406,11 +406,14 @@ __device__ __forceinline__ lrm_grad_stats make_stats(double squares, float max_n
   return r;
 }
 
+// cleared: the stats that gc_ring's blocks write together, or null.
 __global__ void __launch_bounds__(GC_THREADS, 2) gc_norm(const Chunk* __restrict__ chunks, long long count,
-                                                      double* __restrict__ partial) {
+                                                      double* __restrict__ partial,
+                                                      lrm_grad_stats* __restrict__ cleared) {
   __shared__ double s_sum[GC_WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dependency_launch();
+  if (cleared != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *cleared = lrm_grad_stats{0.f, 1.f, 0};
   const long long step = static_cast<long long>(gridDim.x) * GC_WARPS;
   long long i = static_cast<long long>(blockIdx.x) * GC_WARPS + warp;
   double sum = 0.0;
@@ -473,25 +476,47 @@ __global__ void __launch_bounds__(GC_THREADS) gc_stats(const double* __restrict_
 // Every block of the launch arrives once and waits for the others (all are
 // resident: the launch is cooperative).  The arrivals are never reset, so that a
 // call needs nothing cleared before it: they are a multiple of the grid between
-// calls.  False when the wait ran out.
-__device__ bool grid_barrier(unsigned long long* arrivals, unsigned long long wait_ns) {
+// calls.
+//
+// All blocks return the same: true once all have arrived, or false if one gave
+// up before that.  A block gives up by setting the call's bit in the word that
+// counts the arrivals, and only while the count is short, so whoever sees all
+// arrivals sees the bit as well.  `late` blocks give up before they arrive, and
+// so do those that are given no time while there are others to wait for.  The
+// calls of a list take the two bits in turn; the first to arrive clears the
+// other one, which only the call before used.
+constexpr unsigned long long GC_COUNT = (1ull << 62) - 1;
+__device__ __forceinline__ unsigned long long ld_acquire(const unsigned long long* p) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned long long given_up_bit(unsigned long long call) { return 1ull << (62 + (call & 1)); }
+__device__ bool grid_barrier(unsigned long long* arrivals, bool late, unsigned long long wait_ns) {
   __shared__ int s_ok;
   __syncthreads();
   if (threadIdx.x == 0) {
+    // this block's arrival is missing, so the count is still that of this call
+    if (late || (wait_ns == 0 && gridDim.x > 1))
+      atomicOr(arrivals, given_up_bit((ld_acquire(arrivals) & GC_COUNT) / gridDim.x));
     __threadfence();
-    const unsigned long long mine = atomicAdd(arrivals, 1ull), want = (mine / gridDim.x + 1) * gridDim.x;
+    const unsigned long long mine = atomicAdd(arrivals, 1ull), call = (mine & GC_COUNT) / gridDim.x;
+    const unsigned long long want = (call + 1) * gridDim.x, bit = given_up_bit(call), old_bit = given_up_bit(call + 1);
+    if ((mine & old_bit) != 0 && (mine & GC_COUNT) == call * gridDim.x) atomicAnd(arrivals, ~old_bit);
     const uint64_t t0 = globaltimer_ns();
-    int ok = 1;
     for (uint32_t it = 1;; ++it) {
-      unsigned long long now;
-      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(now) : "l"(arrivals) : "memory");
-      if (now >= want) break;
-      if ((it & 15u) == 0 && globaltimer_ns() - t0 > wait_ns) {
-        ok = 0;
+      const unsigned long long now = ld_acquire(arrivals);
+      if ((now & bit) != 0) {
+        s_ok = 0;
         break;
       }
+      if ((now & GC_COUNT) >= want) {
+        s_ok = 1;
+        break;
+      }
+      // fails where another block came in between, at most a grid's number of times; looked at again in both cases
+      if ((it & 15u) == 0 && globaltimer_ns() - t0 > wait_ns) atomicCAS(arrivals, now, now | bit);
     }
-    s_ok = ok;
   }
   __syncthreads();
   return s_ok != 0;
@@ -557,17 +582,20 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
     }
   }
   const double total = block_squares(sum);
-  // a copy that did not come makes the norm NaN, so that no block scales by it
-  if (threadIdx.x == 0) partial[blockIdx.x] = s_late ? __longlong_as_double(0x7ff8000000000000ll) : total;
-  const bool met = grid_barrier(arrivals, wait_ns);
-  if ((s_late || !met) && threadIdx.x == 0) raise_flag(status, LRM_ERR_TIMEOUT);
-  if (s_late) {  // a late copy gets a last chance to land before the block ends
+  if (threadIdx.x == 0) partial[blockIdx.x] = total;
+  if (!grid_barrier(arrivals, s_late != 0, wait_ns)) {  // in every block: none of them scales
+    if (threadIdx.x == 0) {
+      raise_flag(status, LRM_ERR_TIMEOUT);
+      if (blockIdx.x == 0) *stats = lrm_grad_stats{nanf(""), 1.f, 1};
+    }
+    if (s_late) {  // a late copy gets a last chance to land before the block ends
 #pragma unroll
-    for (int j = 0; j < GC_HELD; ++j)
-      if (kept[j].n > 0 && src_vec(kept[j])) mbar_wait(&full[j], 0, GC_DRAIN_NS, nullptr);
+      for (int j = 0; j < GC_HELD; ++j)
+        if (kept[j].n > 0 && src_vec(kept[j])) mbar_wait(&full[j], 0, GC_DRAIN_NS, nullptr);
+    }
     return;
   }
-  if (!met || (!scale && blockIdx.x != 0)) return;
+  if (!scale && blockIdx.x != 0) return;
   const lrm_grad_stats r = block_stats(partial, gridDim.x, scale ? max_norm : INFINITY);
   if (blockIdx.x == 0 && threadIdx.x == 0) *stats = r;
   if (!scale || (in_place && r.coef == 1.f)) return;
@@ -621,6 +649,14 @@ __global__ void __launch_bounds__(GC_THREADS) gc_clip(const Chunk* __restrict__ 
   }
 }
 
+// The stats that gc_norm cleared are written by block 0 of gc_ring and, where a
+// copy does not come, by that copy's warp, in any order: a norm's bits grow with it
+// and NaN's are above them all, so the maximum stands for both.
+__device__ __forceinline__ void merge_stats(lrm_grad_stats* stats, float norm, int nonfinite) {
+  atomicMax(reinterpret_cast<unsigned int*>(&stats->norm), __float_as_uint(norm));
+  atomicOr(&stats->nonfinite, nonfinite);
+}
+
 // The scaling of lists beyond the L2.  A warp's ring: its chunks come by bulk
 // copies GC_STAGES ahead, are scaled in shared memory and leave by bulk copies,
 // so that DRAM sees runs of 16 KB each way (2.4 GB of fp32, norm and scaling:
@@ -660,7 +696,10 @@ __global__ void __launch_bounds__(GC_RING_THREADS, 1) gc_ring(const Chunk* __res
   for (int j = 0; j < GC_STAGES; ++j) fetch(j, first - j * step);
   grid_dependency_wait();
   const lrm_grad_stats r = block_stats(partial, nblk, max_norm);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *stats = r;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    stats->coef = r.coef;
+    merge_stats(stats, r.norm, r.nonfinite);
+  }
   const bool scale = !(in_place && r.coef == 1.f);
   uint32_t phases = 0;  // bit j: the parity that stage j's next copy completes
   bool ok = true;
@@ -701,7 +740,10 @@ __global__ void __launch_bounds__(GC_RING_THREADS, 1) gc_ring(const Chunk* __res
     }
     if (!scale) break;
   }
-  if (!ok && lane == 0) raise_flag(status, LRM_ERR_TIMEOUT);
+  if (!ok && lane == 0) {
+    raise_flag(status, LRM_ERR_TIMEOUT);
+    merge_stats(stats, nanf(""), 1);
+  }
   // copies still under way (after a wait that ran out) get a last chance to land
 #pragma unroll
   for (int j = 0; j < GC_STAGES; ++j)
@@ -805,9 +847,10 @@ lrm_status launch_hold(lrm_ctx* ctx, const lrm_grad_list* list, int scale, float
   return LRM_OK;
 }
 
-lrm_status launch_norm(const lrm_grad_list* list, cudaStream_t s) {
+lrm_status launch_norm(const lrm_grad_list* list, lrm_grad_stats* cleared, cudaStream_t s) {
   if (list->chunks == 0) return LRM_OK;
-  gc_norm<<<list->grid_norm, GC_THREADS, 0, s>>>(chunks_of(list), list->chunks, static_cast<double*>(list->table));
+  gc_norm<<<list->grid_norm, GC_THREADS, 0, s>>>(chunks_of(list), list->chunks, static_cast<double*>(list->table),
+                                                 cleared);
   return launch_status();
 }
 
@@ -917,7 +960,7 @@ extern "C" lrm_status lrm_grad_norm(lrm_ctx* ctx, const lrm_grad_list* list, lrm
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (list->by == GC_BY_SMALL) return launch_small(list, 0, 0.f, stats, s);
   if (list->by == GC_BY_HOLD) return launch_hold(ctx, list, 0, 0.f, stats, s);
-  const lrm_status st = launch_norm(list, s);
+  const lrm_status st = launch_norm(list, nullptr, s);
   if (st != LRM_OK) return st;
   return launch_dependent(gc_stats, 1, GC_THREADS, 0, 1, s, static_cast<const double*>(list->table), list->grid_norm,
                           stats);
@@ -934,7 +977,7 @@ extern "C" lrm_status lrm_grad_clip(lrm_ctx* ctx, const lrm_grad_list* list, flo
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (list->by == GC_BY_SMALL) return launch_small(list, 1, max_norm, stats, s);
   if (list->by == GC_BY_HOLD) return launch_hold(ctx, list, 1, max_norm, stats, s);
-  const lrm_status st = launch_norm(list, s);
+  const lrm_status st = launch_norm(list, list->by == GC_BY_RING ? stats : nullptr, s);
   if (st != LRM_OK) return st;
   const Chunk* chunks = chunks_of(list);
   const double* partial = static_cast<const double*>(list->table);

@@ -485,8 +485,12 @@ LRM_API lrm_status lrm_router_backward(lrm_ctx* ctx, const void* logits, int32_t
  * the order is fixed, so the same inputs give the same bits.  Calls on one
  * list share its table: serialise them.  Lists up to 24 MB run as one cooperative
  * launch, whose blocks wait for one another; that wait and those on copies are
- * bounded (lrm_set_wait_budget): one that runs out sets LRM_ERR_TIMEOUT, the
- * outputs are then incomplete, and the list stays usable.
+ * bounded (lrm_set_wait_budget).  One that runs out sets LRM_ERR_TIMEOUT and
+ * leaves norm = NaN and nonfinite = 1, so that a caller who skips such a step
+ * skips this one, and the list stays usable (with a budget of 0 the blocks of
+ * one launch never wait for one another, so it always runs out).  Lists up to 24 MB are then left
+ * alone (coef = 1, no dst written); of longer ones, whose copies run while they
+ * are scaled, some values may have been written times the coef that stats holds.
  */
 typedef struct lrm_tensor {
   const void* src;

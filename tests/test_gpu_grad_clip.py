@@ -385,3 +385,61 @@ def test_large_tensor():
     c.clip(1.0)
     assert abs(float(c.norm.item()) - 0.5 * math.sqrt(n)) <= REL * 0.5 * math.sqrt(n)
     assert torch.all(x == 0.5 * c.coef)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_no_time_for_the_other_blocks_writes_nothing_and_says_so(in_place):
+    # no time at all: no block can wait for the others, so the wait runs out in every call
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    ctx = L.lrm_create(0)
+    try:
+        x = torch.linspace(-1.0, 1.0, 1 << 20, device="cuda")
+        kept, norm = x.clone(), math.sqrt(float(x.double().square().sum()))
+        out = x if in_place else torch.full_like(x, 7.0)
+        before = out.clone()
+        c = GradClip([x], None if in_place else [out], ctx=ctx)
+        for calls in (1, 2, 3):  # an odd and an even number of calls in a row that gave up
+            c.clip(2.0 * norm)
+            assert abs(float(c.norm) - norm) <= REL * norm and int(c.nonfinite) == 0
+            out.copy_(before)
+            L.lrm_set_wait_budget(ctx, 0)
+            for i in range(calls):
+                c.clip(0.25 * norm) if i != 1 else c.measure()
+                assert L.lrm_get_device_status(ctx) == 1 << L.LRM_ERR_TIMEOUT
+                assert math.isnan(float(c.norm)) and float(c.coef) == 1.0 and int(c.nonfinite) == 1
+                assert torch.equal(out, before) and torch.equal(x, kept)
+            L.lrm_set_wait_budget(ctx, 2_000_000_000)
+        c.clip(0.25 * norm)
+        assert L.lrm_get_device_status(ctx) == 0 and int(c.nonfinite) == 0
+        assert abs(float(c.norm) - norm) <= REL * norm and torch.equal(out, kept * c.coef)
+        c.close()
+    finally:
+        L.lrm_destroy(ctx)
+
+
+def test_a_long_list_whose_copies_ran_out_of_time_says_so():
+    # beyond 128 MB: the copies may come in time all the same, and then everything is written
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    ctx = L.lrm_create(0)
+    try:
+        x = torch.full((50_000_000,), 0.5, device="cuda")
+        out, norm = torch.empty_like(x), 0.5 * math.sqrt(50_000_000)
+        c = GradClip([x], [out], ctx=ctx)
+        L.lrm_set_wait_budget(ctx, 0)
+        for _ in range(5):
+            out.zero_()
+            c.clip(1.0)
+            late = L.lrm_get_device_status(ctx)
+            assert late in (0, 1 << L.LRM_ERR_TIMEOUT)
+            assert int(c.nonfinite) == (1 if late else 0)
+            if late:
+                assert math.isnan(float(c.norm)) and bool(((out == 0) | (out == x * c.coef)).all())
+            else:
+                assert abs(float(c.norm) - norm) <= REL * norm and torch.equal(out, x * c.coef)
+        c.close()
+    finally:
+        L.lrm_destroy(ctx)
