@@ -80,8 +80,10 @@ struct __align__(32) Chunk {
   int64_t pad;
 };
 
-// The table's head: the blocks' sums, then the arrivals at gc_hold's barrier (zero when the list is made).
+// The table's head: the blocks' sums, then the arrivals at gc_hold's barrier and the list's status word (zero
+// when the list is made).
 constexpr size_t GC_ARRIVALS_OFF = GC_MAX_GRID * sizeof(double);
+constexpr size_t GC_STATUS_OFF = GC_ARRIVALS_OFF + 128;
 constexpr size_t GC_SCRATCH_BYTES = GC_ARRIVALS_OFF + 256;
 
 // The chunks of a list, in order: sink(chunk) for each.  Tensors whose src
@@ -473,6 +475,12 @@ __global__ void __launch_bounds__(GC_THREADS) gc_stats(const double* __restrict_
   if (threadIdx.x == 0) *stats = r;
 }
 
+// In the context's word and in the list's own: lists may share a context.
+__device__ __forceinline__ void raise_timeout(unsigned int* status, unsigned int* own_status) {
+  raise_flag(status, LRM_ERR_TIMEOUT);
+  raise_flag(own_status, LRM_ERR_TIMEOUT);
+}
+
 // Every block of the launch arrives once and waits for the others (all are
 // resident: the launch is cooperative).  The arrivals are never reset, so that a
 // call needs nothing cleared before it: they are a multiple of the grid between
@@ -531,7 +539,8 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
                                                         double* __restrict__ partial, unsigned long long* arrivals,
                                                         int scale, float max_norm, int in_place,
                                                         lrm_grad_stats* __restrict__ stats,
-                                                        unsigned long long wait_ns, unsigned int* status) {
+                                                        unsigned long long wait_ns, unsigned int* status,
+                                                        unsigned int* own_status) {
   extern __shared__ __align__(128) unsigned char gc_smem[];
   __shared__ uint64_t s_full[GC_WARPS][GC_HELD];
   __shared__ int s_late;
@@ -585,7 +594,7 @@ __global__ void __launch_bounds__(GC_THREADS, 1) gc_hold(const Chunk* __restrict
   if (threadIdx.x == 0) partial[blockIdx.x] = total;
   if (!grid_barrier(arrivals, s_late != 0, wait_ns)) {  // in every block: none of them scales
     if (threadIdx.x == 0) {
-      raise_flag(status, LRM_ERR_TIMEOUT);
+      raise_timeout(status, own_status);
       if (blockIdx.x == 0) *stats = lrm_grad_stats{nanf(""), 1.f, 1};
     }
     if (s_late) {  // a late copy gets a last chance to land before the block ends
@@ -667,7 +676,8 @@ __global__ void __launch_bounds__(GC_RING_THREADS, 1) gc_ring(const Chunk* __res
                                                              const double* __restrict__ partial, int nblk,
                                                              float max_norm, int in_place,
                                                              lrm_grad_stats* __restrict__ stats,
-                                                             unsigned long long wait_ns, unsigned int* status) {
+                                                             unsigned long long wait_ns, unsigned int* status,
+                                                             unsigned int* own_status) {
   extern __shared__ __align__(128) unsigned char gc_smem[];
   __shared__ uint64_t s_full[GC_RING_WARPS][GC_STAGES];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -741,7 +751,7 @@ __global__ void __launch_bounds__(GC_RING_THREADS, 1) gc_ring(const Chunk* __res
     if (!scale) break;
   }
   if (!ok && lane == 0) {
-    raise_flag(status, LRM_ERR_TIMEOUT);
+    raise_timeout(status, own_status);
     merge_stats(stats, nanf(""), 1);
   }
   // copies still under way (after a wait that ran out) get a last chance to land
@@ -801,6 +811,10 @@ const Chunk* chunks_of(const lrm_grad_list* list) {
   return reinterpret_cast<const Chunk*>(static_cast<char*>(list->table) + GC_SCRATCH_BYTES);
 }
 
+unsigned int* status_of(const lrm_grad_list* list) {
+  return reinterpret_cast<unsigned int*>(static_cast<char*>(list->table) + GC_STATUS_OFF);
+}
+
 lrm_status launch_small(const lrm_grad_list* list, int scale, float max_norm, lrm_grad_stats* stats, cudaStream_t s) {
   const int count = static_cast<int>(list->chunks);
   int ranks = (count + 7) / 8;  // eight warps a block, more once there are eight blocks
@@ -840,7 +854,8 @@ lrm_status launch_hold(lrm_ctx* ctx, const lrm_grad_list* list, int scale, float
   unsigned long long* arrivals =
       reinterpret_cast<unsigned long long*>(static_cast<char*>(list->table) + GC_ARRIVALS_OFF);
   if (cudaLaunchKernelEx(&cfg, gc_hold, chunks_of(list), list->chunks, static_cast<double*>(list->table), arrivals,
-                         scale, max_norm, list->in_place, stats, ctx->wait_budget_ns, ctx->d_status) != cudaSuccess) {
+                         scale, max_norm, list->in_place, stats, ctx->wait_budget_ns, ctx->d_status,
+                         status_of(list)) != cudaSuccess) {
     cudaGetLastError();
     return LRM_ERR_CUDA;
   }
@@ -952,6 +967,24 @@ extern "C" lrm_status lrm_grad_list_destroy(lrm_grad_list* list) {
   return LRM_OK;
 }
 
+extern "C" lrm_status lrm_grad_list_status(lrm_ctx* ctx, const lrm_grad_list* list, void* stream, uint32_t* flags) {
+  if (ctx == nullptr || list == nullptr || flags == nullptr || list->device != ctx->device) return LRM_ERR_INVALID_ARG;
+  *flags = 0;
+  if (list->chunks == 0) return LRM_OK;  // its table was not written, and nothing of it can fail
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return LRM_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  unsigned int host = 0;
+  LRM_CHECK_CUDA(cudaMemcpyAsync(&host, status_of(list), sizeof(host), cudaMemcpyDeviceToHost, s));
+  LRM_CHECK_CUDA(cudaStreamSynchronize(s));
+  if (host != 0) {
+    LRM_CHECK_CUDA(cudaMemsetAsync(status_of(list), 0, sizeof(host), s));
+    LRM_CHECK_CUDA(cudaStreamSynchronize(s));
+  }
+  *flags = host;
+  return LRM_OK;
+}
+
 extern "C" lrm_status lrm_grad_norm(lrm_ctx* ctx, const lrm_grad_list* list, lrm_grad_stats* stats, void* stream) {
   if (ctx == nullptr || list == nullptr || stats == nullptr || list->device != ctx->device) return LRM_ERR_INVALID_ARG;
   if (!aligned(stats, 4)) return LRM_ERR_ALIGN;
@@ -983,7 +1016,8 @@ extern "C" lrm_status lrm_grad_clip(lrm_ctx* ctx, const lrm_grad_list* list, flo
   const double* partial = static_cast<const double*>(list->table);
   if (list->by == GC_BY_RING)
     return launch_dependent(gc_ring, list->grid_clip, GC_RING_THREADS, GC_RING_SMEM, 1, s, chunks, list->chunks, partial,
-                            list->grid_norm, max_norm, list->in_place, stats, ctx->wait_budget_ns, ctx->d_status);
+                            list->grid_norm, max_norm, list->in_place, stats, ctx->wait_budget_ns, ctx->d_status,
+                            status_of(list));
   return launch_dependent(gc_clip, list->grid_clip, GC_THREADS, 0, 1, s, chunks, list->chunks, partial,
                           list->grid_norm, max_norm, list->in_place, stats);
 }

@@ -71,6 +71,7 @@ EXPORTED = (
     "lrm_grad_table_size",
     "lrm_grad_list_create",
     "lrm_grad_list_destroy",
+    "lrm_grad_list_status",
     "lrm_grad_norm",
     "lrm_grad_clip",
 )
@@ -177,6 +178,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lrm_grad_table_size": ([ctypes.POINTER(Tensor), i32, ctypes.POINTER(size)], st),
         "lrm_grad_list_create": ([P, ctypes.POINTER(Tensor), i32, P, size, P, ctypes.POINTER(P)], st),
         "lrm_grad_list_destroy": ([P], st),
+        "lrm_grad_list_status": ([P, P, P, ctypes.POINTER(ctypes.c_uint32)], st),
         "lrm_grad_norm": ([P, P, P, P], st),
         "lrm_grad_clip": ([P, P, f32, P, P], st),
     })
@@ -417,6 +419,13 @@ def lrm_grad_list_create(ctx, tensors, count: int, table, table_bytes: int, stre
 
 def lrm_grad_list_destroy(grad_list: int) -> None:
     _check(load_library().lrm_grad_list_destroy(grad_list), "lrm_grad_list_destroy")
+
+
+def lrm_grad_list_status(ctx, grad_list: int, stream=None) -> int:
+    out = ctypes.c_uint32()
+    _check(load_library().lrm_grad_list_status(ctx, grad_list, _stream(stream), ctypes.byref(out)),
+           "lrm_grad_list_status")
+    return out.value
 
 
 def lrm_grad_norm(ctx, grad_list: int, stats, stream=None) -> None:

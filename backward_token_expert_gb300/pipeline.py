@@ -386,6 +386,9 @@ class Router:
                               self.z_coef, self.dlogits, _DTYPES[self.dlogits_dtype], stream)
         return self.dlogits
 
+    def device_status(self, stream=None) -> int:
+        return L.lrm_get_device_status(self.ctx, stream)
+
 
 def _dense(t) -> bool:
     """Whether the tensor's elements fill its memory range, in any dimension order."""
@@ -401,8 +404,8 @@ _clip_contexts: dict[int, int] = {}
 
 
 def _clip_context(device: int) -> int:
-    """The context of a device's clips that were given none (they raise no
-    device status, so they can share one)."""
+    """The context of a device's clips that were given none.  They can share
+    one: a list has a status word of its own."""
     if device not in _clip_contexts:
         _clip_contexts[device] = L.lrm_create(device)
     return _clip_contexts[device]
@@ -415,7 +418,8 @@ class GradClip:
     any shape and dimension order, but dense: their elements fill their memory
     range; an output has its gradient's type, shape and strides.  The result's
     ``norm``, ``coef`` (fp32 [1]) and ``nonfinite`` (int32 [1]) stay on the
-    device."""
+    device; ``nonfinite`` is not 0 for a step to skip: an element was infinite
+    or NaN, or a bounded wait ran out (``device_status``)."""
 
     def __init__(self, grads, outs=None, ctx=None, stream=None):
         grads = list(grads)
@@ -480,6 +484,10 @@ class GradClip:
     def clip(self, max_norm: float, stream=None) -> None:
         """norm, and every gradient times min(1, max_norm / norm) into its output."""
         L.lrm_grad_clip(self.ctx, self.list, max_norm, self._stats, stream)
+
+    def device_status(self, stream=None) -> int:
+        """Flags (1 << code) that calls on this list raised on the device since the last read."""
+        return L.lrm_grad_list_status(self.ctx, self.list, stream)
 
 
 class TrainingStep:

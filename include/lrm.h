@@ -485,12 +485,15 @@ LRM_API lrm_status lrm_router_backward(lrm_ctx* ctx, const void* logits, int32_t
  * the order is fixed, so the same inputs give the same bits.  Calls on one
  * list share its table: serialise them.  Lists up to 24 MB run as one cooperative
  * launch, whose blocks wait for one another; that wait and those on copies are
- * bounded (lrm_set_wait_budget).  One that runs out sets LRM_ERR_TIMEOUT and
+ * bounded (lrm_set_wait_budget).  One that runs out sets LRM_ERR_TIMEOUT, in the
+ * context's status word and in the list's own, and
  * leaves norm = NaN and nonfinite = 1, so that a caller who skips such a step
  * skips this one, and the list stays usable (with a budget of 0 the blocks of
  * one launch never wait for one another, so it always runs out).  Lists up to 24 MB are then left
  * alone (coef = 1, no dst written); of longer ones, whose copies run while they
  * are scaled, some values may have been written times the coef that stats holds.
+ * lrm_grad_list_status synchronises `stream`, returns the list's word in *flags and
+ * clears it, as lrm_get_device_status does with the context's.
  */
 typedef struct lrm_tensor {
   const void* src;
@@ -507,6 +510,7 @@ LRM_API lrm_status lrm_grad_table_size(const lrm_tensor* tensors, int32_t count,
 LRM_API lrm_status lrm_grad_list_create(lrm_ctx* ctx, const lrm_tensor* tensors, int32_t count, void* table,
                                         size_t table_bytes, void* stream, lrm_grad_list** out);
 LRM_API lrm_status lrm_grad_list_destroy(lrm_grad_list* list);
+LRM_API lrm_status lrm_grad_list_status(lrm_ctx* ctx, const lrm_grad_list* list, void* stream, uint32_t* flags);
 LRM_API lrm_status lrm_grad_norm(lrm_ctx* ctx, const lrm_grad_list* list, lrm_grad_stats* stats, void* stream);
 LRM_API lrm_status lrm_grad_clip(lrm_ctx* ctx, const lrm_grad_list* list, float max_norm, lrm_grad_stats* stats,
                                  void* stream);

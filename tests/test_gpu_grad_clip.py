@@ -443,3 +443,38 @@ def test_a_long_list_whose_copies_ran_out_of_time_says_so():
         c.close()
     finally:
         L.lrm_destroy(ctx)
+
+
+def test_lists_without_a_context_report_their_own_timeouts():
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    x = torch.full((1 << 20,), 0.5, device="cuda")
+    late, other, short, empty = (GradClip([t]) for t in (x, x.clone(), x[:100].clone(), x[:0]))
+    assert [c.device_status() for c in (late, other, short, empty)] == [0] * 4
+    L.lrm_set_wait_budget(late.ctx, 0)  # their common context's
+    try:
+        late.clip(1.0)
+        late.clip(1.0)
+    finally:
+        L.lrm_set_wait_budget(late.ctx, 2_000_000_000)
+    for c in (other, short, empty):
+        c.clip(1.0)
+        assert c.device_status() == 0
+    assert late.device_status() == 1 << L.LRM_ERR_TIMEOUT
+    assert late.device_status() == 0  # cleared by the read
+    late.clip(1.0)
+    assert late.device_status() == 0 and float(late.norm) == 512.0
+    L.lrm_get_device_status(late.ctx)  # the common word
+
+
+def test_status_refusals():
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    c = GradClip([torch.ones(3, device="cuda")])
+    for ctx, lst in ((None, c.list), (c.ctx, None)):
+        with pytest.raises(L.LrmError) as ei:
+            L.lrm_grad_list_status(ctx, lst)
+        assert ei.value.code == L.LRM_ERR_INVALID_ARG
+    assert L.load_library().lrm_grad_list_status(c.ctx, c.list, None, None) == L.LRM_ERR_INVALID_ARG

@@ -613,3 +613,16 @@ def test_feeds_route_stats():
         assert abs(rec.summary()["aux_unscaled"] - float(r.losses[1])) <= 4e-5 * float(r.losses[1])
     finally:
         rec.close()
+
+
+def test_router_reports_its_device_status():
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import Router
+
+    r = Router(4, 8, 2, True, AUX, Z)
+    x = torch.zeros(4, 8, device="cuda")
+    r.forward(x)
+    r.expert_idx[1, 0] = 9
+    r.backward(x, torch.ones(8, device="cuda"))
+    assert r.device_status() == 1 << L.LRM_ERR_INDEX
+    assert r.device_status() == 0
