@@ -314,6 +314,22 @@ def _require(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
+def _hold(seen: set, stream, tensors):
+    """The raw handle of `stream` (None: the current one) for a call that uses
+    `tensors`.  The first call on a stream that is not in `seen` tells the
+    allocator, so that their memory is not given away while that stream still
+    works on it.  A raw handle's owner keeps them alive instead: the allocator
+    may not use it once the owner has destroyed it."""
+    raw = L._stream(stream)
+    if raw not in seen:
+        seen.add(raw)
+        if not isinstance(stream, int):
+            s = torch.cuda.current_stream() if stream is None else stream
+            for t in tensors:
+                t.record_stream(s)
+    return raw
+
+
 class Router:
     """The router of one layer shape through the C ABI: gates and balance loss
     of a batch of logits (lrm_router_forward) and the logits' gradient
@@ -460,10 +476,16 @@ class GradClip:
         tensors = L.tensor_array(entries)
         need = L.lrm_grad_table_size(tensors, len(grads))
         self.table = torch.empty(need, dtype=torch.uint8, device=self.device)
-        self.list = L.lrm_grad_list_create(self.ctx, tensors, len(grads), self.table, need, stream)
         self._stats = torch.zeros(3, dtype=torch.float32, device=self.device)  # lrm_grad_stats
         self.norm, self.coef = self._stats[0:1], self._stats[1:2]
         self.nonfinite = self._stats.view(torch.int32)[2:3]
+        # the memory is the current stream's, where work on what it held before may be pending, and the fill is:
+        # done before the table is written, on the stream that lrm_grad_list_create waits for
+        home = torch.cuda.current_stream(self.device)
+        self._streams = {home.cuda_stream}
+        if stream is not None and L._stream(stream) != home.cuda_stream:
+            home.synchronize()
+        self.list = L.lrm_grad_list_create(self.ctx, tensors, len(grads), self.table, need, stream)
 
     def close(self):
         if getattr(self, "list", None):
@@ -477,13 +499,16 @@ class GradClip:
         except Exception:
             pass
 
+    def _on(self, stream):
+        return _hold(self._streams, stream, [self.table, self._stats, *self.grads, *self.outs])
+
     def measure(self, stream=None) -> None:
         """norm of all gradients, nothing clipped."""
-        L.lrm_grad_norm(self.ctx, self.list, self._stats, stream)
+        L.lrm_grad_norm(self.ctx, self.list, self._stats, self._on(stream))
 
     def clip(self, max_norm: float, stream=None) -> None:
         """norm, and every gradient times min(1, max_norm / norm) into its output."""
-        L.lrm_grad_clip(self.ctx, self.list, max_norm, self._stats, stream)
+        L.lrm_grad_clip(self.ctx, self.list, max_norm, self._stats, self._on(stream))
 
     def device_status(self, stream=None) -> int:
         """Flags (1 << code) that calls on this list raised on the device since the last read."""

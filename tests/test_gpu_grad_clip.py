@@ -478,3 +478,41 @@ def test_status_refusals():
             L.lrm_grad_list_status(ctx, lst)
         assert ei.value.code == L.LRM_ERR_INVALID_ARG
     assert L.load_library().lrm_grad_list_status(c.ctx, c.list, None, None) == L.LRM_ERR_INVALID_ARG
+
+
+def test_a_list_made_while_the_current_stream_is_busy():
+    # what the constructor fills on the current stream is there before another stream clips
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    for n in (300, 300000):
+        x = torch.full((n,), 0.5, device="cuda")
+        out, s = torch.zeros_like(x), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        c = GradClip([x], [out], stream=s)
+        c.clip(1.0, stream=s)
+        torch.cuda.synchronize()
+        assert abs(float(c.norm) - 0.5 * math.sqrt(n)) <= REL * 0.5 * math.sqrt(n)
+        assert int(c.nonfinite) == 0 and torch.equal(out, x * c.coef)
+
+
+def test_memory_of_a_dropped_list_stays_until_its_stream_is_done():
+    from backward_token_expert_gb300.pipeline import GradClip
+
+    x = torch.full((300000,), 0.5, device="cuda")
+    out, s = torch.zeros_like(x), torch.cuda.Stream()
+    c = GradClip([x], [out])
+    size, table, stats = c.table.numel(), c.table.data_ptr(), c._stats.data_ptr()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    c.clip(1.0, stream=s)
+    del c
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    others += [torch.empty(3, device="cuda") for _ in range(64)]
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in others]
+    assert not s.query()  # still asleep, the clip behind it
+    for at in (table, stats):
+        assert not any(a <= at < b for a, b in spans)
+    s.synchronize()
+    assert abs(float(out[0]) * 0.5 * math.sqrt(300000) - 0.5) <= 2 * REL
