@@ -364,6 +364,15 @@ class Router:
         self.dlogits = torch.empty(self.T, self.E, dtype=self.dlogits_dtype, device=self.device)
         need = L.lrm_workspace_size(self.ctx, L.LRM_OP_ROUTER, self.dims)
         self.ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        # the memory is the current stream's, where the fill and work on what it held before may be pending
+        home = torch.cuda.current_stream(self.device)
+        self._streams = {home.cuda_stream}
+        if not torch.cuda.is_current_stream_capturing():
+            home.synchronize()
+
+    def _on(self, stream):
+        return _hold(self._streams, stream, [self.expert_idx, self.alpha, self.row_stats, self.counts, self.f, self.P,
+                                             self._losses, self.dlogits, self.ws])
 
     def close(self):
         if self._own_ctx and getattr(self, "ctx", None):
@@ -384,7 +393,7 @@ class Router:
             _require(valid, "valid", torch.uint8, (self.T,), self.device)
         L.lrm_router_forward(self.ctx, logits, _DTYPES[self.dtype], valid, self.dims, self.renorm, self.aux_coef,
                              self.z_coef, self.expert_idx, self.alpha, self.row_stats, self.counts, self.f, self.P,
-                             self._losses, self.ws, self.ws.numel(), stream)
+                             self._losses, self.ws, self.ws.numel(), self._on(stream))
 
     def backward(self, logits, dgate=None, f=None, stream=None):
         """The gradient of the loss (with its coefficients) and, given `dgate`
@@ -399,7 +408,7 @@ class Router:
             _require(f, "f", torch.float32, (self.E,), self.device)
         L.lrm_router_backward(self.ctx, logits, _DTYPES[self.dtype], self.expert_idx, self.alpha, self.row_stats,
                               dgate, self.f if f is None else f, self._losses, self.dims, self.renorm, self.aux_coef,
-                              self.z_coef, self.dlogits, _DTYPES[self.dlogits_dtype], stream)
+                              self.z_coef, self.dlogits, _DTYPES[self.dlogits_dtype], self._on(stream))
         return self.dlogits
 
     def device_status(self, stream=None) -> int:

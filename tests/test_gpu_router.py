@@ -626,3 +626,41 @@ def test_router_reports_its_device_status():
     r.backward(x, torch.ones(8, device="cuda"))
     assert r.device_status() == 1 << L.LRM_ERR_INDEX
     assert r.device_status() == 0
+
+
+def test_router_made_while_the_current_stream_is_busy():
+    # the losses' fill on the current stream does not come after another stream's forward
+    from backward_token_expert_gb300.pipeline import Router
+
+    x = _logits(50, 8, "f32", 40).cuda()
+    want = Router(50, 8, 2, True, AUX, Z)
+    want.forward(x)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ctx = want.ctx  # one that is there: making one waits for the GPU
+    torch.cuda._sleep(20_000_000)
+    r = Router(50, 8, 2, True, AUX, Z, ctx=ctx)
+    r.forward(x, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(r._losses.view(torch.int32), want._losses.view(torch.int32)) and int(r.tokens) == 50
+
+
+def test_memory_of_a_dropped_router_stays_until_its_stream_is_done():
+    from backward_token_expert_gb300.pipeline import Router
+
+    x = _logits(50, 8, "f32", 41).cuda()
+    keep = Router(50, 8, 2, True, AUX, Z)
+    r = Router(50, 8, 2, True, AUX, Z, ctx=keep.ctx)
+    own = {t.data_ptr(): t.numel() * t.element_size() for t in (r.alpha, r.row_stats, r.expert_idx, r.dlogits, r.ws)}
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    r.forward(x, stream=s)
+    r.backward(x, stream=s)
+    del r
+    others = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in own.values() for _ in range(64)]
+    assert not s.query()
+    for at in own:
+        assert not any(t.data_ptr() <= at < t.data_ptr() + t.numel() for t in others)
+    s.synchronize()
