@@ -347,6 +347,8 @@ class Router:
         if dtype not in _DTYPES or self.dlogits_dtype not in _DTYPES:
             raise ValueError("router logits and their gradient are float32 or bfloat16")
         self.device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+        if self.device.index is None:  # "cuda": tensors name the device with its index
+            self.device = torch.device(self.device.type, torch.cuda.current_device())
         self.dims = L.dims_of(T, E, k, 8, 8)
         self._own_ctx = ctx is None
         self.ctx = L.lrm_create(self.device.index or 0) if ctx is None else ctx

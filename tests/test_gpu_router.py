@@ -664,3 +664,15 @@ def test_memory_of_a_dropped_router_stays_until_its_stream_is_done():
     for at in own:
         assert not any(t.data_ptr() <= at < t.data_ptr() + t.numel() for t in others)
     s.synchronize()
+
+
+@pytest.mark.parametrize("device", [0, "cuda", "cuda:0", torch.device("cuda"), torch.device("cuda", 0)])
+def test_names_of_the_device(device):
+    from backward_token_expert_gb300.pipeline import Router
+
+    r = Router(4, 8, 2, True, AUX, Z, device=device)
+    x = torch.eye(4, 8, device="cuda")
+    valid = torch.ones(4, dtype=torch.uint8, device="cuda")
+    r.forward(x, valid)
+    r.backward(x, torch.ones(8, device="cuda"), torch.ones(8, device="cuda"))
+    assert int(r.tokens) == 4 and r.expert_idx[:, 0].tolist() == [0, 1, 2, 3] and r.dlogits.device == x.device

@@ -103,3 +103,21 @@ def test_refusals():
     for kw in (dict(E=12), dict(max_norm=-1.0), dict(max_norm=float("nan"))):
         with pytest.raises(ValueError):
             TrainingStep(**dict(dict(T=64, E=8, k=2, h=64, I=32), **kw))
+
+
+def test_a_step_on_the_device_named_without_its_index():
+    from backward_token_expert_gb300.pipeline import TrainingStep
+
+    T, E, k, h, I = 64, 8, 2, 64, 32
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    step = TrainingStep(T, E, k, h, I, device="cuda")
+    try:
+        logits = torch.randn(T, E, device="cuda")
+        step.route(logits)
+        step.backward(logits, torch.randn(T, h, **bf), torch.randn(T * k, I, **bf), torch.randn(E, h, I, **bf),
+                      torch.randn(T, h, **bf), torch.randn(T * k, 2 * I, **bf), torch.randn(E, 2 * I, h, **bf),
+                      torch.randn(E, h, **bf))
+        assert step.device_status() == 0 and int(step.clip.nonfinite) == 0
+        assert abs(float(torch.cat([g.double().flatten() for g in step.clip.grads]).norm()) - 1.0) <= 1e-5
+    finally:
+        step.close()
