@@ -20,10 +20,16 @@
 //               chunking as rs_count, scatters its pair ids stably into the
 //               bucket (each warp owns a contiguous sub-range, ranks inside a
 //               warp come from __match_any_sync).
+//
+// lrm_route_stats_counted takes the statistics of the tokens that
+// lrm_router_forward counted (a sum in row_stats that is not 0): pairs of the
+// others get no count and no place in the bucket, their logits and ids are not
+// read, and T and N are the counted tokens' and pairs', known on the device.
 #include <limits.h>
 #include <math.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "block_scan.cuh"
 #include "lrm_internal.cuh"
@@ -58,17 +64,39 @@ RsLayout rs_layout(const lrm_dims& d) {
   return L;
 }
 
+// The tokens that count: all T, or those that lrm_router_forward counted.
+struct AllTokens {
+  __device__ __forceinline__ bool has(int) const { return true; }
+  __device__ __forceinline__ int total(int T) const { return T; }
+};
+struct CountedTokens {
+  const float2* row_stats;
+  const lrm_router_losses* losses;
+  __device__ __forceinline__ bool has(int t) const { return __ldg(row_stats + t).y != 0.f; }
+  __device__ __forceinline__ int total(int T) const { return min(max(__ldg(&losses->tokens), 0), T); }
+};
+
 // Stages the block's pair ids [p0, p1) in shared memory (p0 is the first
 // pair of a token) and replaces every invalid id (outside [0,E) or equal to
 // an earlier slot of the same token) by -1.  Returns true if one was found.
+// The ids of tokens that do not count become RS_LEFT_OUT and are not checked.
+constexpr int RS_LEFT_OUT = INT_MIN;
+template <typename Tokens>
 __device__ __forceinline__ bool stage_ids(const int32_t* __restrict__ idx, int p0, int p1, int k, int E,
-                                          int* s_ids) {
-  for (int p = p0 + static_cast<int>(threadIdx.x); p < p1; p += RS_THREADS) s_ids[p - p0] = __ldg(idx + p);
+                                          const Tokens& tokens, int* s_ids) {
+  constexpr bool ALL = std::is_same<Tokens, AllTokens>::value;
+  for (int p = p0 + static_cast<int>(threadIdx.x); p < p1; p += RS_THREADS) {
+    if constexpr (ALL)
+      s_ids[p - p0] = __ldg(idx + p);
+    else
+      s_ids[p - p0] = tokens.has(p / k) ? max(__ldg(idx + p), -1) : RS_LEFT_OUT;
+  }
   __syncthreads();
   int fix[RS_MAX_PER_THREAD];
   int nf = 0;
   for (int i = threadIdx.x; i < p1 - p0; i += RS_THREADS) {
     const int e = s_ids[i];
+    if (!ALL && e == RS_LEFT_OUT) continue;
     bool ok = e >= 0 && e < E;
     for (int q = i - (i % k); ok && q < i; ++q) ok = s_ids[q] != e;
     if (!ok) fix[nf++] = i;
@@ -88,10 +116,10 @@ __device__ __forceinline__ void load_logits(const float* __restrict__ row, int E
   }
 }
 
-template <int VPL>
+template <int VPL, typename Tokens>
 __global__ void __launch_bounds__(RS_THREADS) rs_count(const float* __restrict__ logits,
-                                                       const int32_t* __restrict__ idx, int T, int E, int k,
-                                                       int tpb, int nblk, int32_t* __restrict__ ws_hist,
+                                                       const int32_t* __restrict__ idx, Tokens tokens, int T, int E,
+                                                       int k, int tpb, int nblk, int32_t* __restrict__ ws_hist,
                                                        float* __restrict__ ws_p, unsigned int* status) {
   extern __shared__ float rs_smem[];
   float* pw = rs_smem;                                         // [RS_WARPS][E]
@@ -102,7 +130,7 @@ __global__ void __launch_bounds__(RS_THREADS) rs_count(const float* __restrict__
 
   const int tok0 = blockIdx.x * tpb;
   const int tok1 = min(T, tok0 + tpb);
-  if (stage_ids(idx, tok0 * k, tok1 * k, k, E, s_ids)) raise_flag(status, LRM_ERR_INDEX);
+  if (stage_ids(idx, tok0 * k, tok1 * k, k, E, tokens, s_ids)) raise_flag(status, LRM_ERR_INDEX);
   for (int i = tid; i < (tok1 - tok0) * k; i += RS_THREADS) {
     const int e = s_ids[i];
     if (e >= 0) atomicAdd(&hist[e], 1);
@@ -117,10 +145,12 @@ __global__ void __launch_bounds__(RS_THREADS) rs_count(const float* __restrict__
   for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
   for (int t0 = tok0 + warp; t0 < tok1; t0 += DEPTH * RS_WARPS) {
     float cur[DEPTH][VPL];
+    bool in[DEPTH];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
       const int t = t0 + d * RS_WARPS;
-      if (t < tok1) {
+      in[d] = t < tok1 && tokens.has(t);
+      if (in[d]) {
         load_logits<VPL>(logits + static_cast<size_t>(t) * E, E, lane, cur[d]);
       } else {
 #pragma unroll
@@ -129,7 +159,7 @@ __global__ void __launch_bounds__(RS_THREADS) rs_count(const float* __restrict__
     }
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      if (t0 + d * RS_WARPS >= tok1) break;
+      if (!in[d]) continue;
       float mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, cur[d][i]);
@@ -171,7 +201,8 @@ __global__ void __launch_bounds__(RS_THREADS) rs_count(const float* __restrict__
 // block relative to the expert's first bucket slot (an exclusive scan along
 // the row).  Writes the per-expert outputs: n_e, P_e, f_e and the quota
 // Q_e = ceil(rho min(n_e, C)) in exact integer arithmetic.
-__global__ void __launch_bounds__(RR_THREADS) rs_rows(int T, int E, int k, int nblk, int32_t cf_num, int32_t cf_den,
+template <typename Tokens>
+__global__ void __launch_bounds__(RR_THREADS) rs_rows(Tokens tokens, int T, int E, int k, int nblk, int32_t cf_num, int32_t cf_den,
                                                       int32_t rho_num, int32_t rho_den,
                                                       int32_t* __restrict__ ws_hist, const float* __restrict__ ws_p,
                                                       int32_t* __restrict__ counts, float* __restrict__ P,
@@ -179,6 +210,7 @@ __global__ void __launch_bounds__(RR_THREADS) rs_rows(int T, int E, int k, int n
   const int lane = threadIdx.x & 31;
   const int x = blockIdx.x * RR_WARPS + (threadIdx.x >> 5);
   if (x >= E) return;
+  T = tokens.total(T);
   const long long N = static_cast<long long>(T) * k;
   const size_t row = static_cast<size_t>(x) * nblk;
   int run = 0;
@@ -274,8 +306,9 @@ __device__ void write_summary(int T, int E, int k, int32_t cf_num, int32_t cf_de
 // writes offsets[] and the summary.  Then the stable scatter of the block's
 // pairs (none when the layer has no token: one block is launched for the
 // offsets and the summary).
-__global__ void __launch_bounds__(RS_THREADS) rs_scatter(const int32_t* __restrict__ idx, int T, int E, int k,
-                                                         int tpb, int nblk, int32_t cf_num, int32_t cf_den,
+template <typename Tokens>
+__global__ void __launch_bounds__(RS_THREADS) rs_scatter(const int32_t* __restrict__ idx, Tokens tokens, int T, int E,
+                                                         int k, int tpb, int nblk, int32_t cf_num, int32_t cf_den,
                                                          const int32_t* __restrict__ ws_base,
                                                          const int32_t* __restrict__ counts,
                                                          const float* __restrict__ P, const float* __restrict__ f,
@@ -307,13 +340,13 @@ __global__ void __launch_bounds__(RS_THREADS) rs_scatter(const int32_t* __restri
     }
     if (blockIdx.x == 0 && lane == 31) offsets[E] = incl;
   } else if (warp == 1 && blockIdx.x == 0) {
-    write_summary(T, E, k, cf_num, cf_den, counts, P, f, quota, summary);
+    write_summary(tokens.total(T), E, k, cf_num, cf_den, counts, P, f, quota, summary);
   }
   if (nblk == 0) return;
   for (int i = tid; i < RS_WARPS * E; i += RS_THREADS) rs_cnt[i] = 0;
   const int p0 = blockIdx.x * tpb * k;
   const int p1 = min(T, (blockIdx.x + 1) * tpb) * k;
-  stage_ids(idx, p0, p1, k, E, s_ids);
+  stage_ids(idx, p0, p1, k, E, tokens, s_ids);
   const int span = (p1 - p0 + RS_WARPS - 1) / RS_WARPS;
   const int w0 = min(p1, p0 + warp * span);
   const int w1 = min(p1, w0 + span);
@@ -356,54 +389,61 @@ __global__ void __launch_bounds__(RS_THREADS) rs_scatter(const int32_t* __restri
   }
 }
 
-template <int VPL>
+template <int VPL, typename Tokens>
 cudaError_t launch_count(int nblk, size_t smem, cudaStream_t s, const float* logits, const int32_t* idx,
-                         const lrm_dims& d, int tpb, int32_t* ws_hist, float* ws_p, unsigned int* status) {
+                         const Tokens& tokens, const lrm_dims& d, int tpb, int32_t* ws_hist, float* ws_p,
+                         unsigned int* status) {
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(rs_count<VPL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(rs_count<VPL, Tokens>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  rs_count<VPL><<<nblk, RS_THREADS, smem, s>>>(logits, idx, d.T, d.E, d.k, tpb, nblk, ws_hist, ws_p, status);
+  rs_count<VPL, Tokens><<<nblk, RS_THREADS, smem, s>>>(logits, idx, tokens, d.T, d.E, d.k, tpb, nblk, ws_hist, ws_p,
+                                                       status);
   return cudaGetLastError();
 }
 
-// The three launches of the step on `s` (shared by both entry points).
+// The three launches of the step on `s` (shared by the entry points).
+template <typename Tokens>
 lrm_status launch_route_stats(lrm_ctx* ctx, const RsLayout& L, const lrm_dims& dims, const float* logits,
-                              const int32_t* expert_idx, int32_t cf_num, int32_t cf_den, int32_t rho_num,
-                              int32_t rho_den, int32_t* counts, int32_t* offsets, int32_t* bucket, float* P, float* f,
-                              int32_t* quota, lrm_route_summary* summary, int32_t* ws_hist, float* ws_p,
-                              cudaStream_t s) {
+                              const int32_t* expert_idx, const Tokens& tokens, int32_t cf_num, int32_t cf_den,
+                              int32_t rho_num, int32_t rho_den, int32_t* counts, int32_t* offsets, int32_t* bucket,
+                              float* P, float* f, int32_t* quota, lrm_route_summary* summary, int32_t* ws_hist,
+                              float* ws_p, cudaStream_t s) {
   if (L.nblk > 0) {
     const size_t smem1 = (RS_WARPS * dims.E + dims.E + RS_PAIRS_PER_BLOCK) * sizeof(float);
     const int vpl = (dims.E + 31) / 32;
+    const auto count = [&](auto n) {
+      return launch_count<decltype(n)::value>(L.nblk, smem1, s, logits, expert_idx, tokens, dims, L.tpb, ws_hist, ws_p,
+                                              ctx->d_status);
+    };
     cudaError_t e;
     if (vpl <= 1)
-      e = launch_count<1>(L.nblk, smem1, s, logits, expert_idx, dims, L.tpb, ws_hist, ws_p, ctx->d_status);
+      e = count(std::integral_constant<int, 1>{});
     else if (vpl <= 2)
-      e = launch_count<2>(L.nblk, smem1, s, logits, expert_idx, dims, L.tpb, ws_hist, ws_p, ctx->d_status);
+      e = count(std::integral_constant<int, 2>{});
     else if (vpl <= 4)
-      e = launch_count<4>(L.nblk, smem1, s, logits, expert_idx, dims, L.tpb, ws_hist, ws_p, ctx->d_status);
+      e = count(std::integral_constant<int, 4>{});
     else if (vpl <= 8)
-      e = launch_count<8>(L.nblk, smem1, s, logits, expert_idx, dims, L.tpb, ws_hist, ws_p, ctx->d_status);
+      e = count(std::integral_constant<int, 8>{});
     else if (vpl <= 16)
-      e = launch_count<16>(L.nblk, smem1, s, logits, expert_idx, dims, L.tpb, ws_hist, ws_p, ctx->d_status);
+      e = count(std::integral_constant<int, 16>{});
     else
-      e = launch_count<32>(L.nblk, smem1, s, logits, expert_idx, dims, L.tpb, ws_hist, ws_p, ctx->d_status);
+      e = count(std::integral_constant<int, 32>{});
     if (e != cudaSuccess) return LRM_ERR_CUDA;
   }
-  rs_rows<<<(dims.E + RR_WARPS - 1) / RR_WARPS, RR_THREADS, 0, s>>>(dims.T, dims.E, dims.k, L.nblk, cf_num, cf_den,
-                                                                     rho_num, rho_den, ws_hist, ws_p, counts, P, f,
-                                                                     quota);
+  rs_rows<<<(dims.E + RR_WARPS - 1) / RR_WARPS, RR_THREADS, 0, s>>>(tokens, dims.T, dims.E, dims.k, L.nblk, cf_num,
+                                                                     cf_den, rho_num, rho_den, ws_hist, ws_p, counts,
+                                                                     P, f, quota);
   lrm_status st = launch_status();
   if (st != LRM_OK) return st;
   const size_t smem3 = (RS_WARPS * dims.E + RS_PAIRS_PER_BLOCK) * sizeof(int);
   if (smem3 > 48 * 1024 &&
-      cudaFuncSetAttribute(rs_scatter, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem3)) !=
-          cudaSuccess)
+      cudaFuncSetAttribute(rs_scatter<Tokens>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem3)) != cudaSuccess)
     return LRM_ERR_CUDA;
-  rs_scatter<<<L.nblk > 0 ? L.nblk : 1, RS_THREADS, smem3, s>>>(expert_idx, dims.T, dims.E, dims.k, L.tpb, L.nblk,
-                                                                 cf_num, cf_den, ws_hist, counts, P, f, quota,
+  rs_scatter<<<L.nblk > 0 ? L.nblk : 1, RS_THREADS, smem3, s>>>(expert_idx, tokens, dims.T, dims.E, dims.k, L.tpb,
+                                                                 L.nblk, cf_num, cf_den, ws_hist, counts, P, f, quota,
                                                                  offsets, summary, bucket);
   return launch_status();
 }
@@ -416,11 +456,14 @@ size_t route_stats_workspace_bytes(const lrm_dims& d) { return rs_layout(d).byte
 
 using namespace lrm;
 
-extern "C" lrm_status lrm_route_stats(lrm_ctx* ctx, const float* logits, const int32_t* expert_idx, lrm_dims dims,
-                                      int32_t cf_num, int32_t cf_den, int32_t rho_num, int32_t rho_den,
-                                      int32_t* counts, int32_t* offsets, int32_t* bucket, float* P, float* f,
-                                      int32_t* quota, lrm_route_summary* summary, void* ws, size_t ws_bytes,
-                                      void* stream) {
+namespace {
+
+// The checks and launches of the two entry points with a caller's workspace.
+template <typename Tokens>
+lrm_status route_stats(lrm_ctx* ctx, const float* logits, const int32_t* expert_idx, const Tokens& tokens,
+                       lrm_dims dims, int32_t cf_num, int32_t cf_den, int32_t rho_num, int32_t rho_den,
+                       int32_t* counts, int32_t* offsets, int32_t* bucket, float* P, float* f, int32_t* quota,
+                       lrm_route_summary* summary, void* ws, size_t ws_bytes, void* stream) {
   if (ctx == nullptr) return LRM_ERR_INVALID_ARG;
   lrm_status st = check_dims(dims);
   if (st != LRM_OK) return st;
@@ -431,6 +474,10 @@ extern "C" lrm_status lrm_route_stats(lrm_ctx* ctx, const float* logits, const i
     return LRM_ERR_INVALID_ARG;
   if (dims.T > 0 && (logits == nullptr || expert_idx == nullptr || bucket == nullptr))
     return LRM_ERR_INVALID_ARG;
+  if constexpr (std::is_same<Tokens, CountedTokens>::value) {
+    if (tokens.losses == nullptr || (dims.T > 0 && tokens.row_stats == nullptr)) return LRM_ERR_INVALID_ARG;
+    if (!aligned(tokens.row_stats, 8) || !aligned(tokens.losses, 4)) return LRM_ERR_ALIGN;
+  }
   const void* ptrs[] = {logits, expert_idx, counts, offsets, bucket, P, f, quota, summary, ws};
   for (const void* p : ptrs)
     if (p != nullptr && !aligned(p, 4)) return LRM_ERR_ALIGN;
@@ -442,8 +489,30 @@ extern "C" lrm_status lrm_route_stats(lrm_ctx* ctx, const float* logits, const i
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int32_t* ws_hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.hist_off);
   float* ws_p = reinterpret_cast<float*>(static_cast<char*>(ws) + L.p_off);
-  return launch_route_stats(ctx, L, dims, logits, expert_idx, cf_num, cf_den, rho_num, rho_den, counts, offsets,
-                            bucket, P, f, quota, summary, ws_hist, ws_p, s);
+  return launch_route_stats(ctx, L, dims, logits, expert_idx, tokens, cf_num, cf_den, rho_num, rho_den, counts,
+                            offsets, bucket, P, f, quota, summary, ws_hist, ws_p, s);
+}
+
+}  // namespace
+
+extern "C" lrm_status lrm_route_stats(lrm_ctx* ctx, const float* logits, const int32_t* expert_idx, lrm_dims dims,
+                                      int32_t cf_num, int32_t cf_den, int32_t rho_num, int32_t rho_den,
+                                      int32_t* counts, int32_t* offsets, int32_t* bucket, float* P, float* f,
+                                      int32_t* quota, lrm_route_summary* summary, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  return route_stats(ctx, logits, expert_idx, AllTokens{}, dims, cf_num, cf_den, rho_num, rho_den, counts, offsets,
+                     bucket, P, f, quota, summary, ws, ws_bytes, stream);
+}
+
+extern "C" lrm_status lrm_route_stats_counted(lrm_ctx* ctx, const float* logits, const int32_t* expert_idx,
+                                              const float* row_stats, const lrm_router_losses* losses, lrm_dims dims,
+                                              int32_t cf_num, int32_t cf_den, int32_t rho_num, int32_t rho_den,
+                                              int32_t* counts, int32_t* offsets, int32_t* bucket, float* P, float* f,
+                                              int32_t* quota, lrm_route_summary* summary, void* ws, size_t ws_bytes,
+                                              void* stream) {
+  const CountedTokens tokens{reinterpret_cast<const float2*>(row_stats), losses};
+  return route_stats(ctx, logits, expert_idx, tokens, dims, cf_num, cf_den, rho_num, rho_den, counts, offsets, bucket,
+                     P, f, quota, summary, ws, ws_bytes, stream);
 }
 
 // Host queries of the capacity and quota rule, with the kernels' own helpers.
@@ -556,6 +625,6 @@ extern "C" lrm_status lrm_route_stats_noalloc(lrm_ctx* ctx, const float* logits,
   if ((st = scratch_address(ctx->device, s, &ws)) != LRM_OK) return st;
   int32_t* ws_hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.hist_off);
   float* ws_p = reinterpret_cast<float*>(static_cast<char*>(ws) + L.p_off);
-  return launch_route_stats(ctx, L, dims, logits, expert_idx, cf_num, cf_den, rho_num, rho_den, counts, offsets,
-                            bucket, P, f, quota, summary, ws_hist, ws_p, s);
+  return launch_route_stats(ctx, L, dims, logits, expert_idx, AllTokens{}, cf_num, cf_den, rho_num, rho_den, counts,
+                            offsets, bucket, P, f, quota, summary, ws_hist, ws_p, s);
 }

@@ -66,6 +66,7 @@ EXPORTED = (
     "lrm_capacity",
     "lrm_max_rows",
     "lrm_router_forward",
+    "lrm_route_stats_counted",
     "lrm_router_backward",
     "lrm_gate_grad",
     "lrm_grad_table_size",
@@ -173,6 +174,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     size = ctypes.c_size_t
     sig.update({
         "lrm_router_forward": ([P, P, i32, P, Dims, i32, f32, f32, P, P, P, P, P, P, P, P, size, P], st),
+        "lrm_route_stats_counted": ([P, P, P, P, P, Dims] + [i32] * 4 + [P] * 8 + [size, P], st),
         "lrm_router_backward": ([P, P, i32, P, P, P, P, P, P, Dims, i32, f32, f32, P, i32, P], st),
         "lrm_gate_grad": ([P, P, P, P, P, Dims, i32, P, P], st),
         "lrm_grad_table_size": ([ctypes.POINTER(Tensor), i32, ctypes.POINTER(size)], st),
@@ -380,6 +382,16 @@ def lrm_router_forward(ctx, logits, logits_dtype: int, valid, dims: Dims, renorm
                                              z_coef, _ptr(expert_idx), _ptr(alpha), _ptr(row_stats), _ptr(counts),
                                              _ptr(f), _ptr(P), _ptr(losses), _ptr(ws), ws_bytes, _stream(stream)),
            "lrm_router_forward")
+
+
+def lrm_route_stats_counted(ctx, logits, expert_idx, row_stats, losses, dims: Dims, cf: Fraction, rho: Fraction,
+                            counts, offsets, bucket, P, f, quota, summary, ws, ws_bytes: int, stream=None) -> None:
+    cf, rho = Fraction(cf), Fraction(rho)
+    _check(load_library().lrm_route_stats_counted(ctx, _ptr(logits), _ptr(expert_idx), _ptr(row_stats), _ptr(losses),
+                                                  dims, cf.numerator, cf.denominator, rho.numerator, rho.denominator,
+                                                  _ptr(counts), _ptr(offsets), _ptr(bucket), _ptr(P), _ptr(f),
+                                                  _ptr(quota), _ptr(summary), _ptr(ws), ws_bytes, _stream(stream)),
+           "lrm_route_stats_counted")
 
 
 def lrm_router_backward(ctx, logits, logits_dtype: int, expert_idx, alpha, row_stats, dgate, f, losses, dims: Dims,

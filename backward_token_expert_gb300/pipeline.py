@@ -122,10 +122,15 @@ class Recalibration:
 
     # -- the steps -----------------------------------------------------------
 
-    def route_stats(self, logits, expert_idx, stream=None, quota_override=None):
+    def route_stats(self, logits, expert_idx, stream=None, quota_override=None, counted=None):
+        """Step 1.  `counted` (``Router.counted``) leaves the tokens that the
+        router did not count out of it, and so out of the whole path."""
         b = self.buf
-        L.lrm_route_stats(self.ctx, logits, expert_idx, self.dims, self.cf, self.rho, b.counts, b.offsets,
-                          b.bucket, b.P, b.f, b.quota, b.summary, b.ws_route, self.ws_bytes, stream)
+        out = (b.counts, b.offsets, b.bucket, b.P, b.f, b.quota, b.summary, b.ws_route, self.ws_bytes, stream)
+        if counted is None:
+            L.lrm_route_stats(self.ctx, logits, expert_idx, self.dims, self.cf, self.rho, *out)
+        else:
+            L.lrm_route_stats_counted(self.ctx, logits, expert_idx, *counted, self.dims, self.cf, self.rho, *out)
         if quota_override is not None:
             b.quota.copy_(quota_override)
 
@@ -238,13 +243,14 @@ class Recalibration:
         else:
             self.wgrad(stream)
 
-    def run(self, logits, expert_idx, g, phi, alpha, W, stream=None, dw_bf16: bool = False, side_stream=None):
+    def run(self, logits, expert_idx, g, phi, alpha, W, stream=None, dw_bf16: bool = False, side_stream=None,
+            counted=None):
         """The whole path, enqueued on one stream.  Route statistics and score
         read disjoint inputs, so with `side_stream` (a torch stream; `stream`
         must then be a torch stream or None) route statistics run on it beside
-        score, and select waits for both."""
+        score, and select waits for both.  `counted`: as in route_stats."""
         if side_stream is None:
-            self.route_stats(logits, expert_idx, stream)
+            self.route_stats(logits, expert_idx, stream, counted=counted)
             self.backward_steps(g, phi, alpha, W, stream, dw_bf16=dw_bf16)
             return
         main = torch.cuda.current_stream(self.device) if stream is None else stream
@@ -253,7 +259,7 @@ class Recalibration:
         fork = torch.cuda.Event()
         fork.record(main)
         side_stream.wait_event(fork)
-        self.route_stats(logits, expert_idx, side_stream)
+        self.route_stats(logits, expert_idx, side_stream, counted=counted)
         self.score(g, phi, alpha, main)
         join = torch.cuda.Event()
         join.record(side_stream)
@@ -396,6 +402,11 @@ class Router:
         L.lrm_router_forward(self.ctx, logits, _DTYPES[self.dtype], valid, self.dims, self.renorm, self.aux_coef,
                              self.z_coef, self.expert_idx, self.alpha, self.row_stats, self.counts, self.f, self.P,
                              self._losses, self.ws, self.ws.numel(), self._on(stream))
+
+    @property
+    def counted(self):
+        """What ``Recalibration.run`` takes to leave out the tokens that the last ``forward`` did not count."""
+        return self.row_stats, self._losses
 
     def backward(self, logits, dgate=None, f=None, stream=None):
         """The gradient of the loss (with its coefficients) and, given `dgate`
@@ -561,7 +572,9 @@ class TrainingStep:
         self.clip = GradClip([self.rec.buf.dW, self.rec._fc1_buffers().dW1, self.dWr], ctx=self.rec.ctx)
 
     def route(self, logits, valid=None, stream=None):
-        """Ids and gates of the batch (``router.expert_idx``, ``router.alpha``) and its losses."""
+        """Ids and gates of the batch (``router.expert_idx``, ``router.alpha``) and its losses.  The tokens
+        that `valid` leaves out take no part in the backward either: capacity, quotas, selection and gradients
+        are those of a batch without them, and their rows of logits, g, phi and ab may hold anything."""
         self.router.forward(logits, valid, stream)
 
     def backward(self, logits, g, phi, W, x, ab, W1, Wr, stream=None):
@@ -570,7 +583,7 @@ class TrainingStep:
         output of every pair, x [T, h] the layer's input (bf16); W [E, h, I],
         W1 [E, 2I, h], Wr [E, h] the weights (bf16)."""
         rec, r = self.rec, self.router
-        rec.run(logits, r.expert_idx, g, phi, r.alpha, W, stream)
+        rec.run(logits, r.expert_idx, g, phi, r.alpha, W, stream, counted=r.counted)
         rec.gate_grad(stream)
         rec.fc1_backward(x, ab, W1, stream)
         r.backward(logits, rec.dgate, stream=stream)

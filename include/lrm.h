@@ -413,7 +413,8 @@ LRM_API lrm_status lrm_route_stats_noalloc(lrm_ctx* ctx, const float* logits, co
  *   expert_idx [T, k] int32 out, alpha [T*k] fp32 out, row_stats [T, 2] fp32 out
  *   counts     [E]    int32 out, f, P [E] fp32 out, losses [1] device struct out
  *   ws                workspace of lrm_workspace_size(LRM_OP_ROUTER), 256-byte aligned
- * expert_idx, alpha and logits (fp32) are what lrm_route_stats and lrm_score take.
+ * expert_idx, alpha and logits (fp32) are what lrm_route_stats_counted (lrm_route_stats
+ * where every token counts) and lrm_score take.
  */
 typedef struct lrm_router_losses {
   float loss, aux, z;
@@ -423,6 +424,23 @@ LRM_API lrm_status lrm_router_forward(lrm_ctx* ctx, const void* logits, int32_t 
                                       lrm_dims dims, int32_t renorm, float aux_coef, float z_coef,
                                       int32_t* expert_idx, float* alpha, float* row_stats, int32_t* counts, float* f,
                                       float* P, lrm_router_losses* losses, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * lrm_route_stats over the tokens that lrm_router_forward counted: N = Tc k
+ * pairs, with capacity, quotas, P, f and the summary of a batch that holds the
+ * counted tokens alone.  Pairs of other tokens are in no count and have no place
+ * in the bucket (so lrm_select cannot retain one, whatever its score), and their
+ * logits and ids are not read.
+ *   row_stats, losses  as the forward wrote them (of losses only the token count
+ *                      is read)
+ *   bucket             [N] int32 out: the first Tc k entries are written
+ */
+LRM_API lrm_status lrm_route_stats_counted(lrm_ctx* ctx, const float* logits, const int32_t* expert_idx,
+                                           const float* row_stats, const lrm_router_losses* losses, lrm_dims dims,
+                                           int32_t cf_num, int32_t cf_den, int32_t rho_num, int32_t rho_den,
+                                           int32_t* counts, int32_t* offsets, int32_t* bucket, float* P, float* f,
+                                           int32_t* quota, lrm_route_summary* summary, void* ws, size_t ws_bytes,
+                                           void* stream);
 
 /*
  * lrm_gate_grad: the gate weights' gradient on the retained pairs, in the form

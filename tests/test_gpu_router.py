@@ -676,3 +676,76 @@ def test_names_of_the_device(device):
     r.forward(x, valid)
     r.backward(x, torch.ones(8, device="cuda"), torch.ones(8, device="cuda"))
     assert int(r.tokens) == 4 and r.expert_idx[:, 0].tolist() == [0, 1, 2, 3] and r.dlogits.device == x.device
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (700, 5, 3), (3000, 33, 4), (2500, 128, 8), (900, 500, 32), (300, 1024, 10)])
+@pytest.mark.parametrize("share", [0.0, 0.4, 1.0])
+def test_route_stats_of_the_counted_tokens(T, E, k, share):
+    # against the statistics of a batch that holds the counted tokens alone, with garbage in the other tokens
+    from fractions import Fraction
+
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import Recalibration, Router
+
+    x = _logits(T, E, "f32", T + E).cuda()
+    valid = torch.rand(T, generator=torch.Generator(device="cuda").manual_seed(T), device="cuda") < share
+    kept = valid.nonzero().flatten()
+    n = kept.numel()
+    r = Router(T, E, k, True, AUX, Z)
+    r.forward(x, valid.to(torch.uint8))
+    x[~valid] = float("nan")
+    r.expert_idx[~valid] = torch.randint(-1 << 31, (1 << 31) - 1, (T - n, k), device="cuda", dtype=torch.int32)
+    cf, rho = Fraction(5, 4), Fraction(2, 3)
+    a, b = Recalibration(T, E, k, 8, 8, cf, rho), Recalibration(n, E, k, 8, 8, cf, rho)
+    try:
+        a.buf.bucket.fill_(-7)
+        a.route_stats(x, r.expert_idx, counted=r.counted)
+        b.route_stats(x[kept].contiguous(), r.expert_idx[kept].contiguous())
+        assert a.device_status() == 0 and b.device_status() == 0
+        for name in ("counts", "offsets", "quota", "f"):
+            assert torch.equal(getattr(a.buf, name), getattr(b.buf, name)), name
+        assert torch.allclose(a.buf.P, b.buf.P, rtol=2e-5, atol=1e-37)
+        pairs = (kept[:, None] * k + torch.arange(k, device="cuda")).flatten()
+        assert torch.equal(a.buf.bucket[: n * k].long(), pairs[b.buf.bucket[: n * k].long()])
+        assert bool((a.buf.bucket[n * k:] == -7).all())
+        sa, sb = a.summary(), b.summary()
+        for name in sa:
+            tol = 2e-5 * abs(sb[name]) if name in ("aux_unscaled", "sum_P") else 0
+            assert abs(sa[name] - sb[name]) <= tol, name
+        if n:  # a counted token's bad ids are still found
+            r.expert_idx[kept[0], 0] = -(1 << 31)
+            a.route_stats(x, r.expert_idx, counted=r.counted)
+            assert a.device_status() == 1 << L.LRM_ERR_INDEX
+            assert int(a.buf.offsets[-1]) == n * k - 1
+    finally:
+        a.close()
+        b.close()
+
+
+def test_refusals_of_the_counted_route_stats():
+    from fractions import Fraction
+
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import Recalibration, Router
+
+    r, rec = Router(8, 4, 2, True, AUX, Z), Recalibration(8, 4, 2, 8, 8)
+    x = torch.zeros(8, 4, device="cuda")
+    r.forward(x)
+    good = dict(ctx=rec.ctx, logits=x, idx=r.expert_idx, stats=r.row_stats, losses=r._losses, cf=Fraction(1), ws=rec.buf.ws_route)
+    b = rec.buf
+
+    def call(**kw):
+        a = dict(good, **kw)
+        L.lrm_route_stats_counted(a["ctx"], a["logits"], a["idx"], a["stats"], a["losses"], rec.dims, a["cf"],
+                                  Fraction(1, 2), b.counts, b.offsets, b.bucket, b.P, b.f, b.quota, b.summary, a["ws"],
+                                  rec.ws_bytes)
+
+    call()
+    inv, al = L.LRM_ERR_INVALID_ARG, L.LRM_ERR_ALIGN
+    for kw, code in [(dict(ctx=None), inv), (dict(logits=None), inv), (dict(idx=None), inv), (dict(stats=None), inv),
+                     (dict(losses=None), inv), (dict(cf=Fraction(0)), inv), (dict(stats=r.row_stats.data_ptr() + 4), al),
+                     (dict(losses=r._losses.data_ptr() + 2), al), (dict(ws=None), L.LRM_ERR_WORKSPACE)]:
+        with pytest.raises(L.LrmError) as ei:
+            call(**kw)
+        assert ei.value.code == code, kw
+    rec.close()

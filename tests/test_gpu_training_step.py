@@ -121,3 +121,85 @@ def test_a_step_on_the_device_named_without_its_index():
         assert abs(float(torch.cat([g.double().flatten() for g in step.clip.grads]).norm()) - 1.0) <= 1e-5
     finally:
         step.close()
+
+
+def _batch(T, E, k, h, I, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    bf = lambda *n: torch.randn(*n, generator=g, device="cuda").mul_(0.3).to(torch.bfloat16)  # noqa: E731
+    skew = torch.linspace(1.5, -1.5, E, device="cuda")
+    return (torch.randn(T, E, generator=g, device="cuda") + skew, bf(T, h), bf(T * k, I), bf(T, h), bf(T * k, 2 * I),
+            bf(E, h, I), bf(E, 2 * I, h), bf(E, h))
+
+
+def _step(T, E, k, h, I, batch, valid=None):
+    """Results of a step, cloned; a batch of its own shape."""
+    from backward_token_expert_gb300.pipeline import TrainingStep
+
+    logits, g, phi, x, ab, W, W1, Wr = batch
+    step = TrainingStep(T, E, k, h, I, Fraction(5, 4), Fraction(3, 4), 0.5, 0.1, max_norm=1e9)
+    try:
+        step.route(logits, valid)
+        step.backward(logits, g, phi, W, x, ab, W1, Wr)
+        torch.cuda.synchronize()
+        assert step.device_status() == 0
+        r, b = step.router, step.rec.buf
+        total = int(b.sel_offsets[-1])
+        out = dict(counts=b.counts, router_counts=r.counts, quota=b.quota, offsets=b.offsets, f=b.f, P=b.P,
+                   sel_offsets=b.sel_offsets, sel_ids=b.sel_ids[:total], dW=b.dW, dW1=step.rec.fc1.dW1,
+                   dx=step.rec.fc1.dx, dgate=step.rec.dgate, dlogits=r.dlogits, dxr=step.dxr, dWr=step.dWr,
+                   norm=step.clip.norm, P_router=r.P, f_router=r.f)
+        return {n: t.clone() for n, t in out.items()}, step.rec.summary()
+    finally:
+        step.close()
+
+
+@pytest.mark.parametrize("T,E,k,share", [(600, 8, 2, 0.5), (1500, 24, 4, 0.3), (333, 16, 4, 0.9), (2100, 40, 8, 0.05)])
+def test_padding_takes_no_part(T, E, k, share):
+    # the step of a padded batch against that of the batch without its padding
+    h, I = 64, 40
+    batch = _batch(T, E, k, h, I, T)
+    valid = torch.rand(T, generator=torch.Generator(device="cuda").manual_seed(E), device="cuda") < share
+    kept = valid.nonzero().flatten()
+    n = kept.numel()
+    pairs = (kept[:, None] * k + torch.arange(k, device="cuda")).flatten()
+    logits, g, phi, x, ab, W, W1, Wr = batch
+    alone, alone_summary = _step(n, E, k, h, I, (logits[kept], g[kept], phi[pairs], x[kept], ab[pairs], W, W1, Wr))
+    for t in (logits, g):
+        t[~valid] = float("nan")
+    pad_pairs = torch.ones(T * k, dtype=torch.bool, device="cuda")
+    pad_pairs[pairs] = False
+    phi[pad_pairs], ab[pad_pairs] = float("inf"), float("nan")
+    got, summary = _step(T, E, k, h, I, batch, valid.to(torch.uint8))
+    for name in ("counts", "router_counts", "quota", "offsets", "f", "sel_offsets", "dW", "dW1"):
+        assert torch.equal(got[name], alone[name]), name
+    assert torch.equal(got["counts"], got["router_counts"]) and torch.equal(got["f"], got["f_router"])
+    assert torch.allclose(got["P"], got["P_router"], rtol=2e-5, atol=0)
+    assert torch.equal(got["sel_ids"].long(), pairs[alone["sel_ids"].long()])
+    for name in ("dx", "dlogits", "dxr"):
+        assert torch.equal(got[name][kept], alone[name]) and not got[name][~valid].any(), name
+    assert torch.equal(got["dgate"][pairs], alone["dgate"]) and not got["dgate"][pad_pairs].any()
+    for name in ("N", "C", "slots", "dropped", "retained", "max_count", "min_count", "nonempty", "drop_rate", "rho_real"):
+        assert summary[name] == alone_summary[name], name
+    assert abs(summary["aux_unscaled"] - alone_summary["aux_unscaled"]) <= 2e-5 * alone_summary["aux_unscaled"]
+    # fp32 sums of the same products in another order
+    mag = alone["dlogits"].double().abs().t() @ x[kept].double().abs()
+    assert bool(((got["dWr"] - alone["dWr"]).abs() <= 2 * T * 2.0 ** -24 * mag).all())
+
+
+def test_no_token_of_a_batch_counts():
+    T, E, k, h, I = 100, 8, 2, 64, 32
+    batch = _batch(T, E, k, h, I, 5)
+    got, summary = _step(T, E, k, h, I, batch, torch.zeros(T, dtype=torch.uint8, device="cuda"))
+    assert summary["N"] == summary["C"] == summary["retained"] == 0
+    for name in ("counts", "quota", "offsets", "f", "P", "dW", "dW1", "dx", "dgate", "dlogits", "dxr", "dWr", "norm"):
+        assert not got[name].any(), name
+
+
+def test_rows_of_minus_infinity_take_no_part():
+    T, E, k, h, I = 200, 8, 2, 64, 32
+    batch = _batch(T, E, k, h, I, 6)
+    batch[0][::3] = -float("inf")
+    got, summary = _step(T, E, k, h, I, batch)
+    dead = torch.arange(T, device="cuda") % 3 == 0
+    assert summary["N"] == 2 * int((~dead).sum()) and torch.isfinite(got["P"]).all()
+    assert torch.equal(got["counts"], got["router_counts"]) and not got["dx"][dead].any()
