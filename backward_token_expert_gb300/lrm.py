@@ -67,6 +67,7 @@ EXPORTED = (
     "lrm_max_rows",
     "lrm_router_forward",
     "lrm_route_stats_counted",
+    "lrm_counted_rows",
     "lrm_router_backward",
     "lrm_gate_grad",
     "lrm_grad_table_size",
@@ -175,6 +176,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     sig.update({
         "lrm_router_forward": ([P, P, i32, P, Dims, i32, f32, f32, P, P, P, P, P, P, P, P, size, P], st),
         "lrm_route_stats_counted": ([P, P, P, P, P, Dims] + [i32] * 4 + [P] * 8 + [size, P], st),
+        "lrm_counted_rows": ([P, P, P, Dims, i32, P, P], st),
         "lrm_router_backward": ([P, P, i32, P, P, P, P, P, P, Dims, i32, f32, f32, P, i32, P], st),
         "lrm_gate_grad": ([P, P, P, P, P, Dims, i32, P, P], st),
         "lrm_grad_table_size": ([ctypes.POINTER(Tensor), i32, ctypes.POINTER(size)], st),
@@ -392,6 +394,11 @@ def lrm_route_stats_counted(ctx, logits, expert_idx, row_stats, losses, dims: Di
                                                   _ptr(counts), _ptr(offsets), _ptr(bucket), _ptr(P), _ptr(f),
                                                   _ptr(quota), _ptr(summary), _ptr(ws), ws_bytes, _stream(stream)),
            "lrm_route_stats_counted")
+
+
+def lrm_counted_rows(ctx, rows, row_stats, dims: Dims, width: int, out, stream=None) -> None:
+    _check(load_library().lrm_counted_rows(ctx, _ptr(rows), _ptr(row_stats), dims, width, _ptr(out), _stream(stream)),
+           "lrm_counted_rows")
 
 
 def lrm_router_backward(ctx, logits, logits_dtype: int, expert_idx, alpha, row_stats, dgate, f, losses, dims: Dims,

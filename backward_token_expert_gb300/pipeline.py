@@ -569,12 +569,19 @@ class TrainingStep:
         self.dxr = torch.zeros(T, h, dtype=torch.bfloat16, device=dev)
         self._dims_r = L.dims_of(T, 1, 1, E, h)  # the router as one expert: rows of width E, weight [E, h]
         self._segment = torch.tensor([0, T], dtype=torch.int32, device=dev)
+        self._masked = False  # whether the last route had a mask
+        self._x = None  # x with zeros in the rows of padding, made for the first masked batch
         self.clip = GradClip([self.rec.buf.dW, self.rec._fc1_buffers().dW1, self.dWr], ctx=self.rec.ctx)
 
     def route(self, logits, valid=None, stream=None):
         """Ids and gates of the batch (``router.expert_idx``, ``router.alpha``) and its losses.  The tokens
         that `valid` leaves out take no part in the backward either: capacity, quotas, selection and gradients
-        are those of a batch without them, and their rows of logits, g, phi and ab may hold anything."""
+        are those of a batch without them, and their rows of logits, g, phi, x and ab may hold anything."""
+        self._masked = valid is not None
+        if self._masked and self._x is None:
+            self._x = torch.empty(self.rec.T, self.rec.h, dtype=torch.bfloat16, device=self.dWr.device)
+            if not torch.cuda.is_current_stream_capturing():  # work on what the memory held before may be pending
+                torch.cuda.current_stream(self._x.device).synchronize()
         self.router.forward(logits, valid, stream)
 
     def backward(self, logits, g, phi, W, x, ab, W1, Wr, stream=None):
@@ -588,6 +595,9 @@ class TrainingStep:
         rec.fc1_backward(x, ab, W1, stream)
         r.backward(logits, rec.dgate, stream=stream)
         T = rec.T
+        if self._masked:  # dlogits holds zeros there, whose products with NaN would not be zeros
+            L.lrm_counted_rows(rec.ctx, x, r.row_stats, rec.dims, rec.h, self._x, stream)
+            x = self._x
         L.lrm_grouped_wgrad(rec.ctx, r.dlogits, x, self._segment, self._dims_r, T, 0, self.dWr, stream)
         L.lrm_grouped_dgrad(rec.ctx, r.dlogits, Wr, self._segment, self._dims_r, T, self.dxr, stream)
         self.clip.clip(self.max_norm, stream)

@@ -443,6 +443,16 @@ LRM_API lrm_status lrm_route_stats_counted(lrm_ctx* ctx, const float* logits, co
                                            void* stream);
 
 /*
+ * lrm_counted_rows: out[t] = rows[t] for the tokens that lrm_router_forward
+ * counted, zeros for the others, whose rows are not read: what a product with
+ * the logits' gradient (zeros in those rows) takes where the rows of padding may
+ * hold NaN or infinity.
+ *   rows, out [T, width] bf16, not overlapping, width a multiple of 8
+ */
+LRM_API lrm_status lrm_counted_rows(lrm_ctx* ctx, const uint16_t* rows, const float* row_stats, lrm_dims dims,
+                                    int32_t width, uint16_t* out, void* stream);
+
+/*
  * lrm_gate_grad: the gate weights' gradient on the retained pairs, in the form
  * the softmax's backward takes it: dgate[u] = alpha_u dL/dalpha_u.  With
  * y_t = sum_u alpha_u W_e phi_u and dphi_c[r] = (alpha_u g_t) W_e (the rows of

@@ -749,3 +749,41 @@ def test_refusals_of_the_counted_route_stats():
             call(**kw)
         assert ei.value.code == code, kw
     rec.close()
+
+
+@pytest.mark.parametrize("T,width", [(1, 8), (7, 264), (3000, 136), (500, 2048), (33, 65536)])
+def test_counted_rows(T, width):
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import Router
+
+    r = Router(T, 8, 2, True, AUX, Z)
+    counted = torch.rand(T, generator=torch.Generator(device="cuda").manual_seed(T), device="cuda") < 0.5
+    r.row_stats[:, 0], r.row_stats[:, 1] = 0.0, counted.float()
+    rows = torch.randn(T, width, device="cuda").to(torch.bfloat16)
+    rows[~counted] = float("nan")
+    out = torch.full_like(rows, 5.0)
+    L.lrm_counted_rows(r.ctx, rows, r.row_stats, r.dims, width, out)
+    assert torch.equal(out[counted], rows[counted]) and not out[~counted].any()
+    r.row_stats[0, 1] = float("nan")  # a counted token with a NaN logit
+    L.lrm_counted_rows(r.ctx, rows, r.row_stats, r.dims, width, out)
+    assert torch.equal(out[0].view(torch.int16), rows[0].view(torch.int16))
+
+
+def test_refusals_of_counted_rows():
+    from backward_token_expert_gb300 import lrm as L
+    from backward_token_expert_gb300.pipeline import Router
+
+    r = Router(4, 8, 2, True, AUX, Z)
+    x, out = (torch.zeros(4, 16, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    inv, al = L.LRM_ERR_INVALID_ARG, L.LRM_ERR_ALIGN
+    for ctx, rows, stats, dims, width, to, code in [
+            (None, x, r.row_stats, r.dims, 16, out, inv), (r.ctx, None, r.row_stats, r.dims, 16, out, inv),
+            (r.ctx, x, None, r.dims, 16, out, inv), (r.ctx, x, r.row_stats, r.dims, 16, None, inv),
+            (r.ctx, x, r.row_stats, r.dims, 12, out, inv), (r.ctx, x, r.row_stats, r.dims, 0, out, inv),
+            (r.ctx, x, r.row_stats, r.dims, 65544, out, inv), (r.ctx, x.data_ptr() + 2, r.row_stats, r.dims, 16, out, al),
+            (r.ctx, x, r.row_stats.data_ptr() + 4, r.dims, 16, out, al),
+            (r.ctx, x, r.row_stats, L.dims_of(4, 8, 9, 8, 8), 16, out, L.LRM_ERR_SHAPE)]:
+        with pytest.raises(L.LrmError) as ei:
+            L.lrm_counted_rows(ctx, rows, stats, dims, width, to)
+        assert ei.value.code == code
+    L.lrm_counted_rows(r.ctx, None, None, L.dims_of(0, 8, 2, 8, 8), 16, None)

@@ -203,3 +203,40 @@ def test_rows_of_minus_infinity_take_no_part():
     dead = torch.arange(T, device="cuda") % 3 == 0
     assert summary["N"] == 2 * int((~dead).sum()) and torch.isfinite(got["P"]).all()
     assert torch.equal(got["counts"], got["router_counts"]) and not got["dx"][dead].any()
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -float("inf")])
+def test_garbage_in_the_paddings_inputs_reaches_no_result(fill):
+    T, E, k, h, I = 500, 16, 3, 72, 40
+    batch = _batch(T, E, k, h, I, 8)
+    valid = torch.rand(T, generator=torch.Generator(device="cuda").manual_seed(9), device="cuda") < 0.6
+    want, _ = _step(T, E, k, h, I, batch, valid.to(torch.uint8))
+    logits, g, phi, x, ab, *_ = batch
+    for t in (logits, g, x):
+        t[~valid] = fill
+    phi.view(T, k, I)[~valid] = fill
+    ab.view(T, k, 2 * I)[~valid] = fill
+    got, _ = _step(T, E, k, h, I, batch, valid.to(torch.uint8))
+    for name, t in want.items():
+        assert torch.isfinite(t.float()).all() and torch.equal(got[name], t), name
+
+
+def test_a_step_with_and_without_a_mask_in_turn():
+    from backward_token_expert_gb300.pipeline import TrainingStep
+
+    T, E, k, h, I = 300, 8, 2, 64, 32
+    logits, g, phi, x, ab, W, W1, Wr = _batch(T, E, k, h, I, 10)
+    valid = torch.ones(T, dtype=torch.uint8, device="cuda")
+    valid[::4] = 0
+    step = TrainingStep(T, E, k, h, I, max_norm=1e9)
+    try:
+        got = []
+        for v in (None, valid, None, valid):
+            step.route(logits, v)
+            step.backward(logits, g, phi, W, x, ab, W1, Wr)
+            got.append([t.clone() for t in (step.dWr, step.rec.buf.dW, step.rec.fc1.dW1, step.dxr)])
+        assert step.device_status() == 0
+        assert all(torch.equal(a, b) for i in (0, 1) for a, b in zip(got[i], got[i + 2]))
+        assert not torch.equal(got[0][0], got[1][0])
+    finally:
+        step.close()
