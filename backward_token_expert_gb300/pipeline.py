@@ -210,10 +210,13 @@ class Recalibration:
         pairs that were not retained), after dgrad and compact: what
         ``Router.backward`` takes."""
         b = self.buf
+        L.lrm_gate_grad(self.ctx, b.dphi_c, b.phi_c, b.sel_offsets, b.sel_ids, self.dims, self.max_rows,
+                        self._dgate_buffer(), stream)
+        return self.dgate
+
+    def _dgate_buffer(self):
         if getattr(self, "dgate", None) is None:
-            self.dgate = torch.empty(max(1, self.N), dtype=torch.float32, device=b.dW.device)[: self.N]
-        L.lrm_gate_grad(self.ctx, b.dphi_c, b.phi_c, b.sel_offsets, b.sel_ids, self.dims, self.max_rows, self.dgate,
-                        stream)
+            self.dgate = torch.empty(max(1, self.N), dtype=torch.float32, device=self.buf.dW.device)[: self.N]
         return self.dgate
 
     def wgrad(self, stream=None, accumulate=0):
@@ -571,6 +574,9 @@ class TrainingStep:
         self._segment = torch.tensor([0, T], dtype=torch.int32, device=dev)
         self._masked = False  # whether the last route had a mask
         self._x = None  # x with zeros in the rows of padding, made for the first masked batch
+        # every buffer of the step is made before the clip's list, which waits for the current stream: what is pending
+        # there on memory that they reuse, and their fills, do not come after another stream's step
+        self.rec._dgate_buffer()
         self.clip = GradClip([self.rec.buf.dW, self.rec._fc1_buffers().dW1, self.dWr], ctx=self.rec.ctx)
 
     def route(self, logits, valid=None, stream=None):

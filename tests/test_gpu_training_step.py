@@ -240,3 +240,34 @@ def test_a_step_with_and_without_a_mask_in_turn():
         assert not torch.equal(got[0][0], got[1][0])
     finally:
         step.close()
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_a_first_step_on_another_stream_beside_a_busy_one(masked):
+    # work pending on the current stream over memory that it has given back: no buffer of the step may take it
+    from backward_token_expert_gb300.pipeline import TrainingStep
+
+    T, E, k, h, I = 300, 8, 2, 64, 32
+    logits, g, phi, x, ab, W, W1, Wr = _batch(T, E, k, h, I, 11)
+    valid = (torch.arange(T, device="cuda") % 4 != 0).to(torch.uint8) if masked else None
+    step, want = TrainingStep(T, E, k, h, I, max_norm=1e9), TrainingStep(T, E, k, h, I, max_norm=1e9)
+    try:
+        s = torch.cuda.Stream()
+        want.route(logits, valid)
+        want.backward(logits, g, phi, W, x, ab, W1, Wr)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)
+        for n in (T * k, T * h):  # of the gate gradients' size, and of x's
+            held = [torch.empty(n * b, dtype=torch.uint8, device="cuda") for b in (2, 4) for _ in range(20)]
+            [t.fill_(255) for t in held]
+            del held
+        step.route(logits, valid, s)
+        step.backward(logits, g, phi, W, x, ab, W1, Wr, s)
+        torch.cuda.synchronize()
+        assert step.device_status() == 0
+        for a, b in ((step.rec.dgate, want.rec.dgate), (step.dWr, want.dWr), (step.dxr, want.dxr),
+                     (step.rec.buf.dW, want.rec.buf.dW), (step.rec.fc1.dx, want.rec.fc1.dx)):
+            assert torch.equal(a, b)
+    finally:
+        step.close()
+        want.close()
