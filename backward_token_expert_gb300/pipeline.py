@@ -441,6 +441,12 @@ def _dense(t) -> bool:
     return True
 
 
+def _same_order(a, b) -> bool:
+    """Whether two tensors of one shape hold their elements in the same order: equal strides, but in
+    dimensions of one element, where a stride leads nowhere."""
+    return a.stride() == b.stride() or all(x == y for x, y, n in zip(a.stride(), b.stride(), a.shape) if n != 1)
+
+
 _clip_contexts: dict[int, int] = {}
 
 
@@ -482,7 +488,7 @@ class GradClip:
             n, src = g.numel(), g.data_ptr()
             dst = src
             if o is not g:
-                if o.dtype != g.dtype or o.shape != g.shape or (n and o.stride() != g.stride()):
+                if o.dtype != g.dtype or o.shape != g.shape or (n and not _same_order(o, g)):
                     raise ValueError("an output needs its gradient's type, shape and strides")
                 dst = o.data_ptr()
             if n:

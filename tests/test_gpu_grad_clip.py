@@ -516,3 +516,14 @@ def test_memory_of_a_dropped_list_stays_until_its_stream_is_done():
         assert not any(a <= at < b for a, b in spans)
     s.synchronize()
     assert abs(float(out[0]) * 0.5 * math.sqrt(300000) - 0.5) <= 2 * REL
+
+
+def test_strides_of_dimensions_of_one_element():
+    # a column or a row cut out of a larger buffer: its stride in the dimension of one element is the buffer's
+    g = torch.linspace(-1.0, 1.0, 40, device="cuda")
+    whole = torch.full((3, 40), 7.0, device="cuda")
+    check([g.view(1, 40), g.clone().view(40, 1), g.clone().view(1, 8, 1, 5)], 0.5,
+          outs=[whole[1:2], torch.empty(40, device="cuda").as_strided((40, 1), (1, 40)),
+                torch.empty(40, device="cuda").as_strided((1, 8, 1, 5), (999, 5, 7, 1))])
+    assert bool((whole[0] == 7.0).all()) and bool((whole[2] == 7.0).all())
+    check([whole[1:2]], 0.1, outs=[torch.empty(1, 40, device="cuda")])
