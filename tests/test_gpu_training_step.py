@@ -271,3 +271,56 @@ def test_a_first_step_on_another_stream_beside_a_busy_one(masked):
     finally:
         step.close()
         want.close()
+
+
+@pytest.mark.parametrize("T,E,k,h,I,masked,dead", [(256, 8, 2, 64, 32, False, 0), (1000, 24, 3, 136, 72, True, 3),
+                                                  (700, 16, 4, 64, 40, True, 1)])
+def test_selection_and_fc1_side_against_the_oracle(T, E, k, h, I, masked, dead):
+    # quotas and selection from the oracle's statistics of the counted tokens; dW1, dx and the empty experts' zeros
+    # from the GPU's own input-gradient rows, whose products are held to the path's bound
+    from backward_token_expert_gb300.pipeline import TrainingStep
+
+    inp = custom_inputs(T=T, E=E, k=k, h=h, I=I, s=1.0, rho=Fraction(3, 4), seed=62, dead=dead)
+    w, f1 = inp.workload, fc1_inputs(inp.workload)
+    rng = np.random.default_rng(8)
+    Wr = f32_to_bf16_bits((rng.standard_normal((E, h)) * 0.05).astype(np.float32))
+    valid = rng.random(T) < 0.6 if masked else np.ones(T, bool)
+    step = TrainingStep(T, E, k, h, I, w.cf, w.rho, 0.5, 0.1, max_norm=1e9)
+    try:
+        logits = torch.from_numpy(inp.logits).cuda()
+        step.route(logits, torch.from_numpy(valid.astype(np.uint8)).cuda() if masked else None)
+        step.backward(logits, *[_dev(a) for a in (inp.g, inp.phi, inp.W, f1.x, f1.ab, f1.W1, Wr)])
+        torch.cuda.synchronize()
+        assert step.device_status() == 0
+        b = step.rec.buf
+        so = b.sel_offsets.cpu().numpy().astype(np.int64)
+        ids = b.sel_ids[: so[-1]].cpu().numpy().astype(np.int64)
+        quota, score, idx = b.quota.cpu().numpy(), b.score.cpu().numpy()[: T * k], step.router.expert_idx.cpu().numpy()
+        dphi_c = O.bf16_to_f64(bf16_np(b.dphi_c[: so[-1]]))
+        dW, dW1 = b.dW.cpu().numpy(), step.rec.fc1.dW1.cpu().numpy()
+        dx = O.bf16_to_f64(bf16_np(step.rec.fc1.dx))
+    finally:
+        step.close()
+
+    kept = np.flatnonzero(valid)
+    pairs = (kept[:, None] * k + np.arange(k)).reshape(-1)
+    st = O.route_stats(inp.logits[kept], idx[kept], E, w.cf, w.rho)
+    assert np.array_equal(quota, st["quota"])
+    ref_so, ref_ids = O.select(score[pairs].astype(np.float64), idx[kept], E, st["quota"])
+    assert np.array_equal(so, ref_so) and np.array_equal(ids, pairs[ref_ids])
+    ref_dW1, ref_rows = O.fc1_backward(O.bf16_to_f64(f1.x[ids // k]), O.bf16_to_f64(f1.ab[ids]),
+                                       {e: O.bf16_to_f64(f1.W1[e]) for e in range(E)}, dphi_c, so, np.arange(ids.size),
+                                       E, 1)
+    empty = 0
+    for e in range(E):
+        if so[e] == so[e + 1]:
+            empty += 1
+            assert np.all(dW[e] == 0) and np.all(dW1[e] == 0)
+        else:
+            assert rel_fro(dW1[e], ref_dW1[e]) <= RTOL
+    assert empty >= dead
+    ref_dx = O.combine_pairs(ref_rows, ids, T, k)
+    assert rel_fro(dx, ref_dx) <= RTOL
+    none = np.ones(T, bool)
+    none[ids // k] = False
+    assert np.all(dx[none] == 0) and (not masked or none[~valid].all())
