@@ -58,7 +58,11 @@ constexpr float LN2 = 0.6931471805599453f;
 // Lanes per token (G) and groups of four logits per lane (C): the fewest lanes
 // that have a slot each and at most 16 logits (32 for the widest layers), so
 // that what a token costs once (reductions, slots, addresses) is shared by the
-// tokens of a warp.  At E = 128 a warp a token took 346 instructions a token in
+// tokens of a warp.  From 8 lanes on C is 1, 2, 3 or 4: three groups where two do not reach and
+// four would be a quarter empty (65536 tokens, k = 6, forward / backward with three and with four:
+// E = 96 fp32 19.1 / 11.6 and 21.2 / 11.8 us, bf16 16.8 / 7.9 and 19.0 / 8.5; E = 160 fp32 32.3 / 18.0
+// and 36.3 / 18.3, bf16 29.6 / 14.1 and 33.7 / 16.0; E = 384 fp32 44.3 / 33.8 and 51.0 / 35.6, bf16
+// 44.9 / 25.6 and 52.9 / 28.4).  At E = 128 a warp a token took 346 instructions a token in
 // the forward (45 us for 131072 tokens) and 31.3 us in the backward; four tokens a
 // warp take 175 (37 us; 35 with merged lists) and 25 us.
 template <int N>
@@ -67,7 +71,8 @@ using Int = std::integral_constant<int, N>;
 struct Split {
   int G, C;
 };
-constexpr Split kSplits[] = {{4, 1}, {8, 1}, {8, 2}, {8, 4}, {16, 1}, {16, 2}, {16, 3}, {16, 4}, {32, 1}, {32, 2}, {32, 4}, {32, 8}};
+constexpr Split kSplits[] = {{4, 1}, {8, 1}, {8, 2}, {8, 3}, {8, 4}, {16, 1}, {16, 2}, {16, 3}, {16, 4},
+                              {32, 1}, {32, 2}, {32, 3}, {32, 4}, {32, 8}};
 Split split_of(int E, int k) {
   for (const Split& s : kSplits)
     if (E <= 4 * s.G * s.C && k <= s.G) return s;
@@ -83,6 +88,7 @@ lrm_status with_split(int E, int k, Run run) {
     case 4 * 16 + 1: return pick(Int<4>{}, Int<1>{});
     case 8 * 16 + 1: return pick(Int<8>{}, Int<1>{});
     case 8 * 16 + 2: return pick(Int<8>{}, Int<2>{});
+    case 8 * 16 + 3: return pick(Int<8>{}, Int<3>{});
     case 8 * 16 + 4: return pick(Int<8>{}, Int<4>{});
     case 16 * 16 + 1: return pick(Int<16>{}, Int<1>{});
     case 16 * 16 + 2: return pick(Int<16>{}, Int<2>{});
@@ -90,6 +96,7 @@ lrm_status with_split(int E, int k, Run run) {
     case 16 * 16 + 4: return pick(Int<16>{}, Int<4>{});
     case 32 * 16 + 1: return pick(Int<32>{}, Int<1>{});
     case 32 * 16 + 2: return pick(Int<32>{}, Int<2>{});
+    case 32 * 16 + 3: return pick(Int<32>{}, Int<3>{});
     case 32 * 16 + 4: return pick(Int<32>{}, Int<4>{});
   }
   return pick(Int<32>{}, Int<8>{});

@@ -787,3 +787,13 @@ def test_refusals_of_counted_rows():
             L.lrm_counted_rows(ctx, rows, stats, dims, width, to)
         assert ei.value.code == code
     L.lrm_counted_rows(r.ctx, None, None, L.dims_of(0, 8, 2, 8, 8), 16, None)
+
+
+# three groups of four logits a lane, at 8, 16 and 32 lanes, and the sizes on both sides
+@pytest.mark.parametrize("E,k", [(64, 6), (65, 8), (68, 1), (77, 5), (93, 8), (96, 3), (97, 8), (129, 9), (190, 16), (192, 8),
+                                 (193, 10), (256, 17), (257, 8), (258, 32), (300, 20), (381, 4), (384, 8), (385, 12)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_three_groups_a_lane(E, k, dtype):
+    run(700, E, k, dtype, renorm=bool(E % 2), seed=E + k)
+    x = np.round(np.random.default_rng(E).standard_normal((90, E)) * 2) / 2  # ties
+    run(90, E, k, dtype, logits=torch.from_numpy(x.astype(np.float32)).to(DT[dtype]), seed=E)
