@@ -323,18 +323,18 @@ def _require(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
-def _hold(seen: set, stream, tensors):
+def _stream_of(owner, stream):
     """The raw handle of `stream` (None: the current one) for a call that uses
-    `tensors`.  The first call on a stream that is not in `seen` tells the
-    allocator, so that their memory is not given away while that stream still
-    works on it.  A raw handle's owner keeps them alive instead: the allocator
-    may not use it once the owner has destroyed it."""
+    ``owner._held()``.  The first call on a stream that is not in
+    ``owner._streams`` tells the allocator, so that their memory is not given
+    away while that stream still works on it.  A raw handle's owner keeps them
+    alive instead: the allocator may not use it once it has been destroyed."""
     raw = L._stream(stream)
-    if raw not in seen:
-        seen.add(raw)
+    if raw not in owner._streams:
+        owner._streams.add(raw)
         if not isinstance(stream, int):
             s = torch.cuda.current_stream() if stream is None else stream
-            for t in tensors:
+            for t in owner._held():
                 t.record_stream(s)
     return raw
 
@@ -381,9 +381,9 @@ class Router:
         if not torch.cuda.is_current_stream_capturing():
             home.synchronize()
 
-    def _on(self, stream):
-        return _hold(self._streams, stream, [self.expert_idx, self.alpha, self.row_stats, self.counts, self.f, self.P,
-                                             self._losses, self.dlogits, self.ws])
+    def _held(self):
+        return (self.expert_idx, self.alpha, self.row_stats, self.counts, self.f, self.P, self._losses, self.dlogits,
+                self.ws)
 
     def close(self):
         if self._own_ctx and getattr(self, "ctx", None):
@@ -404,7 +404,7 @@ class Router:
             _require(valid, "valid", torch.uint8, (self.T,), self.device)
         L.lrm_router_forward(self.ctx, logits, _DTYPES[self.dtype], valid, self.dims, self.renorm, self.aux_coef,
                              self.z_coef, self.expert_idx, self.alpha, self.row_stats, self.counts, self.f, self.P,
-                             self._losses, self.ws, self.ws.numel(), self._on(stream))
+                             self._losses, self.ws, self.ws.numel(), _stream_of(self, stream))
 
     @property
     def counted(self):
@@ -424,7 +424,7 @@ class Router:
             _require(f, "f", torch.float32, (self.E,), self.device)
         L.lrm_router_backward(self.ctx, logits, _DTYPES[self.dtype], self.expert_idx, self.alpha, self.row_stats,
                               dgate, self.f if f is None else f, self._losses, self.dims, self.renorm, self.aux_coef,
-                              self.z_coef, self.dlogits, _DTYPES[self.dlogits_dtype], self._on(stream))
+                              self.z_coef, self.dlogits, _DTYPES[self.dlogits_dtype], _stream_of(self, stream))
         return self.dlogits
 
     def device_status(self, stream=None) -> int:
@@ -530,16 +530,16 @@ class GradClip:
         except Exception:
             pass
 
-    def _on(self, stream):
-        return _hold(self._streams, stream, [self.table, self._stats, *self.grads, *self.outs])
+    def _held(self):
+        return self.table, self._stats, *self.grads, *self.outs
 
     def measure(self, stream=None) -> None:
         """norm of all gradients, nothing clipped."""
-        L.lrm_grad_norm(self.ctx, self.list, self._stats, self._on(stream))
+        L.lrm_grad_norm(self.ctx, self.list, self._stats, _stream_of(self, stream))
 
     def clip(self, max_norm: float, stream=None) -> None:
         """norm, and every gradient times min(1, max_norm / norm) into its output."""
-        L.lrm_grad_clip(self.ctx, self.list, max_norm, self._stats, self._on(stream))
+        L.lrm_grad_clip(self.ctx, self.list, max_norm, self._stats, _stream_of(self, stream))
 
     def device_status(self, stream=None) -> int:
         """Flags (1 << code) that calls on this list raised on the device since the last read."""
