@@ -27,9 +27,12 @@
 // in fp32 while its largest magnitude lies in [2^-56, 2^52]: no sum of squares
 // overflows, and a square that fp32 holds as a subnormal is off by at most
 // 2^-150, 2^-38 of the largest square.  Other batches are squared in fp64
-// (exact); batches of zeros add nothing.  A lane's few batches in gc_small and
-// gc_hold and the sums of a block are added in fp32 too, the many batches of
-// gc_norm and the blocks' sums in fp64.
+// (exact); batches of zeros add nothing.  A lane of gc_norm adds its many batches
+// in fp64.  The other sums (of a lane's one to three batches in gc_small and gc_hold,
+// over lanes, warps and blocks) are added in fp32 where fp32 holds every term and the
+// sum with room to spare, in fp64 where not.  On the way to the norm a square passes at most
+// 18 roundings in its batch, 22 in those sums and one in the root: 21 of 2^-24 on
+// the norm at the worst, 1.3e-6.
 #include <math.h>
 #include <stdlib.h>
 #include <string.h>

@@ -103,10 +103,10 @@ lrm_status with_split(int E, int k, Run run) {
 }
 
 // Threads of a block of rf_rows, one block an SM: as many as the registers of C
-// groups allow without spilling (640 threads of 96 registers at C = 4 gain 1 %
-// at 131072 x 128 and lose 10 % at 16384 x 128; blocks sized to the batch, so
-// that a small one has a warp on every SM, lose 4 % at 8192 x 128: rf_sums then
-// adds more rows).
+// groups allow (three instantiations of C = 4 spill one to three of them).  640
+// threads of 96 registers at C = 4 gain 1 % at 131072 x 128 and lose 10 % at
+// 16384 x 128; blocks sized to the batch, so that a small one has a warp on every
+// SM, lose 4 % at 8192 x 128: rf_sums then adds more rows.
 __host__ __device__ constexpr int rf_threads(int C) { return C == 1 ? 768 : C <= 4 ? 512 : 256; }
 
 struct RouterLayout {
@@ -245,8 +245,9 @@ __device__ __forceinline__ void store_four(TO* __restrict__ row, int e0, int E, 
 }
 
 // e^x for x <= 0 as 2^(x log2 e): the product's rounding is 2^-24 |x| log2 e in
-// the exponent, so the relative error is about 6e-8 |x| + 2 ulp, largest where
-// the term itself is smallest; results below 2^-126 are 0.
+// the exponent and the constant's 1.3e-8 |x| log2 e, so the relative error is up to
+// 7.3e-8 |x| + 2 ulp, largest where the term itself is smallest; results below
+// 2^-126 are 0.
 __device__ __forceinline__ float exp_neg(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * LOG2E));

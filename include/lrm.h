@@ -406,7 +406,10 @@ LRM_API lrm_status lrm_route_stats_noalloc(lrm_ctx* ctx, const float* logits, co
  * token gets k distinct experts; one that is not counted gets alpha = 0 and
  * row_stats = (0, 0), and no value of its logits reaches any other output.
  * Without a counted token f, P and the losses are 0.  +inf and NaN logits of
- * a counted token give NaN in its gates and in the sums, as the formulas do.
+ * a counted token give NaN where the formulas do: in s, P and the losses, in gates
+ * that divide by s (renorm = 0), and in renormalised gates if one has a slot.
+ * exp is 2^(x log2 e), within 7.3e-8 |x| + 2.4e-7 of its value, relative, and 0 below 2^-126;
+ * quotients by s and by the slots' sum are within 2^-22.
  * The same inputs give the same bits.
  *   logits     [T, E] fp32 or bf16 (logits_dtype, an lrm_dtype)
  *   valid      [T]    uint8, or NULL: every token is valid
@@ -472,7 +475,8 @@ LRM_API lrm_status lrm_gate_grad(lrm_ctx* ctx, const uint16_t* dphi_c, const uin
  *   dlogits[t,e] = aux_coef E / Tc p_e (f_e - sum_i f_i p_i) + 2 z_coef / Tc lse p_e
  *                  + dgate[t,j] - alpha[t,j] S where e is slot j's expert (renorm = 1), or
  *                  + dgate[t,j] there and - p_e S everywhere (renorm = 0),
- * and a token that is not counted gets zeros.  f is a constant of the gradient
+ * and a token that is not counted gets zeros (exp and quotients as in the forward,
+ * ln s within 2.4e-7, relative above s = 2).  f is a constant of the gradient
  * (a count has none); it may be the caller's own, for example of a larger batch.
  *   logits as given to the forward; expert_idx, alpha, row_stats, f and losses
  *   (only its token count is read) as the forward wrote them
@@ -508,18 +512,21 @@ LRM_API lrm_status lrm_router_backward(lrm_ctx* ctx, const void* logits, int32_t
  * nonfinite is 1, coef is 1 and norm is that infinity or NaN: the caller skips
  * its step.  max_norm >= 0; infinity never clips.
  *
- * Squares are summed so that neither large nor small values are lost (fp64
- * where a square would leave fp32's range, and across batches of elements);
- * the order is fixed, so the same inputs give the same bits.  Calls on one
- * list share its table: serialise them.  Lists up to 24 MB run as one cooperative
- * launch, whose blocks wait for one another; that wait and those on copies are
- * bounded (lrm_set_wait_budget).  One that runs out sets LRM_ERR_TIMEOUT, in the
- * context's status word and in the list's own, and
- * leaves norm = NaN and nonfinite = 1, so that a caller who skips such a step
- * skips this one, and the list stays usable (with a budget of 0 the blocks of
- * one launch never wait for one another, so it always runs out).  Lists up to 24 MB are then left
- * alone (coef = 1, no dst written); of longer ones, whose copies run while they
- * are scaled, some values may have been written times the coef that stats holds.
+ * Squares are summed so that neither large nor small values are lost: in fp32
+ * where it holds them and their sums, else in fp64; the norm is within 1.3e-6
+ * (relative) of the exact one.  The order is fixed, so the same inputs give the
+ * same bits.  Calls on one list share its table: serialise them.
+ *
+ * Lists up to 512 KB (in at most 128 runs) take one cluster of blocks, those up to
+ * 24 MB (in at most 7296 runs of up to 4 KB of a tensor each) one cooperative launch
+ * whose blocks wait for one another, others two launches.  The wait for the other
+ * blocks and those on copies (lists up to 24 MB or beyond 128 MB) are bounded
+ * (lrm_set_wait_budget; with a budget of 0 blocks never wait for one another).
+ * One that runs out sets LRM_ERR_TIMEOUT, in the context's status word and in the
+ * list's own, and leaves norm = NaN and nonfinite = 1, so that a caller who skips
+ * such a step skips this one; the list stays usable.  The cooperative launch then
+ * writes no dst (coef = 1); beyond 128 MB, where copies run while values are scaled,
+ * some of them may have been written, times the coef that stats holds.
  * lrm_grad_list_status synchronises `stream`, returns the list's word in *flags and
  * clears it, as lrm_get_device_status does with the context's.
  */
