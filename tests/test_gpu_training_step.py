@@ -324,3 +324,24 @@ def test_selection_and_fc1_side_against_the_oracle(T, E, k, h, I, masked, dead):
     none = np.ones(T, bool)
     none[ids // k] = False
     assert np.all(dx[none] == 0) and (not masked or none[~valid].all())
+
+
+def test_statistics_of_the_counted_tokens_on_a_side_stream():
+    from backward_token_expert_gb300.pipeline import Recalibration, Router
+
+    T, E, k, h, I = 900, 16, 4, 64, 40
+    logits, g, phi, _, _, W, _, _ = _batch(T, E, k, h, I, 12)
+    valid = (torch.arange(T, device="cuda") % 3 != 0).to(torch.uint8)
+    rec = Recalibration(T, E, k, h, I)
+    r = Router(T, E, k, ctx=rec.ctx)
+    try:
+        r.forward(logits, valid)
+        got = []
+        for side in (None, torch.cuda.Stream()):
+            rec.run(logits, r.expert_idx, g, phi, r.alpha, W, side_stream=side, counted=r.counted)
+            got.append([t.clone() for t in (rec.buf.counts, rec.buf.quota, rec.buf.sel_offsets, rec.buf.dW)])
+        assert rec.device_status() == 0 and torch.equal(got[0][0], r.counts)
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+    finally:
+        r.close()
+        rec.close()
