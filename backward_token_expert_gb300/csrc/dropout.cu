@@ -1,0 +1,161 @@
+// Dropout with a residual, out_i = residual_i + (kept_i ? x_i / (1 - p) : 0),
+// whose mask is never stored: element i is kept unless word i mod 4 of
+// Philox4x32-10 (Salmon, Moraes, Dror and Shaw, SC 2011) at counter
+// (i div 4, offset) with the seed as key is below floor(p 2^32).  The backward
+// draws the same mask again: it is the same call on the gradient.
+//
+// One read of x and residual, one write: memory bounds it as long as the ten
+// rounds (two 32 x 32 -> 64 bit products and four exclusive ors for four
+// elements each) hide behind it.  A thread has 16 bytes of each operand, two
+// Philox blocks in bf16 and one in fp32; the ten round keys are the same for
+// all threads and are computed once.
+#include "lrm_internal.cuh"
+#include "vec.cuh"
+
+namespace lrm {
+namespace {
+
+constexpr int DR_THREADS = 256;
+
+__device__ __forceinline__ void philox4x32_10(uint64_t block, uint64_t offset, uint64_t seed, uint32_t (&c)[4]) {
+  c[0] = static_cast<uint32_t>(block);
+  c[1] = static_cast<uint32_t>(block >> 32);
+  c[2] = static_cast<uint32_t>(offset);
+  c[3] = static_cast<uint32_t>(offset >> 32);
+  uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t p0 = static_cast<uint64_t>(c[0]) * 0xD2511F53u, p1 = static_cast<uint64_t>(c[2]) * 0xCD9E8D57u;
+    c[0] = static_cast<uint32_t>(p1 >> 32) ^ c[1] ^ k0;
+    c[1] = static_cast<uint32_t>(p1);
+    c[2] = static_cast<uint32_t>(p0 >> 32) ^ c[3] ^ k1;
+    c[3] = static_cast<uint32_t>(p0);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+
+struct DropoutArgs {
+  uint64_t seed, offset;
+  const uint64_t* step;  // device value added to offset, or NULL
+  uint32_t last;         // the largest word that drops its element
+  float scale;           // 1 / (1 - p)
+};
+
+template <typename T>
+__device__ __forceinline__ float to_float(T v);
+template <>
+__device__ __forceinline__ float to_float<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ float to_float<uint16_t>(uint16_t v) {
+  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ uint16_t from_float<uint16_t>(float v) {
+  const __nv_bfloat16 b = __float2bfloat16_rn(v);
+  return *reinterpret_cast<const uint16_t*>(&b);
+}
+
+// DROP = false: p = 0, nothing is drawn.  VECTOR: 16-byte accesses.
+template <typename T, bool DROP, bool VECTOR>
+__global__ void __launch_bounds__(DR_THREADS)
+    dropout_kernel(const T* x, const T* residual, long long n, const __grid_constant__ DropoutArgs a, T* out) {
+  constexpr int N = 16 / sizeof(T);
+  grid_dependency_wait();
+  const uint64_t offset = a.offset + (a.step != nullptr ? __ldg(a.step) : 0);
+  const long long items = (n + N - 1) / N;
+  for (long long i = static_cast<long long>(blockIdx.x) * DR_THREADS + threadIdx.x; i < items;
+       i += static_cast<long long>(gridDim.x) * DR_THREADS) {
+    const long long e0 = i * N;
+    const bool whole = VECTOR && e0 + N <= n;
+    T xv[N], rv[N];
+    if (whole) {
+      // plain loads: out may be x or residual
+      *reinterpret_cast<uint4*>(xv) = *reinterpret_cast<const uint4*>(x + e0);
+      if (residual != nullptr) *reinterpret_cast<uint4*>(rv) = *reinterpret_cast<const uint4*>(residual + e0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        xv[j] = e0 + j < n ? x[e0 + j] : T(0);
+        rv[j] = residual != nullptr && e0 + j < n ? residual[e0 + j] : T(0);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < N / 4; ++b) {
+      uint32_t w[4];
+      if (DROP) philox4x32_10(static_cast<uint64_t>(i) * (N / 4) + b, offset, a.seed, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int m = b * 4 + j;
+        const float r = residual != nullptr ? to_float(rv[m]) : 0.0f;
+        const float v = residual != nullptr ? fmaf(to_float(xv[m]), a.scale, r) : to_float(xv[m]) * a.scale;
+        xv[m] = from_float<T>(!DROP || w[j] > a.last ? v : r);
+      }
+    }
+    if (whole) {
+      *reinterpret_cast<uint4*>(out + e0) = *reinterpret_cast<const uint4*>(xv);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (e0 + j < n) out[e0 + j] = xv[j];
+    }
+  }
+}
+
+template <typename T, bool DROP, bool VECTOR>
+lrm_status launch(lrm_ctx* ctx, const void* x, const void* residual, long long n, const DropoutArgs& a, void* out,
+                  cudaStream_t s) {
+  auto kern = dropout_kernel<T, DROP, VECTOR>;
+  static thread_local int dev = -1, cap = 0;
+  if (dev != ctx->device) {
+    cap = resident_grid(ctx, kern, DR_THREADS, 0);
+    dev = ctx->device;
+  }
+  constexpr long long per = static_cast<long long>(DR_THREADS) * (16 / sizeof(T));
+  const long long need = (n + per - 1) / per;
+  return launch_dependent(kern, static_cast<int>(need < cap ? need : cap), DR_THREADS, 0, 0, s,
+                          static_cast<const T*>(x), static_cast<const T*>(residual), n, a, static_cast<T*>(out));
+}
+
+template <typename T>
+lrm_status dispatch(lrm_ctx* ctx, const void* x, const void* residual, long long n, bool drop, const DropoutArgs& a,
+                    void* out, cudaStream_t s) {
+  const bool vec = aligned(x, 16) && aligned(out, 16) && aligned(residual, 16);
+  if (drop)
+    return vec ? launch<T, true, true>(ctx, x, residual, n, a, out, s)
+               : launch<T, true, false>(ctx, x, residual, n, a, out, s);
+  return vec ? launch<T, false, true>(ctx, x, residual, n, a, out, s)
+             : launch<T, false, false>(ctx, x, residual, n, a, out, s);
+}
+
+}  // namespace
+}  // namespace lrm
+
+using namespace lrm;
+
+extern "C" lrm_status lrm_dropout_add(lrm_ctx* ctx, const void* x, const void* residual, int32_t dtype, int64_t n,
+                                      double p, uint64_t seed, uint64_t offset, const uint64_t* step, void* out,
+                                      void* stream) {
+  if (ctx == nullptr || n < 0 || !(p >= 0.0 && p <= 1.0)) return LRM_ERR_INVALID_ARG;
+  if (dtype != LRM_F32 && dtype != LRM_BF16) return LRM_ERR_INVALID_ARG;
+  if (n == 0) return LRM_OK;
+  if (x == nullptr || out == nullptr) return LRM_ERR_INVALID_ARG;
+  const size_t es = dtype == LRM_F32 ? 4 : 2;
+  if (!aligned(x, es) || !aligned(out, es) || !aligned(residual, es) || !aligned(step, 8)) return LRM_ERR_ALIGN;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return LRM_ERR_CUDA;
+  const uint64_t below = static_cast<uint64_t>(p * 4294967296.0);  // words that drop: 0 .. below - 1
+  DropoutArgs a{seed, offset, step, static_cast<uint32_t>(below - 1), p < 1.0 ? static_cast<float>(1.0 / (1.0 - p))
+                                                                              : 0.0f};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return dtype == LRM_F32 ? dispatch<float>(ctx, x, residual, n, below > 0, a, out, s)
+                          : dispatch<uint16_t>(ctx, x, residual, n, below > 0, a, out, s);
+}

@@ -13,6 +13,7 @@
 //                       MoE combine over its k experts), fp32 sums, bf16 out;
 //                       a pair -> row map first, then one warp per token.
 #include "lrm_internal.cuh"
+#include "swiglu.cuh"
 #include "vec.cuh"
 
 namespace lrm {
@@ -20,17 +21,6 @@ namespace {
 
 constexpr int F1_THREADS = 256;
 constexpr int F1_WARPS = F1_THREADS / 32;
-
-__device__ __forceinline__ float silu_grad(float a, float& silu) {
-  const float s = 1.0f / (1.0f + expf(-a));
-  silu = a * s;
-  return s * (1.0f + a * (1.0f - s));
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 
 // one bf16 pair (2 columns) of a row: dphi word d, gate word a, up word b
 __device__ __forceinline__ void swiglu_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t& da, uint32_t& db) {

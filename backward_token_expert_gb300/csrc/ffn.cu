@@ -1,0 +1,527 @@
+// Forward of the routed experts: the gated feed-forward block
+//   up    [a | b] = W1_e x_t, phi_u = silu(a) b       (lrm_ffn_up, one kernel)
+//   down  row_u = W_e phi_u                           (lrm_ffn_down)
+//   y_t = sum over the k pairs u of t of alpha_u row_u (lrm_ffn_combine)
+// for the pairs u = t k + j of every expert's segment of `ids`.
+//
+// Both products are one kernel template: persistent clusters of two CTAs whose
+// even CTA issues tcgen05.mma.cta_group::2 with M = 256 rows of the weight and
+// N = up to 256 pairs (fp32 accumulators in TMEM, double-buffered), K blocks of
+// 64.  The pairs are the N dimension because N is cut to multiples of 32 at a
+// segment's end, where M would be rounded up to 256: a single token costs the
+// weights it has to read and little else.  Both operands are K-major:
+//   A  weight rows through one TMA box a CTA.  Up takes 64 gate rows and the 64
+//      up rows of the same features, so that a and b of a pair's feature are in
+//      one CTA's TMEM, 64 lanes apart, and the activation needs no second pass.
+//   B  the pairs' rows, gathered by their ids with gather4 TMA loads: x and phi
+//      are never copied into expert order.
+//   warp 0    TMA producer: every lane gathers four rows of a stage
+//   warp 1    MMA issuer (even CTA)
+//   warps 2-9 epilogue, two a TMEM lane quarter, half of the tile's pairs each
+// Every wait is bounded as in the other grouped products (grouped_gemm.cu); the
+// two warps that share an activation agree on a wait's outcome before either
+// goes on, since they meet at named barriers.
+#include <cuda_bf16.h>
+
+#include "grouped.cuh"
+#include "lrm_internal.cuh"
+#include "swiglu.cuh"
+#include "vec.cuh"
+
+namespace lrm {
+namespace {
+
+struct CfgFfn {
+  static constexpr int BN = 256;                     // pairs of a tile
+  static constexpr int BKS = 64;                     // K of a stage: one 128-byte swizzle row, 4 MMAs
+  static constexpr int A_BYTES = 128 * BKS * 2;      // this CTA's 128 weight rows
+  static constexpr int B_BYTES = (BN / 2) * BKS * 2;  // this CTA's half of the pairs
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 5;
+  static constexpr int TMEM_COLS = 2 * BN;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int XCH_BYTES = 16 * 32 * 4;  // fp32 [16 pairs][32 features] a warp hands to its partner
+  static constexpr int ROW_BYTES = 32 * 32 * 2;  // bf16 [32 pairs][32 features] a warp transposes
+  static constexpr int PHI_BYTES = 16 * 32 * 2;  // bf16 [16 pairs][32 features] of phi
+  static constexpr int EPI_BYTES = XCH_BYTES + ROW_BYTES + PHI_BYTES;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * EPI_BYTES + 1024;
+};
+
+// element (row, lane) of a [rows][32] bf16 buffer: 16-byte chunks XOR-swizzled by row, so that neither the
+// column-wise writes nor the row-wise 16-byte reads conflict
+__device__ __forceinline__ int swz(int row, int chunk) { return row * 32 + (((chunk ^ (row >> 1)) & 3) << 3); }
+
+template <bool UP>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
+    ffn_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const int32_t* __restrict__ offsets, const int32_t* __restrict__ ids, int E, int K, int M, int N,
+               int div, int max_rows, uint16_t* __restrict__ out, uint16_t* __restrict__ ab, unsigned int* status,
+               unsigned long long budget_ns) {
+  using C = CfgFfn;
+  extern __shared__ uint8_t dsmem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~uintptr_t(1023));
+
+  __shared__ __align__(8) uint64_t full_bar[C::STAGES];
+  __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
+  __shared__ __align__(8) uint64_t tfull_bar[2];
+  __shared__ __align__(8) uint64_t tempty_bar[2];
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ uint32_t s_tmem_base;
+  __shared__ int s_abort;
+  __shared__ int s_len[MAX_E];
+  __shared__ int s_start[MAX_E];
+  __shared__ int s_prefix[MAX_E + 1];  // first pair tile of each expert
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  // features of a pair tile: up has a gate and an up row for each
+  constexpr int TILE_M = UP ? 128 : 256;
+  const int tiles_m = (M + TILE_M - 1) / TILE_M;
+
+  if (tid == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    s_abort = 0;
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full_bar[i], 2);  // both arrivals come from the even CTA's producer
+      mbar_init(&empty_bar[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull_bar[i], 1);
+      mbar_init(&tempty_bar[i], 2 * C::EPI_WARPS);
+    }
+    mbar_init(&drain_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&s_tmem_base, C::TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  grid_dependency_wait();  // the segments, the rows and the buffers written below may be an earlier kernel's
+  for (int e = tid; e < E; e += C::THREADS) {
+    int st, ln;
+    segment(offsets, e, max_rows, st, ln);
+    s_len[e] = ln;
+    s_start[e] = st;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // pair tiles per expert: a run of experts a lane, then a warp scan
+    const int per = (E + 31) / 32;
+    const int i0 = lane * per, i1 = min(E, i0 + per);
+    int local = 0;
+    for (int i = i0; i < i1; ++i) local += ((s_len[i] + C::BN - 1) / C::BN) * tiles_m;
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    int run = incl - local;
+    for (int i = i0; i < i1; ++i) {
+      s_prefix[i] = run;
+      run += ((s_len[i] + C::BN - 1) / C::BN) * tiles_m;
+    }
+    if (lane == 31) s_prefix[E] = incl;
+    if (lane == 0 && blockIdx.x == 0 && __ldg(offsets + E) > max_rows) raise_flag(status, LRM_ERR_SHAPE);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  grid_dependency_launch();
+  const uint32_t tmem_base = s_tmem_base;
+  const int total_tiles = s_prefix[E];
+  volatile int* abort_flag = &s_abort;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    raise_flag(status, LRM_ERR_TIMEOUT);
+  };
+  // tile -> expert, row tile nt (over the segment), feature tile mt; the row tiles of one feature tile run side by
+  // side, so neighbouring CTA pairs share its weights through L2
+  auto decode = [&](int tile, int& e, int& nt, int& mt) {
+    int lo = 0, hi = E - 1;  // last expert with s_prefix <= tile
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_prefix[mid] <= tile)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    e = lo;
+    const int rem = tile - s_prefix[lo];
+    const int n_nt = (s_len[e] + C::BN - 1) / C::BN;
+    mt = rem / n_nt;
+    nt = rem - mt * n_nt;
+  };
+  // pairs of a row tile that the MMA computes: the remainder rounded up to 32
+  auto tile_rows = [&](int len, int nt) { return min(C::BN, ((len - nt * C::BN + 31) / 32) * 32); };
+  const int nkb = (K + C::BKS - 1) / C::BKS;  // K past the end reads as zeros (tensor bounds)
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const uint32_t full0 = mapa_shared(&full_bar[0], 0);  // the even CTA's full barriers
+    uint32_t it = 0;
+    bool ok = true;
+    for (int tile = pair; tile < total_tiles && ok; tile += npairs) {
+      int e, nt, mt;
+      decode(tile, e, nt, mt);
+      const int start = s_start[e], len = s_len[e];
+      const int half = tile_rows(len, nt) / 2;  // a multiple of 16
+      const bool loads = lane * 4 < half;
+      int row[4] = {0, 0, 0, 0};
+      if (loads) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // rows past the segment repeat its last one: computed for nothing, never stored
+          const int r = min(nt * C::BN + static_cast<int>(rank) * half + 4 * lane + i, len - 1);
+          const int u = __ldg(ids + start + r);
+          row[i] = u >= 0 && u < N ? u / div : 0;  // the epilogue flags a bad id and stores nothing for it
+        }
+      }
+      const int m0 = mt * TILE_M + static_cast<int>(rank) * (TILE_M / 2);
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const uint32_t s = it % C::STAGES;
+        const uint32_t ph = (it / C::STAGES) & 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty_bar[s], ph ^ 1u, budget_ns, abort_flag))) {
+          if (lane == 0) fail();
+          ok = false;
+          break;
+        }
+        uint8_t* a_dst = smem + s * C::STAGE_BYTES;
+        uint8_t* b_dst = a_dst + C::A_BYTES;
+        const uint32_t bar = full0 + s * 8;
+        if (lane == 0) {
+          if (leader) {
+            mbar_arrive_expect_tx(&full_bar[s], 2 * (C::A_BYTES + half * C::BKS * 2));
+            mbar_arrive(&full_bar[s]);
+          }
+          tma_load_4d_pair(a_dst, &tmA, bar, kb * C::BKS, m0, 0, e);
+        }
+        if (loads) tma_gather4_pair(b_dst + lane * 512, &tmB, bar, kb * C::BKS, row);
+        __syncwarp();
+      }
+    }
+    // the even CTA's commits arrive on these barriers asynchronously: wait for the release of the last STAGES
+    // stages before the block can exit
+    if (lane == 0) {
+      for (uint32_t j = it; j < it + C::STAGES; ++j)
+        if (!mbar_wait(&empty_bar[j % C::STAGES], ((j / C::STAGES) & 1u) ^ 1u, budget_ns, ok ? abort_flag : nullptr))
+          break;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    uint32_t it = 0, acc_it = 0;
+    bool ok = leader;
+    for (int tile = pair; tile < total_tiles && ok; tile += npairs) {
+      int e, nt, mt;
+      decode(tile, e, nt, mt);
+      const uint32_t idesc = idesc_bf16_f32(256, static_cast<uint32_t>(tile_rows(s_len[e], nt)), 0u, 0u);
+      const uint32_t acc = acc_it & 1u;
+      const uint32_t aph = (acc_it >> 1) & 1u;
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty_bar[acc], aph ^ 1u, budget_ns, abort_flag))) {
+        if (lane == 0) fail();
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + acc * C::BN;
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const uint32_t s = it % C::STAGES;
+        const uint32_t ph = (it / C::STAGES) & 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[s], ph, budget_ns, abort_flag))) {
+          if (lane == 0) fail();
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t a_addr = smem_u32(smem + s * C::STAGE_BYTES);
+          const uint64_t adesc = smem_desc_sw128(a_addr, 16, 1024);
+          const uint64_t bdesc = smem_desc_sw128(a_addr + C::A_BYTES, 16, 1024);
+          // 16 K are 32 bytes of the swizzled row, 2 in the descriptors' address field
+#pragma unroll
+          for (int kk = 0; kk < C::BKS / 16; ++kk)
+            mma_bf16_ss_pair(d_tmem, adesc + kk * 2, bdesc + kk * 2, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_pair_multicast(&empty_bar[s]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (lane == 0) mma_commit_pair_multicast(&tfull_bar[acc]);
+      __syncwarp();
+      ++acc_it;
+    }
+    if (leader) {
+      if (lane == 0) {
+        mma_commit_pair_local(&drain_bar);
+        if (!mbar_wait(&drain_bar, 0, budget_ns, nullptr)) raise_flag(status, LRM_ERR_TIMEOUT);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;              // TMEM lane quarter this warp may access
+    const int hf = (warp - 2) >> 2;      // its half of the tile's pairs
+    const int c_begin = hf * (C::BN / 2);
+    // up: quarters 0 and 1 hold the gate's features, 2 and 3 the up projection's; the warps of one feature block
+    // and half share a barrier
+    const int is_up = UP ? q >> 1 : 0;
+    const int xbar = 1 + hf * 2 + (q & 1);
+    uint8_t* epi = smem + C::STAGES * C::STAGE_BYTES;
+    const int partner = 2 + ((warp - 2) ^ 2);  // quarter q ^ 2, same half
+    float* xch = reinterpret_cast<float*>(epi + (warp - 2) * C::EPI_BYTES);
+    const float* xch_partner = reinterpret_cast<const float*>(epi + (partner - 2) * C::EPI_BYTES);
+    uint16_t* rbuf = reinterpret_cast<uint16_t*>(epi + (warp - 2) * C::EPI_BYTES + C::XCH_BYTES);
+    uint16_t* pbuf = rbuf + C::ROW_BYTES / 2;
+    const uint32_t tempty0 = mapa_shared(&tempty_bar[0], 0);
+    uint32_t acc_it = 0;
+    for (int tile = pair; tile < total_tiles; tile += npairs) {
+      int e, nt, mt;
+      decode(tile, e, nt, mt);
+      const int n_cols = tile_rows(s_len[e], nt);
+      const int rows_valid = s_len[e] - nt * C::BN;  // pairs of this tile inside the segment
+      const int32_t* tile_ids = ids + s_start[e] + nt * C::BN;
+      const uint32_t acc = acc_it & 1u;
+      const uint32_t aph = (acc_it >> 1) & 1u;
+      bool got = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[acc], aph, budget_ns, abort_flag));
+      if (!got && lane == 0) fail();
+      if (UP) got = named_barrier_and(xbar, 64, got);
+      if (!got) break;
+      tc_fence_after();
+      const int col0 = UP ? mt * TILE_M + static_cast<int>(rank) * 64 + (q & 1) * 32
+                          : mt * TILE_M + static_cast<int>(rank) * 128 + q * 32;  // first feature of this warp
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * C::BN;
+      const int c_end = min(n_cols, c_begin + C::BN / 2);
+      for (int c = c_begin; c < c_end; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(taddr + c, r);  // lane = feature, r[j] = pair c + j
+        int u = -1;                        // id of pair c + lane, -1: nothing to store
+        if (c + lane < rows_valid) {
+          u = __ldg(tile_ids + c + lane);
+          if (u < 0 || u >= N) {
+            raise_flag(status, LRM_ERR_INDEX);
+            u = -1;
+          }
+        }
+        tmem_ld_wait();
+        if (UP) {
+          // The gate's warp keeps a of pairs 0-15 and gets their b, its partner keeps b of pairs 16-31 and gets
+          // their a: both do half of the activations, in fp32 on unrounded sums.
+#pragma unroll
+          for (int j = 0; j < 16; ++j) xch[j * 32 + lane] = __uint_as_float(is_up ? r[j] : r[16 + j]);
+        }
+        const bool stores_rows = !UP || ab != nullptr;
+        if (stores_rows) {
+          __syncwarp();  // the previous chunk's reads of the buffer are done
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(r[j]));
+            rbuf[swz(j, lane >> 3) + (lane & 7)] = *reinterpret_cast<const uint16_t*>(&b);
+          }
+          __syncwarp();
+          if (u >= 0) {  // lane = pair c + lane: 64 contiguous bytes of its row
+            const uint4* src = reinterpret_cast<const uint4*>(rbuf);
+            uint16_t* orow = UP ? ab + static_cast<size_t>(u) * 2 * M + static_cast<size_t>(is_up) * M + col0
+                                : out + static_cast<size_t>(u) * M + col0;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (col0 + v * 8 < M) *reinterpret_cast<uint4*>(orow + v * 8) = src[swz(lane, v) / 8];
+          }
+        }
+        if (UP) {
+          named_barrier(xbar, 64);  // both halves are in shared memory
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float other = xch_partner[j * 32 + lane];
+            const float own = __uint_as_float(is_up ? r[16 + j] : r[j]);
+            const float a = is_up ? other : own, b = is_up ? own : other;
+            const __nv_bfloat16 p = __float2bfloat16_rn(a / (1.0f + expf(-a)) * b);
+            pbuf[swz(j, lane >> 3) + (lane & 7)] = *reinterpret_cast<const uint16_t*>(&p);
+          }
+          __syncwarp();
+          const int row = lane >> 1, up_ = __shfl_sync(0xffffffffu, u, is_up * 16 + row);
+          if (up_ >= 0) {
+            const uint4* src = reinterpret_cast<const uint4*>(pbuf);
+            uint16_t* orow = out + static_cast<size_t>(up_) * M + col0;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const int chunk = (lane & 1) * 2 + v;
+              if (col0 + chunk * 8 < M) *reinterpret_cast<uint4*>(orow + chunk * 8) = src[swz(row, chunk) / 8];
+            }
+          }
+          named_barrier(xbar, 64);  // the partner has read before either writes again
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader)
+          mbar_arrive(&tempty_bar[acc]);
+        else
+          mbar_arrive_cluster(tempty0 + acc * 8);
+      }
+      ++acc_it;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its partner may still read its shared memory or TMEM
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+}
+
+constexpr int CB_THREADS = 256;
+
+// y_t = sum_j alpha_tj row_tj in fp32, one thread per token and 8 columns; a pair with gate 0 is not read.
+__global__ void __launch_bounds__(CB_THREADS) ffn_combine_kernel(const uint4* __restrict__ rows,
+                                                                 const float* __restrict__ alpha, long long items,
+                                                                 int k, int wv, uint4* __restrict__ out) {
+  grid_dependency_wait();
+  for (long long i = static_cast<long long>(blockIdx.x) * CB_THREADS + threadIdx.x; i < items;
+       i += static_cast<long long>(gridDim.x) * CB_THREADS) {
+    const long long t = i / wv;
+    const int v = static_cast<int>(i - t * wv);
+    const float* at = alpha + t * k;
+    const uint4* rt = rows + t * k * wv + v;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < k; j0 += 4) {
+      float a[4];
+      uint4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] = j0 + j < k ? __ldg(at + j0 + j) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[j] = a[j] != 0.0f ? ld_stream(rt + static_cast<long long>(j0 + j) * wv) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (a[j] != 0.0f) {
+          acc[0] = fmaf(a[j], bf16_lo(x[j].x), acc[0]);
+          acc[1] = fmaf(a[j], bf16_hi(x[j].x), acc[1]);
+          acc[2] = fmaf(a[j], bf16_lo(x[j].y), acc[2]);
+          acc[3] = fmaf(a[j], bf16_hi(x[j].y), acc[3]);
+          acc[4] = fmaf(a[j], bf16_lo(x[j].z), acc[4]);
+          acc[5] = fmaf(a[j], bf16_hi(x[j].z), acc[5]);
+          acc[6] = fmaf(a[j], bf16_lo(x[j].w), acc[6]);
+          acc[7] = fmaf(a[j], bf16_hi(x[j].w), acc[7]);
+        }
+      }
+    }
+    out[i] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+                        pack_bf16x2(acc[6], acc[7]));
+  }
+}
+
+// Weights [E][parts][rows][K] bf16 as a 4-D tensor (K, rows, parts, E) with [1][parts][box_rows][64] boxes.
+lrm_status encode_weight(lrm_ctx* ctx, CUtensorMap* map, const void* base, uint64_t K, uint64_t rows, uint64_t parts,
+                         uint64_t E, uint32_t box_rows) {
+  const cuuint64_t dims[4] = {K, rows, parts, E};
+  const cuuint64_t strides[3] = {K * 2, rows * K * 2, parts * rows * K * 2};
+  const cuuint32_t box[4] = {64, box_rows, static_cast<cuuint32_t>(parts), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = ctx->encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+                                 box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? LRM_OK : LRM_ERR_CUDA;
+}
+
+// Both products: rows [in_rows, K] gathered by id / div, weights [E][parts][M][K], out [N, M].
+template <bool UP>
+lrm_status launch_ffn(lrm_ctx* ctx, const uint16_t* in, uint64_t in_rows, const uint16_t* weight,
+                      const int32_t* offsets, const int32_t* ids, const lrm_dims& d, int max_rows, uint16_t* out,
+                      uint16_t* ab, cudaStream_t s) {
+  using C = CfgFfn;
+  auto kern = ffn_kernel<UP>;
+  static thread_local int configured_device = -1;
+  static thread_local int clusters = 0;
+  if (configured_device != ctx->device) {
+    if (ctx->smem_optin < C::SMEM_BYTES + 14 * 1024) return LRM_ERR_ARCH;
+    LRM_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctx->sm_count & ~1, 1, 1);
+    cfg.blockDim = dim3(C::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    int n = 0;
+    LRM_CHECK_CUDA(cudaOccupancyMaxActiveClusters(&n, kern, &cfg));
+    if (n < 1) return LRM_ERR_ARCH;
+    clusters = n;
+    configured_device = ctx->device;
+  }
+  const int K = UP ? d.h : d.I, M = UP ? d.I : d.h, N = d.T * d.k;
+  alignas(64) CUtensorMap ma, mb;
+  lrm_status st = encode_weight(ctx, &ma, weight, K, M, UP ? 2 : 1, d.E, UP ? 64 : 128);
+  if (st != LRM_OK) return st;
+  if ((st = encode_2d(ctx, &mb, in, K, in_rows, 1)) != LRM_OK) return st;
+  return launch_dependent(kern, 2 * clusters, C::THREADS, C::SMEM_BYTES, 0, s, ma, mb, offsets, ids, d.E, K, M, N,
+                          UP ? d.k : 1, max_rows, out, ab, ctx->d_status, ctx->wait_budget_ns);
+}
+
+lrm_status check_ffn(const lrm_ctx* ctx, const lrm_dims& dims, int max_rows, const void* in, const void* weight,
+                     const int32_t* offsets, const int32_t* ids, const void* out, const void* ab, bool& empty) {
+  empty = false;
+  if (ctx == nullptr) return LRM_ERR_INVALID_ARG;
+  const lrm_status st = check_dims(dims);
+  if (st != LRM_OK) return st;
+  if (max_rows < 0 || offsets == nullptr) return LRM_ERR_INVALID_ARG;
+  if (max_rows == 0 || dims.T == 0) {
+    empty = true;
+    return LRM_OK;
+  }
+  if (in == nullptr || weight == nullptr || ids == nullptr || out == nullptr) return LRM_ERR_INVALID_ARG;
+  if (!aligned(in, 16) || !aligned(weight, 16) || !aligned(out, 16) || (ab != nullptr && !aligned(ab, 16)) ||
+      !aligned(offsets, 4) || !aligned(ids, 4))
+    return LRM_ERR_ALIGN;
+  return LRM_OK;
+}
+
+}  // namespace
+}  // namespace lrm
+
+using namespace lrm;
+
+extern "C" lrm_status lrm_ffn_up(lrm_ctx* ctx, const uint16_t* x, const uint16_t* W1, const int32_t* offsets,
+                                 const int32_t* ids, lrm_dims dims, int32_t max_rows, uint16_t* ab, uint16_t* phi,
+                                 void* stream) {
+  bool empty;
+  const lrm_status st = check_ffn(ctx, dims, max_rows, x, W1, offsets, ids, phi, ab, empty);
+  if (st != LRM_OK || empty) return st;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return LRM_ERR_CUDA;
+  return launch_ffn<true>(ctx, x, dims.T, W1, offsets, ids, dims, max_rows, phi, ab,
+                          static_cast<cudaStream_t>(stream));
+}
+
+extern "C" lrm_status lrm_ffn_down(lrm_ctx* ctx, const uint16_t* phi, const uint16_t* W, const int32_t* offsets,
+                                   const int32_t* ids, lrm_dims dims, int32_t max_rows, uint16_t* rows,
+                                   void* stream) {
+  bool empty;
+  const lrm_status st = check_ffn(ctx, dims, max_rows, phi, W, offsets, ids, rows, nullptr, empty);
+  if (st != LRM_OK || empty) return st;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return LRM_ERR_CUDA;
+  return launch_ffn<false>(ctx, phi, static_cast<uint64_t>(dims.T) * dims.k, W, offsets, ids, dims, max_rows, rows,
+                           nullptr, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" lrm_status lrm_ffn_combine(lrm_ctx* ctx, const uint16_t* rows, const float* alpha, lrm_dims dims,
+                                      uint16_t* out, void* stream) {
+  if (ctx == nullptr) return LRM_ERR_INVALID_ARG;
+  const lrm_status st = check_dims(dims);
+  if (st != LRM_OK) return st;
+  if (dims.T == 0) return LRM_OK;
+  if (rows == nullptr || alpha == nullptr || out == nullptr) return LRM_ERR_INVALID_ARG;
+  if (!aligned(rows, 16) || !aligned(out, 16) || !aligned(alpha, 4)) return LRM_ERR_ALIGN;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return LRM_ERR_CUDA;
+  const int wv = dims.h / 8;
+  const long long items = static_cast<long long>(dims.T) * wv;
+  const long long need = (items + CB_THREADS - 1) / CB_THREADS;
+  const long long cap = 1 << 20;
+  return launch_dependent(ffn_combine_kernel, static_cast<int>(need < cap ? need : cap), CB_THREADS, 0, 0,
+                          static_cast<cudaStream_t>(stream), reinterpret_cast<const uint4*>(rows), alpha, items,
+                          dims.k, wv, reinterpret_cast<uint4*>(out));
+}

@@ -28,12 +28,13 @@
 // frees its TMEM before returning.
 #include <cuda_bf16.h>
 
+#include "grouped.cuh"
 #include "lrm_internal.cuh"
+#include "swiglu.cuh"
+#include "vec.cuh"
 
 namespace lrm {
 namespace {
-
-constexpr int MAX_E = 1024;
 
 // ---------------------------------------------------------------------------
 // wgrad on CTA pairs: dW_e [h, I] in 256 x BN output tiles, one per cluster of
@@ -104,16 +105,6 @@ __device__ __forceinline__ void quad_transpose_4x4(uint32_t (&r)[32], int lane) 
       }
     }
   }
-}
-
-// Start row and length of expert e's segment, clamped to the buffers.
-__device__ __forceinline__ void segment(const int32_t* __restrict__ sel_offsets, int e, int max_rows, int& start,
-                                        int& len) {
-  int st = __ldg(sel_offsets + e), en = __ldg(sel_offsets + e + 1);
-  st = min(max(st, 0), max_rows);
-  en = min(max(en, st), max_rows);
-  start = st;
-  len = en - st;
 }
 
 // dW element type: fp32, or bf16 (round to nearest even) when OutT is uint16_t
@@ -547,12 +538,25 @@ struct CfgDgradPair {
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024;
 };
 
-template <int BNR>
+// What the epilogue of lrm_ffn_backward reads and writes beside the product.
+struct SwigluArgs {
+  const uint16_t* ab;  // [N, 2I] saved projections of every pair
+  uint16_t* dh1;       // [max_rows, 2I]
+  float* partial;      // [max_rows, parts] dot products over 32 columns each, or NULL
+  float* dgate;        // [N], zeroed here
+  int N, parts;
+};
+
+// SWIGLU: the epilogue of lrm_ffn_backward.  The product dphi stays in fp32: 16 rows of the warp's 32 columns at a
+// time go through its shared memory, so that a lane has half of a row's 32 columns in order, reads the pair's a and b
+// there (32 bytes each, through the selection; loaded one step ahead) and writes dh1 = [dphi b silu'(a) | dphi silu(a)]
+// rounded once, and the partial sum of dphi silu(a) b.
+template <int BNR, bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::THREADS, 1)
     dgrad_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const int32_t* __restrict__ sel_offsets, int E, int h, int I, int max_rows,
                       uint16_t* __restrict__ out, const int32_t* __restrict__ row_map, int out_rows,
-                      unsigned int* status, unsigned long long budget_ns) {
+                      const __grid_constant__ SwigluArgs sw, unsigned int* status, unsigned long long budget_ns) {
   using C = CfgDgradPair<BNR>;
   extern __shared__ uint8_t dsmem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~uintptr_t(1023));
@@ -782,6 +786,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
     uint16_t* tbuf = reinterpret_cast<uint16_t*>(smem + C::STAGES * C::STAGE_BYTES) + (warp - 2) * 32 * C::T_PITCH;
     const uint32_t tempty0 = mapa_shared(&tempty_bar[0], 0);
     uint32_t acc_it = 0;
+    if constexpr (SWIGLU) {
+      if (sw.dgate != nullptr)  // pairs that were not retained get 0; the sums follow in the next kernel
+        for (int i = blockIdx.x * 32 * C::EPI_WARPS + tid - 64; i < sw.N; i += gridDim.x * 32 * C::EPI_WARPS)
+          sw.dgate[i] = 0.0f;
+    }
     for (int tile = pair; tile < total_tiles; tile += npairs) {
       int e, nt, mt;
       decode(tile, e, nt, mt);
@@ -799,36 +808,113 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
       const int row0 = start + nt * BNR;  // first compacted row of this tile
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BNR;
       const int c_end = min(n_cols, c_begin + BNR / 2);
-      for (int c = c_begin; c < c_end; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(taddr + c, r);  // lane = I column, r[j] = output row c + j
-        tmem_ld_wait();
-        __syncwarp();  // the previous chunk's reads of the buffer are done
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          // row j, I column `lane`: 16-byte chunk lane / 8 of the row, XOR-swizzled by row
-          const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(r[j]));
-          tbuf[j * C::T_PITCH + ((((lane >> 3) ^ (j >> 1)) & 3) << 3) + (lane & 7)] =
-              *reinterpret_cast<const uint16_t*>(&b);
-        }
-        __syncwarp();
-        if (c + lane < rows_valid) {  // lane = output row c + lane
-          // compacted layout: row r of out; with a row map (the inverse mapping
-          // of the selection), row row_map[r] of the [out_rows, I] array
-          int r = row0 + c + lane;
-          if (row_map != nullptr) {
-            r = __ldg(row_map + r);
-            if (r < 0 || r >= out_rows) {
+      if constexpr (SWIGLU) {
+        float* fbuf = reinterpret_cast<float*>(tbuf);  // [16 rows][32 columns], 16-byte chunks XOR-swizzled by row
+        const int frow = lane >> 1, fhalf = lane & 1;
+        const int fcol = col0 + fhalf * 16;  // first of this lane's 16 columns
+        uint4 ga[2], gb[2];                  // the step's a and b
+        int pid;                             // the pair of row c + frow of the step, -1: none
+        auto fetch = [&](int c) {
+          pid = -1;
+          ga[0] = ga[1] = gb[0] = gb[1] = make_uint4(0u, 0u, 0u, 0u);
+          if (c + frow < min(c_end, rows_valid)) {
+            pid = __ldg(row_map + row0 + c + frow);
+            if (pid < 0 || pid >= sw.N) {
               raise_flag(status, LRM_ERR_INDEX);
-              r = -1;
+              pid = -1;
+              return;
             }
+            const uint16_t* arow = sw.ab + static_cast<size_t>(pid) * 2 * I + fcol;
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+              if (fcol + v * 8 < I) {
+                ga[v] = ld_stream(reinterpret_cast<const uint4*>(arow + v * 8));
+                gb[v] = ld_stream(reinterpret_cast<const uint4*>(arow + I + v * 8));
+              }
           }
-          if (r >= 0) {
-            const uint4* src = reinterpret_cast<const uint4*>(tbuf + lane * C::T_PITCH);
-            uint16_t* orow = out + static_cast<size_t>(r) * I + col0;
+        };
+        if (c_begin < c_end) fetch(c_begin);
+        for (int c = c_begin; c < c_end; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(taddr + c, r);  // lane = I column, r[j] = output row c + j
+          tmem_ld_wait();
+#pragma unroll
+          for (int step = 0; step < 2; ++step) {
+            __syncwarp();  // the previous step's reads of the buffer are done
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              fbuf[j * 32 + ((((lane >> 2) ^ j) & 7) << 2) + (lane & 3)] = __uint_as_float(r[step * 16 + j]);
+            __syncwarp();
+            float d[16];
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-              if (col0 + v * 8 < I) *reinterpret_cast<uint4*>(orow + v * 8) = src[(v ^ (lane >> 1)) & 3];
+              *reinterpret_cast<float4*>(d + 4 * v) =
+                  *reinterpret_cast<const float4*>(fbuf + frow * 32 + (((fhalf * 4 + v) ^ frow) & 7) * 4);
+            const int u = pid;
+            uint32_t aw[8], bw[8], da[8], db[8];
+            *reinterpret_cast<uint4*>(aw) = ga[0];
+            *reinterpret_cast<uint4*>(aw + 4) = ga[1];
+            *reinterpret_cast<uint4*>(bw) = gb[0];
+            *reinterpret_cast<uint4*>(bw + 4) = gb[1];
+            fetch(c + 16 * (step + 1));  // past c_end: nothing
+            float dot = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+              float s0, s1;
+              const float g0 = silu_grad(bf16_lo(aw[w]), s0), g1 = silu_grad(bf16_hi(aw[w]), s1);
+              const float b0 = bf16_lo(bw[w]), b1 = bf16_hi(bw[w]);
+              const float ds0 = d[2 * w] * s0, ds1 = d[2 * w + 1] * s1;
+              da[w] = pack_bf16x2(d[2 * w] * b0 * g0, d[2 * w + 1] * b1 * g1);
+              db[w] = pack_bf16x2(ds0, ds1);
+              dot = fmaf(ds0, b0, dot);
+              dot = fmaf(ds1, b1, dot);
+            }
+            dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+            if (u >= 0) {
+              const size_t row = static_cast<size_t>(row0 + c + step * 16 + frow);
+              uint16_t* orow = sw.dh1 + row * 2 * I + fcol;
+#pragma unroll
+              for (int v = 0; v < 2; ++v)
+                if (fcol + v * 8 < I) {
+                  *reinterpret_cast<uint4*>(orow + v * 8) = *reinterpret_cast<const uint4*>(da + 4 * v);
+                  *reinterpret_cast<uint4*>(orow + I + v * 8) = *reinterpret_cast<const uint4*>(db + 4 * v);
+                }
+              if (sw.partial != nullptr && fhalf == 0 && col0 < I) sw.partial[row * sw.parts + col0 / 32] = dot;
+            }
+          }
+        }
+      } else {
+        for (int c = c_begin; c < c_end; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(taddr + c, r);  // lane = I column, r[j] = output row c + j
+          tmem_ld_wait();
+          __syncwarp();  // the previous chunk's reads of the buffer are done
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            // row j, I column `lane`: 16-byte chunk lane / 8 of the row, XOR-swizzled by row
+            const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(r[j]));
+            tbuf[j * C::T_PITCH + ((((lane >> 3) ^ (j >> 1)) & 3) << 3) + (lane & 7)] =
+                *reinterpret_cast<const uint16_t*>(&b);
+          }
+          __syncwarp();
+          if (c + lane < rows_valid) {  // lane = output row c + lane
+            // compacted layout: row r of out; with a row map (the inverse mapping
+            // of the selection), row row_map[r] of the [out_rows, I] array
+            int r = row0 + c + lane;
+            if (row_map != nullptr) {
+              r = __ldg(row_map + r);
+              if (r < 0 || r >= out_rows) {
+                raise_flag(status, LRM_ERR_INDEX);
+                r = -1;
+              }
+            }
+            if (r >= 0) {
+              const uint4* src = reinterpret_cast<const uint4*>(tbuf + lane * C::T_PITCH);
+              uint16_t* orow = out + static_cast<size_t>(r) * I + col0;
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                if (col0 + v * 8 < I) *reinterpret_cast<uint4*>(orow + v * 8) = src[(v ^ (lane >> 1)) & 3];
+            }
           }
         }
       }
@@ -849,19 +935,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
   cluster_sync_all();  // no CTA leaves while its partner may still read its shared memory or TMEM
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
-}
-
-// Row-major 2-D bf16 tensor [rows][cols] with [box_rows][64] boxes.
-lrm_status encode_2d(lrm_ctx* ctx, CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
-                     uint32_t box_rows) {
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * 2};
-  const cuuint32_t box[2] = {64, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  CUresult r = ctx->encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-                                 box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? LRM_OK : LRM_ERR_CUDA;
 }
 
 // W [E][h][I] bf16 as a 3-D tensor (I, h, E) with [1][box_h][64] boxes.
@@ -904,12 +977,12 @@ lrm_status launch_wgrad_pair(lrm_ctx* ctx, const CUtensorMap& a, const CUtensorM
 }
 
 // a = W_e^T operand (W map), b = segment rows operand (delta_c map)
-template <int BNR>
+template <int BNR, bool SWIGLU>
 lrm_status launch_dgrad_pair(lrm_ctx* ctx, const CUtensorMap& a, const CUtensorMap& b, const int32_t* sel_offsets,
                              const lrm_dims& d, int max_rows, uint16_t* out, const int32_t* row_map, int out_rows,
-                             cudaStream_t s) {
+                             const SwigluArgs& sw, cudaStream_t s) {
   using C = CfgDgradPair<BNR>;
-  auto kern = dgrad_pair_kernel<BNR>;
+  auto kern = dgrad_pair_kernel<BNR, SWIGLU>;
   static thread_local int configured_device = -1;
   static thread_local int clusters = 0;
   if (configured_device != ctx->device) {
@@ -926,8 +999,35 @@ lrm_status launch_dgrad_pair(lrm_ctx* ctx, const CUtensorMap& a, const CUtensorM
     configured_device = ctx->device;
   }
   kern<<<2 * clusters, C::THREADS, C::SMEM_BYTES, s>>>(a, b, sel_offsets, d.E, d.h, d.I, max_rows, out, row_map,
-                                                       out_rows, ctx->d_status, ctx->wait_budget_ns);
+                                                       out_rows, sw, ctx->d_status, ctx->wait_budget_ns);
   return launch_status();
+}
+
+int dot_parts(const lrm_dims& d) { return (d.I + 31) / 32; }
+
+constexpr int GS_THREADS = 256;
+constexpr int GS_LANES = 8;  // lanes that sum a row's partial dot products
+
+// dgate[u] = the sum of row r's partial dot products, in a fixed order, for pair u = ids[r]
+__global__ void __launch_bounds__(GS_THREADS)
+    gate_sum_kernel(const float* __restrict__ partial, int parts, const int32_t* __restrict__ sel_offsets, int E,
+                    const int32_t* __restrict__ ids, int max_rows, int N, float* __restrict__ dgate) {
+  grid_dependency_wait();
+  const int total = min(max(__ldg(sel_offsets + E), 0), max_rows);
+  const int sub = threadIdx.x % GS_LANES;
+  for (long long r0 = static_cast<long long>(blockIdx.x) * (GS_THREADS / GS_LANES); r0 < total;
+       r0 += static_cast<long long>(gridDim.x) * (GS_THREADS / GS_LANES)) {
+    const long long r = r0 + threadIdx.x / GS_LANES;
+    float sum = 0.0f;
+    if (r < total)
+      for (int i = sub; i < parts; i += GS_LANES) sum += partial[r * parts + i];
+#pragma unroll
+    for (int o = GS_LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (r < total && sub == 0) {
+      const int u = __ldg(ids + r);
+      if (u >= 0 && u < N) dgate[u] = sum;
+    }
+  }
 }
 
 }  // namespace
@@ -936,6 +1036,13 @@ lrm_status launch_dgrad_pair(lrm_ctx* ctx, const CUtensorMap& a, const CUtensorM
 using namespace lrm;
 
 namespace {
+
+// Maps of the input-gradient product's operands: rows (a pair's half of a tile) and W (half-stage boxes).
+lrm_status encode_dgrad(lrm_ctx* ctx, CUtensorMap* rows, CUtensorMap* w, const uint16_t* delta_c, const uint16_t* W,
+                        const lrm_dims& d, int max_rows) {
+  const lrm_status st = encode_2d(ctx, rows, delta_c, d.h, max_rows, 256 / 2);
+  return st != LRM_OK ? st : encode_w(ctx, w, W, d.I, d.h, d.E, CfgDgradPair<256>::BKS / 2);
+}
 
 // Both dgrad entry points: rows go to `out` in the compacted order, or through
 // `row_map` to rows of an [out_rows, I] array.
@@ -954,11 +1061,10 @@ lrm_status grouped_dgrad(lrm_ctx* ctx, const uint16_t* delta_c, const uint16_t* 
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return LRM_ERR_CUDA;
   alignas(64) CUtensorMap ma, mb;
-  using CD = CfgDgradPair<256>;
-  if ((st = encode_2d(ctx, &ma, delta_c, dims.h, max_rows, 256 / 2)) != LRM_OK) return st;
-  if ((st = encode_w(ctx, &mb, W, dims.I, dims.h, dims.E, CD::BKS / 2)) != LRM_OK) return st;  // half-stage boxes
+  if ((st = encode_dgrad(ctx, &ma, &mb, delta_c, W, dims, max_rows)) != LRM_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launch_dgrad_pair<256>(ctx, mb, ma, sel_offsets, dims, max_rows, out, row_map, out_rows, s);
+  return launch_dgrad_pair<256, false>(ctx, mb, ma, sel_offsets, dims, max_rows, out, row_map, out_rows, SwigluArgs{},
+                                       s);
 }
 
 }  // namespace
@@ -974,6 +1080,58 @@ extern "C" lrm_status lrm_grouped_dgrad_scatter(lrm_ctx* ctx, const uint16_t* de
                                                 int32_t max_rows, uint16_t* dphi_rows, void* stream) {
   if (sel_ids == nullptr && max_rows > 0) return LRM_ERR_INVALID_ARG;
   return grouped_dgrad(ctx, delta_c, W, sel_offsets, dims, max_rows, dphi_rows, sel_ids, dims.T * dims.k, stream);
+}
+
+extern "C" lrm_status lrm_ffn_backward_workspace(const lrm_ctx* ctx, lrm_dims dims, int32_t max_rows, size_t* bytes) {
+  if (ctx == nullptr || bytes == nullptr || max_rows < 0) return LRM_ERR_INVALID_ARG;
+  const lrm_status st = check_dims(dims);
+  if (st != LRM_OK) return st;
+  *bytes = static_cast<size_t>(max_rows) * dot_parts(dims) * sizeof(float);
+  return LRM_OK;
+}
+
+extern "C" lrm_status lrm_ffn_backward(lrm_ctx* ctx, const uint16_t* delta_c, const uint16_t* W, const uint16_t* ab,
+                                       const int32_t* sel_offsets, const int32_t* sel_ids, lrm_dims dims,
+                                       int32_t max_rows, uint16_t* dh1, float* dgate, void* ws, size_t ws_bytes,
+                                       void* stream) {
+  if (ctx == nullptr) return LRM_ERR_INVALID_ARG;
+  lrm_status st = check_dims(dims);
+  if (st != LRM_OK) return st;
+  if (max_rows < 0 || sel_offsets == nullptr) return LRM_ERR_INVALID_ARG;
+  const int N = dims.T * dims.k;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (max_rows > 0) {
+    if (delta_c == nullptr || W == nullptr || ab == nullptr || sel_ids == nullptr || dh1 == nullptr)
+      return LRM_ERR_INVALID_ARG;
+    if (!aligned(delta_c, 16) || !aligned(W, 16) || !aligned(ab, 16) || !aligned(dh1, 16) ||
+        !aligned(sel_offsets, 4) || !aligned(sel_ids, 4) || (dgate != nullptr && !aligned(dgate, 4)))
+      return LRM_ERR_ALIGN;
+    if (dgate != nullptr) {
+      if (ws == nullptr || ws_bytes < static_cast<size_t>(max_rows) * dot_parts(dims) * sizeof(float))
+        return LRM_ERR_WORKSPACE;
+      if (!aligned(ws, 4)) return LRM_ERR_ALIGN;
+    }
+  }
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return LRM_ERR_CUDA;
+  if (max_rows == 0 || N == 0) {
+    if (dgate != nullptr && N > 0) {
+      if (!aligned(dgate, 4)) return LRM_ERR_ALIGN;
+      LRM_CHECK_CUDA(cudaMemsetAsync(dgate, 0, static_cast<size_t>(N) * sizeof(float), s));
+    }
+    return LRM_OK;
+  }
+  alignas(64) CUtensorMap ma, mb;
+  if ((st = encode_dgrad(ctx, &ma, &mb, delta_c, W, dims, max_rows)) != LRM_OK) return st;
+  SwigluArgs sw{ab, dh1, dgate != nullptr ? static_cast<float*>(ws) : nullptr, dgate, N, dot_parts(dims)};
+  if ((st = launch_dgrad_pair<256, true>(ctx, mb, ma, sel_offsets, dims, max_rows, nullptr, sel_ids, N, sw, s)) !=
+      LRM_OK)
+    return st;
+  if (dgate == nullptr) return LRM_OK;
+  const long long need = (static_cast<long long>(max_rows) * GS_LANES + GS_THREADS - 1) / GS_THREADS;
+  const int cap = ctx->sm_count * (2048 / GS_THREADS);
+  return launch_dependent(gate_sum_kernel, static_cast<int>(need < cap ? need : cap), GS_THREADS, 0, 0, s,
+                          sw.partial, sw.parts, sel_offsets, dims.E, sel_ids, max_rows, N, dgate);
 }
 
 namespace {

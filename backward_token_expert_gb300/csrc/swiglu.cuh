@@ -1,0 +1,21 @@
+// The gated activation phi = silu(a) b, silu(a) = a / (1 + exp(-a)), and its
+// derivative, in fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace lrm {
+
+__device__ __forceinline__ float silu_grad(float a, float& silu) {
+  const float s = 1.0f / (1.0f + expf(-a));
+  silu = a * s;
+  return s * (1.0f + a * (1.0f - s));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+}  // namespace lrm

@@ -76,6 +76,15 @@ EXPORTED = (
     "lrm_grad_list_status",
     "lrm_grad_norm",
     "lrm_grad_clip",
+    "lrm_ffn_up",
+    "lrm_ffn_down",
+    "lrm_ffn_combine",
+    "lrm_ffn_backward_workspace",
+    "lrm_ffn_backward",
+    "lrm_layer_norm",
+    "lrm_layer_norm_workspace",
+    "lrm_layer_norm_backward",
+    "lrm_dropout_add",
 )
 
 # selection metrics of lrm_score_metric (the ablation of LRMoE sec. 4.7, Table 2)
@@ -185,6 +194,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lrm_grad_list_status": ([P, P, P, ctypes.POINTER(ctypes.c_uint32)], st),
         "lrm_grad_norm": ([P, P, P, P], st),
         "lrm_grad_clip": ([P, P, f32, P, P], st),
+    })
+    sig.update({
+        "lrm_ffn_up": ([P, P, P, P, P, Dims, i32, P, P, P], st),
+        "lrm_ffn_down": ([P, P, P, P, P, Dims, i32, P, P], st),
+        "lrm_ffn_combine": ([P, P, P, Dims, P, P], st),
+        "lrm_ffn_backward_workspace": ([P, Dims, i32, ctypes.POINTER(size)], st),
+        "lrm_ffn_backward": ([P] * 6 + [Dims, i32, P, P, P, size, P], st),
+        "lrm_layer_norm": ([P, P, i32, P, P, P, i32, i32, f32, P, P, P], st),
+        "lrm_layer_norm_workspace": ([P, i32, i32, ctypes.POINTER(size)], st),
+        "lrm_layer_norm_backward": ([P, P, i32, P, P, P, P, P, i32, i32, P, P, P, P, size, P], st),
+        "lrm_dropout_add": ([P, P, P, i32, ctypes.c_int64, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, P, P, P],
+                            st),
     })
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -453,6 +474,61 @@ def lrm_grad_norm(ctx, grad_list: int, stats, stream=None) -> None:
 
 def lrm_grad_clip(ctx, grad_list: int, max_norm: float, stats, stream=None) -> None:
     _check(load_library().lrm_grad_clip(ctx, grad_list, max_norm, _ptr(stats), _stream(stream)), "lrm_grad_clip")
+
+
+def lrm_ffn_up(ctx, x, W1, offsets, ids, dims: Dims, max_rows: int, ab, phi, stream=None) -> None:
+    _check(load_library().lrm_ffn_up(ctx, _ptr(x), _ptr(W1), _ptr(offsets), _ptr(ids), dims, max_rows, _ptr(ab),
+                                     _ptr(phi), _stream(stream)), "lrm_ffn_up")
+
+
+def lrm_ffn_down(ctx, phi, W, offsets, ids, dims: Dims, max_rows: int, rows, stream=None) -> None:
+    _check(load_library().lrm_ffn_down(ctx, _ptr(phi), _ptr(W), _ptr(offsets), _ptr(ids), dims, max_rows, _ptr(rows),
+                                       _stream(stream)), "lrm_ffn_down")
+
+
+def lrm_ffn_combine(ctx, rows, alpha, dims: Dims, out, stream=None) -> None:
+    _check(load_library().lrm_ffn_combine(ctx, _ptr(rows), _ptr(alpha), dims, _ptr(out), _stream(stream)),
+           "lrm_ffn_combine")
+
+
+def lrm_ffn_backward_workspace(ctx, dims: Dims, max_rows: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load_library().lrm_ffn_backward_workspace(ctx, dims, max_rows, ctypes.byref(out)),
+           "lrm_ffn_backward_workspace")
+    return out.value
+
+
+def lrm_ffn_backward(ctx, delta_c, W, ab, sel_offsets, sel_ids, dims: Dims, max_rows: int, dh1, dgate, ws,
+                     ws_bytes: int, stream=None) -> None:
+    _check(load_library().lrm_ffn_backward(ctx, _ptr(delta_c), _ptr(W), _ptr(ab), _ptr(sel_offsets), _ptr(sel_ids),
+                                           dims, max_rows, _ptr(dh1), _ptr(dgate), _ptr(ws), ws_bytes,
+                                           _stream(stream)), "lrm_ffn_backward")
+
+
+def lrm_layer_norm(ctx, x, dtype: int, gamma, beta, valid, rows: int, width: int, eps: float, y, stats,
+                   stream=None) -> None:
+    _check(load_library().lrm_layer_norm(ctx, _ptr(x), dtype, _ptr(gamma), _ptr(beta), _ptr(valid), rows, width, eps,
+                                         _ptr(y), _ptr(stats), _stream(stream)), "lrm_layer_norm")
+
+
+def lrm_layer_norm_workspace(ctx, rows: int, width: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load_library().lrm_layer_norm_workspace(ctx, rows, width, ctypes.byref(out)), "lrm_layer_norm_workspace")
+    return out.value
+
+
+def lrm_layer_norm_backward(ctx, x, dtype: int, dy, gamma, stats, valid, dres, rows: int, width: int, dx, dgamma,
+                            dbeta, ws, ws_bytes: int, stream=None) -> None:
+    _check(load_library().lrm_layer_norm_backward(ctx, _ptr(x), dtype, _ptr(dy), _ptr(gamma), _ptr(stats),
+                                                  _ptr(valid), _ptr(dres), rows, width, _ptr(dx), _ptr(dgamma),
+                                                  _ptr(dbeta), _ptr(ws), ws_bytes, _stream(stream)),
+           "lrm_layer_norm_backward")
+
+
+def lrm_dropout_add(ctx, x, residual, dtype: int, n: int, p: float, seed: int, offset: int, step, out,
+                    stream=None) -> None:
+    _check(load_library().lrm_dropout_add(ctx, _ptr(x), _ptr(residual), dtype, n, p, seed, offset, _ptr(step),
+                                          _ptr(out), _stream(stream)), "lrm_dropout_add")
 
 
 def lrm_get_device_status(ctx, stream=None) -> int:

@@ -550,13 +550,111 @@ LRM_API lrm_status lrm_grad_norm(lrm_ctx* ctx, const lrm_grad_list* list, lrm_gr
 LRM_API lrm_status lrm_grad_clip(lrm_ctx* ctx, const lrm_grad_list* list, float max_norm, lrm_grad_stats* stats,
                                  void* stream);
 
+/*
+ * The forward of the routed experts: the gated feed-forward block that the
+ * recalibrated backward differentiates (it produces the phi and ab that
+ * lrm_score, lrm_compact and lrm_ffn_backward read).  For the pairs u = ids[r] of
+ * every expert e's segment, r in [offsets[e], offsets[e+1]) (the counts' offsets
+ * and the bucket of lrm_route_stats, or sel_offsets and sel_ids), t = u div k:
+ *   lrm_ffn_up       [a | b] = W1_e x_t in fp32, phi[u] = bf16(silu(a) b),
+ *                    silu(a) = a / (1 + exp(-a)); both projections, the
+ *                    activation and the product in one kernel.  With ab,
+ *                    ab[u] = bf16([a | b]) for the backward.
+ *   lrm_ffn_down     rows[u] = bf16(W_e phi[u])
+ *   lrm_ffn_combine  out[t] = bf16(sum over the k pairs u of t of alpha[u] rows[u]),
+ *                    fp32, in slot order.  A pair with alpha[u] = 0 adds nothing
+ *                    and its row is not read, whatever it holds.
+ *   x [T, h], W1 [E, 2I, h] (I gate rows, then I up rows), W [E, h, I] bf16
+ *   ab [N, 2I] or NULL, phi [N, I], rows [N, h], out [T, h] bf16 out
+ *   ids [max_rows] int32: each pair at most once; offsets [E+1] int32
+ * Rows of pairs in no segment are neither read nor written.  An id outside [0, N)
+ * sets LRM_ERR_INDEX and is skipped; a total above max_rows sets LRM_ERR_SHAPE and
+ * the rest is skipped.  The same inputs give the same bits.  No output may overlap
+ * an input of the same call.
+ */
+LRM_API lrm_status lrm_ffn_up(lrm_ctx* ctx, const uint16_t* x, const uint16_t* W1, const int32_t* offsets,
+                              const int32_t* ids, lrm_dims dims, int32_t max_rows, uint16_t* ab, uint16_t* phi,
+                              void* stream);
+LRM_API lrm_status lrm_ffn_down(lrm_ctx* ctx, const uint16_t* phi, const uint16_t* W, const int32_t* offsets,
+                                const int32_t* ids, lrm_dims dims, int32_t max_rows, uint16_t* rows, void* stream);
+LRM_API lrm_status lrm_ffn_combine(lrm_ctx* ctx, const uint16_t* rows, const float* alpha, lrm_dims dims,
+                                   uint16_t* out, void* stream);
+
+/*
+ * lrm_ffn_backward: from the compacted output gradients to the gradient of the
+ * first projections and the gates in one product, for row r < sel_offsets[E]
+ * (clamped to max_rows) of pair u = sel_ids[r] with [a | b] = ab[u]:
+ *   dphi    = delta_c[r] W_e                                  (fp32, never stored)
+ *   dh1[r]  = bf16([dphi b silu'(a) | dphi silu(a)])           [max_rows, 2I] bf16 out
+ *   dgate[u] = <dphi, silu(a) b>, 0 for pairs that were not retained
+ *              (alpha_u dL/dalpha_u as lrm_gate_grad gives it; dgate [N] fp32 out, or NULL)
+ * It stands in for lrm_grouped_dgrad, the compaction of ab, lrm_swiglu_backward and
+ * lrm_gate_grad where dphi itself is not wanted; unlike them it rounds dphi nowhere.
+ *   delta_c [max_rows, h] as lrm_compact writes it, W [E, h, I], ab [N, 2I] bf16
+ *   ws      lrm_ffn_backward_workspace bytes (only read where dgate is not NULL)
+ * Rows of dh1 at or beyond the total are left untouched.  A sel_ids entry outside
+ * [0, N) sets LRM_ERR_INDEX and its row is skipped; each pair occurs at most once.
+ */
+LRM_API lrm_status lrm_ffn_backward_workspace(const lrm_ctx* ctx, lrm_dims dims, int32_t max_rows, size_t* bytes);
+LRM_API lrm_status lrm_ffn_backward(lrm_ctx* ctx, const uint16_t* delta_c, const uint16_t* W, const uint16_t* ab,
+                                    const int32_t* sel_offsets, const int32_t* sel_ids, lrm_dims dims,
+                                    int32_t max_rows, uint16_t* dh1, float* dgate, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/*
+ * Layer norm of the rows of x [rows, width] (Ba, Kiros and Hinton, 2016), fp32 or
+ * bf16 (dtype, an lrm_dtype), 1 <= width <= 16384, any width:
+ *   lrm_layer_norm           mean and var = mean of (x - mean)^2 of the row,
+ *                            rstd = 1 / sqrt(var + eps), eps >= 0;
+ *                            y = (x - mean) rstd gamma + beta, stats[row] = (mean, rstd)
+ *   lrm_layer_norm_backward  d = dy gamma, xhat = (x - mean) rstd with the saved stats,
+ *                            dx = rstd (d - mean(d) - xhat mean(d xhat)) [+ dres]
+ *                            dgamma = sum over rows of dy xhat, dbeta = sum of dy
+ * Sums are fp32, in a fixed order: the same inputs give the same bits.
+ *   x, y, dy, dx       [rows, width] of dtype; dres likewise or NULL: the gradient that
+ *                      reaches x past the norm (a residual connection's)
+ *   gamma, beta        [width] fp32; dgamma, dbeta [width] fp32 out, overwritten
+ *   valid              [rows] uint8 or NULL: a row whose entry is 0 gets y = 0, stats = 0
+ *                      and dx = 0 and takes no part in dgamma and dbeta, whatever it and
+ *                      its gradients hold
+ *   stats              [rows, 2] fp32
+ *   ws                 lrm_layer_norm_workspace bytes
+ * x, y, dy, dx and dres are aligned to their type and lie at one distance from a
+ * 16-byte boundary (else LRM_ERR_ALIGN).  No output may overlap an input.
+ */
+LRM_API lrm_status lrm_layer_norm(lrm_ctx* ctx, const void* x, int32_t dtype, const float* gamma, const float* beta,
+                                  const uint8_t* valid, int32_t rows, int32_t width, float eps, void* y,
+                                  float* stats, void* stream);
+LRM_API lrm_status lrm_layer_norm_workspace(const lrm_ctx* ctx, int32_t rows, int32_t width, size_t* bytes);
+LRM_API lrm_status lrm_layer_norm_backward(lrm_ctx* ctx, const void* x, int32_t dtype, const void* dy,
+                                           const float* gamma, const float* stats, const uint8_t* valid,
+                                           const void* dres, int32_t rows, int32_t width, void* dx, float* dgamma,
+                                           float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Dropout with a residual, out[i] = residual[i] + (kept_i ? x[i] / (1 - p) : 0), fp32
+ * arithmetic rounded once.  The mask is drawn, never stored: element i is dropped if
+ * word i mod 4 of Philox4x32-10 (Salmon et al., SC 2011) with the 64-bit key `seed`
+ * and the counter (i div 4, offset + *step), low words first, is below floor(p 2^32).
+ * The backward is the same call on the output's gradient, without a residual.  A
+ * dropped element adds nothing, whatever x holds there.
+ *   x, out    [n] fp32 or bf16 (dtype); residual likewise or NULL.  out may be x or
+ *             residual itself, else it overlaps neither.
+ *   p         0 <= p <= 1; p = 1 drops everything
+ *   step      device uint64 added to offset (modulo 2^64), or NULL for 0: a captured
+ *             graph draws a new mask at every replay if the step is counted up between
+ */
+LRM_API lrm_status lrm_dropout_add(lrm_ctx* ctx, const void* x, const void* residual, int32_t dtype, int64_t n,
+                                   double p, uint64_t seed, uint64_t offset, const uint64_t* step, void* out,
+                                   void* stream);
+
 /* Synchronise `stream`, return the device status word in *flags (bit
  * (1u << code) for every lrm_status code raised on the device since the last
  * read) and clear it. */
 LRM_API lrm_status lrm_get_device_status(lrm_ctx* ctx, void* stream, uint32_t* flags);
 
-/* Time limit, in nanoseconds, of every device-side wait of the grouped GEMM
- * and the clipping kernels (default 2e9).  A wait that runs out sets LRM_ERR_TIMEOUT and the
+/* Time limit, in nanoseconds, of every device-side wait of the grouped GEMM,
+ * feed-forward and clipping kernels (default 2e9).  A wait that runs out sets LRM_ERR_TIMEOUT and the
  * kernel winds down and returns. */
 LRM_API lrm_status lrm_set_wait_budget(lrm_ctx* ctx, uint64_t ns);
 

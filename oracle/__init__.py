@@ -7,3 +7,4 @@ baseline leg use it.  It shares no code with the CUDA library.
 
 from .lrm_oracle import *  # noqa: F401,F403
 from .router_oracle import *  # noqa: F401,F403,E402
+from .sublayer_oracle import *  # noqa: F401,F403,E402
