@@ -10,14 +10,18 @@
 // 64.  The pairs are the N dimension because N is cut to multiples of 32 at a
 // segment's end, where M would be rounded up to 256: a single token costs the
 // weights it has to read and little else.  Both operands are K-major:
-//   A  weight rows through one TMA box a CTA.  Up takes 64 gate rows and the 64
-//      up rows of the same features, so that a and b of a pair's feature are in
-//      one CTA's TMEM, 64 lanes apart, and the activation needs no second pass.
-//   B  the pairs' rows, gathered by their ids with gather4 TMA loads: x and phi
-//      are never copied into expert order.
-//   warp 0    TMA producer: every lane gathers four rows of a stage
-//   warp 1    MMA issuer (even CTA)
-//   warps 2-9 epilogue, two a TMEM lane quarter, half of the tile's pairs each
+//   A  weight rows by TMA.  Up takes 64 gate rows and the 64 up rows of the same
+//      features for each CTA, so that a and b of a pair's feature are in one CTA's
+//      TMEM, 64 lanes apart.
+//   B  the pairs' rows, gathered by their ids with gather4 TMA loads into the
+//      swizzled tile: x and phi are never copied into expert order.
+//   warp 0       TMA producer of the weights
+//   warp 1       MMA issuer (even CTA)
+//   warps 2-9    epilogue, two a TMEM lane quarter, half of the tile's pairs
+//                each.  A lane has one feature of 32 pairs; the warp transposes
+//                them through shared memory, so that four lanes store the 64
+//                bytes of a pair's row.
+//   warps 10-..  TMA producers of the pairs' rows, a share of each stage's each
 // Every wait is bounded as in the other grouped products (grouped_gemm.cu); the
 // two warps that share an activation agree on a wait's outcome before either
 // goes on, since they meet at named barriers.
@@ -32,25 +36,27 @@ namespace lrm {
 namespace {
 
 struct CfgFfn {
-  static constexpr int BN = 256;                     // pairs of a tile
-  static constexpr int BKS = 64;                     // K of a stage: one 128-byte swizzle row, 4 MMAs
-  static constexpr int A_BYTES = 128 * BKS * 2;      // this CTA's 128 weight rows
+  static constexpr int BN = 256;                      // pairs of a tile
+  static constexpr int BKS = 64;                      // K of a stage: one 128-byte swizzle row, 4 MMAs
+  static constexpr int A_BYTES = 128 * BKS * 2;       // this CTA's 128 weight rows
   static constexpr int B_BYTES = (BN / 2) * BKS * 2;  // this CTA's half of the pairs
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 5;
+  static constexpr int STAGES = 6;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int EPI_WARPS = 8;
-  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-  static constexpr int XCH_BYTES = 16 * 32 * 4;  // fp32 [16 pairs][32 features] a warp hands to its partner
-  static constexpr int ROW_BYTES = 32 * 32 * 2;  // bf16 [32 pairs][32 features] a warp transposes
-  static constexpr int PHI_BYTES = 16 * 32 * 2;  // bf16 [16 pairs][32 features] of phi
-  static constexpr int EPI_BYTES = XCH_BYTES + ROW_BYTES + PHI_BYTES;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * EPI_BYTES + 1024;
+  static constexpr int GATHER_WARPS = 8;
+  static constexpr int ROUND = 8 * GATHER_WARPS;  // a tile's pairs are a multiple: each gather warp has its share of four rows
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS + 32 * GATHER_WARPS;
+  // a warp's: fp32 [16 pairs][32 features] for its partner, then bf16 [32 pairs][32 features]
+  static constexpr int BUF_BYTES = 16 * 32 * 4;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * BUF_BYTES + 1024;
+  static_assert(ROUND % 32 == 0, "N of an M = 256 pair MMA is a multiple of 32");
 };
 
-// element (row, lane) of a [rows][32] bf16 buffer: 16-byte chunks XOR-swizzled by row, so that neither the
-// column-wise writes nor the row-wise 16-byte reads conflict
-__device__ __forceinline__ int swz(int row, int chunk) { return row * 32 + (((chunk ^ (row >> 1)) & 3) << 3); }
+__device__ __forceinline__ uint16_t bf16_bits(float v) {
+  const __nv_bfloat16 b = __float2bfloat16_rn(v);
+  return *reinterpret_cast<const uint16_t*>(&b);
+}
 
 template <bool UP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
@@ -77,8 +83,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  // features of a pair tile: up has a gate and an up row for each
-  constexpr int TILE_M = UP ? 128 : 256;
+  constexpr int TILE_M = UP ? 128 : 256;  // features of a tile: up has a gate and an up row for each
   const int tiles_m = (M + TILE_M - 1) / TILE_M;
 
   if (tid == 0) {
@@ -86,7 +91,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     tma_prefetch_desc(&tmB);
     s_abort = 0;
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&full_bar[i], 2);  // both arrivals come from the even CTA's producer
+      mbar_init(&full_bar[i], 2);  // both arrivals come from the even CTA's weight producer
       mbar_init(&empty_bar[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -157,32 +162,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     mt = rem / n_nt;
     nt = rem - mt * n_nt;
   };
-  // pairs of a row tile that the MMA computes: the remainder rounded up to 32
-  auto tile_rows = [&](int len, int nt) { return min(C::BN, ((len - nt * C::BN + 31) / 32) * 32); };
+  // pairs of a row tile that the MMA computes: the remainder rounded up
+  auto tile_rows = [&](int len, int nt) {
+    return min(C::BN, (len - nt * C::BN + C::ROUND - 1) / C::ROUND * C::ROUND);
+  };
   const int nkb = (K + C::BKS - 1) / C::BKS;  // K past the end reads as zeros (tensor bounds)
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    const uint32_t full0 = mapa_shared(&full_bar[0], 0);  // the even CTA's full barriers
+    // ------------------------------------------------------------ weights
+    if (lane == 0) {
+      const uint32_t full0 = mapa_shared(&full_bar[0], 0);  // the even CTA's full barriers
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = pair; tile < total_tiles && ok; tile += npairs) {
+        int e, nt, mt;
+        decode(tile, e, nt, mt);
+        const int m0 = mt * TILE_M + static_cast<int>(rank) * (TILE_M / 2);
+        const int half = tile_rows(s_len[e], nt) / 2;
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const uint32_t s = it % C::STAGES;
+          const uint32_t ph = (it / C::STAGES) & 1u;
+          if (!mbar_wait(&empty_bar[s], ph ^ 1u, budget_ns, abort_flag)) {
+            fail();
+            ok = false;
+            break;
+          }
+          if (leader) {
+            mbar_arrive_expect_tx(&full_bar[s], 2 * (C::A_BYTES + half * C::BKS * 2));
+            mbar_arrive(&full_bar[s]);
+          }
+          tma_load_4d_pair(smem + s * C::STAGE_BYTES, &tmA, full0 + s * 8, kb * C::BKS, m0, 0, e);
+        }
+      }
+      // the even CTA's commits arrive on these barriers asynchronously: wait for the release of the last STAGES
+      // stages before the block can exit
+      for (uint32_t j = it; j < it + C::STAGES; ++j)
+        if (!mbar_wait(&empty_bar[j % C::STAGES], ((j / C::STAGES) & 1u) ^ 1u, budget_ns, ok ? abort_flag : nullptr))
+          break;
+    }
+    __syncwarp();
+  } else if (warp >= 2 + C::EPI_WARPS) {
+    // ------------------------------------------------------------ gather
+    // A gather takes its operands from uniform registers, so a warp's are issued one after the other, some 75 cycles
+    // each by as many lanes (150 by one lane with all the rows): eight warps share a stage's 32.  Every warp has as
+    // many, at least one: a warp without a copy in a stage could fall behind the ring by a phase, whose parity it
+    // would take for another's.
+    const int g = warp - 2 - C::EPI_WARPS;
+    const uint32_t full0 = mapa_shared(&full_bar[0], 0);
     uint32_t it = 0;
     bool ok = true;
     for (int tile = pair; tile < total_tiles && ok; tile += npairs) {
       int e, nt, mt;
       decode(tile, e, nt, mt);
       const int start = s_start[e], len = s_len[e];
-      const int half = tile_rows(len, nt) / 2;  // a multiple of 16
-      const bool loads = lane * 4 < half;
+      const int half = tile_rows(len, nt) / 2;
+      const int n = half / 4 / C::GATHER_WARPS;  // this warp's gathers: one for each of its first n lanes
       int row[4] = {0, 0, 0, 0};
-      if (loads) {
+      if (lane < n) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // rows past the segment repeat its last one: computed for nothing, never stored
-          const int r = min(nt * C::BN + static_cast<int>(rank) * half + 4 * lane + i, len - 1);
+          const int r = min(nt * C::BN + static_cast<int>(rank) * half + 4 * (g * n + lane) + i, len - 1);
           const int u = __ldg(ids + start + r);
           row[i] = u >= 0 && u < N ? u / div : 0;  // the epilogue flags a bad id and stores nothing for it
         }
       }
-      const int m0 = mt * TILE_M + static_cast<int>(rank) * (TILE_M / 2);
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const uint32_t s = it % C::STAGES;
         const uint32_t ph = (it / C::STAGES) & 1u;
@@ -191,23 +235,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
           ok = false;
           break;
         }
-        uint8_t* a_dst = smem + s * C::STAGE_BYTES;
-        uint8_t* b_dst = a_dst + C::A_BYTES;
-        const uint32_t bar = full0 + s * 8;
-        if (lane == 0) {
-          if (leader) {
-            mbar_arrive_expect_tx(&full_bar[s], 2 * (C::A_BYTES + half * C::BKS * 2));
-            mbar_arrive(&full_bar[s]);
-          }
-          tma_load_4d_pair(a_dst, &tmA, bar, kb * C::BKS, m0, 0, e);
-        }
-        if (loads) tma_gather4_pair(b_dst + lane * 512, &tmB, bar, kb * C::BKS, row);
+        if (lane < n)
+          tma_gather4_pair(smem + s * C::STAGE_BYTES + C::A_BYTES + (g * n + lane) * 512, &tmB, full0 + s * 8,
+                           kb * C::BKS, row);
         __syncwarp();
       }
     }
-    // the even CTA's commits arrive on these barriers asynchronously: wait for the release of the last STAGES
-    // stages before the block can exit
-    if (lane == 0) {
+    if (lane == 0) {  // as above: lets this warp's own copies land, too
       for (uint32_t j = it; j < it + C::STAGES; ++j)
         if (!mbar_wait(&empty_bar[j % C::STAGES], ((j / C::STAGES) & 1u) ^ 1u, budget_ns, ok ? abort_flag : nullptr))
           break;
@@ -264,19 +298,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;              // TMEM lane quarter this warp may access
-    const int hf = (warp - 2) >> 2;      // its half of the tile's pairs
+    const int q = warp & 3;                               // TMEM lane quarter this warp may access
+    const int hf = (warp - 2) >> 2;                       // its half of the tile's pairs
     const int c_begin = hf * (C::BN / 2);
-    // up: quarters 0 and 1 hold the gate's features, 2 and 3 the up projection's; the warps of one feature block
+    constexpr int CHUNKS = C::BN / 2 / 32;
+    // up: quarters 0 and 1 hold the gate's features, 2 and 3 the up projection's; the two warps of a feature block
     // and half share a barrier
     const int is_up = UP ? q >> 1 : 0;
     const int xbar = 1 + hf * 2 + (q & 1);
-    uint8_t* epi = smem + C::STAGES * C::STAGE_BYTES;
-    const int partner = 2 + ((warp - 2) ^ 2);  // quarter q ^ 2, same half
-    float* xch = reinterpret_cast<float*>(epi + (warp - 2) * C::EPI_BYTES);
-    const float* xch_partner = reinterpret_cast<const float*>(epi + (partner - 2) * C::EPI_BYTES);
-    uint16_t* rbuf = reinterpret_cast<uint16_t*>(epi + (warp - 2) * C::EPI_BYTES + C::XCH_BYTES);
-    uint16_t* pbuf = rbuf + C::ROW_BYTES / 2;
+    uint8_t* bufs = smem + C::STAGES * C::STAGE_BYTES;
+    float* xch = reinterpret_cast<float*>(bufs + (warp - 2) * C::BUF_BYTES);
+    uint16_t* rbuf = reinterpret_cast<uint16_t*>(xch);
+    const float* xch_partner = reinterpret_cast<const float*>(bufs + ((warp - 2) ^ 2) * C::BUF_BYTES);  // quarter q ^ 2
+    const int sub = lane >> 2, quad = lane & 3;  // a store's row of eight, 16-byte part of its 64 bytes
+    // rows [0, n) of rbuf to the rows of their pairs: `pitch` values a row, `at` the warp's first column; id: of pair
+    // `lane` of the chunk, -1 for none; the buffer's first row is pair `first` of the chunk
+    auto store_rows = [&](uint16_t* at, size_t pitch, int n, int id, int first, bool in) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (8 * i >= n) break;
+        const int u = __shfl_sync(0xffffffffu, id, first + 8 * i + sub);
+        if (u >= 0 && in)
+          *reinterpret_cast<uint4*>(at + u * pitch + quad * 8) =
+              *reinterpret_cast<const uint4*>(rbuf + (8 * i + sub) * 32 + quad * 8);
+      }
+      __syncwarp();
+    };
     const uint32_t tempty0 = mapa_shared(&tempty_bar[0], 0);
     uint32_t acc_it = 0;
     for (int tile = pair; tile < total_tiles; tile += npairs) {
@@ -284,7 +332,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
       decode(tile, e, nt, mt);
       const int n_cols = tile_rows(s_len[e], nt);
       const int rows_valid = s_len[e] - nt * C::BN;  // pairs of this tile inside the segment
-      const int32_t* tile_ids = ids + s_start[e] + nt * C::BN;
+      int ids_of[CHUNKS];  // ids of pairs c_begin + 32 i + lane, -1: nothing to store
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) {
+        const int c = c_begin + 32 * i + lane;
+        ids_of[i] = -1;
+        if (c < rows_valid) {
+          const int u = __ldg(ids + s_start[e] + nt * C::BN + c);
+          if (u >= 0 && u < N)
+            ids_of[i] = u;
+          else
+            raise_flag(status, LRM_ERR_INDEX);
+        }
+      }
       const uint32_t acc = acc_it & 1u;
       const uint32_t aph = (acc_it >> 1) & 1u;
       bool got = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[acc], aph, budget_ns, abort_flag));
@@ -292,68 +352,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
       if (UP) got = named_barrier_and(xbar, 64, got);
       if (!got) break;
       tc_fence_after();
-      const int col0 = UP ? mt * TILE_M + static_cast<int>(rank) * 64 + (q & 1) * 32
-                          : mt * TILE_M + static_cast<int>(rank) * 128 + q * 32;  // first feature of this warp
+      const int col0 = mt * TILE_M + static_cast<int>(rank) * (TILE_M / 2) + (UP ? q & 1 : q) * 32;  // first feature
+      const bool in = col0 + quad * 8 < M;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * C::BN;
       const int c_end = min(n_cols, c_begin + C::BN / 2);
-      for (int c = c_begin; c < c_end; c += 32) {
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) {
+        const int c = c_begin + 32 * i;
+        if (c >= c_end) break;
         uint32_t r[32];
-        tmem_ld_32x32b_x32(taddr + c, r);  // lane = feature, r[j] = pair c + j
-        int u = -1;                        // id of pair c + lane, -1: nothing to store
-        if (c + lane < rows_valid) {
-          u = __ldg(tile_ids + c + lane);
-          if (u < 0 || u >= N) {
-            raise_flag(status, LRM_ERR_INDEX);
-            u = -1;
-          }
-        }
+        tmem_ld_32x32b_x32(taddr + c, r);  // lane = feature, r[j]: pair c + j
         tmem_ld_wait();
         if (UP) {
           // The gate's warp keeps a of pairs 0-15 and gets their b, its partner keeps b of pairs 16-31 and gets
           // their a: both do half of the activations, in fp32 on unrounded sums.
+          float other[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) xch[j * 32 + lane] = __uint_as_float(is_up ? r[j] : r[16 + j]);
-        }
-        const bool stores_rows = !UP || ab != nullptr;
-        if (stores_rows) {
-          __syncwarp();  // the previous chunk's reads of the buffer are done
+          named_barrier(xbar, 64);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(r[j]));
-            rbuf[swz(j, lane >> 3) + (lane & 7)] = *reinterpret_cast<const uint16_t*>(&b);
-          }
-          __syncwarp();
-          if (u >= 0) {  // lane = pair c + lane: 64 contiguous bytes of its row
-            const uint4* src = reinterpret_cast<const uint4*>(rbuf);
-            uint16_t* orow = UP ? ab + static_cast<size_t>(u) * 2 * M + static_cast<size_t>(is_up) * M + col0
-                                : out + static_cast<size_t>(u) * M + col0;
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              if (col0 + v * 8 < M) *reinterpret_cast<uint4*>(orow + v * 8) = src[swz(lane, v) / 8];
-          }
-        }
-        if (UP) {
-          named_barrier(xbar, 64);  // both halves are in shared memory
+          for (int j = 0; j < 16; ++j) other[j] = xch_partner[j * 32 + lane];
+          named_barrier(xbar, 64);  // the partner has read before this warp's buffer is written again
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float other = xch_partner[j * 32 + lane];
             const float own = __uint_as_float(is_up ? r[16 + j] : r[j]);
-            const float a = is_up ? other : own, b = is_up ? own : other;
-            const __nv_bfloat16 p = __float2bfloat16_rn(a / (1.0f + expf(-a)) * b);
-            pbuf[swz(j, lane >> 3) + (lane & 7)] = *reinterpret_cast<const uint16_t*>(&p);
+            rbuf[j * 32 + lane] = bf16_bits(is_up ? silu(other[j]) * own : silu(own) * other[j]);
           }
-          __syncwarp();
-          const int row = lane >> 1, up_ = __shfl_sync(0xffffffffu, u, is_up * 16 + row);
-          if (up_ >= 0) {
-            const uint4* src = reinterpret_cast<const uint4*>(pbuf);
-            uint16_t* orow = out + static_cast<size_t>(up_) * M + col0;
+          store_rows(out + col0, M, 16, ids_of[i], is_up * 16, in);
+        }
+        if (!UP || ab != nullptr) {
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const int chunk = (lane & 1) * 2 + v;
-              if (col0 + chunk * 8 < M) *reinterpret_cast<uint4*>(orow + chunk * 8) = src[swz(row, chunk) / 8];
-            }
-          }
-          named_barrier(xbar, 64);  // the partner has read before either writes again
+          for (int j = 0; j < 32; ++j) rbuf[j * 32 + lane] = bf16_bits(__uint_as_float(r[j]));
+          store_rows(UP ? ab + static_cast<size_t>(is_up) * M + col0 : out + col0,
+                     UP ? 2 * static_cast<size_t>(M) : M, 32, ids_of[i], 0, in);
         }
       }
       tc_fence_before();
@@ -429,7 +460,7 @@ lrm_status encode_weight(lrm_ctx* ctx, CUtensorMap* map, const void* base, uint6
   return r == CUDA_SUCCESS ? LRM_OK : LRM_ERR_CUDA;
 }
 
-// Both products: rows [in_rows, K] gathered by id / div, weights [E][parts][M][K], out [N, M].
+// Both products: rows of in [in_rows, K] gathered by id / div, weights [E][parts][M][K], out [N, M].
 template <bool UP>
 lrm_status launch_ffn(lrm_ctx* ctx, const uint16_t* in, uint64_t in_rows, const uint16_t* weight,
                       const int32_t* offsets, const int32_t* ids, const lrm_dims& d, int max_rows, uint16_t* out,

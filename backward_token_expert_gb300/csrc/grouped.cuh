@@ -18,9 +18,9 @@ __device__ __forceinline__ void segment(const int32_t* __restrict__ sel_offsets,
   len = en - st;
 }
 
-// Row-major 2-D bf16 tensor [rows][cols] with [box_rows][64] boxes (one row for a gather of rows).
+// Row-major 2-D bf16 tensor [rows][cols] with [box_rows][64] boxes.
 inline lrm_status encode_2d(lrm_ctx* ctx, CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
-                     uint32_t box_rows) {
+                            uint32_t box_rows) {
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols * 2};
   const cuuint32_t box[2] = {64, box_rows};

@@ -7,6 +7,10 @@
 
 namespace lrm {
 
+// One exponential and one quotient, both approximate: within (2 + |a|) 2^-22 of the value, relative, and 0 below
+// a = -87 (a value that would be smaller than 1e-36).
+__device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
+
 __device__ __forceinline__ float silu_grad(float a, float& silu) {
   const float s = 1.0f / (1.0f + expf(-a));
   silu = a * s;
