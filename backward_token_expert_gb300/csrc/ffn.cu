@@ -10,21 +10,23 @@
 // 64.  The pairs are the N dimension because N is cut to multiples of 32 at a
 // segment's end, where M would be rounded up to 256: a single token costs the
 // weights it has to read and little else.  Both operands are K-major:
-//   A  weight rows by TMA.  Up takes 64 gate rows and the 64 up rows of the same
-//      features for each CTA, so that a and b of a pair's feature are in one CTA's
-//      TMEM, 64 lanes apart.
+//   A  weight rows, one TMA box a CTA and stage.  Up interleaves eight gate rows
+//      with the eight up rows of the same features (a 5-D view of W1 does that in
+//      the box), so that a thread of the epilogue that reads TMEM in 16-lane
+//      fragments gets a and b of its features.
 //   B  the pairs' rows, gathered by their ids with gather4 TMA loads into the
 //      swizzled tile: x and phi are never copied into expert order.
 //   warp 0       TMA producer of the weights
 //   warp 1       MMA issuer (even CTA)
 //   warps 2-9    epilogue, two a TMEM lane quarter, half of the tile's pairs
-//                each.  A lane has one feature of 32 pairs; the warp transposes
-//                them through shared memory, so that four lanes store the 64
-//                bytes of a pair's row.
+//                each: fragments of 8 features x 8 pairs are transposed by
+//                stmatrix into shared memory, from where a pair's features are
+//                stored 16 bytes a lane, 32 or 64 contiguous bytes a row.  (Shared
+//                memory's bandwidth is what the operands of the products need:
+//                32 KB written and 32 KB read a stage of 512 cycles, so the less
+//                the epilogue takes of it, the better.)
 //   warps 10-..  TMA producers of the pairs' rows, a share of each stage's each
-// Every wait is bounded as in the other grouped products (grouped_gemm.cu); the
-// two warps that share an activation agree on a wait's outcome before either
-// goes on, since they meet at named barriers.
+// Every wait is bounded as in the other grouped products (grouped_gemm.cu).
 #include <cuda_bf16.h>
 
 #include "grouped.cuh"
@@ -47,16 +49,10 @@ struct CfgFfn {
   static constexpr int GATHER_WARPS = 8;
   static constexpr int ROUND = 8 * GATHER_WARPS;  // a tile's pairs are a multiple: each gather warp has its share of four rows
   static constexpr int THREADS = 64 + 32 * EPI_WARPS + 32 * GATHER_WARPS;
-  // a warp's: fp32 [16 pairs][32 features] for its partner, then bf16 [32 pairs][32 features]
-  static constexpr int BUF_BYTES = 16 * 32 * 4;
+  static constexpr int BUF_BYTES = 32 * 64;  // a warp's: 32 pairs, 32 bf16 values each
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * BUF_BYTES + 1024;
   static_assert(ROUND % 32 == 0, "N of an M = 256 pair MMA is a multiple of 32");
 };
-
-__device__ __forceinline__ uint16_t bf16_bits(float v) {
-  const __nv_bfloat16 b = __float2bfloat16_rn(v);
-  return *reinterpret_cast<const uint16_t*>(&b);
-}
 
 template <bool UP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
@@ -182,7 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const uint32_t s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1u;
-          if (!mbar_wait(&empty_bar[s], ph ^ 1u, budget_ns, abort_flag)) {
+          if (!mbar_wait_suspended(&empty_bar[s], ph ^ 1u, budget_ns, abort_flag)) {
             fail();
             ok = false;
             break;
@@ -191,13 +187,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
             mbar_arrive_expect_tx(&full_bar[s], 2 * (C::A_BYTES + half * C::BKS * 2));
             mbar_arrive(&full_bar[s]);
           }
-          tma_load_4d_pair(smem + s * C::STAGE_BYTES, &tmA, full0 + s * 8, kb * C::BKS, m0, 0, e);
+          tma_load_5d_pair(smem + s * C::STAGE_BYTES, &tmA, full0 + s * 8, kb * C::BKS, 0, 0, m0 / 8, e);
         }
       }
       // the even CTA's commits arrive on these barriers asynchronously: wait for the release of the last STAGES
       // stages before the block can exit
       for (uint32_t j = it; j < it + C::STAGES; ++j)
-        if (!mbar_wait(&empty_bar[j % C::STAGES], ((j / C::STAGES) & 1u) ^ 1u, budget_ns, ok ? abort_flag : nullptr))
+        if (!mbar_wait_suspended(&empty_bar[j % C::STAGES], ((j / C::STAGES) & 1u) ^ 1u, budget_ns, ok ? abort_flag : nullptr))
           break;
     }
     __syncwarp();
@@ -230,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const uint32_t s = it % C::STAGES;
         const uint32_t ph = (it / C::STAGES) & 1u;
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty_bar[s], ph ^ 1u, budget_ns, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_suspended(&empty_bar[s], ph ^ 1u, budget_ns, abort_flag))) {
           if (lane == 0) fail();
           ok = false;
           break;
@@ -243,7 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     }
     if (lane == 0) {  // as above: lets this warp's own copies land, too
       for (uint32_t j = it; j < it + C::STAGES; ++j)
-        if (!mbar_wait(&empty_bar[j % C::STAGES], ((j / C::STAGES) & 1u) ^ 1u, budget_ns, ok ? abort_flag : nullptr))
+        if (!mbar_wait_suspended(&empty_bar[j % C::STAGES], ((j / C::STAGES) & 1u) ^ 1u, budget_ns, ok ? abort_flag : nullptr))
           break;
     }
     __syncwarp();
@@ -257,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
       const uint32_t idesc = idesc_bf16_f32(256, static_cast<uint32_t>(tile_rows(s_len[e], nt)), 0u, 0u);
       const uint32_t acc = acc_it & 1u;
       const uint32_t aph = (acc_it >> 1) & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty_bar[acc], aph ^ 1u, budget_ns, abort_flag))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_suspended<true>(&tempty_bar[acc], aph ^ 1u, budget_ns, abort_flag))) {
         if (lane == 0) fail();
         break;
       }
@@ -266,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const uint32_t s = it % C::STAGES;
         const uint32_t ph = (it / C::STAGES) & 1u;
-        if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[s], ph, budget_ns, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_suspended(&full_bar[s], ph, budget_ns, abort_flag))) {
           if (lane == 0) fail();
           ok = false;
           break;
@@ -292,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     if (leader) {
       if (lane == 0) {
         mma_commit_pair_local(&drain_bar);
-        if (!mbar_wait(&drain_bar, 0, budget_ns, nullptr)) raise_flag(status, LRM_ERR_TIMEOUT);
+        if (!mbar_wait_suspended(&drain_bar, 0, budget_ns, nullptr)) raise_flag(status, LRM_ERR_TIMEOUT);
       }
       __syncwarp();
     }
@@ -302,29 +298,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     const int hf = (warp - 2) >> 2;                       // its half of the tile's pairs
     const int c_begin = hf * (C::BN / 2);
     constexpr int CHUNKS = C::BN / 2 / 32;
-    // up: quarters 0 and 1 hold the gate's features, 2 and 3 the up projection's; the two warps of a feature block
-    // and half share a barrier
-    const int is_up = UP ? q >> 1 : 0;
-    const int xbar = 1 + hf * 2 + (q & 1);
-    uint8_t* bufs = smem + C::STAGES * C::STAGE_BYTES;
-    float* xch = reinterpret_cast<float*>(bufs + (warp - 2) * C::BUF_BYTES);
-    uint16_t* rbuf = reinterpret_cast<uint16_t*>(xch);
-    const float* xch_partner = reinterpret_cast<const float*>(bufs + ((warp - 2) ^ 2) * C::BUF_BYTES);  // quarter q ^ 2
-    const int sub = lane >> 2, quad = lane & 3;  // a store's row of eight, 16-byte part of its 64 bytes
-    // rows [0, n) of rbuf to the rows of their pairs: `pitch` values a row, `at` the warp's first column; id: of pair
-    // `lane` of the chunk, -1 for none; the buffer's first row is pair `first` of the chunk
-    auto store_rows = [&](uint16_t* at, size_t pitch, int n, int id, int first, bool in) {
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (8 * i >= n) break;
-        const int u = __shfl_sync(0xffffffffu, id, first + 8 * i + sub);
-        if (u >= 0 && in)
-          *reinterpret_cast<uint4*>(at + u * pitch + quad * 8) =
-              *reinterpret_cast<const uint4*>(rbuf + (8 * i + sub) * 32 + quad * 8);
-      }
-      __syncwarp();
-    };
+    uint8_t* buf = smem + C::STAGES * C::STAGE_BYTES + (warp - 2) * C::BUF_BYTES;
+    // 16-byte chunks of a pair's row in the buffer, swizzled so that neither eight rows of a chunk nor a warp's
+    // contiguous reads share banks
+    auto at4 = [&](int row, int chunk) { return buf + row * 64 + ((chunk ^ (row >> 1)) & 3) * 16; };
+    auto at2 = [&](int row, int chunk) { return buf + row * 32 + ((chunk ^ (row >> 2)) & 1) * 16; };
     const uint32_t tempty0 = mapa_shared(&tempty_bar[0], 0);
     uint32_t acc_it = 0;
     for (int tile = pair; tile < total_tiles; tile += npairs) {
@@ -347,44 +325,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
       }
       const uint32_t acc = acc_it & 1u;
       const uint32_t aph = (acc_it >> 1) & 1u;
-      bool got = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[acc], aph, budget_ns, abort_flag));
-      if (!got && lane == 0) fail();
-      if (UP) got = named_barrier_and(xbar, 64, got);
-      if (!got) break;
+      if (!__all_sync(0xffffffffu, mbar_wait_suspended(&tfull_bar[acc], aph, budget_ns, abort_flag))) {
+        if (lane == 0) fail();
+        break;
+      }
       tc_fence_after();
-      const int col0 = mt * TILE_M + static_cast<int>(rank) * (TILE_M / 2) + (UP ? q & 1 : q) * 32;  // first feature
-      const bool in = col0 + quad * 8 < M;
+      constexpr int COLS = UP ? 16 : 32;  // features of this warp
+      const int col0 = mt * TILE_M + static_cast<int>(rank) * (TILE_M / 2) + q * COLS;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * C::BN;
       const int c_end = min(n_cols, c_begin + C::BN / 2);
 #pragma unroll
       for (int i = 0; i < CHUNKS; ++i) {
         const int c = c_begin + 32 * i;
         if (c >= c_end) break;
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(taddr + c, r);  // lane = feature, r[j]: pair c + j
+        // v[hh][4 n + x]: TMEM lane 16 hh + lane / 4 (x < 2) or 8 further, pair c + 8 n + 2 (lane % 4) + x % 2
+        uint32_t v[2][16];
+        tmem_ld_16x256b_x4(taddr + c, v[0]);
+        tmem_ld_16x256b_x4(taddr + (16u << 16) + c, v[1]);
         tmem_ld_wait();
-        if (UP) {
-          // The gate's warp keeps a of pairs 0-15 and gets their b, its partner keeps b of pairs 16-31 and gets
-          // their a: both do half of the activations, in fp32 on unrounded sums.
-          float other[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) xch[j * 32 + lane] = __uint_as_float(is_up ? r[j] : r[16 + j]);
-          named_barrier(xbar, 64);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) other[j] = xch_partner[j * 32 + lane];
-          named_barrier(xbar, 64);  // the partner has read before this warp's buffer is written again
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float own = __uint_as_float(is_up ? r[16 + j] : r[j]);
-            rbuf[j * 32 + lane] = bf16_bits(is_up ? silu(other[j]) * own : silu(own) * other[j]);
-          }
-          store_rows(out + col0, M, 16, ids_of[i], is_up * 16, in);
-        }
+        auto val = [&](int hh, int n, int x) { return __uint_as_float(v[hh][4 * n + x]); };
+        __syncwarp();  // the previous chunk's reads of the buffer are done
         if (!UP || ab != nullptr) {
+          // four groups of 8 features: down 8 f .. of this warp's, up a and a, b and b
 #pragma unroll
-          for (int j = 0; j < 32; ++j) rbuf[j * 32 + lane] = bf16_bits(__uint_as_float(r[j]));
-          store_rows(UP ? ab + static_cast<size_t>(is_up) * M + col0 : out + col0,
-                     UP ? 2 * static_cast<size_t>(M) : M, 32, ids_of[i], 0, in);
+          for (int f = 0; f < 4; ++f) {
+            const int hh = UP ? f & 1 : f >> 1, o = UP ? f & 2 : 2 * (f & 1);
+            uint32_t m[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) m[n] = pack_bf16x2(val(hh, n, o), val(hh, n, o + 1));
+            stmatrix_x4_trans(at4(lane, f), m);
+          }
+          __syncwarp();
+          const int chunk = lane & 3;
+          const int col = col0 + (UP ? chunk & 1 : chunk) * 8;
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int row = it * 8 + (lane >> 2);
+            const int u = __shfl_sync(0xffffffffu, ids_of[i], row);
+            if (u >= 0 && col < M) {
+              uint16_t* o = UP ? ab + (2 * static_cast<size_t>(u) + (chunk >> 1)) * M + col
+                               : out + static_cast<size_t>(u) * M + col;
+              *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(at4(row, chunk));
+            }
+          }
+          if (UP) __syncwarp();
+        }
+        if (UP) {  // the activation in fp32, of the unrounded sums
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t m[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+              m[n] = pack_bf16x2(silu(val(hh, n, 0)) * val(hh, n, 2), silu(val(hh, n, 1)) * val(hh, n, 3));
+            stmatrix_x4_trans(at2(lane, hh), m);
+          }
+          __syncwarp();
+          const int chunk = lane & 1, col = col0 + chunk * 8;
+#pragma unroll
+          for (int it = 0; it < 2; ++it) {
+            const int row = it * 16 + (lane >> 1);
+            const int u = __shfl_sync(0xffffffffu, ids_of[i], row);
+            if (u >= 0 && col < M)
+              *reinterpret_cast<uint4*>(out + static_cast<size_t>(u) * M + col) =
+                  *reinterpret_cast<const uint4*>(at2(row, chunk));
+          }
         }
       }
       tc_fence_before();
@@ -447,14 +451,15 @@ __global__ void __launch_bounds__(CB_THREADS) ffn_combine_kernel(const uint4* __
   }
 }
 
-// Weights [E][parts][rows][K] bf16 as a 4-D tensor (K, rows, parts, E) with [1][parts][box_rows][64] boxes.
+// Weights [E][parts][rows][K] bf16, rows a multiple of 8, as a 5-D tensor (K, 8 rows, parts, rows / 8, E): a box of
+// 128 rows holds 8 rows of each part in turn.
 lrm_status encode_weight(lrm_ctx* ctx, CUtensorMap* map, const void* base, uint64_t K, uint64_t rows, uint64_t parts,
-                         uint64_t E, uint32_t box_rows) {
-  const cuuint64_t dims[4] = {K, rows, parts, E};
-  const cuuint64_t strides[3] = {K * 2, rows * K * 2, parts * rows * K * 2};
-  const cuuint32_t box[4] = {64, box_rows, static_cast<cuuint32_t>(parts), 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = ctx->encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+                         uint64_t E) {
+  const cuuint64_t dims[5] = {K, 8, parts, rows / 8, E};
+  const cuuint64_t strides[4] = {K * 2, rows * K * 2, 8 * K * 2, parts * rows * K * 2};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(parts), static_cast<cuuint32_t>(16 / parts), 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = ctx->encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides,
                                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? LRM_OK : LRM_ERR_CUDA;
@@ -484,7 +489,7 @@ lrm_status launch_ffn(lrm_ctx* ctx, const uint16_t* in, uint64_t in_rows, const 
   }
   const int K = UP ? d.h : d.I, M = UP ? d.I : d.h, N = d.T * d.k;
   alignas(64) CUtensorMap ma, mb;
-  lrm_status st = encode_weight(ctx, &ma, weight, K, M, UP ? 2 : 1, d.E, UP ? 64 : 128);
+  lrm_status st = encode_weight(ctx, &ma, weight, K, M, UP ? 2 : 1, d.E);
   if (st != LRM_OK) return st;
   if ((st = encode_2d(ctx, &mb, in, K, in_rows, 1)) != LRM_OK) return st;
   return launch_dependent(kern, 2 * clusters, C::THREADS, C::SMEM_BYTES, 0, s, ma, mb, offsets, ids, d.E, K, M, N,
