@@ -17,26 +17,46 @@ namespace {
 
 constexpr int DR_THREADS = 256;
 
-__device__ __forceinline__ void philox4x32_10(uint64_t block, uint64_t offset, uint64_t seed, uint32_t (&c)[4]) {
-  c[0] = static_cast<uint32_t>(block);
-  c[1] = static_cast<uint32_t>(block >> 32);
-  c[2] = static_cast<uint32_t>(offset);
-  c[3] = static_cast<uint32_t>(offset >> 32);
-  uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
-#pragma unroll
-  for (int r = 0; r < 10; ++r) {
-    const uint64_t p0 = static_cast<uint64_t>(c[0]) * 0xD2511F53u, p1 = static_cast<uint64_t>(c[2]) * 0xCD9E8D57u;
-    c[0] = static_cast<uint32_t>(p1 >> 32) ^ c[1] ^ k0;
-    c[1] = static_cast<uint32_t>(p1);
-    c[2] = static_cast<uint32_t>(p0 >> 32) ^ c[3] ^ k1;
-    c[3] = static_cast<uint32_t>(p0);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
+struct RoundKeys {
+  uint32_t a[10], b[10];
+};
+
+// Philox4x32-10 of the counters (word 0 = a thread's, the other three the same for the whole block): rounds 1 and 2
+// then have one product of the thread's own each, the other is the block's.
+struct Philox {
+  uint32_t r1_c0, r1_c1, r1_c3;  // round 1: c0 and c1; what is exclusive-ored into c2
+  uint32_t r2_c0, r2_c2, r2_c3;  // round 2: what goes into c0 and c2; c3
+  __device__ __forceinline__ Philox(uint32_t block_hi, uint64_t offset, const RoundKeys& k) {
+    const uint64_t p1 = static_cast<uint64_t>(static_cast<uint32_t>(offset)) * 0xCD9E8D57u;
+    r1_c0 = static_cast<uint32_t>(p1 >> 32) ^ block_hi ^ k.a[0];
+    r1_c1 = static_cast<uint32_t>(p1);
+    r1_c3 = static_cast<uint32_t>(offset >> 32) ^ k.b[0];
+    const uint64_t p0 = static_cast<uint64_t>(r1_c0) * 0xD2511F53u;
+    r2_c0 = r1_c1 ^ k.a[1];
+    r2_c2 = static_cast<uint32_t>(p0 >> 32) ^ k.b[1];
+    r2_c3 = static_cast<uint32_t>(p0);
   }
-}
+  __device__ __forceinline__ void operator()(uint32_t word, const RoundKeys& k, uint32_t (&c)[4]) const {
+    const uint64_t p0 = static_cast<uint64_t>(word) * 0xD2511F53u;
+    const uint64_t p1 = static_cast<uint64_t>(static_cast<uint32_t>(p0 >> 32) ^ r1_c3) * 0xCD9E8D57u;
+    c[0] = static_cast<uint32_t>(p1 >> 32) ^ r2_c0;
+    c[1] = static_cast<uint32_t>(p1);
+    c[2] = static_cast<uint32_t>(p0) ^ r2_c2;
+    c[3] = r2_c3;
+#pragma unroll
+    for (int r = 2; r < 10; ++r) {
+      const uint64_t q0 = static_cast<uint64_t>(c[0]) * 0xD2511F53u, q1 = static_cast<uint64_t>(c[2]) * 0xCD9E8D57u;
+      c[0] = static_cast<uint32_t>(q1 >> 32) ^ c[1] ^ k.a[r];
+      c[1] = static_cast<uint32_t>(q1);
+      c[2] = static_cast<uint32_t>(q0 >> 32) ^ c[3] ^ k.b[r];
+      c[3] = static_cast<uint32_t>(q0);
+    }
+  }
+};
 
 struct DropoutArgs {
-  uint64_t seed, offset;
+  RoundKeys keys;
+  uint64_t offset;
   const uint64_t* step;  // device value added to offset, or NULL
   uint32_t last;         // the largest word that drops its element
   float scale;           // 1 / (1 - p)
@@ -72,8 +92,10 @@ __global__ void __launch_bounds__(DR_THREADS)
   grid_dependency_wait();
   const uint64_t offset = a.offset + (a.step != nullptr ? __ldg(a.step) : 0);
   const long long items = (n + N - 1) / N;
-  for (long long i = static_cast<long long>(blockIdx.x) * DR_THREADS + threadIdx.x; i < items;
-       i += static_cast<long long>(gridDim.x) * DR_THREADS) {
+  for (long long i0 = static_cast<long long>(blockIdx.x) * DR_THREADS; i0 < items;
+       i0 += static_cast<long long>(gridDim.x) * DR_THREADS) {
+    const long long i = i0 + threadIdx.x;
+    if (i >= items) break;
     const long long e0 = i * N;
     const bool whole = VECTOR && e0 + N <= n;
     T xv[N], rv[N];
@@ -88,10 +110,13 @@ __global__ void __launch_bounds__(DR_THREADS)
         rv[j] = residual != nullptr && e0 + j < n ? residual[e0 + j] : T(0);
       }
     }
+    // a block's counters start at a multiple of DR_THREADS, so they share their upper word
+    const uint64_t q0 = static_cast<uint64_t>(i0) * (N / 4);
+    const Philox draw(static_cast<uint32_t>(q0 >> 32), offset, a.keys);
 #pragma unroll
     for (int b = 0; b < N / 4; ++b) {
       uint32_t w[4];
-      if (DROP) philox4x32_10(static_cast<uint64_t>(i) * (N / 4) + b, offset, a.seed, w);
+      if (DROP) draw(static_cast<uint32_t>(q0) + threadIdx.x * (N / 4) + b, a.keys, w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int m = b * 4 + j;
@@ -153,8 +178,15 @@ extern "C" lrm_status lrm_dropout_add(lrm_ctx* ctx, const void* x, const void* r
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return LRM_ERR_CUDA;
   const uint64_t below = static_cast<uint64_t>(p * 4294967296.0);  // words that drop: 0 .. below - 1
-  DropoutArgs a{seed, offset, step, static_cast<uint32_t>(below - 1), p < 1.0 ? static_cast<float>(1.0 / (1.0 - p))
-                                                                              : 0.0f};
+  DropoutArgs a;
+  for (int r = 0; r < 10; ++r) {
+    a.keys.a[r] = static_cast<uint32_t>(seed) + r * 0x9E3779B9u;
+    a.keys.b[r] = static_cast<uint32_t>(seed >> 32) + r * 0xBB67AE85u;
+  }
+  a.offset = offset;
+  a.step = step;
+  a.last = static_cast<uint32_t>(below - 1);
+  a.scale = p < 1.0 ? static_cast<float>(1.0 / (1.0 - p)) : 0.0f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dtype == LRM_F32 ? dispatch<float>(ctx, x, residual, n, below > 0, a, out, s)
                           : dispatch<uint16_t>(ctx, x, residual, n, below > 0, a, out, s);

@@ -547,10 +547,11 @@ struct SwigluArgs {
   int N, parts;
 };
 
-// SWIGLU: the epilogue of lrm_ffn_backward.  The product dphi stays in fp32: 16 rows of the warp's 32 columns at a
-// time go through its shared memory, so that a lane has half of a row's 32 columns in order, reads the pair's a and b
-// there (32 bytes each, through the selection; loaded one step ahead) and writes dh1 = [dphi b silu'(a) | dphi silu(a)]
-// rounded once, and the partial sum of dphi silu(a) b.
+// SWIGLU: the epilogue of lrm_ffn_backward.  The product dphi stays in fp32: 8 rows of the warp's 32 columns at a time
+// are read back from its shared memory, so that a lane has 8 columns of a row in order and four lanes the 64 bytes
+// that a row of a, b and dh1 has there.  A chunk's a and b are loaded, through the selection, while the one before it
+// is computed.  dh1 = [dphi b silu'(a) | dphi silu(a)] is rounded once; the sums of dphi silu(a) b over 32 columns
+// go to `partial`.
 template <int BNR, bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::THREADS, 1)
     dgrad_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -643,6 +644,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
     *abort_flag = 1;
     raise_flag(status, LRM_ERR_TIMEOUT);
   };
+  auto wait_bar = [&](uint64_t* bar, uint32_t parity) {
+    return SWIGLU ? mbar_wait_suspended(bar, parity, budget_ns, abort_flag)
+                  : mbar_wait(bar, parity, budget_ns, abort_flag);
+  };
   // tile -> expert, row tile nt (over the segment), width tile mt (over I);
   // within an expert the row tiles run fastest, so pairs dealt neighbouring
   // tiles share the same W_e columns (1-4 % faster than width tiles fastest
@@ -685,7 +690,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const uint32_t s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1u;
-          if (!mbar_wait(&empty_lo[s], ph ^ 1u, budget_ns, abort_flag)) {
+          if (!wait_bar(&empty_lo[s], ph ^ 1u)) {
             fail();
             ok = false;
             break;
@@ -706,7 +711,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
 #pragma unroll
           for (int c = 0; c < 2; ++c) tma_load_3d_pair(a_dst + c * C::A_ATOM, &tmA, bar, xa + c * 64, kb * C::BKS, e);
           tma_load_2d_pair(b_dst, &tmB, bar, kb * C::BKS, yb);
-          if (!mbar_wait(&empty_hi[s], ph ^ 1u, budget_ns, abort_flag)) {
+          if (!wait_bar(&empty_hi[s], ph ^ 1u)) {
             fail();
             ok = false;
             ++it;  // this stage's first half is in flight
@@ -736,7 +741,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
       const uint32_t idesc = idesc_bf16_f32(256, static_cast<uint32_t>(tile_rows(len, nt)), 1u, 0u);
       const uint32_t acc = acc_it & 1u;
       const uint32_t aph = (acc_it >> 1) & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty_bar[acc], aph ^ 1u, budget_ns, abort_flag))) {
+      if (!__all_sync(0xffffffffu, (SWIGLU ? mbar_wait_suspended<true>(&tempty_bar[acc], aph ^ 1u, budget_ns, abort_flag)
+                                           : mbar_wait_cluster(&tempty_bar[acc], aph ^ 1u, budget_ns, abort_flag)))) {
         if (lane == 0) fail();
         break;
       }
@@ -745,7 +751,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const uint32_t s = it % C::STAGES;
         const uint32_t ph = (it / C::STAGES) & 1u;
-        if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[s], ph, budget_ns, abort_flag))) {
+        if (!__all_sync(0xffffffffu, wait_bar(&full_bar[s], ph))) {
           if (lane == 0) fail();
           ok = false;
           break;
@@ -799,87 +805,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
       const int rows_valid = len - nt * BNR;  // rows of this tile inside the segment
       const uint32_t acc = acc_it & 1u;
       const uint32_t aph = (acc_it >> 1) & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait(&tfull_bar[acc], aph, budget_ns, abort_flag))) {
-        if (lane == 0) fail();
-        break;
-      }
-      tc_fence_after();
+      auto wait_full = [&](uint32_t a, uint32_t parity) {
+        if (!__all_sync(0xffffffffu, wait_bar(&tfull_bar[a], parity))) {
+          if (lane == 0) fail();
+          return false;
+        }
+        tc_fence_after();
+        return true;
+      };
+      if (!SWIGLU && !wait_full(acc, aph)) break;
       const int col0 = mt * 256 + static_cast<int>(rank) * 128 + q * 32;  // first I column of this warp
       const int row0 = start + nt * BNR;  // first compacted row of this tile
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BNR;
       const int c_end = min(n_cols, c_begin + BNR / 2);
       if constexpr (SWIGLU) {
         float* fbuf = reinterpret_cast<float*>(tbuf);  // [16 rows][32 columns], 16-byte chunks XOR-swizzled by row
-        const int frow = lane >> 1, fhalf = lane & 1;
-        const int fcol = col0 + fhalf * 16;  // first of this lane's 16 columns
-        uint4 ga[2], gb[2];                  // the step's a and b
-        int pid;                             // the pair of row c + frow of the step, -1: none
-        auto fetch = [&](int c) {
-          pid = -1;
-          ga[0] = ga[1] = gb[0] = gb[1] = make_uint4(0u, 0u, 0u, 0u);
-          if (c + frow < min(c_end, rows_valid)) {
-            pid = __ldg(row_map + row0 + c + frow);
-            if (pid < 0 || pid >= sw.N) {
-              raise_flag(status, LRM_ERR_INDEX);
-              pid = -1;
-              return;
-            }
-            const uint16_t* arow = sw.ab + static_cast<size_t>(pid) * 2 * I + fcol;
+        const int sub = lane >> 2, quad = lane & 3;    // a step's row of eight, 8 columns of its 32
+        const int fcol = col0 + quad * 8;              // first of this lane's columns
+        uint4 ga[4], gb[4];                            // a and b of rows c + 8 i + sub of a chunk
+        int pid[4];                                    // their pairs, -1: none
+        auto fetch_ids = [&](int c) {
 #pragma unroll
-            for (int v = 0; v < 2; ++v)
-              if (fcol + v * 8 < I) {
-                ga[v] = ld_stream(reinterpret_cast<const uint4*>(arow + v * 8));
-                gb[v] = ld_stream(reinterpret_cast<const uint4*>(arow + I + v * 8));
-              }
+          for (int i = 0; i < 4; ++i) {
+            const int r = c + 8 * i + sub;
+            pid[i] = r < min(c_end, rows_valid) ? __ldg(row_map + row0 + r) : -1;
+            if (pid[i] >= sw.N || (pid[i] < 0 && r < min(c_end, rows_valid))) {
+              raise_flag(status, LRM_ERR_INDEX);
+              pid[i] = -1;
+            }
           }
         };
-        if (c_begin < c_end) fetch(c_begin);
+        auto fetch = [&]() {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ga[i] = gb[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (pid[i] >= 0 && fcol < I) {
+              const uint16_t* arow = sw.ab + static_cast<size_t>(pid[i]) * 2 * I + fcol;
+              ga[i] = ld_stream(reinterpret_cast<const uint4*>(arow));
+              gb[i] = ld_stream(reinterpret_cast<const uint4*>(arow + I));
+            }
+          }
+        };
+        fetch_ids(c_begin);
+        fetch();
+        if (!wait_full(acc, aph)) break;
         for (int c = c_begin; c < c_end; c += 32) {
           uint32_t r[32];
           tmem_ld_32x32b_x32(taddr + c, r);  // lane = I column, r[j] = output row c + j
           tmem_ld_wait();
+          uint4 ca[4], cb[4];
+          bool has[4];
 #pragma unroll
-          for (int step = 0; step < 2; ++step) {
-            __syncwarp();  // the previous step's reads of the buffer are done
+          for (int i = 0; i < 4; ++i) ca[i] = ga[i], cb[i] = gb[i], has[i] = pid[i] >= 0;
+          fetch_ids(c + 32);  // past c_end: nothing
+          fetch();
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              fbuf[j * 32 + ((((lane >> 2) ^ j) & 7) << 2) + (lane & 3)] = __uint_as_float(r[step * 16 + j]);
-            __syncwarp();
-            float d[16];
+          for (int i = 0; i < 4; ++i) {
+            if (i % 2 == 0) {
+              __syncwarp();  // the reads of the 16 rows before are done
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
+              for (int j = 0; j < 16; ++j)
+                fbuf[j * 32 + ((((lane >> 2) ^ j) & 7) << 2) + (lane & 3)] = __uint_as_float(r[i * 8 + j]);
+              __syncwarp();
+            }
+            const int frow = (i % 2) * 8 + sub;
+            float d[8];
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
               *reinterpret_cast<float4*>(d + 4 * v) =
-                  *reinterpret_cast<const float4*>(fbuf + frow * 32 + (((fhalf * 4 + v) ^ frow) & 7) * 4);
-            const int u = pid;
-            uint32_t aw[8], bw[8], da[8], db[8];
-            *reinterpret_cast<uint4*>(aw) = ga[0];
-            *reinterpret_cast<uint4*>(aw + 4) = ga[1];
-            *reinterpret_cast<uint4*>(bw) = gb[0];
-            *reinterpret_cast<uint4*>(bw + 4) = gb[1];
-            fetch(c + 16 * (step + 1));  // past c_end: nothing
+                  *reinterpret_cast<const float4*>(fbuf + frow * 32 + (((quad * 2 + v) ^ frow) & 7) * 4);
+            const uint32_t aw[4] = {ca[i].x, ca[i].y, ca[i].z, ca[i].w}, bw[4] = {cb[i].x, cb[i].y, cb[i].z, cb[i].w};
+            uint32_t da[4], db[4];
             float dot = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
+            for (int w = 0; w < 4; ++w) {
               float s0, s1;
-              const float g0 = silu_grad(bf16_lo(aw[w]), s0), g1 = silu_grad(bf16_hi(aw[w]), s1);
-              const float b0 = bf16_lo(bw[w]), b1 = bf16_hi(bw[w]);
-              const float ds0 = d[2 * w] * s0, ds1 = d[2 * w + 1] * s1;
-              da[w] = pack_bf16x2(d[2 * w] * b0 * g0, d[2 * w + 1] * b1 * g1);
+              const float g0 = silu_grad_fast(bf16_lo(aw[w]), s0), g1 = silu_grad_fast(bf16_hi(aw[w]), s1);
+              const float d0 = d[2 * w], d1 = d[2 * w + 1], b0 = bf16_lo(bw[w]), b1 = bf16_hi(bw[w]);
+              const float ds0 = d0 * s0, ds1 = d1 * s1;
+              da[w] = pack_bf16x2(d0 * b0 * g0, d1 * b1 * g1);
               db[w] = pack_bf16x2(ds0, ds1);
               dot = fmaf(ds0, b0, dot);
               dot = fmaf(ds1, b1, dot);
             }
             dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-            if (u >= 0) {
-              const size_t row = static_cast<size_t>(row0 + c + step * 16 + frow);
+            dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+            if (has[i] && fcol < I) {
+              const size_t row = static_cast<size_t>(row0 + c + 8 * i + sub);
               uint16_t* orow = sw.dh1 + row * 2 * I + fcol;
-#pragma unroll
-              for (int v = 0; v < 2; ++v)
-                if (fcol + v * 8 < I) {
-                  *reinterpret_cast<uint4*>(orow + v * 8) = *reinterpret_cast<const uint4*>(da + 4 * v);
-                  *reinterpret_cast<uint4*>(orow + I + v * 8) = *reinterpret_cast<const uint4*>(db + 4 * v);
-                }
-              if (sw.partial != nullptr && fhalf == 0 && col0 < I) sw.partial[row * sw.parts + col0 / 32] = dot;
+              *reinterpret_cast<uint4*>(orow) = make_uint4(da[0], da[1], da[2], da[3]);
+              *reinterpret_cast<uint4*>(orow + I) = make_uint4(db[0], db[1], db[2], db[3]);
+              if (sw.partial != nullptr && quad == 0) sw.partial[row * sw.parts + col0 / 32] = dot;
             }
           }
         }
