@@ -85,69 +85,83 @@ __device__ __forceinline__ uint16_t from_float<uint16_t>(float v) {
 }
 
 // DROP = false: p = 0, nothing is drawn.  VECTOR: 16-byte accesses.
-template <typename T, bool DROP, bool VECTOR>
+template <typename T, bool DROP, bool VECTOR, bool RES>
 __global__ void __launch_bounds__(DR_THREADS)
     dropout_kernel(const T* x, const T* residual, long long n, const __grid_constant__ DropoutArgs a, T* out) {
   constexpr int N = 16 / sizeof(T);
   grid_dependency_wait();
   const uint64_t offset = a.offset + (a.step != nullptr ? __ldg(a.step) : 0);
   const long long items = (n + N - 1) / N;
-  for (long long i0 = static_cast<long long>(blockIdx.x) * DR_THREADS; i0 < items;
-       i0 += static_cast<long long>(gridDim.x) * DR_THREADS) {
-    const long long i = i0 + threadIdx.x;
-    if (i >= items) break;
-    const long long e0 = i * N;
-    const bool whole = VECTOR && e0 + N <= n;
-    T xv[N], rv[N];
-    if (whole) {
-      // plain loads: out may be x or residual
-      *reinterpret_cast<uint4*>(xv) = *reinterpret_cast<const uint4*>(x + e0);
-      if (residual != nullptr) *reinterpret_cast<uint4*>(rv) = *reinterpret_cast<const uint4*>(residual + e0);
-    } else {
+  constexpr int U = 2;  // vectors a thread has in flight
+  for (long long i0 = static_cast<long long>(blockIdx.x) * (U * DR_THREADS); i0 < items;
+       i0 += static_cast<long long>(gridDim.x) * (U * DR_THREADS)) {
+    T xv[U][N], rv[U][N];
+    bool whole[U];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        xv[j] = e0 + j < n ? x[e0 + j] : T(0);
-        rv[j] = residual != nullptr && e0 + j < n ? residual[e0 + j] : T(0);
+    for (int u = 0; u < U; ++u) {
+      const long long e0 = (i0 + u * DR_THREADS + threadIdx.x) * N;
+      whole[u] = VECTOR && e0 + N <= n;
+      if (whole[u]) {
+        // plain loads: out may be x or residual
+        *reinterpret_cast<uint4*>(xv[u]) = *reinterpret_cast<const uint4*>(x + e0);
+        if (RES) *reinterpret_cast<uint4*>(rv[u]) = *reinterpret_cast<const uint4*>(residual + e0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          xv[u][j] = e0 + j < n ? x[e0 + j] : T(0);
+          rv[u][j] = RES && e0 + j < n ? residual[e0 + j] : T(0);
+        }
       }
     }
-    // a block's counters start at a multiple of DR_THREADS, so they share their upper word
+    // a block's counters start at a multiple of U DR_THREADS N / 4, so they share their upper word
     const uint64_t q0 = static_cast<uint64_t>(i0) * (N / 4);
     const Philox draw(static_cast<uint32_t>(q0 >> 32), offset, a.keys);
 #pragma unroll
-    for (int b = 0; b < N / 4; ++b) {
-      uint32_t w[4];
-      if (DROP) draw(static_cast<uint32_t>(q0) + threadIdx.x * (N / 4) + b, a.keys, w);
+    for (int u = 0; u < U; ++u) {
+      const long long e0 = (i0 + u * DR_THREADS + threadIdx.x) * N;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = b * 4 + j;
-        const float r = residual != nullptr ? to_float(rv[m]) : 0.0f;
-        const float v = residual != nullptr ? fmaf(to_float(xv[m]), a.scale, r) : to_float(xv[m]) * a.scale;
-        xv[m] = from_float<T>(!DROP || w[j] > a.last ? v : r);
+      for (int b = 0; b < N / 4; ++b) {
+        uint32_t w[4];
+        if (DROP) draw(static_cast<uint32_t>(q0) + (u * DR_THREADS + threadIdx.x) * (N / 4) + b, a.keys, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int m = b * 4 + j;
+          const float r = RES ? to_float(rv[u][m]) : 0.0f;
+          const float v = RES ? fmaf(to_float(xv[u][m]), a.scale, r) : to_float(xv[u][m]) * a.scale;
+          xv[u][m] = from_float<T>(!DROP || w[j] > a.last ? v : r);
+        }
       }
-    }
-    if (whole) {
-      *reinterpret_cast<uint4*>(out + e0) = *reinterpret_cast<const uint4*>(xv);
-    } else {
+      if (whole[u]) {
+        *reinterpret_cast<uint4*>(out + e0) = *reinterpret_cast<const uint4*>(xv[u]);
+      } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (e0 + j < n) out[e0 + j] = xv[j];
+        for (int j = 0; j < N; ++j)
+          if (e0 + j < n) out[e0 + j] = xv[u][j];
+      }
     }
   }
 }
 
-template <typename T, bool DROP, bool VECTOR>
+template <typename T, bool DROP, bool VECTOR, bool RES>
 lrm_status launch(lrm_ctx* ctx, const void* x, const void* residual, long long n, const DropoutArgs& a, void* out,
                   cudaStream_t s) {
-  auto kern = dropout_kernel<T, DROP, VECTOR>;
+  auto kern = dropout_kernel<T, DROP, VECTOR, RES>;
   static thread_local int dev = -1, cap = 0;
   if (dev != ctx->device) {
     cap = resident_grid(ctx, kern, DR_THREADS, 0);
     dev = ctx->device;
   }
-  constexpr long long per = static_cast<long long>(DR_THREADS) * (16 / sizeof(T));
+  constexpr long long per = static_cast<long long>(2 * DR_THREADS) * (16 / sizeof(T));
   const long long need = (n + per - 1) / per;
   return launch_dependent(kern, static_cast<int>(need < cap ? need : cap), DR_THREADS, 0, 0, s,
                           static_cast<const T*>(x), static_cast<const T*>(residual), n, a, static_cast<T*>(out));
+}
+
+template <typename T, bool DROP, bool VECTOR>
+lrm_status dispatch2(lrm_ctx* ctx, const void* x, const void* residual, long long n, const DropoutArgs& a, void* out,
+                     cudaStream_t s) {
+  return residual != nullptr ? launch<T, DROP, VECTOR, true>(ctx, x, residual, n, a, out, s)
+                             : launch<T, DROP, VECTOR, false>(ctx, x, residual, n, a, out, s);
 }
 
 template <typename T>
@@ -155,10 +169,10 @@ lrm_status dispatch(lrm_ctx* ctx, const void* x, const void* residual, long long
                     void* out, cudaStream_t s) {
   const bool vec = aligned(x, 16) && aligned(out, 16) && aligned(residual, 16);
   if (drop)
-    return vec ? launch<T, true, true>(ctx, x, residual, n, a, out, s)
-               : launch<T, true, false>(ctx, x, residual, n, a, out, s);
-  return vec ? launch<T, false, true>(ctx, x, residual, n, a, out, s)
-             : launch<T, false, false>(ctx, x, residual, n, a, out, s);
+    return vec ? dispatch2<T, true, true>(ctx, x, residual, n, a, out, s)
+               : dispatch2<T, true, false>(ctx, x, residual, n, a, out, s);
+  return vec ? dispatch2<T, false, true>(ctx, x, residual, n, a, out, s)
+             : dispatch2<T, false, false>(ctx, x, residual, n, a, out, s);
 }
 
 }  // namespace

@@ -5,15 +5,19 @@
 //   dx = rstd (d - mean(d) - xhat mean(d xhat)) [+ dres]
 //   dgamma = sum over rows of dy xhat,   dbeta = sum over rows of dy
 // Both read every value once and write every result once, so memory bounds
-// them.  A row's values stay in registers between its statistics and its
-// output: the variance is that of the centred values, all sums are fp32, and
-// each output is rounded once.
+// them.  All sums are fp32, the variance is that of the centred values, and each
+// output is rounded once.
 //
-// Rows that do not start at a 16-byte boundary (a width that is no multiple of
-// the vector, or a tensor that starts between two) are read and written in the
-// aligned vectors that cover them; a vector that is shared with the
-// neighbouring row is stored element by element, and one that reaches beyond
-// the tensor is read so too.
+// A thread has the same columns in every row it takes part in, so gamma, beta
+// and, in the backward, the sums of the weights' gradients stay in its registers
+// while the row's values stream through: up to 8192 columns 16 a thread (as
+// pairs, for the packed fp32 instructions), with the next row's loads in flight
+// while one is reduced.  Narrow rows share a warp.  Rows that do not start at a
+// 16-byte boundary (a width that is no multiple of the vector, or a tensor that
+// starts between two) are read and written in the aligned vectors that cover
+// them, and a block takes only rows that start at the same place of a vector
+// (every N-th row at most).  A vector that is shared with the neighbouring row is
+// masked where it is used and stored element by element.
 #include <type_traits>
 
 #include "lrm_internal.cuh"
@@ -24,109 +28,105 @@ namespace lrm {
 namespace {
 
 constexpr int MAX_WIDTH = 16384;
+// Columns of a thread that holds its columns' weights, and the registers that needs: 64 bytes of a row forward, 32
+// backward, where the sums take their place.
+template <typename T>
+constexpr int FWD_COLS = sizeof(T) == 2 ? 32 : 16;
+template <typename T>
+constexpr int FWD_REGS = sizeof(T) == 2 ? 128 : 96;
+template <typename T>
+constexpr int BWD_COLS = sizeof(T) == 2 ? 16 : 8;
+template <typename T>
+constexpr int BWD_REGS = sizeof(T) == 2 ? 128 : 112;
+// threads that fit an SM beside one another
+constexpr int threads_per_sm(int regs) { return 65536 / regs / 128 * 128; }
 
+// two fp32 values and the packed instructions on them, rounded as the single ones are
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ float2 get() const {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+  }
+};
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// a 16-byte vector of a type as pairs of fp32 values
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  __device__ static __forceinline__ void unpack(const uint4& w, float (&f)[4]) {
-    f[0] = __uint_as_float(w.x);
-    f[1] = __uint_as_float(w.y);
-    f[2] = __uint_as_float(w.z);
-    f[3] = __uint_as_float(w.w);
+  __device__ static __forceinline__ void unpack(const uint4& w, F2 (&f)[2]) {
+    f[0] = F2(__uint_as_float(w.x), __uint_as_float(w.y));
+    f[1] = F2(__uint_as_float(w.z), __uint_as_float(w.w));
   }
-  __device__ static __forceinline__ uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  __device__ static __forceinline__ uint4 pack(const F2 (&f)[2]) {
+    const float2 a = f[0].get(), b = f[1].get();
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
   }
-  __device__ static __forceinline__ float get(const float* p) { return *p; }
-  __device__ static __forceinline__ void put(float* p, float v) { *p = v; }
+  __device__ static __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
 };
 template <>
 struct Vec<uint16_t> {  // bf16 bits
   static constexpr int N = 8;
-  __device__ static __forceinline__ void unpack(const uint4& w, float (&f)[8]) {
-    f[0] = bf16_lo(w.x), f[1] = bf16_hi(w.x), f[2] = bf16_lo(w.y), f[3] = bf16_hi(w.y);
-    f[4] = bf16_lo(w.z), f[5] = bf16_hi(w.z), f[6] = bf16_lo(w.w), f[7] = bf16_hi(w.w);
+  __device__ static __forceinline__ void unpack(const uint4& w, F2 (&f)[4]) {
+    f[0] = F2(bf16_lo(w.x), bf16_hi(w.x));
+    f[1] = F2(bf16_lo(w.y), bf16_hi(w.y));
+    f[2] = F2(bf16_lo(w.z), bf16_hi(w.z));
+    f[3] = F2(bf16_lo(w.w), bf16_hi(w.w));
   }
-  __device__ static __forceinline__ uint4 pack(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
-  }
-  __device__ static __forceinline__ float get(const uint16_t* p) {
-    return __uint_as_float(static_cast<uint32_t>(*p) << 16);
-  }
-  __device__ static __forceinline__ void put(uint16_t* p, float v) {
-    const __nv_bfloat16 b = __float2bfloat16_rn(v);
-    *p = *reinterpret_cast<const uint16_t*>(&b);
+  __device__ static __forceinline__ uint4 pack(const F2 (&f)[4]) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = f[i].get();
+      r[i] = pack_bf16x2(a.x, a.y);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
   }
 };
 
-// The vectors that cover a row: `lead` elements of the first one belong to what lies before the row.
-template <typename T, bool ALIGNED>
-struct RowSpan {
-  static constexpr int N = Vec<T>::N;
-  long long start;  // first element of the row
-  int lead, count;  // elements before the row in its first vector; vectors
+constexpr int MAX_WARPS = 16;
 
-  // `shift`: elements of the tensor's start beyond a 16-byte boundary
-  __device__ __forceinline__ RowSpan(long long row, int width, int shift) {
-    start = row * width;
-    lead = ALIGNED ? 0 : static_cast<int>((start + shift) % N);
-    count = (lead + width + N - 1) / N;
-  }
-  // Vector v of the row as fp32; elements outside the row are 0.
-  __device__ __forceinline__ uint4 load_raw(const T* base, int v, int width, long long total) const {
-    const long long e0 = start - lead + static_cast<long long>(v) * N;
-    if constexpr (ALIGNED) {
-      return ld_stream(reinterpret_cast<const uint4*>(base + e0));
-    } else {
-      if (e0 >= 0 && e0 + N <= total) return ld_stream(reinterpret_cast<const uint4*>(base + e0));
-      float f[N];
-#pragma unroll
-      for (int j = 0; j < N; ++j) f[j] = e0 + j >= 0 && e0 + j < total ? Vec<T>::get(base + e0 + j) : 0.0f;
-      return Vec<T>::pack(f);
-    }
-  }
-  // first column of vector v (negative in a row's first vector where `lead` > 0)
-  __device__ __forceinline__ int column(int v) const { return v * N - lead; }
-  __device__ __forceinline__ void store(T* base, int v, int width, const float (&f)[N]) const {
-    const int c0 = column(v);
-    T* at = base + start + c0;
-    if constexpr (ALIGNED) {
-      *reinterpret_cast<uint4*>(at) = Vec<T>::pack(f);
-    } else {
-      if (c0 >= 0 && c0 + N <= width) {
-        *reinterpret_cast<uint4*>(at) = Vec<T>::pack(f);
-        return;
-      }
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (c0 + j >= 0 && c0 + j < width) Vec<T>::put(at + j, f[j]);
-    }
-  }
-};
-
-// Sum over a row's threads: its warps' lanes by shuffles, then, with more than one warp, over the block through
-// shared memory.  `slot` alternates between calls, so that one barrier a call is enough.
+// Sums over a row's threads: `lanes` of a warp by shuffles, then, where a row has several warps, the warps' sums
+// through shared memory in a fixed order.  `slot` alternates between calls, so that one barrier a call is enough.
 template <int K>
-__device__ __forceinline__ void row_sum(float (&s)[K], int warps, float (*buf)[32][K], int& slot) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+__device__ __forceinline__ void row_sum(float (&s)[K], int lanes, float (*buf)[K][MAX_WARPS], int& slot) {
+  for (int o = min(lanes, 32) / 2; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < K; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-  if (warps == 1) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0)
+  if (lanes <= 32) return;
+  const int warp = threadIdx.x >> 5, warps = lanes >> 5;
+  if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int i = 0; i < K; ++i) buf[slot][warp][i] = s[i];
+    for (int i = 0; i < K; ++i) buf[slot][i][warp] = s[i];
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < K; ++i) s[i] = lane < warps ? buf[slot][lane][i] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < K; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+  for (int i = 0; i < K; ++i) {
+    s[i] = 0.0f;
+    for (int w = 0; w < warps; w += 4) {  // zeros beyond the row's warps
+      const float4 f = *reinterpret_cast<const float4*>(&buf[slot][i][w]);
+      s[i] += (f.x + f.y) + (f.z + f.w);
+    }
+  }
   slot ^= 1;
 }
 
@@ -134,216 +134,338 @@ __device__ __forceinline__ void row_sum(float (&s)[K], int warps, float (*buf)[3
 // the skew spreads over all banks
 __device__ __forceinline__ int skew(int c, int n) { return c + c / n; }
 
-// `warps` warps a row: the whole block, or 1 (the block's warps then have rows of their own).
+// The rows of a block and a thread's columns, which are the same in all of them: rows of class blockIdx.x % classes
+// (rows `classes` apart start at one place of a vector).  `lanes` threads have a row: a power of two up to a warp (the
+// block then has several rows at a time) or the whole block.
 template <typename T, int NV, bool ALIGNED>
-__global__ void __launch_bounds__(512)
-    layer_norm_kernel(const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta,
-                      const uint8_t* __restrict__ valid, int rows, int width, int shift, float eps, int warps, T* y,
-                      float* __restrict__ stats) {
-  constexpr int N = Vec<T>::N;
-  extern __shared__ float s_weights[];  // ALIGNED: none; else gamma and beta, skewed
-  __shared__ float s_buf[2][32][1];
-  grid_dependency_wait();
-  const int per = skew(width, N) + 1;
-  if (!ALIGNED) {
-    for (int c = threadIdx.x; c < width; c += blockDim.x) {
-      s_weights[skew(c, N)] = gamma[c];
-      s_weights[per + skew(c, N)] = beta[c];
-    }
-    __syncthreads();
+struct Block {
+  static constexpr int N = Vec<T>::N;
+  int lanes, lane, groups, group, cls, classes, lead, count, width;
+  long long step, rows;
+
+  __device__ __forceinline__ Block(int rows_, int width_, int shift, int classes_, int lanes_)
+      : lanes(lanes_), lane(threadIdx.x % lanes_), groups(blockDim.x / lanes_), group(threadIdx.x / lanes_),
+        cls(blockIdx.x % classes_), classes(classes_), width(width_),
+        step(static_cast<long long>(gridDim.x / classes_) * groups * classes_), rows(rows_) {
+    // elements before the row in its first vector; vectors that cover a row
+    lead = ALIGNED ? 0 : static_cast<int>((static_cast<long long>(cls) * width + shift) % N);
+    count = (lead + width + N - 1) / N;
   }
-  const int lanes = warps * 32;
-  const int groups = blockDim.x / lanes;  // rows the block has at a time
-  const int lane = threadIdx.x % lanes;
-  const long long total = static_cast<long long>(rows) * width;
+  // a vector with elements that are not the row's own: its first or last at most
+  __device__ __forceinline__ bool edge(int i) const {
+    return !ALIGNED && ((vector(i) == 0 && lead > 0) || (vector(i) == count - 1 && lead + width < count * N));
+  }
+  __device__ __forceinline__ long long first() const {
+    return (static_cast<long long>(blockIdx.x / classes) * groups + group) * classes + cls;
+  }
+  // the block goes on while its first row is there: all its threads take part in the sums of every pass
+  __device__ __forceinline__ long long first_of_block() const {
+    return static_cast<long long>(blockIdx.x / classes) * groups * classes + cls;
+  }
+  __device__ __forceinline__ int vector(int i) const { return lane + i * lanes; }
+  __device__ __forceinline__ int column(int i) const { return vector(i) * N - lead; }
+  // Vector i of a row as it lies in memory: its elements outside the row are a neighbour's, which clean() removes where
+  // the values are used (masking here would wait for them).
+  __device__ __forceinline__ uint4 load(const T* base, long long row, int i) const {
+    if (vector(i) >= count) return make_uint4(0u, 0u, 0u, 0u);
+    const long long e0 = row * width + column(i);
+    if (ALIGNED || (e0 >= 0 && e0 + N <= rows * width)) return ld_stream(reinterpret_cast<const uint4*>(base + e0));
+    uint32_t w[4] = {0u, 0u, 0u, 0u};  // reaches beyond the tensor
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (column(i) + j >= 0 && column(i) + j < width) {
+        if constexpr (N == 4)
+          w[j] = __float_as_uint(base[e0 + j]);
+        else
+          w[j / 2] |= static_cast<uint32_t>(base[e0 + j]) << (16 * (j % 2));
+      }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ uint4 clean(const uint4& r, int i) const {
+    if (!edge(i)) return r;
+    uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      constexpr int PER = N / 4;  // elements of a 32-bit word
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int c = column(i) + k * PER + j;
+        if (c < 0 || c >= width) w[k] &= PER == 1 ? 0u : (j == 0 ? 0xFFFF0000u : 0x0000FFFFu);
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void store(T* base, long long row, int i, const F2 (&f)[N / 2]) const {
+    if (vector(i) >= count) return;
+    T* at = base + row * width + column(i);
+    const uint4 r = Vec<T>::pack(f);
+    if (!edge(i)) {
+      *reinterpret_cast<uint4*>(at) = r;
+      return;
+    }
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (column(i) + j >= 0 && column(i) + j < width) {
+        if constexpr (N == 4)
+          at[j] = __uint_as_float(w[j]);
+        else
+          at[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j % 2)));
+      }
+  }
+  // the pair's weights, 0 outside the row
+  __device__ __forceinline__ F2 weights(const float* p, int i, int pair) const {
+    const int c = column(i) + 2 * pair;
+    return F2(c >= 0 && c < width ? __ldg(p + c) : 0.0f, c + 1 >= 0 && c + 1 < width ? __ldg(p + c + 1) : 0.0f);
+  }
+  __device__ __forceinline__ F2 skewed(const float* p, int i, int pair) const {
+    const int c = column(i) + 2 * pair;
+    return F2(p[skew(min(max(c, 0), width - 1), N)], p[skew(min(max(c + 1, 0), width - 1), N)]);
+  }
+};
+
+__device__ __forceinline__ void clear_sums(float* buf, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) buf[i] = 0.0f;
+}
+
+// HOLD (16 columns a thread): gamma and beta in registers, the next row's values loaded ahead; else (wide rows) gamma
+// and beta in shared memory, skewed.
+template <typename T, int NV, bool HOLD, bool ALIGNED>
+__global__ void __maxnreg__(HOLD ? FWD_REGS<T> : 128)
+    layer_norm_kernel(const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta,
+                      const uint8_t* __restrict__ valid, int rows, int width, int shift, int classes, float eps,
+                      int lanes, T* __restrict__ y, float* __restrict__ stats) {
+  constexpr int N = Vec<T>::N, P = N / 2;
+  extern __shared__ float s_dyn[];  // !HOLD: gamma and beta, skewed
+  __shared__ __align__(16) float s_buf[2][1][MAX_WARPS];
+  clear_sums(&s_buf[0][0][0], 2 * MAX_WARPS);
+  grid_dependency_wait();
+  const Block<T, NV, ALIGNED> b(rows, width, shift, classes, lanes);
+  const int per = skew(width, N) + 1;
+  if (!HOLD)
+    for (int c = threadIdx.x; c < width; c += blockDim.x) {
+      s_dyn[skew(c, N)] = __ldg(gamma + c);
+      s_dyn[per + skew(c, N)] = __ldg(beta + c);
+    }
+  __syncthreads();
+  F2 ga[HOLD ? NV : 1][P], be[HOLD ? NV : 1][P];
+  if constexpr (HOLD)
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < P; ++j) ga[i][j] = b.weights(gamma, i, j), be[i][j] = b.weights(beta, i, j);
   const float inv = 1.0f / static_cast<float>(width);
   int slot = 0;
-  for (long long row = static_cast<long long>(blockIdx.x) * groups + threadIdx.x / lanes; row < rows;
-       row += static_cast<long long>(gridDim.x) * groups) {
-    const RowSpan<T, ALIGNED> span(row, width, shift);
-    if (valid != nullptr && valid[row] == 0) {  // the same for all threads of the row
-      const float zero[N] = {};
-      for (int v = lane; v < span.count; v += lanes) span.store(y, v, width, zero);
-      if (lane < 2) stats[row * 2 + lane] = 0.0f;
-      continue;
-    }
-    uint4 raw[NV];
+  uint4 raw[NV];
+  bool on = false;  // the row whose values are in raw is there and no padding
+  auto fetch = [&](long long row) {
+    on = row < rows && (valid == nullptr || valid[row] != 0);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = lane + i * lanes;
-      raw[i] = v < span.count ? span.load_raw(x, v, width, total) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    float s[1] = {0.0f};
+    for (int i = 0; i < NV; ++i) raw[i] = on ? b.load(x, row, i) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  long long row = b.first();
+  fetch(row);
+  for (long long q = b.first_of_block(); q < rows; q += b.step, row += b.step) {
+    F2 f[NV][P];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float f[N];
-      Vec<T>::unpack(raw[i], f);
-      const int c0 = span.column(lane + i * lanes);
+    for (int i = 0; i < NV; ++i) Vec<T>::unpack(b.clean(raw[i], i), f[i]);
+    const bool counted = on;
+    if (HOLD) fetch(row + b.step);
+    F2 acc(0.0f, 0.0f);
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (ALIGNED ? c0 < width : (c0 + j >= 0 && c0 + j < width)) s[0] += f[j];
-    }
-    row_sum(s, warps, s_buf, slot);
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < P; ++j) acc = add2(acc, f[i][j]);  // zeros outside the row
+    float s[1] = {acc.get().x + acc.get().y};
+    row_sum(s, lanes, s_buf, slot);
     const float mean = s[0] * inv;
-    s[0] = 0.0f;
+    const F2 minus(-mean, -mean);
+    acc = F2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float f[N];
-      Vec<T>::unpack(raw[i], f);
-      const int c0 = span.column(lane + i * lanes);
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (ALIGNED ? c0 < width : (c0 + j >= 0 && c0 + j < width)) s[0] = fmaf(f[j] - mean, f[j] - mean, s[0]);
-    }
-    row_sum(s, warps, s_buf, slot);
-    const float rstd = 1.0f / sqrtf(s[0] * inv + eps);
+      for (int j = 0; j < P; ++j) f[i][j] = add2(f[i][j], minus);
+      if (b.vector(i) >= b.count || b.edge(i)) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = lane + i * lanes;
-      if (v >= span.count) continue;
-      float f[N];
-      Vec<T>::unpack(raw[i], f);
-      const int c0 = span.column(v);
-      if (ALIGNED) {
-#pragma unroll
-        for (int j = 0; j < N; j += 4) {
-          const float4 g = __ldg(reinterpret_cast<const float4*>(gamma + c0 + j));
-          const float4 b = __ldg(reinterpret_cast<const float4*>(beta + c0 + j));
-          f[j] = fmaf((f[j] - mean) * rstd, g.x, b.x);
-          f[j + 1] = fmaf((f[j + 1] - mean) * rstd, g.y, b.y);
-          f[j + 2] = fmaf((f[j + 2] - mean) * rstd, g.z, b.z);
-          f[j + 3] = fmaf((f[j + 3] - mean) * rstd, g.w, b.w);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int c = min(max(c0 + j, 0), width - 1);
-          f[j] = fmaf((f[j] - mean) * rstd, s_weights[skew(c, N)], s_weights[per + skew(c, N)]);
+        for (int j = 0; j < P; ++j) {
+          const int c = b.column(i) + 2 * j;
+          const float2 v = f[i][j].get();
+          f[i][j] = F2(c >= 0 && c < width ? v.x : 0.0f, c + 1 >= 0 && c + 1 < width ? v.y : 0.0f);
         }
       }
-      span.store(y, v, width, f);
+#pragma unroll
+      for (int j = 0; j < P; ++j) acc = fma2(f[i][j], f[i][j], acc);
     }
-    if (lane == 0) {
-      stats[row * 2] = mean;
-      stats[row * 2 + 1] = rstd;
+    s[0] = acc.get().x + acc.get().y;
+    row_sum(s, lanes, s_buf, slot);
+    const float rstd = 1.0f / sqrtf(s[0] * inv + eps);
+    if (row < rows) {
+      const F2 scale(rstd, rstd);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          if constexpr (HOLD)
+            f[i][j] = fma2(mul2(f[i][j], scale), ga[i][j], be[i][j]);
+          else
+            f[i][j] = fma2(mul2(f[i][j], scale), b.skewed(s_dyn, i, j), b.skewed(s_dyn + per, i, j));
+          if (!counted) f[i][j] = F2(0.0f, 0.0f);
+        }
+        b.store(y, row, i, f[i]);
+      }
+      if (b.lane == 0) *reinterpret_cast<float2*>(stats + row * 2) = counted ? make_float2(mean, rstd) : make_float2(0.0f, 0.0f);
     }
+    if (!HOLD) fetch(row + b.step);
   }
 }
 
-// Backward.  A thread has the same columns in every row of its block, so the weights' gradients are sums in its
-// registers: where rows start at different places of a vector, a block takes only rows of one place (rows `classes`
-// apart).  Blocks leave their sums in partial [blocks, 2, width], which weight_sum_kernel adds in a fixed order.
-// `warps` as above; with one warp a row, the block's warps add their sums through shared memory first.
-// With one vector a thread, a row's values and gamma stay in registers; with more, where they would not fit beside
-// the sums, gamma lies in shared memory (skewed) and the second pass over a row reads it again, out of the L2.
-template <typename T, int NV, bool ALIGNED>
-__global__ void __launch_bounds__(512)
+// Backward.  Blocks leave their sums of the weights' gradients in partial [blocks, 2, width], which weight_sum_kernel
+// adds in a fixed order; where a block has several rows at a time, they are added through shared memory first.
+// HOLD as above; else gamma lies in shared memory and the second pass over a row reads it again, out of the L2.
+template <typename T, int NV, bool HOLD, bool ALIGNED, bool RES>
+__global__ void __maxnreg__(HOLD ? BWD_REGS<T> : 128)
     layer_norm_bwd_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ gamma,
                           const float* __restrict__ stats, const uint8_t* __restrict__ valid,
-                          const T* __restrict__ dres, int rows, int width, int shift, int classes, int warps,
+                          const T* __restrict__ dres, int rows, int width, int shift, int classes, int lanes,
                           T* __restrict__ dx, float* __restrict__ partial) {
-  constexpr int N = Vec<T>::N;
-  constexpr bool HOLD = NV == 1;
-  extern __shared__ float s_dyn[];  // HOLD and one warp a row: [warps of the block][2][width]; !HOLD: gamma, skewed
-  __shared__ float s_buf[2][32][2];
+  constexpr int N = Vec<T>::N, P = N / 2;
+  extern __shared__ float s_dyn[];  // several rows at a time: [groups][2][width]; !HOLD: gamma, skewed
+  __shared__ __align__(16) float s_buf[2][2][MAX_WARPS];
+  clear_sums(&s_buf[0][0][0], 4 * MAX_WARPS);
   grid_dependency_wait();
-  const int lanes = warps * 32;
-  const int groups = blockDim.x / lanes;
-  const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
-  const int cls = blockIdx.x % classes;
-  const long long step = static_cast<long long>(gridDim.x / classes) * groups;
-  const long long total = static_cast<long long>(rows) * width;
+  const Block<T, NV, ALIGNED> b(rows, width, shift, classes, lanes);
   const float inv = 1.0f / static_cast<float>(width);
-  const int lead = RowSpan<T, ALIGNED>(cls, width, shift).lead;  // that of all the block's rows
-  float dg[NV][N], db[NV][N], ga[N];
-  if (!HOLD) {
+  F2 dg[NV][P], db[NV][P], ga[HOLD ? NV : 1][P];
+  if (!HOLD)
     for (int c = threadIdx.x; c < width; c += blockDim.x) s_dyn[skew(c, N)] = __ldg(gamma + c);
-    __syncthreads();
-  }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int c = (lane + i * lanes) * N - lead + j;
-      if (HOLD) ga[j] = c >= 0 && c < width ? __ldg(gamma + c) : 0.0f;
-      dg[i][j] = db[i][j] = 0.0f;
+    for (int j = 0; j < P; ++j) {
+      if constexpr (HOLD) ga[i][j] = b.weights(gamma, i, j);
+      dg[i][j] = db[i][j] = F2(0.0f, 0.0f);
     }
-  auto weight = [&](int c0, int j) { return HOLD ? ga[j] : s_dyn[skew(min(max(c0 + j, 0), width - 1), N)]; };
+  auto weight = [&](int i, int j) {
+    if constexpr (HOLD)
+      return ga[i][j];
+    else
+      return b.skewed(s_dyn, i, j);
+  };
   int slot = 0;
-  for (long long q = static_cast<long long>(blockIdx.x / classes) * groups + group; q * classes + cls < rows;
-       q += step) {
-    const long long row = q * classes + cls;
-    const RowSpan<T, ALIGNED> span(row, width, shift);
-    if (valid != nullptr && valid[row] == 0) {
-      const float zero[N] = {};
-      for (int v = lane; v < span.count; v += lanes) span.store(dx, v, width, zero);
-      continue;
+  constexpr int HV = HOLD ? NV : 1;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  uint4 nx[HV], ny[HV], nr[HV];  // HOLD: the next row's
+  float mean = 0.0f, rstd = 0.0f;
+  bool on = false;
+  auto fetch = [&](long long r) {
+    on = r < rows && (valid == nullptr || valid[r] != 0);
+    mean = rstd = 0.0f;
+    if (on) {
+      mean = __ldg(stats + r * 2);
+      rstd = __ldg(stats + r * 2 + 1);
     }
-    const float mean = __ldg(stats + row * 2), rstd = __ldg(stats + row * 2 + 1);
-    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-    uint4 xr, yr, rr = none;
-    if (HOLD && dres != nullptr && lane < span.count) rr = span.load_raw(dres, lane, width, total);
-    float s[2] = {0.0f, 0.0f};
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        nx[i] = on ? b.load(x, r, i) : none;
+        ny[i] = on ? b.load(dy, r, i) : none;
+        if (RES) nr[i] = on ? b.load(dres, r, i) : none;
+      }
+    }
+  };
+  long long row = b.first();
+  fetch(row);
+  for (long long q = b.first_of_block(); q < rows; q += b.step, row += b.step) {
+    const bool counted = on;
+    const F2 minus(-mean, -mean), scale(rstd, rstd);
+    uint4 xr[HV], yr[HV], rr[HV];
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) xr[i] = nx[i], yr[i] = ny[i], rr[i] = RES ? nr[i] : none;
+      fetch(row + b.step);
+    }
+    // xhat and dy of vector i, twice out of the same 16 bytes: fp32 copies would take twice the registers in bf16
+    auto values = [&](int i, F2 (&vx)[P], F2 (&vy)[P]) {
+      const int k = HOLD ? i : 0;
+      if constexpr (!HOLD) {
+        xr[0] = counted ? b.load(x, row, i) : none;
+        yr[0] = counted ? b.load(dy, row, i) : none;
+      }
+      Vec<T>::unpack(b.clean(xr[k], i), vx);
+      Vec<T>::unpack(b.clean(yr[k], i), vy);
+#pragma unroll
+      for (int j = 0; j < P; ++j) vx[j] = mul2(add2(vx[j], minus), scale);
+    };
+    F2 s0(0.0f, 0.0f), s1(0.0f, 0.0f);
+    // the elements of a vector that are not the row's own have dy = 0 and add nothing
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = lane + i * lanes;
-      xr = v < span.count ? span.load_raw(x, v, width, total) : none;
-      yr = v < span.count ? span.load_raw(dy, v, width, total) : none;
-      float fx[N], fy[N];
-      Vec<T>::unpack(xr, fx);
-      Vec<T>::unpack(yr, fy);
-      const int c0 = span.column(v);
+      F2 vx[P], vy[P];
+      values(i, vx, vy);
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (ALIGNED ? c0 < width : (c0 + j >= 0 && c0 + j < width)) {
-          const float xhat = (fx[j] - mean) * rstd, d = fy[j] * weight(c0, j);
-          s[0] += d;
-          s[1] = fmaf(d, xhat, s[1]);
-          dg[i][j] = fmaf(fy[j], xhat, dg[i][j]);
-          db[i][j] += fy[j];
+      for (int j = 0; j < P; ++j) {
+        const F2 d = mul2(vy[j], weight(i, j));
+        s0 = add2(s0, d);
+        s1 = fma2(d, vx[j], s1);
+        dg[i][j] = fma2(vy[j], vx[j], dg[i][j]);
+        db[i][j] = add2(db[i][j], vy[j]);
+      }
+    }
+    float s[2] = {s0.get().x + s0.get().y, s1.get().x + s1.get().y};
+    row_sum(s, lanes, s_buf, slot);
+    if constexpr (HOLD && sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {  // unpacked anew below
+        asm volatile("" : "+r"(xr[i].x), "+r"(xr[i].y), "+r"(xr[i].z), "+r"(xr[i].w));
+        asm volatile("" : "+r"(yr[i].x), "+r"(yr[i].y), "+r"(yr[i].z), "+r"(yr[i].w));
+      }
+    }
+    if (row < rows) {
+      const F2 m0(-s[0] * inv, -s[0] * inv), m1(-s[1] * inv, -s[1] * inv);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        F2 vx[P], vy[P], vr[P];
+        values(i, vx, vy);
+        if constexpr (RES) {
+          if constexpr (!HOLD) rr[0] = counted ? b.load(dres, row, i) : none;
+          Vec<T>::unpack(rr[HOLD ? i : 0], vr);  // a neighbour's values go no further than the store
         }
-    }
-    row_sum(s, warps, s_buf, slot);
-    const float m0 = s[0] * inv, m1 = s[1] * inv;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = lane + i * lanes;
-      if (v >= span.count) continue;
-      if (!HOLD) {
-        xr = span.load_raw(x, v, width, total);
-        yr = span.load_raw(dy, v, width, total);
-        if (dres != nullptr) rr = span.load_raw(dres, v, width, total);
+        for (int j = 0; j < P; ++j) {
+          const F2 g = fma2(vx[j], m1, fma2(vy[j], weight(i, j), m0));
+          if constexpr (RES)
+            vx[j] = fma2(g, scale, vr[j]);
+          else
+            vx[j] = mul2(g, scale);
+          if (!counted) vx[j] = F2(0.0f, 0.0f);
+        }
+        b.store(dx, row, i, vx);
       }
-      float fx[N], fy[N], fr[N];
-      Vec<T>::unpack(xr, fx);
-      Vec<T>::unpack(yr, fy);
-      Vec<T>::unpack(rr, fr);
-      const int c0 = span.column(v);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float xhat = (fx[j] - mean) * rstd;
-        const float g = rstd * (fmaf(fy[j], weight(c0, j), -m0) - xhat * m1);
-        fx[j] = dres != nullptr ? g + fr[j] : g;
-      }
-      span.store(dx, v, width, fx);
     }
+    if (!HOLD) fetch(row + b.step);
   }
-  float* out = groups > 1 ? s_dyn + group * 2 * width : partial + static_cast<size_t>(blockIdx.x) * 2 * width;
+  float* out = b.groups > 1 ? s_dyn + b.group * 2 * width : partial + static_cast<size_t>(blockIdx.x) * 2 * width;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int c = (lane + i * lanes) * N - lead + j;
+    for (int j = 0; j < P; ++j) {
+      const int c = b.column(i) + 2 * j;
+      const float2 g = dg[i][j].get(), e = db[i][j].get();
       if (c >= 0 && c < width) {
-        out[c] = dg[i][j];
-        out[width + c] = db[i][j];
+        out[c] = g.x;
+        out[width + c] = e.x;
+      }
+      if (c + 1 >= 0 && c + 1 < width) {
+        out[c + 1] = g.y;
+        out[width + c + 1] = e.y;
       }
     }
-  if (groups > 1) {
+  if (b.groups > 1) {
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * width; c += blockDim.x) {
       float sum = 0.0f;
-      for (int g = 0; g < groups; ++g) sum += s_dyn[g * 2 * width + c];
+      for (int g = 0; g < b.groups; ++g) sum += s_dyn[g * 2 * width + c];
       partial[static_cast<size_t>(blockIdx.x) * 2 * width + c] = sum;
     }
   }
@@ -391,110 +513,93 @@ int shift_of(const void* p) {
   return static_cast<int>((reinterpret_cast<uintptr_t>(p) % 16) / sizeof(T));
 }
 
-template <typename T, int NV, bool ALIGNED>
-lrm_status launch_fwd(lrm_ctx* ctx, const T* x, const float* gamma, const float* beta, const uint8_t* valid, int rows,
-                      int width, float eps, int warps, T* y, float* stats, cudaStream_t s) {
-  auto kern = layer_norm_kernel<T, NV, ALIGNED>;
-  const int threads = warps == 1 ? 128 : warps * 32;
-  const size_t smem = ALIGNED ? 0 : 2 * (width + width / Vec<T>::N + 1) * sizeof(float);
-  static thread_local int dev = -1, of_threads = 0, cap = 0;  // the last launch's: occupancy queries cost microseconds
-  static thread_local size_t of_smem = 0;
-  if (dev != ctx->device || of_threads != threads || of_smem != smem) {
-    LRM_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-    cap = resident_grid(ctx, kern, threads, smem);
-    dev = ctx->device, of_threads = threads, of_smem = smem;
-  }
-  const int need = ceil_div(rows, threads / (32 * warps));
-  return launch_dependent(kern, need < cap ? need : cap, threads, smem, 0, s, x, gamma, beta, valid, rows, width,
-                          shift_of<T>(x), eps, warps, y, stats);
-}
-
-template <typename T, bool ALIGNED>
-lrm_status forward(lrm_ctx* ctx, const void* x, const float* gamma, const float* beta, const uint8_t* valid, int rows,
-                   int width, float eps, void* y, float* stats, cudaStream_t s) {
-  const int nvec = row_vectors<T>(width, ALIGNED);
-  constexpr int MOST = 64 / Vec<T>::N;  // vectors a lane: 64 values
-  int warps = 1;
-  while (warps * 32 * MOST < nvec) warps *= 2;
-  // few rows: more warps a row, for their latency
-  while (warps < 16 && warps * 32 < nvec && static_cast<long long>(rows) * warps < ctx->sm_count * 4) warps *= 2;
-  const int nv = ceil_div(nvec, warps * 32);
-  auto go = [&](auto n) {
-    return launch_fwd<T, decltype(n)::value, ALIGNED>(ctx, static_cast<const T*>(x), gamma, beta, valid, rows, width,
-                                                      eps, warps, static_cast<T*>(y), stats, s);
-  };
-  if (nv <= 1) return go(std::integral_constant<int, 1>());
-  if (nv <= 2) return go(std::integral_constant<int, 2>());
-  if (nv <= 4) return go(std::integral_constant<int, 4>());
-  if (MOST == 8 || nv <= 8) return go(std::integral_constant<int, 8>());
-  return go(std::integral_constant<int, MOST>());
-}
-
-// How the backward cuts its work, the same for the launch and for the workspace's size.
-struct BwdPlan {
-  int warps, nv, threads, classes, blocks;
+// How a call cuts its work; the same for the backward's launch and its workspace's size.
+struct Plan {
+  int lanes, nv, threads, classes, blocks;
 };
 
-template <typename T>
-BwdPlan bwd_plan(int sm_count, int rows, int width, bool al) {
-  BwdPlan p;
+template <typename T, int COLS>
+Plan plan(int sm_count, int rows, int width, bool al, int resident) {
+  Plan p;
+  constexpr int HELD = COLS / Vec<T>::N;  // vectors of a thread that holds its columns' weights
   const int nvec = row_vectors<T>(width, al);
-  p.warps = 1;
-  while (p.warps < 16 && p.warps * 32 < nvec) ++p.warps;
-  p.nv = ceil_div(nvec, p.warps * 32);
-  p.threads = p.warps == 1 ? 256 : p.warps * 32;
+  p.lanes = 1;
+  while (p.lanes < 32 && p.lanes * HELD < nvec) p.lanes *= 2;
+  while (p.lanes >= 32 && p.lanes < 32 * MAX_WARPS && p.lanes * HELD < nvec) p.lanes += 32;
+  p.nv = ceil_div(nvec, p.lanes);
+  p.threads = p.lanes > 32 ? p.lanes : 128;
   p.classes = 1;
   if (!al) {
     p.classes = Vec<T>::N;
     for (int w = width; p.classes > 1 && w % 2 == 0; w /= 2) p.classes /= 2;
   }
-  const int groups = p.threads / (32 * p.warps);
+  const int groups = p.threads / p.lanes;
   const int per_class = ceil_div(ceil_div(rows, p.classes), groups);
-  int per_sm = 1024 / p.threads;
+  int per_sm = resident / p.threads;
   if (per_sm < 1) per_sm = 1;
   int most = sm_count * per_sm / p.classes;
   if (most < 1) most = 1;
   p.blocks = p.classes * (per_class < most ? (per_class > 0 ? per_class : 1) : most);
   return p;
 }
+template <typename T>
+Plan bwd_plan(int sm_count, int rows, int width, bool al) {
+  return plan<T, BWD_COLS<T>>(sm_count, rows, width, al, threads_per_sm(BWD_REGS<T>));
+}
 
-template <typename T, int NV, bool ALIGNED>
-lrm_status launch_bwd(const BwdPlan& p, const T* x, const T* dy, const float* gamma, const float* stats,
-                      const uint8_t* valid, const T* dres, int rows, int width, T* dx, float* partial,
-                      cudaStream_t s) {
-  auto kern = layer_norm_bwd_kernel<T, NV, ALIGNED>;
-  const int groups = p.threads / (32 * p.warps);
-  const size_t smem = groups > 1 ? static_cast<size_t>(groups) * 2 * width * sizeof(float)
-                      : NV > 1   ? static_cast<size_t>(width + width / Vec<T>::N + 1) * sizeof(float)
-                                 : 0;
+// Calls go(vectors a thread, whether it holds its columns' weights): up to 5 vectors in bf16 and 9 in fp32 at the largest
+// width, one more than it fills where rows are cut.
+template <typename T, int COLS, typename Go>
+lrm_status with_vectors(int nv, Go go) {
+  constexpr int HELD = COLS / Vec<T>::N;
+  if (nv <= HELD) return go(std::integral_constant<int, HELD>(), std::true_type());
+  if constexpr (HELD < 2)
+    if (nv <= 2) return go(std::integral_constant<int, 2>(), std::false_type());
+  if constexpr (HELD < 3)
+    if (nv <= 3) return go(std::integral_constant<int, 3>(), std::false_type());
+  if constexpr (Vec<T>::N == 4)
+    if (nv > 5) return go(std::integral_constant<int, 9>(), std::false_type());
+  return go(std::integral_constant<int, 5>(), std::false_type());
+}
+
+template <typename Kern>
+lrm_status allow_smem(Kern kern, size_t smem) {
   if (smem > 40 * 1024)
     LRM_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-  return launch_dependent(kern, p.blocks, p.threads, smem, 0, s, x, dy, gamma, stats, valid, dres, rows, width,
-                          shift_of<T>(x), p.classes, p.warps, dx, partial);
+  return LRM_OK;
 }
 
 template <typename T, bool ALIGNED>
+lrm_status forward(lrm_ctx* ctx, const void* x, const float* gamma, const float* beta, const uint8_t* valid, int rows,
+                   int width, float eps, void* y, float* stats, cudaStream_t s) {
+  const Plan p = plan<T, FWD_COLS<T>>(ctx->sm_count, rows, width, ALIGNED, threads_per_sm(FWD_REGS<T>));
+  return with_vectors<T, FWD_COLS<T>>(p.nv, [&](auto n, auto hold) {
+    auto kern = layer_norm_kernel<T, decltype(n)::value, decltype(hold)::value, ALIGNED>;
+    const size_t smem = decltype(hold)::value ? 0 : 2 * (width + width / Vec<T>::N + 1) * sizeof(float);
+    const lrm_status st = allow_smem(kern, smem);
+    if (st != LRM_OK) return st;
+    return launch_dependent(kern, p.blocks, p.threads, smem, 0, s, static_cast<const T*>(x), gamma, beta, valid, rows,
+                            width, shift_of<T>(x), p.classes, eps, p.lanes, static_cast<T*>(y), stats);
+  });
+}
+
+template <typename T, bool ALIGNED, bool RES>
 lrm_status backward(lrm_ctx* ctx, const void* x, const void* dy, const float* gamma, const float* stats,
                     const uint8_t* valid, const void* dres, int rows, int width, void* dx, float* dgamma,
                     float* dbeta, float* partial, cudaStream_t s) {
-  const BwdPlan p = bwd_plan<T>(ctx->sm_count, rows, width, ALIGNED);
-  auto go = [&](auto n) {
-    return launch_bwd<T, decltype(n)::value, ALIGNED>(p, static_cast<const T*>(x), static_cast<const T*>(dy), gamma,
-                                                      stats, valid, static_cast<const T*>(dres), rows, width,
-                                                      static_cast<T*>(dx), partial, s);
-  };
-  // vectors a thread: up to 5 in bf16 and 9 in fp32 at the largest width, one more than it fills where rows are cut
-  lrm_status st;
-  if (p.nv <= 1)
-    st = go(std::integral_constant<int, 1>());
-  else if (p.nv <= 2)
-    st = go(std::integral_constant<int, 2>());
-  else if (p.nv <= 3)
-    st = go(std::integral_constant<int, 3>());
-  else if (p.nv <= 5)
-    st = go(std::integral_constant<int, 5>());
-  else
-    st = go(std::integral_constant<int, Vec<T>::N == 4 ? 9 : 5>());
+  const Plan p = bwd_plan<T>(ctx->sm_count, rows, width, ALIGNED);
+  const int groups = p.threads / p.lanes;
+  const lrm_status st = with_vectors<T, BWD_COLS<T>>(p.nv, [&](auto n, auto hold) {
+    auto kern = layer_norm_bwd_kernel<T, decltype(n)::value, decltype(hold)::value, ALIGNED, RES>;
+    const size_t smem = groups > 1                ? static_cast<size_t>(groups) * 2 * width * sizeof(float)
+                        : decltype(hold)::value ? 0
+                                                  : (width + width / Vec<T>::N + 1) * sizeof(float);
+    const lrm_status a = allow_smem(kern, smem);
+    if (a != LRM_OK) return a;
+    return launch_dependent(kern, p.blocks, p.threads, smem, 0, s, static_cast<const T*>(x),
+                            static_cast<const T*>(dy), gamma, stats, valid, static_cast<const T*>(dres), rows, width,
+                            shift_of<T>(x), p.classes, p.lanes, static_cast<T*>(dx), partial);
+  });
   if (st != LRM_OK) return st;
   return launch_dependent(weight_sum_kernel, ceil_div(2ll * width, 32), 32 * WS_ROWS, 0, 0, s, partial, p.blocks,
                           width, dgamma, dbeta);
@@ -533,7 +638,7 @@ extern "C" lrm_status lrm_layer_norm(lrm_ctx* ctx, const void* x, int32_t dtype,
   if (x == nullptr || gamma == nullptr || beta == nullptr || y == nullptr || stats == nullptr)
     return LRM_ERR_INVALID_ARG;
   const size_t es = dtype == LRM_F32 ? 4 : 2;
-  if (!aligned(x, es) || !aligned(y, es) || !aligned(gamma, 4) || !aligned(beta, 4) || !aligned(stats, 4))
+  if (!aligned(x, es) || !aligned(y, es) || !aligned(gamma, 4) || !aligned(beta, 4) || !aligned(stats, 8))
     return LRM_ERR_ALIGN;
   // the vectors of a row cut x and y alike
   if (reinterpret_cast<uintptr_t>(x) % 16 != reinterpret_cast<uintptr_t>(y) % 16) return LRM_ERR_ALIGN;
@@ -541,10 +646,10 @@ extern "C" lrm_status lrm_layer_norm(lrm_ctx* ctx, const void* x, int32_t dtype,
   if (!guard.ok) return LRM_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == LRM_F32)
-    return aligned_rows<float>(x, y, gamma, beta, width)
+    return aligned_rows<float>(x, y, nullptr, nullptr, width)
                ? forward<float, true>(ctx, x, gamma, beta, valid, rows, width, eps, y, stats, s)
                : forward<float, false>(ctx, x, gamma, beta, valid, rows, width, eps, y, stats, s);
-  return aligned_rows<uint16_t>(x, y, gamma, beta, width)
+  return aligned_rows<uint16_t>(x, y, nullptr, nullptr, width)
              ? forward<uint16_t, true>(ctx, x, gamma, beta, valid, rows, width, eps, y, stats, s)
              : forward<uint16_t, false>(ctx, x, gamma, beta, valid, rows, width, eps, y, stats, s);
 }
@@ -585,13 +690,16 @@ extern "C" lrm_status lrm_layer_norm_backward(lrm_ctx* ctx, const void* x, int32
     return LRM_OK;
   }
   float* part = static_cast<float*>(ws);
+  auto go = [&](auto type, auto al) {
+    using T = decltype(type);
+    constexpr bool ALIGNED = decltype(al)::value;
+    return dres != nullptr ? backward<T, ALIGNED, true>(ctx, x, dy, gamma, stats, valid, dres, rows, width, dx,
+                                                        dgamma, dbeta, part, s)
+                           : backward<T, ALIGNED, false>(ctx, x, dy, gamma, stats, valid, dres, rows, width, dx,
+                                                         dgamma, dbeta, part, s);
+  };
   if (dtype == LRM_F32)
-    return aligned_rows<float>(x, dy, dx, dres, width)
-               ? backward<float, true>(ctx, x, dy, gamma, stats, valid, dres, rows, width, dx, dgamma, dbeta, part, s)
-               : backward<float, false>(ctx, x, dy, gamma, stats, valid, dres, rows, width, dx, dgamma, dbeta, part,
-                                        s);
-  return aligned_rows<uint16_t>(x, dy, dx, dres, width)
-             ? backward<uint16_t, true>(ctx, x, dy, gamma, stats, valid, dres, rows, width, dx, dgamma, dbeta, part, s)
-             : backward<uint16_t, false>(ctx, x, dy, gamma, stats, valid, dres, rows, width, dx, dgamma, dbeta, part,
-                                         s);
+    return aligned_rows<float>(x, dy, dx, dres, width) ? go(float(), std::true_type()) : go(float(), std::false_type());
+  return aligned_rows<uint16_t>(x, dy, dx, dres, width) ? go(uint16_t(), std::true_type())
+                                                         : go(uint16_t(), std::false_type());
 }
