@@ -29,6 +29,7 @@
 // Every wait is bounded as in the other grouped products (grouped_gemm.cu).
 #include <cuda_bf16.h>
 
+#include "f32x2.cuh"
 #include "grouped.cuh"
 #include "lrm_internal.cuh"
 #include "swiglu.cuh"
@@ -410,6 +411,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
 }
 
+// ---------------------------------------------------------------------------
+// Few pairs (a token or a few): the products are bound by the bytes of the weights, and the tiles above leave half of
+// the SMs without one (48 tiles for eight pairs of 768 features) and spend their time in set-up and barriers.  Here a
+// warp takes four weight rows (up: gate and up of two features; down: four features) for one pair: its lanes stream
+// the rows 16 bytes at a time, K in steps of 256, with two steps in flight, and read the pair's row out of L1; the
+// sums are fp32 and are added over the lanes at the end.  Pairs of one expert read its weights again, out of the L2.
+
+// Measured against the tiles, up and down together, h = 2048, I = 768: 17.4 and 32.5 us for one token of 8 pairs over
+// 128 experts (3.9 + 7.4 us of reading at the HBM's rate), 37.9 and 51.6 for 32 pairs, 60.6 and 69.3 for 64, 82.8 and
+// 76.6 for 96; 25.5 and 26.8 for 32 pairs over 4 experts, 38.1 and 26.8 for 48.
+constexpr int FEW_PAIRS = 64;  // at most
+constexpr int FEW_ANYWAY = 32;  // also where several pairs are sure to share an expert
+constexpr int FEW_THREADS = 256;
+
+template <bool UP>
+__global__ void __launch_bounds__(FEW_THREADS, 3)
+    ffn_few_kernel(const uint16_t* __restrict__ in, const uint16_t* __restrict__ weight,
+                   const int32_t* __restrict__ offsets, const int32_t* __restrict__ ids, int E, int K, int M, int N,
+                   int div, int max_rows, uint16_t* __restrict__ out, uint16_t* __restrict__ ab,
+                   unsigned int* status) {
+  __shared__ int s_expert[FEW_PAIRS], s_ids[FEW_PAIRS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < max_rows) s_expert[threadIdx.x] = -1;
+  __syncthreads();
+  grid_dependency_wait();
+  if (threadIdx.x < max_rows) s_ids[threadIdx.x] = __ldg(ids + threadIdx.x);
+  for (int e = threadIdx.x; e < E; e += FEW_THREADS) {
+    int st, ln;
+    segment(offsets, e, max_rows, st, ln);
+    for (int i = 0; i < ln; ++i) s_expert[st + i] = e;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(offsets + E) > max_rows) raise_flag(status, LRM_ERR_SHAPE);
+  __syncthreads();
+  grid_dependency_launch();
+  constexpr int FEATURES = UP ? 2 : 4;  // of a warp's task
+  const int groups = M / FEATURES;      // M is a multiple of 8
+  const int tasks = max_rows * groups;
+  const int kv = K / 8;  // 16-byte vectors of a row
+  // tasks go round the blocks first: what is left after whole rounds is spread over the SMs
+  for (int task = warp * gridDim.x + blockIdx.x; task < tasks; task += gridDim.x * (FEW_THREADS / 32)) {
+    const int r = task / groups, f = (task - r * groups) * FEATURES;
+    const int e = s_expert[r], u = s_ids[r];
+    if (e < 0) continue;  // beyond the total
+    if (u < 0 || u >= N) {
+      if (lane == 0) raise_flag(status, LRM_ERR_INDEX);
+      continue;
+    }
+    // rows f (+ 1; up: and those of the up projection; down: + 2, + 3) of the expert
+    const uint4* w0 = reinterpret_cast<const uint4*>(weight + (static_cast<size_t>(e) * (UP ? 2 : 1) * M + f) * K) + lane;
+    const size_t far = static_cast<size_t>(UP ? M : 2) * kv;
+    const uint4* x0 = reinterpret_cast<const uint4*>(in + static_cast<size_t>(u / div) * K) + lane;
+    F2 acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = F2(0.0f, 0.0f);
+    constexpr int STEPS = 2;  // of 32 vectors, in flight (four, with a third less blocks: the same)
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    for (int v = lane; v < kv; v += 32 * STEPS, w0 += 32 * STEPS, x0 += 32 * STEPS) {
+      uint4 w[STEPS][4], x[STEPS];
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const bool in_k = v + 32 * s < kv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[s][i] = in_k ? ld_stream(w0 + 32 * s + (i & 1) * kv + (i >> 1) * far) : none;
+        x[s] = in_k ? __ldg(x0 + 32 * s) : none;
+      }
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const F2 xa(bf16_lo(x[s].x), bf16_hi(x[s].x)), xb(bf16_lo(x[s].y), bf16_hi(x[s].y));
+        const F2 xc(bf16_lo(x[s].z), bf16_hi(x[s].z)), xd(bf16_lo(x[s].w), bf16_hi(x[s].w));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4& q = w[s][i];
+          acc[i] = fma2(F2(bf16_lo(q.x), bf16_hi(q.x)), xa, acc[i]);
+          acc[i] = fma2(F2(bf16_lo(q.y), bf16_hi(q.y)), xb, acc[i]);
+          acc[i] = fma2(F2(bf16_lo(q.z), bf16_hi(q.z)), xc, acc[i]);
+          acc[i] = fma2(F2(bf16_lo(q.w), bf16_hi(q.w)), xd, acc[i]);
+        }
+      }
+    }
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = acc[i].get();
+      s[i] = a.x + a.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+    if (lane != 0) continue;
+    if (UP) {  // a of both features, then b
+      *reinterpret_cast<uint32_t*>(out + static_cast<size_t>(u) * M + f) =
+          pack_bf16x2(silu(s[0]) * s[2], silu(s[1]) * s[3]);
+      if (ab != nullptr) {
+        uint16_t* o = ab + static_cast<size_t>(u) * 2 * M + f;
+        *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(s[0], s[1]);
+        *reinterpret_cast<uint32_t*>(o + M) = pack_bf16x2(s[2], s[3]);
+      }
+    } else {
+      *reinterpret_cast<uint2*>(out + static_cast<size_t>(u) * M + f) =
+          make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+    }
+  }
+}
+
 constexpr int CB_THREADS = 256;
 
 // y_t = sum_j alpha_tj row_tj in fp32, one thread per token and 8 columns; a pair with gate 0 is not read.
@@ -471,6 +577,19 @@ lrm_status launch_ffn(lrm_ctx* ctx, const uint16_t* in, uint64_t in_rows, const 
                       const int32_t* offsets, const int32_t* ids, const lrm_dims& d, int max_rows, uint16_t* out,
                       uint16_t* ab, cudaStream_t s) {
   using C = CfgFfn;
+  const int K = UP ? d.h : d.I, M = UP ? d.I : d.h, N = d.T * d.k;
+  if (max_rows <= FEW_ANYWAY || (max_rows <= FEW_PAIRS && max_rows <= d.E)) {
+    auto few = ffn_few_kernel<UP>;
+    static thread_local int few_device = -1, grid = 0;
+    if (few_device != ctx->device) {
+      grid = resident_grid(ctx, few, FEW_THREADS, 0);
+      few_device = ctx->device;
+    }
+    const long long tasks = static_cast<long long>(max_rows) * (M / (UP ? 2 : 4));
+    const long long need = (tasks + FEW_THREADS / 32 - 1) / (FEW_THREADS / 32);
+    return launch_dependent(few, static_cast<int>(need < grid ? need : grid), FEW_THREADS, 0, 0, s, in, weight,
+                            offsets, ids, d.E, K, M, N, UP ? d.k : 1, max_rows, out, ab, ctx->d_status);
+  }
   auto kern = ffn_kernel<UP>;
   static thread_local int configured_device = -1;
   static thread_local int clusters = 0;
@@ -487,7 +606,6 @@ lrm_status launch_ffn(lrm_ctx* ctx, const uint16_t* in, uint64_t in_rows, const 
     clusters = n;
     configured_device = ctx->device;
   }
-  const int K = UP ? d.h : d.I, M = UP ? d.I : d.h, N = d.T * d.k;
   alignas(64) CUtensorMap ma, mb;
   lrm_status st = encode_weight(ctx, &ma, weight, K, M, UP ? 2 : 1, d.E);
   if (st != LRM_OK) return st;

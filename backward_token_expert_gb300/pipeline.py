@@ -431,6 +431,176 @@ class Router:
         return L.lrm_get_device_status(self.ctx, stream)
 
 
+class _Operator:
+    """Device buffers of a fixed shape beside the calls that use them, for one
+    device; several may share a context."""
+
+    def _open(self, device, ctx):
+        self.device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+        if self.device.index is None:  # "cuda": tensors name the device with its index
+            self.device = torch.device(self.device.type, torch.cuda.current_device())
+        self._own_ctx = ctx is None
+        self.ctx = L.lrm_create(self.device.index or 0) if ctx is None else ctx
+
+    def _made(self, *held):
+        """After the buffers: their memory is the current stream's, where fills
+        and work on what it held before may be pending."""
+        self._buffers = tuple(t for t in held if t is not None)
+        home = torch.cuda.current_stream(self.device)
+        self._streams = {home.cuda_stream}
+        if not torch.cuda.is_current_stream_capturing():
+            home.synchronize()
+
+    def _held(self):
+        return self._buffers
+
+    def device_status(self, stream=None) -> int:
+        return L.lrm_get_device_status(self.ctx, stream)
+
+    def close(self):
+        if getattr(self, "_own_ctx", False) and getattr(self, "ctx", None):
+            L.lrm_destroy(self.ctx)
+        self.ctx = None
+
+    def __del__(self):  # pragma: no cover - best effort
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class ExpertFFN(_Operator):
+    """The forward of the routed experts, the gated feed-forward block
+    W (silu(Wg x) * (Wu x)), for the pairs of a routing (lrm_ffn_up,
+    lrm_ffn_down, lrm_ffn_combine): ``y`` [T, h] bf16, and what the backward
+    reads: ``phi`` [N, I] and, unless `save` is False, ``ab`` [N, 2I]."""
+
+    def __init__(self, T, E, k, h, I, save: bool = True, device=0, ctx=None):
+        self.T, self.E, self.k, self.h, self.I = int(T), int(E), int(k), int(h), int(I)
+        self.N = self.T * self.k
+        self.dims = L.dims_of(T, E, k, h, I)
+        self._open(device, ctx)
+        bf = dict(dtype=torch.bfloat16, device=self.device)
+        self.phi = torch.zeros(self.N, self.I, **bf)
+        self.ab = torch.zeros(self.N, 2 * self.I, **bf) if save else None
+        self.rows = torch.empty(self.N, self.h, **bf)
+        self.y = torch.empty(self.T, self.h, **bf)
+        self._made(self.phi, self.ab, self.rows, self.y)
+
+    def forward(self, x, W1, W, offsets, ids, alpha, stream=None):
+        """x [T, h], W1 [E, 2I, h] (gate rows, then up rows) and W [E, h, I] bf16;
+        `offsets` [E+1] and `ids` int32: the pairs of every expert (the offsets and
+        the bucket of route statistics); `alpha` [N] fp32: their gates, 0 for pairs
+        that are in no segment."""
+        bf = torch.bfloat16
+        _require(x, "x", bf, (self.T, self.h), self.device)
+        _require(W1, "W1", bf, (self.E, 2 * self.I, self.h), self.device)
+        _require(W, "W", bf, (self.E, self.h, self.I), self.device)
+        _require(offsets, "offsets", torch.int32, (self.E + 1,), self.device)
+        if alpha.numel() != self.N:
+            raise ValueError(f"alpha must hold {self.N} gates")
+        _require(alpha, "alpha", torch.float32, tuple(alpha.shape), self.device)
+        _require(ids, "ids", torch.int32, (ids.numel(),), self.device)
+        raw = _stream_of(self, stream)
+        n = min(self.N, ids.numel())
+        L.lrm_ffn_up(self.ctx, x, W1, offsets, ids, self.dims, n, self.ab, self.phi, raw)
+        L.lrm_ffn_down(self.ctx, self.phi, W, offsets, ids, self.dims, n, self.rows, raw)
+        L.lrm_ffn_combine(self.ctx, self.rows, alpha, self.dims, self.y, raw)
+        return self.y
+
+
+class LayerNorm(_Operator):
+    """Layer norm of `rows` rows of `width` values (lrm_layer_norm,
+    lrm_layer_norm_backward).  ``forward`` writes ``y`` and ``stats`` (mean and
+    1 / standard deviation of every row), ``backward`` reads them and writes
+    ``dx``, ``dgamma`` and ``dbeta`` (fp32)."""
+
+    def __init__(self, rows, width, dtype=torch.bfloat16, eps: float = 1e-5, device=0, ctx=None):
+        self.rows, self.width, self.dtype, self.eps = int(rows), int(width), dtype, float(eps)
+        if dtype not in _DTYPES:
+            raise ValueError("layer norm takes float32 or bfloat16")
+        if not self.eps >= 0:
+            raise ValueError("eps must be at least 0")
+        self._open(device, ctx)
+        need = L.lrm_layer_norm_workspace(self.ctx, self.rows, self.width)
+        f32 = dict(dtype=torch.float32, device=self.device)
+        self.y = torch.empty(self.rows, self.width, dtype=dtype, device=self.device)
+        self.stats = torch.empty(self.rows, 2, **f32)
+        self.dx = torch.empty_like(self.y)
+        self.dgamma, self.dbeta = torch.zeros(self.width, **f32), torch.zeros(self.width, **f32)
+        self.ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        self._made(self.y, self.stats, self.dx, self.dgamma, self.dbeta, self.ws)
+
+    def _check(self, valid, **tensors):
+        for name, t in tensors.items():
+            _require(t, name, self.dtype, (self.rows, self.width), self.device)
+            if t.data_ptr() % 16 != 0:
+                raise ValueError(f"{name} must be 16-byte aligned")
+        if valid is not None:
+            _require(valid, "valid", torch.uint8, (self.rows,), self.device)
+
+    def forward(self, x, gamma, beta, valid=None, stream=None):
+        """`gamma`, `beta` [width] fp32; rows whose entry of `valid` [rows] uint8 is
+        0 become zeros and take no part in the backward."""
+        self._check(valid, x=x)
+        for name, t in (("gamma", gamma), ("beta", beta)):
+            _require(t, name, torch.float32, (self.width,), self.device)
+        L.lrm_layer_norm(self.ctx, x, _DTYPES[self.dtype], gamma, beta, valid, self.rows, self.width, self.eps, self.y,
+                         self.stats, _stream_of(self, stream))
+        return self.y
+
+    def backward(self, x, dy, gamma, valid=None, dres=None, stream=None):
+        """The gradients of the last ``forward`` (x, gamma and valid as there) for the
+        output's gradient `dy`; `dres` is added to dx: a residual connection's share."""
+        self._check(valid, x=x, dy=dy, **({} if dres is None else dict(dres=dres)))
+        _require(gamma, "gamma", torch.float32, (self.width,), self.device)
+        L.lrm_layer_norm_backward(self.ctx, x, _DTYPES[self.dtype], dy, gamma, self.stats, valid, dres, self.rows,
+                                  self.width, self.dx, self.dgamma, self.dbeta, self.ws, self.ws.numel(),
+                                  _stream_of(self, stream))
+        return self.dx
+
+
+class Dropout(_Operator):
+    """Dropout with a residual (lrm_dropout_add): the mask is drawn from `seed`,
+    `offset` and the device counter ``step`` and never stored.  ``backward`` draws
+    that of the last ``forward`` again as long as ``step`` is the same;
+    ``advance`` counts it up (also in a captured graph)."""
+
+    def __init__(self, p: float, seed: int = 0, offset: int = 0, device=0, ctx=None):
+        if not 0.0 <= float(p) <= 1.0:
+            raise ValueError("p must be in [0, 1]")
+        self.p, self.seed, self.offset = float(p), int(seed) & ((1 << 64) - 1), int(offset) & ((1 << 64) - 1)
+        self._open(device, ctx)
+        self.step = torch.zeros(1, dtype=torch.int64, device=self.device)
+        self._made(self.step)
+
+    def _call(self, x, residual, out, stream):
+        if x.dtype not in _DTYPES:
+            raise ValueError("dropout takes float32 or bfloat16")
+        for name, t in (("x", x), ("out", out)) + ((("residual", residual),) if residual is not None else ()):
+            _require(t, name, x.dtype, tuple(x.shape), self.device)
+        L.lrm_dropout_add(self.ctx, x, residual, _DTYPES[x.dtype], x.numel(), self.p, self.seed, self.offset, self.step,
+                          out, _stream_of(self, stream))
+        return out
+
+    def forward(self, x, out, residual=None, stream=None):
+        """out = residual + dropout(x); out may be x or residual itself."""
+        return self._call(x, residual, out, stream)
+
+    def backward(self, dy, out, stream=None):
+        """out = dy where the forward kept the element, over 1 - p, and 0 elsewhere."""
+        return self._call(dy, None, out, stream)
+
+    def advance(self, stream=None) -> None:
+        """A new mask from here on.  `stream`: a torch stream or None, the current one."""
+        if stream is None:
+            self.step.add_(1)
+        else:
+            _stream_of(self, stream)
+            with torch.cuda.stream(stream):
+                self.step.add_(1)
+
+
 def _dense(t) -> bool:
     """Whether the tensor's elements fill its memory range, in any dimension order."""
     run = 1
@@ -621,6 +791,92 @@ class TrainingStep:
         self.clip.close()
         self.router.close()
         self.rec.close()
+
+
+class SublayerStep(TrainingStep):
+    """The training step of a whole pre-norm MoE sublayer,
+    out = x + dropout(experts(norm(x))), enqueued on one stream:
+
+        normalize  x -> n, the layer norm's output (``norm``); the caller's router
+                   product turns it into logits
+        route      logits -> ids, gates, losses, and the pairs of every expert
+        experts    n -> y (``ffn``), x + dropout(y) in ``out``; what the backward
+                   needs of it is kept
+        backward   the output's gradient -> the weights' gradients, clipped over
+                   all of them, and ``norm.dx`` [T, h] bf16, that of x
+
+    In the backward, lrm_ffn_backward takes the retained pairs from their output
+    gradients to the first projections' and the gates' in one product.  Weight
+    gradients: ``rec.buf.dW``, ``rec.fc1.dW1``, ``dWr``, ``norm.dgamma`` and
+    ``norm.dbeta``.  ``drop.advance()`` draws a new mask for the next step."""
+
+    def __init__(self, T, E, k, h, I, cf=Fraction(5, 4), rho=Fraction(3, 4), aux_coef: float = 0.01,
+                 z_coef: float = 0.001, max_norm: float = 1.0, p: float = 0.0, seed: int = 0, eps: float = 1e-5,
+                 device=0):
+        super().__init__(T, E, k, h, I, cf, rho, aux_coef, z_coef, max_norm, device)
+        rec = self.rec
+        dev, ctx = self.dWr.device, rec.ctx
+        self.norm = LayerNorm(T, h, torch.bfloat16, eps, dev, ctx)
+        self.ffn = ExpertFFN(T, E, k, h, I, device=dev, ctx=ctx)
+        self.drop = Dropout(p, seed, device=dev, ctx=ctx)
+        bf = dict(dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty(T, h, **bf)
+        self._g, self._dn = torch.empty(T, h, **bf), torch.empty(T, h, **bf)
+        self._side = torch.empty(max(rec.max_rows, 1), 8, **bf)  # second operand of a compaction that has only one
+        need = L.lrm_ffn_backward_workspace(ctx, rec.dims, rec.max_rows)
+        self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        self._logits = self._valid = None
+        self.clip.close()
+        self.clip = GradClip([rec.buf.dW, rec.fc1.dW1, self.dWr, self.norm.dgamma, self.norm.dbeta], ctx=ctx)
+
+    def normalize(self, x, gamma, beta, valid=None, stream=None):
+        """The layer norm of x [T, h] bf16; rows that `valid` leaves out become zeros."""
+        self._valid = valid
+        return self.norm.forward(x, gamma, beta, valid, stream)
+
+    def route(self, logits, valid=None, stream=None):
+        """As in TrainingStep (`valid` as given to ``normalize``), and the routed pairs by expert."""
+        super().route(logits, valid, stream)
+        self._logits = logits
+        self.rec.route_stats(logits, self.router.expert_idx, stream, counted=self.router.counted)
+
+    def experts(self, x, W1, W, stream=None):
+        """out = x + dropout(y), y the gated sum of the experts' outputs for the normalised rows."""
+        b = self.rec.buf
+        y = self.ffn.forward(self.norm.y, W1, W, b.offsets, b.bucket[: self.rec.N], self.router.alpha, stream)
+        return self.drop.forward(y, self.out, x, stream)
+
+    def backward(self, dout, x, W, W1, Wr, gamma, stream=None):
+        """For dout [T, h] bf16, the gradient of ``out``; x, W, W1 and gamma as in the forward, Wr [E, h] bf16."""
+        rec, r, f, b = self.rec, self.router, self.rec.fc1, self.rec.buf
+        T, E, k, h, I = rec.T, rec.E, rec.k, rec.h, rec.I
+        n, R = self.norm.y, rec.max_rows
+        self.drop.backward(dout, self._g, stream)
+        rec.score(self._g, self.ffn.phi, r.alpha, stream)
+        rec.select(stream)
+        rec.compact(self._g, self.ffn.phi, r.alpha, stream)
+        L.lrm_ffn_backward(rec.ctx, b.delta_c, W, self.ffn.ab, b.sel_offsets, b.sel_ids, rec.dims, R, f.dh1, rec.dgate,
+                           self._ws, self._ws.numel(), stream)
+        rec.wgrad(stream)
+        L.lrm_compact(rec.ctx, n, self.ffn.phi, f.ones, b.sel_offsets, b.sel_ids, L.Dims(T, E, k, h, 8), R, f.xc,
+                      self._side, None, stream)
+        d_fc1 = L.Dims(T, E, k, 2 * I, h)
+        L.lrm_grouped_dgrad(rec.ctx, f.dh1, W1, b.sel_offsets, d_fc1, R, f.dxc, stream)
+        L.lrm_grouped_wgrad(rec.ctx, f.dh1, f.xc, b.sel_offsets, d_fc1, R, 0, f.dW1, stream)
+        L.lrm_combine_rows(rec.ctx, f.dxc, b.sel_offsets, b.sel_ids, rec.dims, R, h, f.dx, f.ws, f.ws.numel(), stream)
+        r.backward(self._logits, rec.dgate, stream=stream)
+        L.lrm_grouped_wgrad(rec.ctx, r.dlogits, n, self._segment, self._dims_r, T, 0, self.dWr, stream)
+        L.lrm_grouped_dgrad(rec.ctx, r.dlogits, Wr, self._segment, self._dims_r, T, self.dxr, stream)
+        # the two gradients of n, through the experts and through the router
+        L.lrm_dropout_add(rec.ctx, f.dx, self.dxr, L.DTYPE_BF16, T * h, 0.0, 0, 0, None, self._dn, stream)
+        self.norm.backward(x, self._dn, gamma, self._valid, dout, stream)
+        self.clip.clip(self.max_norm, stream)
+        return self.norm.dx
+
+    def close(self):
+        for part in (self.norm, self.ffn, self.drop):
+            part.close()
+        super().close()
 
 
 def to_device_inputs(inp, device="cuda"):

@@ -66,7 +66,8 @@ SHAPES = [  # T, E, k, h, I, skew, masked
     (256, 8, 2, 64, 32, 1.0, False), (300, 5, 3, 200, 136, 2.0, True), (520, 2, 1, 328, 64, 0.5, False),
     (900, 20, 3, 1032, 1000, 1.0, True), (700, 160, 6, 136, 264, 1.5, True), (2100, 3, 2, 64, 8, 0.3, False),
     (77, 16, 4, 8, 520, 1.0, False), (40, 1024, 32, 48, 24, 0.5, False), (513, 1, 1, 520, 776, 0.0, False),
-    (64, 6, 2, 2048, 768, 0.5, False)]
+    (64, 6, 2, 2048, 768, 0.5, False), (8, 128, 8, 264, 136, 0.5, False), (32, 2, 1, 1032, 520, 0.0, True),
+    (33, 2, 1, 72, 64, 0.0, False), (13, 64, 5, 2048, 40, 3.0, True)]
 
 
 @pytest.mark.parametrize("T,E,k,h,I,skew,masked", SHAPES)
