@@ -344,6 +344,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
         tmem_ld_16x256b_x4(taddr + c, v[0]);
         tmem_ld_16x256b_x4(taddr + (16u << 16) + c, v[1]);
         tmem_ld_wait();
+        pin_registers(v[0]);
+        pin_registers(v[1]);
         auto val = [&](int hh, int n, int x) { return __uint_as_float(v[hh][4 * n + x]); };
         __syncwarp();  // the previous chunk's reads of the buffer are done
         if (!UP || ab != nullptr) {

@@ -520,7 +520,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgPair<BN>::THREADS
 //             contiguous bytes (16-byte stores); rows past the segment are
 //             skipped.
 
-template <int BNR>
+#ifndef EW
+#define EW 8
+#endif
+template <int BNR, bool SWIGLU = false>
 struct CfgDgradPair {
   static constexpr int BKS = 128;                    // K (= h) per stage: 8 MMAs per barrier round
   static constexpr int A_ATOM = 64 * BKS * 2;         // [BKS][64] bf16: 64 I columns of W_e, MN-major
@@ -531,10 +534,11 @@ struct CfgDgradPair {
   static constexpr int STAGES = 3;
   static_assert(BKS == 128, "a stage is released in two K halves of one B atom each");
   static constexpr int TMEM_COLS = 2 * BNR;
-  static constexpr int EPI_WARPS = 8;
+  static constexpr int EPI_WARPS = SWIGLU ? EW : 8;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int T_PITCH = 32;  // bf16 per row of a warp's transpose buffer (64 B; 16-byte chunks XOR-swizzled)
-  static constexpr int STAGING_BYTES = EPI_WARPS * 32 * T_PITCH * 2;
+  static constexpr int WARP_BYTES = SWIGLU ? 8 * 32 * 4 : 32 * T_PITCH * 2;
+  static constexpr int STAGING_BYTES = EPI_WARPS * WARP_BYTES;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024;
 };
 
@@ -547,18 +551,19 @@ struct SwigluArgs {
   int N, parts;
 };
 
-// SWIGLU: the epilogue of lrm_ffn_backward.  The product dphi stays in fp32: 8 rows of the warp's 32 columns at a time
-// are read back from its shared memory, so that a lane has 8 columns of a row in order and four lanes the 64 bytes
-// that a row of a, b and dh1 has there.  A chunk's a and b are loaded, through the selection, while the one before it
-// is computed.  dh1 = [dphi b silu'(a) | dphi silu(a)] is rounded once; the sums of dphi silu(a) b over 32 columns
-// go to `partial`.
+// SWIGLU: the epilogue of lrm_ffn_backward, by 16 warps, since what it reads, computes and writes takes a warp longer
+// than the products.  The product dphi stays in fp32: 8 rows of the warp's 32 columns at a time are read back from its
+// shared memory, so that a lane has 8 columns of a row in order and four lanes the 64 bytes that a row of a, b and dh1
+// has there.  A chunk's a and b are loaded, through the selection, while the one before it is computed, and a tile's
+// pair ids while the tile before it is.  dh1 = [dphi b silu'(a) | dphi silu(a)] is rounded once; the sums of
+// dphi silu(a) b over 32 columns go to `partial`.
 template <int BNR, bool SWIGLU>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR, SWIGLU>::THREADS, 1)
     dgrad_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const int32_t* __restrict__ sel_offsets, int E, int h, int I, int max_rows,
                       uint16_t* __restrict__ out, const int32_t* __restrict__ row_map, int out_rows,
                       const __grid_constant__ SwigluArgs sw, unsigned int* status, unsigned long long budget_ns) {
-  using C = CfgDgradPair<BNR>;
+  using C = CfgDgradPair<BNR, SWIGLU>;
   extern __shared__ uint8_t dsmem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~uintptr_t(1023));
 
@@ -788,8 +793,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                             // TMEM lane quarter this warp may access
-    const int c_begin = ((warp - 2) >> 2) * (BNR / 2);  // this warp's half of the tile's rows
-    uint16_t* tbuf = reinterpret_cast<uint16_t*>(smem + C::STAGES * C::STAGE_BYTES) + (warp - 2) * 32 * C::T_PITCH;
+    constexpr int SHARE = BNR / (C::EPI_WARPS / 4);
+    const int c_begin = ((warp - 2) >> 2) * SHARE;  // this warp's share of the tile's rows
+    uint8_t* wbuf = smem + C::STAGES * C::STAGE_BYTES + (warp - 2) * C::WARP_BYTES;
     const uint32_t tempty0 = mapa_shared(&tempty_bar[0], 0);
     uint32_t acc_it = 0;
     if constexpr (SWIGLU) {
@@ -797,84 +803,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
         for (int i = blockIdx.x * 32 * C::EPI_WARPS + tid - 64; i < sw.N; i += gridDim.x * 32 * C::EPI_WARPS)
           sw.dgate[i] = 0.0f;
     }
-    for (int tile = pair; tile < total_tiles; tile += npairs) {
-      int e, nt, mt;
-      decode(tile, e, nt, mt);
-      const int start = s_start[e], len = s_len[e];
-      const int n_cols = tile_rows(len, nt);
-      const int rows_valid = len - nt * BNR;  // rows of this tile inside the segment
-      const uint32_t acc = acc_it & 1u;
-      const uint32_t aph = (acc_it >> 1) & 1u;
-      auto wait_full = [&](uint32_t a, uint32_t parity) {
-        if (!__all_sync(0xffffffffu, wait_bar(&tfull_bar[a], parity))) {
-          if (lane == 0) fail();
-          return false;
-        }
-        tc_fence_after();
-        return true;
+    auto wait_full = [&](uint32_t acc) {
+      if (!__all_sync(0xffffffffu, wait_bar(&tfull_bar[acc], (acc_it >> 1) & 1u))) {
+        if (lane == 0) fail();
+        return false;
+      }
+      tc_fence_after();
+      return true;
+    };
+    auto release = [&](uint32_t acc) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader)
+          mbar_arrive(&tempty_bar[acc]);
+        else
+          mbar_arrive_cluster(tempty0 + acc * 8);
+      }
+      ++acc_it;
+    };
+    // TMEM address of this warp's lanes in an accumulator
+    auto tmem_of = [&](uint32_t acc) { return tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BNR; };
+    if constexpr (SWIGLU) {
+      constexpr int CHUNKS = SHARE / 16;
+      float* fbuf = reinterpret_cast<float*>(wbuf);  // [8 rows][32 columns], 16-byte chunks XOR-swizzled by row
+      const int sub = lane >> 2, quad = lane & 3;    // a step's row of eight, 8 columns of its 32
+      // A tile as this warp sees it: its rows are c_begin .. c_end, row0 the compacted row of the tile's first,
+      // ids[i] the pair of row c_begin + 32 i + lane (-1: none), col0 the warp's first column.
+      struct Tile {
+        int row0, c_end, col0, ids[CHUNKS / 2];
       };
-      if (!SWIGLU && !wait_full(acc, aph)) break;
-      const int col0 = mt * 256 + static_cast<int>(rank) * 128 + q * 32;  // first I column of this warp
-      const int row0 = start + nt * BNR;  // first compacted row of this tile
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BNR;
-      const int c_end = min(n_cols, c_begin + BNR / 2);
-      if constexpr (SWIGLU) {
-        float* fbuf = reinterpret_cast<float*>(tbuf);  // [16 rows][32 columns], 16-byte chunks XOR-swizzled by row
-        const int sub = lane >> 2, quad = lane & 3;    // a step's row of eight, 8 columns of its 32
-        const int fcol = col0 + quad * 8;              // first of this lane's columns
-        uint4 ga[4], gb[4];                            // a and b of rows c + 8 i + sub of a chunk
-        int pid[4];                                    // their pairs, -1: none
-        auto fetch_ids = [&](int c) {
+      auto look = [&](int tile, Tile& t) {
+        t.c_end = c_begin;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = c + 8 * i + sub;
-            pid[i] = r < min(c_end, rows_valid) ? __ldg(row_map + row0 + r) : -1;
-            if (pid[i] >= sw.N || (pid[i] < 0 && r < min(c_end, rows_valid))) {
-              raise_flag(status, LRM_ERR_INDEX);
-              pid[i] = -1;
-            }
-          }
-        };
-        auto fetch = [&]() {
+        for (int i = 0; i < CHUNKS / 2; ++i) t.ids[i] = -1;
+        if (tile >= total_tiles) return;
+        int e, nt, mt;
+        decode(tile, e, nt, mt);
+        const int len = s_len[e];
+        t.row0 = s_start[e] + nt * BNR;
+        t.c_end = min(tile_rows(len, nt), c_begin + SHARE);
+        t.col0 = mt * 256 + static_cast<int>(rank) * 128 + q * 32;
+        const int rows_valid = len - nt * BNR;  // rows of this tile inside the segment
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            ga[i] = gb[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (pid[i] >= 0 && fcol < I) {
-              const uint16_t* arow = sw.ab + static_cast<size_t>(pid[i]) * 2 * I + fcol;
-              ga[i] = ld_stream(reinterpret_cast<const uint4*>(arow));
-              gb[i] = ld_stream(reinterpret_cast<const uint4*>(arow + I));
-            }
+        for (int i = 0; i < CHUNKS / 2; ++i) {
+          const int r = c_begin + 32 * i + lane;
+          t.ids[i] = r < min(t.c_end, rows_valid) ? __ldg(row_map + t.row0 + r) : -1;
+        }
+      };
+      // a and b of rows 8 i + sub of a chunk of 16 rows and their pairs (-1: none): one chunk computed, AHEAD on their
+      // way, the next tile's first ones at a tile's end
+      constexpr int AHEAD = 3;
+      uint4 ga[AHEAD + 1][2], gb[AHEAD + 1][2];
+      int pid[AHEAD + 1][2];
+      auto fetch = [&](const Tile& t, int ci, int buf) {
+        const int col = t.col0 + quad * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          int u = __shfl_sync(0xffffffffu, t.ids[ci / 2], (ci % 2) * 16 + 8 * i + sub);
+          if (u >= sw.N || u < -1) {
+            raise_flag(status, LRM_ERR_INDEX);
+            u = -1;
           }
-        };
-        fetch_ids(c_begin);
-        fetch();
-        if (!wait_full(acc, aph)) break;
-        for (int c = c_begin; c < c_end; c += 32) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(taddr + c, r);  // lane = I column, r[j] = output row c + j
+          pid[buf][i] = u;
+          ga[buf][i] = gb[buf][i] = make_uint4(0u, 0u, 0u, 0u);
+          if (u >= 0 && col < I) {
+            const uint16_t* arow = sw.ab + static_cast<size_t>(u) * 2 * I + col;
+            ga[buf][i] = ld_stream(reinterpret_cast<const uint4*>(arow));
+            gb[buf][i] = ld_stream(reinterpret_cast<const uint4*>(arow + I));
+          }
+        }
+      };
+      Tile t, next;
+      look(pair, t);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) fetch(t, i, i);
+      for (int tile = pair; tile < total_tiles; tile += npairs) {
+        const uint32_t acc = acc_it & 1u;
+        look(tile + npairs, next);  // its ids arrive while this tile is computed
+        if (!wait_full(acc)) break;
+        const int fcol = t.col0 + quad * 8;
+#pragma unroll
+        for (int ci = 0; ci < CHUNKS; ++ci) {
+          const int c = c_begin + 16 * ci;
+          const int buf = ci % (AHEAD + 1);
+          fetch(ci + AHEAD < CHUNKS ? t : next, (ci + AHEAD) % CHUNKS, (ci + AHEAD) % (AHEAD + 1));
+          if (c >= t.c_end) continue;
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(tmem_of(acc) + c, r);  // lane = I column, r[j] = output row c + j
           tmem_ld_wait();
-          uint4 ca[4], cb[4];
-          bool has[4];
+          pin_registers(r);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) ca[i] = ga[i], cb[i] = gb[i], has[i] = pid[i] >= 0;
-          fetch_ids(c + 32);  // past c_end: nothing
-          fetch();
+          for (int i = 0; i < 2; ++i) {
+            __syncwarp();  // the reads of the 8 rows before are done
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i % 2 == 0) {
-              __syncwarp();  // the reads of the 16 rows before are done
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                fbuf[j * 32 + ((((lane >> 2) ^ j) & 7) << 2) + (lane & 3)] = __uint_as_float(r[i * 8 + j]);
-              __syncwarp();
-            }
-            const int frow = (i % 2) * 8 + sub;
+            for (int j = 0; j < 8; ++j)
+              fbuf[j * 32 + ((((lane >> 2) ^ j) & 7) << 2) + (lane & 3)] = __uint_as_float(r[i * 8 + j]);
+            __syncwarp();
             float d[8];
 #pragma unroll
             for (int v = 0; v < 2; ++v)
               *reinterpret_cast<float4*>(d + 4 * v) =
-                  *reinterpret_cast<const float4*>(fbuf + frow * 32 + (((quad * 2 + v) ^ frow) & 7) * 4);
-            const uint32_t aw[4] = {ca[i].x, ca[i].y, ca[i].z, ca[i].w}, bw[4] = {cb[i].x, cb[i].y, cb[i].z, cb[i].w};
+                  *reinterpret_cast<const float4*>(fbuf + sub * 32 + (((quad * 2 + v) ^ sub) & 7) * 4);
+            const uint4 av = ga[buf][i], bv = gb[buf][i];
+            const uint32_t aw[4] = {av.x, av.y, av.z, av.w}, bw[4] = {bv.x, bv.y, bv.z, bv.w};
             uint32_t da[4], db[4];
             float dot = 0.0f;
 #pragma unroll
@@ -890,19 +922,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
             }
             dot += __shfl_xor_sync(0xffffffffu, dot, 1);
             dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-            if (has[i] && fcol < I) {
-              const size_t row = static_cast<size_t>(row0 + c + 8 * i + sub);
+            if (pid[buf][i] >= 0 && fcol < I) {
+              const size_t row = static_cast<size_t>(t.row0 + c + 8 * i + sub);
               uint16_t* orow = sw.dh1 + row * 2 * I + fcol;
               *reinterpret_cast<uint4*>(orow) = make_uint4(da[0], da[1], da[2], da[3]);
               *reinterpret_cast<uint4*>(orow + I) = make_uint4(db[0], db[1], db[2], db[3]);
-              if (sw.partial != nullptr && quad == 0) sw.partial[row * sw.parts + col0 / 32] = dot;
+              if (sw.partial != nullptr && quad == 0) sw.partial[row * sw.parts + t.col0 / 32] = dot;
             }
           }
         }
-      } else {
+        release(acc);
+        t = next;
+      }
+    } else {
+      for (int tile = pair; tile < total_tiles; tile += npairs) {
+        int e, nt, mt;
+        decode(tile, e, nt, mt);
+        const int start = s_start[e], len = s_len[e];
+        const int n_cols = tile_rows(len, nt);
+        const int rows_valid = len - nt * BNR;  // rows of this tile inside the segment
+        const uint32_t acc = acc_it & 1u;
+        if (!wait_full(acc)) break;
+        const int col0 = mt * 256 + static_cast<int>(rank) * 128 + q * 32;  // first I column of this warp
+        const int row0 = start + nt * BNR;  // first compacted row of this tile
+        const int c_end = min(n_cols, c_begin + SHARE);
+        uint16_t* tbuf = reinterpret_cast<uint16_t*>(wbuf);
         for (int c = c_begin; c < c_end; c += 32) {
           uint32_t r[32];
-          tmem_ld_32x32b_x32(taddr + c, r);  // lane = I column, r[j] = output row c + j
+          tmem_ld_32x32b_x32(tmem_of(acc) + c, r);  // lane = I column, r[j] = output row c + j
           tmem_ld_wait();
           __syncwarp();  // the previous chunk's reads of the buffer are done
 #pragma unroll
@@ -933,16 +980,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR>::T
             }
           }
         }
+        release(acc);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (leader)
-          mbar_arrive(&tempty_bar[acc]);
-        else
-          mbar_arrive_cluster(tempty0 + acc * 8);
-      }
-      ++acc_it;
     }
   }
 
@@ -997,7 +1036,7 @@ template <int BNR, bool SWIGLU>
 lrm_status launch_dgrad_pair(lrm_ctx* ctx, const CUtensorMap& a, const CUtensorMap& b, const int32_t* sel_offsets,
                              const lrm_dims& d, int max_rows, uint16_t* out, const int32_t* row_map, int out_rows,
                              const SwigluArgs& sw, cudaStream_t s) {
-  using C = CfgDgradPair<BNR>;
+  using C = CfgDgradPair<BNR, SWIGLU>;
   auto kern = dgrad_pair_kernel<BNR, SWIGLU>;
   static thread_local int configured_device = -1;
   static thread_local int clusters = 0;

@@ -334,6 +334,16 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
+// 32 TMEM lanes x 16 consecutive columns, as above.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 // 16 TMEM lanes x 32 columns as four fragments of 8 columns: thread i gets lane (base + i / 4), columns 2 (i % 4) and
 // the next of fragment n in r[4 n], r[4 n + 1], and the same columns of the lane 8 further in r[4 n + 2], r[4 n + 3].
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
@@ -354,6 +364,12 @@ __device__ __forceinline__ void stmatrix_x4_trans(void* row, const uint32_t (&m)
 }
 
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// After tmem_ld_wait: no arithmetic on the loaded registers moves before it.
+__device__ __forceinline__ void pin_registers(uint32_t (&r)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
 
 // ---- CTA pairs (clusters of 2) ----------------------------------------------
 
