@@ -10,9 +10,9 @@
 //
 // A thread has the same columns in every row it takes part in, so gamma, beta
 // and, in the backward, the sums of the weights' gradients stay in its registers
-// while the row's values stream through: up to 8192 columns 16 a thread (as
-// pairs, for the packed fp32 instructions), with the next row's loads in flight
-// while one is reduced.  Narrow rows share a warp.  Rows that do not start at a
+// while the rows stream through, with the next row's loads in flight while one is
+// reduced.  Narrow rows share a warp.  Arithmetic is on pairs (packed fp32
+// instructions).  Rows that do not start at a
 // 16-byte boundary (a width that is no multiple of the vector, or a tensor that
 // starts between two) are read and written in the aligned vectors that cover
 // them, and a block takes only rows that start at the same place of a vector
@@ -198,12 +198,68 @@ struct Block {
   }
 };
 
+constexpr uint64_t DRAIN_NS = 2000000000ull;
+
+// The rows of a block of more than one warp, copied ahead into shared memory: slot n % depth holds row
+// first + n step, A arrays one after the other, as the aligned vectors that cover the row.
+template <typename T, int A>
+struct Ring {
+  uint8_t* slots;
+  uint64_t* bars;
+  int depth, stride;  // rows; bytes of an array's row
+  const T* src[A];
+  const uint8_t* valid;
+  unsigned int* status;
+  unsigned long long budget_ns;
+
+  __device__ __forceinline__ const uint4* slot(int n, int array) const {
+    return reinterpret_cast<const uint4*>(slots + ((n % depth) * A + array) * stride);
+  }
+  // One thread: copies row `row` into slot n % depth, unless it is padding.  Vectors that reach beyond the tensor are
+  // left to their readers.
+  template <int NV, bool ALIGNED>
+  __device__ __forceinline__ void issue(const Block<T, NV, ALIGNED>& b, int n, long long row, bool wanted) const {
+    uint64_t* bar = bars + n % depth;
+    const long long e0 = row * b.width - b.lead;
+    const int v0 = !ALIGNED && e0 < 0 ? 1 : 0;
+    const int v1 = b.count - (!ALIGNED && e0 + static_cast<long long>(b.count) * b.N > b.rows * b.width ? 1 : 0);
+    const uint32_t bytes = v1 > v0 ? (v1 - v0) * 16 : 0;
+    if (!wanted || bytes == 0) {
+      mbar_arrive(bar);
+      return;
+    }
+    mbar_arrive_expect_tx(bar, A * bytes);
+#pragma unroll
+    for (int a = 0; a < A; ++a)
+      bulk_load(slots + ((n % depth) * A + a) * stride + v0 * 16, src[a] + e0 + v0 * b.N, bytes, bar);
+  }
+  // Row n has arrived.  A wait that runs out is flagged and goes on up to a limit of its own, so that no copy is left
+  // on its way into the memory of a block that is gone.
+  __device__ __forceinline__ void wait(int n) const {
+    if (mbar_wait(bars + n % depth, (n / depth) & 1, budget_ns, nullptr)) return;
+    raise_flag(status, LRM_ERR_TIMEOUT);
+    mbar_wait(bars + n % depth, (n / depth) & 1, DRAIN_NS, nullptr);
+  }
+  template <int NV, bool ALIGNED>
+  __device__ __forceinline__ uint4 read(const Block<T, NV, ALIGNED>& b, int n, int array, long long row, int i) const {
+    if (b.vector(i) >= b.count) return make_uint4(0u, 0u, 0u, 0u);
+    if (!ALIGNED && b.edge(i)) {
+      const long long e0 = row * b.width + b.column(i);
+      if (e0 < 0 || e0 + b.N > b.rows * b.width) return b.load(src[array], row, i);
+    }
+    return slot(n, array)[b.vector(i)];
+  }
+};
+constexpr int MAX_DEPTH = 8;
+
 __device__ __forceinline__ void clear_sums(float* buf, int n) {
   for (int i = threadIdx.x; i < n; i += blockDim.x) buf[i] = 0.0f;
 }
 
-// HOLD (16 columns a thread): gamma and beta in registers, the next row's values loaded ahead; else (wide rows) gamma
-// and beta in shared memory, skewed.
+// HOLD (64 bytes of a row's columns a thread): gamma and beta in registers, the next row's values loaded ahead; else
+// (wider rows than that gives) gamma and beta in shared memory, skewed.  (32768 bf16 rows of 2048 values: 51 us, and 62
+// with 32 bytes a thread, 92 with 16; one warp a row with gamma and beta in shared memory takes 58, rows through a ring
+// of bulk copies 61.)
 template <typename T, int NV, bool HOLD, bool ALIGNED>
 __global__ void __maxnreg__(HOLD ? FWD_REGS<T> : 128)
     layer_norm_kernel(const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta,
@@ -293,18 +349,32 @@ __global__ void __maxnreg__(HOLD ? FWD_REGS<T> : 128)
   }
 }
 
+// How a row's values reach a thread of the backward, which holds 32 bytes of a row's columns: HOLD, loaded a row ahead
+// into registers; RING (fp32, where that takes too many), through shared memory; WIDE, more columns than registers
+// have room for the sums beside gamma, which lies in shared memory then, skewed.
+enum Mode { HELD, RING, WIDE };
+
+struct RingArgs {
+  int depth;
+  unsigned int* status;
+  unsigned long long budget_ns;
+};
+
 // Backward.  Blocks leave their sums of the weights' gradients in partial [blocks, 2, width], which weight_sum_kernel
 // adds in a fixed order; where a block has several rows at a time, they are added through shared memory first.
-// HOLD as above; else gamma lies in shared memory and the second pass over a row reads it again, out of the L2.
-template <typename T, int NV, bool HOLD, bool ALIGNED, bool RES>
-__global__ void __maxnreg__(HOLD ? BWD_REGS<T> : 128)
+// Modes as above; WIDE: gamma lies in shared memory and the second pass over a row reads it again, out of the L2.
+template <typename T, int NV, Mode MODE, bool ALIGNED, bool RES>
+__global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
     layer_norm_bwd_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ gamma,
                           const float* __restrict__ stats, const uint8_t* __restrict__ valid,
                           const T* __restrict__ dres, int rows, int width, int shift, int classes, int lanes,
-                          T* __restrict__ dx, float* __restrict__ partial) {
+                          const RingArgs args, T* __restrict__ dx, float* __restrict__ partial) {
   constexpr int N = Vec<T>::N, P = N / 2;
-  extern __shared__ float s_dyn[];  // several rows at a time: [groups][2][width]; !HOLD: gamma, skewed
+  constexpr bool HOLD = MODE != WIDE;
+  // HELD, several rows at a time: [groups][2][width]; RING: the rows; WIDE: gamma, skewed
+  extern __shared__ __align__(16) float s_dyn[];
   __shared__ __align__(16) float s_buf[2][2][MAX_WARPS];
+  __shared__ __align__(8) uint64_t s_bars[MAX_DEPTH];
   clear_sums(&s_buf[0][0][0], 4 * MAX_WARPS);
   grid_dependency_wait();
   const Block<T, NV, ALIGNED> b(rows, width, shift, classes, lanes);
@@ -329,17 +399,18 @@ __global__ void __maxnreg__(HOLD ? BWD_REGS<T> : 128)
   int slot = 0;
   constexpr int HV = HOLD ? NV : 1;
   const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  uint4 nx[HV], ny[HV], nr[HV];  // HOLD: the next row's
+  uint4 nx[HV], ny[HV], nr[HV];  // HELD: the next row's
   float mean = 0.0f, rstd = 0.0f;
   bool on = false;
+  auto counts = [&](long long r) { return r < rows && (valid == nullptr || valid[r] != 0); };
   auto fetch = [&](long long r) {
-    on = r < rows && (valid == nullptr || valid[r] != 0);
+    on = counts(r);
     mean = rstd = 0.0f;
     if (on) {
       mean = __ldg(stats + r * 2);
       rstd = __ldg(stats + r * 2 + 1);
     }
-    if constexpr (HOLD) {
+    if constexpr (MODE == HELD) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         nx[i] = on ? b.load(x, r, i) : none;
@@ -348,17 +419,40 @@ __global__ void __maxnreg__(HOLD ? BWD_REGS<T> : 128)
       }
     }
   };
+  Ring<T, RES ? 3 : 2> ring{reinterpret_cast<uint8_t*>(s_dyn), s_bars, args.depth, b.count * 16, {x, dy}, valid,
+                            args.status, args.budget_ns};
+  if constexpr (RES) ring.src[2] = dres;
   long long row = b.first();
+  bool ahead = false;  // RING, the first thread: whether the row after those on their way counts
+  if constexpr (MODE == RING) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < args.depth; ++i) mbar_init(s_bars + i, 1);
+      fence_mbar_init();
+      for (int i = 0; i < args.depth; ++i)
+        if (row + i * b.step < rows) ring.issue(b, i, row + i * b.step, counts(row + i * b.step));
+      ahead = counts(row + args.depth * b.step);
+    }
+    __syncthreads();
+  }
   fetch(row);
-  for (long long q = b.first_of_block(); q < rows; q += b.step, row += b.step) {
+  int n = 0;
+  for (long long q = b.first_of_block(); q < rows; q += b.step, row += b.step, ++n) {
     const bool counted = on;
     const F2 minus(-mean, -mean), scale(rstd, rstd);
     uint4 xr[HV], yr[HV], rr[HV];
-    if constexpr (HOLD) {
+    if constexpr (MODE == RING) {
+      ring.wait(n);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        xr[i] = counted ? ring.read(b, n, 0, row, i) : none;
+        yr[i] = counted ? ring.read(b, n, 1, row, i) : none;
+        rr[i] = RES && counted ? ring.read(b, n, RES ? 2 : 0, row, i) : none;
+      }
+    } else if constexpr (HOLD) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) xr[i] = nx[i], yr[i] = ny[i], rr[i] = RES ? nr[i] : none;
-      fetch(row + b.step);
     }
+    if constexpr (HOLD) fetch(row + b.step);
     // xhat and dy of vector i, twice out of the same 16 bytes: fp32 copies would take twice the registers in bf16
     auto values = [&](int i, F2 (&vx)[P], F2 (&vy)[P]) {
       const int k = HOLD ? i : 0;
@@ -388,6 +482,12 @@ __global__ void __maxnreg__(HOLD ? BWD_REGS<T> : 128)
     }
     float s[2] = {s0.get().x + s0.get().y, s1.get().x + s1.get().y};
     row_sum(s, lanes, s_buf, slot);
+    if constexpr (MODE == RING) {  // all threads have read the row: its slot takes the next one
+      if (threadIdx.x == 0 && row + args.depth * b.step < rows) {
+        ring.issue(b, n + args.depth, row + args.depth * b.step, ahead);
+        ahead = counts(row + (args.depth + 1) * b.step);
+      }
+    }
     if constexpr (HOLD && sizeof(T) == 2) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {  // unpacked anew below
@@ -489,17 +589,17 @@ int shift_of(const void* p) {
 
 // How a call cuts its work; the same for the backward's launch and its workspace's size.
 struct Plan {
-  int lanes, nv, threads, classes, blocks;
+  int lanes, nv, threads, classes, blocks, per_sm;
 };
 
-template <typename T, int COLS>
-Plan plan(int sm_count, int rows, int width, bool al, int resident) {
+// `most`: vectors a thread at most, `resident`: threads an SM has room for
+template <typename T>
+Plan plan(int sm_count, int rows, int width, bool al, int most, int resident) {
   Plan p;
-  constexpr int HELD = COLS / Vec<T>::N;  // vectors of a thread that holds its columns' weights
   const int nvec = row_vectors<T>(width, al);
   p.lanes = 1;
-  while (p.lanes < 32 && p.lanes * HELD < nvec) p.lanes *= 2;
-  while (p.lanes >= 32 && p.lanes < 32 * MAX_WARPS && p.lanes * HELD < nvec) p.lanes += 32;
+  while (p.lanes < 32 && p.lanes * most < nvec) p.lanes *= 2;
+  while (p.lanes >= 32 && p.lanes < 32 * MAX_WARPS && p.lanes * most < nvec) p.lanes += 32;
   p.nv = ceil_div(nvec, p.lanes);
   p.threads = p.lanes > 32 ? p.lanes : 128;
   p.classes = 1;
@@ -509,31 +609,40 @@ Plan plan(int sm_count, int rows, int width, bool al, int resident) {
   }
   const int groups = p.threads / p.lanes;
   const int per_class = ceil_div(ceil_div(rows, p.classes), groups);
-  int per_sm = resident / p.threads;
-  if (per_sm < 1) per_sm = 1;
-  int most = sm_count * per_sm / p.classes;
-  if (most < 1) most = 1;
-  p.blocks = p.classes * (per_class < most ? (per_class > 0 ? per_class : 1) : most);
+  p.per_sm = resident / p.threads;
+  if (p.per_sm < 1) p.per_sm = 1;
+  int blocks = sm_count * p.per_sm / p.classes;
+  if (blocks < 1) blocks = 1;
+  p.blocks = p.classes * (per_class < blocks ? (per_class > 0 ? per_class : 1) : blocks);
   return p;
 }
 template <typename T>
 Plan bwd_plan(int sm_count, int rows, int width, bool al) {
-  return plan<T, BWD_COLS<T>>(sm_count, rows, width, al, threads_per_sm(BWD_REGS<T>));
+  return plan<T>(sm_count, rows, width, al, BWD_COLS<T> / Vec<T>::N, threads_per_sm(BWD_REGS<T>));
 }
 
-// Calls go(vectors a thread, whether it holds its columns' weights): up to 5 vectors in bf16 and 9 in fp32 at the largest
-// width, one more than it fills where rows are cut.
-template <typename T, int COLS, typename Go>
-lrm_status with_vectors(int nv, Go go) {
-  constexpr int HELD = COLS / Vec<T>::N;
-  if (nv <= HELD) return go(std::integral_constant<int, HELD>(), std::true_type());
-  if constexpr (HELD < 2)
-    if (nv <= 2) return go(std::integral_constant<int, 2>(), std::false_type());
-  if constexpr (HELD < 3)
-    if (nv <= 3) return go(std::integral_constant<int, 3>(), std::false_type());
+// Rows of a ring: as many as the blocks of an SM have room for beside one another.
+int ring_depth(const Plan& p, int arrays, int width, int type_size) {
+  const int row = arrays * (width * type_size + 32);  // with the vectors it shares
+  const int depth = 200 * 1024 / p.per_sm / row;
+  return depth < 2 ? 2 : depth > MAX_DEPTH ? MAX_DEPTH : depth;
+}
+
+// Calls go(vectors a thread, mode): WIDE up to 5 vectors in bf16 and 9 in fp32 at the largest width, one more than it
+// fills where rows are cut.
+template <typename T, typename Go>
+lrm_status with_vectors(const Plan& p, Go go) {
+  constexpr int HOLDS = BWD_COLS<T> / Vec<T>::N;
+  using Wide = std::integral_constant<Mode, WIDE>;
+  if (p.nv <= HOLDS) {
+    if constexpr (sizeof(T) == 4)
+      if (p.lanes > 32) return go(std::integral_constant<int, HOLDS>(), std::integral_constant<Mode, RING>());
+    return go(std::integral_constant<int, HOLDS>(), std::integral_constant<Mode, HELD>());
+  }
+  if (p.nv <= 3) return go(std::integral_constant<int, 3>(), Wide());
   if constexpr (Vec<T>::N == 4)
-    if (nv > 5) return go(std::integral_constant<int, 9>(), std::false_type());
-  return go(std::integral_constant<int, 5>(), std::false_type());
+    if (p.nv > 5) return go(std::integral_constant<int, 9>(), Wide());
+  return go(std::integral_constant<int, 5>(), Wide());
 }
 
 template <typename Kern>
@@ -546,15 +655,21 @@ lrm_status allow_smem(Kern kern, size_t smem) {
 template <typename T, bool ALIGNED>
 lrm_status forward(lrm_ctx* ctx, const void* x, const float* gamma, const float* beta, const uint8_t* valid, int rows,
                    int width, float eps, void* y, float* stats, cudaStream_t s) {
-  const Plan p = plan<T, FWD_COLS<T>>(ctx->sm_count, rows, width, ALIGNED, threads_per_sm(FWD_REGS<T>));
-  return with_vectors<T, FWD_COLS<T>>(p.nv, [&](auto n, auto hold) {
+  constexpr int HOLDS = FWD_COLS<T> / Vec<T>::N;
+  const Plan p = plan<T>(ctx->sm_count, rows, width, ALIGNED, HOLDS, threads_per_sm(FWD_REGS<T>));
+  auto go = [&](auto n, auto hold) {
     auto kern = layer_norm_kernel<T, decltype(n)::value, decltype(hold)::value, ALIGNED>;
     const size_t smem = decltype(hold)::value ? 0 : 2 * (width + width / Vec<T>::N + 1) * sizeof(float);
     const lrm_status st = allow_smem(kern, smem);
     if (st != LRM_OK) return st;
     return launch_dependent(kern, p.blocks, p.threads, smem, 0, s, static_cast<const T*>(x), gamma, beta, valid, rows,
                             width, shift_of<T>(x), p.classes, eps, p.lanes, static_cast<T*>(y), stats);
-  });
+  };
+  if (p.nv <= HOLDS) return go(std::integral_constant<int, HOLDS>(), std::true_type());
+  // fp32 above 8192 columns, bf16 where the widest rows are cut
+  if constexpr (Vec<T>::N == 4)
+    if (p.nv > 5) return go(std::integral_constant<int, 9>(), std::false_type());
+  return go(std::integral_constant<int, 5>(), std::false_type());
 }
 
 template <typename T, bool ALIGNED, bool RES>
@@ -563,16 +678,20 @@ lrm_status backward(lrm_ctx* ctx, const void* x, const void* dy, const float* ga
                     float* dbeta, float* partial, cudaStream_t s) {
   const Plan p = bwd_plan<T>(ctx->sm_count, rows, width, ALIGNED);
   const int groups = p.threads / p.lanes;
-  const lrm_status st = with_vectors<T, BWD_COLS<T>>(p.nv, [&](auto n, auto hold) {
-    auto kern = layer_norm_bwd_kernel<T, decltype(n)::value, decltype(hold)::value, ALIGNED, RES>;
-    const size_t smem = groups > 1                ? static_cast<size_t>(groups) * 2 * width * sizeof(float)
-                        : decltype(hold)::value ? 0
-                                                  : (width + width / Vec<T>::N + 1) * sizeof(float);
+  const lrm_status st = with_vectors<T>(p, [&](auto n, auto mode) {
+    constexpr Mode MODE = decltype(mode)::value;
+    auto kern = layer_norm_bwd_kernel<T, decltype(n)::value, MODE, ALIGNED, RES>;
+    constexpr int ARRAYS = RES ? 3 : 2;
+    const RingArgs ring{ring_depth(p, ARRAYS, width, sizeof(T)), ctx->d_status, ctx->wait_budget_ns};
+    const size_t smem = MODE == WIDE   ? (width + width / Vec<T>::N + 1) * sizeof(float)
+                        : MODE == RING ? static_cast<size_t>(ring.depth) * ARRAYS * row_vectors<T>(width, ALIGNED) * 16
+                        : groups > 1   ? static_cast<size_t>(groups) * 2 * width * sizeof(float)
+                                       : 0;
     const lrm_status a = allow_smem(kern, smem);
     if (a != LRM_OK) return a;
     return launch_dependent(kern, p.blocks, p.threads, smem, 0, s, static_cast<const T*>(x),
                             static_cast<const T*>(dy), gamma, stats, valid, static_cast<const T*>(dres), rows, width,
-                            shift_of<T>(x), p.classes, p.lanes, static_cast<T*>(dx), partial);
+                            shift_of<T>(x), p.classes, p.lanes, ring, static_cast<T*>(dx), partial);
   });
   if (st != LRM_OK) return st;
   return launch_dependent(weight_sum_kernel, ceil_div(2ll * width, 32), 32 * WS_ROWS, 0, 0, s, partial, p.blocks,
