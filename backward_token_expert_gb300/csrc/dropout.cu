@@ -5,10 +5,12 @@
 // draws the same mask again: it is the same call on the gradient.
 //
 // One read of x and residual, one write: memory bounds it as long as the ten
-// rounds (two 32 x 32 -> 64 bit products and four exclusive ors for four
-// elements each) hide behind it.  A thread has 16 bytes of each operand, two
-// Philox blocks in bf16 and one in fp32; the ten round keys are the same for
-// all threads and are computed once.
+// rounds (two 32 x 32 -> 64 bit products and two three-way exclusive ors for four
+// elements each) hide behind it, which takes all the threads an SM can have (32
+// registers).  The round keys come with the launch; what the block's counters have
+// in common in rounds 1 and 2 is computed once.  67108864 elements: fp32 82 us
+// (0.96 of the HBM's rate), bf16 with a residual 64 us (0.93), bf16 alone, where
+// eight elements move only 32 bytes, 56 us (0.70): the integer pipe bounds that.
 #include "lrm_internal.cuh"
 #include "vec.cuh"
 
@@ -16,6 +18,8 @@ namespace lrm {
 namespace {
 
 constexpr int DR_THREADS = 256;
+template <typename T>
+constexpr int VECTORS = sizeof(T) == 2 ? 2 : 1;  // a thread has in flight
 
 struct RoundKeys {
   uint32_t a[10], b[10];
@@ -86,13 +90,13 @@ __device__ __forceinline__ uint16_t from_float<uint16_t>(float v) {
 
 // DROP = false: p = 0, nothing is drawn.  VECTOR: 16-byte accesses.
 template <typename T, bool DROP, bool VECTOR, bool RES>
-__global__ void __launch_bounds__(DR_THREADS)
+__global__ void __launch_bounds__(DR_THREADS, 8)
     dropout_kernel(const T* x, const T* residual, long long n, const __grid_constant__ DropoutArgs a, T* out) {
   constexpr int N = 16 / sizeof(T);
   grid_dependency_wait();
   const uint64_t offset = a.offset + (a.step != nullptr ? __ldg(a.step) : 0);
   const long long items = (n + N - 1) / N;
-  constexpr int U = 2;  // vectors a thread has in flight
+  constexpr int U = VECTORS<T>;
   for (long long i0 = static_cast<long long>(blockIdx.x) * (U * DR_THREADS); i0 < items;
        i0 += static_cast<long long>(gridDim.x) * (U * DR_THREADS)) {
     T xv[U][N], rv[U][N];
@@ -151,7 +155,7 @@ lrm_status launch(lrm_ctx* ctx, const void* x, const void* residual, long long n
     cap = resident_grid(ctx, kern, DR_THREADS, 0);
     dev = ctx->device;
   }
-  constexpr long long per = static_cast<long long>(2 * DR_THREADS) * (16 / sizeof(T));
+  constexpr long long per = static_cast<long long>(VECTORS<T> * DR_THREADS) * (16 / sizeof(T));
   const long long need = (n + per - 1) / per;
   return launch_dependent(kern, static_cast<int>(need < cap ? need : cap), DR_THREADS, 0, 0, s,
                           static_cast<const T*>(x), static_cast<const T*>(residual), n, a, static_cast<T*>(out));

@@ -4,28 +4,38 @@
 //   y_t = sum over the k pairs u of t of alpha_u row_u (lrm_ffn_combine)
 // for the pairs u = t k + j of every expert's segment of `ids`.
 //
-// Both products are one kernel template: persistent clusters of two CTAs whose
-// even CTA issues tcgen05.mma.cta_group::2 with M = 256 rows of the weight and
-// N = up to 256 pairs (fp32 accumulators in TMEM, double-buffered), K blocks of
-// 64.  The pairs are the N dimension because N is cut to multiples of 32 at a
-// segment's end, where M would be rounded up to 256: a single token costs the
-// weights it has to read and little else.  Both operands are K-major:
+// Both products are one kernel template: persistent clusters of four CTAs, two
+// pairs.  A pair's even CTA issues tcgen05.mma.cta_group::2 with M = 256 rows of
+// the weight and N = up to 256 pairs of the routing (fp32 accumulators in TMEM,
+// double-buffered), K blocks of 64; the two CTA pairs of a cluster take
+// neighbouring feature tiles of the same 256 routed pairs.  The routed pairs are
+// the N dimension because N is cut to multiples of 64 at a segment's end, where M
+// would be rounded up to 256.  Both operands are K-major:
 //   A  weight rows, one TMA box a CTA and stage.  Up interleaves eight gate rows
 //      with the eight up rows of the same features (a 5-D view of W1 does that in
 //      the box), so that a thread of the epilogue that reads TMEM in 16-lane
 //      fragments gets a and b of its features.
-//   B  the pairs' rows, gathered by their ids with gather4 TMA loads into the
-//      swizzled tile: x and phi are never copied into expert order.
-//   warp 0       TMA producer of the weights
-//   warp 1       MMA issuer (even CTA)
-//   warps 2-9    epilogue, two a TMEM lane quarter, half of the tile's pairs
-//                each: fragments of 8 features x 8 pairs are transposed by
-//                stmatrix into shared memory, from where a pair's features are
-//                stored 16 bytes a lane, 32 or 64 contiguous bytes a row.  (Shared
-//                memory's bandwidth is what the operands of the products need:
-//                32 KB written and 32 KB read a stage of 512 cycles, so the less
-//                the epilogue takes of it, the better.)
-//   warps 10-..  TMA producers of the pairs' rows, a share of each stage's each
+//   B  the routed pairs' rows, gathered by their ids with gather4 TMA loads into
+//      the swizzled tile: x and phi are never copied into expert order.  A gather
+//      of four rows takes the TMA unit some 23 cycles, so that the 32 of a stage
+//      would take longer than its products (512 cycles): each CTA pair gathers
+//      half of them and multicasts it to both.
+//   warp 0        TMA producer of the weights
+//   warp 1        MMA issuer (even CTAs)
+//   warps 2-9     epilogue, two a TMEM lane quarter, half of the tile's pairs
+//                 each: fragments of 8 features x 8 pairs are transposed by
+//                 stmatrix into shared memory, from where a pair's features are
+//                 stored 16 bytes a lane, 32 or 64 contiguous bytes a row.  (The
+//                 operands take nearly all of the shared memory's bandwidth, 32
+//                 KB written and 32 KB read a stage, so the epilogue's share
+//                 costs products' time.)
+//   warps 10-13   TMA producers of the pairs' rows, a quarter of a CTA's each
+// Layer of 32768 x 8 pairs, h = 2048, I = 768: up 1.19 ms (1.39 PFLOP/s), down
+// 0.68 ms (1.22).  Clusters of one CTA pair: 1.25 and 0.70 ms; rows copied by
+// cp.async and handed over with a proxy fence: 2.4 and 1.7 ms; two blocks of M =
+// 256 over 128 pairs (half the gathers, but operands of N = 128 products need more
+// of the shared memory than it gives): 1.56 and 0.85 ms.  Without the epilogue the
+// two take 1.07 and 0.60 ms, without the gathers, too, 1.00 and 0.55.
 // Every wait is bounded as in the other grouped products (grouped_gemm.cu).
 #include <cuda_bf16.h>
 
@@ -47,8 +57,8 @@ struct CfgFfn {
   static constexpr int STAGES = 6;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int EPI_WARPS = 8;
-  static constexpr int GATHER_WARPS = 8;
-  static constexpr int ROUND = 8 * GATHER_WARPS;  // a tile's pairs are a multiple: each gather warp has its share of four rows
+  static constexpr int GATHER_WARPS = 4;
+  static constexpr int ROUND = 16 * GATHER_WARPS;  // a tile's pairs are a multiple: each gather warp has its share of four rows
   static constexpr int THREADS = 64 + 32 * EPI_WARPS + 32 * GATHER_WARPS;
   static constexpr int BUF_BYTES = 32 * 64;  // a warp's: 32 pairs, 32 bf16 values each
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * BUF_BYTES + 1024;
@@ -56,7 +66,7 @@ struct CfgFfn {
 };
 
 template <bool UP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     ffn_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const int32_t* __restrict__ offsets, const int32_t* __restrict__ ids, int E, int K, int M, int N,
                int div, int max_rows, uint16_t* __restrict__ out, uint16_t* __restrict__ ab, unsigned int* status,
@@ -77,11 +87,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
   __shared__ int s_prefix[MAX_E + 1];  // first pair tile of each expert
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t crank = cluster_ctarank();
+  const uint32_t rank = crank & 1, which = crank >> 1;  // in the CTA pair, the pair in its cluster
+  const uint32_t leader_rank = crank & ~1u;
   const bool leader = rank == 0;
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int pair = blockIdx.x >> 2, npairs = gridDim.x >> 2;  // clusters
   constexpr int TILE_M = UP ? 128 : 256;  // features of a tile: up has a gate and an up row for each
-  const int tiles_m = (M + TILE_M - 1) / TILE_M;
+  const int tiles_m = (M + 2 * TILE_M - 1) / (2 * TILE_M);  // of both pairs
 
   if (tid == 0) {
     tma_prefetch_desc(&tmA);
@@ -89,7 +101,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     s_abort = 0;
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&full_bar[i], 2);  // both arrivals come from the even CTA's weight producer
-      mbar_init(&empty_bar[i], 1);
+      mbar_init(&empty_bar[i], 2);  // both pairs' MMAs have read the stage
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull_bar[i], 1);
@@ -158,6 +170,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     const int n_nt = (s_len[e] + C::BN - 1) / C::BN;
     mt = rem / n_nt;
     nt = rem - mt * n_nt;
+    mt = 2 * mt + static_cast<int>(which);
   };
   // pairs of a row tile that the MMA computes: the remainder rounded up
   auto tile_rows = [&](int len, int nt) {
@@ -168,7 +181,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ weights
     if (lane == 0) {
-      const uint32_t full0 = mapa_shared(&full_bar[0], 0);  // the even CTA's full barriers
+      const uint32_t full0 = mapa_shared(&full_bar[0], leader_rank);  // the even CTA's full barriers
       uint32_t it = 0;
       bool ok = true;
       for (int tile = pair; tile < total_tiles && ok; tile += npairs) {
@@ -201,11 +214,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
   } else if (warp >= 2 + C::EPI_WARPS) {
     // ------------------------------------------------------------ gather
     // A gather takes its operands from uniform registers, so a warp's are issued one after the other, some 75 cycles
-    // each by as many lanes (150 by one lane with all the rows): eight warps share a stage's 32.  Every warp has as
+    // each by as many lanes (150 by one lane with all the rows): four warps share a stage's 16.  Every warp has as
     // many, at least one: a warp without a copy in a stage could fall behind the ring by a phase, whose parity it
     // would take for another's.
     const int g = warp - 2 - C::EPI_WARPS;
-    const uint32_t full0 = mapa_shared(&full_bar[0], 0);
+    const uint32_t full0 = mapa_shared(&full_bar[0], leader_rank);
+    const uint16_t both = static_cast<uint16_t>(5u << rank);  // this CTA and its like in the other pair
     uint32_t it = 0;
     bool ok = true;
     for (int tile = pair; tile < total_tiles && ok; tile += npairs) {
@@ -213,13 +227,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
       decode(tile, e, nt, mt);
       const int start = s_start[e], len = s_len[e];
       const int half = tile_rows(len, nt) / 2;
-      const int n = half / 4 / C::GATHER_WARPS;  // this warp's gathers: one for each of its first n lanes
+      // this warp's gathers, one for each of its first n lanes, of the half that this pair gathers for both
+      const int n = half / 8 / C::GATHER_WARPS;
+      const int mine = (static_cast<int>(which) * C::GATHER_WARPS + g) * n + lane;  // of the CTA's half, in fours
       int row[4] = {0, 0, 0, 0};
       if (lane < n) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // rows past the segment repeat its last one: computed for nothing, never stored
-          const int r = min(nt * C::BN + static_cast<int>(rank) * half + 4 * (g * n + lane) + i, len - 1);
+          const int r = min(nt * C::BN + static_cast<int>(rank) * half + 4 * mine + i, len - 1);
           const int u = __ldg(ids + start + r);
           row[i] = u >= 0 && u < N ? u / div : 0;  // the epilogue flags a bad id and stores nothing for it
         }
@@ -233,8 +249,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
           break;
         }
         if (lane < n)
-          tma_gather4_pair(smem + s * C::STAGE_BYTES + C::A_BYTES + (g * n + lane) * 512, &tmB, full0 + s * 8,
-                           kb * C::BKS, row);
+          tma_gather4_pair_multicast(smem + s * C::STAGE_BYTES + C::A_BYTES + mine * 512, &tmB, full0 + s * 8,
+                                     kb * C::BKS, row, both);
         __syncwarp();
       }
     }
@@ -277,12 +293,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
 #pragma unroll
           for (int kk = 0; kk < C::BKS / 16; ++kk)
             mma_bf16_ss_pair(d_tmem, adesc + kk * 2, bdesc + kk * 2, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_pair_multicast(&empty_bar[s]);
+          mma_commit_pair_multicast(&empty_bar[s], 0xF);
         }
         __syncwarp();
       }
       if (!ok) break;
-      if (lane == 0) mma_commit_pair_multicast(&tfull_bar[acc]);
+      if (lane == 0) mma_commit_pair_multicast(&tfull_bar[acc], static_cast<uint16_t>(3u << leader_rank));
       __syncwarp();
       ++acc_it;
     }
@@ -304,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     // contiguous reads share banks
     auto at4 = [&](int row, int chunk) { return buf + row * 64 + ((chunk ^ (row >> 1)) & 3) * 16; };
     auto at2 = [&](int row, int chunk) { return buf + row * 32 + ((chunk ^ (row >> 2)) & 1) * 16; };
-    const uint32_t tempty0 = mapa_shared(&tempty_bar[0], 0);
+    const uint32_t tempty0 = mapa_shared(&tempty_bar[0], leader_rank);
     uint32_t acc_it = 0;
     for (int tile = pair; tile < total_tiles; tile += npairs) {
       int e, nt, mt;
@@ -599,7 +615,7 @@ lrm_status launch_ffn(lrm_ctx* ctx, const uint16_t* in, uint64_t in_rows, const 
     if (ctx->smem_optin < C::SMEM_BYTES + 14 * 1024) return LRM_ERR_ARCH;
     LRM_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctx->sm_count & ~1, 1, 1);
+    cfg.gridDim = dim3(ctx->sm_count & ~3, 1, 1);
     cfg.blockDim = dim3(C::THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     int n = 0;
@@ -612,7 +628,7 @@ lrm_status launch_ffn(lrm_ctx* ctx, const uint16_t* in, uint64_t in_rows, const 
   lrm_status st = encode_weight(ctx, &ma, weight, K, M, UP ? 2 : 1, d.E);
   if (st != LRM_OK) return st;
   if ((st = encode_2d(ctx, &mb, in, K, in_rows, 1)) != LRM_OK) return st;
-  return launch_dependent(kern, 2 * clusters, C::THREADS, C::SMEM_BYTES, 0, s, ma, mb, offsets, ids, d.E, K, M, N,
+  return launch_dependent(kern, 4 * clusters, C::THREADS, C::SMEM_BYTES, 0, s, ma, mb, offsets, ids, d.E, K, M, N,
                           UP ? d.k : 1, max_rows, out, ab, ctx->d_status, ctx->wait_budget_ns);
 }
 

@@ -304,6 +304,18 @@ __device__ __forceinline__ void tma_gather4_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// The same, written at the same offset of every CTA in `mask` and counted on the barrier of the even CTA of each one's
+// pair (bar_cluster: that of this CTA's own pair).
+__device__ __forceinline__ void tma_gather4_pair_multicast(void* dst, const CUtensorMap* map, uint32_t bar_cluster,
+                                                           int32_t x, const int32_t (&y)[4], uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster"
+      ".cta_group::2 [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+      "h"(mask)
+      : "memory");
+}
+
 // Makes this thread's generic-proxy shared-memory writes visible to later
 // async-proxy readers (tensor-core operand reads).
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -459,10 +471,9 @@ __device__ __forceinline__ void mma_commit_pair_local(uint64_t* bar) {
                : "memory");
 }
 
-// Arrive once on `bar` (same offset) in both CTAs of the pair when the pair
-// MMAs issued so far complete.
-__device__ __forceinline__ void mma_commit_pair_multicast(uint64_t* bar) {
-  const uint16_t mask = 0x3;
+// Arrive once on `bar` (same offset) in the CTAs of `mask`, both of a cluster of
+// one pair, when the pair MMAs issued so far complete.
+__device__ __forceinline__ void mma_commit_pair_multicast(uint64_t* bar, uint16_t mask = 0x3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
