@@ -424,7 +424,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // no CTA leaves while its partner may still read its shared memory or TMEM
+  if (*abort_flag) let_copies_land();
+  cluster_sync_all();  // no CTA leaves while another may still read or write its shared memory or TMEM
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
 }

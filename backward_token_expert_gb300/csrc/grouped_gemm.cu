@@ -987,6 +987,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR, SW
 
   tc_fence_before();
   __syncthreads();
+  if (SWIGLU && *abort_flag) let_copies_land();
   cluster_sync_all();  // no CTA leaves while its partner may still read its shared memory or TMEM
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);

@@ -769,7 +769,7 @@ extern "C" lrm_status lrm_layer_norm_backward(lrm_ctx* ctx, const void* x, int32
       return LRM_ERR_INVALID_ARG;
     if (ws == nullptr || ws_bytes < bwd_bytes(ctx->sm_count, rows, width)) return LRM_ERR_WORKSPACE;
     const size_t es = dtype == LRM_F32 ? 4 : 2;
-    if (!aligned(x, es) || !aligned(gamma, 4) || !aligned(stats, 4) || !aligned(ws, 4)) return LRM_ERR_ALIGN;
+    if (!aligned(x, es) || !aligned(gamma, 4) || !aligned(stats, 8) || !aligned(ws, 4)) return LRM_ERR_ALIGN;
     const uintptr_t at = reinterpret_cast<uintptr_t>(x) % 16;
     if (reinterpret_cast<uintptr_t>(dy) % 16 != at || reinterpret_cast<uintptr_t>(dx) % 16 != at ||
         (dres != nullptr && reinterpret_cast<uintptr_t>(dres) % 16 != at))

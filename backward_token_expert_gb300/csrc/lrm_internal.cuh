@@ -223,6 +223,13 @@ __device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t pari
   }
 }
 
+// After a wait of a block ran out: time for the copies and products that its threads have issued to end, a thousand
+// times what they take, before its shared memory and TMEM go to another block.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 2000000) __nanosleep(1000);
+}
+
 // ---- TMA -------------------------------------------------------------------
 
 // Untiled bulk copies (cp.async.bulk): both addresses 16-byte aligned, the

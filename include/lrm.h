@@ -617,7 +617,7 @@ LRM_API lrm_status lrm_ffn_backward(lrm_ctx* ctx, const uint16_t* delta_c, const
  *   valid              [rows] uint8 or NULL: a row whose entry is 0 gets y = 0, stats = 0
  *                      and dx = 0 and takes no part in dgamma and dbeta, whatever it and
  *                      its gradients hold
- *   stats              [rows, 2] fp32
+ *   stats              [rows, 2] fp32, 8-byte aligned
  *   ws                 lrm_layer_norm_workspace bytes
  * x, y, dy, dx and dres are aligned to their type and lie at one distance from a
  * 16-byte boundary (else LRM_ERR_ALIGN).  No output may overlap an input.
@@ -654,7 +654,7 @@ LRM_API lrm_status lrm_dropout_add(lrm_ctx* ctx, const void* x, const void* resi
 LRM_API lrm_status lrm_get_device_status(lrm_ctx* ctx, void* stream, uint32_t* flags);
 
 /* Time limit, in nanoseconds, of every device-side wait of the grouped GEMM,
- * feed-forward and clipping kernels (default 2e9).  A wait that runs out sets LRM_ERR_TIMEOUT and the
+ * feed-forward, layer norm and clipping kernels (default 2e9).  A wait that runs out sets LRM_ERR_TIMEOUT and the
  * kernel winds down and returns. */
 LRM_API lrm_status lrm_set_wait_budget(lrm_ctx* ctx, uint64_t ns);
 

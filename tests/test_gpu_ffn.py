@@ -317,6 +317,101 @@ def test_same_bits_in_a_graph_and_on_another_stream(ctx):
         assert torch.equal(a[name], b[name]) and torch.equal(a[name], c[name]), name
 
 
+def test_short_wait_budgets_leave_the_context_usable():
+    """Waits that may run out at once: a call either gives its result or is flagged, and the next one is whole."""
+    from backward_token_expert_gb300 import lrm as L
+
+    own = L.lrm_create(0)
+    try:
+        rng = np.random.default_rng(17)
+        T, E, k, h, I = 700, 5, 2, 520, 264
+        N = T * k
+        ids, offsets = _routing(rng, T, E, k, 0.5, False)
+        dids, doff = _dev(ids, offsets, 0)
+        x, W1, W = _bf(rng, T, h).cuda(), _bf(rng, E, 2 * I, h).cuda(), _bf(rng, E, h, I).cuda()
+        delta, dims = _bf(rng, N, h).cuda(), L.dims_of(T, E, k, h, I)
+        bf = dict(dtype=torch.bfloat16, device="cuda")
+        need = L.lrm_ffn_backward_workspace(own, dims, N)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        gamma = torch.ones(h, device="cuda")
+        nws = torch.empty(L.lrm_layer_norm_workspace(own, T, h), dtype=torch.uint8, device="cuda")
+
+        def run():
+            o = dict(ab=torch.zeros(N, 2 * I, **bf), phi=torch.zeros(N, I, **bf), rows=torch.zeros(N, h, **bf),
+                     dh1=torch.zeros(N, 2 * I, **bf), dgate=torch.zeros(N, device="cuda"),
+                     dx=torch.zeros(T, h, device="cuda"), dg=torch.zeros(h, device="cuda"),
+                     db=torch.zeros(h, device="cuda"))
+            L.lrm_ffn_up(own, x, W1, doff, dids, dims, N, o["ab"], o["phi"])
+            L.lrm_ffn_down(own, o["phi"], W, doff, dids, dims, N, o["rows"])
+            L.lrm_ffn_backward(own, delta, W, o["ab"], doff, dids, dims, N, o["dh1"], o["dgate"], ws, need)
+            xf, stats = x.float(), torch.ones(T, 2, device="cuda")
+            L.lrm_layer_norm_backward(own, xf, L.DTYPE_F32, xf, gamma, stats, None, None, T, h, o["dx"], o["dg"],
+                                      o["db"], nws, nws.numel())
+            torch.cuda.synchronize()
+            return o, L.lrm_get_device_status(own)
+
+        want, flags = run()
+        assert flags == 0
+        for budget in (0, 1000, 100000):
+            L.lrm_set_wait_budget(own, budget)
+            got, flags = run()
+            assert flags in (0, 1 << L.LRM_ERR_TIMEOUT)
+            assert flags or all(torch.equal(a, b) for a, b in zip(want.values(), got.values()))
+        L.lrm_set_wait_budget(own, 2000000000)
+        got, flags = run()
+        assert flags == 0 and all(torch.equal(a, b) for a, b in zip(want.values(), got.values()))
+    finally:
+        L.lrm_destroy(own)
+
+
+def test_two_streams_and_offsets_beyond_32_bits(ctx):
+    """Two calls at once on two streams, and rows of ab past 2^31 elements."""
+    from backward_token_expert_gb300 import lrm as L
+
+    rng = np.random.default_rng(23)
+    I, h, E, k = 4096, 64, 2, 1
+    T = (1 << 31) // (2 * I) + 300
+    x, W1 = torch.zeros(T, h, dtype=torch.bfloat16, device="cuda"), _bf(rng, E, 2 * I, h, scale=h ** -0.5).cuda()
+    x[-200:] = _bf(rng, 200, h).cuda()
+    ids = torch.arange(T, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, T - 100, T], dtype=torch.int32, device="cuda")
+    dims = L.dims_of(T, E, k, h, I)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    outs = []
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            ab, phi = torch.full((T, 2 * I), 7.0, **bf), torch.full((T, I), 7.0, **bf)
+            L.lrm_ffn_up(ctx, x, W1, off, ids, dims, T, ab, phi, s)
+            outs.append((ab, phi))
+    torch.cuda.synchronize()
+    assert L.lrm_get_device_status(ctx) == 0
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    ab, phi = outs[0]
+    assert (ab[:-200] == 0).all() and (phi[:-200] == 0).all()
+    got, W1n, xn = _np(ab[-200:]), _np(W1), _np(x[-200:])
+    for e, rows in ((0, slice(0, 100)), (1, slice(100, 200))):
+        ref, S = xn[rows] @ W1n[e].T, np.abs(xn[rows]) @ np.abs(W1n[e]).T * _steps(h)
+        assert np.all(np.abs(got[rows] - ref) <= BF * (np.abs(ref) + S) + S + 2.0 ** -133)
+    # the backward reads those rows
+    delta, W = _bf(rng, 200, h).cuda(), _bf(rng, E, h, I, scale=h ** -0.5).cuda()
+    dh1 = torch.empty(200, 2 * I, **bf)
+    soff = torch.tensor([0, 100, 200], dtype=torch.int32, device="cuda")
+    L.lrm_ffn_backward(ctx, delta, W, ab, soff, ids[-200:].contiguous(), dims, 200, dh1, None, None, 0)
+    torch.cuda.synchronize()
+    assert L.lrm_get_device_status(ctx) == 0
+    ref, _ = O.ffn_backward(_np(delta), _np(W), got, np.array([0, 100, 200]), np.arange(200), 200)
+    a, b = got[:, :I], got[:, I:]
+    td = np.concatenate([np.abs(_np(delta)[r]) @ np.abs(_np(W)[e]) for e, r in ((0, slice(0, 100)), (1, slice(100, 200)))])
+    td = td * _steps(h)
+    size = np.concatenate([td * 1.1 * np.abs(b), td * np.abs(a)], 1)
+    dphi = np.concatenate([_np(delta)[r] @ _np(W)[e] for e, r in ((0, slice(0, 100)), (1, slice(100, 200)))])
+    ev = (2 + np.abs(a)) * 2.0 ** -20
+    size += np.concatenate([np.abs(dphi * b) * ev, np.abs(dphi * a) * ev], 1)
+    assert np.all(np.abs(_np(dh1) - ref) <= BF * (np.abs(ref) + size) + size + 2.0 ** -133)
+
+
 def test_refusals(ctx):
     from backward_token_expert_gb300 import lrm as L
 

@@ -254,7 +254,7 @@ def test_refusals(ctx):
             (fwd, dict(x=None), inv), (fwd, dict(g=None), inv), (fwd, dict(b=None), inv), (fwd, dict(y=None), inv),
             (fwd, dict(stats=None), inv), (fwd, dict(dt=2), inv), (fwd, dict(rows=-1), inv), (fwd, dict(width=0), inv),
             (fwd, dict(eps=-1.0), inv), (fwd, dict(eps=float("nan")), inv), (fwd, dict(width=16385), shape),
-            (fwd, dict(x=p + 2), al), (fwd, dict(y=p + 4), al), (fwd, dict(g=p + 2), al),
+            (fwd, dict(x=p + 2), al), (fwd, dict(y=p + 4), al), (fwd, dict(g=p + 2), al), (fwd, dict(stats=p + 4), al),
             (bwd, dict(dy=None), inv), (bwd, dict(dx=None), inv), (bwd, dict(dg=None), inv), (bwd, dict(db=None), inv),
             (bwd, dict(ws=None), wsp), (bwd, dict(nb=127), wsp), (bwd, dict(dy=p + 2), al), (bwd, dict(dres=p + 2), al),
             (bwd, dict(dx=p + 8), al), (bwd, dict(x=p + 1), al), (bwd, dict(width=16385), shape)]:
