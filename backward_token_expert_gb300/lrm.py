@@ -216,21 +216,23 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def _ptr(x) -> int | None:
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    return x if x is None or isinstance(x, int) else x.data_ptr()
+
+
+_raw_stream = None  # torch's (lookup of a device's current raw stream, lookup of the current device), once CUDA is up
 
 
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
 
+            if not torch.cuda.is_initialized():
+                return torch.cuda.current_stream().cuda_stream
+            _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         # the raw handle: making a torch stream object costs about 3 us a call, a third of a small call's host time
-        if torch.cuda.is_initialized():
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream[0](_raw_stream[1]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
