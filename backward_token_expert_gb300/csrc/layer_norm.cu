@@ -29,10 +29,11 @@ namespace lrm {
 namespace {
 
 constexpr int MAX_WIDTH = 16384;
-// Columns of a thread that holds its columns' weights, and the registers that needs: 64 bytes of a row forward, 32
+// Columns of a thread that holds its columns' weights, and the registers that needs: 64 bytes of a row forward (48 of
+// unaligned ones, whose edges take registers: 20011 bf16 rows of 1497 values took 38 us so, 56 with 64, 42 with 32), 32
 // backward, where the sums take their place.
-template <typename T>
-constexpr int FWD_COLS = sizeof(T) == 2 ? 32 : 16;
+template <typename T, bool ALIGNED>
+constexpr int FWD_COLS = (ALIGNED ? 64 : 48) / sizeof(T);
 template <typename T>
 constexpr int FWD_REGS = sizeof(T) == 2 ? 128 : 96;
 template <typename T>
@@ -79,20 +80,22 @@ struct Vec<uint16_t> {  // bf16 bits
 };
 
 constexpr int MAX_WARPS = 16;
+constexpr int MAX_GROUPS = 8;  // rows of more than one warp that a block has at a time
 
 // Sums over a row's threads: `lanes` of a warp by shuffles, then, where a row has several warps, the warps' sums
-// through shared memory in a fixed order.  `slot` alternates between calls, so that one barrier a call is enough.
+// through shared memory in a fixed order.  `slot` alternates between calls, so that one barrier a call is enough, which
+// is that of the row's threads alone.
 template <int K>
-__device__ __forceinline__ void row_sum(float (&s)[K], int lanes, float (*buf)[K][MAX_WARPS], int& slot) {
+__device__ __forceinline__ void row_sum(float (&s)[K], int lanes, int group, float (*buf)[K][MAX_WARPS], int& slot) {
   for (int o = min(lanes, 32) / 2; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < K; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
   if (lanes <= 32) return;
-  const int warp = threadIdx.x >> 5, warps = lanes >> 5;
+  const int warp = (threadIdx.x >> 5) - group * (lanes >> 5), warps = lanes >> 5;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
     for (int i = 0; i < K; ++i) buf[slot][i][warp] = s[i];
-  __syncthreads();
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
 #pragma unroll
   for (int i = 0; i < K; ++i) {
     s[i] = 0.0f;
@@ -115,76 +118,111 @@ template <typename T, int NV, bool ALIGNED>
 struct Block {
   static constexpr int N = Vec<T>::N;
   int lanes, lane, groups, group, cls, classes, lead, count, width;
-  long long step, rows;
+  uint32_t step, rows;  // rows and a few steps beyond them fit 32 bits
+  uint4* edges;  // shared: the bits of the row's own elements in its first and its last vector
+  using Bits = std::conditional_t<(NV * N > 32), uint64_t, uint32_t>;
+  Bits own_bits = 0;  // !ALIGNED
 
-  __device__ __forceinline__ Block(int rows_, int width_, int shift, int classes_, int lanes_)
+  // The block's threads meet before the first clean().
+  __device__ __forceinline__ Block(int rows_, int width_, int shift, int classes_, int lanes_, uint4* edges_)
       : lanes(lanes_), lane(threadIdx.x % lanes_), groups(blockDim.x / lanes_), group(threadIdx.x / lanes_),
         cls(blockIdx.x % classes_), classes(classes_), width(width_),
-        step(static_cast<long long>(gridDim.x / classes_) * groups * classes_), rows(rows_) {
+        step(gridDim.x / classes_ * groups * classes_), rows(rows_), edges(edges_) {
     // elements before the row in its first vector; vectors that cover a row
     lead = ALIGNED ? 0 : static_cast<int>((static_cast<long long>(cls) * width + shift) % N);
     count = (lead + width + N - 1) / N;
+    if (ALIGNED) return;
+    const uint32_t first = ~0u << lead, last = (1u << (lead + width - (count - 1) * N)) - 1u;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      uint32_t w = (1u << N) - 1u;
+      if (vector(i) == 0) w &= first;
+      if (vector(i) == count - 1) w &= last;
+      if (vector(i) < count) own_bits |= static_cast<Bits>(w) << (i * N);
+    }
+    if (threadIdx.x < 2) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w[k] = 0u;
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j)
+          if ((threadIdx.x == 0 ? first : last) >> (k * (N / 4) + j) & 1u) w[k] |= N == 4 ? ~0u : 0xFFFFu << (16 * j);
+      }
+      edges[threadIdx.x] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
-  // a vector with elements that are not the row's own: its first or last at most
-  __device__ __forceinline__ bool edge(int i) const {
-    return !ALIGNED && ((vector(i) == 0 && lead > 0) || (vector(i) == count - 1 && lead + width < count * N));
+  // bit j: element j of vector i is the row's own
+  __device__ __forceinline__ uint32_t own(int i) const {
+    return static_cast<uint32_t>(own_bits >> (i * N)) & ((1u << N) - 1u);
   }
-  __device__ __forceinline__ long long first() const {
-    return (static_cast<long long>(blockIdx.x / classes) * groups + group) * classes + cls;
+  // a vector with elements that are not the row's own
+  __device__ __forceinline__ bool edge(int i) const { return !ALIGNED && own(i) != (1u << N) - 1u; }
+  __device__ __forceinline__ uint32_t first() const {
+    return (blockIdx.x / classes * groups + group) * classes + cls;
   }
   // the block goes on while its first row is there: all its threads take part in the sums of every pass
-  __device__ __forceinline__ long long first_of_block() const {
-    return static_cast<long long>(blockIdx.x / classes) * groups * classes + cls;
+  __device__ __forceinline__ uint32_t first_of_block() const {
+    return blockIdx.x / classes * groups * classes + cls;
   }
+  // element offset of a row's column, and of what lies behind the last row
+  __device__ __forceinline__ long long at(uint32_t row, int c) const {
+    return static_cast<long long>(static_cast<uint64_t>(row) * static_cast<uint32_t>(width)) + c;
+  }
+  __device__ __forceinline__ long long end() const { return at(rows, 0); }
   __device__ __forceinline__ int vector(int i) const { return lane + i * lanes; }
   __device__ __forceinline__ int column(int i) const { return vector(i) * N - lead; }
   // Vector i of a row as it lies in memory: its elements outside the row are a neighbour's, which clean() removes where
   // the values are used (masking here would wait for them).
-  __device__ __forceinline__ uint4 load(const T* base, long long row, int i) const {
+  __device__ __forceinline__ uint4 load(const T* base, uint32_t row, int i) const {
     if (vector(i) >= count) return make_uint4(0u, 0u, 0u, 0u);
-    const long long e0 = row * width + column(i);
-    if (ALIGNED || (e0 >= 0 && e0 + N <= rows * width)) return ld_stream(reinterpret_cast<const uint4*>(base + e0));
+    const long long e0 = at(row, column(i));
+    if (ALIGNED || (row > 0 && row < rows - 1) || (e0 >= 0 && e0 + N <= end()))
+      return ld_stream(reinterpret_cast<const uint4*>(base + e0));
     uint32_t w[4] = {0u, 0u, 0u, 0u};  // reaches beyond the tensor
+#pragma unroll 1
+    for (int j = 0; j < N; ++j) {  // element by element from the top, in few instructions: two vectors of a tensor come here
+      const T* from = base + e0 + j;
+      const bool mine = own(i) >> j & 1u;
+      if constexpr (N == 4) {
+        w[0] = w[1], w[1] = w[2], w[2] = w[3];
+        w[3] = mine ? __float_as_uint(*from) : 0u;
+      } else {
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (column(i) + j >= 0 && column(i) + j < width) {
-        if constexpr (N == 4)
-          w[j] = __float_as_uint(base[e0 + j]);
-        else
-          w[j / 2] |= static_cast<uint32_t>(base[e0 + j]) << (16 * (j % 2));
-      }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  __device__ __forceinline__ uint4 clean(const uint4& r, int i) const {
-    if (!edge(i)) return r;
-    uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      constexpr int PER = N / 4;  // elements of a 32-bit word
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const int c = column(i) + k * PER + j;
-        if (c < 0 || c >= width) w[k] &= PER == 1 ? 0u : (j == 0 ? 0xFFFF0000u : 0x0000FFFFu);
+        for (int k = 0; k < 3; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+        w[3] = w[3] >> 16 | (mine ? static_cast<uint32_t>(*from) : 0u) << 16;
       }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ __forceinline__ void store(T* base, long long row, int i, const F2 (&f)[N / 2]) const {
+  __device__ __forceinline__ uint4 clean(uint4 r, int i) const {
+    if (!edge(i)) return r;
+    if (vector(i) == 0) r = both(r, edges[0]);
+    if (vector(i) == count - 1) r = both(r, edges[1]);
+    return r;
+  }
+  __device__ static __forceinline__ uint4 both(const uint4& a, const uint4& b) {
+    return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
+  }
+  // zeros for a row that does not count
+  __device__ __forceinline__ void store(T* base, uint32_t row, int i, const F2 (&f)[N / 2], bool counted) const {
     if (vector(i) >= count) return;
-    T* at = base + row * width + column(i);
-    const uint4 r = Vec<T>::pack(f);
+    T* to = base + at(row, column(i));
+    const uint32_t keep = counted ? ~0u : 0u;
+    uint4 r = Vec<T>::pack(f);
+    r = make_uint4(r.x & keep, r.y & keep, r.z & keep, r.w & keep);
     if (!edge(i)) {
-      *reinterpret_cast<uint4*>(at) = r;
+      *reinterpret_cast<uint4*>(to) = r;
       return;
     }
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      if (column(i) + j >= 0 && column(i) + j < width) {
+      if (own(i) >> j & 1u) {
         if constexpr (N == 4)
-          at[j] = __uint_as_float(w[j]);
+          to[j] = __uint_as_float(w[j]);
         else
-          at[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j % 2)));
+          to[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j % 2)));
       }
   }
   // the pair's weights, 0 outside the row
@@ -218,11 +256,11 @@ struct Ring {
   // One thread: copies row `row` into slot n % depth, unless it is padding.  Vectors that reach beyond the tensor are
   // left to their readers.
   template <int NV, bool ALIGNED>
-  __device__ __forceinline__ void issue(const Block<T, NV, ALIGNED>& b, int n, long long row, bool wanted) const {
+  __device__ __forceinline__ void issue(const Block<T, NV, ALIGNED>& b, int n, uint32_t row, bool wanted) const {
     uint64_t* bar = bars + n % depth;
-    const long long e0 = row * b.width - b.lead;
+    const long long e0 = b.at(row, -b.lead);
     const int v0 = !ALIGNED && e0 < 0 ? 1 : 0;
-    const int v1 = b.count - (!ALIGNED && e0 + static_cast<long long>(b.count) * b.N > b.rows * b.width ? 1 : 0);
+    const int v1 = b.count - (!ALIGNED && e0 + static_cast<long long>(b.count) * b.N > b.end() ? 1 : 0);
     const uint32_t bytes = v1 > v0 ? (v1 - v0) * 16 : 0;
     if (!wanted || bytes == 0) {
       mbar_arrive(bar);
@@ -241,11 +279,11 @@ struct Ring {
     mbar_wait(bars + n % depth, (n / depth) & 1, DRAIN_NS, nullptr);
   }
   template <int NV, bool ALIGNED>
-  __device__ __forceinline__ uint4 read(const Block<T, NV, ALIGNED>& b, int n, int array, long long row, int i) const {
+  __device__ __forceinline__ uint4 read(const Block<T, NV, ALIGNED>& b, int n, int array, uint32_t row, int i) const {
     if (b.vector(i) >= b.count) return make_uint4(0u, 0u, 0u, 0u);
     if (!ALIGNED && b.edge(i)) {
-      const long long e0 = row * b.width + b.column(i);
-      if (e0 < 0 || e0 + b.N > b.rows * b.width) return b.load(src[array], row, i);
+      const long long e0 = b.at(row, b.column(i));
+      if (e0 < 0 || e0 + b.N > b.end()) return b.load(src[array], row, i);
     }
     return slot(n, array)[b.vector(i)];
   }
@@ -257,7 +295,7 @@ __device__ __forceinline__ void clear_sums(float* buf, int n) {
 }
 
 // HOLD (64 bytes of a row's columns a thread): gamma and beta in registers, the next row's values loaded ahead; else
-// (wider rows than that gives) gamma and beta in shared memory, skewed.  (32768 bf16 rows of 2048 values: 51 us, and 62
+// (wider rows than that gives) gamma and beta in shared memory, skewed.  (32768 bf16 rows of 2048 values: 50 us, and 62
 // with 32 bytes a thread, 92 with 16; one warp a row with gamma and beta in shared memory takes 58, rows through a ring
 // of bulk copies 61.)
 template <typename T, int NV, bool HOLD, bool ALIGNED>
@@ -270,7 +308,8 @@ __global__ void __maxnreg__(HOLD ? FWD_REGS<T> : 128)
   __shared__ __align__(16) float s_buf[2][1][MAX_WARPS];
   clear_sums(&s_buf[0][0][0], 2 * MAX_WARPS);
   grid_dependency_wait();
-  const Block<T, NV, ALIGNED> b(rows, width, shift, classes, lanes);
+  __shared__ uint4 s_edges[2];
+  const Block<T, NV, ALIGNED> b(rows, width, shift, classes, lanes, s_edges);
   const int per = skew(width, N) + 1;
   if (!HOLD)
     for (int c = threadIdx.x; c < width; c += blockDim.x) {
@@ -288,14 +327,14 @@ __global__ void __maxnreg__(HOLD ? FWD_REGS<T> : 128)
   int slot = 0;
   uint4 raw[NV];
   bool on = false;  // the row whose values are in raw is there and no padding
-  auto fetch = [&](long long row) {
-    on = row < rows && (valid == nullptr || valid[row] != 0);
+  auto fetch = [&](uint32_t row) {
+    on = row < b.rows && (valid == nullptr || valid[row] != 0);
 #pragma unroll
     for (int i = 0; i < NV; ++i) raw[i] = on ? b.load(x, row, i) : make_uint4(0u, 0u, 0u, 0u);
   };
-  long long row = b.first();
+  uint32_t row = b.first();
   fetch(row);
-  for (long long q = b.first_of_block(); q < rows; q += b.step, row += b.step) {
+  for (uint32_t q = b.first_of_block(); q < b.rows; q += b.step, row += b.step) {
     F2 f[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) Vec<T>::unpack(b.clean(raw[i], i), f[i]);
@@ -307,7 +346,7 @@ __global__ void __maxnreg__(HOLD ? FWD_REGS<T> : 128)
 #pragma unroll
       for (int j = 0; j < P; ++j) acc = add2(acc, f[i][j]);  // zeros outside the row
     float s[1] = {acc.get().x + acc.get().y};
-    row_sum(s, lanes, s_buf, slot);
+    row_sum(s, lanes, 0, s_buf, slot);
     const float mean = s[0] * inv;
     const F2 minus(-mean, -mean);
     acc = F2(0.0f, 0.0f);
@@ -315,21 +354,25 @@ __global__ void __maxnreg__(HOLD ? FWD_REGS<T> : 128)
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int j = 0; j < P; ++j) f[i][j] = add2(f[i][j], minus);
-      if (b.vector(i) >= b.count || b.edge(i)) {
+      if (ALIGNED && b.vector(i) >= b.count) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) f[i][j] = F2(0.0f, 0.0f);
+      }
+      if (b.edge(i)) {
+        const uint32_t own = b.own(i);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          const int c = b.column(i) + 2 * j;
           const float2 v = f[i][j].get();
-          f[i][j] = F2(c >= 0 && c < width ? v.x : 0.0f, c + 1 >= 0 && c + 1 < width ? v.y : 0.0f);
+          f[i][j] = F2(own >> (2 * j) & 1u ? v.x : 0.0f, own >> (2 * j + 1) & 1u ? v.y : 0.0f);
         }
       }
 #pragma unroll
       for (int j = 0; j < P; ++j) acc = fma2(f[i][j], f[i][j], acc);
     }
     s[0] = acc.get().x + acc.get().y;
-    row_sum(s, lanes, s_buf, slot);
+    row_sum(s, lanes, 0, s_buf, slot);
     const float rstd = 1.0f / sqrtf(s[0] * inv + eps);
-    if (row < rows) {
+    if (row < b.rows) {
       const F2 scale(rstd, rstd);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -339,17 +382,16 @@ __global__ void __maxnreg__(HOLD ? FWD_REGS<T> : 128)
             f[i][j] = fma2(mul2(f[i][j], scale), ga[i][j], be[i][j]);
           else
             f[i][j] = fma2(mul2(f[i][j], scale), b.skewed(s_dyn, i, j), b.skewed(s_dyn + per, i, j));
-          if (!counted) f[i][j] = F2(0.0f, 0.0f);
         }
-        b.store(y, row, i, f[i]);
+        b.store(y, row, i, f[i], counted);
       }
-      if (b.lane == 0) *reinterpret_cast<float2*>(stats + row * 2) = counted ? make_float2(mean, rstd) : make_float2(0.0f, 0.0f);
+      if (b.lane == 0) reinterpret_cast<float2*>(stats)[row] = counted ? make_float2(mean, rstd) : make_float2(0.0f, 0.0f);
     }
     if (!HOLD) fetch(row + b.step);
   }
 }
 
-// How a row's values reach a thread of the backward, which holds 32 bytes of a row's columns: HOLD, loaded a row ahead
+// How a row's values reach a thread of the backward, which holds 32 bytes of a row's columns: HELD, loaded a row ahead
 // into registers; RING (fp32, where that takes too many), through shared memory; WIDE, more columns than registers
 // have room for the sums beside gamma, which lies in shared memory then, skewed.
 enum Mode { HELD, RING, WIDE };
@@ -360,9 +402,11 @@ struct RingArgs {
   unsigned long long budget_ns;
 };
 
-// Backward.  Blocks leave their sums of the weights' gradients in partial [blocks, 2, width], which weight_sum_kernel
-// adds in a fixed order; where a block has several rows at a time, they are added through shared memory first.
-// Modes as above; WIDE: gamma lies in shared memory and the second pass over a row reads it again, out of the L2.
+// Backward.  Instructions bound it in bf16 (32768 rows of 2048 values: 76 us, and 99 when the second pass unpacked the
+// values anew instead of keeping xhat and d) and memory in fp32 (with a residual's gradient 160 us).  Blocks leave
+// their sums of the weights' gradients in partial [blocks, 2, width], which weight_sum_kernel adds in a fixed order;
+// where a block has several rows at a time, they are added through shared memory first.  Modes as above; WIDE: gamma lies in shared memory and
+// the second pass over a row reads it again, out of the L2.
 template <typename T, int NV, Mode MODE, bool ALIGNED, bool RES>
 __global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
     layer_norm_bwd_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ gamma,
@@ -373,11 +417,12 @@ __global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
   constexpr bool HOLD = MODE != WIDE;
   // HELD, several rows at a time: [groups][2][width]; RING: the rows; WIDE: gamma, skewed
   extern __shared__ __align__(16) float s_dyn[];
-  __shared__ __align__(16) float s_buf[2][2][MAX_WARPS];
+  __shared__ __align__(16) float s_buf[MAX_GROUPS][2][2][MAX_WARPS];
   __shared__ __align__(8) uint64_t s_bars[MAX_DEPTH];
-  clear_sums(&s_buf[0][0][0], 4 * MAX_WARPS);
+  clear_sums(&s_buf[0][0][0][0], MAX_GROUPS * 4 * MAX_WARPS);
   grid_dependency_wait();
-  const Block<T, NV, ALIGNED> b(rows, width, shift, classes, lanes);
+  __shared__ uint4 s_edges[2];
+  const Block<T, NV, ALIGNED> b(rows, width, shift, classes, lanes, s_edges);
   const float inv = 1.0f / static_cast<float>(width);
   F2 dg[NV][P], db[NV][P], ga[HOLD ? NV : 1][P];
   if (!HOLD)
@@ -402,13 +447,14 @@ __global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
   uint4 nx[HV], ny[HV], nr[HV];  // HELD: the next row's
   float mean = 0.0f, rstd = 0.0f;
   bool on = false;
-  auto counts = [&](long long r) { return r < rows && (valid == nullptr || valid[r] != 0); };
-  auto fetch = [&](long long r) {
-    on = counts(r);
+  auto counts = [&](uint32_t r) { return r < b.rows && (valid == nullptr || valid[r] != 0); };
+  auto fetch = [&](uint32_t r, bool counted) {
+    on = counted;
     mean = rstd = 0.0f;
     if (on) {
-      mean = __ldg(stats + r * 2);
-      rstd = __ldg(stats + r * 2 + 1);
+      const float2 st = __ldg(reinterpret_cast<const float2*>(stats) + r);
+      mean = st.x;
+      rstd = st.y;
     }
     if constexpr (MODE == HELD) {
 #pragma unroll
@@ -422,23 +468,24 @@ __global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
   Ring<T, RES ? 3 : 2> ring{reinterpret_cast<uint8_t*>(s_dyn), s_bars, args.depth, b.count * 16, {x, dy}, valid,
                             args.status, args.budget_ns};
   if constexpr (RES) ring.src[2] = dres;
-  long long row = b.first();
+  uint32_t row = b.first();
   bool ahead = false;  // RING, the first thread: whether the row after those on their way counts
   if constexpr (MODE == RING) {
     if (threadIdx.x == 0) {
       for (int i = 0; i < args.depth; ++i) mbar_init(s_bars + i, 1);
       fence_mbar_init();
       for (int i = 0; i < args.depth; ++i)
-        if (row + i * b.step < rows) ring.issue(b, i, row + i * b.step, counts(row + i * b.step));
+        if (row + i * b.step < b.rows) ring.issue(b, i, row + i * b.step, counts(row + i * b.step));
       ahead = counts(row + args.depth * b.step);
     }
     __syncthreads();
   }
-  fetch(row);
+  fetch(row, counts(row));
+  bool next_on = counts(row + b.step);
   int n = 0;
-  for (long long q = b.first_of_block(); q < rows; q += b.step, row += b.step, ++n) {
+  for (uint32_t q = b.first_of_block(); q < b.rows; q += b.step, row += b.step, ++n) {
     const bool counted = on;
-    const F2 minus(-mean, -mean), scale(rstd, rstd);
+    const float mu = mean, rs = rstd;
     uint4 xr[HV], yr[HV], rr[HV];
     if constexpr (MODE == RING) {
       ring.wait(n);
@@ -452,8 +499,8 @@ __global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
 #pragma unroll
       for (int i = 0; i < NV; ++i) xr[i] = nx[i], yr[i] = ny[i], rr[i] = RES ? nr[i] : none;
     }
-    if constexpr (HOLD) fetch(row + b.step);
-    // xhat and dy of vector i, twice out of the same 16 bytes: fp32 copies would take twice the registers in bf16
+    // xhat and dy of vector i; the elements that are not the row's own have dy = 0 and add nothing
+    const F2 minus(-mu, -mu), scale(rs, rs);
     auto values = [&](int i, F2 (&vx)[P], F2 (&vy)[P]) {
       const int k = HOLD ? i : 0;
       if constexpr (!HOLD) {
@@ -465,60 +512,64 @@ __global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
 #pragma unroll
       for (int j = 0; j < P; ++j) vx[j] = mul2(add2(vx[j], minus), scale);
     };
+    F2 vx[HV][P], vd[HV][P];  // HOLD: xhat and d, kept for the second pass
     F2 s0(0.0f, 0.0f), s1(0.0f, 0.0f);
-    // the elements of a vector that are not the row's own have dy = 0 and add nothing
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      F2 vx[P], vy[P];
-      values(i, vx, vy);
+      const int k = HOLD ? i : 0;
+      F2 vy[P];
+      values(i, vx[k], vy);
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        const F2 d = mul2(vy[j], weight(i, j));
-        s0 = add2(s0, d);
-        s1 = fma2(d, vx[j], s1);
-        dg[i][j] = fma2(vy[j], vx[j], dg[i][j]);
+        vd[k][j] = mul2(vy[j], weight(i, j));
+        s0 = add2(s0, vd[k][j]);
+        s1 = fma2(vd[k][j], vx[k][j], s1);
+        dg[i][j] = fma2(vy[j], vx[k][j], dg[i][j]);
         db[i][j] = add2(db[i][j], vy[j]);
       }
     }
+    if constexpr (HOLD) {
+      fetch(row + b.step, next_on);
+      next_on = counts(row + 2 * b.step);
+    }
     float s[2] = {s0.get().x + s0.get().y, s1.get().x + s1.get().y};
-    row_sum(s, lanes, s_buf, slot);
+    row_sum(s, lanes, b.group, s_buf[lanes > 32 ? b.group : 0], slot);
     if constexpr (MODE == RING) {  // all threads have read the row: its slot takes the next one
-      if (threadIdx.x == 0 && row + args.depth * b.step < rows) {
+      if (threadIdx.x == 0 && row + args.depth * b.step < b.rows) {
         ring.issue(b, n + args.depth, row + args.depth * b.step, ahead);
         ahead = counts(row + (args.depth + 1) * b.step);
       }
     }
-    if constexpr (HOLD && sizeof(T) == 2) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {  // unpacked anew below
-        asm volatile("" : "+r"(xr[i].x), "+r"(xr[i].y), "+r"(xr[i].z), "+r"(xr[i].w));
-        asm volatile("" : "+r"(yr[i].x), "+r"(yr[i].y), "+r"(yr[i].z), "+r"(yr[i].w));
-      }
-    }
-    if (row < rows) {
-      const F2 m0(-s[0] * inv, -s[0] * inv), m1(-s[1] * inv, -s[1] * inv);
+    if (row < b.rows) {
+      const float c0 = -s[0] * inv * rs, c1 = -s[1] * inv * rs;
+      const F2 m0(c0, c0), m1(c1, c1);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        F2 vx[P], vy[P], vr[P];
-        values(i, vx, vy);
+        const int k = HOLD ? i : 0;
+        F2 vr[P], vo[P];
+        if constexpr (!HOLD) {
+          values(i, vx[0], vd[0]);
+#pragma unroll
+          for (int j = 0; j < P; ++j) vd[0][j] = mul2(vd[0][j], weight(i, j));
+        }
         if constexpr (RES) {
           if constexpr (!HOLD) rr[0] = counted ? b.load(dres, row, i) : none;
-          Vec<T>::unpack(rr[HOLD ? i : 0], vr);  // a neighbour's values go no further than the store
+          Vec<T>::unpack(rr[k], vr);  // a neighbour's values go no further than the store
         }
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          const F2 g = fma2(vx[j], m1, fma2(vy[j], weight(i, j), m0));
-          if constexpr (RES)
-            vx[j] = fma2(g, scale, vr[j]);
-          else
-            vx[j] = mul2(g, scale);
-          if (!counted) vx[j] = F2(0.0f, 0.0f);
+          const F2 t = fma2(vx[k][j], m1, RES ? add2(vr[j], m0) : m0);
+          vo[j] = fma2(vd[k][j], scale, t);
         }
-        b.store(dx, row, i, vx);
+        b.store(dx, row, i, vo, counted);
       }
     }
-    if (!HOLD) fetch(row + b.step);
+    if (!HOLD) {
+      fetch(row + b.step, next_on);
+      next_on = counts(row + 2 * b.step);
+    }
   }
+  grid_dependency_launch();
   float* out = b.groups > 1 ? s_dyn + b.group * 2 * width : partial + static_cast<size_t>(blockIdx.x) * 2 * width;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -545,26 +596,37 @@ __global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
   }
 }
 
-constexpr int WS_ROWS = 32;  // threads that share a column's blocks
+constexpr int WS_COLS = 16, WS_PARTS = 64;  // of a block: columns, threads that share a column's sums
 
-// column c of [dgamma | dbeta] = the sum of the blocks' partial sums
-__global__ void __launch_bounds__(32 * WS_ROWS)
+// Column c of [dgamma | dbeta] = the sum of the blocks' partial sums.  Latency bounds it: the loads of a thread are all
+// in flight at once (READS, for the one wave of blocks that leave sums).
+__global__ void __launch_bounds__(WS_COLS* WS_PARTS)
     weight_sum_kernel(const float* __restrict__ partial, int blocks, int width, float* __restrict__ dgamma,
                       float* __restrict__ dbeta) {
-  __shared__ float s[WS_ROWS][33];
+  constexpr int READS = 12;
+  __shared__ float s[WS_PARTS][WS_COLS + 1];
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  const int col = threadIdx.x % WS_COLS, part = threadIdx.x / WS_COLS;
+  const int c = blockIdx.x * WS_COLS + col;
   float sum = 0.0f;
   if (c < 2 * width)
-    for (int b = part; b < blocks; b += WS_ROWS) sum += __ldg(partial + static_cast<size_t>(b) * 2 * width + c);
-  s[part][lane] = sum;
+    for (int b = part; b < blocks; b += READS * WS_PARTS) {
+      float v[READS];
+#pragma unroll
+      for (int i = 0; i < READS; ++i)
+        v[i] = b + i * WS_PARTS < blocks ? __ldg(partial + static_cast<size_t>(b + i * WS_PARTS) * 2 * width + c) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < READS; ++i) sum += v[i];
+    }
+  s[part][col] = sum;
   __syncthreads();
-  sum = s[lane][part];  // thread (part, lane): partial sum `lane` of column `part` of the block
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp >= WS_COLS) return;
+  sum = s[lane][warp] + s[lane + 32][warp];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const int col = blockIdx.x * 32 + part;
-  if (lane == 0 && col < 2 * width) (col < width ? dgamma[col] : dbeta[col - width]) = sum;
+  const int to = blockIdx.x * WS_COLS + warp;
+  if (lane == 0 && to < 2 * width) (to < width ? dgamma[to] : dbeta[to - width]) = sum;
 }
 
 int ceil_div(long long a, int b) { return static_cast<int>((a + b - 1) / b); }
@@ -592,9 +654,9 @@ struct Plan {
   int lanes, nv, threads, classes, blocks, per_sm;
 };
 
-// `most`: vectors a thread at most, `resident`: threads an SM has room for
+// `most`: vectors a thread at most, `resident`: threads an SM has room for, `together`: in as few blocks as that takes
 template <typename T>
-Plan plan(int sm_count, int rows, int width, bool al, int most, int resident) {
+Plan plan(int sm_count, int rows, int width, bool al, int most, int resident, bool together) {
   Plan p;
   const int nvec = row_vectors<T>(width, al);
   p.lanes = 1;
@@ -602,6 +664,12 @@ Plan plan(int sm_count, int rows, int width, bool al, int most, int resident) {
   while (p.lanes >= 32 && p.lanes < 32 * MAX_WARPS && p.lanes * most < nvec) p.lanes += 32;
   p.nv = ceil_div(nvec, p.lanes);
   p.threads = p.lanes > 32 ? p.lanes : 128;
+  if (together && p.nv <= most) {
+    // no more rows at a time than give every SM a block
+    int groups = ceil_div(rows, sm_count);
+    if (groups > resident / p.lanes) groups = resident / p.lanes;
+    if (groups * p.lanes > p.threads) p.threads = ceil_div(groups * p.lanes, 32) * 32;
+  }
   p.classes = 1;
   if (!al) {
     p.classes = Vec<T>::N;
@@ -618,7 +686,11 @@ Plan plan(int sm_count, int rows, int width, bool al, int most, int resident) {
 }
 template <typename T>
 Plan bwd_plan(int sm_count, int rows, int width, bool al) {
-  return plan<T>(sm_count, rows, width, al, BWD_COLS<T> / Vec<T>::N, threads_per_sm(BWD_REGS<T>));
+  // A block leaves one sum of the weights' gradients: one block an SM with several rows at a time takes 58 us for 20011
+  // bf16 rows of 1497 values, a block a row 62 (10 and 16 for 760 rows).  A ring's block has one row.
+  const Plan p = plan<T>(sm_count, rows, width, al, BWD_COLS<T> / Vec<T>::N, threads_per_sm(BWD_REGS<T>), false);
+  if (sizeof(T) == 4 && p.lanes > 32) return p;
+  return plan<T>(sm_count, rows, width, al, BWD_COLS<T> / Vec<T>::N, threads_per_sm(BWD_REGS<T>), true);
 }
 
 // Rows of a ring: as many as the blocks of an SM have room for beside one another.
@@ -655,8 +727,8 @@ lrm_status allow_smem(Kern kern, size_t smem) {
 template <typename T, bool ALIGNED>
 lrm_status forward(lrm_ctx* ctx, const void* x, const float* gamma, const float* beta, const uint8_t* valid, int rows,
                    int width, float eps, void* y, float* stats, cudaStream_t s) {
-  constexpr int HOLDS = FWD_COLS<T> / Vec<T>::N;
-  const Plan p = plan<T>(ctx->sm_count, rows, width, ALIGNED, HOLDS, threads_per_sm(FWD_REGS<T>));
+  constexpr int HOLDS = FWD_COLS<T, ALIGNED> / Vec<T>::N;
+  const Plan p = plan<T>(ctx->sm_count, rows, width, ALIGNED, HOLDS, threads_per_sm(FWD_REGS<T>), false);
   auto go = [&](auto n, auto hold) {
     auto kern = layer_norm_kernel<T, decltype(n)::value, decltype(hold)::value, ALIGNED>;
     const size_t smem = decltype(hold)::value ? 0 : 2 * (width + width / Vec<T>::N + 1) * sizeof(float);
@@ -694,7 +766,7 @@ lrm_status backward(lrm_ctx* ctx, const void* x, const void* dy, const float* ga
                             shift_of<T>(x), p.classes, p.lanes, ring, static_cast<T*>(dx), partial);
   });
   if (st != LRM_OK) return st;
-  return launch_dependent(weight_sum_kernel, ceil_div(2ll * width, 32), 32 * WS_ROWS, 0, 0, s, partial, p.blocks,
+  return launch_dependent(weight_sum_kernel, ceil_div(2ll * width, WS_COLS), WS_COLS * WS_PARTS, 0, 0, s, partial, p.blocks,
                           width, dgamma, dbeta);
 }
 
