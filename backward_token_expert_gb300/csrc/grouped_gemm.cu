@@ -827,15 +827,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR, SW
       constexpr int CHUNKS = SHARE / 16;
       float* fbuf = reinterpret_cast<float*>(wbuf);  // [8 rows][32 columns], 16-byte chunks XOR-swizzled by row
       const int sub = lane >> 2, quad = lane & 3;    // a step's row of eight, 8 columns of its 32
-      // A tile as this warp sees it: its rows are c_begin .. c_end, row0 the compacted row of the tile's first,
-      // ids[i] the pair of row c_begin + 32 i + lane (-1: none), col0 the warp's first column.
+      // A tile as this warp sees it: its rows are c_begin .. c_end, those below `end` in the segment, row0 the compacted
+      // row of the tile's first, ids[i] the pair of row c_begin + 32 i + lane, col0 the warp's first column.
       struct Tile {
-        int row0, c_end, col0, ids[CHUNKS / 2];
+        int row0, c_end, end, col0, ids[CHUNKS / 2];
       };
       auto look = [&](int tile, Tile& t) {
-        t.c_end = c_begin;
-#pragma unroll
-        for (int i = 0; i < CHUNKS / 2; ++i) t.ids[i] = -1;
+        t.c_end = t.end = c_begin;
         if (tile >= total_tiles) return;
         int e, nt, mt;
         decode(tile, e, nt, mt);
@@ -843,11 +841,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR, SW
         t.row0 = s_start[e] + nt * BNR;
         t.c_end = min(tile_rows(len, nt), c_begin + SHARE);
         t.col0 = mt * 256 + static_cast<int>(rank) * 128 + q * 32;
-        const int rows_valid = len - nt * BNR;  // rows of this tile inside the segment
+        t.end = min(t.c_end, len - nt * BNR);
 #pragma unroll
         for (int i = 0; i < CHUNKS / 2; ++i) {
           const int r = c_begin + 32 * i + lane;
-          t.ids[i] = r < min(t.c_end, rows_valid) ? __ldg(row_map + t.row0 + r) : -1;
+          t.ids[i] = r < t.end ? __ldg(row_map + t.row0 + r) : 0;
         }
       };
       // a and b of rows 8 i + sub of a chunk of 16 rows and their pairs (-1: none): one chunk computed, AHEAD on their
@@ -860,10 +858,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR, SW
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           int u = __shfl_sync(0xffffffffu, t.ids[ci / 2], (ci % 2) * 16 + 8 * i + sub);
-          if (u >= sw.N || u < -1) {
-            raise_flag(status, LRM_ERR_INDEX);
-            u = -1;
-          }
+          const bool there = c_begin + 16 * ci + 8 * i + sub < t.end;
+          if (there && (u < 0 || u >= sw.N)) raise_flag(status, LRM_ERR_INDEX);
+          if (!there || u >= sw.N) u = -1;
           pid[buf][i] = u;
           ga[buf][i] = gb[buf][i] = make_uint4(0u, 0u, 0u, 0u);
           if (u >= 0 && col < I) {

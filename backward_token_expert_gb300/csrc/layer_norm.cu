@@ -405,8 +405,8 @@ struct RingArgs {
 // Backward.  Instructions bound it in bf16 (32768 rows of 2048 values: 76 us, and 99 when the second pass unpacked the
 // values anew instead of keeping xhat and d) and memory in fp32 (with a residual's gradient 160 us).  Blocks leave
 // their sums of the weights' gradients in partial [blocks, 2, width], which weight_sum_kernel adds in a fixed order;
-// where a block has several rows at a time, they are added through shared memory first.  Modes as above; WIDE: gamma lies in shared memory and
-// the second pass over a row reads it again, out of the L2.
+// where a block has several rows at a time, they are added through shared memory first.  Modes as above; WIDE: gamma
+// lies in shared memory and the second pass over a row reads it again, out of the L2.
 template <typename T, int NV, Mode MODE, bool ALIGNED, bool RES>
 __global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
     layer_norm_bwd_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ gamma,

@@ -301,18 +301,9 @@ __device__ __forceinline__ void tma_load_5d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// Four rows y[0..3] of a 2-D tensor (a map with boxes one row high), written one after the other.
-__device__ __forceinline__ void tma_gather4_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int32_t x,
-                                                 const int32_t (&y)[4]) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
-      "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-      : "memory");
-}
-
-// The same, written at the same offset of every CTA in `mask` and counted on the barrier of the even CTA of each one's
-// pair (bar_cluster: that of this CTA's own pair).
+// Four rows y[0..3] of a 2-D tensor (a map with boxes one row high), one after the other, written at the same offset of
+// every CTA in `mask` and counted on the barrier of the even CTA of each one's pair (bar_cluster: that of this CTA's own
+// pair).
 __device__ __forceinline__ void tma_gather4_pair_multicast(void* dst, const CUtensorMap* map, uint32_t bar_cluster,
                                                            int32_t x, const int32_t (&y)[4], uint16_t mask) {
   asm volatile(

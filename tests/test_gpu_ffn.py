@@ -252,6 +252,44 @@ def test_bad_ids_and_totals(ctx):
     assert torch.equal(d0[:30], d1[:30]) and (d1[30:] == 7.0).all() and (g1[30:] == 0).all()
 
 
+@pytest.mark.parametrize("bad", [-1, -7, -2 ** 31])
+def test_a_negative_id_is_flagged_by_every_call(ctx, bad):
+    from backward_token_expert_gb300 import lrm as L
+
+    rng = np.random.default_rng(6)
+    T, E, k, h, I = 40, 2, 2, 64, 40
+    N = T * k
+    good, doff = _dev(np.arange(N), np.array([0, 50, N]), 0)
+    ids = good.clone()
+    ids[17] = bad
+    x, W1, W = _bf(rng, T, h).cuda(), _bf(rng, E, 2 * I, h).cuda(), _bf(rng, E, h, I).cuda()
+    delta, ab = _bf(rng, N, h).cuda(), _bf(rng, N, 2 * I).cuda()
+    dims = L.dims_of(T, E, k, h, I)
+    need = L.lrm_ffn_backward_workspace(ctx, dims, N)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    new = lambda w: torch.full((N, w), 7.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+
+    def run(i):
+        phi, rows, dh1, dgate = new(I), new(h), new(2 * I), torch.full((N,), 7.0, device="cuda")
+        flags = []
+        for call in (lambda: L.lrm_ffn_up(ctx, x, W1, doff, i, dims, N, None, phi),
+                     lambda: L.lrm_ffn_down(ctx, phi, W, doff, i, dims, N, rows),
+                     lambda: L.lrm_ffn_backward(ctx, delta, W, ab, doff, i, dims, N, dh1, dgate, ws, need)):
+            call()
+            torch.cuda.synchronize()
+            flags.append(L.lrm_get_device_status(ctx))
+        return flags, (phi, rows, dh1, dgate)
+
+    flags, want = run(good)
+    assert flags == [0, 0, 0]
+    flags, got = run(ids)
+    assert flags == [1 << L.LRM_ERR_INDEX] * 3
+    keep = [r for r in range(N) if r != 17]
+    for a, b in zip(want, got):
+        assert torch.equal(a[keep], b[keep])
+    assert (got[0][17] == 7.0).all() and (got[1][17] == 7.0).all() and (got[2][17] == 7.0).all() and got[3][17] == 0
+
+
 def test_extreme_activations(ctx):
     """Gates far below and above zero, infinities and NaN reach their own pair's outputs only."""
     from backward_token_expert_gb300 import lrm as L

@@ -62,7 +62,9 @@ def _untouched(buf, shift, n):
 SHAPES = [  # rows, width, shift of the tensors
     (1, 1, 0), (3, 2, 1), (5, 8, 0), (7, 16, 3), (33, 31, 0), (64, 64, 0), (129, 257, 5), (40, 256, 0), (300, 1000, 0),
     (301, 1497, 0), (500, 2048, 0), (9, 2048, 0), (150, 2050, 0), (70, 4104, 0), (60, 5120, 0), (33, 8191, 2), (20, 8192, 0),
-    (17, 16384, 0), (11, 16383, 1), (5000, 24, 0), (3001, 100, 0), (1, 2048, 0), (2, 5, 0)]
+    (17, 16384, 0), (11, 16383, 1), (5000, 24, 0), (3001, 100, 0), (1, 2048, 0), (2, 5, 0),
+    # several rows of several warps a block in the backward
+    (3000, 1497, 3), (2777, 704, 0), (1600, 2048, 0), (700, 6001, 1)]
 
 
 def _inputs(rows, width, dtype, seed, masked):
