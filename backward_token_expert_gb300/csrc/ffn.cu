@@ -58,7 +58,7 @@ struct CfgFfn {
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int EPI_WARPS = 8;
   static constexpr int GATHER_WARPS = 4;
-  static constexpr int ROUND = 16 * GATHER_WARPS;  // a tile's pairs are a multiple: each gather warp has its share of four rows
+  static constexpr int ROUND = 32;  // a tile's pairs are a multiple: each gather warp has four rows at least
   static constexpr int THREADS = 64 + 32 * EPI_WARPS + 32 * GATHER_WARPS;
   static constexpr int BUF_BYTES = 32 * 64;  // a warp's: 32 pairs, 32 bf16 values each
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * BUF_BYTES + 1024;
@@ -156,17 +156,15 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
   };
   // tile -> expert, row tile nt (over the segment), feature tile mt; the row tiles of one feature tile run side by
   // side, so neighbouring CTA pairs share its weights through L2
-  auto decode = [&](int tile, int& e, int& nt, int& mt) {
-    int lo = 0, hi = E - 1;  // last expert with s_prefix <= tile
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_prefix[mid] <= tile)
-        lo = mid;
-      else
-        hi = mid - 1;
+  int e = 0;  // a warp's tiles come in order: the expert of its last one
+  auto decode = [&](int tile, int& nt, int& mt) {
+    for (;;) {  // the last expert with s_prefix <= tile, 32 at a time
+      const int i = e + 1 + lane;
+      const unsigned m = __ballot_sync(0xffffffffu, i < E && s_prefix[i] <= tile);
+      e += __popc(m);
+      if (m != 0xffffffffu) break;
     }
-    e = lo;
-    const int rem = tile - s_prefix[lo];
+    const int rem = tile - s_prefix[e];
     const int n_nt = (s_len[e] + C::BN - 1) / C::BN;
     mt = rem / n_nt;
     nt = rem - mt * n_nt;
@@ -180,112 +178,117 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ weights
-    if (lane == 0) {
-      const uint32_t full0 = mapa_shared(&full_bar[0], leader_rank);  // the even CTA's full barriers
-      uint32_t it = 0;
-      bool ok = true;
-      for (int tile = pair; tile < total_tiles && ok; tile += npairs) {
-        int e, nt, mt;
-        decode(tile, e, nt, mt);
+    const uint32_t full0 = mapa_shared(&full_bar[0], leader_rank);  // the even CTA's full barriers
+    uint32_t it = 0;
+    bool ok = true;
+    for (int tile = pair; tile < total_tiles && ok; tile += npairs) {
+      int nt, mt;
+      decode(tile, nt, mt);
+      if (elect_one()) {
         const int m0 = mt * TILE_M + static_cast<int>(rank) * (TILE_M / 2);
-        const int half = tile_rows(s_len[e], nt) / 2;
+        const int rows = tile_rows(s_len[e], nt);
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const uint32_t s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1u;
-          if (!mbar_wait_suspended(&empty_bar[s], ph ^ 1u, budget_ns, abort_flag)) {
+          ok = mbar_wait_suspended(&empty_bar[s], ph ^ 1u, budget_ns, abort_flag);
+          if (!ok) {
             fail();
-            ok = false;
             break;
           }
           if (leader) {
-            mbar_arrive_expect_tx(&full_bar[s], 2 * (C::A_BYTES + half * C::BKS * 2));
+            mbar_arrive_expect_tx(&full_bar[s], 2 * (C::A_BYTES + rows / 2 * C::BKS * 2));
             mbar_arrive(&full_bar[s]);
           }
           tma_load_5d_pair(smem + s * C::STAGE_BYTES, &tmA, full0 + s * 8, kb * C::BKS, 0, 0, m0 / 8, e);
         }
       }
-      // the even CTA's commits arrive on these barriers asynchronously: wait for the release of the last STAGES
-      // stages before the block can exit
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    // the even CTAs' commits arrive on these barriers asynchronously: wait for the release of the last STAGES stages,
+    // whose copies have landed then, before the block can exit
+    if (elect_one())
       for (uint32_t j = it; j < it + C::STAGES; ++j)
         if (!mbar_wait_suspended(&empty_bar[j % C::STAGES], ((j / C::STAGES) & 1u) ^ 1u, budget_ns, ok ? abort_flag : nullptr))
           break;
-    }
     __syncwarp();
   } else if (warp >= 2 + C::EPI_WARPS) {
     // ------------------------------------------------------------ gather
     // A gather takes its operands from uniform registers, so a warp's are issued one after the other, some 75 cycles
-    // each by as many lanes (150 by one lane with all the rows): four warps share a stage's 16.  Every warp has as
-    // many, at least one: a warp without a copy in a stage could fall behind the ring by a phase, whose parity it
-    // would take for another's.
+    // each by as many lanes (150 by one lane with all the rows).  Two warps share a stage's 16, the other two have the
+    // next stage's: four warps at every stage take 300 cycles for it and some 200 for the wait before, as long as the
+    // products (8192 tokens over 32 experts: up 470 thousand cycles instead of 411).  A tile's ids are loaded while the rows of the one before are gathered.
     const int g = warp - 2 - C::EPI_WARPS;
+    const uint32_t par = g & 1, part = g >> 1;
     const uint32_t full0 = mapa_shared(&full_bar[0], leader_rank);
     const uint16_t both = static_cast<uint16_t>(5u << rank);  // this CTA and its like in the other pair
-    uint32_t it = 0;
-    bool ok = true;
-    for (int tile = pair; tile < total_tiles && ok; tile += npairs) {
-      int e, nt, mt;
-      decode(tile, e, nt, mt);
-      const int start = s_start[e], len = s_len[e];
+    // this warp's gathers of a tile, one for each of its first n lanes, of the half that this pair gathers for both
+    int n = 0, id[4] = {0, 0, 0, 0};
+    auto first = [&](int n) { return (static_cast<int>(which) * 2 + static_cast<int>(part)) * n + lane; };  // in fours
+    auto look = [&](int tile) {
+      if (tile >= total_tiles) return;
+      int nt, mt;
+      decode(tile, nt, mt);
+      const int len = s_len[e];
       const int half = tile_rows(len, nt) / 2;
-      // this warp's gathers, one for each of its first n lanes, of the half that this pair gathers for both
-      const int n = half / 8 / C::GATHER_WARPS;
-      const int mine = (static_cast<int>(which) * C::GATHER_WARPS + g) * n + lane;  // of the CTA's half, in fours
-      int row[4] = {0, 0, 0, 0};
+      n = half / 16;
       if (lane < n) {
+        const int at = nt * C::BN + static_cast<int>(rank) * half + 4 * first(n);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // rows past the segment repeat its last one: computed for nothing, never stored
-          const int r = min(nt * C::BN + static_cast<int>(rank) * half + 4 * mine + i, len - 1);
-          const int u = __ldg(ids + start + r);
-          row[i] = u >= 0 && u < N ? u / div : 0;  // the epilogue flags a bad id and stores nothing for it
-        }
+        for (int i = 0; i < 4; ++i)  // rows past the segment repeat its last one: computed for nothing, never stored
+          id[i] = __ldg(ids + s_start[e] + min(at + i, len - 1));
       }
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t s = it % C::STAGES;
-        const uint32_t ph = (it / C::STAGES) & 1u;
+    };
+    uint32_t it0 = 0;
+    bool ok = true;
+    look(pair);
+    for (int tile = pair; tile < total_tiles && ok; tile += npairs, it0 += nkb) {
+      const bool mine = lane < n;
+      const uint32_t dst = C::A_BYTES + first(n) * 512;
+      int row[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // the epilogue flags a bad id and stores nothing for it
+        row[i] = id[i] >= 0 && id[i] < N ? id[i] / div : 0;
+      look(tile + npairs);
+      for (int kb = (it0 & 1u) != par ? 1 : 0; kb < nkb; kb += 2) {
+        const uint32_t s = (it0 + kb) % C::STAGES;
+        const uint32_t ph = ((it0 + kb) / C::STAGES) & 1u;
         if (!__all_sync(0xffffffffu, mbar_wait_suspended(&empty_bar[s], ph ^ 1u, budget_ns, abort_flag))) {
           if (lane == 0) fail();
           ok = false;
           break;
         }
-        if (lane < n)
-          tma_gather4_pair_multicast(smem + s * C::STAGE_BYTES + C::A_BYTES + mine * 512, &tmB, full0 + s * 8,
-                                     kb * C::BKS, row, both);
+        if (mine) tma_gather4_pair_multicast(smem + s * C::STAGE_BYTES + dst, &tmB, full0 + s * 8, kb * C::BKS, row, both);
         __syncwarp();
       }
     }
-    if (lane == 0) {  // as above: lets this warp's own copies land, too
-      for (uint32_t j = it; j < it + C::STAGES; ++j)
-        if (!mbar_wait_suspended(&empty_bar[j % C::STAGES], ((j / C::STAGES) & 1u) ^ 1u, budget_ns, ok ? abort_flag : nullptr))
-          break;
-    }
-    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
+    // One thread, whose own time has to stay short of the products' (a stage's four take 512 cycles, the tensor core
+    // holds only a few ahead): the warp finds the next tile's shape before it issues a tile.  (With the products issued
+    // by lane 0 after a wait of the whole warp and its vote: up of the same tokens 562 thousand cycles instead of 470.)
     uint32_t it = 0, acc_it = 0;
     bool ok = leader;
-    for (int tile = pair; tile < total_tiles && ok; tile += npairs) {
-      int e, nt, mt;
-      decode(tile, e, nt, mt);
-      const uint32_t idesc = idesc_bf16_f32(256, static_cast<uint32_t>(tile_rows(s_len[e], nt)), 0u, 0u);
+    int rows = 0;
+    auto look = [&](int tile) {
+      if (tile >= total_tiles) return;
+      int nt, mt;
+      decode(tile, nt, mt);
+      rows = tile_rows(s_len[e], nt);
+    };
+    look(pair);
+    for (int tile = pair; tile < total_tiles && ok; tile += npairs, ++acc_it) {
+      const uint32_t idesc = idesc_bf16_f32(256, static_cast<uint32_t>(rows), 0u, 0u);
+      look(tile + npairs);
       const uint32_t acc = acc_it & 1u;
-      const uint32_t aph = (acc_it >> 1) & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait_suspended<true>(&tempty_bar[acc], aph ^ 1u, budget_ns, abort_flag))) {
-        if (lane == 0) fail();
-        break;
-      }
-      tc_fence_after();
       const uint32_t d_tmem = tmem_base + acc * C::BN;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t s = it % C::STAGES;
-        const uint32_t ph = (it / C::STAGES) & 1u;
-        if (!__all_sync(0xffffffffu, mbar_wait_suspended(&full_bar[s], ph, budget_ns, abort_flag))) {
-          if (lane == 0) fail();
-          ok = false;
-          break;
-        }
+      if (elect_one()) {
+        ok = mbar_wait_suspended<true>(&tempty_bar[acc], ((acc_it >> 1) & 1u) ^ 1u, budget_ns, abort_flag);
         tc_fence_after();
-        if (lane == 0) {
+        for (int kb = 0; kb < nkb && ok; ++kb, ++it) {
+          const uint32_t s = it % C::STAGES;
+          ok = mbar_wait_suspended(&full_bar[s], (it / C::STAGES) & 1u, budget_ns, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
           const uint32_t a_addr = smem_u32(smem + s * C::STAGE_BYTES);
           const uint64_t adesc = smem_desc_sw128(a_addr, 16, 1024);
           const uint64_t bdesc = smem_desc_sw128(a_addr + C::A_BYTES, 16, 1024);
@@ -295,15 +298,15 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
             mma_bf16_ss_pair(d_tmem, adesc + kk * 2, bdesc + kk * 2, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
           mma_commit_pair_multicast(&empty_bar[s], 0xF);
         }
-        __syncwarp();
+        if (ok)
+          mma_commit_pair_multicast(&tfull_bar[acc], static_cast<uint16_t>(3u << leader_rank));
+        else
+          fail();
       }
-      if (!ok) break;
-      if (lane == 0) mma_commit_pair_multicast(&tfull_bar[acc], static_cast<uint16_t>(3u << leader_rank));
-      __syncwarp();
-      ++acc_it;
+      ok = __all_sync(0xffffffffu, ok);
     }
     if (leader) {
-      if (lane == 0) {
+      if (elect_one()) {
         mma_commit_pair_local(&drain_bar);
         if (!mbar_wait_suspended(&drain_bar, 0, budget_ns, nullptr)) raise_flag(status, LRM_ERR_TIMEOUT);
       }
@@ -323,8 +326,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     const uint32_t tempty0 = mapa_shared(&tempty_bar[0], leader_rank);
     uint32_t acc_it = 0;
     for (int tile = pair; tile < total_tiles; tile += npairs) {
-      int e, nt, mt;
-      decode(tile, e, nt, mt);
+      int nt, mt;
+      decode(tile, nt, mt);
       const int n_cols = tile_rows(s_len[e], nt);
       const int rows_valid = s_len[e] - nt * C::BN;  // pairs of this tile inside the segment
       int ids_of[CHUNKS];  // ids of pairs c_begin + 32 i + lane, -1: nothing to store

@@ -223,6 +223,15 @@ __device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t pari
   }
 }
 
+// One thread of the warp, the same at every call.  Operands that are the same for the whole warp reach an asynchronous
+// instruction issued under this condition in uniform registers; under `lane == 0` the compiler does not see that one
+// thread is left and goes round the threads for them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // After a wait of a block ran out: time for the copies and products that its threads have issued to end, a thousand
 // times what they take, before its shared memory and TMEM go to another block.
 __device__ __forceinline__ void let_copies_land() {
