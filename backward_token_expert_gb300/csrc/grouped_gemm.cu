@@ -534,7 +534,7 @@ struct CfgDgradPair {
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int T_PITCH = 32;  // bf16 per row of a warp's transpose buffer (64 B; 16-byte chunks XOR-swizzled)
-  static constexpr int WARP_BYTES = SWIGLU ? 8 * 32 * 4 : 32 * T_PITCH * 2;
+  static constexpr int WARP_BYTES = SWIGLU ? 16 * 32 * 4 : 32 * T_PITCH * 2;
   static constexpr int STAGING_BYTES = EPI_WARPS * WARP_BYTES;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024;
 };
@@ -548,12 +548,14 @@ struct SwigluArgs {
   int N, parts;
 };
 
-// SWIGLU: the epilogue of lrm_ffn_backward.  The product dphi stays in fp32: 8 rows of the warp's 32 columns at a time
+// SWIGLU: the epilogue of lrm_ffn_backward.  The product dphi stays in fp32: 16 rows of the warp's 32 columns at a time
 // are read back from its shared memory, so that a lane has 8 columns of a row in order and four lanes the 64 bytes
 // that a row of a, b and dh1 has there.  A chunk's a and b are loaded, through the selection, three chunks of 16 rows
 // before it is computed, and a tile's pair ids one tile before.  dh1 = [dphi b silu'(a) | dphi silu(a)] is rounded
-// once; the sums of dphi silu(a) b over 32 columns go to `partial`.  (Sixteen warps with less of a tile each: the same.
-// Without the reads of a and b the layer takes 217 us instead of 249, without the writes of dh1 218, without both 192.)
+// once; the sums of dphi silu(a) b over 32 columns go to `partial`.  The layer takes 245 us (8 rows at a time: 251,
+// sixteen warps with less of a tile each: the same, the products issued by an elected thread: the same; at 249 us,
+// without the reads of a and b 217, without the writes of dh1 218, without both 192): what the epilogue moves through
+// the L1 and the shared memory competes with the products' operands.
 template <int BNR, bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR, SWIGLU>::THREADS, 1)
     dgrad_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -825,7 +827,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR, SW
     auto tmem_of = [&](uint32_t acc) { return tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BNR; };
     if constexpr (SWIGLU) {
       constexpr int CHUNKS = SHARE / 16;
-      float* fbuf = reinterpret_cast<float*>(wbuf);  // [8 rows][32 columns], 16-byte chunks XOR-swizzled by row
+      float* fbuf = reinterpret_cast<float*>(wbuf);  // [16 rows][32 columns], 16-byte chunks XOR-swizzled by row
       const int sub = lane >> 2, quad = lane & 3;    // a step's row of eight, 8 columns of its 32
       // A tile as this warp sees it: its rows are c_begin .. c_end, those below `end` in the segment, row0 the compacted
       // row of the tile's first, ids[i] the pair of row c_begin + 32 i + lane, col0 the warp's first column.
@@ -890,43 +892,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR, SW
           tmem_ld_32x32b_x16(tmem_of(acc) + c, r);  // lane = I column, r[j] = output row c + j
           tmem_ld_wait();
           pin_registers(r);
+          __syncwarp();  // the reads of the 16 rows before are done
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            fbuf[j * 32 + ((((lane >> 2) ^ j) & 7) << 2) + (lane & 3)] = __uint_as_float(r[j]);
+          __syncwarp();
+          uint32_t da[2][4], db[2][4];
+          float dot[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            __syncwarp();  // the reads of the 8 rows before are done
+            F2 d[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              fbuf[j * 32 + ((((lane >> 2) ^ j) & 7) << 2) + (lane & 3)] = __uint_as_float(r[i * 8 + j]);
-            __syncwarp();
-            float d[8];
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-              *reinterpret_cast<float4*>(d + 4 * v) =
-                  *reinterpret_cast<const float4*>(fbuf + sub * 32 + (((quad * 2 + v) ^ sub) & 7) * 4);
+            for (int v = 0; v < 2; ++v) {
+              const float4 f =
+                  *reinterpret_cast<const float4*>(fbuf + (8 * i + sub) * 32 + (((quad * 2 + v) ^ sub) & 7) * 4);
+              d[2 * v] = F2(f.x, f.y);
+              d[2 * v + 1] = F2(f.z, f.w);
+            }
             const uint4 av = ga[buf][i], bv = gb[buf][i];
             const uint32_t aw[4] = {av.x, av.y, av.z, av.w}, bw[4] = {bv.x, bv.y, bv.z, bv.w};
-            uint32_t da[4], db[4];
-            float dot = 0.0f;
+            F2 sum(0.0f, 0.0f);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              float s0, s1;
-              const float g0 = silu_grad_fast(bf16_lo(aw[w]), s0), g1 = silu_grad_fast(bf16_hi(aw[w]), s1);
-              const float d0 = d[2 * w], d1 = d[2 * w + 1], b0 = bf16_lo(bw[w]), b1 = bf16_hi(bw[w]);
-              const float ds0 = d0 * s0, ds1 = d1 * s1;
-              da[w] = pack_bf16x2(d0 * b0 * g0, d1 * b1 * g1);
-              db[w] = pack_bf16x2(ds0, ds1);
-              dot = fmaf(ds0, b0, dot);
-              dot = fmaf(ds1, b1, dot);
+              F2 s;
+              const F2 b(bf16_lo(bw[w]), bf16_hi(bw[w]));
+              const F2 g = silu_grad2(F2(bf16_lo(aw[w]), bf16_hi(aw[w])), s);
+              const F2 ds = mul2(d[w], s);
+              da[i][w] = pack_bf16x2(mul2(mul2(d[w], b), g));
+              db[i][w] = pack_bf16x2(ds);
+              sum = fma2(ds, b, sum);
             }
-            dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-            dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+            dot[i] = sum.get().x + sum.get().y;
+          }
+#pragma unroll
+          for (int o = 1; o < 4; o *= 2)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], o);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
             if (pid[buf][i] >= 0 && fcol < I) {
               const size_t row = static_cast<size_t>(t.row0 + c + 8 * i + sub);
               uint16_t* orow = sw.dh1 + row * 2 * I + fcol;
-              *reinterpret_cast<uint4*>(orow) = make_uint4(da[0], da[1], da[2], da[3]);
-              *reinterpret_cast<uint4*>(orow + I) = make_uint4(db[0], db[1], db[2], db[3]);
-              if (sw.partial != nullptr && quad == 0) sw.partial[row * sw.parts + t.col0 / 32] = dot;
+              *reinterpret_cast<uint4*>(orow) = make_uint4(da[i][0], da[i][1], da[i][2], da[i][3]);
+              *reinterpret_cast<uint4*>(orow + I) = make_uint4(db[i][0], db[i][1], db[i][2], db[i][3]);
+              if (sw.partial != nullptr && quad == 0) sw.partial[row * sw.parts + t.col0 / 32] = dot[i];
             }
-          }
         }
         release(acc);
         t = next;
