@@ -398,7 +398,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
             uint32_t m[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
-              m[n] = pack_bf16x2(silu(val(hh, n, 0)) * val(hh, n, 2), silu(val(hh, n, 1)) * val(hh, n, 3));
+              m[n] = pack_bf16x2(mul2(silu2(F2(val(hh, n, 0), val(hh, n, 1))), F2(val(hh, n, 2), val(hh, n, 3))));
             stmatrix_x4_trans(at2(lane, hh), m);
           }
           __syncwarp();
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 3)
     if (lane != 0) continue;
     if (UP) {  // a of both features, then b
       *reinterpret_cast<uint32_t*>(out + static_cast<size_t>(u) * M + f) =
-          pack_bf16x2(silu(s[0]) * s[2], silu(s[1]) * s[3]);
+          pack_bf16x2(mul2(silu2(F2(s[0], s[1])), F2(s[2], s[3])));
       if (ab != nullptr) {
         uint16_t* o = ab + static_cast<size_t>(u) * 2 * M + f;
         *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(s[0], s[1]);

@@ -9,10 +9,6 @@
 
 namespace lrm {
 
-// One exponential and one quotient, both approximate: within (2 + |a|) 2^-22 of the value, relative, and 0 below
-// a = -87 (a value that would be smaller than 1e-36).
-__device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
-
 __device__ __forceinline__ float silu_grad(float a, float& silu) {
   const float s = 1.0f / (1.0f + expf(-a));
   silu = a * s;
@@ -36,6 +32,8 @@ __device__ __forceinline__ F2 sigmoid2(F2 a) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d.y));
   return F2(x, y);
 }
+
+__device__ __forceinline__ F2 silu2(F2 a) { return mul2(a, sigmoid2(a)); }
 
 // silu'(a) and silu(a) of two values, from those: within (2 + |a|) 2^-22 of 1 + |a|.
 __device__ __forceinline__ F2 silu_grad2(F2 a, F2& silu) {
