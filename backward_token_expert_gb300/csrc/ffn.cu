@@ -9,7 +9,7 @@
 // the weight and N = up to 256 pairs of the routing (fp32 accumulators in TMEM,
 // double-buffered), K blocks of 64; the two CTA pairs of a cluster take
 // neighbouring feature tiles of the same 256 routed pairs.  The routed pairs are
-// the N dimension because N is cut to multiples of 64 at a segment's end, where M
+// the N dimension because N is cut to multiples of 32 at a segment's end, where M
 // would be rounded up to 256.  Both operands are K-major:
 //   A  weight rows, one TMA box a CTA and stage.  Up interleaves eight gate rows
 //      with the eight up rows of the same features (a 5-D view of W1 does that in
@@ -21,7 +21,7 @@
 //      would take longer than its products (512 cycles): each CTA pair gathers
 //      half of them and multicasts it to both.
 //   warp 0        TMA producer of the weights
-//   warp 1        MMA issuer (even CTAs)
+//   warp 1        MMA issuer (even CTAs), one elected thread
 //   warps 2-9     epilogue, two a TMEM lane quarter, half of the tile's pairs
 //                 each: fragments of 8 features x 8 pairs are transposed by
 //                 stmatrix into shared memory, from where a pair's features are
@@ -29,13 +29,15 @@
 //                 operands take nearly all of the shared memory's bandwidth, 32
 //                 KB written and 32 KB read a stage, so the epilogue's share
 //                 costs products' time.)
-//   warps 10-13   TMA producers of the pairs' rows, a quarter of a CTA's each
-// Layer of 32768 x 8 pairs, h = 2048, I = 768: up 1.19 ms (1.39 PFLOP/s), down
-// 0.68 ms (1.22).  Clusters of one CTA pair: 1.25 and 0.70 ms; rows copied by
-// cp.async and handed over with a proxy fence: 2.4 and 1.7 ms; two blocks of M =
-// 256 over 128 pairs (half the gathers, but operands of N = 128 products need more
-// of the shared memory than it gives): 1.56 and 0.85 ms.  Without the epilogue the
-// two take 1.07 and 0.60 ms, without the gathers, too, 1.00 and 0.55.
+//   warps 10-13   TMA producers of the pairs' rows, two for the even stages and two
+//                 for the odd ones
+// Layer of 32768 x 8 pairs, h = 2048, I = 768: up 1.01 ms (1.64 PFLOP/s), down 0.61
+// to 0.67 ms (1.23 to 1.35), the clock at 1.7 to 1.85 GHz under the power cap.  Before
+// the elected issuer, with 1.19 and 0.68 ms: clusters of one CTA pair 1.25 and 0.70;
+// rows copied by cp.async and handed over with a proxy fence 2.4 and 1.7; two blocks
+// of M = 256 over 128 pairs (half the gathers, but operands of N = 128 products need
+// more of the shared memory than it gives) 1.56 and 0.85.  Without the epilogue the
+// two take 1.55 and 0.82 million cycles, with it 1.71 and 1.02.
 // Every wait is bounded as in the other grouped products (grouped_gemm.cu).
 #include <cuda_bf16.h>
 
@@ -440,11 +442,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
 // the rows 16 bytes at a time, K in steps of 256, with two steps in flight, and read the pair's row out of L1; the
 // sums are fp32 and are added over the lanes at the end.  Pairs of one expert read its weights again, out of the L2.
 
-// Measured against the tiles, up and down together, h = 2048, I = 768: 17.4 and 32.5 us for one token of 8 pairs over
-// 128 experts (3.9 + 7.4 us of reading at the HBM's rate), 37.9 and 51.6 for 32 pairs, 60.6 and 69.3 for 64, 82.8 and
-// 76.6 for 96; 25.5 and 26.8 for 32 pairs over 4 experts, 38.1 and 26.8 for 48.
-constexpr int FEW_PAIRS = 64;  // at most
-constexpr int FEW_ANYWAY = 32;  // also where several pairs are sure to share an expert
+// Measured against the tiles, up and down together, h = 2048, I = 768: 17.5 and 25.4 us for one token of 8 pairs over
+// 128 experts (3.9 + 7.4 us of reading at the HBM's rate), 25.5 and 34.8 for 16 pairs, 37.9 and 40.9 for 32, 60.6 and
+// 56.9 for 64; over 4 experts 18.0 and 19.1 for 16 pairs, 28.3 and 19.5 for 32.
+constexpr int FEW_PAIRS = 32;  // at most
+constexpr int FEW_ANYWAY = 16;  // also where several pairs are sure to share an expert
 constexpr int FEW_THREADS = 256;
 
 template <bool UP>

@@ -67,7 +67,10 @@ SHAPES = [  # T, E, k, h, I, skew, masked
     (900, 20, 3, 1032, 1000, 1.0, True), (700, 160, 6, 136, 264, 1.5, True), (2100, 3, 2, 64, 8, 0.3, False),
     (77, 16, 4, 8, 520, 1.0, False), (40, 1024, 32, 48, 24, 0.5, False), (513, 1, 1, 520, 776, 0.0, False),
     (64, 6, 2, 2048, 768, 0.5, False), (8, 128, 8, 264, 136, 0.5, False), (32, 2, 1, 1032, 520, 0.0, True),
-    (33, 2, 1, 72, 64, 0.0, False), (13, 64, 5, 2048, 40, 3.0, True)]
+    (33, 2, 1, 72, 64, 0.0, False), (13, 64, 5, 2048, 40, 3.0, True),
+    # the last sizes of the kernel for few pairs and the first beyond; several tiles a cluster of one and of three stages
+    (16, 2, 1, 136, 72, 0.0, False), (17, 2, 1, 136, 72, 0.0, True), (4, 32, 8, 136, 72, 1.0, False),
+    (6000, 40, 2, 64, 40, 0.3, False), (6000, 40, 2, 192, 136, 0.3, True)]
 
 
 @pytest.mark.parametrize("T,E,k,h,I,skew,masked", SHAPES)
