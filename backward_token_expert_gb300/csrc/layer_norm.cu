@@ -177,7 +177,8 @@ struct Block {
   __device__ __forceinline__ uint4 load(const T* base, uint32_t row, int i) const {
     if (vector(i) >= count) return make_uint4(0u, 0u, 0u, 0u);
     const long long e0 = at(row, column(i));
-    if (ALIGNED || (row > 0 && row < rows - 1) || (e0 >= 0 && e0 + N <= end()))
+    // of rows that fill a vector only the first and the last can reach beyond the tensor
+    if (ALIGNED || (width >= N && row > 0 && row < rows - 1) || (e0 >= 0 && e0 + N <= end()))
       return ld_stream(reinterpret_cast<const uint4*>(base + e0));
     uint32_t w[4] = {0u, 0u, 0u, 0u};  // reaches beyond the tensor
 #pragma unroll 1
