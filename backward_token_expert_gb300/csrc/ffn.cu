@@ -215,7 +215,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     // whose copies have landed then, before the block can exit
     if (elect_one())
       for (uint32_t j = it; j < it + C::STAGES; ++j)
-        if (!mbar_wait_suspended(&empty_bar[j % C::STAGES], ((j / C::STAGES) & 1u) ^ 1u, budget_ns, ok ? abort_flag : nullptr))
+        if (!mbar_wait_suspended(&empty_bar[j % C::STAGES], ((j / C::STAGES) & 1u) ^ 1u, budget_ns,
+                                 ok ? abort_flag : nullptr))
           break;
     __syncwarp();
   } else if (warp >= 2 + C::EPI_WARPS) {
@@ -223,7 +224,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     // A gather takes its operands from uniform registers, so a warp's are issued one after the other, some 75 cycles
     // each by as many lanes (150 by one lane with all the rows).  Two warps share a stage's 16, the other two have the
     // next stage's: four warps at every stage take 300 cycles for it and some 200 for the wait before, as long as the
-    // products (8192 tokens over 32 experts: up 470 thousand cycles instead of 411).  A tile's ids are loaded while the rows of the one before are gathered.
+    // products (8192 tokens over 32 experts: up 470 thousand cycles instead of 411).  A tile's ids are loaded while the
+    // rows of the one before are gathered.
     const int g = warp - 2 - C::EPI_WARPS;
     const uint32_t par = g & 1, part = g >> 1;
     const uint32_t full0 = mapa_shared(&full_bar[0], leader_rank);
@@ -264,7 +266,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
           ok = false;
           break;
         }
-        if (mine) tma_gather4_pair_multicast(smem + s * C::STAGE_BYTES + dst, &tmB, full0 + s * 8, kb * C::BKS, row, both);
+        if (mine)
+          tma_gather4_pair_multicast(smem + s * C::STAGE_BYTES + dst, &tmB, full0 + s * 8, kb * C::BKS, row, both);
         __syncwarp();
       }
     }

@@ -553,10 +553,10 @@ struct SwigluArgs {
 // that a row of a, b and dh1 has there.  A chunk's a and b are loaded, through the selection, three chunks of 16 rows
 // before it is computed, and a tile's pair ids one tile before.  dh1 = [dphi b silu'(a) | dphi silu(a)] is rounded
 // once; the sums of dphi silu(a) b over 32 columns go to `partial` (off by 1e-9 h, relative: the tensor core truncates at
-// each step of its fp32 sum).  The layer takes 245 us (8 rows at a time: 251,
-// sixteen warps with less of a tile each: the same, the products issued by an elected thread: the same; at 249 us,
-// without the reads of a and b 217, without the writes of dh1 218, without both 192): what the epilogue moves through
-// the L1 and the shared memory competes with the products' operands.
+// each step of its fp32 sum).  The layer takes 245 us (8 rows at a time 251; sixteen warps with less of a tile each, or
+// the products issued by an elected thread: the same; when it took 249, without the reads of a and b 217, without the
+// writes of dh1 218, without both 192): what the epilogue moves through the L1 and the shared memory competes with the
+// products' operands.
 template <int BNR, bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgDgradPair<BNR, SWIGLU>::THREADS, 1)
     dgrad_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,

@@ -654,8 +654,8 @@ LRM_API lrm_status lrm_dropout_add(lrm_ctx* ctx, const void* x, const void* resi
 LRM_API lrm_status lrm_get_device_status(lrm_ctx* ctx, void* stream, uint32_t* flags);
 
 /* Time limit, in nanoseconds, of every device-side wait of the grouped GEMM,
- * feed-forward, layer norm and clipping kernels (default 2e9).  A wait that runs out sets LRM_ERR_TIMEOUT and the
- * kernel winds down and returns. */
+ * feed-forward, layer norm and clipping kernels (default 2e9).  A wait that runs
+ * out sets LRM_ERR_TIMEOUT and the kernel winds down and returns. */
 LRM_API lrm_status lrm_set_wait_budget(lrm_ctx* ctx, uint64_t ns);
 
 /* Failure-detection self test: launch one block that waits, with the same
