@@ -447,18 +447,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
 // Few pairs (a token or a few): the products are bound by the bytes of the weights, and the tiles above leave half of
 // the SMs without one (48 tiles for eight pairs of 768 features) and spend their time in set-up and barriers.  Here a
 // warp takes four weight rows (up: gate and up of two features; down: four features) for one pair: its lanes stream
-// the rows 16 bytes at a time, K in steps of 256, with two steps in flight, and read the pair's row out of L1; the
-// sums are fp32 and are added over the lanes at the end.  Pairs of one expert read its weights again, out of the L2.
-
-// Measured against the tiles, up and down together, h = 2048, I = 768: 17.5 and 25.4 us for one token of 8 pairs over
-// 128 experts (3.9 + 7.4 us of reading at the HBM's rate), 25.5 and 34.8 for 16 pairs, 37.9 and 40.9 for 32, 60.6 and
-// 56.9 for 64; over 4 experts 18.0 and 19.1 for 16 pairs, 28.3 and 19.5 for 32.
+// the rows 16 bytes at a time, K in steps of 256, with two or three steps in flight, and read the pair's row out of L1;
+// the sums are fp32 and are added over the lanes at the end.  Pairs of one expert read its weights again, out of the L2.
+//
+// Measured against the tiles, up and down together, h = 2048, I = 768: 16.1 and 25.5 us for one token of 8 pairs over
+// 128 experts (7.4 + 3.7 us of reading at the HBM's rate), 24.8 and 34.6 for 16 pairs, 37.1 and 40.4 for 32, 59.9 and
+// 56.0 for 64; over 4 experts 17.9 and 19.1 for 16 pairs, 27.8 and 19.6 for 32.
 constexpr int FEW_PAIRS = 32;  // at most
 constexpr int FEW_ANYWAY = 16;  // also where several pairs are sure to share an expert
 constexpr int FEW_THREADS = 256;
 
 template <bool UP>
-__global__ void __launch_bounds__(FEW_THREADS, 3)
+__global__ void __launch_bounds__(FEW_THREADS, UP ? 3 : 2)
     ffn_few_kernel(const uint16_t* __restrict__ in, const uint16_t* __restrict__ weight,
                    const int32_t* __restrict__ offsets, const int32_t* __restrict__ ids, int E, int K, int M, int N,
                    int div, int max_rows, uint16_t* __restrict__ out, uint16_t* __restrict__ ab,
@@ -497,7 +497,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 3)
     F2 acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = F2(0.0f, 0.0f);
-    constexpr int STEPS = 2;  // of 32 vectors, in flight (four, with a third less blocks: the same)
+    // of 32 vectors, in flight (down of one token with two and three blocks an SM: 7.5 us instead of 6.4; up with four
+    // and two blocks: 10.5 instead of 9.9)
+    constexpr int STEPS = UP ? 2 : 3;
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
     for (int v = lane; v < kv; v += 32 * STEPS, w0 += 32 * STEPS, x0 += 32 * STEPS) {
       uint4 w[STEPS][4], x[STEPS];
