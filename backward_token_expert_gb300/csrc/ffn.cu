@@ -4,22 +4,19 @@
 //   y_t = sum over the k pairs u of t of alpha_u row_u (lrm_ffn_combine)
 // for the pairs u = t k + j of every expert's segment of `ids`.
 //
-// Both products are one kernel template: persistent clusters of four CTAs, two
-// pairs.  A pair's even CTA issues tcgen05.mma.cta_group::2 with M = 256 rows of
-// the weight and N = up to 256 pairs of the routing (fp32 accumulators in TMEM,
-// double-buffered), K blocks of 64; the two CTA pairs of a cluster take
-// neighbouring feature tiles of the same 256 routed pairs.  The routed pairs are
-// the N dimension because N is cut to multiples of 32 at a segment's end, where M
-// would be rounded up to 256.  Both operands are K-major:
+// Both products are one kernel template: persistent clusters of one CTA pair, whose
+// even CTA issues tcgen05.mma.cta_group::2 with M = 256 rows of the weight and N =
+// up to 256 pairs of the routing (fp32 accumulators in TMEM, double-buffered), K
+// blocks of 64.  The routed pairs are the N dimension because N is cut to multiples
+// of 32 at a segment's end, where M would be rounded up to 256.  Both operands are K-major:
 //   A  weight rows, one TMA box a CTA and stage.  Up interleaves eight gate rows
 //      with the eight up rows of the same features (a 5-D view of W1 does that in
 //      the box), so that a thread of the epilogue that reads TMEM in 16-lane
 //      fragments gets a and b of its features.
 //   B  the routed pairs' rows, gathered by their ids with gather4 TMA loads into
-//      the swizzled tile: x and phi are never copied into expert order.  A gather
-//      of four rows takes the TMA unit some 23 cycles, so that the 32 of a stage
-//      would take longer than its products (512 cycles): each CTA pair gathers
-//      half of them and multicasts it to both.
+//      the swizzled tile: x and phi are never copied into expert order.  The 32
+//      gathers of a CTA and stage take the TMA unit longer than its products' 512
+//      cycles (up of the layer: some 670 a stage), so they bound full tiles.
 //   warp 0        TMA producer of the weights
 //   warp 1        MMA issuer (even CTAs), one elected thread
 //   warps 2-9     epilogue, two a TMEM lane quarter, half of the tile's pairs
@@ -29,21 +26,20 @@
 //                 operands take nearly all of the shared memory's bandwidth, 32
 //                 KB written and 32 KB read a stage, so the epilogue's share
 //                 costs products' time.)
-//   warps 10-13   TMA producers of the pairs' rows, two for the even stages and two
-//                 for the odd ones
-// Layer of 32768 x 8 pairs, h = 2048, I = 768: up 1.01 ms (1.64 PFLOP/s), down 0.61
-// to 0.67 ms (1.23 to 1.35), the clock at 1.7 to 1.85 GHz under the power cap.  Before
-// the elected issuer, with 1.19 and 0.68 ms: clusters of one CTA pair 1.25 and 0.70;
-// rows copied by cp.async and handed over with a proxy fence 2.4 and 1.7; two blocks
-// of M = 256 over 128 pairs (half the gathers, but operands of N = 128 products need
-// more of the shared memory than it gives) 1.56 and 0.85.  Without the epilogue the
-// two take 1.55 and 0.82 million cycles, with it 1.71 and 1.02.
+//   warps 10-17   TMA producers of the pairs' rows, four for the even stages and
+//                 four for the odd ones
+// Layer of 32768 x 8 pairs, h = 2048, I = 768: up 1.07 to 1.10 ms (1.50 to 1.54 PFLOP/s), down
+// 0.65 to 0.72 ms (1.15 to 1.27), the clock at 1.7 to 1.85 GHz under the power cap.  Four
+// gather warps: 1.16 and 0.70 ms.  Rows copied by cp.async and handed over with a
+// proxy fence took 2.4 and 1.7 where gathers took 1.25 and 0.70; two blocks of M =
+// 256 over 128 pairs (half the gathers, but operands of N = 128 products need more
+// of the shared memory than it gives) 1.56 and 0.85.
 // Every wait is bounded as in the other grouped products (grouped_gemm.cu).
 //
 // Roundings to bf16: phi (the second product's operand, saved for the backward), the
 // pairs' rows and y.  y is off by 2.9e-3 of its size for it, sqrt(3) of one rounding.
 // Rows in fp32 would leave 2.3e-3 and double the bytes that down writes and combine
-// reads, 2 x 1.07 GB or 0.3 of the layer's 1.75 ms.
+// reads, 2 x 1.07 GB or 0.3 of the layer's 1.80 ms.
 #include <cuda_bf16.h>
 
 #include "f32x2.cuh"
@@ -64,16 +60,17 @@ struct CfgFfn {
   static constexpr int STAGES = 6;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int EPI_WARPS = 8;
-  static constexpr int GATHER_WARPS = 4;
+  static constexpr int GATHER_WARPS = 8;
   static constexpr int ROUND = 32;  // a tile's pairs are a multiple: each gather warp has four rows at least
   static constexpr int THREADS = 64 + 32 * EPI_WARPS + 32 * GATHER_WARPS;
   static constexpr int BUF_BYTES = 32 * 64;  // a warp's: 32 pairs, 32 bf16 values each
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * BUF_BYTES + 1024;
+  static_assert(ROUND % (4 * GATHER_WARPS) == 0, "half a tile is cut into the shares of half the gather warps, in fours");
   static_assert(ROUND % 32 == 0, "N of an M = 256 pair MMA is a multiple of 32");
 };
 
 template <bool UP>
-__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     ffn_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const int32_t* __restrict__ offsets, const int32_t* __restrict__ ids, int E, int K, int M, int N,
                int div, int max_rows, uint16_t* __restrict__ out, uint16_t* __restrict__ ab, unsigned int* status,
@@ -94,13 +91,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
   __shared__ int s_prefix[MAX_E + 1];  // first pair tile of each expert
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t crank = cluster_ctarank();
-  const uint32_t rank = crank & 1, which = crank >> 1;  // in the CTA pair, the pair in its cluster
-  const uint32_t leader_rank = crank & ~1u;
+  const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int pair = blockIdx.x >> 2, npairs = gridDim.x >> 2;  // clusters
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   constexpr int TILE_M = UP ? 128 : 256;  // features of a tile: up has a gate and an up row for each
-  const int tiles_m = (M + 2 * TILE_M - 1) / (2 * TILE_M);  // of both pairs
+  const int tiles_m = (M + TILE_M - 1) / TILE_M;
 
   if (tid == 0) {
     tma_prefetch_desc(&tmA);
@@ -108,7 +103,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     s_abort = 0;
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&full_bar[i], 2);  // both arrivals come from the even CTA's weight producer
-      mbar_init(&empty_bar[i], 2);  // both pairs' MMAs have read the stage
+      mbar_init(&empty_bar[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull_bar[i], 1);
@@ -175,7 +170,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     const int n_nt = (s_len[e] + C::BN - 1) / C::BN;
     mt = rem / n_nt;
     nt = rem - mt * n_nt;
-    mt = 2 * mt + static_cast<int>(which);
   };
   // pairs of a row tile that the MMA computes: the remainder rounded up
   auto tile_rows = [&](int len, int nt) {
@@ -185,7 +179,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ weights
-    const uint32_t full0 = mapa_shared(&full_bar[0], leader_rank);  // the even CTA's full barriers
+    const uint32_t full0 = mapa_shared(&full_bar[0], 0);  // the even CTA's full barriers
     uint32_t it = 0;
     bool ok = true;
     for (int tile = pair; tile < total_tiles && ok; tile += npairs) {
@@ -222,24 +216,22 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
   } else if (warp >= 2 + C::EPI_WARPS) {
     // ------------------------------------------------------------ gather
     // A gather takes its operands from uniform registers, so a warp's are issued one after the other, some 75 cycles
-    // each by as many lanes (150 by one lane with all the rows).  Two warps share a stage's 16, the other two have the
-    // next stage's: four warps at every stage take 300 cycles for it and some 200 for the wait before, as long as the
-    // products (8192 tokens over 32 experts: up 470 thousand cycles instead of 411).  A tile's ids are loaded while the
-    // rows of the one before are gathered.
+    // each by as many lanes (150 by one lane with all the rows).  Four warps share a stage's 32, the other four have the
+    // next stage's, so that a warp's wait falls into the time of the others' gathers (two at each: up of 65536 pairs 286
+    // us instead of 251).  A tile's ids are loaded while the rows of the one before are gathered.
     const int g = warp - 2 - C::EPI_WARPS;
     const uint32_t par = g & 1, part = g >> 1;
-    const uint32_t full0 = mapa_shared(&full_bar[0], leader_rank);
-    const uint16_t both = static_cast<uint16_t>(5u << rank);  // this CTA and its like in the other pair
-    // this warp's gathers of a tile, one for each of its first n lanes, of the half that this pair gathers for both
+    const uint32_t full0 = mapa_shared(&full_bar[0], 0);
+    // this warp's gathers of a tile, one for each of its first n lanes
     int n = 0, id[4] = {0, 0, 0, 0};
-    auto first = [&](int n) { return (static_cast<int>(which) * 2 + static_cast<int>(part)) * n + lane; };  // in fours
+    auto first = [&](int n) { return static_cast<int>(part) * n + lane; };  // in fours
     auto look = [&](int tile) {
       if (tile >= total_tiles) return;
       int nt, mt;
       decode(tile, nt, mt);
       const int len = s_len[e];
       const int half = tile_rows(len, nt) / 2;
-      n = half / 16;
+      n = half / (2 * C::GATHER_WARPS);
       if (lane < n) {
         const int at = nt * C::BN + static_cast<int>(rank) * half + 4 * first(n);
 #pragma unroll
@@ -267,7 +259,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
           break;
         }
         if (mine)
-          tma_gather4_pair_multicast(smem + s * C::STAGE_BYTES + dst, &tmB, full0 + s * 8, kb * C::BKS, row, both);
+          tma_gather4_pair(smem + s * C::STAGE_BYTES + dst, &tmB, full0 + s * 8, kb * C::BKS, row);
         __syncwarp();
       }
     }
@@ -306,10 +298,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
 #pragma unroll
           for (int kk = 0; kk < C::BKS / 16; ++kk)
             mma_bf16_ss_pair(d_tmem, adesc + kk * 2, bdesc + kk * 2, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_pair_multicast(&empty_bar[s], 0xF);
+          mma_commit_pair_multicast(&empty_bar[s]);
         }
         if (ok)
-          mma_commit_pair_multicast(&tfull_bar[acc], static_cast<uint16_t>(3u << leader_rank));
+          mma_commit_pair_multicast(&tfull_bar[acc]);
         else
           fail();
       }
@@ -333,7 +325,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
     // contiguous reads share banks
     auto at4 = [&](int row, int chunk) { return buf + row * 64 + ((chunk ^ (row >> 1)) & 3) * 16; };
     auto at2 = [&](int row, int chunk) { return buf + row * 32 + ((chunk ^ (row >> 2)) & 1) * 16; };
-    const uint32_t tempty0 = mapa_shared(&tempty_bar[0], leader_rank);
+    const uint32_t tempty0 = mapa_shared(&tempty_bar[0], 0);
     uint32_t acc_it = 0;
     for (int tile = pair; tile < total_tiles; tile += npairs) {
       int nt, mt;
@@ -633,7 +625,7 @@ lrm_status launch_ffn(lrm_ctx* ctx, const uint16_t* in, uint64_t in_rows, const 
     if (ctx->smem_optin < C::SMEM_BYTES + 14 * 1024) return LRM_ERR_ARCH;
     LRM_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctx->sm_count & ~3, 1, 1);
+    cfg.gridDim = dim3(ctx->sm_count & ~1, 1, 1);
     cfg.blockDim = dim3(C::THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     int n = 0;
@@ -646,7 +638,7 @@ lrm_status launch_ffn(lrm_ctx* ctx, const uint16_t* in, uint64_t in_rows, const 
   lrm_status st = encode_weight(ctx, &ma, weight, K, M, UP ? 2 : 1, d.E);
   if (st != LRM_OK) return st;
   if ((st = encode_2d(ctx, &mb, in, K, in_rows, 1)) != LRM_OK) return st;
-  return launch_dependent(kern, 4 * clusters, C::THREADS, C::SMEM_BYTES, 0, s, ma, mb, offsets, ids, d.E, K, M, N,
+  return launch_dependent(kern, 2 * clusters, C::THREADS, C::SMEM_BYTES, 0, s, ma, mb, offsets, ids, d.E, K, M, N,
                           UP ? d.k : 1, max_rows, out, ab, ctx->d_status, ctx->wait_budget_ns);
 }
 

@@ -310,16 +310,13 @@ __device__ __forceinline__ void tma_load_5d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// Four rows y[0..3] of a 2-D tensor (a map with boxes one row high), one after the other, written at the same offset of
-// every CTA in `mask` and counted on the barrier of the even CTA of each one's pair (bar_cluster: that of this CTA's own
-// pair).
-__device__ __forceinline__ void tma_gather4_pair_multicast(void* dst, const CUtensorMap* map, uint32_t bar_cluster,
-                                                           int32_t x, const int32_t (&y)[4], uint16_t mask) {
+// Four rows y[0..3] of a 2-D tensor (a map with boxes one row high), one after the other.
+__device__ __forceinline__ void tma_gather4_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int32_t x,
+                                                 const int32_t (&y)[4]) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".cta_group::2 [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
-      "h"(mask)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+      "{%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
       : "memory");
 }
 
@@ -478,9 +475,10 @@ __device__ __forceinline__ void mma_commit_pair_local(uint64_t* bar) {
                : "memory");
 }
 
-// Arrive once on `bar` (same offset) in the CTAs of `mask`, both of a cluster of
-// one pair, when the pair MMAs issued so far complete.
-__device__ __forceinline__ void mma_commit_pair_multicast(uint64_t* bar, uint16_t mask = 0x3) {
+// Arrive once on `bar` (same offset) in both CTAs of the pair when the pair
+// MMAs issued so far complete.
+__device__ __forceinline__ void mma_commit_pair_multicast(uint64_t* bar) {
+  const uint16_t mask = 0x3;
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
