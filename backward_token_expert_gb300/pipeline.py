@@ -847,9 +847,16 @@ class SublayerStep(TrainingStep):
         return self.drop.forward(y, self.out, x, stream)
 
     def backward(self, dout, x, W, W1, Wr, gamma, stream=None):
-        """For dout [T, h] bf16, the gradient of ``out``; x, W, W1 and gamma as in the forward, Wr [E, h] bf16."""
-        rec, r, f, b = self.rec, self.router, self.rec.fc1, self.rec.buf
+        """For dout [T, h] bf16, the gradient of ``out``; x, W [E, h, I], W1 [E, 2I, h] and gamma as in the
+        forward, Wr [E, h] bf16."""
+        rec = self.rec
         T, E, k, h, I = rec.T, rec.E, rec.k, rec.h, rec.I
+        # all of them before the first call: the products take shapes from the layer, not from the tensors
+        for name, t, shape in (("dout", dout, (T, h)), ("x", x, (T, h)), ("W", W, (E, h, I)), ("W1", W1, (E, 2 * I, h)),
+                               ("Wr", Wr, (E, h))):
+            _require(t, name, torch.bfloat16, shape, self.dWr.device)
+        _require(gamma, "gamma", torch.float32, (h,), self.dWr.device)
+        r, f, b = self.router, rec.fc1, rec.buf
         n, R = self.norm.y, rec.max_rows
         self.drop.backward(dout, self._g, stream)
         rec.score(self._g, self.ffn.phi, r.alpha, stream)
