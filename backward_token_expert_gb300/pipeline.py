@@ -754,6 +754,12 @@ class TrainingStep:
         # there on memory that they reuse, and their fills, do not come after another stream's step
         self.rec._dgate_buffer()
         self.clip = GradClip([self.rec.buf.dW, self.rec._fc1_buffers().dW1, self.dWr], ctx=self.rec.ctx)
+        self._streams = {torch.cuda.current_stream(dev).cuda_stream}
+
+    def _held(self):
+        rec = self.rec
+        held = (*vars(rec.buf).values(), *vars(rec.fc1).values(), rec.dgate, self.dWr, self.dxr, self._segment)
+        return held if self._x is None else (*held, self._x)
 
     def route(self, logits, valid=None, stream=None):
         """Ids and gates of the batch (``router.expert_idx``, ``router.alpha``) and its losses.  The tokens
@@ -764,6 +770,8 @@ class TrainingStep:
             self._x = torch.empty(self.rec.T, self.rec.h, dtype=torch.bfloat16, device=self.dWr.device)
             if not torch.cuda.is_current_stream_capturing():  # work on what the memory held before may be pending
                 torch.cuda.current_stream(self._x.device).synchronize()
+            self._streams = {torch.cuda.current_stream(self._x.device).cuda_stream}  # the others do not know it yet
+        _stream_of(self, stream)
         self.router.forward(logits, valid, stream)
 
     def backward(self, logits, g, phi, W, x, ab, W1, Wr, stream=None):
@@ -772,6 +780,7 @@ class TrainingStep:
         output of every pair, x [T, h] the layer's input (bf16); W [E, h, I],
         W1 [E, 2I, h], Wr [E, h] the weights (bf16)."""
         rec, r = self.rec, self.router
+        _stream_of(self, stream)
         rec.run(logits, r.expert_idx, g, phi, r.alpha, W, stream, counted=r.counted)
         rec.gate_grad(stream)
         rec.fc1_backward(x, ab, W1, stream)
@@ -829,6 +838,9 @@ class SublayerStep(TrainingStep):
         self.clip.close()
         self.clip = GradClip([rec.buf.dW, rec.fc1.dW1, self.dWr, self.norm.dgamma, self.norm.dbeta], ctx=ctx)
 
+    def _held(self):
+        return *super()._held(), self.out, self._g, self._dn, self._side, self._ws
+
     def normalize(self, x, gamma, beta, valid=None, stream=None):
         """The layer norm of x [T, h] bf16; rows that `valid` leaves out become zeros."""
         self._valid = valid
@@ -843,6 +855,7 @@ class SublayerStep(TrainingStep):
     def experts(self, x, W1, W, stream=None):
         """out = x + dropout(y), y the gated sum of the experts' outputs for the normalised rows."""
         b = self.rec.buf
+        _stream_of(self, stream)
         y = self.ffn.forward(self.norm.y, W1, W, b.offsets, b.bucket[: self.rec.N], self.router.alpha, stream)
         return self.drop.forward(y, self.out, x, stream)
 
@@ -856,6 +869,7 @@ class SublayerStep(TrainingStep):
                                ("Wr", Wr, (E, h))):
             _require(t, name, torch.bfloat16, shape, self.dWr.device)
         _require(gamma, "gamma", torch.float32, (h,), self.dWr.device)
+        _stream_of(self, stream)
         r, f, b = self.router, rec.fc1, rec.buf
         n, R = self.norm.y, rec.max_rows
         self.drop.backward(dout, self._g, stream)

@@ -44,3 +44,46 @@ def test_a_refused_backward_leaves_the_step_as_it_was():
         assert _same(_results(step), want) and step.device_status() == 0
     finally:
         step.close()
+
+
+@pytest.mark.parametrize("kind", ["TrainingStep", "SublayerStep"])
+def test_memory_of_a_dropped_step_stays_until_its_stream_is_done(kind):
+    # the allocator learns of another stream that works on a step's buffers: none of them is given away meanwhile
+    from backward_token_expert_gb300 import pipeline as P
+
+    T, E, k, h, I = 50, 8, 2, 64, 32
+    d = {n: t.cuda() for n, t in _inputs(T, E, h, I, 5).items()}
+    logits = torch.randn(T, E, device="cuda")
+    phi, ab = torch.randn(T * k, I, device="cuda").bfloat16(), torch.randn(T * k, 2 * I, device="cuda").bfloat16()
+    step = getattr(P, kind)(T, E, k, h, I)
+    rec = step.rec  # kept: its context goes with it, which waits for the GPU
+    held = [*vars(rec.buf).values(), *vars(rec.fc1).values(), rec.dgate, step.dWr, step.dxr, step._segment]
+    if kind == "SublayerStep":
+        held += [step.out, step._g, step._dn, step._side, step._ws]
+    own = {t.data_ptr(): t.numel() * t.element_size() for t in held}
+    assert len(own) == len(held)
+
+    def run(stream):
+        if kind == "SublayerStep":
+            step.normalize(d["x"], d["gamma"], d["beta"], stream=stream)
+            step.route(logits, stream=stream)
+            step.experts(d["x"], d["W1"], d["W"], stream)
+            step.backward(d["dout"], d["x"], d["W"], d["W1"], d["Wr"], d["gamma"], stream)
+        else:
+            step.route(logits, stream=stream)
+            step.backward(logits, d["dout"], phi, d["W"], d["x"], ab, d["W1"], d["Wr"], stream)
+
+    run(None)  # the kernels' first launches, which wait for the GPU
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(1_000_000_000)
+    run(s)
+    rec.buf = rec.fc1 = rec.dgate = held = None
+    del step, run
+    others = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in own.values() for _ in range(24)]
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in others]
+    assert not s.query()  # still asleep, the step behind it
+    assert not [at for at in own if any(a <= at < b for a, b in spans)]
+    s.synchronize()
+    assert rec.device_status() == 0
