@@ -339,6 +339,15 @@ def _stream_of(owner, stream):
     return raw
 
 
+def _keep(buffer, t, stream):
+    """A copy of `t` in `buffer`, on `stream` (a torch stream, a raw handle or None)."""
+    if isinstance(stream, int):  # 0, the default stream's handle, would stand for a new stream
+        dev = buffer.device
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):  # None: as it is
+        buffer.copy_(t)
+
+
 class Router:
     """The router of one layer shape through the C ABI: gates and balance loss
     of a batch of logits (lrm_router_forward) and the logits' gradient
@@ -817,7 +826,9 @@ class SublayerStep(TrainingStep):
     In the backward, lrm_ffn_backward takes the retained pairs from their output
     gradients to the first projections' and the gates' in one product.  Weight
     gradients: ``rec.buf.dW``, ``rec.fc1.dW1``, ``dWr``, ``norm.dgamma`` and
-    ``norm.dbeta``.  ``drop.advance()`` draws a new mask for the next step."""
+    ``norm.dbeta``.  ``drop.advance()`` draws a new mask for the next step, not
+    before this one's backward.  The logits and `valid` are copied: their buffers
+    may be another layer's by the time of the backward."""
 
     def __init__(self, T, E, k, h, I, cf=Fraction(5, 4), rho=Fraction(3, 4), aux_coef: float = 0.01,
                  z_coef: float = 0.001, max_norm: float = 1.0, p: float = 0.0, seed: int = 0, eps: float = 1e-5,
@@ -834,22 +845,30 @@ class SublayerStep(TrainingStep):
         self._side = torch.empty(max(rec.max_rows, 1), 8, **bf)  # second operand of a compaction that has only one
         need = L.lrm_ffn_backward_workspace(ctx, rec.dims, rec.max_rows)
         self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        self._logits = self._valid = None
+        # what the backward reads of the forward's inputs: the caller's buffers may hold another layer's by then
+        self._logits = torch.empty(T, E, dtype=torch.float32, device=dev)
+        self._valid = torch.empty(T, dtype=torch.uint8, device=dev)
+        self._padded = self._routed = False
         self.clip.close()
         self.clip = GradClip([rec.buf.dW, rec.fc1.dW1, self.dWr, self.norm.dgamma, self.norm.dbeta], ctx=ctx)
 
     def _held(self):
-        return *super()._held(), self.out, self._g, self._dn, self._side, self._ws
+        return *super()._held(), self.out, self._g, self._dn, self._side, self._ws, self._logits, self._valid
 
     def normalize(self, x, gamma, beta, valid=None, stream=None):
         """The layer norm of x [T, h] bf16; rows that `valid` leaves out become zeros."""
-        self._valid = valid
-        return self.norm.forward(x, gamma, beta, valid, stream)
+        _stream_of(self, stream)
+        self.norm.forward(x, gamma, beta, valid, stream)
+        self._padded = valid is not None
+        if self._padded:
+            _keep(self._valid, valid, stream)
+        return self.norm.y
 
     def route(self, logits, valid=None, stream=None):
         """As in TrainingStep (`valid` as given to ``normalize``), and the routed pairs by expert."""
         super().route(logits, valid, stream)
-        self._logits = logits
+        _keep(self._logits, logits, stream)
+        self._routed = True
         self.rec.route_stats(logits, self.router.expert_idx, stream, counted=self.router.counted)
 
     def experts(self, x, W1, W, stream=None):
@@ -864,6 +883,8 @@ class SublayerStep(TrainingStep):
         forward, Wr [E, h] bf16."""
         rec = self.rec
         T, E, k, h, I = rec.T, rec.E, rec.k, rec.h, rec.I
+        if not self._routed:
+            raise ValueError("the backward of a batch needs its forward")
         # all of them before the first call: the products take shapes from the layer, not from the tensors
         for name, t, shape in (("dout", dout, (T, h)), ("x", x, (T, h)), ("W", W, (E, h, I)), ("W1", W1, (E, 2 * I, h)),
                                ("Wr", Wr, (E, h))):
@@ -890,7 +911,7 @@ class SublayerStep(TrainingStep):
         L.lrm_grouped_dgrad(rec.ctx, r.dlogits, Wr, self._segment, self._dims_r, T, self.dxr, stream)
         # the two gradients of n, through the experts and through the router
         L.lrm_dropout_add(rec.ctx, f.dx, self.dxr, L.DTYPE_BF16, T * h, 0.0, 0, 0, None, self._dn, stream)
-        self.norm.backward(x, self._dn, gamma, self._valid, dout, stream)
+        self.norm.backward(x, self._dn, gamma, self._valid if self._padded else None, dout, stream)
         self.clip.clip(self.max_norm, stream)
         return self.norm.dx
 

@@ -87,3 +87,57 @@ def test_memory_of_a_dropped_step_stays_until_its_stream_is_done(kind):
     assert not [at for at in own if any(a <= at < b for a, b in spans)]
     s.synchronize()
     assert rec.device_status() == 0
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("how", ["current", "stream", "raw", "default"])
+def test_two_layers_forward_then_backward_with_buffers_in_common(masked, how):
+    # a model's layers run forward one after the other through one buffer of logits and one mask, which hold the next
+    # layer's, or the next batch's, by the time of the backward
+    from backward_token_expert_gb300.pipeline import SublayerStep
+
+    T, E, k, h, I = 120, 8, 2, 64, 32
+    d = [{n: t.cuda() for n, t in _inputs(T, E, h, I, seed).items()} for seed in (6, 7)]
+    masks = [(torch.arange(T, device="cuda") % m != 0).to(torch.uint8) for m in (3, 5)] if masked else [None, None]
+    steps = [SublayerStep(T, E, k, h, I, p=0.2, seed=seed) for seed in (1, 2)]
+    try:
+        want = []
+        for step, v, m in zip(steps, d, masks):
+            _enqueue(step, v, torch.empty(T, E, device="cuda"), m)
+            want.append(_results(step))
+        side = torch.cuda.Stream()
+        stream = dict(current=None, stream=side, raw=side.cuda_stream, default=0)[how]
+        logits, mask = torch.empty(T, E, device="cuda"), torch.empty(T, dtype=torch.uint8, device="cuda")
+        mask = mask if masked else None
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side if how in ("stream", "raw") else torch.cuda.default_stream()):
+            for step, v, m in zip(steps, d, masks):
+                if masked:
+                    mask.copy_(m)
+                n = step.normalize(v["x"], v["gamma"], v["beta"], mask, stream)
+                torch.matmul(n.float(), v["Wr"].float().T, out=logits)
+                step.route(logits, mask, stream)
+                step.experts(v["x"], v["W1"], v["W"], stream)
+            logits.fill_(float("nan"))
+            if masked:
+                mask.fill_(0)
+            for step, v in zip(steps[::-1], d[::-1]):
+                step.backward(v["dout"], v["x"], v["W"], v["W1"], v["Wr"], v["gamma"], stream)
+        for step, w in zip(steps, want):
+            assert _same(_results(step), w) and step.device_status() == 0
+    finally:
+        for step in steps:
+            step.close()
+
+
+def test_a_backward_of_nothing_is_refused():
+    from backward_token_expert_gb300.pipeline import SublayerStep
+
+    T, E, k, h, I = 16, 8, 2, 64, 32
+    d = {n: t.cuda() for n, t in _inputs(T, E, h, I, 8).items()}
+    step = SublayerStep(T, E, k, h, I)
+    try:
+        with pytest.raises(ValueError):
+            step.backward(d["dout"], d["x"], d["W"], d["W1"], d["Wr"], d["gamma"])
+    finally:
+        step.close()

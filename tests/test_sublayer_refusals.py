@@ -21,6 +21,7 @@ def step(monkeypatch):
     s = SublayerStep.__new__(SublayerStep)
     s.rec = SimpleNamespace(T=T, E=E, k=k, h=h, I=I, N=T * k, buf=None, fc1=None, max_rows=T * k, ctx=None)
     s.dWr = torch.zeros(E, h)
+    s._routed = True
     return s
 
 
