@@ -866,7 +866,8 @@ class SublayerStep(TrainingStep):
 
     def route(self, logits, valid=None, stream=None):
         """As in TrainingStep (`valid` as given to ``normalize``), and the routed pairs by expert."""
-        super().route(logits, valid, stream)
+        _stream_of(self, stream)
+        self.router.forward(logits, valid, stream)  # padding needs no more here: its rows of n are zeros
         _keep(self._logits, logits, stream)
         self._routed = True
         self.rec.route_stats(logits, self.router.expert_idx, stream, counted=self.router.counted)

@@ -141,3 +141,27 @@ def test_a_backward_of_nothing_is_refused():
             step.backward(d["dout"], d["x"], d["W"], d["W1"], d["Wr"], d["gamma"])
     finally:
         step.close()
+
+
+def test_a_masked_batch_makes_no_buffer_and_waits_for_nothing():
+    # every buffer is there from the start: a masked route in the middle of a step's launches does not stop the host
+    from backward_token_expert_gb300.pipeline import SublayerStep
+
+    T, E, k, h, I = 64, 8, 2, 64, 32
+    d = {n: t.cuda() for n, t in _inputs(T, E, h, I, 9).items()}
+    valid = (torch.arange(T, device="cuda") % 4 != 0).to(torch.uint8)
+    step, logits = SublayerStep(T, E, k, h, I), torch.randn(T, E, device="cuda")
+    try:
+        step.normalize(d["x"], d["gamma"], d["beta"], valid)  # the first launches wait for the GPU
+        step.route(logits)
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda._sleep(500_000_000)
+        step.normalize(d["x"], d["gamma"], d["beta"], valid)
+        step.route(logits, valid)
+        assert not torch.cuda.current_stream().query()  # still asleep
+        assert torch.cuda.memory_allocated() == before
+        torch.cuda.synchronize()
+        assert step.device_status() == 0 and int(step.router.tokens) == int(valid.sum())
+    finally:
+        step.close()
