@@ -205,6 +205,21 @@ struct Block {
   __device__ static __forceinline__ uint4 both(const uint4& a, const uint4& b) {
     return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
   }
+  // zeros for the elements of vector i that are not the row's own
+  __device__ __forceinline__ void zero_outside(F2 (&f)[N / 2], int i) const {
+    if (ALIGNED && vector(i) >= count) {
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) f[j] = F2(0.0f, 0.0f);
+    }
+    if (edge(i)) {
+      const uint32_t mine = own(i);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        const float2 v = f[j].get();
+        f[j] = F2(mine >> (2 * j) & 1u ? v.x : 0.0f, mine >> (2 * j + 1) & 1u ? v.y : 0.0f);
+      }
+    }
+  }
   // zeros for a row that does not count
   __device__ __forceinline__ void store(T* base, uint32_t row, int i, const F2 (&f)[N / 2], bool counted) const {
     if (vector(i) >= count) return;
@@ -355,18 +370,7 @@ __global__ void __maxnreg__(HOLD ? FWD_REGS<T> : 128)
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int j = 0; j < P; ++j) f[i][j] = add2(f[i][j], minus);
-      if (ALIGNED && b.vector(i) >= b.count) {
-#pragma unroll
-        for (int j = 0; j < P; ++j) f[i][j] = F2(0.0f, 0.0f);
-      }
-      if (b.edge(i)) {
-        const uint32_t own = b.own(i);
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          const float2 v = f[i][j].get();
-          f[i][j] = F2(own >> (2 * j) & 1u ? v.x : 0.0f, own >> (2 * j + 1) & 1u ? v.y : 0.0f);
-        }
-      }
+      b.zero_outside(f[i], i);
 #pragma unroll
       for (int j = 0; j < P; ++j) acc = fma2(f[i][j], f[i][j], acc);
     }
@@ -500,7 +504,8 @@ __global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
 #pragma unroll
       for (int i = 0; i < NV; ++i) xr[i] = nx[i], yr[i] = ny[i], rr[i] = RES ? nr[i] : none;
     }
-    // xhat and dy of vector i; the elements that are not the row's own have dy = 0 and add nothing
+    // xhat and dy of vector i, zeros where they are not the row's own: -mean rstd, what xhat would be there, may be
+    // infinite where the row's own values are not
     const F2 minus(-mu, -mu), scale(rs, rs);
     auto values = [&](int i, F2 (&vx)[P], F2 (&vy)[P]) {
       const int k = HOLD ? i : 0;
@@ -512,6 +517,7 @@ __global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
       Vec<T>::unpack(b.clean(yr[k], i), vy);
 #pragma unroll
       for (int j = 0; j < P; ++j) vx[j] = mul2(add2(vx[j], minus), scale);
+      b.zero_outside(vx, i);
     };
     F2 vx[HV][P], vd[HV][P];  // HOLD: xhat and d, kept for the second pass
     F2 s0(0.0f, 0.0f), s1(0.0f, 0.0f);
