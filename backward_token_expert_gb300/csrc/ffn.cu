@@ -442,12 +442,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CfgFfn::THREADS, 1)
 // the rows 16 bytes at a time, K in steps of 256, with two or three steps in flight, and read the pair's row out of L1;
 // the sums are fp32 and are added over the lanes at the end.  Pairs of one expert read its weights again, out of the L2.
 //
-// Measured against the tiles, up and down together, h = 2048, I = 768: 16.1 and 25.5 us for one token of 8 pairs over
-// 128 experts (7.4 + 3.7 us of reading at the HBM's rate), 24.8 and 34.6 for 16 pairs, 37.1 and 40.4 for 32, 59.9 and
-// 56.0 for 64; over 4 experts 17.9 and 19.1 for 16 pairs, 27.8 and 19.6 for 32.
+// Measured against the tiles, up and down together, us.  Pairs of one expert cost its bytes once more each, at some 18
+// TB/s out of the L2 (an expert of h = 2048, I = 768 has 9.4 MB, of 5120, 1536 47 MB); the tiles cost their set-up, some
+// 9 to 14 more than the bytes.
+//   pairs spread over          1 expert       2              4              8              128
+//   2048, 768:    8 pairs   11.3 | 16.9   11.4 | 17.3   12.4 | 18.3   16.2 | 22.4   17.0 | 23.3
+//                16         15.6 | 16.9   16.0 | 17.4   17.2 | 18.4   20.2 | 22.4   27.8 | 37.1
+//                24         21.0 | 16.9   21.2 | 17.5   22.2 | 18.5   24.8 | 22.6   38.3 | 45.0
+//                32         26.1 | 17.0   26.2 | 17.5   26.9 | 18.5   28.9 | 22.7   48.6 | 57.4
+//   5120, 1536:   4         21.5 | 29.0   23.2 | 31.6   32.9 | 45.0   33.8 | 45.0   33.9 | 44.8
+//                 8         31.2 | 29.1   33.7 | 31.9   41.4 | 45.1   58.5 | 77.8   60.0 | 77.8
+//                12         42.5 | 29.0   46.1 | 31.9   51.9 | 45.5   66.1 | 77.6   85.8 | 97.9
+//                16         53.8 | 29.0   57.2 | 31.6   63.9 | 45.6   75.5 | 78.0    112 | 127
+//   1024, 512:   16          9.1 | 13.1    9.4 | 13.5   10.0 | 13.9   11.4 | 14.7   14.4 | 18.0
+// The call knows the pairs' number and the experts', not who shares one: with 16 pairs of 128 experts all on one the
+// first line's times hold.
 constexpr int FEW_PAIRS = 32;  // at most
-constexpr int FEW_ANYWAY = 16;  // also where several pairs are sure to share an expert
+constexpr int FEW_ANYWAY = 16;  // also where several pairs are sure to share an expert, up to the bytes read again of
+constexpr int FEW_SHARED = 3;    // pairs and
+constexpr long long FEW_SHARED_BYTES = 120ll << 20;  // more
 constexpr int FEW_THREADS = 256;
+
+// Whether a call of max_rows pairs takes the kernel for few of them: both products, by their weights together.
+bool few_pairs(const lrm_dims& d, int max_rows) {
+  if (max_rows <= d.E) return max_rows <= FEW_PAIRS;
+  const long long expert = 3ll * d.h * d.I * sizeof(uint16_t);
+  return max_rows <= FEW_ANYWAY && (max_rows - d.E - FEW_SHARED) * expert <= FEW_SHARED_BYTES;
+}
 
 template <bool UP>
 __global__ void __launch_bounds__(FEW_THREADS, UP ? 3 : 2)
@@ -606,7 +627,7 @@ lrm_status launch_ffn(lrm_ctx* ctx, const uint16_t* in, uint64_t in_rows, const 
                       uint16_t* ab, cudaStream_t s) {
   using C = CfgFfn;
   const int K = UP ? d.h : d.I, M = UP ? d.I : d.h, N = d.T * d.k;
-  if (max_rows <= FEW_ANYWAY || (max_rows <= FEW_PAIRS && max_rows <= d.E)) {
+  if (few_pairs(d, max_rows)) {
     auto few = ffn_few_kernel<UP>;
     static thread_local int few_device = -1, grid = 0;
     if (few_device != ctx->device) {
