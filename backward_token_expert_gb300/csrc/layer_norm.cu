@@ -262,7 +262,6 @@ struct Ring {
   uint64_t* bars;
   int depth, stride;  // rows; bytes of an array's row
   const T* src[A];
-  const uint8_t* valid;
   unsigned int* status;
   unsigned long long budget_ns;
 
@@ -470,8 +469,8 @@ __global__ void __maxnreg__(MODE != WIDE ? BWD_REGS<T> : 128)
       }
     }
   };
-  Ring<T, RES ? 3 : 2> ring{reinterpret_cast<uint8_t*>(s_dyn), s_bars, args.depth, b.count * 16, {x, dy}, valid,
-                            args.status, args.budget_ns};
+  Ring<T, RES ? 3 : 2> ring{reinterpret_cast<uint8_t*>(s_dyn), s_bars, args.depth, b.count * 16, {x, dy}, args.status,
+                            args.budget_ns};
   if constexpr (RES) ring.src[2] = dres;
   uint32_t row = b.first();
   bool ahead = false;  // RING, the first thread: whether the row after those on their way counts
