@@ -10,7 +10,9 @@
 // registers).  The round keys come with the launch; what the block's counters have
 // in common in rounds 1 and 2 is computed once.  67108864 elements: fp32 82 us
 // (0.96 of the HBM's rate), bf16 with a residual 64 us (0.93), bf16 alone, where
-// eight elements move only 32 bytes, 56 us (0.70): the integer pipe bounds that.
+// eight elements move only 32 bytes, 56 us (0.70).  There no unit is full: the pipe
+// of the wide products is busy for 65 % of the cycles, the ALU 58, issue 57, DRAM
+// 47; a thread's loads, draws and stores follow one another.
 #include "lrm_internal.cuh"
 #include "vec.cuh"
 

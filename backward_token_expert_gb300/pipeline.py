@@ -573,7 +573,9 @@ class Dropout(_Operator):
     """Dropout with a residual (lrm_dropout_add): the mask is drawn from `seed`,
     `offset` and the device counter ``step`` and never stored.  ``backward`` draws
     that of the last ``forward`` again as long as ``step`` is the same;
-    ``advance`` counts it up (also in a captured graph)."""
+    ``advance`` counts it up (also in a captured graph).  Every layer needs a
+    `seed` of its own: `offset` and ``step`` are added up, so that offsets one apart
+    under one seed draw each other's masks a step later."""
 
     def __init__(self, p: float, seed: int = 0, offset: int = 0, device=0, ctx=None):
         if not 0.0 <= float(p) <= 1.0:
@@ -827,7 +829,7 @@ class SublayerStep(TrainingStep):
     gradients to the first projections' and the gates' in one product.  Weight
     gradients: ``rec.buf.dW``, ``rec.fc1.dW1``, ``dWr``, ``norm.dgamma`` and
     ``norm.dbeta``.  ``drop.advance()`` draws a new mask for the next step, not
-    before this one's backward.  The logits and `valid` are copied: their buffers
+    before this one's backward; every layer needs a `seed` of its own.  The logits and `valid` are copied: their buffers
     may be another layer's by the time of the backward."""
 
     def __init__(self, T, E, k, h, I, cf=Fraction(5, 4), rho=Fraction(3, 4), aux_coef: float = 0.01,

@@ -637,7 +637,8 @@ LRM_API lrm_status lrm_layer_norm_backward(lrm_ctx* ctx, const void* x, int32_t 
  * word i mod 4 of Philox4x32-10 (Salmon et al., SC 2011) with the 64-bit key `seed`
  * and the counter (i div 4, offset + *step), low words first, is below floor(p 2^32).
  * The backward is the same call on the output's gradient, without a residual.  A
- * dropped element adds nothing, whatever x holds there.
+ * dropped element adds nothing, whatever x holds there.  Every layer needs a seed of
+ * its own: under one seed, offsets one apart draw each other's masks a step later.
  *   x, out    [n] fp32 or bf16 (dtype); residual likewise or NULL.  out may be x or
  *             residual itself, else it overlaps neither.
  *   p         0 <= p <= 1; p = 1 drops everything
