@@ -829,8 +829,9 @@ class SublayerStep(TrainingStep):
     gradients to the first projections' and the gates' in one product.  Weight
     gradients: ``rec.buf.dW``, ``rec.fc1.dW1``, ``dWr``, ``norm.dgamma`` and
     ``norm.dbeta``.  ``drop.advance()`` draws a new mask for the next step, not
-    before this one's backward; every layer needs a `seed` of its own.  The logits and `valid` are copied: their buffers
-    may be another layer's by the time of the backward."""
+    before this one's backward; every layer needs a `seed` of its own.  The logits
+    and `valid` are copied: their buffers may be another layer's by the time of
+    the backward."""
 
     def __init__(self, T, E, k, h, I, cf=Fraction(5, 4), rho=Fraction(3, 4), aux_coef: float = 0.01,
                  z_coef: float = 0.001, max_norm: float = 1.0, p: float = 0.0, seed: int = 0, eps: float = 1e-5,

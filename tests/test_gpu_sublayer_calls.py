@@ -150,10 +150,11 @@ def test_a_masked_batch_makes_no_buffer_and_waits_for_nothing():
     T, E, k, h, I = 64, 8, 2, 64, 32
     d = {n: t.cuda() for n, t in _inputs(T, E, h, I, 9).items()}
     valid = (torch.arange(T, device="cuda") % 4 != 0).to(torch.uint8)
-    step, logits = SublayerStep(T, E, k, h, I), torch.randn(T, E, device="cuda")
+    step, other, logits = SublayerStep(T, E, k, h, I), SublayerStep(T, E, k, h, I), torch.randn(T, E, device="cuda")
     try:
-        step.normalize(d["x"], d["gamma"], d["beta"], valid)  # the first launches wait for the GPU
-        step.route(logits)
+        for s, v in ((other, valid), (step, None)):  # the kernels' first launches wait for the GPU
+            s.normalize(d["x"], d["gamma"], d["beta"], v)
+            s.route(logits, v)
         torch.cuda.synchronize()
         before = torch.cuda.memory_allocated()
         torch.cuda._sleep(500_000_000)
@@ -165,3 +166,4 @@ def test_a_masked_batch_makes_no_buffer_and_waits_for_nothing():
         assert step.device_status() == 0 and int(step.router.tokens) == int(valid.sum())
     finally:
         step.close()
+        other.close()
